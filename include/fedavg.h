@@ -519,6 +519,144 @@ int fedavg_checksum_sum(const void *buf, int64_t count, fa_dtype dtype, uint64_t
                         double *sum_dev, void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Training beside the aggregation: the linear layer of an adapter or a head.
+ *
+ * Adapter-only federation trains small layers on a frozen backbone (FLARE
+ * page, FedUMM example): clients run them and their gradients, and the server
+ * runs them again to evaluate the merged adapters or to distil into them.
+ * All matrices are row-major device memory of one element type (FA_F32 or
+ * FA_BF16); a row pitch ld* is in elements and may exceed the row.  An input's
+ * pitch may be smaller than the row (0 repeats one row).  Pointers need only
+ * the element's alignment; 16-byte aligned matrices whose pitches are
+ * multiples of 16 bytes take the faster loads.
+ * Sums over the inner dimension, the bias, the activation and the residual are
+ * fp32; each result is rounded once to the element type (RNE).  The order of
+ * additions is fixed by the sizes, so results are deterministic.
+ * Limits: M, N, K <= 2^30; M*N, M*K, N*K <= 2^36 (FA_ERR_RANGE).
+ * ------------------------------------------------------------------------ */
+typedef enum { FA_ACT_NONE = 0, FA_ACT_RELU = 1, FA_ACT_GELU = 2, FA_ACT_SILU = 3 } fa_act;
+
+/* Device workspace bytes linear_forward (backward == 0) or linear_backward
+   (backward != 0) needs for these sizes on the current device; may be 0. */
+int linear_workspace_size(fa_dtype dtype, int64_t M, int64_t N, int64_t K, fa_act act, int backward,
+                          size_t *bytes);
+
+/*
+ * linear_forward --  z = alpha * x w^T + bias;  out = act(z) + residual.
+ * x          [M][K]; w [N][K]; bias N values (nullable).
+ * act        FA_ACT_NONE, FA_ACT_RELU, FA_ACT_GELU (z * Phi(z), the exact form)
+ *            or FA_ACT_SILU (z / (1 + exp(-z))).
+ * alpha      a factor of the product, e.g. a LoRA adapter's scale.
+ * residual   [M][N] (nullable), added after the activation.
+ * out        [M][N].  May be the residual itself (same pointer and pitch).
+ * preact     [M][N] (nullable): receives z, which linear_backward takes.
+ * K == 0 gives out = act(bias) + residual; M == 0 or N == 0 is a no-op.
+ * out and preact must not overlap each other or the other inputs
+ * (FA_ERR_ARG).
+ */
+int linear_forward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void *x, int64_t ldx,
+                   const void *w, int64_t ldw, const void *bias, fa_act act, float alpha,
+                   const void *residual, int64_t ldr, void *out, int64_t ldo, void *preact,
+                   int64_t ldp, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * linear_backward -- gradients of linear_forward from dy, the gradient of out:
+ *     dz = dy * act'(preact)     (dy itself for FA_ACT_NONE)
+ *     dx = alpha * dz w,   dw = alpha * dz^T x,   db = column sums of dz.
+ * The residual's gradient is dy.  dx [M][K], dw [N][K] and db (N values) are
+ * each nullable; x is needed for dw, w for dx, preact (which holds z) for an
+ * activation.  For the two products dz is held in the element type, as dy is;
+ * db sums it unrounded.  M == 0 gives zero dw and db; N == 0 gives zero dx.
+ * Outputs must not overlap the inputs or each other (FA_ERR_ARG).
+ */
+int linear_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void *dy, int64_t lddy,
+                    const void *x, int64_t ldx, const void *w, int64_t ldw, fa_act act, float alpha,
+                    const void *preact, int64_t ldp, void *dx, int64_t lddx, void *dw, int64_t lddw,
+                    void *db, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Exchange of distilled knowledge: clients send the top logits of each public
+ * token instead of weights (FLARE page, section on what a federation may
+ * exchange: model weights, adapters or distilled knowledge), and the server
+ * trains its model on them, each client weighted by its sample count as in
+ * the weight average.
+ * ------------------------------------------------------------------------ */
+#define FA_MAX_TOP 256           /* top logits of one row */
+#define FA_MAX_LIST_ENTRIES 4096 /* of one row over all clients */
+
+/*
+ * logits_topk -- the client's side.  Of every row of x (R rows of V logits of
+ * dtype, row pitch ldx elements) the k largest values: their columns, in
+ * increasing order, to idx_out (device int32[R][k]) and the values, widened to
+ * fp32, to val_out (device float[R][k]).  Ties go to the lower column; NaN
+ * counts as largest, -0 as equal to +0.  The result is unique, hence
+ * deterministic.  lse_out (device float[R], nullable) receives
+ * log sum_i exp(x_i / tau), the normaliser of the row's softmax at temperature
+ * tau: -inf for a row of -inf, NaN for one that holds NaN or +inf.
+ * 0 < tau; 0 <= k <= min(V, FA_MAX_TOP); 0 <= V <= 2^30, 0 <= R <= 2^36 / max(V, 1)
+ * (FA_ERR_RANGE).  Asynchronous on `stream`.
+ */
+int logits_topk_workspace_size(fa_dtype dtype, int64_t R, int64_t V, int64_t k, size_t *bytes);
+int logits_topk(const void *x, fa_dtype dtype, int64_t R, int64_t V, int64_t ldx, int64_t k,
+                float tau, int32_t *idx_out, float *val_out, float *lse_out, void *workspace,
+                size_t workspace_bytes, void *stream);
+
+/*
+ * distill_loss -- the server's side: loss of the student logits z against the
+ * clients' top logits, and its gradient.  For row r
+ *     q_cj = exp(val_c[r][j] / tau - L_c)     client c's probability of idx_c[r][j]
+ *     w_c  = n_c / sum of n over the clients that sent row r
+ *     p    = softmax(z[r] / tau)
+ *     loss[r] = g_r tau^2 sum_c w_c sum_j q_cj (log q_cj - log p_j)
+ *     dz[r][i] = d loss[r] / d z[r][i] = g_r tau (m p_i - sum_c w_c q_c,i)
+ *     m = sum_c w_c sum_j q_cj,   g_r = row_weight[r]
+ * L_c is the log-sum-exp of the list (the kept entries sum to one), or, when
+ * teacher_lse is given, teacher_lse[c][r], the normaliser of the client's whole
+ * row (logits_topk's lse_out; the entries not sent then carry no mass).
+ *
+ * clients      1 .. FA_MAX_CLIENTS; n as for fedavg_aggregate (n_c == 0: the
+ *              client's lists are never read and may be NULL).
+ * idx, val     host arrays of device pointers: int32[R][k_c], float[R][k_c].
+ * teacher_lse  host array of device pointers to float[R], or NULL.
+ * k            host int64 array: k_c in [0, FA_MAX_TOP], their sum over clients
+ *              with n_c > 0 at most FA_MAX_LIST_ENTRIES.
+ *              A row's list ends at its first negative index and must be
+ *              strictly increasing and below V; a client whose list is flawed
+ *              counts as not having sent that row and err_flag is set.  A
+ *              client whose entries are all -inf has not sent the row either.
+ *              A row that no client sent has loss 0 and gradient 0.
+ * z            [R][V] of dtype, row pitch ldz.
+ * tau          > 0.
+ * row_weight   device float[R], nullable (all 1).  A row of weight 0 (padding)
+ *              is not read: its loss, lse and gradient are 0.  A row of z that
+ *              is all -inf has lse -inf, loss 0 and gradient 0.
+ * loss         device float[R].
+ * lse          device float[R], nullable: log sum_i exp(z_i / tau), for
+ *              distill_backward.
+ * dz           [R][V] of dtype, row pitch lddz, nullable: no gradient.  May be
+ *              z itself (same pointer and pitch); otherwise it must not overlap.
+ * err_flag     device int, nullable: set to 0, then to FA_ERR_INDEX if some
+ *              list is flawed.
+ * NaN and infinities that enter a row's formulas propagate into its results.
+ * Sums are fp32 in an order fixed by the sizes: results are deterministic.
+ *
+ * distill_backward -- the gradient alone, from the lse that distill_loss wrote
+ * for the same z, tau and row_weight (times, for a chained loss, the incoming
+ * gradient of each row's loss, in row_weight).
+ */
+int distill_workspace_size(fa_dtype dtype, int64_t R, int64_t V, size_t *bytes);
+int distill_loss(int clients, const int32_t *const *idx, const float *const *val,
+                 const float *const *teacher_lse, const int64_t *k, const int64_t *n, const void *z,
+                 fa_dtype dtype, int64_t R, int64_t V, int64_t ldz, float tau,
+                 const float *row_weight, float *loss, float *lse, void *dz, int64_t lddz,
+                 int *err_flag, void *workspace, size_t workspace_bytes, void *stream);
+int distill_backward(int clients, const int32_t *const *idx, const float *const *val,
+                     const float *const *teacher_lse, const int64_t *k, const int64_t *n,
+                     const void *z, fa_dtype dtype, int64_t R, int64_t V, int64_t ldz, float tau,
+                     const float *row_weight, const float *lse, void *dz, int64_t lddz,
+                     int *err_flag, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
  * Launch-shape options (process-wide, for tuning and measurement).  They
  * change how work is spread over the GPU, never the results.
  * ------------------------------------------------------------------------ */

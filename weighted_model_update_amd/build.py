@@ -10,8 +10,11 @@ ROOT = os.path.dirname(HERE)
 LIB_PATH = os.path.join(HERE, "libfedavg.so")
 SOURCES = [os.path.join(HERE, "csrc", "fedavg_kernels.hip"),
            os.path.join(HERE, "csrc", "topk.hip"),
+           os.path.join(HERE, "csrc", "linear.hip"),
+           os.path.join(HERE, "csrc", "logits.hip"),
            os.path.join(HERE, "csrc", "fedavg_api.hip")]
 HEADERS = [os.path.join(HERE, "csrc", "fedavg_internal.h"),
+           os.path.join(HERE, "csrc", "learn_internal.h"),
            os.path.join(ROOT, "include", "fedavg.h")]
 
 # IEEE fp32 arithmetic: no fast-math, no FMA contraction beyond the explicit

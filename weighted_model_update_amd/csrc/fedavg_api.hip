@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "fedavg_internal.h"
+#include "learn_internal.h"
 
 namespace {
 
@@ -1505,6 +1506,454 @@ int fedavg_checksum_sum(const void *buf, int64_t count, fa_dtype dtype, uint64_t
                                            static_cast<double *>(workspace), cap,
                                            static_cast<hipStream_t>(stream));
     return e == hipSuccess ? ok() : hip_fail(e, "checksum and sum launch");
+}
+
+// ============================================================ linear layer
+
+namespace {
+
+constexpr int64_t LINEAR_MAX_DIM = 1ll << 30;
+constexpr int64_t LINEAR_MAX_ELEMS = 1ll << 36;
+
+// A row-major matrix view: `cols` elements per row, row pitch ld elements.
+struct View {
+    const void *p;
+    int64_t rows, cols, ld;
+    size_t es;
+};
+
+// Whether two views share bytes.  Views of one pitch may interleave (column
+// slices of one buffer); with different pitches their whole extents count.
+bool views_overlap(const View &a, const View &b)
+{
+    if (!a.p || !b.p || a.rows == 0 || a.cols == 0 || b.rows == 0 || b.cols == 0)
+        return false;
+    const uint64_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+    const uint64_t ap = (uint64_t)a.ld * a.es, bp = (uint64_t)b.ld * b.es;
+    const uint64_t ac = (uint64_t)a.cols * a.es, bc = (uint64_t)b.cols * b.es;
+    const uint64_t a1 = a0 + (uint64_t)(a.rows - 1) * ap + ac, b1 = b0 + (uint64_t)(b.rows - 1) * bp + bc;
+    if (a1 <= b0 || b1 <= a0)
+        return false;
+    if (a.rows > 1 && b.rows > 1 && ap == bp && ap >= ac && ap >= bc) {
+        const uint64_t d = b0 >= a0 ? (b0 - a0) % ap : (ap - (a0 - b0) % ap) % ap;
+        return d < ac || d + bc > ap;
+    }
+    return true;
+}
+
+bool same_view(const View &a, const View &b)
+{
+    return a.p == b.p && a.rows == b.rows && a.cols == b.cols && (a.ld == b.ld || a.rows <= 1);
+}
+
+// Pointer, pitch and element alignment of one matrix.  `out`: rows may not
+// overlap one another.  Returns FA_OK or the failure.
+int check_view(const char *name, const View &v, bool out)
+{
+    if (v.rows == 0 || v.cols == 0)
+        return FA_OK;
+    if (!v.p)
+        return fail(FA_ERR_ARG, "%s is required", name);
+    if ((reinterpret_cast<uintptr_t>(v.p) & (v.es - 1)) != 0)
+        return fail(FA_ERR_ARG, "%s must be aligned to its element", name);
+    if (v.ld < 0 || (out && v.rows > 1 && v.ld < v.cols))
+        return fail(FA_ERR_ARG, "%s has row pitch %lld for %lld columns", name, (long long)v.ld, (long long)v.cols);
+    if (v.ld > (1ll << 40) || (v.ld > 0 && v.rows > (1ll << 58) / v.ld))
+        return fail(FA_ERR_RANGE, "%s spans too many elements", name);
+    return FA_OK;
+}
+
+int check_linear(int dtype, int64_t M, int64_t N, int64_t K, int act)
+{
+    if (!dtype_ok(dtype))
+        return fail(FA_ERR_DTYPE, "dtype must be FA_F32 or FA_BF16");
+    if (act < FA_ACT_NONE || act > FA_ACT_SILU)
+        return fail(FA_ERR_ARG, "unknown activation %d", act);
+    if (M < 0 || N < 0 || K < 0)
+        return fail(FA_ERR_ARG, "M, N and K must be >= 0");
+    if (M > LINEAR_MAX_DIM || N > LINEAR_MAX_DIM || K > LINEAR_MAX_DIM || M * N > LINEAR_MAX_ELEMS ||
+        M * K > LINEAR_MAX_ELEMS || N * K > LINEAR_MAX_ELEMS)
+        return fail(FA_ERR_RANGE, "M, N, K must be at most 2^30 and their products 2^36");
+    return FA_OK;
+}
+
+int check_workspace(const void *workspace, size_t have, size_t need)
+{
+    if (need > 0 && (!workspace || have < need))
+        return fail(FA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace ? have : (size_t)0, need);
+    if (need > 0 && !aligned16(workspace))
+        return fail(FA_ERR_ARG, "workspace must be 16-byte aligned");
+    return FA_OK;
+}
+
+size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+// linear_backward's workspace: dz, the column sums' partials, and the larger
+// of the two products' partial sums.
+struct BackwardPlan {
+    size_t dz, part, gemm;
+    size_t total() const { return dz + part + gemm; }
+};
+
+BackwardPlan backward_plan(int dtype, int64_t M, int64_t N, int64_t K, int act)
+{
+    BackwardPlan b;
+    const int cus = cu_count();
+    b.dz = act == FA_ACT_NONE ? 0 : round256((size_t)M * N * dsize(dtype));
+    b.part = round256((size_t)fa::act_grad_partials(M, N, cus) * N * sizeof(float));
+    b.gemm = std::max(fa::gemm_workspace_bytes(dtype, M, K, N, fa::GEMM_B_OUTER, cus),
+                      fa::gemm_workspace_bytes(dtype, N, K, M, fa::GEMM_A_OUTER | fa::GEMM_B_OUTER, cus));
+    return b;
+}
+
+} // namespace
+
+int linear_workspace_size(fa_dtype dtype, int64_t M, int64_t N, int64_t K, fa_act act, int backward,
+                          size_t *bytes)
+{
+    if (!bytes)
+        return fail(FA_ERR_ARG, "need a result pointer");
+    const int rc = check_linear(dtype, M, N, K, act);
+    if (rc != FA_OK)
+        return rc;
+    *bytes = backward ? backward_plan(dtype, M, N, K, act).total()
+                      : fa::gemm_workspace_bytes(dtype, M, N, K, 0, cu_count());
+    return ok();
+}
+
+int linear_forward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void *x, int64_t ldx,
+                   const void *w, int64_t ldw, const void *bias, fa_act act, float alpha,
+                   const void *residual, int64_t ldr, void *out, int64_t ldo, void *preact,
+                   int64_t ldp, void *workspace, size_t workspace_bytes, void *stream)
+{
+    int rc = check_linear(dtype, M, N, K, act);
+    if (rc != FA_OK)
+        return rc;
+    if (M == 0 || N == 0)
+        return ok();
+    const size_t es = dsize(dtype);
+    const View vx{x, M, K, ldx, es}, vw{w, N, K, ldw, es}, vb{bias, bias ? 1 : 0, N, N, es},
+        vr{residual, residual ? M : 0, N, ldr, es}, vo{out, M, N, ldo, es}, vp{preact, preact ? M : 0, N, ldp, es};
+    const View vs{workspace, workspace ? 1 : 0, (int64_t)workspace_bytes, 0, 1};
+    if ((rc = check_view("x", vx, false)) != FA_OK || (rc = check_view("w", vw, false)) != FA_OK ||
+        (rc = check_view("bias", vb, false)) != FA_OK || (rc = check_view("residual", vr, false)) != FA_OK ||
+        (rc = check_view("out", vo, true)) != FA_OK || (rc = check_view("preact", vp, true)) != FA_OK)
+        return rc;
+    for (const View &o : {vo, vp})
+        for (const View &i : {vx, vw, vb, vs})
+            if (views_overlap(o, i))
+                return fail(FA_ERR_ARG, "out and preact must not overlap the inputs or the workspace");
+    if (views_overlap(vo, vp) || views_overlap(vp, vr) || (views_overlap(vo, vr) && !same_view(vo, vr)))
+        return fail(FA_ERR_ARG, "out and preact must not overlap each other or, but for out being the "
+                                "residual itself, the residual");
+    const size_t need = fa::gemm_workspace_bytes(dtype, M, N, K, 0, cu_count());
+    if ((rc = check_workspace(workspace, workspace_bytes, need)) != FA_OK)
+        return rc;
+    fa::GemmArgs a{};
+    a.a = x;
+    a.b = w;
+    a.lda = ldx;
+    a.ldb = ldw;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.alpha = alpha;
+    a.bias = bias;
+    a.res = residual;
+    a.ldr = ldr;
+    a.out = out;
+    a.ldo = ldo;
+    a.pre = preact;
+    a.ldp = ldp;
+    a.act = act;
+    const hipError_t e = fa::launch_gemm(a, dtype, 0, workspace, cu_count(), static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, "linear forward launch");
+}
+
+int linear_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void *dy, int64_t lddy,
+                    const void *x, int64_t ldx, const void *w, int64_t ldw, fa_act act, float alpha,
+                    const void *preact, int64_t ldp, void *dx, int64_t lddx, void *dw, int64_t lddw,
+                    void *db, void *workspace, size_t workspace_bytes, void *stream)
+{
+    int rc = check_linear(dtype, M, N, K, act);
+    if (rc != FA_OK)
+        return rc;
+    if (!dx && !dw && !db)
+        return ok();
+    const size_t es = dsize(dtype);
+    const bool has_act = act != FA_ACT_NONE;
+    const View vy{dy, M, N, lddy, es}, vx{x, dw ? M : 0, K, ldx, es}, vw{w, dx ? N : 0, K, ldw, es},
+        vp{preact, has_act ? M : 0, N, ldp, es}, vdx{dx, dx ? M : 0, K, lddx, es},
+        vdw{dw, dw ? N : 0, K, lddw, es}, vdb{db, db ? 1 : 0, N, N, es};
+    const View vs{workspace, workspace ? 1 : 0, (int64_t)workspace_bytes, 0, 1};
+    if ((rc = check_view("dy", vy, false)) != FA_OK || (rc = check_view("x", vx, false)) != FA_OK ||
+        (rc = check_view("w", vw, false)) != FA_OK || (rc = check_view("preact", vp, false)) != FA_OK ||
+        (rc = check_view("dx", vdx, true)) != FA_OK || (rc = check_view("dw", vdw, true)) != FA_OK ||
+        (rc = check_view("db", vdb, true)) != FA_OK)
+        return rc;
+    for (const View &o : {vdx, vdw, vdb})
+        for (const View &i : {vy, vx, vw, vp, vs})
+            if (views_overlap(o, i))
+                return fail(FA_ERR_ARG, "dx, dw and db must not overlap the inputs or the workspace");
+    if (views_overlap(vdx, vdw) || views_overlap(vdx, vdb) || views_overlap(vdw, vdb))
+        return fail(FA_ERR_ARG, "dx, dw and db must not overlap each other");
+    const BackwardPlan plan = backward_plan(dtype, M, N, K, act);
+    if ((rc = check_workspace(workspace, workspace_bytes, plan.total())) != FA_OK)
+        return rc;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    const int cus = cu_count();
+    const void *dz = dy;
+    int64_t lddz = lddy;
+    if (has_act || db) {
+        fa::ActGradArgs g{};
+        g.dy = dy;
+        g.lddy = lddy;
+        g.pre = preact;
+        g.ldp = ldp;
+        g.dz = has_act && (dx || dw) ? ws : nullptr;
+        g.db = db;
+        g.part = reinterpret_cast<float *>(ws + plan.dz);
+        g.M = M;
+        g.N = N;
+        g.act = act;
+        const hipError_t e = fa::launch_act_grad(g, dtype, cus, s);
+        if (e != hipSuccess)
+            return hip_fail(e, "activation gradient launch");
+        if (has_act) {
+            dz = ws;
+            lddz = N;
+        }
+    }
+    char *gws = ws + plan.dz + plan.part;
+    fa::GemmArgs a{};
+    a.a = dz;
+    a.lda = lddz;
+    a.N = (int)K;
+    a.alpha = alpha;
+    if (dx) {
+        a.b = w;
+        a.ldb = ldw;
+        a.M = (int)M;
+        a.K = (int)N;
+        a.out = dx;
+        a.ldo = lddx;
+        const hipError_t e = fa::launch_gemm(a, dtype, fa::GEMM_B_OUTER, gws, cus, s);
+        if (e != hipSuccess)
+            return hip_fail(e, "input gradient launch");
+    }
+    if (dw) {
+        a.b = x;
+        a.ldb = ldx;
+        a.M = (int)N;
+        a.K = (int)M;
+        a.out = dw;
+        a.ldo = lddw;
+        const hipError_t e = fa::launch_gemm(a, dtype, fa::GEMM_A_OUTER | fa::GEMM_B_OUTER, gws, cus, s);
+        if (e != hipSuccess)
+            return hip_fail(e, "weight gradient launch");
+    }
+    return ok();
+}
+
+// ============================================================ top logits of rows, distillation
+
+namespace {
+
+int check_logits(int dtype, int64_t R, int64_t V, float tau)
+{
+    if (!dtype_ok(dtype))
+        return fail(FA_ERR_DTYPE, "logits must be FA_F32 or FA_BF16");
+    if (R < 0 || V < 0)
+        return fail(FA_ERR_ARG, "R and V must be >= 0");
+    if (V > LINEAR_MAX_DIM || R > LINEAR_MAX_ELEMS / std::max<int64_t>(V, 1))
+        return fail(FA_ERR_RANGE, "V must be at most 2^30 and R * V 2^36");
+    if (!(tau > 0.f) || !(tau < INFINITY) || !(1.f / tau < INFINITY))
+        return fail(FA_ERR_ARG, "tau must be positive and finite");
+    return FA_OK;
+}
+
+// Every argument of distill_loss and distill_backward but the results of the
+// loss; fills `a`.
+int distill_args(fa::DistillArgs &a, int clients, const int32_t *const *idx, const float *const *val,
+                 const float *const *teacher_lse, const int64_t *k, const int64_t *n, const void *z, int dtype,
+                 int64_t R, int64_t V, int64_t ldz, float tau, const float *row_weight, void *dz, int64_t lddz,
+                 int *err_flag, void *workspace, size_t workspace_bytes)
+{
+    int rc = check_logits(dtype, R, V, tau);
+    if (rc != FA_OK)
+        return rc;
+    if (clients < 1 || clients > FA_MAX_CLIENTS)
+        return fail(FA_ERR_RANGE, "clients=%d is outside 1 .. %d", clients, FA_MAX_CLIENTS);
+    if (!idx || !val || !k || !n)
+        return fail(FA_ERR_ARG, "idx, val, k and n are required");
+    int64_t total = 0;
+    a.clients = 0;
+    for (int c = 0; c < clients; c++) {
+        if (n[c] < 0 || n[c] > FA_MAX_WEIGHT)
+            return fail(FA_ERR_RANGE, "n[%d]=%lld is outside 0 .. 2^24", c, (long long)n[c]);
+        if (k[c] < 0 || k[c] > FA_MAX_TOP)
+            return fail(FA_ERR_RANGE, "k[%d]=%lld is outside 0 .. %d", c, (long long)k[c], FA_MAX_TOP);
+        if (n[c] == 0 || k[c] == 0)
+            continue;
+        if (R > 0 && (!idx[c] || !val[c] || (teacher_lse && !teacher_lse[c])))
+            return fail(FA_ERR_ARG, "client %d has no list", c);
+        if (((reinterpret_cast<uintptr_t>(idx[c]) | reinterpret_cast<uintptr_t>(val[c]) |
+              (teacher_lse ? reinterpret_cast<uintptr_t>(teacher_lse[c]) : 0)) & 3u) != 0)
+            return fail(FA_ERR_ARG, "client %d's list must be 4-byte aligned", c);
+        const int at = a.clients++;
+        a.idx[at] = idx[c];
+        a.val[at] = val[c];
+        a.tlse[at] = teacher_lse ? teacher_lse[c] : nullptr;
+        a.n[at] = (float)n[c];
+        a.k[at] = (int)k[c];
+        a.first[at] = (int)total;
+        total += k[c];
+        if (total > FA_MAX_LIST_ENTRIES)
+            return fail(FA_ERR_RANGE, "the clients' k sum to more than %d", FA_MAX_LIST_ENTRIES);
+    }
+    a.first[a.clients] = (int)total;
+    a.has_tlse = teacher_lse != nullptr;
+    const size_t es = dsize(dtype);
+    const View vz{z, R, V, ldz, es}, vd{dz, dz ? R : 0, V, lddz, es};
+    if ((rc = check_view("z", vz, false)) != FA_OK || (rc = check_view("dz", vd, true)) != FA_OK)
+        return rc;
+    if (views_overlap(vd, vz) && !same_view(vd, vz))
+        return fail(FA_ERR_ARG, "dz must be z itself or not overlap it");
+    if (((reinterpret_cast<uintptr_t>(row_weight) | reinterpret_cast<uintptr_t>(err_flag)) & 3u) != 0)
+        return fail(FA_ERR_ARG, "row_weight and err_flag must be 4-byte aligned");
+    const View vs{workspace, workspace ? 1 : 0, (int64_t)workspace_bytes, 0, 1};
+    if (views_overlap(vd, vs) || views_overlap(vz, vs))
+        return fail(FA_ERR_ARG, "the workspace must not overlap z or dz");
+    if ((rc = check_workspace(workspace, workspace_bytes, fa::distill_workspace_bytes(dtype, R, V, cu_count()))) != FA_OK)
+        return rc;
+    a.z = z;
+    a.R = R;
+    a.V = V;
+    a.ldz = ldz;
+    a.tau = tau;
+    a.inv_tau = 1.f / tau;
+    a.row_weight = row_weight;
+    a.dz = dz;
+    a.lddz = lddz;
+    a.err = err_flag;
+    a.ws = workspace;
+    return FA_OK;
+}
+
+int run_distill(const fa::DistillArgs &a, int dtype, bool loss, void *stream)
+{
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (a.err) {
+        const hipError_t e = fa::launch_fill_u32(a.err, 1, 0u, s);
+        if (e != hipSuccess)
+            return hip_fail(e, "error flag clear");
+    }
+    const hipError_t e = fa::launch_distill(a, dtype, loss, cu_count(), s);
+    return e == hipSuccess ? ok() : hip_fail(e, "distillation launch");
+}
+
+} // namespace
+
+int logits_topk_workspace_size(fa_dtype dtype, int64_t R, int64_t V, int64_t k, size_t *bytes)
+{
+    if (!bytes)
+        return fail(FA_ERR_ARG, "need a result pointer");
+    const int rc = check_logits(dtype, R, V, 1.f);
+    if (rc != FA_OK)
+        return rc;
+    if (k < 0 || k > V || k > FA_MAX_TOP)
+        return fail(FA_ERR_RANGE, "need 0 <= k <= min(V, %d) (k=%lld, V=%lld)", FA_MAX_TOP, (long long)k, (long long)V);
+    *bytes = fa::top_rows_workspace_bytes(dtype, R, V, k, cu_count());
+    return ok();
+}
+
+int logits_topk(const void *x, fa_dtype dtype, int64_t R, int64_t V, int64_t ldx, int64_t k,
+                float tau, int32_t *idx_out, float *val_out, float *lse_out, void *workspace,
+                size_t workspace_bytes, void *stream)
+{
+    int rc = check_logits(dtype, R, V, tau);
+    if (rc != FA_OK)
+        return rc;
+    if (k < 0 || k > V || k > FA_MAX_TOP)
+        return fail(FA_ERR_RANGE, "need 0 <= k <= min(V, %d) (k=%lld, V=%lld)", FA_MAX_TOP, (long long)k, (long long)V);
+    if (R == 0 || (k == 0 && !lse_out))
+        return ok();
+    const View vx{x, R, V, ldx, dsize(dtype)}, vi{idx_out, R, k, k, 4}, vv{val_out, R, k, k, 4},
+        vl{lse_out, lse_out ? 1 : 0, R, R, 4}, vs{workspace, workspace ? 1 : 0, (int64_t)workspace_bytes, 0, 1};
+    if ((rc = check_view("x", vx, false)) != FA_OK || (rc = check_view("idx_out", vi, true)) != FA_OK ||
+        (rc = check_view("val_out", vv, true)) != FA_OK || (rc = check_view("lse_out", vl, true)) != FA_OK)
+        return rc;
+    for (const View &o : {vi, vv, vl})
+        if (views_overlap(o, vx) || views_overlap(o, vs))
+            return fail(FA_ERR_ARG, "outputs must not overlap the logits or the workspace");
+    if (views_overlap(vi, vv) || views_overlap(vi, vl) || views_overlap(vv, vl))
+        return fail(FA_ERR_ARG, "outputs must not overlap each other");
+    if ((rc = check_workspace(workspace, workspace_bytes, fa::top_rows_workspace_bytes(dtype, R, V, k, cu_count()))) != FA_OK)
+        return rc;
+    const fa::TopRowsArgs a{x, R, V, ldx, (int)k, 1.f / tau, idx_out, val_out, lse_out, workspace};
+    const hipError_t e = fa::launch_top_rows(a, dtype, cu_count(), static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, "top logits launch");
+}
+
+int distill_workspace_size(fa_dtype dtype, int64_t R, int64_t V, size_t *bytes)
+{
+    if (!bytes)
+        return fail(FA_ERR_ARG, "need a result pointer");
+    const int rc = check_logits(dtype, R, V, 1.f);
+    if (rc != FA_OK)
+        return rc;
+    *bytes = fa::distill_workspace_bytes(dtype, R, V, cu_count());
+    return ok();
+}
+
+int distill_loss(int clients, const int32_t *const *idx, const float *const *val,
+                 const float *const *teacher_lse, const int64_t *k, const int64_t *n, const void *z,
+                 fa_dtype dtype, int64_t R, int64_t V, int64_t ldz, float tau,
+                 const float *row_weight, float *loss, float *lse, void *dz, int64_t lddz,
+                 int *err_flag, void *workspace, size_t workspace_bytes, void *stream)
+{
+    fa::DistillArgs a{};
+    int rc = distill_args(a, clients, idx, val, teacher_lse, k, n, z, dtype, R, V, ldz, tau, row_weight, dz, lddz,
+                          err_flag, workspace, workspace_bytes);
+    if (rc != FA_OK)
+        return rc;
+    const View vl{loss, 1, R, R, 4}, ve{lse, lse ? 1 : 0, R, R, 4}, vz{z, R, V, ldz, dsize(dtype)},
+        vd{dz, dz ? R : 0, V, lddz, dsize(dtype)}, vs{workspace, workspace ? 1 : 0, (int64_t)workspace_bytes, 0, 1};
+    if ((rc = check_view("loss", vl, true)) != FA_OK || (rc = check_view("lse", ve, true)) != FA_OK)
+        return rc;
+    for (const View &o : {vl, ve})
+        if (views_overlap(o, vz) || views_overlap(o, vd) || views_overlap(o, vs))
+            return fail(FA_ERR_ARG, "loss and lse must not overlap z, dz or the workspace");
+    if (views_overlap(vl, ve))
+        return fail(FA_ERR_ARG, "loss and lse must not overlap");
+    a.loss = loss;
+    a.lse = lse;
+    return run_distill(a, dtype, true, stream);
+}
+
+int distill_backward(int clients, const int32_t *const *idx, const float *const *val,
+                     const float *const *teacher_lse, const int64_t *k, const int64_t *n,
+                     const void *z, fa_dtype dtype, int64_t R, int64_t V, int64_t ldz, float tau,
+                     const float *row_weight, const float *lse, void *dz, int64_t lddz,
+                     int *err_flag, void *workspace, size_t workspace_bytes, void *stream)
+{
+    fa::DistillArgs a{};
+    int rc = distill_args(a, clients, idx, val, teacher_lse, k, n, z, dtype, R, V, ldz, tau, row_weight, dz, lddz,
+                          err_flag, workspace, workspace_bytes);
+    if (rc != FA_OK)
+        return rc;
+    if (R == 0 || V == 0)
+        return ok();
+    if (!dz)
+        return fail(FA_ERR_ARG, "dz is required");
+    const View ve{lse, 1, R, R, 4}, vd{dz, R, V, lddz, dsize(dtype)};
+    if ((rc = check_view("lse", ve, false)) != FA_OK)
+        return rc;
+    if (views_overlap(vd, ve))
+        return fail(FA_ERR_ARG, "dz must not overlap lse");
+    a.lse = const_cast<float *>(lse);
+    return run_distill(a, dtype, false, stream);
 }
 
 } // extern "C"

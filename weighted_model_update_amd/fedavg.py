@@ -21,7 +21,9 @@ FA_OPT_BLOCKS_PER_CU, FA_OPT_MASK_VECTORS_PER_BLOCK, FA_OPT_SPARSE_BLOCKS, FA_OP
 FA_OPT_SPARSE_TILE = 5
 FA_OPT_TOPK_SAMPLED = 6
 FA_OPT_INDEX_TILES = 7
+FA_ACT_NONE, FA_ACT_RELU, FA_ACT_GELU, FA_ACT_SILU = 0, 1, 2, 3
 FA_MAX_CLIENTS = 64
+FA_MAX_TOP, FA_MAX_LIST_ENTRIES = 256, 4096
 FA_MAX_N = 1 << 40
 
 STATUS_NAMES = {
@@ -39,6 +41,9 @@ EXPORTS = [
     "sparse_workspace_size", "sparse_masked_accumulate", "fedavg_checksum", "fedavg_set_option",
     "fedavg_sum_workspace_size", "fedavg_checksum_sum", "sparse_masked_accumulate_noalloc",
     "fedavg_arena_layout",
+    "linear_workspace_size", "linear_forward", "linear_backward",
+    "logits_topk_workspace_size", "logits_topk",
+    "distill_workspace_size", "distill_loss", "distill_backward",
 ]
 
 
@@ -93,6 +98,18 @@ def load(build_if_missing=True):
         "topk_select": ([P, i32, i64, i64, P, P, P, sz, P], i32),
         "fedavg_set_option": ([i32, i64], i32),
         "fedavg_arena_layout": ([i32, i64, P, P], i32),
+        "linear_workspace_size": ([i32, i64, i64, i64, i32, i32, P], i32),
+        "linear_forward": ([i32, i64, i64, i64, P, i64, P, i64, P, i32, ctypes.c_float, P, i64, P, i64, P, i64,
+                            P, sz, P], i32),
+        "linear_backward": ([i32, i64, i64, i64, P, i64, P, i64, P, i64, i32, ctypes.c_float, P, i64, P, i64,
+                             P, i64, P, P, sz, P], i32),
+        "logits_topk_workspace_size": ([i32, i64, i64, i64, P], i32),
+        "logits_topk": ([P, i32, i64, i64, i64, i64, ctypes.c_float, P, P, P, P, sz, P], i32),
+        "distill_workspace_size": ([i32, i64, i64, P], i32),
+        "distill_loss": ([i32, P, P, P, P, P, P, i32, i64, i64, i64, ctypes.c_float, P, P, P, P, i64, P, P, sz, P],
+                         i32),
+        "distill_backward": ([i32, P, P, P, P, P, P, i32, i64, i64, i64, ctypes.c_float, P, P, P, i64, P, P, sz, P],
+                             i32),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -738,6 +755,267 @@ def topk_count(N, frac):
     from fractions import Fraction
     import math
     return int(math.floor(Fraction(str(frac)) * int(N)))
+
+
+# ------------------------------------------------------------------ linear layer
+
+_ACTS = {"none": FA_ACT_NONE, None: FA_ACT_NONE, "relu": FA_ACT_RELU, "gelu": FA_ACT_GELU, "silu": FA_ACT_SILU}
+
+
+def _act(act):
+    code = _ACTS.get(act, act)
+    if code not in (FA_ACT_NONE, FA_ACT_RELU, FA_ACT_GELU, FA_ACT_SILU):
+        raise ValueError(f"act must be 'none', 'relu', 'gelu' or 'silu', got {act!r}")
+    return code
+
+
+def _matrix(t, name, rows, cols, dtype):
+    """Row pitch of a GPU matrix [rows, cols] of `dtype` with unit column
+    stride (0 for an absent one)."""
+    if t is None:
+        return 0
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    return ld if rows > 1 else max(ld, cols)
+
+
+def _vector(t, name, n, dtype):
+    if t is None:
+        return
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {n} elements")
+
+
+def _new(shape, dtype, device, stream):
+    # memory that the call makes itself belongs to the stream the work runs on
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(workspace, nbytes, device, stream):
+    if workspace is None:
+        return _new(nbytes, torch.uint8, device, stream) if nbytes > 0 else None
+    return _contig(_on_gpu(workspace, "workspace"), "workspace")
+
+
+def _nbytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def linear_workspace_size(M, N, K, dtype=torch.bfloat16, act="none", backward=False):
+    """Device workspace bytes linear_forward or linear_backward needs."""
+    b = ctypes.c_size_t(0)
+    _check(load().linear_workspace_size(_dtype_code(dtype), int(M), int(N), int(K), _act(act), int(bool(backward)),
+                                        ctypes.byref(b)))
+    return b.value
+
+
+def linear_forward(x, w, bias=None, act="none", residual=None, alpha=1.0, out=None, preact=None,
+                   workspace=None, stream=None):
+    """act(alpha * x w^T + bias) + residual for x [M, K], w [N, K], bias [N],
+    residual [M, N]: float32 or bfloat16 GPU tensors of one dtype with unit
+    stride along their rows.  out [M, N] (may be the residual) is made when
+    None; preact [M, N], when given, receives the value before the activation,
+    which linear_backward takes.  Returns out.  See linear_forward in
+    include/fedavg.h."""
+    lib = load()
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w must be matrices")
+    dt, code = x.dtype, _dtype(x)
+    (M, K), N, act = x.shape, w.shape[0], _act(act)
+    ldx, ldw = _matrix(x, "x", M, K, dt), _matrix(w, "w", N, K, dt)
+    _vector(bias, "bias", N, dt)
+    if out is None:
+        out = _new((M, N), dt, x.device, stream)
+    ldr, ldo = _matrix(residual, "residual", M, N, dt), _matrix(out, "out", M, N, dt)
+    ldp = _matrix(preact, "preact", M, N, dt)
+    if workspace is None:
+        b = ctypes.c_size_t(0)
+        _check(lib.linear_workspace_size(code, M, N, K, act, 0, ctypes.byref(b)))
+        workspace = _workspace(None, b.value, x.device, stream)
+    else:
+        workspace = _workspace(workspace, 0, x.device, stream)
+    _check(lib.linear_forward(code, M, N, K, _ptr(x), ldx, _ptr(w), ldw, _ptr(bias), act, float(alpha),
+                              _ptr(residual), ldr, _ptr(out), ldo, _ptr(preact), ldp, _ptr(workspace),
+                              _nbytes(workspace), _stream_handle(stream)))
+    return out
+
+
+def linear_backward(dy, x, w, act="none", preact=None, alpha=1.0, dx=True, dw=True, db=False, workspace=None,
+                    stream=None):
+    """Gradients (dx, dw, db) of linear_forward from dy [M, N], the gradient
+    of its output (which is also the residual's gradient).  dx, dw and db are
+    each a tensor to fill, True to make one, or None/False to leave that
+    gradient out (returned as None).  preact: what linear_forward wrote there,
+    for an activation.  See linear_backward in include/fedavg.h."""
+    lib = load()
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w must be matrices")
+    dt, code = x.dtype, _dtype(x)
+    (M, K), N, act = x.shape, w.shape[0], _act(act)
+
+    def want(t, shape):
+        if t is None or t is False:
+            return None
+        return _new(shape, dt, x.device, stream) if t is True else t
+
+    dx, dw, db = want(dx, (M, K)), want(dw, (N, K)), want(db, (N,))
+    lddy, ldx, ldw = _matrix(dy, "dy", M, N, dt), _matrix(x, "x", M, K, dt), _matrix(w, "w", N, K, dt)
+    ldp = _matrix(preact, "preact", M, N, dt)
+    lddx, lddw = _matrix(dx, "dx", M, K, dt), _matrix(dw, "dw", N, K, dt)
+    _vector(db, "db", N, dt)
+    if workspace is None:
+        b = ctypes.c_size_t(0)
+        _check(lib.linear_workspace_size(code, M, N, K, act, 1, ctypes.byref(b)))
+        workspace = _workspace(None, b.value, x.device, stream)
+    else:
+        workspace = _workspace(workspace, 0, x.device, stream)
+    _check(lib.linear_backward(code, M, N, K, _ptr(dy), lddy, _ptr(x), ldx, _ptr(w), ldw, act, float(alpha),
+                               _ptr(preact), ldp, _ptr(dx), lddx, _ptr(dw), lddw, _ptr(db), _ptr(workspace),
+                               _nbytes(workspace), _stream_handle(stream)))
+    return dx, dw, db
+
+
+# ------------------------------------------------------------------ top logits, distillation
+
+def logits_topk_workspace_size(R, V, k, dtype=torch.bfloat16):
+    """Device workspace bytes logits_topk needs."""
+    b = ctypes.c_size_t(0)
+    _check(load().logits_topk_workspace_size(_dtype_code(dtype), int(R), int(V), int(k), ctypes.byref(b)))
+    return b.value
+
+
+def logits_topk(x, k, tau=1.0, idx_out=None, val_out=None, lse_out=None, workspace=None, stream=None):
+    """A client's top logits: of each row of x [R, V] the k largest (ties to
+    the lower column), as (int32 columns [R, k] in increasing order, float32
+    values [R, k], float32 log-sum-exp [R] of the whole row at temperature
+    tau).  See logits_topk in include/fedavg.h."""
+    lib = load()
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix [R, V]")
+    (R, V), k = x.shape, int(k)
+    ld = _matrix(x, "x", R, V, x.dtype)
+    kk = max(k, 0)
+    idx_out = _new((R, kk), torch.int32, x.device, stream) if idx_out is None else idx_out
+    val_out = _new((R, kk), torch.float32, x.device, stream) if val_out is None else val_out
+    lse_out = _new((R,), torch.float32, x.device, stream) if lse_out is None else lse_out
+    _vector(idx_out, "idx_out", R * kk, torch.int32)
+    _vector(val_out, "val_out", R * kk, torch.float32)
+    _vector(lse_out, "lse_out", R, torch.float32)
+    if workspace is None:
+        b = ctypes.c_size_t(0)
+        _check(lib.logits_topk_workspace_size(_dtype(x), R, V, k, ctypes.byref(b)))
+        workspace = _workspace(None, b.value, x.device, stream)
+    else:
+        workspace = _workspace(workspace, 0, x.device, stream)
+    _check(lib.logits_topk(_ptr(x), _dtype(x), R, V, ld, k, float(tau), _ptr(idx_out), _ptr(val_out),
+                           _ptr(lse_out), _ptr(workspace), _nbytes(workspace), _stream_handle(stream)))
+    return idx_out, val_out, lse_out
+
+
+def distill_workspace_size(R, V, dtype=torch.bfloat16):
+    """Device workspace bytes distill_loss and distill_backward need."""
+    b = ctypes.c_size_t(0)
+    _check(load().distill_workspace_size(_dtype_code(dtype), int(R), int(V), ctypes.byref(b)))
+    return b.value
+
+
+def _distill_lists(idx, val, teacher_lse, n, R):
+    C = len(n)
+    if len(idx) != C or len(val) != C or (teacher_lse is not None and len(teacher_lse) != C):
+        raise ValueError("idx, val, teacher_lse and n must have one entry per client")
+    ks = (ctypes.c_int64 * max(C, 1))()
+    for c in range(C):
+        if int(n[c]) == 0:
+            continue
+        i, v = idx[c], val[c]
+        if i.dim() != 2 or i.shape[0] != R or i.shape != v.shape:
+            raise ValueError(f"idx[{c}] and val[{c}] must both be [{R}, k]")
+        _vector(i, f"idx[{c}]", i.numel(), torch.int32)
+        _vector(v, f"val[{c}]", v.numel(), torch.float32)
+        if teacher_lse is not None:
+            _vector(teacher_lse[c], f"teacher_lse[{c}]", R, torch.float32)
+        ks[c] = i.shape[1]
+    return C, _ptr_array(idx), _ptr_array(val), (None if teacher_lse is None else _ptr_array(teacher_lse)), ks
+
+
+def _distill_workspace(lib, z, workspace, stream):
+    if workspace is not None:
+        return _workspace(workspace, 0, z.device, stream)
+    b = ctypes.c_size_t(0)
+    _check(lib.distill_workspace_size(_dtype(z), z.shape[0], z.shape[1], ctypes.byref(b)))
+    return _workspace(None, b.value, z.device, stream)
+
+
+def _err_flag(err_flag):
+    if err_flag is not None and (err_flag.numel() < 1 or err_flag.dtype != torch.int32):
+        raise ValueError("err_flag must be an int32 tensor of at least one element")
+    return _on_gpu(err_flag, "err_flag")
+
+
+def distill_loss(z, idx, val, n, tau=1.0, teacher_lse=None, row_weight=None, loss=None, lse=None, dz=None,
+                 err_flag=None, workspace=None, stream=None):
+    """Loss of the student logits z [R, V] against the top logits of several
+    clients, client c weighted by its sample count n[c], and optionally its
+    gradient.  idx[c], val[c]: int32 and float32 [R, k_c] as logits_topk makes
+    them (an entry of -1 ends a row's list); teacher_lse[c]: the client's
+    float32 [R] normalisers, or None to renormalise each list.  row_weight:
+    float32 [R], 0 for rows to leave out.  loss and lse (float32 [R]) are made
+    when None; dz: a tensor [R, V] to fill (z itself is allowed), True to make
+    one, None for the loss alone.  Returns (loss, lse, dz).  See distill_loss
+    in include/fedavg.h."""
+    lib = load()
+    if z.dim() != 2:
+        raise ValueError("z must be a matrix [R, V]")
+    R, V = z.shape
+    ldz = _matrix(z, "z", R, V, z.dtype)
+    loss = _new((R,), torch.float32, z.device, stream) if loss is None else loss
+    lse = _new((R,), torch.float32, z.device, stream) if lse is None else lse
+    dz = None if dz is None or dz is False else (_new((R, V), z.dtype, z.device, stream) if dz is True else dz)
+    lddz = _matrix(dz, "dz", R, V, z.dtype)
+    for t, name in ((row_weight, "row_weight"), (loss, "loss"), (lse, "lse")):
+        _vector(t, name, R, torch.float32)
+    C, pi, pv, pl, ks = _distill_lists(idx, val, teacher_lse, n, R)
+    workspace = _distill_workspace(lib, z, workspace, stream)
+    _check(lib.distill_loss(C, pi, pv, pl, ks, _i64_array(n), _ptr(z), _dtype(z), R, V, ldz, float(tau),
+                            _ptr(row_weight), _ptr(loss), _ptr(lse), _ptr(dz), lddz, _ptr(_err_flag(err_flag)),
+                            _ptr(workspace), _nbytes(workspace), _stream_handle(stream)))
+    return loss, lse, dz
+
+
+def distill_backward(z, lse, idx, val, n, tau=1.0, teacher_lse=None, row_weight=None, dz=None, err_flag=None,
+                     workspace=None, stream=None):
+    """The gradient dz [R, V] of distill_loss alone, from the lse it wrote
+    (row_weight then holds the row weights times the incoming gradients of the
+    rows' losses).  dz is made when None; z itself is allowed."""
+    lib = load()
+    if z.dim() != 2:
+        raise ValueError("z must be a matrix [R, V]")
+    R, V = z.shape
+    ldz = _matrix(z, "z", R, V, z.dtype)
+    dz = _new((R, V), z.dtype, z.device, stream) if dz is None else dz
+    lddz = _matrix(dz, "dz", R, V, z.dtype)
+    for t, name in ((row_weight, "row_weight"), (lse, "lse")):
+        _vector(t, name, R, torch.float32)
+    C, pi, pv, pl, ks = _distill_lists(idx, val, teacher_lse, n, R)
+    workspace = _distill_workspace(lib, z, workspace, stream)
+    _check(lib.distill_backward(C, pi, pv, pl, ks, _i64_array(n), _ptr(z), _dtype(z), R, V, ldz, float(tau),
+                                _ptr(row_weight), _ptr(lse), _ptr(dz), lddz, _ptr(_err_flag(err_flag)),
+                                _ptr(workspace), _nbytes(workspace), _stream_handle(stream)))
+    return dz
 
 
 # ------------------------------------------------------------------ sample allocation

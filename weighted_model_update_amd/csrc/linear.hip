@@ -24,6 +24,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int STEP_BYTES = 128; // k per step, as bytes of one row
 constexpr int WAVE = 64;
+constexpr int WAIT_LOADS = 0x0f70; // s_waitcnt vmcnt(0), the other counters as they are
 
 template <typename T> struct traits;
 template <> struct traits<__bf16> { static constexpr int EPC = 8; };
@@ -73,65 +74,68 @@ template <typename T> __device__ __forceinline__ u32x4 load_chunk(const T *p, in
     return r;
 }
 
-// Four consecutive values of a row, of which `valid` may be touched.  Rows
-// are only element-aligned; the hardware takes such vector accesses.
-template <typename T> __device__ __forceinline__ void load4(const T *p, int valid, float *v)
+// W consecutive values of a row, of which `valid` may be touched.  Rows are
+// only element-aligned; the hardware takes such vector accesses.
+template <typename T, int W> __device__ __forceinline__ void load_n(const T *p, int valid, float *v)
 {
-    if (valid >= 4) {
-        T e[4];
+    if (valid >= W) {
+        T e[W];
         __builtin_memcpy(e, p, sizeof e);
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < W; i++)
             v[i] = (float)e[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < W; i++)
             v[i] = i < valid ? (float)p[i] : 0.f;
     }
 }
 
-template <typename T> __device__ __forceinline__ void store4(T *p, int valid, const float *v)
+template <typename T, int W> __device__ __forceinline__ void store_n(T *p, int valid, const float *v)
 {
-    if (valid >= 4) {
-        T e[4];
+    if (valid >= W) {
+        T e[W];
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < W; i++)
             e[i] = (T)v[i]; // round to nearest even
         __builtin_memcpy(p, e, sizeof e);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < W; i++)
             if (i < valid)
                 p[i] = (T)v[i];
     }
 }
 
-// out(m, n..n+3) from the finished sums: z = alpha s + bias, then the
+// out(m, n..n+W-1) from the finished sums: z = alpha s + bias, then the
 // activation, then the residual, all in fp32, each result rounded once.
-template <typename T>
-__device__ __forceinline__ void epilogue4(const GemmArgs &p, int64_t m, int n, const float *s)
+template <typename T, int W>
+__device__ __forceinline__ void epilogue(const GemmArgs &p, int64_t m, int n, const float *s)
 {
     const int valid = p.N - n;
-    float z[4], b[4] = {0.f, 0.f, 0.f, 0.f};
-    if (p.bias)
-        load4(static_cast<const T *>(p.bias) + n, valid, b);
+    float z[W], b[W];
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < W; i++)
+        b[i] = 0.f;
+    if (p.bias)
+        load_n<T, W>(static_cast<const T *>(p.bias) + n, valid, b);
+#pragma unroll
+    for (int i = 0; i < W; i++)
         z[i] = __builtin_fmaf(p.alpha, s[i], b[i]);
     if (p.pre)
-        store4(static_cast<T *>(p.pre) + m * p.ldp + n, valid, z);
+        store_n<T, W>(static_cast<T *>(p.pre) + m * p.ldp + n, valid, z);
     if (p.act != FA_ACT_NONE) {
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < W; i++)
             z[i] = act_of(z[i], p.act);
     }
     if (p.res) {
-        load4(static_cast<const T *>(p.res) + m * p.ldr + n, valid, b);
+        load_n<T, W>(static_cast<const T *>(p.res) + m * p.ldr + n, valid, b);
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < W; i++)
             z[i] += b[i];
     }
-    store4(static_cast<T *>(p.out) + m * p.ldo + n, valid, z);
+    store_n<T, W>(static_cast<T *>(p.out) + m * p.ldo + n, valid, z);
 }
 
 // ------------------------------------------------------------ LDS tiles
@@ -263,37 +267,71 @@ template <typename T, bool OUTER, int ROWS, int THREADS> struct Stage {
     }
 };
 
-template <typename T, int BM, int BN, int WM, int WN, bool AO, bool BO>
-__global__ __launch_bounds__(WM *WN *WAVE) void gemm_kernel(GemmArgs p, int tiles_n)
-{
-    constexpr int THREADS = WM * WN * WAVE;
-    constexpr int BK = STEP_BYTES / (int)sizeof(T);
-    constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
-    __shared__ __attribute__((aligned(16))) char lds[2][(BM + BN) * STEP_BYTES];
+// The same moved straight from memory into LDS (16 bytes a lane, no
+// registers), for operands whose rows start on 16 bytes and end on a whole
+// chunk.  The hardware places a wavefront's 64 chunks one after another, so
+// the exchange of chunks within a row is made on the addresses read.  A chunk
+// outside the operand gets an offset past the buffer's range, which reads 0.
+constexpr uint32_t OUT_OF_RANGE = 0x80000000u;
 
-    const int m0 = (int)(blockIdx.x / tiles_n) * BM, n0 = (int)(blockIdx.x % tiles_n) * BN;
-    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
-    const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
-    const T *a = static_cast<const T *>(p.a), *b = static_cast<const T *>(p.b);
+template <typename T, bool OUTER, int ROWS, int THREADS> struct Direct {
+    static constexpr int EPC = traits<T>::EPC;
+    static constexpr int BK = STEP_BYTES / (int)sizeof(T);
+    static constexpr int CHUNKS = ROWS * STEP_BYTES / 16;
+    static constexpr int CH = (CHUNKS + THREADS - 1) / THREADS;
+    static constexpr int CPR = OUTER ? ROWS / EPC : 8;
+    uint32_t off[CH]; // byte offset of each chunk from the tile's base
+    const char *base;
+    int64_t advance; // bytes from one step to the next
 
-    f32x4 acc[FM][FN] = {};
-    Stage<T, AO, BM, THREADS> sa;
-    Stage<T, BO, BN, THREADS> sb;
-    const int steps = (p.K + BK - 1) / BK;
-    if (steps > 0) {
-        sa.load(a, p.lda, m0, p.M, 0, p.K);
-        sb.load(b, p.ldb, n0, p.N, 0, p.K);
-        sa.store(lds[0]);
-        sb.store(lds[0] + BM * STEP_BYTES);
-    }
-    __syncthreads();
-    for (int t = 0; t < steps; t++) {
-        const char *ta = lds[t & 1], *tb = ta + BM * STEP_BYTES;
-        const bool more = t + 1 < steps;
-        if (more) {
-            sa.load(a, p.lda, m0, p.M, (t + 1) * BK, p.K);
-            sb.load(b, p.ldb, n0, p.N, (t + 1) * BK, p.K);
+    __device__ __forceinline__ void init(const T *p, int64_t ld, int r0, int rows, int k0)
+    {
+        base = reinterpret_cast<const char *>(OUTER ? p + (int64_t)k0 * ld + r0 : p + (int64_t)r0 * ld + k0);
+        advance = OUTER ? BK * ld * (int64_t)sizeof(T) : STEP_BYTES;
+#pragma unroll
+        for (int c = 0; c < CH; c++) {
+            const int q = threadIdx.x + c * THREADS;
+            if constexpr (!OUTER) {
+                const int r = q / 8, ch = (q % 8) ^ (r & 7);
+                off[c] = r0 + r < rows ? (uint32_t)(r * ld * (int64_t)sizeof(T)) + ch * 16 : OUT_OF_RANGE;
+            } else {
+                const int k = q / CPR, ch = (q % CPR) ^ outer_swizzle<T, ROWS>(k);
+                off[c] = r0 + ch * EPC < rows ? (uint32_t)(k * ld * (int64_t)sizeof(T)) + ch * 16 : OUT_OF_RANGE;
+            }
         }
+    }
+
+    // Starts the copies of one step; `left`: values of k from its first on.
+    __device__ __forceinline__ void start(char *tile, int left)
+    {
+        const __amdgpu_buffer_rsrc_t rsrc =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(base), 0, (int)OUT_OF_RANGE, 0x00020000);
+#pragma unroll
+        for (int c = 0; c < CH; c++) {
+            const int first = (threadIdx.x / WAVE) * WAVE + c * THREADS;
+            if (CHUNKS % THREADS != 0 && first >= CHUNKS)
+                break;
+            uint32_t o = off[c];
+            if (left < BK) {
+                const int q = threadIdx.x + c * THREADS;
+                const int k = OUTER ? q / CPR : ((q % 8) ^ ((q / 8) & 7)) * EPC;
+                o = k < left ? o : OUT_OF_RANGE;
+            }
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rsrc, (__attribute__((address_space(3))) void *)(tile + first * 16), 16, o, 0, 0, 0);
+        }
+        base += advance;
+    }
+};
+
+template <typename T, int BM, int BN, int WM, int WN, bool AO, bool BO> struct Tile {
+    static constexpr int THREADS = WM * WN * WAVE;
+    static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
+    f32x4 acc[FM][FN];
+
+    // acc += the products of one step's tiles
+    __device__ __forceinline__ void step(const char *ta, const char *tb, int wm, int wn, int lane)
+    {
 #pragma unroll
         for (int kk = 0; kk < 2; kk++) {
             Frag fa[FM], fb[FN];
@@ -309,39 +347,147 @@ __global__ __launch_bounds__(WM *WN *WAVE) void gemm_kernel(GemmArgs p, int tile
                 for (int j = 0; j < FN; j++)
                     acc[i][j] = mma<T>(fb[j], fa[i], acc[i][j]);
         }
-        if (more) {
-            sa.store(lds[(t + 1) & 1]);
-            sb.store(lds[(t + 1) & 1] + BM * STEP_BYTES);
+    }
+};
+
+// Waits for this wavefront's copies into LDS, then for the other wavefronts;
+// no access to memory moves across.
+__device__ __forceinline__ void copies_done()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(WAIT_LOADS);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Which tile a workgroup takes.  Consecutive workgroups go to the 8 XCDs in
+// turn; each XCD gets a contiguous run of tiles, walked in bands of GROUP tile
+// rows, so the operand rows that it reads again stay in its own L2.
+constexpr int XCDS = 8, GROUP = 8;
+
+__device__ __forceinline__ void tile_of(unsigned id, unsigned tiles_m, unsigned tiles_n, unsigned &tm, unsigned &tn)
+{
+    const unsigned total = tiles_m * tiles_n, per = total / XCDS, rest = total % XCDS;
+    const unsigned x = id % XCDS, at = id / XCDS;
+    id = x * per + (x < rest ? x : rest) + at;
+    const unsigned band = GROUP * tiles_n, first = id / band * GROUP;
+    const unsigned high = tiles_m - first < GROUP ? tiles_m - first : GROUP;
+    tm = first + id % band % high;
+    tn = id % band / high;
+}
+
+template <typename T, int BM, int BN, int WM, int WN, bool AO, bool BO, bool DIRECT>
+__global__ __launch_bounds__(WM *WN *WAVE) void gemm_kernel(GemmArgs p, int tiles_m, int tiles_n)
+{
+    constexpr int THREADS = WM * WN * WAVE;
+    constexpr int BK = STEP_BYTES / (int)sizeof(T);
+    constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
+    constexpr int AB = BM * STEP_BYTES, BB = BN * STEP_BYTES;
+    // two buffers as objects of their own: the compiler then knows that the
+    // copies into one do not touch what is read from the other
+    __shared__ __attribute__((aligned(1024))) char l0[AB + BB];
+    __shared__ __attribute__((aligned(1024))) char l1[AB + BB];
+
+    unsigned tm, tn;
+    tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    const int m0 = (int)tm * BM, n0 = (int)tn * BN;
+    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
+    const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
+    const T *a = static_cast<const T *>(p.a), *b = static_cast<const T *>(p.b);
+    const int steps = (p.K + BK - 1) / BK;
+    Tile<T, BM, BN, WM, WN, AO, BO> t;
+#pragma unroll
+    for (int i = 0; i < FM; i++)
+#pragma unroll
+        for (int j = 0; j < FN; j++)
+            t.acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    if constexpr (DIRECT) {
+        Direct<T, AO, BM, THREADS> da;
+        Direct<T, BO, BN, THREADS> db;
+        da.init(a, p.lda, m0, p.M, 0);
+        db.init(b, p.ldb, n0, p.N, 0);
+        if (steps > 0) {
+            da.start(l0, p.K);
+            db.start(l0 + AB, p.K);
+        }
+        int s = 0;
+        for (; s + 1 < steps; s += 2) {
+            copies_done();
+            da.start(l1, p.K - (s + 1) * BK);
+            db.start(l1 + AB, p.K - (s + 1) * BK);
+            t.step(l0, l0 + AB, wm, wn, lane);
+            copies_done();
+            if (s + 2 < steps) {
+                da.start(l0, p.K - (s + 2) * BK);
+                db.start(l0 + AB, p.K - (s + 2) * BK);
+            }
+            t.step(l1, l1 + AB, wm, wn, lane);
+        }
+        copies_done();
+        if (s < steps)
+            t.step(l0, l0 + AB, wm, wn, lane);
+        __syncthreads();
+    } else {
+        Stage<T, AO, BM, THREADS> sa;
+        Stage<T, BO, BN, THREADS> sb;
+        if (steps > 0) {
+            sa.load(a, p.lda, m0, p.M, 0, p.K);
+            sb.load(b, p.ldb, n0, p.N, 0, p.K);
+            sa.store(l0);
+            sb.store(l0 + AB);
         }
         __syncthreads();
+        for (int s = 0; s < steps; s++) {
+            char *cur = s & 1 ? l1 : l0, *next = s & 1 ? l0 : l1;
+            if (s + 1 < steps) {
+                sa.load(a, p.lda, m0, p.M, (s + 1) * BK, p.K);
+                sb.load(b, p.ldb, n0, p.N, (s + 1) * BK, p.K);
+            }
+            t.step(cur, cur + AB, wm, wn, lane);
+            if (s + 1 < steps) {
+                sa.store(next);
+                sb.store(next + AB);
+            }
+            __syncthreads();
+        }
     }
+    // The finished tile goes through LDS, 16 rows of each row of wavefronts at
+    // a time, so that whole rows are read and written from consecutive lanes.
+    constexpr int W = 8, PITCH = BN + 4, ROWS = WM * 16;
+    static_assert(ROWS * PITCH * 4 <= AB + BB, "a pass of the epilogue fits one buffer");
 #pragma unroll
     for (int i = 0; i < FM; i++) {
-        const int m = m0 + wm + i * 16 + (lane & 15);
-        if (m >= p.M)
-            continue;
+        float *o = reinterpret_cast<float *>(i & 1 ? l1 : l0);
 #pragma unroll
-        for (int j = 0; j < FN; j++) {
-            const int n = n0 + wn + j * 16 + (lane >> 4) * 4;
-            if (n < p.N) {
-                const float s[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                epilogue4<T>(p, m, n, s);
+        for (int j = 0; j < FN; j++)
+            *reinterpret_cast<f32x4 *>(o + ((wave / WN) * 16 + (lane & 15)) * PITCH + wn + j * 16 + (lane >> 4) * 4) =
+                t.acc[i][j];
+        __syncthreads();
+#pragma unroll 1
+        for (int q = threadIdx.x; q < ROWS * BN / W; q += THREADS) {
+            const int r = q / (BN / W), n = n0 + q % (BN / W) * W;
+            const int m = m0 + r / 16 * (BM / WM) + i * 16 + r % 16;
+            if (m < p.M && n < p.N) {
+                float v[W];
+                __builtin_memcpy(v, o + r * PITCH + n - n0, sizeof v);
+                epilogue<T, W>(p, m, n, v);
             }
         }
     }
 }
 
-template <typename T, int BM, int BN, int WM, int WN>
+template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
 hipError_t run_tile(const GemmArgs &a, int layout, hipStream_t s)
 {
     const int64_t tm = ((int64_t)a.M + BM - 1) / BM, tn = ((int64_t)a.N + BN - 1) / BN;
     const dim3 grid((unsigned)(tm * tn)), block(WM * WN * WAVE);
     if (layout == 0)
-        gemm_kernel<T, BM, BN, WM, WN, false, false><<<grid, block, 0, s>>>(a, (int)tn);
+        gemm_kernel<T, BM, BN, WM, WN, false, false, DIRECT><<<grid, block, 0, s>>>(a, (int)tm, (int)tn);
     else if (layout == GEMM_B_OUTER)
-        gemm_kernel<T, BM, BN, WM, WN, false, true><<<grid, block, 0, s>>>(a, (int)tn);
+        gemm_kernel<T, BM, BN, WM, WN, false, true, DIRECT><<<grid, block, 0, s>>>(a, (int)tm, (int)tn);
     else
-        gemm_kernel<T, BM, BN, WM, WN, true, true><<<grid, block, 0, s>>>(a, (int)tn);
+        gemm_kernel<T, BM, BN, WM, WN, true, true, DIRECT><<<grid, block, 0, s>>>(a, (int)tm, (int)tn);
     return hipGetLastError();
 }
 
@@ -363,21 +509,21 @@ template <typename T> __global__ __launch_bounds__(AG_THREADS) void act_grad_ker
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     for (int64_t m = r0; m < r1; m++) {
         float d[4], z[4];
-        load4(static_cast<const T *>(p.dy) + m * p.lddy + n, valid, d);
+        load_n<T, 4>(static_cast<const T *>(p.dy) + m * p.lddy + n, valid, d);
         if (p.act != FA_ACT_NONE) {
-            load4(static_cast<const T *>(p.pre) + m * p.ldp + n, valid, z);
+            load_n<T, 4>(static_cast<const T *>(p.pre) + m * p.ldp + n, valid, z);
 #pragma unroll
             for (int i = 0; i < 4; i++)
                 d[i] *= act_slope(z[i], p.act);
         }
         if (p.dz)
-            store4(static_cast<T *>(p.dz) + m * p.N + n, valid, d);
+            store_n<T, 4>(static_cast<T *>(p.dz) + m * p.N + n, valid, d);
 #pragma unroll
         for (int i = 0; i < 4; i++)
             sum[i] += d[i];
     }
     if (p.db)
-        store4(p.part + (int64_t)blockIdx.y * p.N + n, valid, sum);
+        store_n<float, 4>(p.part + (int64_t)blockIdx.y * p.N + n, valid, sum);
 }
 
 template <typename T> __global__ __launch_bounds__(AG_THREADS) void column_join_kernel(ActGradArgs p, int64_t parts)
@@ -395,13 +541,35 @@ template <typename T> __global__ __launch_bounds__(AG_THREADS) void column_join_
 
 size_t gemm_workspace_bytes(int, int64_t, int64_t, int64_t, int, int) { return 0; }
 
+namespace {
+
+// Whether an operand's rows start on 16 bytes and end on a whole chunk, and a
+// tile of it stays within the 31 bits of a buffer offset.
+bool direct_ok(const void *p, int64_t ld, int64_t row, size_t es)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * (int64_t)es % 16 == 0 && row * (int64_t)es % 16 == 0 &&
+           ld * (int64_t)es * 257 < (int64_t)OUT_OF_RANGE;
+}
+
+template <typename T> hipError_t gemm_of(const GemmArgs &a, int layout, hipStream_t s)
+{
+    const bool direct = direct_ok(a.a, a.lda, layout & GEMM_A_OUTER ? a.M : a.K, sizeof(T)) &&
+                        direct_ok(a.b, a.ldb, layout & GEMM_B_OUTER ? a.N : a.K, sizeof(T));
+    const int64_t big = (((int64_t)a.M + 255) / 256) * (((int64_t)a.N + 255) / 256);
+    if (direct && big >= 200)
+        return run_tile<T, 256, 256, 2, 4, true>(a, layout, s);
+    if (direct)
+        return run_tile<T, 128, 128, 2, 2, true>(a, layout, s);
+    return run_tile<T, 128, 128, 2, 2, false>(a, layout, s);
+}
+
+} // namespace
+
 hipError_t launch_gemm(const GemmArgs &a, int dt, int layout, void *, int, hipStream_t s)
 {
     if (a.M == 0 || a.N == 0)
         return hipSuccess;
-    if (dt == FA_BF16)
-        return run_tile<__bf16, 128, 128, 2, 2>(a, layout, s);
-    return run_tile<float, 128, 128, 2, 2>(a, layout, s);
+    return dt == FA_BF16 ? gemm_of<__bf16>(a, layout, s) : gemm_of<float>(a, layout, s);
 }
 
 int64_t act_grad_partials(int64_t M, int64_t N, int cus)

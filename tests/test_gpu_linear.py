@@ -187,6 +187,24 @@ def test_backward(shape, dt):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
+# enough tiles for the larger tile sizes, ragged at both edges; the last two
+# unaligned
+LARGE = [(2058, 2184, 72), (2600, 5400, 136), (2600, 136, 5400), (136, 2600, 5400), (2059, 2183, 71), (2601, 5399, 67)]
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("shape", LARGE, ids=str)
+def test_large_tiles(shape, dt):
+    M, N, K = shape
+    t = DTYPES[dt]
+    x, w, dy = rnd((M, K), t, 1), rnd((N, K), t, 2, K ** -0.5), rnd((M, N), t, 3)
+    bias, res = rnd((N,), t, 4), rnd((M, N), t, 5)
+    pre = torch.empty(M, N, dtype=t, device="cuda")
+    out = fa.linear_forward(x, w, bias, act="silu", residual=res, preact=pre)
+    check_forward(x, w, bias, "silu", res, 1.0, out, pre)
+    check_backward(dy, x, w, "none", None, 1.0, *fa.linear_backward(dy, x, w, db=True))
+
+
 @pytest.mark.parametrize("act", ["none", "gelu"])
 @pytest.mark.parametrize("only", ["dx", "dw", "db"])
 def test_backward_each_gradient_alone(only, act):

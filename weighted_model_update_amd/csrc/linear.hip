@@ -376,8 +376,10 @@ __device__ __forceinline__ void tile_of(unsigned id, unsigned tiles_m, unsigned 
     tn = id % band / high;
 }
 
+// Workgroup (tile, split): the sums over k in [split * kper, + kper).  With
+// more than one split they go to `part` [split][M][N], else to the epilogue.
 template <typename T, int BM, int BN, int WM, int WN, bool AO, bool BO, bool DIRECT>
-__global__ __launch_bounds__(WM *WN *WAVE) void gemm_kernel(GemmArgs p, int tiles_m, int tiles_n)
+__global__ __launch_bounds__(WM *WN *WAVE) void gemm_kernel(GemmArgs p, int tiles_m, int tiles_n, int kper, float *part)
 {
     constexpr int THREADS = WM * WN * WAVE;
     constexpr int BK = STEP_BYTES / (int)sizeof(T);
@@ -394,7 +396,8 @@ __global__ __launch_bounds__(WM *WN *WAVE) void gemm_kernel(GemmArgs p, int tile
     const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
     const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
     const T *a = static_cast<const T *>(p.a), *b = static_cast<const T *>(p.b);
-    const int steps = (p.K + BK - 1) / BK;
+    const int k0 = blockIdx.y * kper, kend = p.K - k0 < kper ? p.K : k0 + kper;
+    const int steps = (kend - k0 + BK - 1) / BK;
     Tile<T, BM, BN, WM, WN, AO, BO> t;
 #pragma unroll
     for (int i = 0; i < FM; i++)
@@ -405,22 +408,22 @@ __global__ __launch_bounds__(WM *WN *WAVE) void gemm_kernel(GemmArgs p, int tile
     if constexpr (DIRECT) {
         Direct<T, AO, BM, THREADS> da;
         Direct<T, BO, BN, THREADS> db;
-        da.init(a, p.lda, m0, p.M, 0);
-        db.init(b, p.ldb, n0, p.N, 0);
+        da.init(a, p.lda, m0, p.M, k0);
+        db.init(b, p.ldb, n0, p.N, k0);
         if (steps > 0) {
-            da.start(l0, p.K);
-            db.start(l0 + AB, p.K);
+            da.start(l0, kend - k0);
+            db.start(l0 + AB, kend - k0);
         }
         int s = 0;
         for (; s + 1 < steps; s += 2) {
             copies_done();
-            da.start(l1, p.K - (s + 1) * BK);
-            db.start(l1 + AB, p.K - (s + 1) * BK);
+            da.start(l1, kend - k0 - (s + 1) * BK);
+            db.start(l1 + AB, kend - k0 - (s + 1) * BK);
             t.step(l0, l0 + AB, wm, wn, lane);
             copies_done();
             if (s + 2 < steps) {
-                da.start(l0, p.K - (s + 2) * BK);
-                db.start(l0 + AB, p.K - (s + 2) * BK);
+                da.start(l0, kend - k0 - (s + 2) * BK);
+                db.start(l0 + AB, kend - k0 - (s + 2) * BK);
             }
             t.step(l1, l1 + AB, wm, wn, lane);
         }
@@ -432,8 +435,8 @@ __global__ __launch_bounds__(WM *WN *WAVE) void gemm_kernel(GemmArgs p, int tile
         Stage<T, AO, BM, THREADS> sa;
         Stage<T, BO, BN, THREADS> sb;
         if (steps > 0) {
-            sa.load(a, p.lda, m0, p.M, 0, p.K);
-            sb.load(b, p.ldb, n0, p.N, 0, p.K);
+            sa.load(a, p.lda, m0, p.M, k0, kend);
+            sb.load(b, p.ldb, n0, p.N, k0, kend);
             sa.store(l0);
             sb.store(l0 + AB);
         }
@@ -441,8 +444,8 @@ __global__ __launch_bounds__(WM *WN *WAVE) void gemm_kernel(GemmArgs p, int tile
         for (int s = 0; s < steps; s++) {
             char *cur = s & 1 ? l1 : l0, *next = s & 1 ? l0 : l1;
             if (s + 1 < steps) {
-                sa.load(a, p.lda, m0, p.M, (s + 1) * BK, p.K);
-                sb.load(b, p.ldb, n0, p.N, (s + 1) * BK, p.K);
+                sa.load(a, p.lda, m0, p.M, k0 + (s + 1) * BK, kend);
+                sb.load(b, p.ldb, n0, p.N, k0 + (s + 1) * BK, kend);
             }
             t.step(cur, cur + AB, wm, wn, lane);
             if (s + 1 < steps) {
@@ -471,23 +474,57 @@ __global__ __launch_bounds__(WM *WN *WAVE) void gemm_kernel(GemmArgs p, int tile
             if (m < p.M && n < p.N) {
                 float v[W];
                 __builtin_memcpy(v, o + r * PITCH + n - n0, sizeof v);
-                epilogue<T, W>(p, m, n, v);
+                if (part)
+                    store_n<float, W>(part + ((int64_t)blockIdx.y * p.M + m) * p.N + n, p.N - n, v);
+                else
+                    epilogue<T, W>(p, m, n, v);
             }
         }
     }
 }
 
-template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
-hipError_t run_tile(const GemmArgs &a, int layout, hipStream_t s)
+// Joins the splits' sums in split order and finishes them.
+constexpr int JOIN_THREADS = 256, JOIN_W = 4;
+
+template <typename T> __global__ __launch_bounds__(JOIN_THREADS) void join_kernel(GemmArgs p, const float *part, int splits)
 {
+    const int64_t groups = (p.N + JOIN_W - 1) / JOIN_W, at = (int64_t)blockIdx.x * JOIN_THREADS + threadIdx.x;
+    if (at >= p.M * groups)
+        return;
+    const int64_t m = at / groups;
+    const int n = (int)(at % groups) * JOIN_W;
+    float s[JOIN_W] = {};
+#pragma unroll 4
+    for (int z = 0; z < splits; z++) {
+        float v[JOIN_W];
+        load_n<float, JOIN_W>(part + ((int64_t)z * p.M + m) * p.N + n, p.N - n, v);
+#pragma unroll
+        for (int i = 0; i < JOIN_W; i++)
+            s[i] += v[i];
+    }
+    epilogue<T, JOIN_W>(p, m, n, s);
+}
+
+template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
+hipError_t run_tile(const GemmArgs &a, int layout, int splits, float *ws, hipStream_t s)
+{
+    constexpr int BK = STEP_BYTES / (int)sizeof(T);
     const int64_t tm = ((int64_t)a.M + BM - 1) / BM, tn = ((int64_t)a.N + BN - 1) / BN;
-    const dim3 grid((unsigned)(tm * tn)), block(WM * WN * WAVE);
+    const int steps = std::max(1, (a.K + BK - 1) / BK), per = (steps + splits - 1) / splits;
+    splits = (steps + per - 1) / per;
+    float *part = splits > 1 ? ws : nullptr;
+    const dim3 grid((unsigned)(tm * tn), (unsigned)splits), block(WM * WN * WAVE);
     if (layout == 0)
-        gemm_kernel<T, BM, BN, WM, WN, false, false, DIRECT><<<grid, block, 0, s>>>(a, (int)tm, (int)tn);
+        gemm_kernel<T, BM, BN, WM, WN, false, false, DIRECT><<<grid, block, 0, s>>>(a, (int)tm, (int)tn, per * BK, part);
     else if (layout == GEMM_B_OUTER)
-        gemm_kernel<T, BM, BN, WM, WN, false, true, DIRECT><<<grid, block, 0, s>>>(a, (int)tm, (int)tn);
+        gemm_kernel<T, BM, BN, WM, WN, false, true, DIRECT><<<grid, block, 0, s>>>(a, (int)tm, (int)tn, per * BK, part);
     else
-        gemm_kernel<T, BM, BN, WM, WN, true, true, DIRECT><<<grid, block, 0, s>>>(a, (int)tm, (int)tn);
+        gemm_kernel<T, BM, BN, WM, WN, true, true, DIRECT><<<grid, block, 0, s>>>(a, (int)tm, (int)tn, per * BK, part);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !part)
+        return e;
+    const int64_t groups = (int64_t)a.M * ((a.N + JOIN_W - 1) / JOIN_W);
+    join_kernel<T><<<(unsigned)((groups + JOIN_THREADS - 1) / JOIN_THREADS), JOIN_THREADS, 0, s>>>(a, part, splits);
     return hipGetLastError();
 }
 
@@ -539,8 +576,6 @@ template <typename T> __global__ __launch_bounds__(AG_THREADS) void column_join_
 
 } // namespace
 
-size_t gemm_workspace_bytes(int, int64_t, int64_t, int64_t, int, int) { return 0; }
-
 namespace {
 
 // Whether an operand's rows start on 16 bytes and end on a whole chunk, and a
@@ -551,25 +586,78 @@ bool direct_ok(const void *p, int64_t ld, int64_t row, size_t es)
            ld * (int64_t)es * 257 < (int64_t)OUT_OF_RANGE;
 }
 
-template <typename T> hipError_t gemm_of(const GemmArgs &a, int layout, hipStream_t s)
+enum { TILE_256, TILE_128, TILE_64, TILE_THIN_N, TILE_THIN_M };
+
+struct Plan {
+    int tile, splits;
+};
+
+int64_t tiles(int64_t M, int64_t N, int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
+
+Plan plan_of(int64_t M, int64_t N, int64_t K, size_t es, int cus)
 {
-    const bool direct = direct_ok(a.a, a.lda, layout & GEMM_A_OUTER ? a.M : a.K, sizeof(T)) &&
-                        direct_ok(a.b, a.ldb, layout & GEMM_B_OUTER ? a.N : a.K, sizeof(T));
-    const int64_t big = (((int64_t)a.M + 255) / 256) * (((int64_t)a.N + 255) / 256);
-    if (direct && big >= 200)
-        return run_tile<T, 256, 256, 2, 4, true>(a, layout, s);
-    if (direct)
-        return run_tile<T, 128, 128, 2, 2, true>(a, layout, s);
-    return run_tile<T, 128, 128, 2, 2, false>(a, layout, s);
+    if (tiles(M, N, 256, 256) * 4 >= 3 * cus)
+        return {TILE_256, 1};
+    int tile = TILE_64;
+    int64_t count = tiles(M, N, 64, 64);
+    if (N <= 16) {
+        tile = TILE_THIN_N;
+        count = tiles(M, N, 128, 16);
+    } else if (M <= 16) {
+        tile = TILE_THIN_M;
+        count = tiles(M, N, 16, 128);
+    } else if (tiles(M, N, 128, 128) >= cus) {
+        tile = TILE_128;
+        count = tiles(M, N, 128, 128);
+    }
+    // fill the chip, at least 4 steps of k a split
+    const int64_t steps = K * (int64_t)es / STEP_BYTES;
+    const int64_t want = tile == TILE_128 ? 2 * cus : 4 * cus;
+    const int64_t splits = std::min<int64_t>(std::min<int64_t>(want / std::max<int64_t>(count, 1), steps / 4), 64);
+    return {tile, (int)std::max<int64_t>(1, splits)};
+}
+
+template <typename T, bool DIRECT> hipError_t run_plan(const GemmArgs &a, int layout, Plan p, float *ws, hipStream_t s)
+{
+    switch (p.tile) {
+    case TILE_256:
+        if constexpr (DIRECT)
+            return run_tile<T, 256, 256, 2, 4, true>(a, layout, 1, ws, s);
+        [[fallthrough]];
+    case TILE_128:
+        return run_tile<T, 128, 128, 2, 2, DIRECT>(a, layout, p.splits, ws, s);
+    case TILE_64:
+        return run_tile<T, 64, 64, 2, 2, DIRECT>(a, layout, p.splits, ws, s);
+    case TILE_THIN_N:
+        return run_tile<T, 128, 16, 4, 1, DIRECT>(a, layout, p.splits, ws, s);
+    default:
+        return run_tile<T, 16, 128, 1, 4, DIRECT>(a, layout, p.splits, ws, s);
+    }
+}
+
+template <typename T> hipError_t gemm_of(const GemmArgs &a, int layout, float *ws, int cus, hipStream_t s)
+{
+    const Plan p = plan_of(a.M, a.N, a.K, sizeof(T), cus);
+    if (direct_ok(a.a, a.lda, layout & GEMM_A_OUTER ? a.M : a.K, sizeof(T)) &&
+        direct_ok(a.b, a.ldb, layout & GEMM_B_OUTER ? a.N : a.K, sizeof(T)))
+        return run_plan<T, true>(a, layout, p, ws, s);
+    return run_plan<T, false>(a, layout, p, ws, s);
 }
 
 } // namespace
 
-hipError_t launch_gemm(const GemmArgs &a, int dt, int layout, void *, int, hipStream_t s)
+size_t gemm_workspace_bytes(int dt, int64_t M, int64_t N, int64_t K, int, int cus)
+{
+    const Plan p = plan_of(M, N, K, dt == FA_BF16 ? 2 : 4, cus);
+    return p.splits > 1 ? (size_t)p.splits * M * N * sizeof(float) : 0;
+}
+
+hipError_t launch_gemm(const GemmArgs &a, int dt, int layout, void *ws, int cus, hipStream_t s)
 {
     if (a.M == 0 || a.N == 0)
         return hipSuccess;
-    return dt == FA_BF16 ? gemm_of<__bf16>(a, layout, s) : gemm_of<float>(a, layout, s);
+    float *part = static_cast<float *>(ws);
+    return dt == FA_BF16 ? gemm_of<__bf16>(a, layout, part, cus, s) : gemm_of<float>(a, layout, part, cus, s);
 }
 
 int64_t act_grad_partials(int64_t M, int64_t N, int cus)

@@ -95,7 +95,7 @@ def check(z, idx, val, n, tau=1.0, teacher_lse=None, row_weight=None, in_place=F
 @pytest.mark.parametrize("dt", list(DTYPES))
 @pytest.mark.parametrize("R,V,ks", [(1, 1, [1]), (2, 3, [2, 3]), (4, 64, [8]), (3, 257, [16, 1, 30]), (9, 1000, [20, 20, 20, 20]),
                                     (2, 4099, [256]), (3, 8200, [64] * 16), (2, 32003, [100, 50]), (1, 70001, [32] * 3),
-                                    (2, 131073, [200])])
+                                    (2, 131073, [200]), (2, 5000, [256] * 16), (2, 300, [3] * 64)])
 def test_against_the_definition(R, V, ks, dt):
     z = rnd((R, V), R * V + len(ks), 2.5).to(DTYPES[dt]).cuda()
     idx, val = lists(R, V, ks, 7 + V)

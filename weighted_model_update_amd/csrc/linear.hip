@@ -529,49 +529,71 @@ hipError_t run_tile(const GemmArgs &a, int layout, int splits, float *ws, hipStr
 }
 
 // ------------------------------------------------------------ dz and db
-// Four columns a thread, a workgroup's rows in order: a column's partial sum
-// is added in fp32 in row order, and the partials in workgroup order, so db
-// is the same bits on every call.
-constexpr int AG_THREADS = 256;
-constexpr int AG_COLS = AG_THREADS * 4;
+// Eight columns a thread, a workgroup's rows in order: a column's partial sum
+// is added in fp32 in row order, and the partials in a fixed order, so db is
+// the same bits on every call.
+constexpr int AG_THREADS = 256, AG_W = 8, AG_U = 4;
+constexpr int AG_COLS = AG_THREADS * AG_W;
 constexpr int AG_MIN_ROWS = 16;
 
 template <typename T> __global__ __launch_bounds__(AG_THREADS) void act_grad_kernel(ActGradArgs p, int64_t rows_per)
 {
-    const int64_t n = ((int64_t)blockIdx.x * AG_THREADS + threadIdx.x) * 4;
+    const int64_t n = ((int64_t)blockIdx.x * AG_THREADS + threadIdx.x) * AG_W;
     if (n >= p.N)
         return;
-    const int valid = (int)(p.N - n < 4 ? p.N - n : 4);
+    const int valid = (int)(p.N - n < AG_W ? p.N - n : AG_W);
     const int64_t r0 = (int64_t)blockIdx.y * rows_per, r1 = r0 + rows_per < p.M ? r0 + rows_per : p.M;
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t m = r0; m < r1; m++) {
-        float d[4], z[4];
-        load_n<T, 4>(static_cast<const T *>(p.dy) + m * p.lddy + n, valid, d);
-        if (p.act != FA_ACT_NONE) {
-            load_n<T, 4>(static_cast<const T *>(p.pre) + m * p.ldp + n, valid, z);
+    float sum[AG_W] = {};
+    for (int64_t m0 = r0; m0 < r1; m0 += AG_U) {
+        float d[AG_U][AG_W], z[AG_U][AG_W];
 #pragma unroll
-            for (int i = 0; i < 4; i++)
-                d[i] *= act_slope(z[i], p.act);
+        for (int u = 0; u < AG_U; u++) { // rows past the end read nothing and add 0
+            const int v = m0 + u < r1 ? valid : 0;
+            load_n<T, AG_W>(static_cast<const T *>(p.dy) + (m0 + u) * p.lddy + n, v, d[u]);
+            if (p.act != FA_ACT_NONE)
+                load_n<T, AG_W>(static_cast<const T *>(p.pre) + (m0 + u) * p.ldp + n, v, z[u]);
         }
-        if (p.dz)
-            store_n<T, 4>(static_cast<T *>(p.dz) + m * p.N + n, valid, d);
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            sum[i] += d[i];
+        for (int u = 0; u < AG_U; u++) {
+            if (p.act != FA_ACT_NONE) {
+#pragma unroll
+                for (int i = 0; i < AG_W; i++)
+                    d[u][i] *= act_slope(z[u][i], p.act);
+            }
+            if (p.dz)
+                store_n<T, AG_W>(static_cast<T *>(p.dz) + (m0 + u) * p.N + n, m0 + u < r1 ? valid : 0, d[u]);
+#pragma unroll
+            for (int i = 0; i < AG_W; i++)
+                sum[i] += d[u][i];
+        }
     }
     if (p.db)
-        store_n<float, 4>(p.part + (int64_t)blockIdx.y * p.N + n, valid, sum);
+        store_n<float, AG_W>(p.part + (int64_t)blockIdx.y * p.N + n, valid, sum);
 }
 
-template <typename T> __global__ __launch_bounds__(AG_THREADS) void column_join_kernel(ActGradArgs p, int64_t parts)
+// 64 columns a workgroup: each wavefront adds every CJ_WAVES-th partial, and
+// the wavefronts' sums are added in order.
+constexpr int CJ_WAVES = 8;
+
+template <typename T> __global__ __launch_bounds__(CJ_WAVES *WAVE) void column_join_kernel(ActGradArgs p, int64_t parts)
 {
-    const int64_t n = (int64_t)blockIdx.x * AG_THREADS + threadIdx.x;
-    if (n >= p.N)
-        return;
+    __shared__ float sums[CJ_WAVES][WAVE];
+    const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
+    const int64_t n = (int64_t)blockIdx.x * WAVE + lane;
     float s = 0.f;
-    for (int64_t q = 0; q < parts; q++)
-        s += p.part[q * p.N + n];
-    static_cast<T *>(p.db)[n] = (T)s;
+    if (n < p.N) {
+#pragma unroll 8
+        for (int64_t q = wave; q < parts; q += CJ_WAVES)
+            s += p.part[q * p.N + n];
+    }
+    sums[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && n < p.N) {
+#pragma unroll
+        for (int w = 1; w < CJ_WAVES; w++)
+            s += sums[w][lane];
+        static_cast<T *>(p.db)[n] = (T)s;
+    }
 }
 
 } // namespace
@@ -664,7 +686,7 @@ int64_t act_grad_partials(int64_t M, int64_t N, int cus)
 {
     // enough workgroups for the chip, at least AG_MIN_ROWS rows each
     const int64_t across = (N + AG_COLS - 1) / AG_COLS;
-    const int64_t want = std::max<int64_t>(1, 8 * (int64_t)cus / std::max<int64_t>(across, 1));
+    const int64_t want = std::max<int64_t>(1, 4 * (int64_t)cus / std::max<int64_t>(across, 1));
     return std::max<int64_t>(1, std::min(std::min<int64_t>(want, 1024), (M + AG_MIN_ROWS - 1) / AG_MIN_ROWS));
 }
 
@@ -683,11 +705,11 @@ hipError_t launch_act_grad(const ActGradArgs &a, int dt, int cus, hipStream_t s)
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.db)
         return e;
-    const unsigned g = (unsigned)((a.N + AG_THREADS - 1) / AG_THREADS);
+    const unsigned g = (unsigned)((a.N + WAVE - 1) / WAVE);
     if (dt == FA_BF16)
-        column_join_kernel<__bf16><<<g, AG_THREADS, 0, s>>>(a, parts);
+        column_join_kernel<__bf16><<<g, CJ_WAVES * WAVE, 0, s>>>(a, parts);
     else
-        column_join_kernel<float><<<g, AG_THREADS, 0, s>>>(a, parts);
+        column_join_kernel<float><<<g, CJ_WAVES * WAVE, 0, s>>>(a, parts);
     return hipGetLastError();
 }
 

@@ -144,6 +144,21 @@ __device__ __forceinline__ float lse_of(float m, float s, float inv_tau)
     return m == NEG_INF && s == 0.f ? NEG_INF : m * inv_tau + logf(s);
 }
 
+// Partial results of one piece of a row, when rows are split.
+struct TopPiece {
+    float m, s;
+};
+constexpr int SPLIT_MAX = WAVE; // pieces of a row
+
+// The pieces' sums joined, one lane a piece, to every lane.
+__device__ __forceinline__ float lse_of_pieces(const TopPiece *t, int pieces, float c, float inv_tau)
+{
+    const int lane = threadIdx.x % WAVE;
+    const TopPiece q = lane < pieces ? t[lane] : TopPiece{NEG_INF, 0.f};
+    const float M = wave_max(q.m);
+    return lse_of(M, wave_sum(Softmax{q.m, q.s}.scaled_to(M, c)), inv_tau);
+}
+
 // The threads' sums joined, to every thread.
 template <int THREADS> __device__ __forceinline__ void join_block(Softmax &t, float c, float *lds)
 {
@@ -202,7 +217,7 @@ template <> struct Key<__bf16> {
     static __device__ __forceinline__ float value(uint32_t k) { return Key<float>::value(k << 16 | 0xffffu * !(k & 0x8000u)); }
 };
 
-constexpr int TR_SMALL = 256, TR_LARGE = 1024; // threads
+constexpr int TR_SMALL = 256, TR_LARGE = 1024, TR_JOIN = 512; // threads
 constexpr int TR_U = 2;                        // chunks a thread takes per block
 constexpr int TR_PRUNE = 1024;                 // candidates from which on they are cut down to k
 // A block adds at most FA_MAX_TOP - 1 threads' worth above its bound and
@@ -218,40 +233,45 @@ struct TopLds {
     float out_val[FA_MAX_TOP];
     uint32_t best[TR_LARGE];
     int n, hits, kept;
-    int count[16][4];
+    int count[8][16];
     int wave[TR_LARGE / WAVE];
     float red[TR_LARGE / WAVE];
 };
 
-// The largest t with at least k of the n keys at or above it, two bits of t a
-// step: each wavefront counts by ballot and adds to the step's counters.
+// The largest t with at least k of the n keys at or above it, four bits of t
+// a step: each wavefront counts the keys at or above the 15 values tried by
+// ballot, lane b adds the b-th count, and as the counts fall with b the next
+// digit is how many of them reach k.  (Two bits a step took twice the
+// barriers: 27.5 and 24.4 us for a row of 151936 fp32 in two kernels.)
 template <typename T, int THREADS>
 __device__ __forceinline__ uint32_t kth_key(TopLds &l, const uint32_t *keys, int n, int k)
 {
-    if (threadIdx.x < 64)
+    constexpr int STEPS = Key<T>::BITS / 4;
+    const int lane = threadIdx.x % WAVE;
+    if (threadIdx.x < STEPS * 16)
         (&l.count[0][0])[threadIdx.x] = 0;
     __syncthreads();
     uint32_t cut = 0;
-    int step = 0;
 #pragma unroll 1
-    for (int s = Key<T>::BITS - 2; s >= 0; s -= 2, step++) {
-        int c1 = 0, c2 = 0, c3 = 0;
+    for (int step = 0; step < STEPS; step++) {
+        const int s = Key<T>::BITS - 4 - 4 * step;
+        int mine = 0;
 #pragma unroll 1
         for (int i0 = 0; i0 < n; i0 += THREADS) {
             const int i = i0 + threadIdx.x;
-            const uint32_t key = i < n ? keys[i] : 0u; // 0 is below every bound tried
-            c1 += __popcll(__ballot(key >= (cut | (1u << s))));
-            c2 += __popcll(__ballot(key >= (cut | (2u << s))));
-            c3 += __popcll(__ballot(key >= (cut | (3u << s))));
+            const uint32_t key = i < n ? keys[i] : 0u; // 0 is below every value tried
+#pragma unroll
+            for (int b = 1; b < 16; b++) {
+                const int c = __popcll(__ballot(key >= (cut | ((uint32_t)b << s))));
+                mine += lane == b ? c : 0;
+            }
         }
-        if (threadIdx.x % WAVE == 0) {
-            atomicAdd(&l.count[step][1], c1);
-            atomicAdd(&l.count[step][2], c2);
-            atomicAdd(&l.count[step][3], c3);
-        }
+        if (mine)
+            atomicAdd(&l.count[step][lane], mine);
         __syncthreads();
-        const uint32_t b = l.count[step][3] >= k ? 3 : l.count[step][2] >= k ? 2 : l.count[step][1] >= k ? 1 : 0;
-        cut |= b << s;
+        const int c = l.count[step][lane & 15];
+        const uint32_t digit = __popcll(__ballot(lane > 0 && lane < 16 && c >= k));
+        cut |= digit << s;
     }
     return cut;
 }
@@ -506,11 +526,6 @@ __device__ __forceinline__ void gather_top(const T *row, int i0, int i1, int k, 
     prune<T, THREADS>(l, n, n < k ? n : k);
 }
 
-// Partial results of one piece of a row, when rows are split.
-struct TopPiece {
-    float m, s;
-};
-
 __device__ __forceinline__ float *piece_vals(const TopRowsArgs &p, int pieces)
 {
     return reinterpret_cast<float *>(static_cast<TopPiece *>(p.ws) + p.R * pieces);
@@ -558,7 +573,7 @@ __global__ __launch_bounds__(THREADS, THREADS == TR_LARGE ? 8 : 4) void top_rows
 
 // Joins a row's pieces: their entries are the candidates, their softmax sums
 // are added in piece order.
-template <typename T> __global__ __launch_bounds__(TR_SMALL) void top_join_kernel(TopRowsArgs p, int pieces)
+template <typename T> __global__ __launch_bounds__(TR_JOIN) void top_join_kernel(TopRowsArgs p, int pieces)
 {
     __shared__ TopLds l;
     const float c = p.inv_tau * LOG2E;
@@ -568,25 +583,25 @@ template <typename T> __global__ __launch_bounds__(TR_SMALL) void top_join_kerne
         if (threadIdx.x == 0)
             l.n = 0;
         __syncthreads();
-        for (int j = threadIdx.x; j < pieces * p.k; j += TR_SMALL)
-            if (idx[j] >= 0) {
+        for (int j = threadIdx.x; j < pieces * p.k; j += TR_JOIN) {
+            const int32_t i = idx[j];
+            const float v = val[j];
+            if (i >= 0) {
                 const int at = atomicAdd(&l.n, 1);
-                l.key[at] = Key<T>::of(val[j]);
-                l.idx[at] = idx[j];
-                l.val[at] = val[j];
+                l.key[at] = Key<T>::of(v);
+                l.idx[at] = i;
+                l.val[at] = v;
             }
+        }
         const TopPiece *t = static_cast<const TopPiece *>(p.ws) + r * pieces;
-        if (threadIdx.x == 0 && p.lse) {
-            float M = NEG_INF, s = 0.f;
-            for (int q = 0; q < pieces; q++)
-                M = fmaxf(M, t[q].m);
-            for (int q = 0; q < pieces; q++)
-                s += Softmax{t[q].m, t[q].s}.scaled_to(M, c);
-            p.lse[r] = lse_of(M, s, p.inv_tau);
+        if (threadIdx.x < WAVE && p.lse) {
+            const float lse = lse_of_pieces(t, pieces, c, p.inv_tau);
+            if (threadIdx.x == 0)
+                p.lse[r] = lse;
         }
         __syncthreads();
-        prune<T, TR_SMALL>(l, l.n, p.k);
-        for (int j = threadIdx.x; j < p.k; j += TR_SMALL) {
+        prune<T, TR_JOIN>(l, l.n, p.k);
+        for (int j = threadIdx.x; j < p.k; j += TR_JOIN) {
             p.idx[r * p.k + j] = l.idx[j];
             p.val[r * p.k + j] = l.val[j];
         }
@@ -597,7 +612,6 @@ template <typename T> __global__ __launch_bounds__(TR_SMALL) void top_join_kerne
 // How rows are split: only while there are fewer rows than CUs, into pieces
 // of at least SPLIT_MIN bytes whose entries the join can hold.
 constexpr int64_t SPLIT_MIN = 16384;
-constexpr int SPLIT_MAX = 64;
 
 void split_rows(int64_t R, int64_t V, size_t es, int64_t most, int cus, int &pieces, int64_t &len)
 {
@@ -614,42 +628,93 @@ void split_rows(int64_t R, int64_t V, size_t es, int64_t most, int cus, int &pie
 constexpr int DI_SMALL = 256, DI_LARGE = 512;
 constexpr int64_t DI_SMALL_BYTES = 16384; // rows up to this take the small workgroup
 
+// LDS of one row's lists, sized by the entries a row can have: per client its
+// numbers, per entry its probability and its slot, and a table with a slot for
+// each distinct index (open addressing, at most half full).
 struct Lists {
-    int32_t idx[FA_MAX_LIST_ENTRIES];
-    float q[FA_MAX_LIST_ENTRIES];
-    int len[FA_MAX_CLIENTS];     // entries in use; 0: the client did not send the row
-    float share[FA_MAX_CLIENTS]; // n_c over the sum of n of the clients that did
-    float kl[FA_MAX_CLIENTS];
-    float mass[FA_MAX_CLIENTS];
+    int *len;     // [clients] entries in use; 0: the client did not send the row
+    float *mass;  // [clients] sum_j q_cj
+    float *kl;    // [clients] sum_j q_cj (log q_cj - z_j / tau)
+    float *share; // [clients] n_c over the sum of n of the clients that sent the row
+    float *q;     // [entries]
+    int *slot;    // [entries] -1: outside the piece
+    int *index;   // [slots] -1: free
+    float *sum;   // [slots]
+    int slots;
+
+    static __host__ __device__ int slots_for(int entries)
+    {
+        int n = 64;
+        while (n < 2 * entries)
+            n *= 2;
+        return n;
+    }
+    static __host__ size_t bytes(int clients, int entries)
+    {
+        return (size_t)(4 * clients + 2 * entries + 2 * slots_for(entries)) * 4;
+    }
+    __device__ __forceinline__ void place(char *at, int clients, int entries)
+    {
+        slots = slots_for(entries);
+        index = reinterpret_cast<int *>(at);
+        sum = reinterpret_cast<float *>(index + slots);
+        q = sum + slots;
+        slot = reinterpret_cast<int *>(q + entries);
+        len = slot + entries;
+        mass = reinterpret_cast<float *>(len + clients);
+        kl = mass + clients;
+        share = kl + clients;
+    }
 };
 
-// The row's lists into LDS: q_cj = exp(v/tau - L_c), each client's mass
-// sum_j q_cj and, with LOSS, sum_j q_cj (log q_cj - log p_j).  One wavefront a
-// client.  A list is used up to its first negative index; one that is not
-// strictly increasing or passes V is left out whole and raises the flag.
+// The row's lists: q_cj = exp(v/tau - L_c) and what is summed over them; with
+// GRAD also each index in [i0, i1) once, with sum_c w_c q_c added up in client
+// order.  One wavefront a client.  A list is used up to its first negative
+// index; one that is not strictly increasing or passes V is left out whole and
+// raises the flag.
 template <typename T, int THREADS, bool LOSS>
-__device__ __forceinline__ void load_lists(const DistillArgs &p, int64_t r, const T *z, float lse, Lists &l)
+__device__ __forceinline__ void load_lists(const DistillArgs &p, int64_t r, const T *z, int i0, int i1, bool grad, Lists &l)
 {
     const int lane = threadIdx.x % WAVE;
+    if (grad) {
+        for (int i = threadIdx.x; i < l.slots; i += THREADS) {
+            l.index[i] = -1;
+            l.sum[i] = 0.f;
+        }
+        __syncthreads();
+    }
     for (int c = threadIdx.x / WAVE; c < p.clients; c += THREADS / WAVE) {
         const int k = p.k[c], at = p.first[c];
         const int32_t *idx = p.idx[c] + r * k;
         const float *val = p.val[c] + r * k;
-        int len = k;
-        for (int j0 = 0; j0 < k; j0 += WAVE) {
-            const uint64_t b = __ballot(j0 + lane < k && idx[j0 + lane] < 0);
-            if (b) {
-                len = j0 + __builtin_ctzll(b);
-                break;
-            }
+        const float given = p.has_tlse ? p.tlse[c][r] : 0.f;
+        constexpr int PER = FA_MAX_TOP / WAVE;
+        int32_t ix[PER];
+        float y[PER];
+#pragma unroll
+        for (int e = 0; e < PER; e++) {
+            const int j = e * WAVE + lane;
+            ix[e] = j < k ? idx[j] : -1;
+            y[e] = j < k ? val[j] * p.inv_tau : NEG_INF;
         }
+        int len = k;
         bool bad = false;
-        float m = NEG_INF, s = 0.f;
-        for (int j = lane; j < len; j += WAVE) {
-            const int i = idx[j];
-            bad |= i >= p.V || (j > 0 && idx[j - 1] >= i);
-            l.idx[at + j] = i;
-            m = fmaxf(m, val[j] * p.inv_tau);
+#pragma unroll
+        for (int e = PER - 1; e >= 0; e--) {
+            const uint64_t b = __ballot(e * WAVE + lane < k && ix[e] < 0);
+            len = b ? e * WAVE + __builtin_ctzll(b) : len;
+        }
+        int32_t last = -1; // the entry before this group's first
+        float m = NEG_INF;
+#pragma unroll
+        for (int e = 0; e < PER; e++) {
+            int32_t before = __shfl_up(ix[e], 1);
+            before = lane == 0 ? last : before;
+            last = __shfl(ix[e], WAVE - 1);
+            if (e * WAVE + lane < len) {
+                bad |= ix[e] >= p.V || before >= ix[e];
+                m = fmaxf(m, y[e]);
+            }
         }
         if (__ballot(bad)) {
             if (lane == 0 && p.err)
@@ -657,22 +722,42 @@ __device__ __forceinline__ void load_lists(const DistillArgs &p, int64_t r, cons
             len = 0;
         }
         m = wave_max(m);
-        for (int j = lane; j < len; j += WAVE) {
-            const float y = val[j] * p.inv_tau;
-            s += y == NEG_INF ? 0.f : expf(y - m);
-        }
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < PER; e++)
+            if (e * WAVE + lane < len)
+                s += y[e] == NEG_INF ? 0.f : expf(y[e] - m);
         s = wave_sum(s);
         if (m == NEG_INF && s == 0.f)
             len = 0; // nothing, or only -inf
-        const float L = p.has_tlse ? p.tlse[c][r] : m + logf(s);
+        const float L = p.has_tlse ? given : m + logf(s);
         float mass = 0.f, kl = 0.f;
-        for (int j = lane; j < len; j += WAVE) {
-            const float lq = val[j] * p.inv_tau - L;
+#pragma unroll
+        for (int e = 0; e < PER; e++) {
+            const int j = e * WAVE + lane;
+            if (j >= len)
+                continue;
+            const float lq = y[e] - L;
             const float q = expf(lq);
-            l.q[at + j] = q;
             mass += q;
             if (LOSS && q != 0.f)
-                kl += q * (lq - ((float)z[l.idx[at + j]] * p.inv_tau - lse));
+                kl += q * (lq - (float)z[ix[e]] * p.inv_tau);
+            if (grad) {
+                int slot = -1;
+                if (ix[e] >= i0 && ix[e] < i1) {
+                    slot = (uint32_t)ix[e] * 0x9E3779B1u >> 7 & (l.slots - 1);
+                    // the table has more slots than entries: a free one, or
+                    // the index's own, comes within one round
+                    for (int tries = 0; tries < l.slots; tries++) {
+                        const int was = atomicCAS(&l.index[slot], -1, ix[e]);
+                        if (was == -1 || was == ix[e])
+                            break;
+                        slot = (slot + 1) & (l.slots - 1);
+                    }
+                }
+                l.q[at + j] = q;
+                l.slot[at + j] = slot;
+            }
         }
         mass = wave_sum(mass);
         kl = wave_sum(kl);
@@ -683,26 +768,24 @@ __device__ __forceinline__ void load_lists(const DistillArgs &p, int64_t r, cons
         }
     }
     __syncthreads();
+    // exact up to 2^24, and rounded no further than fp32 beyond
     float W = 0.f;
     for (int c = 0; c < p.clients; c++)
         W += l.len[c] ? p.n[c] : 0.f;
     for (int c = threadIdx.x; c < p.clients; c += THREADS)
         l.share[c] = l.len[c] ? p.n[c] / W : 0.f;
+    if (grad)
+        // a client has an index once, so its entries touch different slots
+        for (int c = 0; c < p.clients; c++) {
+            __syncthreads();
+            const float w = l.len[c] ? p.n[c] / W : 0.f;
+            for (int j = threadIdx.x; j < l.len[c]; j += THREADS) {
+                const int s = l.slot[p.first[c] + j];
+                if (s >= 0)
+                    l.sum[s] = __builtin_fmaf(w, l.q[p.first[c] + j], l.sum[s]);
+            }
+        }
     __syncthreads();
-}
-
-// Position of index i in a list of len entries from `at`, or -1.
-__device__ __forceinline__ int find(const Lists &l, int at, int len, int i)
-{
-    int lo = 0, hi = len;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (l.idx[at + mid] < i)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    return lo < len && l.idx[at + lo] == i ? lo : -1;
 }
 
 // 16 bytes of gradient to elements [i, i + EPC) of a row, none past `end`
@@ -739,9 +822,10 @@ template <typename T, int THREADS, bool LOSS, int FROM>
 __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs p, int grad_pieces, int64_t len, int stat_pieces)
 {
     constexpr int EPC = Chunk<T>::EPC;
-    constexpr int PER = FA_MAX_LIST_ENTRIES / THREADS;
-    __shared__ Lists l;
+    extern __shared__ __attribute__((aligned(16))) char dynamic[];
     __shared__ float fl[THREADS / WAVE];
+    Lists l;
+    l.place(dynamic, p.clients, p.first[p.clients]);
     const float c2 = p.inv_tau * LOG2E;
     for (int64_t w = blockIdx.x; w < p.R * grad_pieces; w += gridDim.x) {
         const int64_t r = w / grad_pieces;
@@ -750,34 +834,25 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs p, int gra
         const T *z = static_cast<const T *>(p.z) + r * p.ldz;
         T *dz = p.dz ? static_cast<T *>(p.dz) + r * p.lddz : nullptr;
         const float g = p.row_weight ? p.row_weight[r] : 1.f;
-        float lse = 0.f;
+        float lse = 0.f, M = 0.f, kl = 0.f;
+        bool sent = false;
         if (g != 0.f) {
+            load_lists<T, THREADS, LOSS>(p, r, z, i0, i1, dz != nullptr, l);
             if (FROM == LSE_COMPUTE) {
                 const Softmax t = row_softmax<T, THREADS>(z, 0, (int)p.V, c2, fl);
                 lse = lse_of(t.m, t.s, p.inv_tau);
             } else if (FROM == LSE_PIECES) {
-                const TopPiece *t = static_cast<const TopPiece *>(p.ws) + r * stat_pieces;
-                float M = NEG_INF, s = 0.f;
-                for (int q = 0; q < stat_pieces; q++)
-                    M = fmaxf(M, t[q].m);
-                for (int q = 0; q < stat_pieces; q++)
-                    s += Softmax{t[q].m, t[q].s}.scaled_to(M, c2);
-                lse = lse_of(M, s, p.inv_tau);
+                lse = lse_of_pieces(static_cast<const TopPiece *>(p.ws) + r * stat_pieces, stat_pieces, c2, p.inv_tau);
             } else {
                 lse = p.lse[r];
             }
-        }
-        const bool live = g != 0.f && lse != NEG_INF;
-        float M = 0.f, kl = 0.f;
-        bool sent = false;
-        if (live) {
-            load_lists<T, THREADS, LOSS>(p, r, z, lse, l);
-            for (int c = 0; c < p.clients; c++)
-                if (l.len[c]) {
-                    M = __builtin_fmaf(l.share[c], l.mass[c], M);
-                    kl = __builtin_fmaf(l.share[c], l.kl[c], kl);
-                    sent = true;
-                }
+            if (lse != NEG_INF)
+                for (int c = 0; c < p.clients; c++)
+                    if (l.len[c]) {
+                        M = __builtin_fmaf(l.share[c], l.mass[c], M);
+                        kl = __builtin_fmaf(l.share[c], __builtin_fmaf(lse, l.mass[c], l.kl[c]), kl);
+                        sent = true;
+                    }
         }
         if (LOSS && first && threadIdx.x == 0) {
             p.loss[r] = sent ? g * (p.tau * p.tau) * kl : 0.f;
@@ -789,45 +864,13 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs p, int gra
             for (int i = i0 + threadIdx.x * EPC; i < i1; i += THREADS * EPC)
                 store_row(dz, i, i1, zero);
         } else if (dz) {
-            // Listed indices of this piece: the first client that has an index
-            // adds the clients' shares in client order.  z is read before the
-            // dense pass, as dz may be z, and the result written after it.
-            const float gt = g * p.tau;
-            float fix[PER];
-            int32_t where[PER];
-            const int total = p.first[p.clients];
-#pragma unroll
-            for (int e = 0; e < PER; e++) {
-                const int at = e * THREADS + threadIdx.x;
-                where[e] = -1;
-                if (at >= total)
-                    continue;
-                int c = 0;
-                while (p.first[c + 1] <= at)
-                    c++;
-                if (at - p.first[c] >= l.len[c])
-                    continue;
-                const int i = l.idx[at];
-                if (i < i0 || i >= i1)
-                    continue;
-                float Q = l.share[c] * l.q[at];
-                bool mine = true;
-                for (int o = 0; o < p.clients && mine; o++) {
-                    if (o == c)
-                        continue;
-                    const int j = find(l, p.first[o], l.len[o], i);
-                    if (j >= 0 && o < c)
-                        mine = false;
-                    else if (j >= 0)
-                        Q = __builtin_fmaf(l.share[o], l.q[p.first[o] + j], Q);
-                }
-                if (mine) {
-                    where[e] = i;
-                    fix[e] = gt * (M * prob((float)z[i], p.inv_tau, lse) - Q);
-                }
-            }
+            // The listed entries' gradients are taken from z before the dense
+            // pass, as dz may be z, and written after it.
+            const float gt = g * p.tau, gm = gt * M;
+            for (int i = threadIdx.x; i < l.slots; i += THREADS)
+                if (l.index[i] >= 0)
+                    l.sum[i] = gt * (M * prob((float)z[l.index[i]], p.inv_tau, lse) - l.sum[i]);
             __syncthreads();
-            const float gm = gt * M;
             for (int i = i0 + threadIdx.x * EPC; i < i1; i += THREADS * EPC) {
                 const Chunk<T> k = load_row(z, i, i1);
                 float v[EPC];
@@ -837,10 +880,9 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs p, int gra
                 store_row(dz, i, i1, v);
             }
             __syncthreads();
-#pragma unroll
-            for (int e = 0; e < PER; e++)
-                if (where[e] >= 0)
-                    dz[where[e]] = (T)fix[e];
+            for (int i = threadIdx.x; i < l.slots; i += THREADS)
+                if (l.index[i] >= 0)
+                    dz[l.index[i]] = (T)l.sum[i];
         }
         __syncthreads();
     }
@@ -868,7 +910,12 @@ template <typename T, int THREADS, bool LOSS, int FROM>
 hipError_t run_distill(const DistillArgs &a, int pieces, int64_t len, int stat_pieces, int cus, hipStream_t s)
 {
     const unsigned grid = (unsigned)std::min<int64_t>(a.R * pieces, (int64_t)cus * 16);
-    distill_kernel<T, THREADS, LOSS, FROM><<<grid, THREADS, 0, s>>>(a, pieces, len, stat_pieces);
+    const size_t lds = Lists::bytes(a.clients, a.first[a.clients]);
+    static_assert((4 * FA_MAX_CLIENTS + 2 * FA_MAX_LIST_ENTRIES + 4 * FA_MAX_LIST_ENTRIES) * 4 <= 128 << 10, "the largest lists fit in LDS");
+    static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void *>(&distill_kernel<T, THREADS, LOSS, FROM>),
+                                                          hipFuncAttributeMaxDynamicSharedMemorySize, 128 << 10);
+    (void)allowed; // a launch that needs more than the default then fails and says so
+    distill_kernel<T, THREADS, LOSS, FROM><<<grid, THREADS, lds, s>>>(a, pieces, len, stat_pieces);
     return hipGetLastError();
 }
 
@@ -919,7 +966,7 @@ template <typename T> hipError_t top_rows_of(const TopRowsArgs &a, int cus, hipS
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || pieces == 1)
         return e;
-    top_join_kernel<T><<<(unsigned)std::min<int64_t>(a.R, (int64_t)cus * 16), TR_SMALL, 0, s>>>(a, pieces);
+    top_join_kernel<T><<<(unsigned)std::min<int64_t>(a.R, (int64_t)cus * 16), TR_JOIN, 0, s>>>(a, pieces);
     return hipGetLastError();
 }
 

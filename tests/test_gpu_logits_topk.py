@@ -110,6 +110,35 @@ def test_outputs_given_and_nothing_else_written():
     assert bool((idx[80:] == -9).all()) and bool((val[80:] == -9).all()) and bool((lse[4:] == -9).all())
 
 
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("V,k", [(30000, 20), (66000, 200), (66000, 256), (9000, 256), (400000, 250)])
+def test_unsplit_long_rows_and_their_rare_paths(V, k, dt):
+    """More rows than CUs.  Among random rows some that rise along the row
+    (every bound is too low), some that rise within one thread's share, equal
+    values, and rows with fewer values than are asked for."""
+    t = DTYPES[dt]
+    R = 300 if V < 100000 else 260
+    x = rnd((R, V), V + k).to(t)
+    i = torch.arange(V)
+    x[3] = (i / V * 1000).to(t)
+    x[17] = (-i / V * 1000).to(t)
+    x[40] = ((i // 8 * 8 % 512 == 0).float() * 50 + i / V).to(t)   # few threads hold all large values
+    x[41] = ((i // 4096 % 3 == 0).float() * 50 + torch.randn(V)).to(t)
+    x[99] = 2.5
+    x[120] = -float("inf"); x[120, V // 3:V // 3 + 10] = 1.0
+    x[121] = torch.finfo(t).min; x[121, -5:] = 0.0
+    x[200] = (i % 7).to(t)
+    idx, val, lse = fa.logits_topk(x.cuda(), k, tau=1.0)
+    # a stable descending sort keeps equal values in index order
+    want = torch.sort(x.float(), dim=1, descending=True, stable=True).indices[:, :k].sort(1).values
+    assert torch.equal(idx.cpu().long(), want)
+    assert torch.equal(val.cpu(), x.float().gather(1, want))
+    ex = ref.lse_of(x, 1.0)
+    slack = (V / 256 + 40) * ref.U32 + 16 * ref.U32 * ref.d(x).clamp(min=-1e30).abs().amax(1)
+    fine = ref.d(x).amax(1) > -1e30
+    ref.within(lse.cpu()[fine], ex[fine], slack[fine], torch.float32, "lse")
+
+
 def test_many_rows():
     x = rnd((5000, 130), 21).to(torch.bfloat16).cuda()
     check(x, 9)

@@ -1768,8 +1768,8 @@ int check_logits(int dtype, int64_t R, int64_t V, float tau)
         return fail(FA_ERR_ARG, "R and V must be >= 0");
     if (V > LINEAR_MAX_DIM || R > LINEAR_MAX_ELEMS / std::max<int64_t>(V, 1))
         return fail(FA_ERR_RANGE, "V must be at most 2^30 and R * V 2^36");
-    if (!(tau > 0.f) || !(tau < INFINITY) || !(1.f / tau < INFINITY))
-        return fail(FA_ERR_ARG, "tau must be positive and finite");
+    if (!(tau >= 1e-30f) || !(tau <= 1e30f))
+        return fail(FA_ERR_ARG, "tau must be between 1e-30 and 1e30");
     return FA_OK;
 }
 

@@ -101,35 +101,69 @@ template <typename T> __device__ __forceinline__ Chunk<T> load_row(const T *x, i
     return c;
 }
 
+// max of numbers, NaN aside.  (fmaxf costs two instructions more for each
+// operand whose NaN might be signalling; where one is, the sum that a maximum
+// belongs to is NaN whatever the maximum.)
+__device__ __forceinline__ float max2(float a, float b)
+{
+    float r;
+    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
+// Up to this size x * c - max * c is one fused multiply-add; beyond, where
+// max * c might overflow (the type's lowest values), the difference comes first.
+constexpr float FUSED_UP_TO = 1e30f;
+
 // A softmax's running maximum (of x, before the temperature) and sum of
-// exp((x - max) / tau), c = log2(e) / tau.  The difference is taken before the
-// scaling, so the type's lowest values neither overflow nor lose digits.  A
-// maximum of -inf is taken off as 0, so that -inf entries add 0; NaN and +inf
-// turn the sum into NaN.  v_exp_f32 flushes results below 2^-126, far under
-// the sum's rounding.
+// exp((x - max) / tau), c = log2(e) / tau.  A maximum of -inf is taken off as
+// 0, so that -inf entries add 0; NaN and +inf turn the sum into NaN.  max * c
+// is rounded once, the same for all entries: half a step of the result's
+// max / tau.  v_exp_f32 flushes results below 2^-126, far under the sum's
+// rounding.  What bounds the pass after the memory is the vector unit: about
+// five instructions an entry, the exponential at a quarter of the rate.
 struct Softmax {
     float m = NEG_INF, s = 0.f;
 
-    // Returns the chunk's maximum (of its numbers); `special` is set when it
-    // holds NaN or +inf.
-    template <typename T> __device__ __forceinline__ float add(const Chunk<T> &k, float c, bool &special)
+    // `tops` receives the maximum of each chunk's numbers; `special` is set
+    // when the chunks hold NaN or +inf.
+    template <typename T, int N>
+    __device__ __forceinline__ void add(const Chunk<T> *k, float c, bool &special, float *tops)
     {
         constexpr int EPC = Chunk<T>::EPC;
-        float t = k.get(0);
+        float mn = m;
 #pragma unroll
-        for (int j = 1; j < EPC; j++)
-            t = fmaxf(t, k.get(j));
-        const float mn = fmaxf(m, t);
-        const float b = mn == NEG_INF ? 0.f : mn;
-        s *= __builtin_amdgcn_exp2f((m - b) * c);
+        for (int u = 0; u < N; u++) {
+            float t = max2(k[u].get(0), k[u].get(1));
+#pragma unroll
+            for (int j = 2; j < EPC; j += 2)
+                t = max3(t, k[u].get(j), k[u].get(j + 1));
+            tops[u] = t;
+            mn = max2(mn, t);
+        }
+        const float b = mn == NEG_INF ? 0.f : mn, bc = b * c;
         float a = 0.f;
+        if (__any(fabsf(bc) > FUSED_UP_TO)) {
+            s *= __builtin_amdgcn_exp2f((m - b) * c);
 #pragma unroll
-        for (int j = 0; j < EPC; j++)
-            a += __builtin_amdgcn_exp2f((k.get(j) - b) * c);
+            for (int j = 0; j < EPC * N; j++)
+                a += __builtin_amdgcn_exp2f((k[j / EPC].get(j % EPC) - b) * c);
+        } else {
+            s *= __builtin_amdgcn_exp2f(__builtin_fmaf(m, c, -bc));
+#pragma unroll
+            for (int j = 0; j < EPC * N; j++)
+                a += __builtin_amdgcn_exp2f(__builtin_fmaf(k[j / EPC].get(j % EPC), c, -bc));
+        }
         s += a;
         m = mn;
         special = a != a;
-        return t;
     }
 
     __device__ __forceinline__ float scaled_to(float M, float c) const
@@ -176,6 +210,7 @@ __device__ __forceinline__ Softmax row_softmax(const T *x, int i0, int i1, float
     constexpr int STEP = THREADS * EPC;
     Softmax t;
     bool special;
+    float tops[2];
     int i = i0 + threadIdx.x * EPC;
     for (; i + (UNROLL - 1) * STEP + EPC <= i1; i += UNROLL * STEP) {
         Chunk<T> k[UNROLL];
@@ -183,11 +218,13 @@ __device__ __forceinline__ Softmax row_softmax(const T *x, int i0, int i1, float
         for (int u = 0; u < UNROLL; u++)
             __builtin_memcpy(&k[u].v, x + i + u * STEP, 16);
 #pragma unroll
-        for (int u = 0; u < UNROLL; u++)
-            t.add(k[u], c, special);
+        for (int u = 0; u < UNROLL; u += 2)
+            t.add<T, 2>(k + u, c, special, tops);
     }
-    for (; i < i1; i += STEP)
-        t.add(load_row(x, i, i1), c, special);
+    for (; i < i1; i += STEP) {
+        const Chunk<T> k = load_row(x, i, i1);
+        t.add<T, 1>(&k, c, special, tops);
+    }
     join_block<THREADS>(t, c, lds);
     return t;
 }
@@ -217,25 +254,29 @@ template <> struct Key<__bf16> {
     static __device__ __forceinline__ float value(uint32_t k) { return Key<float>::value(k << 16 | 0xffffu * !(k & 0x8000u)); }
 };
 
-constexpr int TR_SMALL = 256, TR_LARGE = 1024, TR_JOIN = 512; // threads
-constexpr int TR_U = 2;                        // chunks a thread takes per block
-constexpr int TR_PRUNE = 1024;                 // candidates from which on they are cut down to k
-// A block adds at most FA_MAX_TOP - 1 threads' worth above its bound and
-// FA_MAX_TOP equal to it (see gather_top).
-constexpr int TR_CAP = TR_PRUNE + (FA_MAX_TOP - 1) * 8 * TR_U + FA_MAX_TOP + 16;
-
-struct TopLds {
-    uint32_t key[TR_CAP];
-    int32_t idx[TR_CAP];
-    float val[TR_CAP]; // the value itself: keys do not tell -0 or a NaN's bits
-    uint32_t out_key[FA_MAX_TOP];
+// A workgroup's shape and its LDS: THREADS_; QUEUE_, chunks it can hold; CAP_,
+// candidates it can hold; U_, chunks a thread takes for the first bound.
+template <int THREADS_, int QUEUE_, int CAP_, int U_> struct TopLds {
+    static constexpr int THREADS = THREADS_, QUEUE = QUEUE_, CAP = CAP_, U = U_;
+    static_assert(CAP >= 2 * FA_MAX_TOP, "the k largest and their ties fit");
+    union {
+        struct { // candidates
+            uint32_t key[CAP];
+            int32_t idx[CAP];
+            float val[CAP]; // the value itself: keys do not tell -0 or a NaN's bits
+        };
+        struct { // chunks that hold candidates, and where they start in the row
+            u32x4 chunk[QUEUE];
+            int32_t at[QUEUE];
+        };
+    };
     int32_t out_idx[FA_MAX_TOP];
     float out_val[FA_MAX_TOP];
-    uint32_t best[TR_LARGE];
-    int n, hits, kept;
+    uint32_t best[THREADS];
+    int n, kept;
     int count[8][16];
-    int wave[TR_LARGE / WAVE];
-    float red[TR_LARGE / WAVE];
+    int wave[THREADS / WAVE];
+    float red[THREADS / WAVE];
 };
 
 // The largest t with at least k of the n keys at or above it, four bits of t
@@ -243,10 +284,10 @@ struct TopLds {
 // ballot, lane b adds the b-th count, and as the counts fall with b the next
 // digit is how many of them reach k.  (Two bits a step took twice the
 // barriers: 27.5 and 24.4 us for a row of 151936 fp32 in two kernels.)
-template <typename T, int THREADS>
-__device__ __forceinline__ uint32_t kth_key(TopLds &l, const uint32_t *keys, int n, int k)
+template <int BITS, typename L>
+__device__ __forceinline__ uint32_t kth_key(L &l, const uint32_t *keys, int n, int k)
 {
-    constexpr int STEPS = Key<T>::BITS / 4;
+    constexpr int STEPS = BITS / 4;
     const int lane = threadIdx.x % WAVE;
     if (threadIdx.x < STEPS * 16)
         (&l.count[0][0])[threadIdx.x] = 0;
@@ -254,10 +295,10 @@ __device__ __forceinline__ uint32_t kth_key(TopLds &l, const uint32_t *keys, int
     uint32_t cut = 0;
 #pragma unroll 1
     for (int step = 0; step < STEPS; step++) {
-        const int s = Key<T>::BITS - 4 - 4 * step;
+        const int s = BITS - 4 - 4 * step;
         int mine = 0;
 #pragma unroll 1
-        for (int i0 = 0; i0 < n; i0 += THREADS) {
+        for (int i0 = 0; i0 < n; i0 += L::THREADS) {
             const int i = i0 + threadIdx.x;
             const uint32_t key = i < n ? keys[i] : 0u; // 0 is below every value tried
 #pragma unroll
@@ -276,18 +317,16 @@ __device__ __forceinline__ uint32_t kth_key(TopLds &l, const uint32_t *keys, int
     return cut;
 }
 
-// Cuts the n >= k candidates down to the k largest (ties to the lower index),
-// in index order: an entry's place is the number of kept ones before it.
-// Returns the k-th largest key.
-template <typename T, int THREADS> __device__ __forceinline__ uint32_t prune(TopLds &l, int n, int k)
+// Moves the candidates with keys at or above `cut` to the front, in any order:
+// an entry never moves past the tiles that have been read.  Returns how many
+// there are; l.kept counts those above the cut.
+template <typename L> __device__ __forceinline__ int keep_from(L &l, int n, uint32_t cut)
 {
-    const uint32_t cut = kth_key<T, THREADS>(l, l.key, n, k);
     if (threadIdx.x == 0)
         l.n = l.kept = 0;
     __syncthreads();
-    // first those at or above the cut, in any order, moved to the front: an
-    // entry never moves past the tiles that have been read
-    for (int i0 = 0; i0 < n; i0 += THREADS) {
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += L::THREADS) {
         const int i = i0 + threadIdx.x;
         uint32_t key = 0;
         int32_t idx = 0;
@@ -308,8 +347,28 @@ template <typename T, int THREADS> __device__ __forceinline__ uint32_t prune(Top
         }
     }
     __syncthreads();
-    const int m = l.n, ties = k - l.kept;
-    for (int i = threadIdx.x; i < m; i += THREADS) {
+    return l.n;
+}
+
+// Cuts the n >= k candidates down to the k largest (ties to the lower index),
+// in index order: an entry's place is the number of kept ones before it.  Of
+// their keys nothing is left.
+template <typename T, typename L> __device__ __forceinline__ void prune(L &l, int n, int k)
+{
+    uint32_t cut = kth_key<Key<T>::BITS>(l, l.key, n, k);
+    int m = keep_from(l, n, cut);
+    if (m > k + L::THREADS / 4) {
+        // many equal to the cut: the first of them by index, found as the
+        // largest keys again.  (Counting them out below took 0.5 ms for 2000.)
+        for (int i = threadIdx.x; i < m; i += L::THREADS)
+            l.key[i] = l.key[i] > cut ? ~0u : ~(uint32_t)l.idx[i];
+        __syncthreads();
+        cut = kth_key<32>(l, l.key, m, k);
+        m = keep_from(l, m, cut);
+    }
+    const int ties = k - l.kept;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < m; i += L::THREADS) {
         const uint32_t key = l.key[i];
         const int32_t idx = l.idx[i];
         int gt = 0, eq = 0;
@@ -321,209 +380,273 @@ template <typename T, int THREADS> __device__ __forceinline__ uint32_t prune(Top
         }
         if (key > cut || eq < ties) {
             const int at = gt + (eq < ties ? eq : ties);
-            l.out_key[at] = key;
             l.out_idx[at] = idx;
             l.out_val[at] = l.val[i];
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < k; i += THREADS) {
-        l.key[i] = l.out_key[i];
+    for (int i = threadIdx.x; i < k; i += L::THREADS) {
         l.idx[i] = l.out_idx[i];
         l.val[i] = l.out_val[i];
     }
     if (threadIdx.x == 0)
         l.n = k;
     __syncthreads();
-    return cut;
 }
 
-// Entry b of a thread's U chunks (b counts through them in order), and masks
-// over those entries, bit b for entry b.
-template <typename T, int U> __device__ __forceinline__ float select(const Chunk<T> *c, int b)
+// One pass over elements [i0, i1) of a row that queues the chunks with entries
+// above the key `bound` and adds up the softmax.  A chunk is
+// queued whole, from its maximum alone, so that a wavefront in which some lane
+// hits pays about as much as for two more entries a lane.  (Taking the entries
+// out on the spot cost each wavefront several instructions an entry: 396 us
+// where this took 334, 4096 rows of 128256 bf16, k = 64.)  Chunks are
+// counted even where they no longer fit.  No barrier until the end.
+template <typename T, typename L>
+__device__ __forceinline__ int stream_above(const T *x, int i0, int i1, uint32_t bound, float c, L &l, Softmax &sm)
 {
-    constexpr int EPC = Chunk<T>::EPC;
-    float v = 0.f;
+    constexpr int EPC = Chunk<T>::EPC, UNROLL = 4, STEP = L::THREADS * EPC;
+    // above a NaN's key there is nothing; a NaN's place in a chunk is told by
+    // the sum, or here, where +inf is told apart
+    const bool none = bound == Key<T>::NAN_KEY;
+    const float above = none ? __builtin_inff() : Key<T>::value(bound);
+    const auto queue = [&](const Chunk<T> &k, bool hit, int i) {
+        if (hit && !none) {
+            const int p = atomicAdd(&l.n, 1);
+            if (p < L::QUEUE) {
+                l.chunk[p] = k.v;
+                l.at[p] = i;
+            }
+        }
+    };
+    int i = i0 + threadIdx.x * EPC;
+    for (; i + (UNROLL - 1) * STEP + EPC <= i1; i += UNROLL * STEP) {
+        Chunk<T> k[UNROLL];
 #pragma unroll
-    for (int j = 0; j < EPC * U; j++)
-        v = b == j ? c[j / EPC].get(j % EPC) : v;
-    return v;
-}
-
-template <typename T, int U> __device__ __forceinline__ bool select_nan(const Chunk<T> *c)
-{
-    constexpr int EPC = Chunk<T>::EPC;
-    bool n = false;
+        for (int u = 0; u < UNROLL; u++)
+            __builtin_memcpy(&k[u].v, x + i + u * STEP, 16);
 #pragma unroll
-    for (int j = 0; j < EPC * U; j++)
-        n |= c[j / EPC].get(j % EPC) != c[j / EPC].get(j % EPC);
-    return n;
-}
-
-template <typename T, int U> __device__ __forceinline__ uint32_t equal_mask(const Chunk<T> *c, uint32_t key)
-{
-    constexpr int EPC = Chunk<T>::EPC;
-    const float t = Key<T>::value(key);
-    const bool nan = key == Key<T>::NAN_KEY;
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < EPC * U; j++) {
-        const float v = c[j / EPC].get(j % EPC);
-        m |= (uint32_t)(nan ? v != v : v == t) << j;
+        for (int u = 0; u < UNROLL; u += 2) {
+            bool odd;
+            float t[2];
+            sm.add<T, 2>(k + u, c, odd, t);
+            queue(k[u], t[0] > above || odd, i + u * STEP);
+            queue(k[u + 1], t[1] > above || odd, i + (u + 1) * STEP);
+        }
     }
-    return m;
-}
-
-// Entries with keys above `key`; all for 0, none for a NaN's.
-template <typename T, int U> __device__ __forceinline__ uint32_t above_mask(const Chunk<T> *c, uint32_t key)
-{
-    constexpr int EPC = Chunk<T>::EPC;
-    if (key == 0)
-        return ~0u;
-    if (key == Key<T>::NAN_KEY)
-        return 0;
-    const float t = Key<T>::value(key);
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < EPC * U; j++)
-        m |= (uint32_t)(!(c[j / EPC].get(j % EPC) <= t)) << j;
-    return m;
-}
-
-// Entries inside the row: `left` of them from the first chunk's start on,
-// chunks `next` entries apart.
-template <typename T, int U> __device__ __forceinline__ uint32_t valid_mask(int left, int next)
-{
-    constexpr int EPC = Chunk<T>::EPC;
-    uint32_t m = 0;
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-        const int v = left - u * next;
-        m |= (v >= EPC ? (1u << EPC) - 1 : v > 0 ? (1u << v) - 1 : 0u) << (u * EPC);
+    for (; i < i1; i += STEP) {
+        const Chunk<T> k = load_row(x, i, i1);
+        bool odd;
+        float t;
+        sm.add<T, 1>(&k, c, odd, &t);
+        queue(k, t > above || odd, i);
     }
-    return m;
-}
-
-// One pass over elements [i0, i1) of a row (at least one) that leaves in `l`
-// the min(k, i1 - i0) largest, in index order, and the softmax sums of the
-// thread's share in `sm`.  Candidates are the entries above a bound that k
-// earlier entries reach (an equal one has k before it and cannot matter).  The
-// bound is 0 at first and rises in two ways: when TR_PRUNE candidates have
-// gathered they are cut down to k; and when a block's candidates might not fit
-// (always in a long row's first block), to the k-th largest of the threads'
-// own maxima, above which fewer than k threads have entries.  Entries equal to
-// that are taken in index order, k of them at most.
-template <typename T, int THREADS>
-__device__ __forceinline__ void gather_top(const T *row, int i0, int i1, int k, float c, TopLds &l, Softmax &sm)
-{
-    constexpr int EPC = Chunk<T>::EPC, U = TR_U;
-    constexpr int BLOCK = THREADS * EPC * U, NEXT = THREADS * EPC;
-    const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
-    const T *x = row + i0;
-    const int len = i1 - i0;
-    const int mine = threadIdx.x * EPC;
-    if (threadIdx.x == 0)
-        l.n = l.hits = 0;
-    Chunk<T> next[U];
-#pragma unroll
-    for (int u = 0; u < U; u++)
-        next[u] = load_row(x, mine + u * NEXT, len);
-    uint32_t bound = 0;
-    float bound_value = NEG_INF;
-    int n = 0;
     __syncthreads();
-    for (int b0 = 0; b0 < len; b0 += BLOCK) {
-        Chunk<T> cur[U];
-        bool hit;
+    return l.n;
+}
+
+// The entries of the n queued chunks above `bound` become the candidates.
+// Returns how many there are, even where they do not fit.
+template <typename T, typename L>
+__device__ __forceinline__ int take_queued(int n, int i1, uint32_t bound, L &l)
+{
+    constexpr int EPC = Chunk<T>::EPC, PER = (L::QUEUE + L::THREADS - 1) / L::THREADS;
+    Chunk<T> k[PER];
+    int at[PER];
 #pragma unroll
-        for (int u = 0; u < U; u++)
-            cur[u] = next[u];
-        if (b0 + BLOCK < len) {
+    for (int e = 0; e < PER; e++) {
+        const int q = e * L::THREADS + threadIdx.x;
+        at[e] = q < n ? l.at[q] : -1;
+        if (q < n)
+            k[e].v = l.chunk[q];
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+        l.n = 0;
+    __syncthreads();
 #pragma unroll
-            for (int u = 0; u < U; u++)
-                next[u] = load_row(x, mine + b0 + BLOCK + u * NEXT, len);
-        }
-        float top = NEG_INF;
-        bool odd = false;
+    for (int e = 0; e < PER; e++) {
+        if (at[e] < 0)
+            continue;
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            bool special;
-            top = fmaxf(top, sm.add(cur[u], c, special));
-            odd |= special;
-        }
-        hit = top > bound_value || odd || bound == 0;
-        const uint64_t hits = __ballot(hit);
-        if (lane == 0 && hits)
-            atomicAdd(&l.hits, __popcll(hits));
-        __syncthreads();
-        const int threads_hit = l.hits;
-        uint32_t t = bound;
-        const int left = len - (mine + b0);
-        if (threads_hit * EPC * U > TR_CAP - n) {
-            uint32_t best = left > 0 ? Key<T>::of(top) : 0; // 0: no entries
-            if (odd && select_nan<T, U>(cur))
-                best = Key<T>::NAN_KEY;
-            l.best[threadIdx.x] = best;
-            // more threads than k have entries above the old bound, so t > bound
-            t = kth_key<T, THREADS>(l, l.best, THREADS, k);
-            // places of the entries equal to t in index order: chunk u = 0 of
-            // all threads comes before u = 1; both counts travel in one word
-            uint32_t ties = equal_mask<T, U>(cur, t) & valid_mask<T, U>(left, NEXT);
-            const uint32_t cnt = __popc(ties & ((1u << EPC) - 1)) | (uint32_t)__popc(ties >> EPC) << 16;
-            uint32_t upto = cnt;
-#pragma unroll
-            for (int o = 1; o < WAVE; o <<= 1) {
-                const uint32_t v = __shfl_up(upto, o);
-                upto += lane >= o ? v : 0;
-            }
-            if (lane == WAVE - 1)
-                l.wave[wave] = (int)upto;
-            __syncthreads();
-            uint32_t before = upto - cnt, total = 0;
-#pragma unroll 1
-            for (int w = 0; w < THREADS / WAVE; w++) {
-                const uint32_t v = (uint32_t)l.wave[w];
-                before += w < wave ? v : 0;
-                total += v;
-            }
-            int place0 = (int)(before & 0xffff), place1 = (int)((total & 0xffff) + (before >> 16));
-            while (ties) {
-                const int b = __builtin_ctz(ties);
-                ties &= ties - 1;
-                if ((b < EPC ? place0++ : place1++) < k) {
-                    const int p = atomicAdd(&l.n, 1);
-                    l.key[p] = t;
-                    l.idx[p] = i0 + mine + b0 + (b / EPC) * NEXT + b % EPC;
-                    l.val[p] = select<T, U>(cur, b);
+        for (int j = 0; j < EPC; j++) {
+            const float v = k[e].get(j);
+            const uint32_t key = Key<T>::of(v);
+            if (key > bound && at[e] + j < i1) {
+                const int p = atomicAdd(&l.n, 1);
+                if (p < L::CAP) {
+                    l.key[p] = key;
+                    l.idx[p] = at[e] + j;
+                    l.val[p] = v;
                 }
             }
         }
-        if (hit) {
-            uint32_t mask = above_mask<T, U>(cur, t) & valid_mask<T, U>(left, NEXT);
-            while (mask) {
-                const int b = __builtin_ctz(mask);
-                mask &= mask - 1;
-                const float v = select<T, U>(cur, b);
-                const int p = atomicAdd(&l.n, 1);
-                l.key[p] = Key<T>::of(v);
-                l.idx[p] = i0 + mine + b0 + (b / EPC) * NEXT + b % EPC;
+    }
+    __syncthreads();
+    return l.n;
+}
+
+// A pass that makes the entries above `bound` the candidates one by one, for
+// the rare rows whose chunks do not fit the queue.
+template <typename T, typename L>
+__device__ __forceinline__ int list_above(const T *x, int i0, int i1, uint32_t bound, L &l)
+{
+#pragma unroll 1
+    for (int i = i0 + threadIdx.x; i < i1; i += L::THREADS) {
+        const float v = (float)x[i];
+        const uint32_t key = Key<T>::of(v);
+        if (key > bound) {
+            const int p = atomicAdd(&l.n, 1);
+            if (p < L::CAP) {
+                l.key[p] = key;
+                l.idx[p] = i;
                 l.val[p] = v;
             }
         }
-        __syncthreads();
-        n = l.n;
-        if (threadIdx.x == 0)
-            l.hits = 0;
-        if (n > TR_PRUNE) {
-            t = prune<T, THREADS>(l, n, k);
-            n = k;
-        } else {
-            __syncthreads();
-        }
-        bound = t;
-        bound_value = t == 0 ? NEG_INF : t == Key<T>::NAN_KEY ? __builtin_inff() : Key<T>::value(t);
     }
-    prune<T, THREADS>(l, n, n < k ? n : k);
+    __syncthreads();
+    return l.n;
+}
+
+// The first `need` entries with the key `tie`, in index order, join the
+// candidates; the pass ends where they are complete.
+template <typename T, typename L>
+__device__ __forceinline__ void collect_ties(const T *x, int i0, int i1, uint32_t tie, int need, L &l)
+{
+    constexpr int EPC = Chunk<T>::EPC, STEP = L::THREADS * EPC;
+    const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
+    const float t = Key<T>::value(tie);
+    const bool nan = tie == Key<T>::NAN_KEY;
+    for (int b0 = i0; b0 < i1 && need > 0; b0 += STEP) {
+        const int at = b0 + threadIdx.x * EPC;
+        const Chunk<T> k = load_row(x, at, i1);
+        uint32_t mask = 0;
+#pragma unroll
+        for (int j = 0; j < EPC; j++)
+            mask |= (uint32_t)(at + j < i1 && (nan ? k.get(j) != k.get(j) : k.get(j) == t)) << j;
+        int place = __popc(mask);
+#pragma unroll
+        for (int o = 1; o < WAVE; o <<= 1) {
+            const int v = __shfl_up(place, o);
+            place += lane >= o ? v : 0;
+        }
+        if (lane == WAVE - 1)
+            l.wave[wave] = place;
+        __syncthreads();
+        place -= __popc(mask);
+        int total = 0;
+#pragma unroll 1
+        for (int w = 0; w < L::THREADS / WAVE; w++) {
+            place += w < wave ? l.wave[w] : 0;
+            total += l.wave[w];
+        }
+#pragma unroll
+        for (int j = 0; j < EPC; j++)
+            if ((mask >> j & 1) && place++ < need) {
+                const int p = atomicAdd(&l.n, 1);
+                l.key[p] = tie;
+                l.idx[p] = at + j;
+                l.val[p] = k.get(j);
+            }
+        need -= total;
+        __syncthreads();
+    }
+}
+
+// The k-th largest key of a whole row by counting, a bit a pass.
+template <typename T, typename L>
+__device__ __forceinline__ uint32_t kth_of_row(const T *x, int i0, int i1, int k, L &l)
+{
+    uint32_t cut = 0;
+#pragma unroll 1
+    for (int bit = Key<T>::BITS - 1; bit >= 0; bit--) {
+        const uint32_t t = cut | 1u << bit;
+        int c = 0;
+        for (int i = i0 + threadIdx.x; i < i1; i += L::THREADS)
+            c += Key<T>::of((float)x[i]) >= t;
+        if (threadIdx.x == 0)
+            l.n = 0;
+        __syncthreads();
+        atomicAdd(&l.n, c);
+        __syncthreads();
+        cut = l.n >= k ? t : cut;
+        __syncthreads();
+    }
+    return cut;
+}
+
+// Leaves in `l` the min(k, i1 - i0) largest of elements [i0, i1) of a row (at
+// least one), in index order, and the softmax sums of the thread's share in
+// `sm`.  A first block gives a bound that at least k entries reach, the k-th
+// largest of the threads' own maxima; one pass then collects what is above it,
+// a few times k entries for values in no particular order.  Should they not
+// fit (values that rise along the row), the same bound is taken from the
+// threads' maxima over the whole row, and should those above it still not fit,
+// the k-th key itself is counted out.  Fewer than k above the bound (many
+// equal values, masked rows): the missing ones equal it.
+template <typename T, typename L>
+__device__ __forceinline__ void row_top(const T *x, int i0, int i1, int k, float c, L &l, Softmax &sm)
+{
+    constexpr int EPC = Chunk<T>::EPC, U = L::U, STEP = L::THREADS * EPC;
+    const int want = k < i1 - i0 ? k : i1 - i0;
+    if (threadIdx.x == 0)
+        l.n = 0;
+    if (i1 - i0 <= L::CAP) { // all are candidates
+        for (int i = i0 + threadIdx.x * EPC; i < i1; i += STEP) {
+            const Chunk<T> e = load_row(x, i, i1);
+            bool odd;
+            float top;
+            sm.add<T, 1>(&e, c, odd, &top);
+#pragma unroll
+            for (int j = 0; j < EPC; j++)
+                if (i + j < i1) {
+                    l.key[i - i0 + j] = Key<T>::of(e.get(j));
+                    l.idx[i - i0 + j] = i + j;
+                    l.val[i - i0 + j] = e.get(j);
+                }
+        }
+        __syncthreads();
+        prune<T, L>(l, i1 - i0, want);
+        return;
+    }
+    const int at = i0 + threadIdx.x * EPC;
+    Softmax first;
+    bool odd = false, nan = false;
+    Chunk<T> e[U];
+    float tops[U];
+#pragma unroll
+    for (int u = 0; u < U; u++)
+        e[u] = load_row(x, at + u * STEP, i1);
+    first.add<T, U>(e, c, odd, tops);
+    if (odd)
+#pragma unroll
+        for (int j = 0; j < EPC * U; j++)
+            nan |= e[j / EPC].get(j % EPC) != e[j / EPC].get(j % EPC);
+    l.best[threadIdx.x] = at >= i1 ? 0u : nan ? Key<T>::NAN_KEY : Key<T>::of(first.m); // 0: no entries
+    uint32_t bound = kth_key<Key<T>::BITS>(l, l.best, L::THREADS, k);
+    __syncthreads();
+    int q = stream_above<T, L>(x, i0, i1, bound, c, l, sm);
+    int n = q > L::QUEUE ? L::CAP + 1 : take_queued<T, L>(q, i1, bound, l);
+#pragma unroll 1
+    for (int again = 0; again < 2 && n > L::CAP; again++) {
+        __syncthreads();
+        if (again == 0) {
+            l.best[threadIdx.x] = Key<T>::of(sm.m); // of the numbers: FA_MAX_TOP threads or more have some
+            bound = max(bound, kth_key<Key<T>::BITS>(l, l.best, L::THREADS, k));
+        } else {
+            bound = kth_of_row<T, L>(x, i0, i1, k, l);
+        }
+        __syncthreads();
+        if (threadIdx.x == 0)
+            l.n = 0;
+        __syncthreads();
+        n = list_above<T, L>(x, i0, i1, bound, l);
+    }
+    if (n < want) {
+        __syncthreads();
+        collect_ties<T, L>(x, i0, i1, bound, want - n, l);
+        n = want;
+    }
+    prune<T, L>(l, n, want);
 }
 
 __device__ __forceinline__ float *piece_vals(const TopRowsArgs &p, int pieces)
@@ -533,10 +656,11 @@ __device__ __forceinline__ float *piece_vals(const TopRowsArgs &p, int pieces)
 
 // A workgroup per row (pieces = 1) or per piece of a row; a piece's results go
 // to the workspace, unused places with index -1.
-template <typename T, int THREADS>
-__global__ __launch_bounds__(THREADS, THREADS == TR_LARGE ? 8 : 4) void top_rows_kernel(TopRowsArgs p, int pieces, int64_t len)
+template <typename T, typename L>
+__global__ __launch_bounds__(L::THREADS, 8) void top_rows_kernel(TopRowsArgs p, int pieces, int64_t len)
 {
-    __shared__ TopLds l;
+    constexpr int THREADS = L::THREADS;
+    __shared__ L l;
     const float c = p.inv_tau * LOG2E;
     for (int64_t w = blockIdx.x; w < p.R * pieces; w += gridDim.x) {
         const int64_t r = w / pieces;
@@ -545,12 +669,15 @@ __global__ __launch_bounds__(THREADS, THREADS == TR_LARGE ? 8 : 4) void top_rows
         Softmax sm;
         int n = 0;
         if (p.k > 0) {
-            gather_top<T, THREADS>(x, i0, i1, p.k, c, l, sm);
+            row_top<T, L>(x, i0, i1, p.k, c, l, sm);
             n = l.n;
         } else {
             bool special;
-            for (int i = i0 + threadIdx.x * Chunk<T>::EPC; i < i1; i += THREADS * Chunk<T>::EPC)
-                sm.add(load_row(x, i, i1), c, special);
+            float top;
+            for (int i = i0 + threadIdx.x * Chunk<T>::EPC; i < i1; i += THREADS * Chunk<T>::EPC) {
+                const Chunk<T> e = load_row(x, i, i1);
+                sm.add<T, 1>(&e, c, special, &top);
+            }
         }
         join_block<THREADS>(sm, c, l.red);
         int32_t *idx = p.idx + w * p.k;
@@ -573,9 +700,11 @@ __global__ __launch_bounds__(THREADS, THREADS == TR_LARGE ? 8 : 4) void top_rows
 
 // Joins a row's pieces: their entries are the candidates, their softmax sums
 // are added in piece order.
-template <typename T> __global__ __launch_bounds__(TR_JOIN) void top_join_kernel(TopRowsArgs p, int pieces)
+using TopJoin = TopLds<512, 1, 4096, 1>;
+
+template <typename T> __global__ __launch_bounds__(TopJoin::THREADS) void top_join_kernel(TopRowsArgs p, int pieces)
 {
-    __shared__ TopLds l;
+    __shared__ TopJoin l;
     const float c = p.inv_tau * LOG2E;
     for (int64_t r = blockIdx.x; r < p.R; r += gridDim.x) {
         const float *val = piece_vals(p, pieces) + r * pieces * p.k;
@@ -583,7 +712,7 @@ template <typename T> __global__ __launch_bounds__(TR_JOIN) void top_join_kernel
         if (threadIdx.x == 0)
             l.n = 0;
         __syncthreads();
-        for (int j = threadIdx.x; j < pieces * p.k; j += TR_JOIN) {
+        for (int j = threadIdx.x; j < pieces * p.k; j += TopJoin::THREADS) {
             const int32_t i = idx[j];
             const float v = val[j];
             if (i >= 0) {
@@ -600,8 +729,8 @@ template <typename T> __global__ __launch_bounds__(TR_JOIN) void top_join_kernel
                 p.lse[r] = lse;
         }
         __syncthreads();
-        prune<T, TR_JOIN>(l, l.n, p.k);
-        for (int j = threadIdx.x; j < p.k; j += TR_JOIN) {
+        prune<T, TopJoin>(l, l.n, p.k);
+        for (int j = threadIdx.x; j < p.k; j += TopJoin::THREADS) {
             p.idx[r * p.k + j] = l.idx[j];
             p.val[r * p.k + j] = l.val[j];
         }
@@ -609,16 +738,17 @@ template <typename T> __global__ __launch_bounds__(TR_JOIN) void top_join_kernel
     }
 }
 
-// How rows are split: only while there are fewer rows than CUs, into pieces
-// of at least SPLIT_MIN bytes whose entries the join can hold.
+// How rows are split: while there are fewer rows than CUs, into pieces of at
+// least SPLIT_MIN bytes, at most `most`; and into `least` in any case, while
+// `most` allows.
 constexpr int64_t SPLIT_MIN = 16384;
 
-void split_rows(int64_t R, int64_t V, size_t es, int64_t most, int cus, int &pieces, int64_t &len)
+void split_rows(int64_t R, int64_t V, size_t es, int64_t most, int64_t least, int cus, int &pieces, int64_t &len)
 {
     const int64_t unit = 64; // elements: pieces start on a vector of an aligned row
     int64_t s = R > 0 && R < cus ? (2 * cus + R - 1) / R : 1;
-    s = std::min(s, std::min<int64_t>(most, V * (int64_t)es / SPLIT_MIN));
-    s = std::max<int64_t>(1, std::min<int64_t>(s, SPLIT_MAX));
+    s = std::max(std::min(s, V * (int64_t)es / SPLIT_MIN), least);
+    s = std::max<int64_t>(1, std::min<int64_t>(s, std::min<int64_t>(most, SPLIT_MAX)));
     len = (((V + s - 1) / s + unit - 1) / unit) * unit;
     len = std::max(len, unit);
     pieces = (int)std::max<int64_t>(1, (V + len - 1) / len);
@@ -809,8 +939,8 @@ template <typename T> __device__ __forceinline__ void store_row(T *x, int i, int
 // Where a row's normaliser comes from.
 enum { LSE_COMPUTE = 0, LSE_PIECES = 1, LSE_GIVEN = 2 };
 
-// exp((z inv_tau - lse)) of the dense pass: one rounding of the scaled logit
-// and one of the difference; v_exp_f32 flushes below 2^-126.
+// exp(z inv_tau - lse): one rounding of the scaled logit and one of the
+// difference; v_exp_f32 flushes below 2^-126.
 __device__ __forceinline__ float prob(float z, float inv_tau, float lse)
 {
     return __builtin_amdgcn_exp2f((z * inv_tau - lse) * LOG2E);
@@ -871,12 +1001,21 @@ __global__ __launch_bounds__(THREADS) void distill_kernel(DistillArgs p, int gra
                 if (l.index[i] >= 0)
                     l.sum[i] = gt * (M * prob((float)z[l.index[i]], p.inv_tau, lse) - l.sum[i]);
             __syncthreads();
+            const float off = -lse * LOG2E;
+            const bool fused = fabsf(off) <= FUSED_UP_TO;
+#pragma unroll 2
             for (int i = i0 + threadIdx.x * EPC; i < i1; i += THREADS * EPC) {
                 const Chunk<T> k = load_row(z, i, i1);
                 float v[EPC];
+                if (fused) {
 #pragma unroll
-                for (int j = 0; j < EPC; j++)
-                    v[j] = gm * prob(k.get(j), p.inv_tau, lse);
+                    for (int j = 0; j < EPC; j++)
+                        v[j] = gm * __builtin_amdgcn_exp2f(__builtin_fmaf(k.get(j), c2, off));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < EPC; j++)
+                        v[j] = gm * prob(k.get(j), p.inv_tau, lse);
+                }
                 store_row(dz, i, i1, v);
             }
             __syncthreads();
@@ -923,7 +1062,7 @@ template <typename T> hipError_t distill_of(const DistillArgs &a, bool loss, int
 {
     int pieces;
     int64_t len;
-    split_rows(a.R, a.V, sizeof(T), SPLIT_MAX, cus, pieces, len);
+    split_rows(a.R, a.V, sizeof(T), SPLIT_MAX, 1, cus, pieces, len);
     const bool small = a.V * (int64_t)sizeof(T) <= DI_SMALL_BYTES;
     if (!loss) {
         if (small)
@@ -953,20 +1092,44 @@ template <typename T> hipError_t distill_of(const DistillArgs &a, bool loss, int
     return run_distill<T, DI_LARGE, false, LSE_PIECES>(a, pieces, len, pieces, cus, s);
 }
 
+// The workgroups of the top logits.  Rows of up to 16 KB take the small one,
+// whose queue holds the whole row.  Four workgroups of the middle shape fit a
+// CU and hide each other's selection: 263 us against 334 us with two of the
+// large one (4096 rows of 128256 bf16, k = 64).  The large shape has room for
+// more candidates: a pass finds about k times the row's length over the
+// sample's, and top_longest counts a quarter more.
+using TopSmall = TopLds<256, 1024, 2048, 4>;
+using TopMiddle = TopLds<512, 1536, 2560, 4>;
+using TopLarge = TopLds<1024, 3072, 4096, 2>;
+constexpr int64_t TOP_SMALL_BYTES = 16384;
+
+// The longest piece of a row whose candidates shape L is expected to hold.
+template <typename L> int64_t top_longest(int64_t k, size_t es)
+{
+    return (int64_t)L::QUEUE * L::THREADS * L::U * 16 / (int64_t)es * 4 / (5 * std::max<int64_t>(k, 1));
+}
+
+void split_top_rows(int64_t R, int64_t V, int64_t k, size_t es, int cus, int &pieces, int64_t &len)
+{
+    split_rows(R, V, es, TopJoin::CAP / std::max<int64_t>(k, 1), V / top_longest<TopLarge>(k, es) + 1, cus, pieces, len);
+}
+
 template <typename T> hipError_t top_rows_of(const TopRowsArgs &a, int cus, hipStream_t s)
 {
     int pieces;
     int64_t len;
-    split_rows(a.R, a.V, sizeof(T), TR_CAP / std::max(a.k, 1), cus, pieces, len);
+    split_top_rows(a.R, a.V, a.k, sizeof(T), cus, pieces, len);
     const unsigned grid = (unsigned)std::min<int64_t>(a.R * pieces, (int64_t)cus * 16);
-    if (len * (int64_t)sizeof(T) <= DI_SMALL_BYTES)
-        top_rows_kernel<T, TR_SMALL><<<grid, TR_SMALL, 0, s>>>(a, pieces, len);
+    if (len * (int64_t)sizeof(T) <= TOP_SMALL_BYTES)
+        top_rows_kernel<T, TopSmall><<<grid, TopSmall::THREADS, 0, s>>>(a, pieces, len);
+    else if (len <= top_longest<TopMiddle>(a.k, sizeof(T)))
+        top_rows_kernel<T, TopMiddle><<<grid, TopMiddle::THREADS, 0, s>>>(a, pieces, len);
     else
-        top_rows_kernel<T, TR_LARGE><<<grid, TR_LARGE, 0, s>>>(a, pieces, len);
+        top_rows_kernel<T, TopLarge><<<grid, TopLarge::THREADS, 0, s>>>(a, pieces, len);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || pieces == 1)
         return e;
-    top_join_kernel<T><<<(unsigned)std::min<int64_t>(a.R, (int64_t)cus * 16), TR_JOIN, 0, s>>>(a, pieces);
+    top_join_kernel<T><<<(unsigned)std::min<int64_t>(a.R, (int64_t)cus * 16), TopJoin::THREADS, 0, s>>>(a, pieces);
     return hipGetLastError();
 }
 
@@ -976,7 +1139,7 @@ size_t top_rows_workspace_bytes(int dt, int64_t R, int64_t V, int64_t k, int cus
 {
     int pieces;
     int64_t len;
-    split_rows(R, V, dt == FA_BF16 ? 2 : 4, TR_CAP / std::max<int64_t>(k, 1), cus, pieces, len);
+    split_top_rows(R, V, k, dt == FA_BF16 ? 2 : 4, cus, pieces, len);
     return pieces > 1 ? (size_t)(R * pieces) * (sizeof(TopPiece) + 8 * (size_t)k) : 0;
 }
 
@@ -991,7 +1154,7 @@ size_t distill_workspace_bytes(int dt, int64_t R, int64_t V, int cus)
 {
     int pieces;
     int64_t len;
-    split_rows(R, V, dt == FA_BF16 ? 2 : 4, SPLIT_MAX, cus, pieces, len);
+    split_rows(R, V, dt == FA_BF16 ? 2 : 4, SPLIT_MAX, 1, cus, pieces, len);
     return pieces > 1 ? (size_t)(R * pieces) * sizeof(TopPiece) : 0;
 }
 

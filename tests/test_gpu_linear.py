@@ -205,6 +205,22 @@ def test_large_tiles(shape, dt):
     check_backward(dy, x, w, "none", None, 1.0, *fa.linear_backward(dy, x, w, db=True))
 
 
+# outputs [P, Q] and sum length r that take each tile, ragged at both edges, in
+# all three products: the forward one, dx and dw
+@pytest.mark.parametrize("P,Q,r", [(2041, 2040, 136), (634, 12792, 72), (12792, 634, 136), (2600, 5400, 200), (2041, 2040, 72),
+                                   (130, 264, 2200), (10, 300, 1544), (1032, 16, 2056), (2041, 2039, 71)], ids=str)
+def test_each_tile_in_each_product(P, Q, r):
+    t = torch.bfloat16
+    a, b = rnd((P, r), t, 1), rnd((Q, r), t, 2, r ** -0.5)
+    check_forward(a, b, None, "none", None, 1.0, fa.linear_forward(a, b), None)
+    dy, w = rnd((P, r), t, 3), rnd((r, Q), t, 4, r ** -0.5)
+    got = fa.linear_backward(dy, torch.empty(P, Q, dtype=t, device="cuda"), w, dx=True, dw=None)
+    check_backward(dy, torch.zeros(P, Q, dtype=t), w, "none", None, 1.0, got[0], None, None)
+    dy, x = rnd((r, P), t, 5), rnd((r, Q), t, 6, r ** -0.5)
+    got = fa.linear_backward(dy, x, torch.empty(P, Q, dtype=t, device="cuda"), dx=None, dw=True)
+    check_backward(dy, x, torch.zeros(P, Q, dtype=t), "none", None, 1.0, None, got[1], None)
+
+
 @pytest.mark.parametrize("act", ["none", "gelu"])
 @pytest.mark.parametrize("only", ["dx", "dw", "db"])
 def test_backward_each_gradient_alone(only, act):

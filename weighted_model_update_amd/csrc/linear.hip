@@ -31,29 +31,75 @@ template <> struct traits<__bf16> { static constexpr int EPC = 8; };
 template <> struct traits<float> { static constexpr int EPC = 4; };
 
 // ------------------------------------------------------------ activations
-// In IEEE arithmetic as written; GELU is the exact one, z Phi(z).
-__device__ __forceinline__ float act_of(float z, int act)
+// GELU is the exact one, z Phi(z).  With x = |z| / sqrt(2),
+//     Phi(-|z|) = exp(-x^2) P(t) / 2,  t = 1 / (1 + 0.33 x),
+// P a polynomial without constant term fitted to exp(x^2) erfc(x) on
+// [0, 10] for the least relative error (9.4e-8 there, about 3e-7 as evaluated
+// in fp32, also deep in the tail).  It costs a third of the library's erff, and
+// the slope's exp(-z^2 / 2) comes with it.  The sigmoid likewise uses the
+// hardware's exp2 and reciprocal (one unit in the last place each).
+__device__ __forceinline__ float phi_below(float z, float &e) // Phi(-|z|); e = exp(-z^2 / 2)
 {
-    if (act == FA_ACT_RELU)
-        return z > 0.f ? z : (z == z ? 0.f : z);
-    if (act == FA_ACT_GELU)
-        return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-    if (act == FA_ACT_SILU)
-        return z / (1.f + expf(-z));
-    return z;
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(z), 0.33f * 0.70710678118654752f, 1.f));
+    e = __builtin_amdgcn_exp2f(z * z * (-0.5f * 1.44269504088896341f));
+    float q = -0.1353444159f;
+    q = __builtin_fmaf(q, t, 0.4602320194f);
+    q = __builtin_fmaf(q, t, -0.3511412442f);
+    q = __builtin_fmaf(q, t, 0.4084925056f);
+    q = __builtin_fmaf(q, t, 0.04722447693f);
+    q = __builtin_fmaf(q, t, 0.2012227625f);
+    q = __builtin_fmaf(q, t, 0.1829561144f);
+    q = __builtin_fmaf(q, t, 0.1863577962f);
+    return 0.5f * (q * t) * e;
 }
 
-__device__ __forceinline__ float act_slope(float z, int act)
+__device__ __forceinline__ float sigmoid(float z)
 {
-    if (act == FA_ACT_RELU)
-        return z > 0.f ? 1.f : (z == z ? 0.f : z);
-    if (act == FA_ACT_GELU)
-        return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
-    if (act == FA_ACT_SILU) {
-        const float s = 1.f / (1.f + expf(-z));
-        return s * (1.f + z * (1.f - s));
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+}
+
+// z[i] = act(z[i]); NaN stays NaN
+template <int W> __device__ __forceinline__ void apply_act(float *z, int act)
+{
+    if (act == FA_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < W; i++)
+            z[i] = z[i] < 0.f ? 0.f : z[i];
+    } else if (act == FA_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < W; i++) {
+            float e;
+            const float q = phi_below(z[i], e);
+            z[i] *= z[i] > 0.f ? 1.f - q : q;
+        }
+    } else if (act == FA_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < W; i++)
+            z[i] *= sigmoid(z[i]);
     }
-    return 1.f;
+}
+
+// d[i] *= act'(z[i])
+template <int W> __device__ __forceinline__ void apply_slope(float *d, const float *z, int act)
+{
+    if (act == FA_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < W; i++)
+            d[i] *= z[i] > 0.f ? 1.f : z[i] == z[i] ? 0.f : z[i];
+    } else if (act == FA_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < W; i++) {
+            float e;
+            const float q = phi_below(z[i], e);
+            d[i] *= __builtin_fmaf(z[i] * e, 0.39894228040143268f, z[i] > 0.f ? 1.f - q : q);
+        }
+    } else if (act == FA_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < W; i++) {
+            const float s = sigmoid(z[i]);
+            d[i] *= s * __builtin_fmaf(z[i], 1.f - s, 1.f);
+        }
+    }
 }
 
 // 16 bytes of T from an address that is only element-aligned, of which the
@@ -124,11 +170,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs &p, int64_t m, int n, co
         z[i] = __builtin_fmaf(p.alpha, s[i], b[i]);
     if (p.pre)
         store_n<T, W>(static_cast<T *>(p.pre) + m * p.ldp + n, valid, z);
-    if (p.act != FA_ACT_NONE) {
-#pragma unroll
-        for (int i = 0; i < W; i++)
-            z[i] = act_of(z[i], p.act);
-    }
+    apply_act<W>(z, p.act);
     if (p.res) {
         load_n<T, W>(static_cast<const T *>(p.res) + m * p.ldr + n, valid, b);
 #pragma unroll
@@ -139,9 +181,9 @@ __device__ __forceinline__ void epilogue(const GemmArgs &p, int64_t m, int n, co
 }
 
 // ------------------------------------------------------------ LDS tiles
-// An inner operand's tile holds `rows` rows of 128 bytes; its 16-byte chunk c
-// of row r lies at chunk c ^ (r & 7), so the 16 rows that a fragment read
-// touches spread over all banks.  An outer operand's tile holds one row of
+// An inner operand's tile holds `rows` rows of STEP bytes; its 16-byte chunk c
+// of row r lies at chunk c ^ inner_swizzle(r), so the 16 rows that a fragment
+// read touches spread over all banks.  An outer operand's tile holds one row of
 // `cols` elements per k; there the chunks of row k are exchanged by
 // outer_swizzle, so the rows that one transposing read touches do.
 template <typename T, int COLS> __device__ __forceinline__ int outer_swizzle(int k)
@@ -153,20 +195,25 @@ template <typename T, int COLS> __device__ __forceinline__ int outer_swizzle(int
         return (((k >> 2) & 3) << 2) & (CPR - 1);
 }
 
+template <int STEP> __device__ __forceinline__ int inner_swizzle(int r)
+{
+    return STEP == 128 ? r & 7 : (r >> 2) & 3;
+}
+
 struct Frag {
     u32x4 v; // bf16: 8 values of k;  fp32: 4 values of k
 };
 
-// Fragment of 16 rows (or columns) starting at r0, k half kk (0, 1) of the
-// step: lane l holds row l % 16 and the 16 bytes of k of group l / 16.
-template <typename T, bool OUTER, int ROWS>
+// Fragment of 16 rows (or columns) starting at r0, the 64 bytes kk of the
+// step's k: lane l holds row l % 16 and the 16 bytes of group l / 16.
+template <typename T, bool OUTER, int ROWS, int STEP>
 __device__ __forceinline__ Frag read_frag(const char *tile, int r0, int kk, int lane)
 {
     const int i = lane & 15, g = lane >> 4;
     Frag f;
     if constexpr (!OUTER) {
         const int r = r0 + i, c = g + 4 * kk;
-        f.v = *reinterpret_cast<const u32x4 *>(tile + r * STEP_BYTES + ((c ^ (r & 7)) << 4));
+        f.v = *reinterpret_cast<const u32x4 *>(tile + (r * STEP + ((c ^ inner_swizzle<STEP>(r)) << 4)));
     } else if constexpr (sizeof(T) == 2) {
         // Two transposing reads, k = 8g .. 8g+3 and 8g+4 .. 8g+7.  Within 16
         // lanes, lane i supplies the address of row i/4, columns 4(i%4) and
@@ -177,7 +224,7 @@ __device__ __forceinline__ Frag read_frag(const char *tile, int r0, int kk, int 
             const int k = kk * 32 + 8 * g + 4 * j + (i >> 2);
             const int col = r0 + (i & 3) * 4;
             const int c = (col >> 3) ^ outer_swizzle<T, ROWS>(k);
-            const char *at = tile + k * (ROWS * 2) + (c << 4) + ((col & 4) << 1);
+            const char *at = tile + (k * (ROWS * 2) + (c << 4) + ((col & 4) << 1));
             h[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                 (__attribute__((address_space(3))) s16x4 *)const_cast<char *>(at));
         }
@@ -188,7 +235,7 @@ __device__ __forceinline__ Frag read_frag(const char *tile, int r0, int kk, int 
         for (int j = 0; j < 4; j++) {
             const int k = kk * 16 + 4 * g + j, col = r0 + i;
             const int c = (col >> 2) ^ outer_swizzle<T, ROWS>(k);
-            f.v[j] = *reinterpret_cast<const uint32_t *>(tile + k * (ROWS * 4) + (c << 4) + ((col & 3) << 2));
+            f.v[j] = *reinterpret_cast<const uint32_t *>(tile + (k * (ROWS * 4) + (c << 4) + ((col & 3) << 2)));
         }
     }
     return f;
@@ -274,12 +321,12 @@ template <typename T, bool OUTER, int ROWS, int THREADS> struct Stage {
 // outside the operand gets an offset past the buffer's range, which reads 0.
 constexpr uint32_t OUT_OF_RANGE = 0x80000000u;
 
-template <typename T, bool OUTER, int ROWS, int THREADS> struct Direct {
+template <typename T, bool OUTER, int ROWS, int THREADS, int STEP> struct Direct {
     static constexpr int EPC = traits<T>::EPC;
-    static constexpr int BK = STEP_BYTES / (int)sizeof(T);
-    static constexpr int CHUNKS = ROWS * STEP_BYTES / 16;
+    static constexpr int BK = STEP / (int)sizeof(T);
+    static constexpr int CHUNKS = ROWS * STEP / 16;
     static constexpr int CH = (CHUNKS + THREADS - 1) / THREADS;
-    static constexpr int CPR = OUTER ? ROWS / EPC : 8;
+    static constexpr int CPR = OUTER ? ROWS / EPC : STEP / 16;
     uint32_t off[CH]; // byte offset of each chunk from the tile's base
     const char *base;
     int64_t advance; // bytes from one step to the next
@@ -287,12 +334,12 @@ template <typename T, bool OUTER, int ROWS, int THREADS> struct Direct {
     __device__ __forceinline__ void init(const T *p, int64_t ld, int r0, int rows, int k0)
     {
         base = reinterpret_cast<const char *>(OUTER ? p + (int64_t)k0 * ld + r0 : p + (int64_t)r0 * ld + k0);
-        advance = OUTER ? BK * ld * (int64_t)sizeof(T) : STEP_BYTES;
+        advance = OUTER ? BK * ld * (int64_t)sizeof(T) : STEP;
 #pragma unroll
         for (int c = 0; c < CH; c++) {
             const int q = threadIdx.x + c * THREADS;
             if constexpr (!OUTER) {
-                const int r = q / 8, ch = (q % 8) ^ (r & 7);
+                const int r = q / CPR, ch = (q % CPR) ^ inner_swizzle<STEP>(r);
                 off[c] = r0 + r < rows ? (uint32_t)(r * ld * (int64_t)sizeof(T)) + ch * 16 : OUT_OF_RANGE;
             } else {
                 const int k = q / CPR, ch = (q % CPR) ^ outer_swizzle<T, ROWS>(k);
@@ -314,7 +361,7 @@ template <typename T, bool OUTER, int ROWS, int THREADS> struct Direct {
             uint32_t o = off[c];
             if (left < BK) {
                 const int q = threadIdx.x + c * THREADS;
-                const int k = OUTER ? q / CPR : ((q % 8) ^ ((q / 8) & 7)) * EPC;
+                const int k = OUTER ? q / CPR : ((q % CPR) ^ inner_swizzle<STEP>(q / CPR)) * EPC;
                 o = k < left ? o : OUT_OF_RANGE;
             }
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -337,10 +384,10 @@ template <typename T, int BM, int BN, int WM, int WN, bool AO, bool BO> struct T
             Frag fa[FM], fb[FN];
 #pragma unroll
             for (int i = 0; i < FM; i++)
-                fa[i] = read_frag<T, AO, BM>(ta, wm + i * 16, kk, lane);
+                fa[i] = read_frag<T, AO, BM, STEP_BYTES>(ta, wm + i * 16, kk, lane);
 #pragma unroll
             for (int j = 0; j < FN; j++)
-                fb[j] = read_frag<T, BO, BN>(tb, wn + j * 16, kk, lane);
+                fb[j] = read_frag<T, BO, BN, STEP_BYTES>(tb, wn + j * 16, kk, lane);
 #pragma unroll
             for (int i = 0; i < FM; i++)
 #pragma unroll
@@ -376,6 +423,56 @@ __device__ __forceinline__ void tile_of(unsigned id, unsigned tiles_m, unsigned 
     tn = id % band / high;
 }
 
+// The finished tile goes through LDS, 16 rows of each row of wavefronts at a
+// time, so that whole rows are read and written from consecutive lanes.  Two
+// buffers of BYTES take turns; where one does not hold that many rows, the
+// columns go in parts.
+constexpr int EPI_W = 8;
+
+// Where four columns from n of row r lie in such a buffer: the rows that one
+// fragment holds are spread over the banks.
+template <int COLS> __device__ __forceinline__ int write_tile_at(int r, int n)
+{
+    return r * COLS + (((n >> 2) ^ (r & 15 & (COLS / 4 - 1))) << 2);
+}
+
+template <typename T, int BM, int BN, int WM, int WN, int BYTES>
+__device__ __forceinline__ void write_tile(const GemmArgs &p, int m0, int n0, const f32x4 (&acc)[BM / WM / 16][BN / WN / 16],
+                                           char *b0, char *b1, float *part)
+{
+    constexpr int THREADS = WM * WN * WAVE, FM = BM / WM / 16, FN = BN / WN / 16;
+    constexpr int W = EPI_W, ROWS = WM * 16, PARTS = (ROWS * BN * 4 + BYTES - 1) / BYTES, COLS = BN / PARTS;
+    static_assert(WN % PARTS == 0, "a part is whole wavefronts");
+    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE, wn = (wave % WN) * (BN / WN);
+#pragma unroll
+    for (int q = 0; q < FM * PARTS; q++) {
+        const int i = q / PARTS, c0 = q % PARTS * COLS;
+        float *o = reinterpret_cast<float *>(q & 1 ? b1 : b0);
+        if (PARTS == 1 || (wn >= c0 && wn < c0 + COLS)) {
+#pragma unroll
+            for (int j = 0; j < FN; j++)
+                *reinterpret_cast<f32x4 *>(
+                    o + write_tile_at<COLS>((wave / WN) * 16 + (lane & 15), wn - c0 + j * 16 + (lane >> 4) * 4)) = acc[i][j];
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int e = threadIdx.x; e < ROWS * COLS / W; e += THREADS) {
+            const int r = e / (COLS / W), c = e % (COLS / W) * W, n = n0 + c0 + c;
+            const int m = m0 + r / 16 * (BM / WM) + i * 16 + r % 16;
+            if (m < p.M && n < p.N) {
+                float v[W];
+#pragma unroll
+                for (int h = 0; h < W; h += 4)
+                    __builtin_memcpy(v + h, o + write_tile_at<COLS>(r, c + h), 16);
+                if (part)
+                    store_n<float, W>(part + ((int64_t)blockIdx.y * p.M + m) * p.N + n, p.N - n, v);
+                else
+                    epilogue<T, W>(p, m, n, v);
+            }
+        }
+    }
+}
+
 // Workgroup (tile, split): the sums over k in [split * kper, + kper).  With
 // more than one split they go to `part` [split][M][N], else to the epilogue.
 template <typename T, int BM, int BN, int WM, int WN, bool AO, bool BO, bool DIRECT>
@@ -406,8 +503,8 @@ __global__ __launch_bounds__(WM *WN *WAVE) void gemm_kernel(GemmArgs p, int tile
             t.acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     if constexpr (DIRECT) {
-        Direct<T, AO, BM, THREADS> da;
-        Direct<T, BO, BN, THREADS> db;
+        Direct<T, AO, BM, THREADS, STEP_BYTES> da;
+        Direct<T, BO, BN, THREADS, STEP_BYTES> db;
         da.init(a, p.lda, m0, p.M, k0);
         db.init(b, p.ldb, n0, p.N, k0);
         if (steps > 0) {
@@ -455,32 +552,118 @@ __global__ __launch_bounds__(WM *WN *WAVE) void gemm_kernel(GemmArgs p, int tile
             __syncthreads();
         }
     }
-    // The finished tile goes through LDS, 16 rows of each row of wavefronts at
-    // a time, so that whole rows are read and written from consecutive lanes.
-    constexpr int W = 8, PITCH = BN + 4, ROWS = WM * 16;
-    static_assert(ROWS * PITCH * 4 <= AB + BB, "a pass of the epilogue fits one buffer");
+    write_tile<T, BM, BN, WM, WN, AB + BB>(p, m0, n0, t.acc, l0, l1, part);
+}
+
+// The kernel of large products.  Steps of 64 bytes of k, four buffers: while
+// the matrix cores work on step t from registers, the fragments of step t + 1
+// are read from LDS into a second set, and the copies of steps t + 2 and t + 3
+// are on their way.  One barrier a step.
+constexpr int PIPE_STEP = 64;
+
+// LDS reads that read_frag makes.
+template <typename T, bool OUTER> constexpr int reads_per_frag() { return !OUTER ? 1 : sizeof(T) == 2 ? 2 : 4; }
+
+template <typename T, int BM, int BN, int WM, int WN, bool AO, bool BO>
+__global__ __launch_bounds__(WM *WN *WAVE) void pipe_kernel(GemmArgs p, int tiles_m, int tiles_n)
+{
+    constexpr int THREADS = WM * WN * WAVE;
+    constexpr int BK = PIPE_STEP / (int)sizeof(T);
+    constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
+    constexpr int AB = BM * PIPE_STEP, BB = BN * PIPE_STEP;
+    constexpr int COPIES = (AB + BB) / 16 / THREADS; // per thread and step
+    __shared__ __attribute__((aligned(1024))) char l0[AB + BB];
+    __shared__ __attribute__((aligned(1024))) char l1[AB + BB];
+    __shared__ __attribute__((aligned(1024))) char l2[AB + BB];
+    __shared__ __attribute__((aligned(1024))) char l3[AB + BB];
+    static_assert(AB % (16 * THREADS) == 0 && BB % (16 * THREADS) == 0, "every thread copies the same number of chunks");
+
+    unsigned tm, tn;
+    tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    const int m0 = (int)tm * BM, n0 = (int)tn * BN;
+    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
+    const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
+    const int steps = (p.K + BK - 1) / BK;
+    f32x4 acc[FM][FN];
 #pragma unroll
-    for (int i = 0; i < FM; i++) {
-        float *o = reinterpret_cast<float *>(i & 1 ? l1 : l0);
+    for (int i = 0; i < FM; i++)
 #pragma unroll
         for (int j = 0; j < FN; j++)
-            *reinterpret_cast<f32x4 *>(o + ((wave / WN) * 16 + (lane & 15)) * PITCH + wn + j * 16 + (lane >> 4) * 4) =
-                t.acc[i][j];
-        __syncthreads();
-#pragma unroll 1
-        for (int q = threadIdx.x; q < ROWS * BN / W; q += THREADS) {
-            const int r = q / (BN / W), n = n0 + q % (BN / W) * W;
-            const int m = m0 + r / 16 * (BM / WM) + i * 16 + r % 16;
-            if (m < p.M && n < p.N) {
-                float v[W];
-                __builtin_memcpy(v, o + r * PITCH + n - n0, sizeof v);
-                if (part)
-                    store_n<float, W>(part + ((int64_t)blockIdx.y * p.M + m) * p.N + n, p.N - n, v);
-                else
-                    epilogue<T, W>(p, m, n, v);
-            }
+            acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    Direct<T, AO, BM, THREADS, PIPE_STEP> da;
+    Direct<T, BO, BN, THREADS, PIPE_STEP> db;
+    da.init(static_cast<const T *>(p.a), p.lda, m0, p.M, 0);
+    db.init(static_cast<const T *>(p.b), p.ldb, n0, p.N, 0);
+    int left = p.K; // of the next step to copy; steps past the end copy zeros
+    const auto copy = [&](char *l) {
+        da.start(l, left);
+        db.start(l + AB, left);
+        left -= BK;
+    };
+    Frag fa[FM], fb[2][FN];
+    constexpr int RA = reads_per_frag<T, AO>(), RB = reads_per_frag<T, BO>();
+    // step t: `next` holds step t + 1, `free` step t - 1.  A's fragments are
+    // replaced as soon as their row of products is issued, so only B's take
+    // two sets of registers.
+    const auto step = [&](char *next, char *free, int s) {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0x0f70 | COPIES); // step t + 1 is here, t + 2 may be under way
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        copy(free);
+#pragma unroll
+        for (int i = 0; i < FM; i++) {
+#pragma unroll
+            for (int j = 0; j < FN; j++)
+                acc[i][j] = mma<T>(fb[s][j], fa[i], acc[i][j]);
+            fa[i] = read_frag<T, AO, BM, PIPE_STEP>(next, wm + i * 16, 0, lane);
+            if (i < FN)
+                fb[s ^ 1][i] = read_frag<T, BO, BN, PIPE_STEP>(next + AB, wn + i * 16, 0, lane);
         }
+        constexpr int ROW = FN * (sizeof(T) == 2 ? 1 : 4);
+#pragma unroll
+        for (int i = 0; i < FN; i++) {
+            __builtin_amdgcn_sched_group_barrier(0x008, ROW, 0);     // matrix instructions
+            __builtin_amdgcn_sched_group_barrier(0x100, RA + RB, 0); // reads of LDS
+            __builtin_amdgcn_sched_group_barrier(0x020, (COPIES + FN - 1) / FN, 0); // copies
+        }
+#pragma unroll
+        for (int i = FN; i < FM; i++) {
+            __builtin_amdgcn_sched_group_barrier(0x008, ROW, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, RA, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    static_assert(FN <= FM, "B's fragments are read along A's");
+    copy(l0);
+    copy(l1);
+    copy(l2);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0f70 | (2 * COPIES));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < FM; i++)
+        fa[i] = read_frag<T, AO, BM, PIPE_STEP>(l0, wm + i * 16, 0, lane);
+#pragma unroll
+    for (int j = 0; j < FN; j++)
+        fb[0][j] = read_frag<T, BO, BN, PIPE_STEP>(l0 + AB, wn + j * 16, 0, lane);
+    int t = 0;
+    for (; t + 4 <= steps; t += 4) {
+        step(l1, l3, 0);
+        step(l2, l0, 1);
+        step(l3, l1, 0);
+        step(l0, l2, 1);
     }
+    if (t < steps)
+        step(l1, l3, 0);
+    if (t + 1 < steps)
+        step(l2, l0, 1);
+    if (t + 2 < steps)
+        step(l3, l1, 0);
+    copies_done(); // also those past the end
+    write_tile<T, BM, BN, WM, WN, AB + BB>(p, m0, n0, acc, l0, l1, nullptr);
 }
 
 // Joins the splits' sums in split order and finishes them.
@@ -505,26 +688,53 @@ template <typename T> __global__ __launch_bounds__(JOIN_THREADS) void join_kerne
     epilogue<T, JOIN_W>(p, m, n, s);
 }
 
-template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
-hipError_t run_tile(const GemmArgs &a, int layout, int splits, float *ws, hipStream_t s)
+// Steps of `bytes` of k a split, and how many splits that makes.
+struct Split {
+    int kper, splits;
+};
+
+template <typename T> Split split_of(int K, int splits, int bytes)
 {
-    constexpr int BK = STEP_BYTES / (int)sizeof(T);
-    const int64_t tm = ((int64_t)a.M + BM - 1) / BM, tn = ((int64_t)a.N + BN - 1) / BN;
-    const int steps = std::max(1, (a.K + BK - 1) / BK), per = (steps + splits - 1) / splits;
-    splits = (steps + per - 1) / per;
-    float *part = splits > 1 ? ws : nullptr;
-    const dim3 grid((unsigned)(tm * tn), (unsigned)splits), block(WM * WN * WAVE);
-    if (layout == 0)
-        gemm_kernel<T, BM, BN, WM, WN, false, false, DIRECT><<<grid, block, 0, s>>>(a, (int)tm, (int)tn, per * BK, part);
-    else if (layout == GEMM_B_OUTER)
-        gemm_kernel<T, BM, BN, WM, WN, false, true, DIRECT><<<grid, block, 0, s>>>(a, (int)tm, (int)tn, per * BK, part);
-    else
-        gemm_kernel<T, BM, BN, WM, WN, true, true, DIRECT><<<grid, block, 0, s>>>(a, (int)tm, (int)tn, per * BK, part);
+    const int bk = bytes / (int)sizeof(T), steps = std::max(1, (K + bk - 1) / bk), per = (steps + splits - 1) / splits;
+    return {per * bk, (steps + per - 1) / per};
+}
+
+template <typename T> hipError_t run_join(const GemmArgs &a, const float *part, int splits, hipStream_t s)
+{
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !part)
+    if (e != hipSuccess || splits == 1)
         return e;
     const int64_t groups = (int64_t)a.M * ((a.N + JOIN_W - 1) / JOIN_W);
     join_kernel<T><<<(unsigned)((groups + JOIN_THREADS - 1) / JOIN_THREADS), JOIN_THREADS, 0, s>>>(a, part, splits);
+    return hipGetLastError();
+}
+
+template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
+hipError_t run_tile(const GemmArgs &a, int layout, int splits, float *ws, hipStream_t s)
+{
+    const int64_t tm = ((int64_t)a.M + BM - 1) / BM, tn = ((int64_t)a.N + BN - 1) / BN;
+    const Split k = split_of<T>(a.K, splits, STEP_BYTES);
+    float *part = k.splits > 1 ? ws : nullptr;
+    const dim3 grid((unsigned)(tm * tn), (unsigned)k.splits), block(WM * WN * WAVE);
+    if (layout == 0)
+        gemm_kernel<T, BM, BN, WM, WN, false, false, DIRECT><<<grid, block, 0, s>>>(a, (int)tm, (int)tn, k.kper, part);
+    else if (layout == GEMM_B_OUTER)
+        gemm_kernel<T, BM, BN, WM, WN, false, true, DIRECT><<<grid, block, 0, s>>>(a, (int)tm, (int)tn, k.kper, part);
+    else
+        gemm_kernel<T, BM, BN, WM, WN, true, true, DIRECT><<<grid, block, 0, s>>>(a, (int)tm, (int)tn, k.kper, part);
+    return run_join<T>(a, part, k.splits, s);
+}
+
+template <typename T, int BM, int BN, int WM, int WN> hipError_t run_pipe(const GemmArgs &a, int layout, hipStream_t s)
+{
+    const int64_t tm = ((int64_t)a.M + BM - 1) / BM, tn = ((int64_t)a.N + BN - 1) / BN;
+    const dim3 grid((unsigned)(tm * tn)), block(WM * WN * WAVE);
+    if (layout == 0)
+        pipe_kernel<T, BM, BN, WM, WN, false, false><<<grid, block, 0, s>>>(a, (int)tm, (int)tn);
+    else if (layout == GEMM_B_OUTER)
+        pipe_kernel<T, BM, BN, WM, WN, false, true><<<grid, block, 0, s>>>(a, (int)tm, (int)tn);
+    else
+        pipe_kernel<T, BM, BN, WM, WN, true, true><<<grid, block, 0, s>>>(a, (int)tm, (int)tn);
     return hipGetLastError();
 }
 
@@ -555,11 +765,7 @@ template <typename T> __global__ __launch_bounds__(AG_THREADS) void act_grad_ker
         }
 #pragma unroll
         for (int u = 0; u < AG_U; u++) {
-            if (p.act != FA_ACT_NONE) {
-#pragma unroll
-                for (int i = 0; i < AG_W; i++)
-                    d[u][i] *= act_slope(z[u][i], p.act);
-            }
+            apply_slope<AG_W>(d[u], z[u], p.act);
             if (p.dz)
                 store_n<T, AG_W>(static_cast<T *>(p.dz) + (m0 + u) * p.N + n, m0 + u < r1 ? valid : 0, d[u]);
 #pragma unroll
@@ -608,7 +814,8 @@ bool direct_ok(const void *p, int64_t ld, int64_t row, size_t es)
            ld * (int64_t)es * 257 < (int64_t)OUT_OF_RANGE;
 }
 
-enum { TILE_256, TILE_128, TILE_64, TILE_THIN_N, TILE_THIN_M };
+// Tiles: PIPE_* by the pipelined kernel, the others by the two-buffer one.
+enum { PIPE_256_256, PIPE_256_128, PIPE_128_256, PIPE_128_128, TILE_64, TILE_THIN_N, TILE_THIN_M };
 
 struct Plan {
     int tile, splits;
@@ -616,54 +823,74 @@ struct Plan {
 
 int64_t tiles(int64_t M, int64_t N, int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
 
-Plan plan_of(int64_t M, int64_t N, int64_t K, size_t es, int cus)
+// The time of a pipelined tile per k is steady, so tiles are compared by the
+// rounds that they need on all CUs: one 256x256 or 256x128 tile fits a CU at a
+// time, two of 128x128.  Measured on 256 CUs, us for bf16 products of K = 8192:
+// a round of 256x256 226, of 256x128 or 128x256 122, of 128x128 130 with two a
+// CU and 86 with one.  (4096x2048x8192, 128 tiles of 256x256: 173 us; 256 of
+// 128x256: 119; 512 of 128x128: 139.)  fp32 is bound by the matrix cores at
+// any tile (128x128 140 TFLOP/s, 256x128 142, 64x64 133).
+int pipe_for(int64_t M, int64_t N, int cus)
 {
-    if (tiles(M, N, 256, 256) * 4 >= 3 * cus)
-        return {TILE_256, 1};
-    int tile = TILE_64;
-    int64_t count = tiles(M, N, 64, 64);
-    if (N <= 16) {
-        tile = TILE_THIN_N;
-        count = tiles(M, N, 128, 16);
-    } else if (M <= 16) {
-        tile = TILE_THIN_M;
-        count = tiles(M, N, 16, 128);
-    } else if (tiles(M, N, 128, 128) >= cus) {
-        tile = TILE_128;
-        count = tiles(M, N, 128, 128);
-    }
-    // fill the chip, at least 4 steps of k a split
-    const int64_t steps = K * (int64_t)es / STEP_BYTES;
-    const int64_t want = tile == TILE_128 ? 2 * cus : 4 * cus;
-    const int64_t splits = std::min<int64_t>(std::min<int64_t>(want / std::max<int64_t>(count, 1), steps / 4), 64);
-    return {tile, (int)std::max<int64_t>(1, splits)};
+    const auto rounds = [&](int64_t t, int64_t fit) { return (t + fit - 1) / fit; };
+    const int64_t t128 = tiles(M, N, 128, 128), whole = t128 / (2 * cus), rest = t128 % (2 * cus);
+    const int64_t costs[4] = {226 * rounds(tiles(M, N, 256, 256), cus), 122 * rounds(tiles(M, N, 256, 128), cus),
+                              122 * rounds(tiles(M, N, 128, 256), cus),
+                              130 * whole + (rest > cus ? 130 : rest > 0 ? 86 : 0)};
+    return (int)(std::min_element(costs, costs + 4) - costs);
 }
 
-template <typename T, bool DIRECT> hipError_t run_plan(const GemmArgs &a, int layout, Plan p, float *ws, hipStream_t s)
+// Small products: 64x64 tiles with k split until about two workgroups a CU
+// run, SMALL_MIN_STEPS steps of 128 bytes each at least.  Measured, us for bf16
+// with K = 4096: 512x1024 unsplit 34, in 2 23, in 4 17, in 8 19; 256x1024
+// 22, 16, 13, 15; 1024x2048 with K = 512 unsplit 7.5, in 2 20.  Against the
+// pipelined kernel: 2048x2048x4096 64x64 49, 128x128 45.
+constexpr int SMALL_MIN_STEPS = 16, THIN_MIN_STEPS = 4;
+
+Plan plan_of(int64_t M, int64_t N, int64_t K, size_t es, int cus)
 {
-    switch (p.tile) {
-    case TILE_256:
-        if constexpr (DIRECT)
-            return run_tile<T, 256, 256, 2, 4, true>(a, layout, 1, ws, s);
-        [[fallthrough]];
-    case TILE_128:
-        return run_tile<T, 128, 128, 2, 2, DIRECT>(a, layout, p.splits, ws, s);
-    case TILE_64:
-        return run_tile<T, 64, 64, 2, 2, DIRECT>(a, layout, p.splits, ws, s);
-    case TILE_THIN_N:
-        return run_tile<T, 128, 16, 4, 1, DIRECT>(a, layout, p.splits, ws, s);
-    default:
-        return run_tile<T, 16, 128, 1, 4, DIRECT>(a, layout, p.splits, ws, s);
-    }
+    const int64_t steps = K * (int64_t)es / STEP_BYTES;
+    const auto split = [&](int64_t count, int64_t per_cu, int64_t least) {
+        return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(per_cu * cus / std::max<int64_t>(count, 1), steps / least), 64));
+    };
+    if (N <= 16)
+        return {TILE_THIN_N, split(tiles(M, N, 128, 16), 4, THIN_MIN_STEPS)};
+    if (M <= 16)
+        return {TILE_THIN_M, split(tiles(M, N, 16, 128), 4, THIN_MIN_STEPS)};
+    if (es == 2 && tiles(M, N, 128, 128) >= cus)
+        return {pipe_for(M, N, cus), 1};
+    if (es == 4 && tiles(M, N, 128, 128) >= 2 * cus)
+        return {PIPE_128_128, 1};
+    // fp32 works longer on a step, so it pays to even out the CUs' shares
+    return {TILE_64, es == 2 ? split(tiles(M, N, 64, 64), 2, SMALL_MIN_STEPS) : split(tiles(M, N, 64, 64), 5, SMALL_MIN_STEPS + 4)};
 }
 
 template <typename T> hipError_t gemm_of(const GemmArgs &a, int layout, float *ws, int cus, hipStream_t s)
 {
     const Plan p = plan_of(a.M, a.N, a.K, sizeof(T), cus);
-    if (direct_ok(a.a, a.lda, layout & GEMM_A_OUTER ? a.M : a.K, sizeof(T)) &&
-        direct_ok(a.b, a.ldb, layout & GEMM_B_OUTER ? a.N : a.K, sizeof(T)))
-        return run_plan<T, true>(a, layout, p, ws, s);
-    return run_plan<T, false>(a, layout, p, ws, s);
+    const bool direct = direct_ok(a.a, a.lda, layout & GEMM_A_OUTER ? a.M : a.K, sizeof(T)) &&
+                        direct_ok(a.b, a.ldb, layout & GEMM_B_OUTER ? a.N : a.K, sizeof(T));
+    if (p.tile <= PIPE_128_128) {
+        if (!direct)
+            return run_tile<T, 128, 128, 2, 2, false>(a, layout, 1, ws, s);
+        if constexpr (sizeof(T) == 2) {
+            if (p.tile == PIPE_256_256)
+                return run_pipe<T, 256, 256, 2, 4>(a, layout, s);
+            if (p.tile == PIPE_256_128)
+                return run_pipe<T, 256, 128, 4, 2>(a, layout, s);
+            if (p.tile == PIPE_128_256)
+                return run_pipe<T, 128, 256, 2, 4>(a, layout, s);
+        }
+        return run_pipe<T, 128, 128, 2, 4>(a, layout, s);
+    }
+    if (p.tile == TILE_64)
+        return direct ? run_tile<T, 64, 64, 2, 2, true>(a, layout, p.splits, ws, s)
+                      : run_tile<T, 64, 64, 2, 2, false>(a, layout, p.splits, ws, s);
+    if (p.tile == TILE_THIN_N)
+        return direct ? run_tile<T, 128, 16, 4, 1, true>(a, layout, p.splits, ws, s)
+                      : run_tile<T, 128, 16, 4, 1, false>(a, layout, p.splits, ws, s);
+    return direct ? run_tile<T, 16, 128, 1, 4, true>(a, layout, p.splits, ws, s)
+                  : run_tile<T, 16, 128, 1, 4, false>(a, layout, p.splits, ws, s);
 }
 
 } // namespace

@@ -153,29 +153,52 @@ template <typename T, int W> __device__ __forceinline__ void store_n(T *p, int v
     }
 }
 
+// W values of a row as they are stored, so that they can be fetched ahead;
+// zeros where there is nothing to fetch.
+template <typename T, int W> struct Raw {
+    T e[W];
+    __device__ __forceinline__ void fetch(const T *p, int valid)
+    {
+        if (valid >= W) {
+            __builtin_memcpy(e, p, sizeof e);
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; i++)
+                e[i] = i < valid ? p[i] : (T)0.f;
+        }
+    }
+};
+
+template <typename T, int W> __device__ __forceinline__ void fetch_bias(const GemmArgs &p, int n, Raw<T, W> &b)
+{
+    b.fetch(p.bias ? static_cast<const T *>(p.bias) + n : nullptr, p.bias ? p.N - n : 0);
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void fetch_residual(const GemmArgs &p, int64_t m, int n, Raw<T, W> &r)
+{
+    const bool any = p.res && m < p.M;
+    r.fetch(any ? static_cast<const T *>(p.res) + m * p.ldr + n : nullptr, any ? p.N - n : 0);
+}
+
 // out(m, n..n+W-1) from the finished sums: z = alpha s + bias, then the
 // activation, then the residual, all in fp32, each result rounded once.
 template <typename T, int W>
-__device__ __forceinline__ void epilogue(const GemmArgs &p, int64_t m, int n, const float *s)
+__device__ __forceinline__ void epilogue(const GemmArgs &p, int64_t m, int n, const float *s, const Raw<T, W> &bias,
+                                         const Raw<T, W> &res)
 {
     const int valid = p.N - n;
-    float z[W], b[W];
+    float z[W];
 #pragma unroll
     for (int i = 0; i < W; i++)
-        b[i] = 0.f;
-    if (p.bias)
-        load_n<T, W>(static_cast<const T *>(p.bias) + n, valid, b);
-#pragma unroll
-    for (int i = 0; i < W; i++)
-        z[i] = __builtin_fmaf(p.alpha, s[i], b[i]);
+        z[i] = __builtin_fmaf(p.alpha, s[i], (float)bias.e[i]);
     if (p.pre)
         store_n<T, W>(static_cast<T *>(p.pre) + m * p.ldp + n, valid, z);
     apply_act<W>(z, p.act);
     if (p.res) {
-        load_n<T, W>(static_cast<const T *>(p.res) + m * p.ldr + n, valid, b);
 #pragma unroll
         for (int i = 0; i < W; i++)
-            z[i] += b[i];
+            z[i] += (float)res.e[i];
     }
     store_n<T, W>(static_cast<T *>(p.out) + m * p.ldo + n, valid, z);
 }
@@ -442,11 +465,27 @@ __device__ __forceinline__ void write_tile(const GemmArgs &p, int m0, int n0, co
 {
     constexpr int THREADS = WM * WN * WAVE, FM = BM / WM / 16, FN = BN / WN / 16;
     constexpr int W = EPI_W, ROWS = WM * 16, PARTS = (ROWS * BN * 4 + BYTES - 1) / BYTES, COLS = BN / PARTS;
+    constexpr int PER = (ROWS * COLS / W + THREADS - 1) / THREADS; // chunks a thread writes in a pass
     static_assert(WN % PARTS == 0, "a part is whole wavefronts");
+    static_assert(THREADS % (COLS / W) == 0, "a thread keeps its columns");
     const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE, wn = (wave % WN) * (BN / WN);
+    const int c = threadIdx.x % (COLS / W) * W, r0 = threadIdx.x / (COLS / W);
+    const auto row = [&](int q, int e) { // of the thread's e-th chunk in pass q
+        const int r = r0 + e * (THREADS / (COLS / W));
+        return r < ROWS ? m0 + r / 16 * (BM / WM) + q / PARTS * 16 + r % 16 : p.M;
+    };
+    Raw<T, W> bias[PARTS], res[2][PER];
+    if (!part) {
+#pragma unroll
+        for (int h = 0; h < PARTS; h++)
+            fetch_bias(p, n0 + h * COLS + c, bias[h]);
+#pragma unroll
+        for (int e = 0; e < PER; e++)
+            fetch_residual(p, row(0, e), n0 + c, res[0][e]);
+    }
 #pragma unroll
     for (int q = 0; q < FM * PARTS; q++) {
-        const int i = q / PARTS, c0 = q % PARTS * COLS;
+        const int i = q / PARTS, h = q % PARTS, c0 = h * COLS;
         float *o = reinterpret_cast<float *>(q & 1 ? b1 : b0);
         if (PARTS == 1 || (wn >= c0 && wn < c0 + COLS)) {
 #pragma unroll
@@ -454,20 +493,25 @@ __device__ __forceinline__ void write_tile(const GemmArgs &p, int m0, int n0, co
                 *reinterpret_cast<f32x4 *>(
                     o + write_tile_at<COLS>((wave / WN) * 16 + (lane & 15), wn - c0 + j * 16 + (lane >> 4) * 4)) = acc[i][j];
         }
+        // the next pass's residual is on its way while this pass is written
+        if (!part && q + 1 < FM * PARTS) {
+#pragma unroll
+            for (int e = 0; e < PER; e++)
+                fetch_residual(p, row(q + 1, e), n0 + (q + 1) % PARTS * COLS + c, res[(q + 1) & 1][e]);
+        }
         __syncthreads();
-#pragma unroll 1
-        for (int e = threadIdx.x; e < ROWS * COLS / W; e += THREADS) {
-            const int r = e / (COLS / W), c = e % (COLS / W) * W, n = n0 + c0 + c;
-            const int m = m0 + r / 16 * (BM / WM) + i * 16 + r % 16;
+#pragma unroll
+        for (int e = 0; e < PER; e++) {
+            const int n = n0 + c0 + c, m = row(q, e);
             if (m < p.M && n < p.N) {
                 float v[W];
 #pragma unroll
-                for (int h = 0; h < W; h += 4)
-                    __builtin_memcpy(v + h, o + write_tile_at<COLS>(r, c + h), 16);
+                for (int g = 0; g < W; g += 4)
+                    __builtin_memcpy(v + g, o + write_tile_at<COLS>(r0 + e * (THREADS / (COLS / W)), c + g), 16);
                 if (part)
                     store_n<float, W>(part + ((int64_t)blockIdx.y * p.M + m) * p.N + n, p.N - n, v);
                 else
-                    epilogue<T, W>(p, m, n, v);
+                    epilogue<T, W>(p, m, n, v, bias[h], res[q & 1][e]);
             }
         }
     }
@@ -685,7 +729,10 @@ template <typename T> __global__ __launch_bounds__(JOIN_THREADS) void join_kerne
         for (int i = 0; i < JOIN_W; i++)
             s[i] += v[i];
     }
-    epilogue<T, JOIN_W>(p, m, n, s);
+    Raw<T, JOIN_W> bias, res;
+    fetch_bias(p, n, bias);
+    fetch_residual(p, m, n, res);
+    epilogue<T, JOIN_W>(p, m, n, s, bias, res);
 }
 
 // Steps of `bytes` of k a split, and how many splits that makes.

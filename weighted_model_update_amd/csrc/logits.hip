@@ -284,8 +284,10 @@ template <int THREADS_, int QUEUE_, int CAP_, int U_> struct TopLds {
 // ballot, lane b adds the b-th count, and as the counts fall with b the next
 // digit is how many of them reach k.  (Two bits a step took twice the
 // barriers: 27.5 and 24.4 us for a row of 151936 fp32 in two kernels.)
+// It stops where at most `spare` more than k reach it; the lower bits are 0
+// then, which selects the same keys.
 template <int BITS, typename L>
-__device__ __forceinline__ uint32_t kth_key(L &l, const uint32_t *keys, int n, int k)
+__device__ __forceinline__ uint32_t kth_key(L &l, const uint32_t *keys, int n, int k, int spare)
 {
     constexpr int STEPS = BITS / 4;
     const int lane = threadIdx.x % WAVE;
@@ -293,8 +295,9 @@ __device__ __forceinline__ uint32_t kth_key(L &l, const uint32_t *keys, int n, i
         (&l.count[0][0])[threadIdx.x] = 0;
     __syncthreads();
     uint32_t cut = 0;
+    int have = n; // keys at or above the cut
 #pragma unroll 1
-    for (int step = 0; step < STEPS; step++) {
+    for (int step = 0; step < STEPS && have > k + spare; step++) {
         const int s = BITS - 4 - 4 * step;
         int mine = 0;
 #pragma unroll 1
@@ -313,6 +316,7 @@ __device__ __forceinline__ uint32_t kth_key(L &l, const uint32_t *keys, int n, i
         const int c = l.count[step][lane & 15];
         const uint32_t digit = __popcll(__ballot(lane > 0 && lane < 16 && c >= k));
         cut |= digit << s;
+        have = digit > 0 ? __shfl(c, (int)digit) : have;
     }
     return cut;
 }
@@ -355,7 +359,7 @@ template <typename L> __device__ __forceinline__ int keep_from(L &l, int n, uint
 // their keys nothing is left.
 template <typename T, typename L> __device__ __forceinline__ void prune(L &l, int n, int k)
 {
-    uint32_t cut = kth_key<Key<T>::BITS>(l, l.key, n, k);
+    uint32_t cut = kth_key<Key<T>::BITS>(l, l.key, n, k, 0);
     int m = keep_from(l, n, cut);
     if (m > k + L::THREADS / 4) {
         // many equal to the cut: the first of them by index, found as the
@@ -363,7 +367,7 @@ template <typename T, typename L> __device__ __forceinline__ void prune(L &l, in
         for (int i = threadIdx.x; i < m; i += L::THREADS)
             l.key[i] = l.key[i] > cut ? ~0u : ~(uint32_t)l.idx[i];
         __syncthreads();
-        cut = kth_key<32>(l, l.key, m, k);
+        cut = kth_key<32>(l, l.key, m, k, 0);
         m = keep_from(l, m, cut);
     }
     const int ties = k - l.kept;
@@ -407,10 +411,10 @@ __device__ __forceinline__ int stream_above(const T *x, int i0, int i1, uint32_t
     constexpr int EPC = Chunk<T>::EPC, UNROLL = 4, STEP = L::THREADS * EPC;
     // above a NaN's key there is nothing; a NaN's place in a chunk is told by
     // the sum, or here, where +inf is told apart
-    const bool none = bound == Key<T>::NAN_KEY;
+    const bool none = bound == Key<T>::NAN_KEY, all = bound < Key<T>::of(NEG_INF);
     const float above = none ? __builtin_inff() : Key<T>::value(bound);
     const auto queue = [&](const Chunk<T> &k, bool hit, int i) {
-        if (hit && !none) {
+        if ((hit || all) && !none) {
             const int p = atomicAdd(&l.n, 1);
             if (p < L::QUEUE) {
                 l.chunk[p] = k.v;
@@ -590,7 +594,9 @@ __device__ __forceinline__ void row_top(const T *x, int i0, int i1, int k, float
     const int want = k < i1 - i0 ? k : i1 - i0;
     if (threadIdx.x == 0)
         l.n = 0;
-    if (i1 - i0 <= L::CAP) { // all are candidates
+    // short: all are candidates, also where fewer than k threads have entries
+    const int share = (i1 - i0 + EPC - 1) / EPC;
+    if (i1 - i0 <= 512 || share < k) {
         for (int i = i0 + threadIdx.x * EPC; i < i1; i += STEP) {
             const Chunk<T> e = load_row(x, i, i1);
             bool odd;
@@ -622,7 +628,7 @@ __device__ __forceinline__ void row_top(const T *x, int i0, int i1, int k, float
         for (int j = 0; j < EPC * U; j++)
             nan |= e[j / EPC].get(j % EPC) != e[j / EPC].get(j % EPC);
     l.best[threadIdx.x] = at >= i1 ? 0u : nan ? Key<T>::NAN_KEY : Key<T>::of(first.m); // 0: no entries
-    uint32_t bound = kth_key<Key<T>::BITS>(l, l.best, L::THREADS, k);
+    uint32_t bound = kth_key<Key<T>::BITS>(l, l.best, L::THREADS, k, k / 4);
     __syncthreads();
     int q = stream_above<T, L>(x, i0, i1, bound, c, l, sm);
     int n = q > L::QUEUE ? L::CAP + 1 : take_queued<T, L>(q, i1, bound, l);
@@ -631,7 +637,7 @@ __device__ __forceinline__ void row_top(const T *x, int i0, int i1, int k, float
         __syncthreads();
         if (again == 0) {
             l.best[threadIdx.x] = Key<T>::of(sm.m); // of the numbers: FA_MAX_TOP threads or more have some
-            bound = max(bound, kth_key<Key<T>::BITS>(l, l.best, L::THREADS, k));
+            bound = max(bound, kth_key<Key<T>::BITS>(l, l.best, L::THREADS, k, 0));
         } else {
             bound = kth_of_row<T, L>(x, i0, i1, k, l);
         }
@@ -760,7 +766,7 @@ constexpr int64_t DI_SMALL_BYTES = 16384; // rows up to this take the small work
 
 // LDS of one row's lists, sized by the entries a row can have: per client its
 // numbers, per entry its probability and its slot, and a table with a slot for
-// each distinct index (open addressing, at most half full).
+// each distinct index (open addressing, at most four fifths full).
 struct Lists {
     int *len;     // [clients] entries in use; 0: the client did not send the row
     float *mass;  // [clients] sum_j q_cj
@@ -775,7 +781,7 @@ struct Lists {
     static __host__ __device__ int slots_for(int entries)
     {
         int n = 64;
-        while (n < 2 * entries)
+        while (n < entries + entries / 4)
             n *= 2;
         return n;
     }
@@ -1111,7 +1117,11 @@ template <typename L> int64_t top_longest(int64_t k, size_t es)
 
 void split_top_rows(int64_t R, int64_t V, int64_t k, size_t es, int cus, int &pieces, int64_t &len)
 {
-    split_rows(R, V, es, TopJoin::CAP / std::max<int64_t>(k, 1), V / top_longest<TopLarge>(k, es) + 1, cus, pieces, len);
+    // with few rows the pieces' entries are kept to about two a thread of the
+    // join, which is as long as a piece takes
+    const int64_t least = V / top_longest<TopLarge>(k, es) + 1, kk = std::max<int64_t>(k, 1);
+    const int64_t most = std::min<int64_t>(TopJoin::CAP / kk, std::max({2 * TopJoin::THREADS / kk, least, (int64_t)8}));
+    split_rows(R, V, es, most, least, cus, pieces, len);
 }
 
 template <typename T> hipError_t top_rows_of(const TopRowsArgs &a, int cus, hipStream_t s)

@@ -873,16 +873,18 @@ int64_t tiles(int64_t M, int64_t N, int64_t bm, int64_t bn) { return ((M + bm - 
 // The time of a pipelined tile per k is steady, so tiles are compared by the
 // rounds that they need on all CUs: one 256x256 or 256x128 tile fits a CU at a
 // time, two of 128x128.  Measured on 256 CUs, us for bf16 products of K = 8192:
-// a round of 256x256 226, of 256x128 or 128x256 122, of 128x128 130 with two a
-// CU and 86 with one.  (4096x2048x8192, 128 tiles of 256x256: 173 us; 256 of
+// a round of 256x256 226, of 256x128 121 and of 128x256 127 (the other way
+// round, 125 and 119, where only B is outer), of 128x128 130 with two a CU and
+// 86 with one.  (4096x2048x8192, 128 tiles of 256x256: 173 us; 256 of
 // 128x256: 119; 512 of 128x128: 139.)  fp32 is bound by the matrix cores at
 // any tile (128x128 140 TFLOP/s, 256x128 142, 64x64 133).
-int pipe_for(int64_t M, int64_t N, int cus)
+int pipe_for(int64_t M, int64_t N, int layout, int cus)
 {
     const auto rounds = [&](int64_t t, int64_t fit) { return (t + fit - 1) / fit; };
     const int64_t t128 = tiles(M, N, 128, 128), whole = t128 / (2 * cus), rest = t128 % (2 * cus);
-    const int64_t costs[4] = {226 * rounds(tiles(M, N, 256, 256), cus), 122 * rounds(tiles(M, N, 256, 128), cus),
-                              122 * rounds(tiles(M, N, 128, 256), cus),
+    const bool wide = layout == GEMM_B_OUTER;
+    const int64_t costs[4] = {226 * rounds(tiles(M, N, 256, 256), cus), (wide ? 125 : 121) * rounds(tiles(M, N, 256, 128), cus),
+                              (wide ? 119 : 127) * rounds(tiles(M, N, 128, 256), cus),
                               130 * whole + (rest > cus ? 130 : rest > 0 ? 86 : 0)};
     return (int)(std::min_element(costs, costs + 4) - costs);
 }
@@ -894,7 +896,7 @@ int pipe_for(int64_t M, int64_t N, int cus)
 // pipelined kernel: 2048x2048x4096 64x64 49, 128x128 45.
 constexpr int SMALL_MIN_STEPS = 16, THIN_MIN_STEPS = 4;
 
-Plan plan_of(int64_t M, int64_t N, int64_t K, size_t es, int cus)
+Plan plan_of(int64_t M, int64_t N, int64_t K, size_t es, int layout, int cus)
 {
     const int64_t steps = K * (int64_t)es / STEP_BYTES;
     const auto split = [&](int64_t count, int64_t per_cu, int64_t least) {
@@ -905,7 +907,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, size_t es, int cus)
     if (M <= 16)
         return {TILE_THIN_M, split(tiles(M, N, 16, 128), 4, THIN_MIN_STEPS)};
     if (es == 2 && tiles(M, N, 128, 128) >= cus)
-        return {pipe_for(M, N, cus), 1};
+        return {pipe_for(M, N, layout, cus), 1};
     if (es == 4 && tiles(M, N, 128, 128) >= 2 * cus)
         return {PIPE_128_128, 1};
     // fp32 works longer on a step, so it pays to even out the CUs' shares
@@ -914,7 +916,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, size_t es, int cus)
 
 template <typename T> hipError_t gemm_of(const GemmArgs &a, int layout, float *ws, int cus, hipStream_t s)
 {
-    const Plan p = plan_of(a.M, a.N, a.K, sizeof(T), cus);
+    const Plan p = plan_of(a.M, a.N, a.K, sizeof(T), layout, cus);
     const bool direct = direct_ok(a.a, a.lda, layout & GEMM_A_OUTER ? a.M : a.K, sizeof(T)) &&
                         direct_ok(a.b, a.ldb, layout & GEMM_B_OUTER ? a.N : a.K, sizeof(T));
     if (p.tile <= PIPE_128_128) {
@@ -942,9 +944,9 @@ template <typename T> hipError_t gemm_of(const GemmArgs &a, int layout, float *w
 
 } // namespace
 
-size_t gemm_workspace_bytes(int dt, int64_t M, int64_t N, int64_t K, int, int cus)
+size_t gemm_workspace_bytes(int dt, int64_t M, int64_t N, int64_t K, int layout, int cus)
 {
-    const Plan p = plan_of(M, N, K, dt == FA_BF16 ? 2 : 4, cus);
+    const Plan p = plan_of(M, N, K, dt == FA_BF16 ? 2 : 4, layout, cus);
     return p.splits > 1 ? (size_t)p.splits * M * N * sizeof(float) : 0;
 }
 

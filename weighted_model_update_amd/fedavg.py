@@ -7,6 +7,7 @@ library cannot be loaded, every call raises.
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -769,6 +770,8 @@ def _act(act):
     return code
 
 
+# These checks run before every launch of kernels that may take 5 us
+# themselves, so they make as few calls as they can.
 def _matrix(t, name, rows, cols, dtype):
     """Row pitch of a GPU matrix [rows, cols] of `dtype` with unit column
     stride (0 for an absent one)."""
@@ -776,9 +779,9 @@ def _matrix(t, name, rows, cols, dtype):
         return 0
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {list(t.shape)}")
     ld, inner = t.stride()
     if inner != 1 and cols > 1:
@@ -791,10 +794,21 @@ def _vector(t, name, n, dtype):
         return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with {n} elements")
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, t):
+    """Handle of `stream`, or of the current stream of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
 def _new(shape, dtype, device, stream):
@@ -805,14 +819,25 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _workspace(workspace, nbytes, device, stream):
-    if workspace is None:
-        return _new(nbytes, torch.uint8, device, stream) if nbytes > 0 else None
-    return _contig(_on_gpu(workspace, "workspace"), "workspace")
+# Workspace bytes by the sizes alone (and the device, whose CUs they go by).
+@functools.lru_cache(maxsize=1024)
+def _bytes_of(function, device, *sizes):
+    b = ctypes.c_size_t(0)
+    _check(getattr(load(), function)(*sizes, ctypes.byref(b)))
+    return b.value
 
 
-def _nbytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
+def _workspace(workspace, t, stream, function, *sizes):
+    """(tensor to keep, address, bytes) of the caller's workspace or of one
+    made for the call."""
+    if workspace is not None:
+        _contig(_on_gpu(workspace, "workspace"), "workspace")
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    n = _bytes_of(function, t.device.index, *sizes)
+    if n == 0:
+        return None, None, 0
+    w = _new(n, torch.uint8, t.device, stream)
+    return w, w.data_ptr(), n
 
 
 def linear_workspace_size(M, N, K, dtype=torch.bfloat16, act="none", backward=False):
@@ -842,15 +867,11 @@ def linear_forward(x, w, bias=None, act="none", residual=None, alpha=1.0, out=No
         out = _new((M, N), dt, x.device, stream)
     ldr, ldo = _matrix(residual, "residual", M, N, dt), _matrix(out, "out", M, N, dt)
     ldp = _matrix(preact, "preact", M, N, dt)
-    if workspace is None:
-        b = ctypes.c_size_t(0)
-        _check(lib.linear_workspace_size(code, M, N, K, act, 0, ctypes.byref(b)))
-        workspace = _workspace(None, b.value, x.device, stream)
-    else:
-        workspace = _workspace(workspace, 0, x.device, stream)
-    _check(lib.linear_forward(code, M, N, K, _ptr(x), ldx, _ptr(w), ldw, _ptr(bias), act, float(alpha),
-                              _ptr(residual), ldr, _ptr(out), ldo, _ptr(preact), ldp, _ptr(workspace),
-                              _nbytes(workspace), _stream_handle(stream)))
+    keep, ws, nbytes = _workspace(workspace, x, stream, "linear_workspace_size", code, M, N, K, act, 0)
+    rc = lib.linear_forward(code, M, N, K, x.data_ptr(), ldx, w.data_ptr(), ldw, _at(bias), act, alpha, _at(residual),
+                            ldr, out.data_ptr(), ldo, _at(preact), ldp, ws, nbytes, _raw_stream(stream, x))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -877,15 +898,11 @@ def linear_backward(dy, x, w, act="none", preact=None, alpha=1.0, dx=True, dw=Tr
     ldp = _matrix(preact, "preact", M, N, dt)
     lddx, lddw = _matrix(dx, "dx", M, K, dt), _matrix(dw, "dw", N, K, dt)
     _vector(db, "db", N, dt)
-    if workspace is None:
-        b = ctypes.c_size_t(0)
-        _check(lib.linear_workspace_size(code, M, N, K, act, 1, ctypes.byref(b)))
-        workspace = _workspace(None, b.value, x.device, stream)
-    else:
-        workspace = _workspace(workspace, 0, x.device, stream)
-    _check(lib.linear_backward(code, M, N, K, _ptr(dy), lddy, _ptr(x), ldx, _ptr(w), ldw, act, float(alpha),
-                               _ptr(preact), ldp, _ptr(dx), lddx, _ptr(dw), lddw, _ptr(db), _ptr(workspace),
-                               _nbytes(workspace), _stream_handle(stream)))
+    keep, ws, nbytes = _workspace(workspace, x, stream, "linear_workspace_size", code, M, N, K, act, 1)
+    rc = lib.linear_backward(code, M, N, K, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), ldw, act, alpha,
+                             _at(preact), ldp, _at(dx), lddx, _at(dw), lddw, _at(db), ws, nbytes, _raw_stream(stream, x))
+    if rc:
+        _check(rc)
     return dx, dw, db
 
 
@@ -915,14 +932,12 @@ def logits_topk(x, k, tau=1.0, idx_out=None, val_out=None, lse_out=None, workspa
     _vector(idx_out, "idx_out", R * kk, torch.int32)
     _vector(val_out, "val_out", R * kk, torch.float32)
     _vector(lse_out, "lse_out", R, torch.float32)
-    if workspace is None:
-        b = ctypes.c_size_t(0)
-        _check(lib.logits_topk_workspace_size(_dtype(x), R, V, k, ctypes.byref(b)))
-        workspace = _workspace(None, b.value, x.device, stream)
-    else:
-        workspace = _workspace(workspace, 0, x.device, stream)
-    _check(lib.logits_topk(_ptr(x), _dtype(x), R, V, ld, k, float(tau), _ptr(idx_out), _ptr(val_out),
-                           _ptr(lse_out), _ptr(workspace), _nbytes(workspace), _stream_handle(stream)))
+    code = _dtype(x)
+    keep, ws, nbytes = _workspace(workspace, x, stream, "logits_topk_workspace_size", code, R, V, k)
+    rc = lib.logits_topk(x.data_ptr(), code, R, V, ld, k, tau, idx_out.data_ptr(), val_out.data_ptr(),
+                         lse_out.data_ptr(), ws, nbytes, _raw_stream(stream, x))
+    if rc:
+        _check(rc)
     return idx_out, val_out, lse_out
 
 
@@ -950,14 +965,6 @@ def _distill_lists(idx, val, teacher_lse, n, R):
             _vector(teacher_lse[c], f"teacher_lse[{c}]", R, torch.float32)
         ks[c] = i.shape[1]
     return C, _ptr_array(idx), _ptr_array(val), (None if teacher_lse is None else _ptr_array(teacher_lse)), ks
-
-
-def _distill_workspace(lib, z, workspace, stream):
-    if workspace is not None:
-        return _workspace(workspace, 0, z.device, stream)
-    b = ctypes.c_size_t(0)
-    _check(lib.distill_workspace_size(_dtype(z), z.shape[0], z.shape[1], ctypes.byref(b)))
-    return _workspace(None, b.value, z.device, stream)
 
 
 def _err_flag(err_flag):
@@ -989,10 +996,13 @@ def distill_loss(z, idx, val, n, tau=1.0, teacher_lse=None, row_weight=None, los
     for t, name in ((row_weight, "row_weight"), (loss, "loss"), (lse, "lse")):
         _vector(t, name, R, torch.float32)
     C, pi, pv, pl, ks = _distill_lists(idx, val, teacher_lse, n, R)
-    workspace = _distill_workspace(lib, z, workspace, stream)
-    _check(lib.distill_loss(C, pi, pv, pl, ks, _i64_array(n), _ptr(z), _dtype(z), R, V, ldz, float(tau),
-                            _ptr(row_weight), _ptr(loss), _ptr(lse), _ptr(dz), lddz, _ptr(_err_flag(err_flag)),
-                            _ptr(workspace), _nbytes(workspace), _stream_handle(stream)))
+    code = _dtype(z)
+    keep, ws, nbytes = _workspace(workspace, z, stream, "distill_workspace_size", code, R, V)
+    rc = lib.distill_loss(C, pi, pv, pl, ks, _i64_array(n), z.data_ptr(), code, R, V, ldz, tau, _at(row_weight),
+                          loss.data_ptr(), lse.data_ptr(), _at(dz), lddz, _at(_err_flag(err_flag)), ws, nbytes,
+                          _raw_stream(stream, z))
+    if rc:
+        _check(rc)
     return loss, lse, dz
 
 
@@ -1011,10 +1021,13 @@ def distill_backward(z, lse, idx, val, n, tau=1.0, teacher_lse=None, row_weight=
     for t, name in ((row_weight, "row_weight"), (lse, "lse")):
         _vector(t, name, R, torch.float32)
     C, pi, pv, pl, ks = _distill_lists(idx, val, teacher_lse, n, R)
-    workspace = _distill_workspace(lib, z, workspace, stream)
-    _check(lib.distill_backward(C, pi, pv, pl, ks, _i64_array(n), _ptr(z), _dtype(z), R, V, ldz, float(tau),
-                                _ptr(row_weight), _ptr(lse), _ptr(dz), lddz, _ptr(_err_flag(err_flag)),
-                                _ptr(workspace), _nbytes(workspace), _stream_handle(stream)))
+    code = _dtype(z)
+    keep, ws, nbytes = _workspace(workspace, z, stream, "distill_workspace_size", code, R, V)
+    rc = lib.distill_backward(C, pi, pv, pl, ks, _i64_array(n), z.data_ptr(), code, R, V, ldz, tau, _at(row_weight),
+                              lse.data_ptr(), dz.data_ptr(), lddz, _at(_err_flag(err_flag)), ws, nbytes,
+                              _raw_stream(stream, z))
+    if rc:
+        _check(rc)
     return dz
 
 

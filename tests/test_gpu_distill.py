@@ -237,6 +237,32 @@ def test_empty_sizes():
     assert bool((loss == 0).all()) and bool((dz == 0).all())
 
 
+@pytest.mark.parametrize("dt", list(DTYPES))
+def test_more_rows_than_workgroups_hold_at_once(dt):
+    # rows are not split: the paths that keep a row, with long lists, padding
+    # rows, and dense clusters of listed indices
+    R, V = 300, 9001
+    z = rnd((R, V), 5, 2.0).to(DTYPES[dt]).cuda()
+    g = torch.Generator().manual_seed(8)
+    idx, val = [], []
+    for k in (200, 64, 3):
+        i = torch.rand(R, 1200, generator=g).topk(k, 1).indices.sort(1).values.to(torch.int32)
+        i[::7, k // 2:] = -1
+        idx.append((i + torch.where(i >= 0, 4000, 0)).int().cuda())
+        val.append(torch.randn(R, k, generator=g).cuda())
+    rw = torch.rand(R, generator=g) + 0.5
+    rw[::5] = 0.0
+    check(z, idx, val, [3, 1, 9], tau=1.5, row_weight=rw.cuda(), in_place=True)
+
+
+def test_very_long_row():
+    # chains of chunks cover several chunks
+    R, V = 2, 300007
+    z = rnd((R, V), 5, 2.0).to(torch.bfloat16).cuda()
+    idx, val = lists(R, V, [256] * 4, 9, holes=False)
+    check(z, idx, val, [3, 1, 9, 2], tau=2.0, in_place=True)
+
+
 def test_many_rows():
     R, V = 6000, 70
     z = rnd((R, V), 2).to(torch.bfloat16).cuda()

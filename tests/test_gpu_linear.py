@@ -205,6 +205,27 @@ def test_large_tiles(shape, dt):
     check_backward(dy, x, w, "none", None, 1.0, *fa.linear_backward(dy, x, w, db=True))
 
 
+@pytest.mark.parametrize("dt", list(DTYPES))
+def test_large_products_of_views_off_16_bytes(dt):
+    # sizes that are whole chunks at addresses that are not
+    t = DTYPES[dt]
+    M, N, K = 2056, 2072, 136
+    if dt == "f32":
+        M, N = 3000, 3080
+    x, _ = padded(M, K, K, 1, t, 1)
+    w, _ = padded(N, K, K + 3, 0, t, 2)
+    dy, _ = padded(M, N, N, 3, t, 3)
+    out, obuf = padded(M, N, N + 1, 1, t, 0, fill=-77.0)
+    fa.linear_forward(x, w, out=out)
+    check_forward(x, w, None, "none", None, 1.0, out, None)
+    out.fill_(-77.0)
+    assert bool((obuf == -77.0).all())
+    wide = padded(M, N, N, 1, t, 4)[0]       # as the left operand's partner: dx and dw of that size
+    g, _ = padded(M, K, K, 1, t, 5)
+    dx, dw, _ = fa.linear_backward(g, wide, padded(K, N, N, 1, t, 6)[0])
+    check_backward(g, wide, padded(K, N, N, 1, t, 6)[0], "none", None, 1.0, dx, dw, None)
+
+
 # outputs [P, Q] and sum length r that take each tile, ragged at both edges, in
 # all three products: the forward one, dx and dw
 @pytest.mark.parametrize("P,Q,r", [(2041, 2040, 136), (634, 12792, 72), (12792, 634, 136), (2600, 5400, 200), (2041, 2040, 72),

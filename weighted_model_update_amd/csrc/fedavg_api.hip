@@ -1595,11 +1595,14 @@ struct BackwardPlan {
     size_t total() const { return dz + part + gemm; }
 };
 
+// dz rows start on 16 bytes, so the products can copy them whatever N is.
+int64_t dz_pitch(int64_t N) { return (N + 7) & ~7ll; }
+
 BackwardPlan backward_plan(int dtype, int64_t M, int64_t N, int64_t K, int act)
 {
     BackwardPlan b;
     const int cus = cu_count();
-    b.dz = act == FA_ACT_NONE ? 0 : round256((size_t)M * N * dsize(dtype));
+    b.dz = act == FA_ACT_NONE ? 0 : round256((size_t)M * dz_pitch(N) * dsize(dtype));
     b.part = round256((size_t)fa::act_grad_partials(M, N, cus) * N * sizeof(float));
     b.gemm = std::max(fa::gemm_workspace_bytes(dtype, M, K, N, fa::GEMM_B_OUTER, cus),
                       fa::gemm_workspace_bytes(dtype, N, K, M, fa::GEMM_A_OUTER | fa::GEMM_B_OUTER, cus));
@@ -1712,6 +1715,7 @@ int linear_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void 
         g.pre = preact;
         g.ldp = ldp;
         g.dz = has_act && (dx || dw) ? ws : nullptr;
+        g.lddz = dz_pitch(N);
         g.db = db;
         g.part = reinterpret_cast<float *>(ws + plan.dz);
         g.M = M;
@@ -1722,13 +1726,14 @@ int linear_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void 
             return hip_fail(e, "activation gradient launch");
         if (has_act) {
             dz = ws;
-            lddz = N;
+            lddz = dz_pitch(N);
         }
     }
     char *gws = ws + plan.dz + plan.part;
     fa::GemmArgs a{};
     a.a = dz;
     a.lda = lddz;
+    a.a_padded = has_act;
     a.N = (int)K;
     a.alpha = alpha;
     if (dx) {

@@ -26,11 +26,13 @@ struct GemmArgs {
     void *pre; // [M][N], pitch ldp, nullable: the value before the activation
     int64_t ldp;
     int act;
+    bool a_padded; // A's rows are followed by zeros up to whole chunks
 };
 
 enum { GEMM_A_OUTER = 1, GEMM_B_OUTER = 2 };
 
-// Workspace bytes launch_gemm may use for this product (fp32 partial sums).
+// Workspace bytes launch_gemm may use for this product (fp32 partial sums,
+// aligned copies of operands).
 size_t gemm_workspace_bytes(int dt, int64_t M, int64_t N, int64_t K, int layout, int cus);
 hipError_t launch_gemm(const GemmArgs &a, int dt, int layout, void *ws, int cus, hipStream_t s);
 
@@ -39,7 +41,8 @@ hipError_t launch_gemm(const GemmArgs &a, int dt, int layout, void *ws, int cus,
 struct ActGradArgs {
     const void *dy, *pre;
     int64_t lddy, ldp;
-    void *dz; // [M][N] contiguous
+    void *dz; // [M][N], pitch lddz, a multiple of 8, zeros up to it
+    int64_t lddz;
     void *db;
     float *part;
     int64_t M, N;

@@ -756,6 +756,21 @@ template <typename T> hipError_t run_join(const GemmArgs &a, const float *part, 
     return hipGetLastError();
 }
 
+// An operand copied with its rows on 16 bytes and zeros up to whole chunks.
+constexpr int PACK_THREADS = 256;
+
+template <typename T>
+__global__ __launch_bounds__(PACK_THREADS) void pack_kernel(const T *src, int64_t ld, int64_t rows, int64_t cols, T *dst)
+{
+    constexpr int EPC = traits<T>::EPC;
+    const int64_t per = (cols + EPC - 1) / EPC, at = (int64_t)blockIdx.x * PACK_THREADS + threadIdx.x;
+    if (at >= rows * per)
+        return;
+    const int64_t r = at / per, c = at % per * EPC;
+    const u32x4 v = load_chunk(src + r * ld + c, (int)(cols - c < EPC ? cols - c : EPC));
+    *reinterpret_cast<u32x4 *>(dst + at * EPC) = v;
+}
+
 template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
 hipError_t run_tile(const GemmArgs &a, int layout, int splits, float *ws, hipStream_t s)
 {
@@ -814,7 +829,7 @@ template <typename T> __global__ __launch_bounds__(AG_THREADS) void act_grad_ker
         for (int u = 0; u < AG_U; u++) {
             apply_slope<AG_W>(d[u], z[u], p.act);
             if (p.dz)
-                store_n<T, AG_W>(static_cast<T *>(p.dz) + (m0 + u) * p.N + n, m0 + u < r1 ? valid : 0, d[u]);
+                store_n<T, AG_W>(static_cast<T *>(p.dz) + (m0 + u) * p.lddz + n, m0 + u < r1 ? AG_W : 0, d[u]);
 #pragma unroll
             for (int i = 0; i < AG_W; i++)
                 sum[i] += d[u][i];
@@ -853,11 +868,13 @@ template <typename T> __global__ __launch_bounds__(CJ_WAVES *WAVE) void column_j
 
 namespace {
 
-// Whether an operand's rows start on 16 bytes and end on a whole chunk, and a
-// tile of it stays within the 31 bits of a buffer offset.
-bool direct_ok(const void *p, int64_t ld, int64_t row, size_t es)
+// Whether an operand's rows start on 16 bytes and end on a whole chunk (or in
+// zeros up to one), and a tile of it stays within the 31 bits of a buffer
+// offset.
+bool direct_ok(const void *p, int64_t ld, int64_t row, bool padded, size_t es)
 {
-    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * (int64_t)es % 16 == 0 && row * (int64_t)es % 16 == 0 &&
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * (int64_t)es % 16 == 0 &&
+           (padded || row * (int64_t)es % 16 == 0) &&
            ld * (int64_t)es * 257 < (int64_t)OUT_OF_RANGE;
 }
 
@@ -871,21 +888,22 @@ struct Plan {
 int64_t tiles(int64_t M, int64_t N, int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
 
 // The time of a pipelined tile per k is steady, so tiles are compared by the
-// rounds that they need on all CUs: one 256x256 or 256x128 tile fits a CU at a
-// time, two of 128x128.  Measured on 256 CUs, us for bf16 products of K = 8192:
-// a round of 256x256 226, of 256x128 121 and of 128x256 127 (the other way
-// round, 125 and 119, where only B is outer), of 128x128 130 with two a CU and
-// 86 with one.  (4096x2048x8192, 128 tiles of 256x256: 173 us; 256 of
-// 128x256: 119; 512 of 128x128: 139.)  fp32 is bound by the matrix cores at
+// rounds that they need on all CUs: one 256x256, 256x128 or 128x256 tile fits a
+// CU at a time, two of 128x128.  Measured on 256 CUs, us of a round for bf16
+// and K = 8192, by which operands are outer (none, B, both); the last column is
+// a round of 128x128 with one tile a CU.  For example 8192x5000x4000: 256x256
+// 331 us, 256x128 366, 128x256 351, 128x128 412; 4096x2048x8192: 173, 135, 144,
+// 161; 2048x2048x4096: 87, 63, 57, 45.  fp32 is bound by the matrix cores at
 // any tile (128x128 140 TFLOP/s, 256x128 142, 64x64 133).
 int pipe_for(int64_t M, int64_t N, int layout, int cus)
 {
-    const auto rounds = [&](int64_t t, int64_t fit) { return (t + fit - 1) / fit; };
+    static const int us[3][5] = {{222, 140, 138, 155, 90}, {215, 130, 121, 140, 86}, {215, 123, 125, 130, 86}};
+    const int *c = us[layout == 0 ? 0 : layout == GEMM_B_OUTER ? 1 : 2];
+    const auto rounds = [&](int64_t t) { return (t + cus - 1) / cus; };
     const int64_t t128 = tiles(M, N, 128, 128), whole = t128 / (2 * cus), rest = t128 % (2 * cus);
-    const bool wide = layout == GEMM_B_OUTER;
-    const int64_t costs[4] = {226 * rounds(tiles(M, N, 256, 256), cus), (wide ? 125 : 121) * rounds(tiles(M, N, 256, 128), cus),
-                              (wide ? 119 : 127) * rounds(tiles(M, N, 128, 256), cus),
-                              130 * whole + (rest > cus ? 130 : rest > 0 ? 86 : 0)};
+    const int64_t costs[4] = {c[0] * rounds(tiles(M, N, 256, 256)), c[1] * rounds(tiles(M, N, 256, 128)),
+                              c[2] * rounds(tiles(M, N, 128, 256)),
+                              c[3] * whole + (rest > cus ? c[3] : rest > 0 ? c[4] : 0)};
     return (int)(std::min_element(costs, costs + 4) - costs);
 }
 
@@ -894,7 +912,11 @@ int pipe_for(int64_t M, int64_t N, int layout, int cus)
 // with K = 4096: 512x1024 unsplit 34, in 2 23, in 4 17, in 8 19; 256x1024
 // 22, 16, 13, 15; 1024x2048 with K = 512 unsplit 7.5, in 2 20.  Against the
 // pipelined kernel: 2048x2048x4096 64x64 49, 128x128 45.
-constexpr int SMALL_MIN_STEPS = 16, THIN_MIN_STEPS = 4;
+// Thin ones stream one operand: about three workgroups to two CUs keep the
+// memory busy and more only add sums to join: 8192x16x4096 in 4, 6, 8, 16
+// splits of 64 tiles 16.0, 15.8, 16.0, 17.6 us; 1x14336x4096 of 112 tiles in 2,
+// 4, 8 22.7, 20.7, 21.5; 16x4096x4096 of 32 tiles in 4, 8, 16 13.4, 10.8, 12.2.
+constexpr int SMALL_MIN_STEPS = 16, THIN_MIN_STEPS = 4, THIN_MAX_SPLITS = 16;
 
 Plan plan_of(int64_t M, int64_t N, int64_t K, size_t es, int layout, int cus)
 {
@@ -902,10 +924,14 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, size_t es, int layout, int cus)
     const auto split = [&](int64_t count, int64_t per_cu, int64_t least) {
         return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(per_cu * cus / std::max<int64_t>(count, 1), steps / least), 64));
     };
+    const auto thin = [&](int64_t count) {
+        const int64_t want = (3 * cus / 2 + count - 1) / count;
+        return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, steps / THIN_MIN_STEPS), THIN_MAX_SPLITS));
+    };
     if (N <= 16)
-        return {TILE_THIN_N, split(tiles(M, N, 128, 16), 4, THIN_MIN_STEPS)};
+        return {TILE_THIN_N, thin(std::max<int64_t>(1, tiles(M, N, 128, 16)))};
     if (M <= 16)
-        return {TILE_THIN_M, split(tiles(M, N, 16, 128), 4, THIN_MIN_STEPS)};
+        return {TILE_THIN_M, thin(std::max<int64_t>(1, tiles(M, N, 16, 128)))};
     if (es == 2 && tiles(M, N, 128, 128) >= cus)
         return {pipe_for(M, N, layout, cus), 1};
     if (es == 4 && tiles(M, N, 128, 128) >= 2 * cus)
@@ -914,11 +940,47 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, size_t es, int layout, int cus)
     return {TILE_64, es == 2 ? split(tiles(M, N, 64, 64), 2, SMALL_MIN_STEPS) : split(tiles(M, N, 64, 64), 5, SMALL_MIN_STEPS + 4)};
 }
 
-template <typename T> hipError_t gemm_of(const GemmArgs &a, int layout, float *ws, int cus, hipStream_t s)
+// Bytes of the copy of an operand of `rows` rows of `row` elements, 0 where
+// the rows are whole chunks.
+size_t pack_bytes(int64_t rows, int64_t row, size_t es)
+{
+    const int64_t bytes = (row * (int64_t)es + 15) / 16 * 16;
+    return bytes == row * (int64_t)es ? 0 : ((size_t)(rows * bytes) + 255) / 256 * 256;
+}
+
+template <typename T> hipError_t pack(const void *&p, int64_t &ld, int64_t rows, int64_t row, void *to, hipStream_t s)
+{
+    constexpr int EPC = traits<T>::EPC;
+    const int64_t per = (row + EPC - 1) / EPC, chunks = rows * per;
+    pack_kernel<T><<<(unsigned)((chunks + PACK_THREADS - 1) / PACK_THREADS), PACK_THREADS, 0, s>>>(
+        static_cast<const T *>(p), ld, rows, row, static_cast<T *>(to));
+    p = to;
+    ld = per * EPC;
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t gemm_of(GemmArgs a, int layout, float *ws, int cus, hipStream_t s)
 {
     const Plan p = plan_of(a.M, a.N, a.K, sizeof(T), layout, cus);
-    const bool direct = direct_ok(a.a, a.lda, layout & GEMM_A_OUTER ? a.M : a.K, sizeof(T)) &&
-                        direct_ok(a.b, a.ldb, layout & GEMM_B_OUTER ? a.N : a.K, sizeof(T));
+    const int64_t row_a = layout & GEMM_A_OUTER ? a.M : a.K, row_b = layout & GEMM_B_OUTER ? a.N : a.K;
+    const int64_t rows_a = layout & GEMM_A_OUTER ? a.K : a.M, rows_b = layout & GEMM_B_OUTER ? a.K : a.N;
+    bool ok_a = direct_ok(a.a, a.lda, row_a, a.a_padded, sizeof(T)), ok_b = direct_ok(a.b, a.ldb, row_b, false, sizeof(T));
+    if (p.tile <= PIPE_128_128 && !(ok_a && ok_b)) {
+        // A large product repays the copies that the direct loads need:
+        // 8192x5001x4001 bf16 552 us staged through registers, 461 copied
+        // (dx 581 and 339, dw 907 and 411).  Operands whose rows are whole chunks but start off 16 bytes
+        // have no room in the workspace; they are staged.
+        const size_t need_a = pack_bytes(rows_a, row_a, sizeof(T)), need_b = pack_bytes(rows_b, row_b, sizeof(T));
+        if ((ok_a || need_a) && (ok_b || need_b)) {
+            hipError_t e = ok_a ? hipSuccess : pack<T>(a.a, a.lda, rows_a, row_a, ws, s);
+            if (e == hipSuccess && !ok_b)
+                e = pack<T>(a.b, a.ldb, rows_b, row_b, reinterpret_cast<char *>(ws) + need_a, s);
+            if (e != hipSuccess)
+                return e;
+            ok_a = ok_b = true;
+        }
+    }
+    const bool direct = ok_a && ok_b;
     if (p.tile <= PIPE_128_128) {
         if (!direct)
             return run_tile<T, 128, 128, 2, 2, false>(a, layout, 1, ws, s);
@@ -946,7 +1008,11 @@ template <typename T> hipError_t gemm_of(const GemmArgs &a, int layout, float *w
 
 size_t gemm_workspace_bytes(int dt, int64_t M, int64_t N, int64_t K, int layout, int cus)
 {
-    const Plan p = plan_of(M, N, K, dt == FA_BF16 ? 2 : 4, layout, cus);
+    const size_t es = dt == FA_BF16 ? 2 : 4;
+    const Plan p = plan_of(M, N, K, es, layout, cus);
+    if (p.tile <= PIPE_128_128)
+        return (layout & GEMM_A_OUTER ? pack_bytes(K, M, es) : pack_bytes(M, K, es)) +
+               (layout & GEMM_B_OUTER ? pack_bytes(K, N, es) : pack_bytes(N, K, es));
     return p.splits > 1 ? (size_t)p.splits * M * N * sizeof(float) : 0;
 }
 

@@ -949,22 +949,32 @@ def distill_workspace_size(R, V, dtype=torch.bfloat16):
 
 
 def _distill_lists(idx, val, teacher_lse, n, R):
+    """(clients, idx, val and teacher_lse addresses, k, n) for the library."""
     C = len(n)
     if len(idx) != C or len(val) != C or (teacher_lse is not None and len(teacher_lse) != C):
         raise ValueError("idx, val, teacher_lse and n must have one entry per client")
-    ks = (ctypes.c_int64 * max(C, 1))()
+    pi, pv, ks = [None] * C, [None] * C, [0] * C
+    pl = None if teacher_lse is None else [None] * C
+    i32, f32 = torch.int32, torch.float32
     for c in range(C):
-        if int(n[c]) == 0:
+        if n[c] == 0:
             continue
         i, v = idx[c], val[c]
-        if i.dim() != 2 or i.shape[0] != R or i.shape != v.shape:
+        shape = i.shape
+        if len(shape) != 2 or shape[0] != R or v.shape != shape:
             raise ValueError(f"idx[{c}] and val[{c}] must both be [{R}, k]")
-        _vector(i, f"idx[{c}]", i.numel(), torch.int32)
-        _vector(v, f"val[{c}]", v.numel(), torch.float32)
-        if teacher_lse is not None:
-            _vector(teacher_lse[c], f"teacher_lse[{c}]", R, torch.float32)
-        ks[c] = i.shape[1]
-    return C, _ptr_array(idx), _ptr_array(val), (None if teacher_lse is None else _ptr_array(teacher_lse)), ks
+        if not (i.is_cuda and v.is_cuda):
+            raise ValueError(f"idx[{c}] and val[{c}] must be GPU tensors")
+        if i.dtype is not i32 or v.dtype is not f32:
+            raise TypeError(f"idx[{c}] must be int32 and val[{c}] float32")
+        if not (i.is_contiguous() and v.is_contiguous()):
+            raise ValueError(f"idx[{c}] and val[{c}] must be contiguous")
+        pi[c], pv[c], ks[c] = i.data_ptr(), v.data_ptr(), shape[1]
+        if pl is not None:
+            _vector(teacher_lse[c], f"teacher_lse[{c}]", R, f32)
+            pl[c] = teacher_lse[c].data_ptr()
+    P, I = ctypes.c_void_p * C, ctypes.c_int64 * C
+    return C, P(*pi), P(*pv), None if pl is None else P(*pl), I(*ks), I(*map(int, n))
 
 
 def _err_flag(err_flag):
@@ -995,10 +1005,10 @@ def distill_loss(z, idx, val, n, tau=1.0, teacher_lse=None, row_weight=None, los
     lddz = _matrix(dz, "dz", R, V, z.dtype)
     for t, name in ((row_weight, "row_weight"), (loss, "loss"), (lse, "lse")):
         _vector(t, name, R, torch.float32)
-    C, pi, pv, pl, ks = _distill_lists(idx, val, teacher_lse, n, R)
+    C, pi, pv, pl, ks, ns = _distill_lists(idx, val, teacher_lse, n, R)
     code = _dtype(z)
     keep, ws, nbytes = _workspace(workspace, z, stream, "distill_workspace_size", code, R, V)
-    rc = lib.distill_loss(C, pi, pv, pl, ks, _i64_array(n), z.data_ptr(), code, R, V, ldz, tau, _at(row_weight),
+    rc = lib.distill_loss(C, pi, pv, pl, ks, ns, z.data_ptr(), code, R, V, ldz, tau, _at(row_weight),
                           loss.data_ptr(), lse.data_ptr(), _at(dz), lddz, _at(_err_flag(err_flag)), ws, nbytes,
                           _raw_stream(stream, z))
     if rc:
@@ -1020,10 +1030,10 @@ def distill_backward(z, lse, idx, val, n, tau=1.0, teacher_lse=None, row_weight=
     lddz = _matrix(dz, "dz", R, V, z.dtype)
     for t, name in ((row_weight, "row_weight"), (lse, "lse")):
         _vector(t, name, R, torch.float32)
-    C, pi, pv, pl, ks = _distill_lists(idx, val, teacher_lse, n, R)
+    C, pi, pv, pl, ks, ns = _distill_lists(idx, val, teacher_lse, n, R)
     code = _dtype(z)
     keep, ws, nbytes = _workspace(workspace, z, stream, "distill_workspace_size", code, R, V)
-    rc = lib.distill_backward(C, pi, pv, pl, ks, _i64_array(n), z.data_ptr(), code, R, V, ldz, tau, _at(row_weight),
+    rc = lib.distill_backward(C, pi, pv, pl, ks, ns, z.data_ptr(), code, R, V, ldz, tau, _at(row_weight),
                               lse.data_ptr(), dz.data_ptr(), lddz, _at(_err_flag(err_flag)), ws, nbytes,
                               _raw_stream(stream, z))
     if rc:

@@ -532,7 +532,7 @@ int fedavg_checksum_sum(const void *buf, int64_t count, fa_dtype dtype, uint64_t
  * Sums over the inner dimension, the bias, the activation and the residual are
  * fp32; each result is rounded once to the element type (RNE).  The order of
  * additions is fixed by the sizes, so results are deterministic.
- * Limits: M, N, K <= 2^30; M*N, M*K, N*K <= 2^36 (FA_ERR_RANGE).
+ * Limits: M, N, K <= 2^28; M*N, M*K, N*K <= 2^36 (FA_ERR_RANGE).
  * ------------------------------------------------------------------------ */
 typedef enum { FA_ACT_NONE = 0, FA_ACT_RELU = 1, FA_ACT_GELU = 2, FA_ACT_SILU = 3 } fa_act;
 

@@ -26,7 +26,7 @@ def forward(dtype=1, M=4, N=8, K=16, x=at(1), ldx=16, w=at(2), ldw=16, bias=at(3
 
 @pytest.mark.parametrize("kw,code", [
     (dict(dtype=2), DTYPE), (dict(act=4), ARG), (dict(act=-1), ARG), (dict(M=-1), ARG), (dict(K=-3), ARG),
-    (dict(M=(1 << 30) + 1), RANGE), (dict(M=1 << 20, N=1 << 20, ldo=1 << 20), RANGE),
+    (dict(M=(1 << 30) + 1), RANGE), (dict(N=(1 << 28) + 1, ldo=(1 << 28) + 1, ldr=(1 << 28) + 1, ldp=(1 << 28) + 1), RANGE), (dict(M=1 << 20, N=1 << 20, ldo=1 << 20), RANGE),
     (dict(x=None), ARG), (dict(w=None), ARG), (dict(out=None), ARG),
     (dict(x=at(1, 1)), ARG), (dict(dtype=0, w=at(2, 2)), ARG), (dict(bias=at(3, 1)), ARG),
     (dict(ldx=-1), ARG), (dict(ldo=7), ARG), (dict(ldp=0), ARG), (dict(ldx=1 << 41), RANGE),

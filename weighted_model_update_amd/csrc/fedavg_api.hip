@@ -1512,7 +1512,8 @@ int fedavg_checksum_sum(const void *buf, int64_t count, fa_dtype dtype, uint64_t
 
 namespace {
 
-constexpr int64_t LINEAR_MAX_DIM = 1ll << 30;
+constexpr int64_t LINEAR_MAX_DIM = 1ll << 28;
+constexpr int64_t LOGITS_MAX_V = 1ll << 30;
 constexpr int64_t LINEAR_MAX_ELEMS = 1ll << 36;
 
 // A row-major matrix view: `cols` elements per row, row pitch ld elements.
@@ -1573,7 +1574,7 @@ int check_linear(int dtype, int64_t M, int64_t N, int64_t K, int act)
         return fail(FA_ERR_ARG, "M, N and K must be >= 0");
     if (M > LINEAR_MAX_DIM || N > LINEAR_MAX_DIM || K > LINEAR_MAX_DIM || M * N > LINEAR_MAX_ELEMS ||
         M * K > LINEAR_MAX_ELEMS || N * K > LINEAR_MAX_ELEMS)
-        return fail(FA_ERR_RANGE, "M, N, K must be at most 2^30 and their products 2^36");
+        return fail(FA_ERR_RANGE, "M, N, K must be at most 2^28 and their products 2^36");
     return FA_OK;
 }
 
@@ -1771,7 +1772,7 @@ int check_logits(int dtype, int64_t R, int64_t V, float tau)
         return fail(FA_ERR_DTYPE, "logits must be FA_F32 or FA_BF16");
     if (R < 0 || V < 0)
         return fail(FA_ERR_ARG, "R and V must be >= 0");
-    if (V > LINEAR_MAX_DIM || R > LINEAR_MAX_ELEMS / std::max<int64_t>(V, 1))
+    if (V > LOGITS_MAX_V || R > LINEAR_MAX_ELEMS / std::max<int64_t>(V, 1))
         return fail(FA_ERR_RANGE, "V must be at most 2^30 and R * V 2^36");
     if (!(tau >= 1e-30f) || !(tau <= 1e30f))
         return fail(FA_ERR_ARG, "tau must be between 1e-30 and 1e30");

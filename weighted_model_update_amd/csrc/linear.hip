@@ -24,7 +24,6 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int STEP_BYTES = 128; // k per step, as bytes of one row
 constexpr int WAVE = 64;
-constexpr int WAIT_LOADS = 0x0f70; // s_waitcnt vmcnt(0), the other counters as they are
 
 template <typename T> struct traits;
 template <> struct traits<__bf16> { static constexpr int EPC = 8; };
@@ -420,12 +419,18 @@ template <typename T, int BM, int BN, int WM, int WN, bool AO, bool BO> struct T
     }
 };
 
-// Waits for this wavefront's copies into LDS, then for the other wavefronts;
-// no access to memory moves across.
-__device__ __forceinline__ void copies_done()
+// s_waitcnt with at most n copies outstanding, and the LDS accesses done or as
+// they are.
+constexpr int wait_copies(int n, bool lds) { return 0x0070 | n | (lds ? 0 : 0x0f00); }
+
+// Waits for all but the last COPIES of this wavefront's copies into LDS, with
+// LDS also for its reads, then for the other wavefronts; no access to memory
+// moves across.
+template <int COPIES, bool LDS> __device__ __forceinline__ void copies_done()
 {
+    static_assert(COPIES < 16, "the counter's low bits");
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(WAIT_LOADS);
+    __builtin_amdgcn_s_waitcnt(wait_copies(COPIES, LDS));
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
@@ -557,18 +562,18 @@ __global__ __launch_bounds__(WM *WN *WAVE) void gemm_kernel(GemmArgs p, int tile
         }
         int s = 0;
         for (; s + 1 < steps; s += 2) {
-            copies_done();
+            copies_done<0, true>();
             da.start(l1, kend - k0 - (s + 1) * BK);
             db.start(l1 + AB, kend - k0 - (s + 1) * BK);
             t.step(l0, l0 + AB, wm, wn, lane);
-            copies_done();
+            copies_done<0, true>();
             if (s + 2 < steps) {
                 da.start(l0, kend - k0 - (s + 2) * BK);
                 db.start(l0 + AB, kend - k0 - (s + 2) * BK);
             }
             t.step(l1, l1 + AB, wm, wn, lane);
         }
-        copies_done();
+        copies_done<0, true>();
         if (s < steps)
             t.step(l0, l0 + AB, wm, wn, lane);
         __syncthreads();
@@ -650,10 +655,9 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pipe_kernel(GemmArgs p, int tile
     // replaced as soon as their row of products is issued, so only B's take
     // two sets of registers.
     const auto step = [&](char *next, char *free, int s) {
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x0f70 | COPIES); // step t + 1 is here, t + 2 may be under way
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
+        // step t + 1 is here, t + 2 may be under way.  The reads of `free` were
+        // used up by the last step's products, which no scheduling moves here.
+        copies_done<COPIES, false>();
         __builtin_amdgcn_sched_barrier(0);
         copy(free);
 #pragma unroll
@@ -683,10 +687,7 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pipe_kernel(GemmArgs p, int tile
     copy(l0);
     copy(l1);
     copy(l2);
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0f70 | (2 * COPIES));
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    copies_done<2 * COPIES, false>();
 #pragma unroll
     for (int i = 0; i < FM; i++)
         fa[i] = read_frag<T, AO, BM, PIPE_STEP>(l0, wm + i * 16, 0, lane);
@@ -706,7 +707,7 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pipe_kernel(GemmArgs p, int tile
         step(l2, l0, 1);
     if (t + 2 < steps)
         step(l3, l1, 0);
-    copies_done(); // also those past the end
+    copies_done<0, true>(); // also those past the end
     write_tile<T, BM, BN, WM, WN, AB + BB>(p, m0, n0, acc, l0, l1, nullptr);
 }
 
@@ -763,12 +764,12 @@ template <typename T>
 __global__ __launch_bounds__(PACK_THREADS) void pack_kernel(const T *src, int64_t ld, int64_t rows, int64_t cols, T *dst)
 {
     constexpr int EPC = traits<T>::EPC;
-    const int64_t per = (cols + EPC - 1) / EPC, at = (int64_t)blockIdx.x * PACK_THREADS + threadIdx.x;
-    if (at >= rows * per)
-        return;
-    const int64_t r = at / per, c = at % per * EPC;
-    const u32x4 v = load_chunk(src + r * ld + c, (int)(cols - c < EPC ? cols - c : EPC));
-    *reinterpret_cast<u32x4 *>(dst + at * EPC) = v;
+    const int64_t per = (cols + EPC - 1) / EPC, step = (int64_t)gridDim.x * PACK_THREADS;
+    for (int64_t at = (int64_t)blockIdx.x * PACK_THREADS + threadIdx.x; at < rows * per; at += step) {
+        const int64_t r = at / per, c = at % per * EPC;
+        const u32x4 v = load_chunk(src + r * ld + c, (int)(cols - c < EPC ? cols - c : EPC));
+        *reinterpret_cast<u32x4 *>(dst + at * EPC) = v;
+    }
 }
 
 template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
@@ -952,7 +953,8 @@ template <typename T> hipError_t pack(const void *&p, int64_t &ld, int64_t rows,
 {
     constexpr int EPC = traits<T>::EPC;
     const int64_t per = (row + EPC - 1) / EPC, chunks = rows * per;
-    pack_kernel<T><<<(unsigned)((chunks + PACK_THREADS - 1) / PACK_THREADS), PACK_THREADS, 0, s>>>(
+    const unsigned grid = (unsigned)std::min<int64_t>((chunks + PACK_THREADS - 1) / PACK_THREADS, 1 << 22);
+    pack_kernel<T><<<grid, PACK_THREADS, 0, s>>>(
         static_cast<const T *>(p), ld, rows, row, static_cast<T *>(to));
     p = to;
     ld = per * EPC;

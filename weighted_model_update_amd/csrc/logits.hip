@@ -1116,9 +1116,13 @@ hipError_t run_distill(const DistillArgs &a, int pieces, int64_t len, int stat_p
     const size_t lds = Lists::bytes(a.clients, a.first[a.clients], (int)chunks);
     static_assert((4 * FA_MAX_CLIENTS + (1 + 4) * FA_MAX_LIST_ENTRIES + Lists::MAX_HEADS) * 4 + 3 * FA_MAX_LIST_ENTRIES * 2 <= LISTS_LDS,
                   "the largest lists fit in LDS, with two slots an entry");
-    static const hipError_t allowed = hipFuncSetAttribute(reinterpret_cast<const void *>(&distill_kernel<T, THREADS, LOSS, FROM, KEEP>),
-                                                          hipFuncAttributeMaxDynamicSharedMemorySize, LISTS_LDS);
-    (void)allowed; // a launch that needs more than the default then fails and says so
+    if (lds > 64 << 10) { // more than a kernel gets without asking
+        static const hipError_t allowed =
+            hipFuncSetAttribute(reinterpret_cast<const void *>(&distill_kernel<T, THREADS, LOSS, FROM, KEEP>),
+                                hipFuncAttributeMaxDynamicSharedMemorySize, LISTS_LDS);
+        if (allowed != hipSuccess)
+            return allowed;
+    }
     distill_kernel<T, THREADS, LOSS, FROM, KEEP><<<grid, THREADS, lds, s>>>(a, pieces, len, stat_pieces);
     return hipGetLastError();
 }

@@ -591,7 +591,7 @@ __device__ __forceinline__ uint32_t kth_of_row(const T *x, int i0, int i1, int k
 template <typename T, typename L>
 __device__ __forceinline__ void row_top(const T *x, int i0, int i1, int k, float c, L &l, Softmax &sm)
 {
-    constexpr int EPC = Chunk<T>::EPC, U = L::U, STEP = L::THREADS * EPC;
+    constexpr int EPC = Chunk<T>::EPC, STEP = L::THREADS * EPC;
     const int want = k < i1 - i0 ? k : i1 - i0;
     if (threadIdx.x == 0)
         l.n = 0;
@@ -616,19 +616,25 @@ __device__ __forceinline__ void row_top(const T *x, int i0, int i1, int k, float
         return;
     }
     const int at = i0 + threadIdx.x * EPC;
-    Softmax first;
-    bool odd = false, nan = false;
-    Chunk<T> e[U];
-    float tops[U];
+    // (a loop: the sample's chunks held at once cost registers, 434 us)
+    float top = NEG_INF;
+    bool nan = false;
+#pragma unroll 2
+    for (int u = 0; u < L::U; u++) {
+        const Chunk<T> e = load_row(x, at + u * STEP, i1);
+        float t = max2(e.get(0), e.get(1)), a = e.get(0) + e.get(1);
 #pragma unroll
-    for (int u = 0; u < U; u++)
-        e[u] = load_row(x, at + u * STEP, i1);
-    first.add<T, U>(e, c, odd, tops);
-    if (odd)
+        for (int j = 2; j < EPC; j += 2) {
+            t = max3(t, e.get(j), e.get(j + 1));
+            a += e.get(j) + e.get(j + 1);
+        }
+        if (a != a)
 #pragma unroll
-        for (int j = 0; j < EPC * U; j++)
-            nan |= e[j / EPC].get(j % EPC) != e[j / EPC].get(j % EPC);
-    l.best[threadIdx.x] = at >= i1 ? 0u : nan ? Key<T>::NAN_KEY : Key<T>::of(first.m); // 0: no entries
+            for (int j = 0; j < EPC; j++)
+                nan |= e.get(j) != e.get(j);
+        top = max2(top, t);
+    }
+    l.best[threadIdx.x] = at >= i1 ? 0u : nan ? Key<T>::NAN_KEY : Key<T>::of(top); // 0: no entries
     uint32_t bound = kth_key<Key<T>::BITS>(l, l.best, L::THREADS, k, k / 4);
     __syncthreads();
     int q = stream_above<T, L>(x, i0, i1, bound, c, l, sm);
@@ -1166,11 +1172,12 @@ template <typename T> hipError_t distill_of(const DistillArgs &a, bool loss, int
 // The workgroups of the top logits.  Rows of up to 16 KB take the small one,
 // whose queue holds the whole row.  Four workgroups of the middle shape fit a
 // CU and hide each other's selection: 263 us against 334 us with two of the
-// large one (4096 rows of 128256 bf16, k = 64).  The large shape has room for
+// large one (4096 rows of 128256 bf16, k = 64).  Its sample of 8 chunks a
+// thread against 4: 263 us either way at k = 64, 292 against 337 at k = 128.  The large shape has room for
 // more candidates: a pass finds about k times the row's length over the
 // sample's, and top_longest counts a quarter more.
 using TopSmall = TopLds<256, 1024, 2048, 4>;
-using TopMiddle = TopLds<512, 1536, 2560, 4>;
+using TopMiddle = TopLds<512, 1536, 2560, 8>;
 using TopLarge = TopLds<1024, 3072, 4096, 2>;
 constexpr int64_t TOP_SMALL_BYTES = 16384;
 

@@ -910,23 +910,40 @@ int pipe_for(int64_t M, int64_t N, int layout, int cus)
     return (int)(std::min_element(costs, costs + 4) - costs);
 }
 
-// Small products: 64x64 tiles with k split until about two workgroups a CU
-// run, SMALL_MIN_STEPS steps of 128 bytes each at least.  Measured, us for bf16
-// with K = 4096: 512x1024 unsplit 34, in 2 23, in 4 17, in 8 19; 256x1024
-// 22, 16, 13, 15; 1024x2048 with K = 512 unsplit 7.5, in 2 20.  Against the
-// pipelined kernel: 2048x2048x4096 64x64 49, 128x128 45.
+// Small products: 64x64 tiles with k split.  The number of splits is the one of
+// least estimated time: a step of 128 bytes of k takes a workgroup 0.25 us (bf16)
+// while there are two a CU or fewer, or 0.48 us (fp32, bound by the matrix cores)
+// a round; joining takes 3.5 us and the sums' way to memory and back at 3 TB/s.
+// Measured, us for bf16 with K = 4096: 512x1024 unsplit 34, in 2 23, in 4 17, in
+// 8 19; 256x1024 22, 16, 13, 15; 32x4096 34, 22, 14, 12; 1024x2048 with K = 512
+// unsplit 7.5, in 2 20.  Against the pipelined kernel: 2048x2048x4096 64x64 49,
+// 128x128 45.
+int small_splits(int64_t M, int64_t N, int64_t steps, int64_t count, size_t es, int cus)
+{
+    int best = 1;
+    double least = 0;
+    for (int s = 1; s <= 64 && (s == 1 || (steps >= 2 * s && count * s <= 5 * cus)); s++) {
+        const double wgs = (double)count * s;
+        const double step = es == 2 ? 0.25 * std::max(1.0, wgs / (2 * cus)) : 0.48 * (double)((count * s + cus - 1) / cus);
+        const double join = s == 1 ? 0 : 3.5 + s * (double)M * (double)N * 8 / 3e6;
+        const double t = (double)((steps + s - 1) / s) * step + join;
+        if (s == 1 || t < least) {
+            best = s;
+            least = t;
+        }
+    }
+    return best;
+}
+
 // Thin ones stream one operand: about three workgroups to two CUs keep the
 // memory busy and more only add sums to join: 8192x16x4096 in 4, 6, 8, 16
 // splits of 64 tiles 16.0, 15.8, 16.0, 17.6 us; 1x14336x4096 of 112 tiles in 2,
 // 4, 8 22.7, 20.7, 21.5; 16x4096x4096 of 32 tiles in 4, 8, 16 13.4, 10.8, 12.2.
-constexpr int SMALL_MIN_STEPS = 16, THIN_MIN_STEPS = 4, THIN_MAX_SPLITS = 16;
+constexpr int THIN_MIN_STEPS = 4, THIN_MAX_SPLITS = 16;
 
 Plan plan_of(int64_t M, int64_t N, int64_t K, size_t es, int layout, int cus)
 {
     const int64_t steps = K * (int64_t)es / STEP_BYTES;
-    const auto split = [&](int64_t count, int64_t per_cu, int64_t least) {
-        return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(per_cu * cus / std::max<int64_t>(count, 1), steps / least), 64));
-    };
     const auto thin = [&](int64_t count) {
         const int64_t want = (3 * cus / 2 + count - 1) / count;
         return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, steps / THIN_MIN_STEPS), THIN_MAX_SPLITS));
@@ -939,8 +956,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, size_t es, int layout, int cus)
         return {pipe_for(M, N, layout, cus), 1};
     if (es == 4 && tiles(M, N, 128, 128) >= 2 * cus)
         return {PIPE_128_128, 1};
-    // fp32 works longer on a step, so it pays to even out the CUs' shares
-    return {TILE_64, es == 2 ? split(tiles(M, N, 64, 64), 2, SMALL_MIN_STEPS) : split(tiles(M, N, 64, 64), 5, SMALL_MIN_STEPS + 4)};
+    return {TILE_64, small_splits(M, N, steps, std::max<int64_t>(1, tiles(M, N, 64, 64)), es, cus)};
 }
 
 // Bytes of the copy of an operand of `rows` rows of `row` elements, 0 where

@@ -344,3 +344,33 @@ def test_other_stream_and_graph_replays():
         torch.cuda.synchronize()
         for a, b in zip(outs, step()):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+# odd operands of products long enough for aligned copies beside the partial
+# sums of splits; all three products' sums joined in one launch
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("shape", [(1501, 901, 1603), (301, 5003, 1503), (5001, 301, 1501), (203, 801, 12501)], ids=str)
+def test_odd_products_of_small_tiles(shape, dt, act):
+    M, N, K = shape
+    t = DTYPES[dt]
+    x, w, dy = rnd((M, K), t, 1), rnd((N, K), t, 2, K ** -0.5), rnd((M, N), t, 3)
+    pre = rnd((M, N), t, 4, 1.5) if act != "none" else None
+    check_forward(x, w, None, act, None, 1.0, fa.linear_forward(x, w, act=act), None)
+    got = fa.linear_backward(dy, x, w, act=act, preact=pre, db=True)
+    check_backward(dy, x, w, act, pre, 1.0, *got)
+    again = fa.linear_backward(dy, x, w, act=act, preact=pre, db=True)
+    for a, b in zip(got, again):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_rows_too_long_for_a_tile_of_aligned_copies():
+    # 256 rows of 2^22 + 1 bf16 span more than 2 GiB
+    K = 2 ** 22 + 1
+    x = torch.zeros(1, K, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(1, K, dtype=torch.bfloat16, device="cuda")
+    for i, k in enumerate((0, 70, 2 ** 21 + 7, K - 1)):
+        x[0, k] = 2.0 ** i
+        w[0, k] = 1.0
+    out = fa.linear_forward(x.expand(2048, K), w.expand(2048, K))
+    assert bool((out == 15.0).all())

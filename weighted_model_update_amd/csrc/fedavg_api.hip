@@ -1589,11 +1589,11 @@ int check_workspace(const void *workspace, size_t have, size_t need)
 
 size_t round256(size_t b) { return (b + 255) & ~(size_t)255; }
 
-// linear_backward's workspace: dz, the column sums' partials, and the larger
-// of the two products' partial sums.
+// linear_backward's workspace: dz, the column sums' partials, and the two
+// products' partial sums, which are joined together.
 struct BackwardPlan {
-    size_t dz, part, gemm;
-    size_t total() const { return dz + part + gemm; }
+    size_t dz, part, dx, dw;
+    size_t total() const { return dz + part + dx + dw; }
 };
 
 // dz rows start on 16 bytes, so the products can copy them whatever N is.
@@ -1605,8 +1605,8 @@ BackwardPlan backward_plan(int dtype, int64_t M, int64_t N, int64_t K, int act)
     const int cus = cu_count();
     b.dz = act == FA_ACT_NONE ? 0 : round256((size_t)M * dz_pitch(N) * dsize(dtype));
     b.part = round256((size_t)fa::act_grad_partials(M, N, cus) * N * sizeof(float));
-    b.gemm = std::max(fa::gemm_workspace_bytes(dtype, M, K, N, fa::GEMM_B_OUTER, cus),
-                      fa::gemm_workspace_bytes(dtype, N, K, M, fa::GEMM_A_OUTER | fa::GEMM_B_OUTER, cus));
+    b.dx = round256(fa::gemm_workspace_bytes(dtype, M, K, N, fa::GEMM_B_OUTER, cus));
+    b.dw = fa::gemm_workspace_bytes(dtype, N, K, M, fa::GEMM_A_OUTER | fa::GEMM_B_OUTER, cus);
     return b;
 }
 
@@ -1670,7 +1670,11 @@ int linear_forward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void *
     a.pre = preact;
     a.ldp = ldp;
     a.act = act;
-    const hipError_t e = fa::launch_gemm(a, dtype, 0, workspace, cu_count(), static_cast<hipStream_t>(stream));
+    fa::Finish f{};
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    hipError_t e = fa::launch_gemm(a, dtype, 0, workspace, cu_count(), f, s);
+    if (e == hipSuccess)
+        e = fa::launch_finish(f, dtype, s);
     return e == hipSuccess ? ok() : hip_fail(e, "linear forward launch");
 }
 
@@ -1707,6 +1711,7 @@ int linear_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void 
     hipStream_t s = static_cast<hipStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
     const int cus = cu_count();
+    fa::Finish f{};
     const void *dz = dy;
     int64_t lddz = lddy;
     if (has_act || db) {
@@ -1722,7 +1727,7 @@ int linear_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void 
         g.M = M;
         g.N = N;
         g.act = act;
-        const hipError_t e = fa::launch_act_grad(g, dtype, cus, s);
+        const hipError_t e = fa::launch_act_grad(g, dtype, cus, f, s);
         if (e != hipSuccess)
             return hip_fail(e, "activation gradient launch");
         if (has_act) {
@@ -1744,7 +1749,7 @@ int linear_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void 
         a.K = (int)N;
         a.out = dx;
         a.ldo = lddx;
-        const hipError_t e = fa::launch_gemm(a, dtype, fa::GEMM_B_OUTER, gws, cus, s);
+        const hipError_t e = fa::launch_gemm(a, dtype, fa::GEMM_B_OUTER, gws, cus, f, s);
         if (e != hipSuccess)
             return hip_fail(e, "input gradient launch");
     }
@@ -1755,11 +1760,12 @@ int linear_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void 
         a.K = (int)M;
         a.out = dw;
         a.ldo = lddw;
-        const hipError_t e = fa::launch_gemm(a, dtype, fa::GEMM_A_OUTER | fa::GEMM_B_OUTER, gws, cus, s);
+        const hipError_t e = fa::launch_gemm(a, dtype, fa::GEMM_A_OUTER | fa::GEMM_B_OUTER, gws + plan.dx, cus, f, s);
         if (e != hipSuccess)
             return hip_fail(e, "weight gradient launch");
     }
-    return ok();
+    const hipError_t e = fa::launch_finish(f, dtype, s);
+    return e == hipSuccess ? ok() : hip_fail(e, "join of the gradients launch");
 }
 
 // ============================================================ top logits of rows, distillation

@@ -31,11 +31,6 @@ struct GemmArgs {
 
 enum { GEMM_A_OUTER = 1, GEMM_B_OUTER = 2 };
 
-// Workspace bytes launch_gemm may use for this product (fp32 partial sums,
-// aligned copies of operands).
-size_t gemm_workspace_bytes(int dt, int64_t M, int64_t N, int64_t K, int layout, int cus);
-hipError_t launch_gemm(const GemmArgs &a, int dt, int layout, void *ws, int cus, hipStream_t s);
-
 // dz = dy * act'(preact) (dz null: not stored) and db = column sums of the
 // unrounded dz (db null: not wanted; part: act_grad_partials(M, N) floats).
 struct ActGradArgs {
@@ -49,7 +44,24 @@ struct ActGradArgs {
     int act;
 };
 int64_t act_grad_partials(int64_t M, int64_t N, int cus);
-hipError_t launch_act_grad(const ActGradArgs &a, int dt, int cus, hipStream_t s);
+
+// What a call's launches leave to launch_finish, which joins it all at once;
+// zero-initialised.  The workspaces stay in use until then.
+struct Finish {
+    GemmArgs p[2]; // up to two products whose k was split
+    const float *part[2];
+    int splits[2];
+    ActGradArgs g; // db
+    int64_t parts;
+    int64_t blocks[2], columns; // workgroups of each; 0: nothing to join
+};
+
+// Workspace bytes launch_gemm may use for this product (fp32 partial sums,
+// aligned copies of operands).
+size_t gemm_workspace_bytes(int dt, int64_t M, int64_t N, int64_t K, int layout, int cus);
+hipError_t launch_gemm(const GemmArgs &a, int dt, int layout, void *ws, int cus, Finish &f, hipStream_t s);
+hipError_t launch_act_grad(const ActGradArgs &a, int dt, int cus, Finish &f, hipStream_t s);
+hipError_t launch_finish(const Finish &f, int dt, hipStream_t s);
 
 // ---------------------------------------------------------------- logits
 struct TopRowsArgs {

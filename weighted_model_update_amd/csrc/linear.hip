@@ -723,13 +723,13 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pipe_kernel(GemmArgs p, int tile
     write_tile<T, BM, BN, WM, WN, AB + BB>(p, m0, n0, acc, l0, l1, nullptr);
 }
 
-// Joins the splits' sums in split order, the same bits on every call, and
-// finishes them.  Bound by its launch: 3.8 us for 6 splits of 8192 x 16.
-constexpr int JOIN_THREADS = 256, JOIN_W = 4;
+constexpr int FINISH_THREADS = 256, JOIN_W = 4;
 
-template <typename T> __global__ __launch_bounds__(JOIN_THREADS) void join_kernel(GemmArgs p, const float *part, int splits)
+// Joins four neighbouring sums of a product's splits in split order, the same
+// bits on every call, and finishes them.
+template <typename T> __device__ __forceinline__ void join_splits(const GemmArgs &p, const float *part, int splits, int64_t at)
 {
-    const int64_t groups = (p.N + JOIN_W - 1) / JOIN_W, at = (int64_t)blockIdx.x * JOIN_THREADS + threadIdx.x;
+    const int64_t groups = (p.N + JOIN_W - 1) / JOIN_W;
     if (at >= p.M * groups)
         return;
     const int64_t m = at / groups;
@@ -749,6 +749,45 @@ template <typename T> __global__ __launch_bounds__(JOIN_THREADS) void join_kerne
     epilogue<T, JOIN_W>(p, m, n, s, bias, res);
 }
 
+// CJ_COLS columns of db a workgroup: each of the CJ_GROUPS groups of threads
+// adds every CJ_GROUPS-th partial, and the groups' sums are added in order.
+constexpr int CJ_COLS = 32, CJ_GROUPS = FINISH_THREADS / CJ_COLS;
+
+template <typename T> __device__ __forceinline__ void join_columns(const ActGradArgs &p, int64_t parts, int64_t block)
+{
+    __shared__ float sums[CJ_GROUPS][CJ_COLS];
+    const int col = threadIdx.x % CJ_COLS, group = threadIdx.x / CJ_COLS;
+    const int64_t n = block * CJ_COLS + col;
+    float s = 0.f;
+    if (n < p.N) {
+#pragma unroll 8
+        for (int64_t q = group; q < parts; q += CJ_GROUPS)
+            s += p.part[q * p.N + n];
+    }
+    sums[group][col] = s;
+    __syncthreads();
+    if (group == 0 && n < p.N) {
+#pragma unroll
+        for (int w = 1; w < CJ_GROUPS; w++)
+            s += sums[w][col];
+        static_cast<T *>(p.db)[n] = (T)s;
+    }
+}
+
+// What a call's kernels leave to be joined, in one launch: bound by the launch
+// itself, 4.0 us for 6 splits of 8192 x 16, 4.9 for 256 partials of 8192
+// columns.
+template <typename T> __global__ __launch_bounds__(FINISH_THREADS) void finish_kernel(Finish f)
+{
+    const int64_t block = blockIdx.x;
+    if (block < f.blocks[0])
+        join_splits<T>(f.p[0], f.part[0], f.splits[0], block * FINISH_THREADS + threadIdx.x);
+    else if (block < f.blocks[0] + f.blocks[1])
+        join_splits<T>(f.p[1], f.part[1], f.splits[1], (block - f.blocks[0]) * FINISH_THREADS + threadIdx.x);
+    else
+        join_columns<T>(f.g, f.parts, block - f.blocks[0] - f.blocks[1]);
+}
+
 // Steps of `bytes` of k a split, and how many splits that makes.
 struct Split {
     int kper, splits;
@@ -758,16 +797,6 @@ template <typename T> Split split_of(int K, int splits, int bytes)
 {
     const int bk = bytes / (int)sizeof(T), steps = std::max(1, (K + bk - 1) / bk), per = (steps + splits - 1) / splits;
     return {per * bk, (steps + per - 1) / per};
-}
-
-template <typename T> hipError_t run_join(const GemmArgs &a, const float *part, int splits, hipStream_t s)
-{
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || splits == 1)
-        return e;
-    const int64_t groups = (int64_t)a.M * ((a.N + JOIN_W - 1) / JOIN_W);
-    join_kernel<T><<<(unsigned)((groups + JOIN_THREADS - 1) / JOIN_THREADS), JOIN_THREADS, 0, s>>>(a, part, splits);
-    return hipGetLastError();
 }
 
 // An operand copied with its rows on 16 bytes and zeros up to whole chunks;
@@ -787,7 +816,7 @@ __global__ __launch_bounds__(PACK_THREADS) void pack_kernel(const T *src, int64_
 }
 
 template <typename T, int BM, int BN, int WM, int WN, bool DIRECT>
-hipError_t run_tile(const GemmArgs &a, int layout, int splits, float *ws, hipStream_t s)
+hipError_t run_tile(const GemmArgs &a, int layout, int splits, float *ws, Finish &f, hipStream_t s)
 {
     const int64_t tm = ((int64_t)a.M + BM - 1) / BM, tn = ((int64_t)a.N + BN - 1) / BN;
     const Split k = split_of<T>(a.K, splits, STEP_BYTES);
@@ -799,7 +828,14 @@ hipError_t run_tile(const GemmArgs &a, int layout, int splits, float *ws, hipStr
         gemm_kernel<T, BM, BN, WM, WN, false, true, DIRECT><<<grid, block, 0, s>>>(a, (int)tm, (int)tn, k.kper, part);
     else
         gemm_kernel<T, BM, BN, WM, WN, true, true, DIRECT><<<grid, block, 0, s>>>(a, (int)tm, (int)tn, k.kper, part);
-    return run_join<T>(a, part, k.splits, s);
+    if (k.splits > 1) {
+        const int j = f.blocks[0] > 0;
+        f.p[j] = a;
+        f.part[j] = part;
+        f.splits[j] = k.splits;
+        f.blocks[j] = ((int64_t)a.M * ((a.N + JOIN_W - 1) / JOIN_W) + FINISH_THREADS - 1) / FINISH_THREADS;
+    }
+    return hipGetLastError();
 }
 
 template <typename T, int BM, int BN, int WM, int WN> hipError_t run_pipe(const GemmArgs &a, int layout, hipStream_t s)
@@ -855,44 +891,20 @@ template <typename T> __global__ __launch_bounds__(AG_THREADS) void act_grad_ker
         store_n<float, AG_W>(p.part + (int64_t)blockIdx.y * p.N + n, valid, sum);
 }
 
-// 64 columns a workgroup: each wavefront adds every CJ_WAVES-th partial, and
-// the wavefronts' sums are added in order.  4.8 us for 256 partials of 8192
-// columns.
-constexpr int CJ_WAVES = 8;
-
-template <typename T> __global__ __launch_bounds__(CJ_WAVES *WAVE) void column_join_kernel(ActGradArgs p, int64_t parts)
-{
-    __shared__ float sums[CJ_WAVES][WAVE];
-    const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
-    const int64_t n = (int64_t)blockIdx.x * WAVE + lane;
-    float s = 0.f;
-    if (n < p.N) {
-#pragma unroll 8
-        for (int64_t q = wave; q < parts; q += CJ_WAVES)
-            s += p.part[q * p.N + n];
-    }
-    sums[wave][lane] = s;
-    __syncthreads();
-    if (wave == 0 && n < p.N) {
-#pragma unroll
-        for (int w = 1; w < CJ_WAVES; w++)
-            s += sums[w][lane];
-        static_cast<T *>(p.db)[n] = (T)s;
-    }
-}
-
 } // namespace
 
 namespace {
 
+// Whether a tile of an operand with this row pitch stays within the 31 bits of
+// a buffer offset.
+bool pitch_ok(int64_t bytes) { return bytes * 257 < (int64_t)OUT_OF_RANGE; }
+
 // Whether an operand's rows start on 16 bytes and end on a whole chunk (or in
-// zeros up to one), and a tile of it stays within the 31 bits of a buffer
-// offset.
+// zeros up to one), and its pitch suits the direct loads.
 bool direct_ok(const void *p, int64_t ld, int64_t row, bool padded, size_t es)
 {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * (int64_t)es % 16 == 0 &&
-           (padded || row * (int64_t)es % 16 == 0) &&
-           ld * (int64_t)es * 257 < (int64_t)OUT_OF_RANGE;
+           (padded || row * (int64_t)es % 16 == 0) && pitch_ok(ld * (int64_t)es);
 }
 
 // Tiles: PIPE_* by the pipelined kernel, the others by the two-buffer one.
@@ -900,6 +912,7 @@ enum { PIPE_256_256, PIPE_256_128, PIPE_128_256, PIPE_128_128, TILE_64, TILE_THI
 
 struct Plan {
     int tile, splits;
+    bool large; // enough products to repay aligned copies of odd operands
 };
 
 int64_t tiles(int64_t M, int64_t N, int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
@@ -955,6 +968,12 @@ int small_splits(int64_t M, int64_t N, int64_t steps, int64_t count, size_t es, 
 // 4, 8 22.7, 20.7, 21.5; 16x4096x4096 of 32 tiles in 4, 8, 16 13.4, 10.8, 12.2.
 constexpr int THIN_MIN_STEPS = 4, THIN_MAX_SPLITS = 16;
 
+// M N K from which a product of 64x64 tiles repays the copies of odd operands.
+// Staged and copied, us for y, dx, dw in bf16: 1001x1001x1001 14, 19, 25 and
+// 20, 21, 22; 1125x4239x775 37, 57, 44 and 37, 41, 37; 4716x2938x341 38, 64,
+// 126 and 38, 47, 61; 2047x4095x1023 dx 102 and 54.
+constexpr double PACK_LEAST = 2e9;
+
 Plan plan_of(int64_t M, int64_t N, int64_t K, size_t es, int layout, int cus)
 {
     const int64_t steps = K * (int64_t)es / STEP_BYTES;
@@ -963,22 +982,23 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, size_t es, int layout, int cus)
         return (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, steps / THIN_MIN_STEPS), THIN_MAX_SPLITS));
     };
     if (N <= 16)
-        return {TILE_THIN_N, thin(std::max<int64_t>(1, tiles(M, N, 128, 16)))};
+        return {TILE_THIN_N, thin(std::max<int64_t>(1, tiles(M, N, 128, 16))), false};
     if (M <= 16)
-        return {TILE_THIN_M, thin(std::max<int64_t>(1, tiles(M, N, 16, 128)))};
+        return {TILE_THIN_M, thin(std::max<int64_t>(1, tiles(M, N, 16, 128))), false};
     if (es == 2 && tiles(M, N, 128, 128) >= cus)
-        return {pipe_for(M, N, layout, cus), 1};
+        return {pipe_for(M, N, layout, cus), 1, true};
     if (es == 4 && tiles(M, N, 128, 128) >= 2 * cus)
-        return {PIPE_128_128, 1};
-    return {TILE_64, small_splits(M, N, steps, std::max<int64_t>(1, tiles(M, N, 64, 64)), es, cus)};
+        return {PIPE_128_128, 1, true};
+    return {TILE_64, small_splits(M, N, steps, std::max<int64_t>(1, tiles(M, N, 64, 64)), es, cus),
+            (double)M * (double)N * (double)K >= PACK_LEAST};
 }
 
 // Bytes of the copy of an operand of `rows` rows of `row` elements, 0 where
-// the rows are whole chunks.
+// the rows are whole chunks or the copy's would be too long for direct loads.
 size_t pack_bytes(int64_t rows, int64_t row, size_t es)
 {
     const int64_t bytes = (row * (int64_t)es + 15) / 16 * 16;
-    return bytes == row * (int64_t)es ? 0 : ((size_t)(rows * bytes) + 255) / 256 * 256;
+    return bytes == row * (int64_t)es || !pitch_ok(bytes) ? 0 : ((size_t)(rows * bytes) + 255) / 256 * 256;
 }
 
 template <typename T> hipError_t pack(const void *&p, int64_t &ld, int64_t rows, int64_t row, void *to, hipStream_t s)
@@ -993,13 +1013,19 @@ template <typename T> hipError_t pack(const void *&p, int64_t &ld, int64_t rows,
     return hipGetLastError();
 }
 
-template <typename T> hipError_t gemm_of(GemmArgs a, int layout, float *ws, int cus, hipStream_t s)
+// Bytes of the partial sums, at the front of the workspace.
+size_t part_bytes(const Plan &p, int64_t M, int64_t N)
+{
+    return p.splits > 1 ? ((size_t)p.splits * M * N * sizeof(float) + 255) / 256 * 256 : 0;
+}
+
+template <typename T> hipError_t gemm_of(GemmArgs a, int layout, float *ws, int cus, Finish &f, hipStream_t s)
 {
     const Plan p = plan_of(a.M, a.N, a.K, sizeof(T), layout, cus);
     const int64_t row_a = layout & GEMM_A_OUTER ? a.M : a.K, row_b = layout & GEMM_B_OUTER ? a.N : a.K;
     const int64_t rows_a = layout & GEMM_A_OUTER ? a.K : a.M, rows_b = layout & GEMM_B_OUTER ? a.K : a.N;
     bool ok_a = direct_ok(a.a, a.lda, row_a, a.a_padded, sizeof(T)), ok_b = direct_ok(a.b, a.ldb, row_b, false, sizeof(T));
-    if (p.tile <= PIPE_128_128 && !(ok_a && ok_b)) {
+    if (p.large && !(ok_a && ok_b)) {
         // A large product repays the copies that the direct loads need:
         // 8192x5001x4001 bf16 552 us staged through registers, 461 copied
         // (dx 581 and 336, dw 907 and 420).  Operands whose rows are whole
@@ -1007,9 +1033,10 @@ template <typename T> hipError_t gemm_of(GemmArgs a, int layout, float *ws, int 
         // staged.
         const size_t need_a = pack_bytes(rows_a, row_a, sizeof(T)), need_b = pack_bytes(rows_b, row_b, sizeof(T));
         if ((ok_a || need_a) && (ok_b || need_b)) {
-            hipError_t e = ok_a ? hipSuccess : pack<T>(a.a, a.lda, rows_a, row_a, ws, s);
+            char *to = reinterpret_cast<char *>(ws) + part_bytes(p, a.M, a.N);
+            hipError_t e = ok_a ? hipSuccess : pack<T>(a.a, a.lda, rows_a, row_a, to, s);
             if (e == hipSuccess && !ok_b)
-                e = pack<T>(a.b, a.ldb, rows_b, row_b, reinterpret_cast<char *>(ws) + need_a, s);
+                e = pack<T>(a.b, a.ldb, rows_b, row_b, to + need_a, s);
             if (e != hipSuccess)
                 return e;
             ok_a = ok_b = true;
@@ -1018,7 +1045,7 @@ template <typename T> hipError_t gemm_of(GemmArgs a, int layout, float *ws, int 
     const bool direct = ok_a && ok_b;
     if (p.tile <= PIPE_128_128) {
         if (!direct)
-            return run_tile<T, 128, 128, 2, 2, false>(a, layout, 1, ws, s);
+            return run_tile<T, 128, 128, 2, 2, false>(a, layout, 1, ws, f, s);
         if constexpr (sizeof(T) == 2) {
             if (p.tile == PIPE_256_256)
                 return run_pipe<T, 256, 256, 2, 4>(a, layout, s);
@@ -1030,13 +1057,13 @@ template <typename T> hipError_t gemm_of(GemmArgs a, int layout, float *ws, int 
         return run_pipe<T, 128, 128, 2, 4>(a, layout, s);
     }
     if (p.tile == TILE_64)
-        return direct ? run_tile<T, 64, 64, 2, 2, true>(a, layout, p.splits, ws, s)
-                      : run_tile<T, 64, 64, 2, 2, false>(a, layout, p.splits, ws, s);
+        return direct ? run_tile<T, 64, 64, 2, 2, true>(a, layout, p.splits, ws, f, s)
+                      : run_tile<T, 64, 64, 2, 2, false>(a, layout, p.splits, ws, f, s);
     if (p.tile == TILE_THIN_N)
-        return direct ? run_tile<T, 128, 16, 4, 1, true>(a, layout, p.splits, ws, s)
-                      : run_tile<T, 128, 16, 4, 1, false>(a, layout, p.splits, ws, s);
-    return direct ? run_tile<T, 16, 128, 1, 4, true>(a, layout, p.splits, ws, s)
-                  : run_tile<T, 16, 128, 1, 4, false>(a, layout, p.splits, ws, s);
+        return direct ? run_tile<T, 128, 16, 4, 1, true>(a, layout, p.splits, ws, f, s)
+                      : run_tile<T, 128, 16, 4, 1, false>(a, layout, p.splits, ws, f, s);
+    return direct ? run_tile<T, 16, 128, 1, 4, true>(a, layout, p.splits, ws, f, s)
+                  : run_tile<T, 16, 128, 1, 4, false>(a, layout, p.splits, ws, f, s);
 }
 
 } // namespace
@@ -1045,18 +1072,19 @@ size_t gemm_workspace_bytes(int dt, int64_t M, int64_t N, int64_t K, int layout,
 {
     const size_t es = dt == FA_BF16 ? 2 : 4;
     const Plan p = plan_of(M, N, K, es, layout, cus);
-    if (p.tile <= PIPE_128_128)
-        return (layout & GEMM_A_OUTER ? pack_bytes(K, M, es) : pack_bytes(M, K, es)) +
-               (layout & GEMM_B_OUTER ? pack_bytes(K, N, es) : pack_bytes(N, K, es));
-    return p.splits > 1 ? (size_t)p.splits * M * N * sizeof(float) : 0;
+    size_t bytes = part_bytes(p, M, N);
+    if (p.large)
+        bytes += (layout & GEMM_A_OUTER ? pack_bytes(K, M, es) : pack_bytes(M, K, es)) +
+                 (layout & GEMM_B_OUTER ? pack_bytes(K, N, es) : pack_bytes(N, K, es));
+    return bytes;
 }
 
-hipError_t launch_gemm(const GemmArgs &a, int dt, int layout, void *ws, int cus, hipStream_t s)
+hipError_t launch_gemm(const GemmArgs &a, int dt, int layout, void *ws, int cus, Finish &f, hipStream_t s)
 {
     if (a.M == 0 || a.N == 0)
         return hipSuccess;
     float *part = static_cast<float *>(ws);
-    return dt == FA_BF16 ? gemm_of<__bf16>(a, layout, part, cus, s) : gemm_of<float>(a, layout, part, cus, s);
+    return dt == FA_BF16 ? gemm_of<__bf16>(a, layout, part, cus, f, s) : gemm_of<float>(a, layout, part, cus, f, s);
 }
 
 int64_t act_grad_partials(int64_t M, int64_t N, int cus)
@@ -1067,7 +1095,7 @@ int64_t act_grad_partials(int64_t M, int64_t N, int cus)
     return std::max<int64_t>(1, std::min(std::min<int64_t>(want, 1024), (M + AG_MIN_ROWS - 1) / AG_MIN_ROWS));
 }
 
-hipError_t launch_act_grad(const ActGradArgs &a, int dt, int cus, hipStream_t s)
+hipError_t launch_act_grad(const ActGradArgs &a, int dt, int cus, Finish &f, hipStream_t s)
 {
     if (a.N == 0)
         return hipSuccess;
@@ -1079,14 +1107,23 @@ hipError_t launch_act_grad(const ActGradArgs &a, int dt, int cus, hipStream_t s)
         act_grad_kernel<__bf16><<<grid, AG_THREADS, 0, s>>>(a, rows_per);
     else
         act_grad_kernel<float><<<grid, AG_THREADS, 0, s>>>(a, rows_per);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !a.db)
-        return e;
-    const unsigned g = (unsigned)((a.N + WAVE - 1) / WAVE);
+    if (a.db) {
+        f.g = a;
+        f.parts = parts;
+        f.columns = (a.N + CJ_COLS - 1) / CJ_COLS;
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_finish(const Finish &f, int dt, hipStream_t s)
+{
+    const int64_t blocks = f.blocks[0] + f.blocks[1] + f.columns;
+    if (blocks == 0)
+        return hipSuccess;
     if (dt == FA_BF16)
-        column_join_kernel<__bf16><<<g, CJ_WAVES * WAVE, 0, s>>>(a, parts);
+        finish_kernel<__bf16><<<(unsigned)blocks, FINISH_THREADS, 0, s>>>(f);
     else
-        column_join_kernel<float><<<g, CJ_WAVES * WAVE, 0, s>>>(a, parts);
+        finish_kernel<float><<<(unsigned)blocks, FINISH_THREADS, 0, s>>>(f);
     return hipGetLastError();
 }
 

@@ -852,42 +852,60 @@ template <typename T, int BM, int BN, int WM, int WN> hipError_t run_pipe(const 
 }
 
 // ------------------------------------------------------------ dz and db
-// Eight columns a thread, a workgroup's rows in order: a column's partial sum
-// is added in fp32 in row order, and the partials in a fixed order, so db is
-// the same bits on every call.  Bound by memory: 4096 x 8192 bf16 with GELU
-// (dy and the pre-activation read, dz written: 201 MB) in 45 us, 4.5 TB/s.
+// Eight columns a thread; the threads of a workgroup stand `across` side by side
+// in a row, a power of two up to a wavefront, and in AG_THREADS / across groups
+// below one another, which take the rows in turn, AG_U on their way at a time.
+// A column's partial sum is added in fp32 over a group's rows in order, then
+// over the groups, and the partials in a fixed order, so db is the same bits on
+// every call.  Bound by memory: 4096 x
+// 8192 bf16 with GELU (dy and the pre-activation read, dz written: 201 MB) in
+// 44 us, 4.5 TB/s; small ones by the latency of a thread's own elements, so
+// rows are spread over idle threads: GELU of 1126 x 112 16.2 -> 5.4 us, of
+// 1594 x 2440 21.9 -> 12.2 (against 16 rows a thread, 2048 columns a workgroup).
 constexpr int AG_THREADS = 256, AG_W = 8, AG_U = 4;
-constexpr int AG_COLS = AG_THREADS * AG_W;
-constexpr int AG_MIN_ROWS = 16;
 
-template <typename T> __global__ __launch_bounds__(AG_THREADS) void act_grad_kernel(ActGradArgs p, int64_t rows_per)
+template <typename T> __global__ __launch_bounds__(AG_THREADS) void act_grad_kernel(ActGradArgs p, int64_t rows_per, int across)
 {
-    const int64_t n = ((int64_t)blockIdx.x * AG_THREADS + threadIdx.x) * AG_W;
-    if (n >= p.N)
-        return;
+    __shared__ float sums[AG_THREADS][AG_W + 1];
+    const int col = threadIdx.x & (across - 1), group = threadIdx.x / across, groups = AG_THREADS / across;
+    const int64_t n = ((int64_t)blockIdx.x * across + col) * AG_W;
     const int valid = (int)(p.N - n < AG_W ? p.N - n : AG_W);
     const int64_t r0 = (int64_t)blockIdx.y * rows_per, r1 = r0 + rows_per < p.M ? r0 + rows_per : p.M;
     float sum[AG_W] = {};
-    for (int64_t m0 = r0; m0 < r1; m0 += AG_U) {
+    for (int64_t m0 = r0 + group; m0 < r1 && n < p.N; m0 += groups * AG_U) {
         float d[AG_U][AG_W], z[AG_U][AG_W];
 #pragma unroll
-        for (int u = 0; u < AG_U; u++) { // rows past the end read nothing and add 0
-            const int v = m0 + u < r1 ? valid : 0;
-            load_n<T, AG_W>(static_cast<const T *>(p.dy) + (m0 + u) * p.lddy + n, v, d[u]);
+        for (int u = 0; u < AG_U; u++) { // rows past the end read nothing
+            const int64_t m = m0 + u * groups;
+            const int v = m < r1 ? valid : 0;
+            load_n<T, AG_W>(static_cast<const T *>(p.dy) + m * p.lddy + n, v, d[u]);
             if (p.act != FA_ACT_NONE)
-                load_n<T, AG_W>(static_cast<const T *>(p.pre) + (m0 + u) * p.ldp + n, v, z[u]);
+                load_n<T, AG_W>(static_cast<const T *>(p.pre) + m * p.ldp + n, v, z[u]);
         }
 #pragma unroll
         for (int u = 0; u < AG_U; u++) {
+            const int64_t m = m0 + u * groups;
+            if (m >= r1)
+                break;
             apply_slope<AG_W>(d[u], z[u], p.act);
             if (p.dz)
-                store_n<T, AG_W>(static_cast<T *>(p.dz) + (m0 + u) * p.lddz + n, m0 + u < r1 ? AG_W : 0, d[u]);
+                store_n<T, AG_W>(static_cast<T *>(p.dz) + m * p.lddz + n, AG_W, d[u]);
 #pragma unroll
             for (int i = 0; i < AG_W; i++)
                 sum[i] += d[u][i];
         }
     }
-    if (p.db)
+    if (!p.db)
+        return;
+#pragma unroll
+    for (int i = 0; i < AG_W; i++)
+        sums[threadIdx.x][i] = sum[i];
+    __syncthreads();
+    for (int g = 1; g < groups && group == 0; g++)
+#pragma unroll
+        for (int i = 0; i < AG_W; i++)
+            sum[i] += sums[g * across + col][i];
+    if (group == 0 && n < p.N)
         store_n<float, AG_W>(p.part + (int64_t)blockIdx.y * p.N + n, valid, sum);
 }
 
@@ -938,7 +956,7 @@ int pipe_for(int64_t M, int64_t N, int layout, int cus)
 }
 
 // Small products: 64x64 tiles with k split.  The number of splits is the one of
-// least estimated time: a step of 128 bytes of k takes a workgroup 0.25 us (bf16)
+// least estimated time: a step of 128 bytes of k takes a workgroup 0.5 us (bf16)
 // while there are two a CU or fewer, or 0.48 us (fp32, bound by the matrix cores)
 // a round; joining takes 3.5 us and the sums' way to memory and back at 3 TB/s.
 // Measured, us for bf16 with K = 4096: 512x1024 unsplit 34, in 2 23, in 4 17, in
@@ -951,7 +969,7 @@ int small_splits(int64_t M, int64_t N, int64_t steps, int64_t count, size_t es, 
     double least = 0;
     for (int s = 1; s <= 64 && (s == 1 || (steps >= 2 * s && count * s <= 5 * cus)); s++) {
         const double wgs = (double)count * s;
-        const double step = es == 2 ? 0.25 * std::max(1.0, wgs / (2 * cus)) : 0.48 * (double)((count * s + cus - 1) / cus);
+        const double step = es == 2 ? 0.5 * std::max(1.0, wgs / (2 * cus)) : 0.48 * (double)((count * s + cus - 1) / cus);
         const double join = s == 1 ? 0 : 3.5 + s * (double)M * (double)N * 8 / 3e6;
         const double t = (double)((steps + s - 1) / s) * step + join;
         if (s == 1 || t < least) {
@@ -1087,26 +1105,44 @@ hipError_t launch_gemm(const GemmArgs &a, int dt, int layout, void *ws, int cus,
     return dt == FA_BF16 ? gemm_of<__bf16>(a, layout, part, cus, f, s) : gemm_of<float>(a, layout, part, cus, f, s);
 }
 
+namespace {
+
+// Threads side by side for N columns.
+int act_grad_across(int64_t N)
+{
+    int c = 1;
+    while (c < WAVE && (int64_t)c * AG_W < N)
+        c *= 2;
+    return c;
+}
+
+} // namespace
+
+// Enough workgroups for the chip.  Up to 256 partials a group's rows may be as
+// few as one; beyond, where the partials cost more to join, at least 16.
 int64_t act_grad_partials(int64_t M, int64_t N, int cus)
 {
-    // enough workgroups for the chip, at least AG_MIN_ROWS rows each
-    const int64_t across = (N + AG_COLS - 1) / AG_COLS;
-    const int64_t want = std::max<int64_t>(1, 4 * (int64_t)cus / std::max<int64_t>(across, 1));
-    return std::max<int64_t>(1, std::min(std::min<int64_t>(want, 1024), (M + AG_MIN_ROWS - 1) / AG_MIN_ROWS));
+    const int across = act_grad_across(N), groups = AG_THREADS / across;
+    const int64_t wide = std::max<int64_t>(1, (N + (int64_t)across * AG_W - 1) / ((int64_t)across * AG_W));
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(4 * (int64_t)cus / wide, 1024));
+    const auto of = [&](int64_t rows) { return (M + rows * groups - 1) / (rows * groups); };
+    return std::max<int64_t>(1, std::min(want, std::max(std::min<int64_t>(of(1), 256), of(16))));
 }
 
 hipError_t launch_act_grad(const ActGradArgs &a, int dt, int cus, Finish &f, hipStream_t s)
 {
     if (a.N == 0)
         return hipSuccess;
+    const int across = act_grad_across(a.N);
     const int64_t want = act_grad_partials(a.M, a.N, cus);
     const int64_t rows_per = std::max<int64_t>(1, (a.M + want - 1) / want);
     const int64_t parts = std::max<int64_t>(1, (a.M + rows_per - 1) / rows_per);
-    const dim3 grid((unsigned)((a.N + AG_COLS - 1) / AG_COLS), (unsigned)parts);
+    const int64_t columns = (int64_t)across * AG_W;
+    const dim3 grid((unsigned)((a.N + columns - 1) / columns), (unsigned)parts);
     if (dt == FA_BF16)
-        act_grad_kernel<__bf16><<<grid, AG_THREADS, 0, s>>>(a, rows_per);
+        act_grad_kernel<__bf16><<<grid, AG_THREADS, 0, s>>>(a, rows_per, across);
     else
-        act_grad_kernel<float><<<grid, AG_THREADS, 0, s>>>(a, rows_per);
+        act_grad_kernel<float><<<grid, AG_THREADS, 0, s>>>(a, rows_per, across);
     if (a.db) {
         f.g = a;
         f.parts = parts;

@@ -529,8 +529,8 @@ __device__ __forceinline__ void write_tile(const GemmArgs &p, int m0, int n0, co
 // splits are what fills the card: one row through 14336 x 4096 bf16 weights in
 // 18 us and the join's 4 (117 MB, 4.7 TB/s over the whole call), 8192 x 4096 to
 // 16 columns in 13 and 4; as 128 x 128 tiles, unsplit, they took 72 and 54.  fp32
-// is bound by its matrix rate: 777 x 2048 x 2048 in 70 to 78 us (84 to 93
-// TFLOP/s).
+// is bound by its matrix rate: 777 x 2048 x 2048 with GELU, residual and saved
+// pre-activation in 78 us (84 TFLOP/s).
 template <typename T, int BM, int BN, int WM, int WN, bool AO, bool BO, bool DIRECT>
 __global__ __launch_bounds__(WM *WN *WAVE) void gemm_kernel(GemmArgs p, int tiles_m, int tiles_n, int kper, float *part)
 {
@@ -957,11 +957,12 @@ int pipe_for(int64_t M, int64_t N, int layout, int cus)
 
 // Small products: 64x64 tiles with k split.  The number of splits is the one of
 // least estimated time: a step of 128 bytes of k takes a workgroup 0.5 us (bf16)
-// while there are two a CU or fewer, or 0.48 us (fp32, bound by the matrix cores)
-// a round; joining takes 3.5 us and the sums' way to memory and back at 3 TB/s.
+// while there are two a CU or fewer; in fp32, bound by the matrix cores, 0.75 us
+// while there is one a CU, else 0.55 us a round; joining takes 3.5 us and the sums' way to memory and back at 3 TB/s.
 // Measured, us for bf16 with K = 4096: 512x1024 unsplit 34, in 2 23, in 4 17, in
 // 8 19; 256x1024 22, 16, 13, 15; 32x4096 34, 22, 14, 12; 1024x2048 with K = 512
-// unsplit 7.5, in 2 20.  Against the pipelined kernel: 2048x2048x4096 64x64 49,
+// unsplit 7.5, in 2 20.  fp32: 512x1024x4096 in 1, 2, 3, 5 99, 57, 59, 53;
+// 777x2048x2048 84, 82, 81, 84; 1500x1500x600 39, 44, 44, 47.  Against the pipelined kernel: 2048x2048x4096 64x64 49,
 // 128x128 45.
 int small_splits(int64_t M, int64_t N, int64_t steps, int64_t count, size_t es, int cus)
 {
@@ -969,7 +970,8 @@ int small_splits(int64_t M, int64_t N, int64_t steps, int64_t count, size_t es, 
     double least = 0;
     for (int s = 1; s <= 64 && (s == 1 || (steps >= 2 * s && count * s <= 5 * cus)); s++) {
         const double wgs = (double)count * s;
-        const double step = es == 2 ? 0.5 * std::max(1.0, wgs / (2 * cus)) : 0.48 * (double)((count * s + cus - 1) / cus);
+        const int64_t rounds = (count * s + cus - 1) / cus;
+        const double step = es == 2 ? 0.5 * std::max(1.0, wgs / (2 * cus)) : rounds == 1 ? 0.75 : 0.55 * (double)rounds;
         const double join = s == 1 ? 0 : 3.5 + s * (double)M * (double)N * 8 / 3e6;
         const double t = (double)((steps + s - 1) / s) * step + join;
         if (s == 1 || t < least) {

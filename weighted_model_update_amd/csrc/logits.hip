@@ -118,15 +118,18 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
-// Up to this size x * c - max * c is one fused multiply-add; beyond, where
-// max * c might overflow (the type's lowest values), the difference comes first.
-constexpr float FUSED_UP_TO = 1e30f;
+// Up to this size of max * c the exponent x * c - max * c is one fused
+// multiply-add.  It exposes what the rounding of max * c left off, half a step
+// of 64 .. 128 or 2^-18 at most: 2.6e-6 of an entry, below half a step of the
+// normaliser.  Beyond, the difference comes first: from 2^31 on the fused
+// form's exponent alone would leave the range of fp32 (rows under a mask of
+// -1e10, small temperatures).
+constexpr float FUSED_UP_TO = 128.f;
 
 // A softmax's running maximum (of x, before the temperature) and sum of
 // exp((x - max) / tau), c = log2(e) / tau.  A maximum of -inf is taken off as
-// 0, so that -inf entries add 0; NaN and +inf turn the sum into NaN.  max * c
-// is rounded once, the same for all entries: half a step of the result's
-// max / tau.  v_exp_f32 flushes results below 2^-126, far under the sum's
+// 0, so that -inf entries add 0; NaN and +inf turn the sum into NaN.  Each
+// thread's sum refers to its own running maximum.  v_exp_f32 flushes results below 2^-126, far under the sum's
 // rounding.  What bounds the pass after the memory is the vector unit: about
 // five instructions an entry, the exponential at a quarter of the rate.
 struct Softmax {

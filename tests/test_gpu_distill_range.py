@@ -1,0 +1,90 @@
+"""GPU: loss and gradient of the distillation for rows with large offsets,
+rows under finite masks and extreme temperatures, against float64 relative to
+the row's maximum."""
+
+import pytest
+import torch
+
+import learn_ref as ref
+import softmax_ref as sref
+import weighted_model_update_amd as fa
+from test_gpu_softmax_range import rnd
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def lists_of(R, V, ks, seed, first=0):
+    """Per client [R, k] ascending places, the first `first` of the row and
+    random ones among the others, and values."""
+    g = torch.Generator().manual_seed(seed)
+    idx, val = [], []
+    for k in ks:
+        rest = [first + torch.randperm(V - first, generator=g)[:k - first].sort().values for _ in range(R)]
+        idx.append(torch.stack([torch.cat([torch.arange(first), r]) for r in rest]).int())
+        val.append(torch.randn(R, k, generator=g) * 2)
+    return idx, val
+
+
+def want_of(z, idx, val, n, tau, teacher_lse=None, given_lse=False):
+    zz, t = ref.d(z), sref.f32(tau)
+    rows = [sref.distill_row(zz[r], [(i[r].long(), ref.d(v[r])) for i, v in zip(idx, val)], n, t, 1.0,
+                             None if teacher_lse is None else [ref.d(l)[r] for l in teacher_lse], given_lse)
+            for r in range(z.shape[0])]
+    return [torch.stack([torch.as_tensor(r[j]).double() for r in rows]) for j in range(4)]
+
+
+def cuda(ts):
+    return [t.cuda() for t in ts]
+
+
+def check_dz(z, idx, val, n, tau):
+    _, _, dz, off = want_of(z, idx, val, n, tau)
+    zc, args = z.cuda(), (cuda(idx), cuda(val), n)
+    _, lse, got = fa.distill_loss(zc, *args, tau=tau, dz=True)
+    ref.within(got, dz, off, z.dtype, "dz")
+    off = want_of(z, idx, val, n, tau, given_lse=True)[3]
+    back = fa.distill_backward(zc, lse, *args, tau=tau)
+    ref.within(back, dz, off, z.dtype, "dz of the backward call")
+    place = zc.clone()
+    fa.distill_backward(place, lse, *args, tau=tau, dz=place)
+    assert torch.equal(place.view(torch.uint8), back.view(torch.uint8))
+    place = zc.clone()
+    fa.distill_loss(place, *args, tau=tau, dz=place)
+    assert torch.equal(place.view(torch.uint8), got.view(torch.uint8))
+
+
+def check_loss(z, idx, val, n, tau, teacher_lse=None):
+    loss, off, _, _ = want_of(z, idx, val, n, tau, teacher_lse)
+    got = fa.distill_loss(z.cuda(), cuda(idx), cuda(val), n, tau=tau,
+                          teacher_lse=None if teacher_lse is None else cuda(teacher_lse))[0]
+    ref.within(got, loss, off, torch.float32, "loss")
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("tau", [1e-9, 1e-7, 1e-5, 1e-3])
+def test_lists_own_softmax_at_small_temperatures(tau, dt):
+    """Values of a list in steps of tau upon an offset: their softmax does not
+    depend on the offset."""
+    R, V = 5, 900
+    z = torch.zeros(R, V).to(DTYPES[dt])
+    idx, val = lists_of(R, V, (16, 8), 9)
+    val = [(v / 2 * tau).float() for v in val]
+    at = 2.0 ** 10 * tau
+    shifted = [(v + at).float() for v in val]
+    for vs in (val, shifted):
+        check_loss(z, idx, vs, [3, 5], tau)
+        _, _, dz, off = want_of(z, idx, vs, [3, 5], tau)
+        ref.within(fa.distill_loss(z.cuda(), cuda(idx), cuda(vs), [3, 5], tau=tau, dz=True)[2], dz, off, z.dtype, "dz")
+
+
+def test_lists_under_a_finite_mask():
+    """Lists whose values are all one large number are uniform."""
+    R, V, k = 4, 500, 12
+    z = rnd((R, V), 3)
+    idx, val = lists_of(R, V, (k,), 5)
+    for r, v in enumerate((-1e9, -1e10, 1e20, torch.finfo(torch.float32).min)):
+        val[0][r] = v
+    check_dz(z, idx, val, [1], 1.0)
+    check_loss(z, idx, val, [1], 1.0)

@@ -878,12 +878,12 @@ __device__ __forceinline__ void load_lists(const DistillArgs &p, int64_t r, cons
         const float given = p.has_tlse ? p.tlse[c][r] : 0.f;
         constexpr int PER = FA_MAX_TOP / WAVE;
         int32_t ix[PER];
-        float y[PER];
+        float v[PER];
 #pragma unroll
         for (int e = 0; e < PER; e++) {
             const int j = e * WAVE + lane;
             ix[e] = j < k ? idx[j] : -1;
-            y[e] = j < k ? val[j] * p.inv_tau : NEG_INF;
+            v[e] = j < k ? val[j] : NEG_INF;
         }
         int len = k;
         bool bad = false;
@@ -901,7 +901,7 @@ __device__ __forceinline__ void load_lists(const DistillArgs &p, int64_t r, cons
             last = __shfl(ix[e], WAVE - 1);
             if (e * WAVE + lane < len) {
                 bad |= ix[e] >= p.V || before >= ix[e];
-                m = fmaxf(m, y[e]);
+                m = fmaxf(m, v[e]);
             }
         }
         if (__ballot(bad)) {
@@ -910,22 +910,24 @@ __device__ __forceinline__ void load_lists(const DistillArgs &p, int64_t r, cons
             len = 0;
         }
         m = wave_max(m);
+        // the largest value is taken off before the temperature, so the
+        // exponents carry no rounding of an offset that the list has
         float s = 0.f;
 #pragma unroll
         for (int e = 0; e < PER; e++)
             if (e * WAVE + lane < len)
-                s += y[e] == NEG_INF ? 0.f : expf(y[e] - m);
+                s += v[e] == NEG_INF ? 0.f : expf((v[e] - m) * p.inv_tau);
         s = wave_sum(s);
         if (m == NEG_INF && s == 0.f)
             len = 0; // nothing, or only -inf
-        const float L = p.has_tlse ? given : m + logf(s);
+        const float base = p.has_tlse ? 0.f : m, L = p.has_tlse ? given : logf(s);
         float mass = 0.f, kl = 0.f;
 #pragma unroll
         for (int e = 0; e < PER; e++) {
             const int j = e * WAVE + lane;
             if (j >= len)
                 continue;
-            const float lq = y[e] - L;
+            const float lq = __builtin_fmaf(v[e] - base, p.inv_tau, -L);
             const float q = expf(lq);
             mass += q;
             if (LOSS && q != 0.f)

@@ -642,7 +642,10 @@ int logits_topk(const void *x, fa_dtype dtype, int64_t R, int64_t V, int64_t ldx
  *
  * distill_backward -- the gradient alone, from the lse that distill_loss wrote
  * for the same z, tau and row_weight (times, for a chained loss, the incoming
- * gradient of each row's loss, in row_weight).
+ * gradient of each row's loss, in row_weight).  Where an lse is so large that
+ * its rounding would show in p (|lse| above 88, among them the infinite ones of
+ * rows whose max / tau passes fp32), the row's maximum and sum are taken from z
+ * again.
  */
 int distill_workspace_size(fa_dtype dtype, int64_t R, int64_t V, size_t *bytes);
 int distill_loss(int clients, const int32_t *const *idx, const float *const *val,

@@ -8,7 +8,7 @@ import torch
 import learn_ref as ref
 import softmax_ref as sref
 import weighted_model_update_amd as fa
-from test_gpu_softmax_range import rnd
+from test_gpu_softmax_range import offset_rows, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -53,6 +53,44 @@ def check_dz(z, idx, val, n, tau):
     place = zc.clone()
     fa.distill_loss(place, *args, tau=tau, dz=place)
     assert torch.equal(place.view(torch.uint8), got.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("V", [70, 3001, 40003])
+def test_gradient_of_rows_with_large_offsets(V, dt):
+    z = offset_rows(V, DTYPES[dt])
+    idx, val = lists_of(z.shape[0], V, (20, 7), V)
+    check_dz(z, idx, val, [3, 5], 1.0)
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+def test_gradient_of_more_rows_than_workgroups_hold_at_once(dt):
+    z = offset_rows(9001, DTYPES[dt])
+    z = z.repeat(300 // z.shape[0] + 1, 1)[:300]
+    idx, val = lists_of(300, 9001, (12,), 3)
+    check_dz(z, idx, val, [1], 1.0)
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("tau", [1e-9, 1e-8, 1e-6, 1e-5, 1e-3, 0.05, 1e4])
+def test_gradient_at_extreme_temperatures(tau, dt):
+    for R, V in ((6, 700), (2, 50001)):
+        z = rnd((R, V), 5, 2.5).to(DTYPES[dt])
+        # equal values: the lists' own softmax is then exact at any temperature
+        idx, val = lists_of(R, V, (16, 8), 9)
+        val = [torch.full_like(v, 0.5) for v in val]
+        check_dz(z, idx, val, [3, 5], tau)
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("V", [500, 40003])
+def test_gradient_where_the_normaliser_passes_fp32(V, dt):
+    # the type's lowest and largest value over tau: lse is infinite, p is not
+    low = torch.finfo(DTYPES[dt]).min
+    z = torch.stack([torch.full((V,), low), torch.full((V,), -low), rnd((V,), 4)])
+    z[0, ::2] = -float("inf")
+    idx, val = lists_of(3, V, (9,), 2)
+    val = [v / 4 for v in val]
+    check_dz(z.to(DTYPES[dt]), idx, val, [1], 0.25)
 
 
 def check_loss(z, idx, val, n, tau, teacher_lse=None):

@@ -187,12 +187,16 @@ struct TopPiece {
 constexpr int SPLIT_MAX = WAVE; // pieces of a row
 
 // The pieces' sums joined, one lane a piece, to every lane.
-__device__ __forceinline__ float lse_of_pieces(const TopPiece *t, int pieces, float c, float inv_tau)
+__device__ __forceinline__ Softmax join_lanes(const Softmax &q, float c)
+{
+    const float M = wave_max(q.m);
+    return Softmax{M, wave_sum(q.scaled_to(M, c))};
+}
+
+__device__ __forceinline__ Softmax join_pieces(const TopPiece *t, int pieces, float c)
 {
     const int lane = threadIdx.x % WAVE;
-    const TopPiece q = lane < pieces ? t[lane] : TopPiece{NEG_INF, 0.f};
-    const float M = wave_max(q.m);
-    return lse_of(M, wave_sum(Softmax{q.m, q.s}.scaled_to(M, c)), inv_tau);
+    return join_lanes(lane < pieces ? Softmax{t[lane].m, t[lane].s} : Softmax{}, c);
 }
 
 // The threads' sums joined, to every thread.
@@ -232,6 +236,24 @@ __device__ __forceinline__ Softmax row_softmax(const T *x, int i0, int i1, float
     join_block<THREADS>(t, c, lds);
     return t;
 }
+
+// The same of a whole row read piece by piece, with the bits that the pieces'
+// sums joined from the workspace have.
+template <typename T, int THREADS>
+__device__ __forceinline__ Softmax row_by_pieces(const T *x, int V, int len, int pieces, float c, float *lds)
+{
+    Softmax mine;
+    for (int q = 0; q < pieces; q++) {
+        const Softmax t = row_softmax<T, THREADS>(x, q * len, V - q * len < len ? V : (q + 1) * len, c, lds);
+        if ((int)threadIdx.x % WAVE == q)
+            mine = t;
+    }
+    return join_lanes(mine, c);
+}
+
+// Whether a stored normaliser is so large that its own rounding would show in
+// exp(z / tau - lse): then the row's maximum and sum are taken again.
+__device__ __forceinline__ bool lse_too_coarse(float lse) { return !(fabsf(lse) * LOG2E <= FUSED_UP_TO); }
 
 // ------------------------------------------------------------ top logits
 // Unsigned keys in the order of the values: NaN of either sign highest, then
@@ -743,9 +765,9 @@ template <typename T> __global__ __launch_bounds__(TopJoin::THREADS) void top_jo
         }
         const TopPiece *t = static_cast<const TopPiece *>(p.ws) + r * pieces;
         if (threadIdx.x < WAVE && p.lse) {
-            const float lse = lse_of_pieces(t, pieces, c, p.inv_tau);
+            const Softmax row = join_pieces(t, pieces, c);
             if (threadIdx.x == 0)
-                p.lse[r] = lse;
+                p.lse[r] = lse_of(row.m, row.s, p.inv_tau);
         }
         __syncthreads();
         prune<T, TopJoin>(l, l.n, p.k);
@@ -992,13 +1014,6 @@ template <typename T> __device__ __forceinline__ void store_row(T *x, int i, int
 // Where a row's normaliser comes from.
 enum { LSE_COMPUTE = 0, LSE_PIECES = 1, LSE_GIVEN = 2 };
 
-// exp(z inv_tau - lse): one rounding of the scaled logit and one of the
-// difference; v_exp_f32 flushes below 2^-126.
-__device__ __forceinline__ float prob(float z, float inv_tau, float lse)
-{
-    return __builtin_amdgcn_exp2f((z * inv_tau - lse) * LOG2E);
-}
-
 // A workgroup per row, or per piece of a row's gradient.  LOSS: writes loss
 // and lse (piece 0 does).  KEEP: chunks of the row that each thread keeps in
 // registers from the softmax's pass for the gradient's.  Bound by memory: loss
@@ -1025,6 +1040,8 @@ __global__ __launch_bounds__(THREADS, KEEP ? 4 : 1) void distill_kernel(DistillA
         T *dz = p.dz ? static_cast<T *>(p.dz) + r * p.lddz : nullptr;
         const float g = p.row_weight ? p.row_weight[r] : 1.f;
         float lse = 0.f, M = 0.f, kl = 0.f;
+        Softmax t;         // the row's, unless its stored normaliser serves
+        bool stored = false;
         bool sent = false;
         Chunk<T> keep[KEEP > 0 ? KEEP : 1];
         if (g != 0.f) {
@@ -1033,7 +1050,6 @@ __global__ __launch_bounds__(THREADS, KEEP ? 4 : 1) void distill_kernel(DistillA
                 keep[u] = load_row(z, threadIdx.x * EPC + u * STEP, (int)p.V);
             load_lists<T, THREADS, LOSS>(p, r, z, i0, i1, dz != nullptr, l);
             if (FROM == LSE_COMPUTE) {
-                Softmax t;
 #pragma unroll
                 for (int u = 0; u < KEEP; u += 2) {
                     bool special;
@@ -1041,13 +1057,19 @@ __global__ __launch_bounds__(THREADS, KEEP ? 4 : 1) void distill_kernel(DistillA
                     t.add<T, 2>(keep + u, c2, special, tops);
                 }
                 t = row_softmax<T, THREADS>(z, KEEP * STEP, (int)p.V, c2, fl, t);
-                lse = lse_of(t.m, t.s, p.inv_tau);
             } else if (FROM == LSE_PIECES) {
-                lse = lse_of_pieces(static_cast<const TopPiece *>(p.ws) + r * stat_pieces, stat_pieces, c2, p.inv_tau);
+                t = join_pieces(static_cast<const TopPiece *>(p.ws) + r * stat_pieces, stat_pieces, c2);
             } else {
                 lse = p.lse[r];
+                stored = !lse_too_coarse(lse);
+                if (!stored && stat_pieces > 0)
+                    t = join_pieces(static_cast<const TopPiece *>(p.ws) + r * stat_pieces, stat_pieces, c2);
+                else if (!stored)
+                    t = row_by_pieces<T, THREADS>(z, (int)p.V, (int)len, grad_pieces, c2, fl);
             }
-            if (lse != NEG_INF)
+            if (FROM != LSE_GIVEN)
+                lse = lse_of(t.m, t.s, p.inv_tau);
+            if (stored || t.m != NEG_INF || t.s != 0.f) // anything but -inf in the row
                 for (int c = 0; c < p.clients; c++)
                     if (l.len[c]) {
                         M = __builtin_fmaf(l.share[c], l.mass[c], M);
@@ -1071,18 +1093,24 @@ __global__ __launch_bounds__(THREADS, KEEP ? 4 : 1) void distill_kernel(DistillA
             // row twice more: 93 us where this takes 77, 1000 rows of
             // 32003 fp32, 16 clients of 100.)
             const float gt = g * p.tau, gm = gt * M;
-            const float off = -lse * LOG2E;
-            const bool fused = fabsf(off) <= FUSED_UP_TO;
+            // m p_i = scale * 2^(z c2 - base).  From the row's maximum and sum
+            // rather than the normaliser, whose rounding relative to max / tau
+            // would be a factor of every p.  The fused form's base is rounded,
+            // and what that left off goes into the scale.
+            const float top = stored ? lse : t.m, unit = stored ? LOG2E : c2, base = top * unit;
+            const bool fused = fabsf(base) <= FUSED_UP_TO;
+            const float rest = fused ? __builtin_amdgcn_exp2f(__builtin_fmaf(-top, unit, base)) : 1.f;
+            const float scale = (stored ? gm : gm / t.s) * rest;
             const auto grad = [&](const Chunk<T> &k, int i) {
                 float v[EPC];
                 if (fused) {
 #pragma unroll
                     for (int j = 0; j < EPC; j++)
-                        v[j] = gm * __builtin_amdgcn_exp2f(__builtin_fmaf(k.get(j), c2, off));
+                        v[j] = scale * __builtin_amdgcn_exp2f(__builtin_fmaf(k.get(j), c2, -base));
                 } else {
 #pragma unroll
                     for (int j = 0; j < EPC; j++)
-                        v[j] = gm * prob(k.get(j), p.inv_tau, lse);
+                        v[j] = scale * __builtin_amdgcn_exp2f((k.get(j) - top) * c2);
                 }
                 for (int h = l.head[(uint32_t)(i - i0) / EPC >> l.shift]; h;) {
                     const int at = l.index[h - 1] - i;
@@ -1108,16 +1136,17 @@ __global__ __launch_bounds__(THREADS, KEEP ? 4 : 1) void distill_kernel(DistillA
     }
 }
 
-// Softmax sums of the pieces of each row (rows of weight 0 are not read).
+// Softmax sums of the pieces of each row.  Rows of weight 0 are not read, nor,
+// in the gradient alone (`stored`: its normalisers), those that need no sums.
 // 4 us for 3 rows of 128256 bf16 in 15 pieces each.
 template <typename T, int THREADS>
-__global__ __launch_bounds__(THREADS) void row_stats_kernel(DistillArgs p, int pieces, int64_t len)
+__global__ __launch_bounds__(THREADS) void row_stats_kernel(DistillArgs p, int pieces, int64_t len, const float *stored)
 {
     __shared__ float fl[THREADS / WAVE];
     for (int64_t w = blockIdx.x; w < p.R * pieces; w += gridDim.x) {
         const int64_t r = w / pieces;
         const int i0 = (int)((w % pieces) * len), i1 = (int)(i0 + len < p.V ? i0 + len : p.V);
-        if (p.row_weight && p.row_weight[r] == 0.f)
+        if ((p.row_weight && p.row_weight[r] == 0.f) || (stored && !lse_too_coarse(stored[r])))
             continue;
         const T *z = static_cast<const T *>(p.z) + r * p.ldz;
         const Softmax t = row_softmax<T, THREADS>(z, i0, i1, p.inv_tau * LOG2E, fl);
@@ -1153,10 +1182,19 @@ template <typename T> hipError_t distill_of(const DistillArgs &a, bool loss, int
     int64_t len;
     split_rows(a.R, a.V, sizeof(T), SPLIT_MAX, 1, cus, pieces, len);
     const bool small = a.V * (int64_t)sizeof(T) <= DI_SMALL_BYTES;
+    const auto stats = [&](const float *stored) {
+        row_stats_kernel<T, DI_LARGE><<<(unsigned)(a.R * pieces), DI_LARGE, 0, s>>>(a, pieces, len, stored);
+        return hipGetLastError();
+    };
     if (!loss) {
         if (small)
             return run_distill<T, DI_SMALL, false, LSE_GIVEN>(a, pieces, len, 0, cus, s);
-        return run_distill<T, DI_LARGE, false, LSE_GIVEN>(a, pieces, len, 0, cus, s);
+        if (pieces == 1 || a.dz != a.z)
+            return run_distill<T, DI_LARGE, false, LSE_GIVEN>(a, pieces, len, 0, cus, s);
+        // in place: what a piece may need of the whole row is read before
+        // others overwrite it
+        const hipError_t e = stats(a.lse);
+        return e != hipSuccess ? e : run_distill<T, DI_LARGE, false, LSE_GIVEN>(a, pieces, len, pieces, cus, s);
     }
     if (pieces == 1) {
         if (!a.dz)
@@ -1165,8 +1203,7 @@ template <typename T> hipError_t distill_of(const DistillArgs &a, bool loss, int
         return small ? run_distill<T, DI_SMALL, true, LSE_COMPUTE, DI_KEEP_SMALL>(a, 1, len, 0, cus, s)
                      : run_distill<T, DI_LARGE, true, LSE_COMPUTE, DI_KEEP_LARGE>(a, 1, len, 0, cus, s);
     }
-    row_stats_kernel<T, DI_LARGE><<<(unsigned)(a.R * pieces), DI_LARGE, 0, s>>>(a, pieces, len);
-    hipError_t e = hipGetLastError();
+    hipError_t e = stats(nullptr);
     if (e != hipSuccess)
         return e;
     if (!a.dz)

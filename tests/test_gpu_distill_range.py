@@ -101,6 +101,26 @@ def check_loss(z, idx, val, n, tau, teacher_lse=None):
 
 
 @pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("V", [70, 3001, 40003])
+def test_loss_of_rows_with_large_offsets(V, dt):
+    z = offset_rows(V, DTYPES[dt])
+    z = z[[r for r in range(z.shape[0]) if r != 22]]    # its loss, nearly all of fp32's range, may round to infinity
+    # places among the ordinary logits of rows whose end is masked, and others
+    idx, val = lists_of(z.shape[0], V, (20, 7), V, first=5)
+    check_loss(z, idx, val, [3, 5], 1.0)
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("tau", [1e-6, 1e-4, 1e-2, 100.0])
+def test_loss_at_extreme_temperatures(tau, dt):
+    for R, V in ((6, 700), (2, 50001)):
+        z = rnd((R, V), 5, 2.5).to(DTYPES[dt])
+        idx, val = lists_of(R, V, (16, 8), 9)
+        val = [torch.full_like(v, 0.5) for v in val]
+        check_loss(z, idx, val, [3, 5], tau)
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
 @pytest.mark.parametrize("tau", [1e-9, 1e-7, 1e-5, 1e-3])
 def test_lists_own_softmax_at_small_temperatures(tau, dt):
     """Values of a list in steps of tau upon an offset: their softmax does not

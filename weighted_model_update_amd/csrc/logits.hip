@@ -808,9 +808,10 @@ constexpr int64_t DI_SMALL_BYTES = 16384; // rows up to this take the small work
 struct Lists {
     int *len;     // [clients] entries in use; 0: the client did not send the row
     float *mass;  // [clients] sum_j q_cj
-    float *kl;    // [clients] sum_j q_cj (log q_cj - z_j / tau)
+    float *kl;    // [clients] sum_j q_cj log q_cj, then less sum_j q_cj (z_j - max z) / tau
     float *share; // [clients] n_c over the sum of n of the clients that sent the row
     float *q;     // [entries]
+    float *z;     // [entries] the listed logits, for the loss
     short *slot;  // [entries] -1: outside the piece
     int *index;   // [slots] -1: free
     float *sum;   // [slots]
@@ -834,12 +835,12 @@ struct Lists {
             s++;
         return s;
     }
-    static __host__ size_t bytes(int clients, int entries, int chunks)
+    static __host__ size_t bytes(int clients, int entries, int chunks, bool loss)
     {
-        const size_t heads = (size_t)((chunks - 1) >> shift_for(chunks)) + 1;
-        return (4 * (size_t)clients + entries + 2 * (size_t)slots_for(entries) + heads) * 4 + ((size_t)slots_for(entries) + entries) * 2;
+        const size_t heads = (size_t)((chunks - 1) >> shift_for(chunks)) + 1, slots = slots_for(entries);
+        return (4 * (size_t)clients + (loss ? 2 : 1) * (size_t)entries + 2 * slots + heads) * 4 + (slots + entries) * 2;
     }
-    __device__ __forceinline__ void place(char *at, int clients, int entries, int chunks)
+    __device__ __forceinline__ void place(char *at, int clients, int entries, int chunks, bool loss)
     {
         slots = slots_for(entries);
         shift = shift_for(chunks);
@@ -848,7 +849,8 @@ struct Lists {
         sum = reinterpret_cast<float *>(index + slots);
         head = reinterpret_cast<int *>(sum + slots);
         q = reinterpret_cast<float *>(head + heads);
-        len = reinterpret_cast<int *>(q + entries);
+        z = q + entries;
+        len = reinterpret_cast<int *>(loss ? z + entries : z);
         mass = reinterpret_cast<float *>(len + clients);
         kl = mass + clients;
         share = kl + clients;
@@ -876,7 +878,7 @@ struct Lists {
 };
 
 // The row's lists: q_cj = exp(v/tau - L_c) and what is summed over them; with
-// GRAD also each index in [i0, i1) once, with sum_c w_c q_c added up in client
+// LOSS the listed logits, with `grad` also each index in [i0, i1) once, with sum_c w_c q_c added up in client
 // order.  One wavefront a client.  A list is used up to its first negative
 // index; one that is not strictly increasing or passes V is left out whole and
 // raises the flag.
@@ -952,12 +954,14 @@ __device__ __forceinline__ void load_lists(const DistillArgs &p, int64_t r, cons
             const float lq = __builtin_fmaf(v[e] - base, p.inv_tau, -L);
             const float q = expf(lq);
             mass += q;
-            if (LOSS && q != 0.f)
-                kl += q * (lq - (float)z[ix[e]] * p.inv_tau);
-            if (grad) {
-                l.q[at + j] = q;
-                l.slot[at + j] = (short)(ix[e] >= i0 && ix[e] < i1 ? l.insert(ix[e], (ix[e] - i0) / Chunk<T>::EPC) : -1);
+            if (LOSS) {
+                kl += q != 0.f ? q * lq : 0.f;
+                l.z[at + j] = (float)z[ix[e]];
             }
+            if (LOSS || grad)
+                l.q[at + j] = q;
+            if (grad)
+                l.slot[at + j] = (short)(ix[e] >= i0 && ix[e] < i1 ? l.insert(ix[e], (ix[e] - i0) / Chunk<T>::EPC) : -1);
         }
         mass = wave_sum(mass);
         kl = wave_sum(kl);
@@ -985,6 +989,23 @@ __device__ __forceinline__ void load_lists(const DistillArgs &p, int64_t r, cons
                     l.sum[s] = __builtin_fmaf(w, l.q[p.first[c] + j], l.sum[s]);
             }
         }
+    __syncthreads();
+}
+
+// l.kl, less sum_j q_cj (z_j - top) / tau with the row's maximum `top`: taken off
+// first, so that a sum of log q - log p holds whatever the row's offset is.  Each
+// lane has the entries that it stored.
+template <int THREADS> __device__ __forceinline__ void finish_kl(const DistillArgs &p, float top, Lists &l)
+{
+    const int lane = threadIdx.x % WAVE;
+    for (int c = threadIdx.x / WAVE; c < p.clients; c += THREADS / WAVE) {
+        float s = 0.f;
+        for (int j = p.first[c] + lane; j < p.first[c] + l.len[c]; j += WAVE)
+            s += l.q[j] != 0.f ? l.q[j] * ((l.z[j] - top) * p.inv_tau) : 0.f;
+        s = wave_sum(s);
+        if (lane == 0)
+            l.kl[c] -= s;
+    }
     __syncthreads();
 }
 
@@ -1030,7 +1051,7 @@ __global__ __launch_bounds__(THREADS, KEEP ? 4 : 1) void distill_kernel(DistillA
     extern __shared__ __attribute__((aligned(16))) char dynamic[];
     __shared__ float fl[THREADS / WAVE];
     Lists l;
-    l.place(dynamic, p.clients, p.first[p.clients], p.dz ? (int)((len + EPC - 1) / EPC) : 1);
+    l.place(dynamic, p.clients, p.first[p.clients], p.dz ? (int)((len + EPC - 1) / EPC) : 1, LOSS);
     const float c2 = p.inv_tau * LOG2E;
     for (int64_t w = blockIdx.x; w < p.R * grad_pieces; w += gridDim.x) {
         const int64_t r = w / grad_pieces;
@@ -1069,11 +1090,15 @@ __global__ __launch_bounds__(THREADS, KEEP ? 4 : 1) void distill_kernel(DistillA
             }
             if (FROM != LSE_GIVEN)
                 lse = lse_of(t.m, t.s, p.inv_tau);
+            if (LOSS)
+                finish_kl<THREADS>(p, t.m, l);
+            const float log_s = LOSS ? logf(t.s) : 0.f;
             if (stored || t.m != NEG_INF || t.s != 0.f) // anything but -inf in the row
                 for (int c = 0; c < p.clients; c++)
                     if (l.len[c]) {
                         M = __builtin_fmaf(l.share[c], l.mass[c], M);
-                        kl = __builtin_fmaf(l.share[c], __builtin_fmaf(lse, l.mass[c], l.kl[c]), kl);
+                        if (LOSS)
+                            kl = __builtin_fmaf(l.share[c], __builtin_fmaf(log_s, l.mass[c], l.kl[c]), kl);
                         sent = true;
                     }
         }
@@ -1162,8 +1187,8 @@ hipError_t run_distill(const DistillArgs &a, int pieces, int64_t len, int stat_p
     const unsigned grid = (unsigned)std::min<int64_t>(a.R * pieces, (int64_t)cus * 16);
     // without a gradient there is no table
     const int64_t chunks = a.dz ? (len + Chunk<T>::EPC - 1) / Chunk<T>::EPC : 1;
-    const size_t lds = Lists::bytes(a.clients, a.first[a.clients], (int)chunks);
-    static_assert((4 * FA_MAX_CLIENTS + (1 + 4) * FA_MAX_LIST_ENTRIES + Lists::MAX_HEADS) * 4 + 3 * FA_MAX_LIST_ENTRIES * 2 <= LISTS_LDS,
+    const size_t lds = Lists::bytes(a.clients, a.first[a.clients], (int)chunks, LOSS);
+    static_assert((4 * FA_MAX_CLIENTS + (2 + 4) * FA_MAX_LIST_ENTRIES + Lists::MAX_HEADS) * 4 + 3 * FA_MAX_LIST_ENTRIES * 2 <= LISTS_LDS,
                   "the largest lists fit in LDS, with two slots an entry");
     if (lds > 64 << 10) { // more than a kernel gets without asking
         static const hipError_t allowed =

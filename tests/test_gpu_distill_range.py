@@ -146,3 +146,12 @@ def test_lists_under_a_finite_mask():
         val[0][r] = v
     check_dz(z, idx, val, [1], 1.0)
     check_loss(z, idx, val, [1], 1.0)
+
+
+@pytest.mark.parametrize("tau", [1e-25, 1e-21, 1e-15])
+def test_loss_at_temperatures_whose_square_is_below_fp32(tau):
+    # loss = tau^2 * kl and kl grows as 1 / tau: the product is a number
+    R, V = 3, 300
+    z = rnd((R, V), 5, 2.5)
+    idx, val = lists_of(R, V, (1,), 9)
+    check_loss(z, idx, val, [1], tau)

@@ -1103,7 +1103,8 @@ __global__ __launch_bounds__(THREADS, KEEP ? 4 : 1) void distill_kernel(DistillA
                     }
         }
         if (LOSS && first && threadIdx.x == 0) {
-            p.loss[r] = sent ? g * (p.tau * p.tau) * kl : 0.f;
+            // not tau^2, which fp32 does not hold where tau * kl is a number
+            p.loss[r] = sent ? g * p.tau * (p.tau * kl) : 0.f;
             if (p.lse)
                 p.lse[r] = lse;
         }

@@ -551,8 +551,8 @@ int linear_workspace_size(fa_dtype dtype, int64_t M, int64_t N, int64_t K, fa_ac
  * out        [M][N].  May be the residual itself (same pointer and pitch).
  * preact     [M][N] (nullable): receives z, which linear_backward takes.
  * K == 0 gives out = act(bias) + residual; M == 0 or N == 0 is a no-op.
- * out and preact must not overlap each other or the other inputs
- * (FA_ERR_ARG).
+ * out and preact must not overlap each other or the other inputs, nor the
+ * workspace anything else (FA_ERR_ARG).
  */
 int linear_forward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void *x, int64_t ldx,
                    const void *w, int64_t ldw, const void *bias, fa_act act, float alpha,
@@ -567,7 +567,8 @@ int linear_forward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void *
  * each nullable; x is needed for dw, w for dx, preact (which holds z) for an
  * activation.  For the two products dz is held in the element type, as dy is;
  * db sums it unrounded.  M == 0 gives zero dw and db; N == 0 gives zero dx.
- * Outputs must not overlap the inputs or each other (FA_ERR_ARG).
+ * Outputs must not overlap the inputs or each other, nor the workspace
+ * anything else (FA_ERR_ARG).
  */
 int linear_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void *dy, int64_t lddy,
                     const void *x, int64_t ldx, const void *w, int64_t ldw, fa_act act, float alpha,
@@ -594,7 +595,8 @@ int linear_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void 
  * log sum_i exp(x_i / tau), the normaliser of the row's softmax at temperature
  * tau: -inf for a row of -inf, NaN for one that holds NaN or +inf.
  * 1e-30 <= tau <= 1e30; 0 <= k <= min(V, FA_MAX_TOP); 0 <= V <= 2^30, 0 <= R <= 2^36 / max(V, 1)
- * (FA_ERR_RANGE).  Asynchronous on `stream`.
+ * (FA_ERR_RANGE).  The outputs and the workspace must not overlap x or one
+ * another (FA_ERR_ARG).  Asynchronous on `stream`.
  */
 int logits_topk_workspace_size(fa_dtype dtype, int64_t R, int64_t V, int64_t k, size_t *bytes);
 int logits_topk(const void *x, fa_dtype dtype, int64_t R, int64_t V, int64_t ldx, int64_t k,
@@ -637,6 +639,8 @@ int logits_topk(const void *x, fa_dtype dtype, int64_t R, int64_t V, int64_t ldx
  *              z itself (same pointer and pitch); otherwise it must not overlap.
  * err_flag     device int, nullable: set to 0, then to FA_ERR_INDEX if some
  *              list is flawed.
+ * loss, lse, dz, err_flag and the workspace must not overlap one another or an
+ * input, but for dz being z itself (FA_ERR_ARG).
  * NaN and infinities that enter a row's formulas propagate into its results.
  * Sums are fp32 in an order fixed by the sizes: results are deterministic.
  *

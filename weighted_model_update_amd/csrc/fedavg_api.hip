@@ -1647,6 +1647,9 @@ int linear_forward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void *
         for (const View &i : {vx, vw, vb, vs})
             if (views_overlap(o, i))
                 return fail(FA_ERR_ARG, "out and preact must not overlap the inputs or the workspace");
+    for (const View &i : {vx, vw, vb, vr})
+        if (views_overlap(vs, i))
+            return fail(FA_ERR_ARG, "the workspace must not overlap the inputs");
     if (views_overlap(vo, vp) || views_overlap(vp, vr) || (views_overlap(vo, vr) && !same_view(vo, vr)))
         return fail(FA_ERR_ARG, "out and preact must not overlap each other or, but for out being the "
                                 "residual itself, the residual");
@@ -1703,6 +1706,9 @@ int linear_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void 
         for (const View &i : {vy, vx, vw, vp, vs})
             if (views_overlap(o, i))
                 return fail(FA_ERR_ARG, "dx, dw and db must not overlap the inputs or the workspace");
+    for (const View &i : {vy, vx, vw, vp})
+        if (views_overlap(vs, i))
+            return fail(FA_ERR_ARG, "the workspace must not overlap the inputs");
     if (views_overlap(vdx, vdw) || views_overlap(vdx, vdb) || views_overlap(vdw, vdb))
         return fail(FA_ERR_ARG, "dx, dw and db must not overlap each other");
     const BackwardPlan plan = backward_plan(dtype, M, N, K, act);
@@ -1785,6 +1791,20 @@ int check_logits(int dtype, int64_t R, int64_t V, float tau)
     return FA_OK;
 }
 
+// Whether a result shares bytes with what each row's workgroups read besides
+// the logits: the contributing clients' lists and normalisers, the row weights.
+bool overlaps_row_inputs(const fa::DistillArgs &a, const View &o, int64_t R, const float *row_weight)
+{
+    const auto flat = [&](const void *p, int64_t per) { return View{p, p ? R : 0, per, per, 4}; };
+    if (views_overlap(o, flat(row_weight, 1)))
+        return true;
+    for (int c = 0; c < a.clients; c++)
+        if (views_overlap(o, flat(a.idx[c], a.k[c])) || views_overlap(o, flat(a.val[c], a.k[c])) ||
+            views_overlap(o, flat(a.tlse[c], 1)))
+            return true;
+    return false;
+}
+
 // Every argument of distill_loss and distill_backward but the results of the
 // loss; fills `a`.
 int distill_args(fa::DistillArgs &a, int clients, const int32_t *const *idx, const float *const *val,
@@ -1834,9 +1854,14 @@ int distill_args(fa::DistillArgs &a, int clients, const int32_t *const *idx, con
         return fail(FA_ERR_ARG, "dz must be z itself or not overlap it");
     if (((reinterpret_cast<uintptr_t>(row_weight) | reinterpret_cast<uintptr_t>(err_flag)) & 3u) != 0)
         return fail(FA_ERR_ARG, "row_weight and err_flag must be 4-byte aligned");
-    const View vs{workspace, workspace ? 1 : 0, (int64_t)workspace_bytes, 0, 1};
+    const View vs{workspace, workspace ? 1 : 0, (int64_t)workspace_bytes, 0, 1}, ve{err_flag, err_flag ? 1 : 0, 1, 1, 4};
     if (views_overlap(vd, vs) || views_overlap(vz, vs))
         return fail(FA_ERR_ARG, "the workspace must not overlap z or dz");
+    if (views_overlap(ve, vz) || views_overlap(ve, vd) || views_overlap(ve, vs))
+        return fail(FA_ERR_ARG, "err_flag must not overlap z, dz or the workspace");
+    for (const View &o : {vd, vs, ve})
+        if (overlaps_row_inputs(a, o, R, row_weight))
+            return fail(FA_ERR_ARG, "dz, err_flag and the workspace must not overlap the lists, teacher_lse or row_weight");
     if ((rc = check_workspace(workspace, workspace_bytes, fa::distill_workspace_bytes(dtype, R, V, cu_count()))) != FA_OK)
         return rc;
     a.z = z;
@@ -1901,6 +1926,8 @@ int logits_topk(const void *x, fa_dtype dtype, int64_t R, int64_t V, int64_t ldx
             return fail(FA_ERR_ARG, "outputs must not overlap the logits or the workspace");
     if (views_overlap(vi, vv) || views_overlap(vi, vl) || views_overlap(vv, vl))
         return fail(FA_ERR_ARG, "outputs must not overlap each other");
+    if (views_overlap(vx, vs))
+        return fail(FA_ERR_ARG, "the workspace must not overlap the logits");
     if ((rc = check_workspace(workspace, workspace_bytes, fa::top_rows_workspace_bytes(dtype, R, V, k, cu_count()))) != FA_OK)
         return rc;
     const fa::TopRowsArgs a{x, R, V, ldx, (int)k, 1.f / tau, idx_out, val_out, lse_out, workspace};
@@ -1934,9 +1961,13 @@ int distill_loss(int clients, const int32_t *const *idx, const float *const *val
         vd{dz, dz ? R : 0, V, lddz, dsize(dtype)}, vs{workspace, workspace ? 1 : 0, (int64_t)workspace_bytes, 0, 1};
     if ((rc = check_view("loss", vl, true)) != FA_OK || (rc = check_view("lse", ve, true)) != FA_OK)
         return rc;
-    for (const View &o : {vl, ve})
-        if (views_overlap(o, vz) || views_overlap(o, vd) || views_overlap(o, vs))
-            return fail(FA_ERR_ARG, "loss and lse must not overlap z, dz or the workspace");
+    const View vf{err_flag, err_flag ? 1 : 0, 1, 1, 4};
+    for (const View &o : {vl, ve}) {
+        if (views_overlap(o, vz) || views_overlap(o, vd) || views_overlap(o, vs) || views_overlap(o, vf))
+            return fail(FA_ERR_ARG, "loss and lse must not overlap z, dz, err_flag or the workspace");
+        if (overlaps_row_inputs(a, o, R, row_weight))
+            return fail(FA_ERR_ARG, "loss and lse must not overlap the lists, teacher_lse or row_weight");
+    }
     if (views_overlap(vl, ve))
         return fail(FA_ERR_ARG, "loss and lse must not overlap");
     a.loss = loss;
@@ -1962,8 +1993,9 @@ int distill_backward(int clients, const int32_t *const *idx, const float *const 
     const View ve{lse, 1, R, R, 4}, vd{dz, R, V, lddz, dsize(dtype)};
     if ((rc = check_view("lse", ve, false)) != FA_OK)
         return rc;
-    if (views_overlap(vd, ve))
-        return fail(FA_ERR_ARG, "dz must not overlap lse");
+    const View vs{workspace, workspace ? 1 : 0, (int64_t)workspace_bytes, 0, 1}, vf{err_flag, err_flag ? 1 : 0, 1, 1, 4};
+    if (views_overlap(ve, vd) || views_overlap(ve, vs) || views_overlap(ve, vf))
+        return fail(FA_ERR_ARG, "dz, err_flag and the workspace must not overlap lse");
     a.lse = const_cast<float *>(lse);
     return run_distill(a, dtype, false, stream);
 }

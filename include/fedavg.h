@@ -49,6 +49,8 @@
  *   - Argument errors are detected and returned before any device work is
  *     enqueued.  Device work is asynchronous on the stream(s) given (a
  *     hipStream_t passed as void*; NULL is the default stream).
+ *   - Work is launched on the calling thread's current device, which must be
+ *     the stream's and that of every device buffer.
  *   - The caller owns every device buffer, pinned host buffer and stream.
  *     Only the streaming handle (host memory and its HIP events, plus one
  *     internal copy stream when the caller passes none) belongs to the

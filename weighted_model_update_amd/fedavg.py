@@ -772,13 +772,35 @@ def _act(act):
 
 # These checks run before every launch of kernels that may take 5 us
 # themselves, so they make as few calls as they can.
-def _matrix(t, name, rows, cols, dtype):
-    """Row pitch of a GPU matrix [rows, cols] of `dtype` with unit column
-    stride (0 for an absent one)."""
+def _current_device():
+    return torch._C._cuda_getDevice()
+
+
+def _device(t, name, stream):
+    """Index of the GPU that the call runs on: the tensor's, which must be the
+    current one, as the library launches there, and the stream's."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if dev != _current_device():
+        raise ValueError(f"{name} is on GPU {dev}, the current device is {_current_device()}")
+    if stream is not None and stream.device_index != dev:
+        raise ValueError(f"{name} is on GPU {dev}, the stream on {stream.device_index}")
+    return dev
+
+
+def _on_device(t, name, dev):
+    at = t.get_device()
+    if at != dev:
+        raise ValueError(f"{name} must be a GPU tensor" if at < 0 else f"{name} is on GPU {at}, the call runs on {dev}")
+
+
+def _matrix(t, name, rows, cols, dtype, dev):
+    """Row pitch of a matrix [rows, cols] of `dtype` on GPU `dev` with unit
+    column stride (0 for an absent one)."""
     if t is None:
         return 0
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
+    _on_device(t, name, dev)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != (rows, cols):
@@ -789,11 +811,10 @@ def _matrix(t, name, rows, cols, dtype):
     return ld if rows > 1 else max(ld, cols)
 
 
-def _vector(t, name, n, dtype):
+def _vector(t, name, n, dtype, dev):
     if t is None:
         return
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
+    _on_device(t, name, dev)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.numel() != n or not t.is_contiguous():
@@ -804,11 +825,11 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(stream, t):
-    """Handle of `stream`, or of the current stream of t's device."""
+def _raw_stream(stream, dev):
+    """Handle of `stream`, or of the device's current stream."""
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _new(shape, dtype, device, stream):
@@ -831,7 +852,7 @@ def _workspace(workspace, t, stream, function, *sizes):
     """(tensor to keep, address, bytes) of the caller's workspace or of one
     made for the call."""
     if workspace is not None:
-        _contig(_on_gpu(workspace, "workspace"), "workspace")
+        _on_device(_contig(workspace, "workspace"), "workspace", t.get_device())
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     n = _bytes_of(function, t.device.index, *sizes)
     if n == 0:
@@ -860,16 +881,16 @@ def linear_forward(x, w, bias=None, act="none", residual=None, alpha=1.0, out=No
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w must be matrices")
     dt, code = x.dtype, _dtype(x)
-    (M, K), N, act = x.shape, w.shape[0], _act(act)
-    ldx, ldw = _matrix(x, "x", M, K, dt), _matrix(w, "w", N, K, dt)
-    _vector(bias, "bias", N, dt)
+    (M, K), N, act, dev = x.shape, w.shape[0], _act(act), _device(x, "x", stream)
+    ldx, ldw = _matrix(x, "x", M, K, dt, dev), _matrix(w, "w", N, K, dt, dev)
+    _vector(bias, "bias", N, dt, dev)
     if out is None:
         out = _new((M, N), dt, x.device, stream)
-    ldr, ldo = _matrix(residual, "residual", M, N, dt), _matrix(out, "out", M, N, dt)
-    ldp = _matrix(preact, "preact", M, N, dt)
+    ldr, ldo = _matrix(residual, "residual", M, N, dt, dev), _matrix(out, "out", M, N, dt, dev)
+    ldp = _matrix(preact, "preact", M, N, dt, dev)
     keep, ws, nbytes = _workspace(workspace, x, stream, "linear_workspace_size", code, M, N, K, act, 0)
     rc = lib.linear_forward(code, M, N, K, x.data_ptr(), ldx, w.data_ptr(), ldw, _at(bias), act, alpha, _at(residual),
-                            ldr, out.data_ptr(), ldo, _at(preact), ldp, ws, nbytes, _raw_stream(stream, x))
+                            ldr, out.data_ptr(), ldo, _at(preact), ldp, ws, nbytes, _raw_stream(stream, dev))
     if rc:
         _check(rc)
     return out
@@ -886,7 +907,7 @@ def linear_backward(dy, x, w, act="none", preact=None, alpha=1.0, dx=True, dw=Tr
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w must be matrices")
     dt, code = x.dtype, _dtype(x)
-    (M, K), N, act = x.shape, w.shape[0], _act(act)
+    (M, K), N, act, dev = x.shape, w.shape[0], _act(act), _device(x, "x", stream)
 
     def want(t, shape):
         if t is None or t is False:
@@ -894,13 +915,13 @@ def linear_backward(dy, x, w, act="none", preact=None, alpha=1.0, dx=True, dw=Tr
         return _new(shape, dt, x.device, stream) if t is True else t
 
     dx, dw, db = want(dx, (M, K)), want(dw, (N, K)), want(db, (N,))
-    lddy, ldx, ldw = _matrix(dy, "dy", M, N, dt), _matrix(x, "x", M, K, dt), _matrix(w, "w", N, K, dt)
-    ldp = _matrix(preact, "preact", M, N, dt)
-    lddx, lddw = _matrix(dx, "dx", M, K, dt), _matrix(dw, "dw", N, K, dt)
-    _vector(db, "db", N, dt)
+    lddy, ldx, ldw = _matrix(dy, "dy", M, N, dt, dev), _matrix(x, "x", M, K, dt, dev), _matrix(w, "w", N, K, dt, dev)
+    ldp = _matrix(preact, "preact", M, N, dt, dev)
+    lddx, lddw = _matrix(dx, "dx", M, K, dt, dev), _matrix(dw, "dw", N, K, dt, dev)
+    _vector(db, "db", N, dt, dev)
     keep, ws, nbytes = _workspace(workspace, x, stream, "linear_workspace_size", code, M, N, K, act, 1)
     rc = lib.linear_backward(code, M, N, K, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), ldw, act, alpha,
-                             _at(preact), ldp, _at(dx), lddx, _at(dw), lddw, _at(db), ws, nbytes, _raw_stream(stream, x))
+                             _at(preact), ldp, _at(dx), lddx, _at(dw), lddw, _at(db), ws, nbytes, _raw_stream(stream, dev))
     if rc:
         _check(rc)
     return dx, dw, db
@@ -924,18 +945,19 @@ def logits_topk(x, k, tau=1.0, idx_out=None, val_out=None, lse_out=None, workspa
     if x.dim() != 2:
         raise ValueError("x must be a matrix [R, V]")
     (R, V), k = x.shape, int(k)
-    ld = _matrix(x, "x", R, V, x.dtype)
+    dev = _device(x, "x", stream)
+    ld = _matrix(x, "x", R, V, x.dtype, dev)
     kk = max(k, 0)
     idx_out = _new((R, kk), torch.int32, x.device, stream) if idx_out is None else idx_out
     val_out = _new((R, kk), torch.float32, x.device, stream) if val_out is None else val_out
     lse_out = _new((R,), torch.float32, x.device, stream) if lse_out is None else lse_out
-    _vector(idx_out, "idx_out", R * kk, torch.int32)
-    _vector(val_out, "val_out", R * kk, torch.float32)
-    _vector(lse_out, "lse_out", R, torch.float32)
+    _vector(idx_out, "idx_out", R * kk, torch.int32, dev)
+    _vector(val_out, "val_out", R * kk, torch.float32, dev)
+    _vector(lse_out, "lse_out", R, torch.float32, dev)
     code = _dtype(x)
     keep, ws, nbytes = _workspace(workspace, x, stream, "logits_topk_workspace_size", code, R, V, k)
     rc = lib.logits_topk(x.data_ptr(), code, R, V, ld, k, tau, idx_out.data_ptr(), val_out.data_ptr(),
-                         lse_out.data_ptr(), ws, nbytes, _raw_stream(stream, x))
+                         lse_out.data_ptr(), ws, nbytes, _raw_stream(stream, dev))
     if rc:
         _check(rc)
     return idx_out, val_out, lse_out
@@ -948,7 +970,7 @@ def distill_workspace_size(R, V, dtype=torch.bfloat16):
     return b.value
 
 
-def _distill_lists(idx, val, teacher_lse, n, R):
+def _distill_lists(idx, val, teacher_lse, n, R, dev):
     """(clients, idx, val and teacher_lse addresses, k, n) for the library."""
     C = len(n)
     if len(idx) != C or len(val) != C or (teacher_lse is not None and len(teacher_lse) != C):
@@ -963,24 +985,27 @@ def _distill_lists(idx, val, teacher_lse, n, R):
         shape = i.shape
         if len(shape) != 2 or shape[0] != R or v.shape != shape:
             raise ValueError(f"idx[{c}] and val[{c}] must both be [{R}, k]")
-        if not (i.is_cuda and v.is_cuda):
-            raise ValueError(f"idx[{c}] and val[{c}] must be GPU tensors")
+        if i.get_device() != dev or v.get_device() != dev:
+            raise ValueError(f"idx[{c}] and val[{c}] must be GPU tensors on GPU {dev}")
         if i.dtype is not i32 or v.dtype is not f32:
             raise TypeError(f"idx[{c}] must be int32 and val[{c}] float32")
         if not (i.is_contiguous() and v.is_contiguous()):
             raise ValueError(f"idx[{c}] and val[{c}] must be contiguous")
         pi[c], pv[c], ks[c] = i.data_ptr(), v.data_ptr(), shape[1]
         if pl is not None:
-            _vector(teacher_lse[c], f"teacher_lse[{c}]", R, f32)
+            _vector(teacher_lse[c], f"teacher_lse[{c}]", R, f32, dev)
             pl[c] = teacher_lse[c].data_ptr()
     P, I = ctypes.c_void_p * C, ctypes.c_int64 * C
     return C, P(*pi), P(*pv), None if pl is None else P(*pl), I(*ks), I(*map(int, n))
 
 
-def _err_flag(err_flag):
-    if err_flag is not None and (err_flag.numel() < 1 or err_flag.dtype != torch.int32):
+def _err_flag(err_flag, dev):
+    if err_flag is None:
+        return None
+    if err_flag.numel() < 1 or err_flag.dtype != torch.int32:
         raise ValueError("err_flag must be an int32 tensor of at least one element")
-    return _on_gpu(err_flag, "err_flag")
+    _on_device(err_flag, "err_flag", dev)
+    return err_flag.data_ptr()
 
 
 def distill_loss(z, idx, val, n, tau=1.0, teacher_lse=None, row_weight=None, loss=None, lse=None, dz=None,
@@ -998,19 +1023,20 @@ def distill_loss(z, idx, val, n, tau=1.0, teacher_lse=None, row_weight=None, los
     if z.dim() != 2:
         raise ValueError("z must be a matrix [R, V]")
     R, V = z.shape
-    ldz = _matrix(z, "z", R, V, z.dtype)
+    dev = _device(z, "z", stream)
+    ldz = _matrix(z, "z", R, V, z.dtype, dev)
     loss = _new((R,), torch.float32, z.device, stream) if loss is None else loss
     lse = _new((R,), torch.float32, z.device, stream) if lse is None else lse
     dz = None if dz is None or dz is False else (_new((R, V), z.dtype, z.device, stream) if dz is True else dz)
-    lddz = _matrix(dz, "dz", R, V, z.dtype)
+    lddz = _matrix(dz, "dz", R, V, z.dtype, dev)
     for t, name in ((row_weight, "row_weight"), (loss, "loss"), (lse, "lse")):
-        _vector(t, name, R, torch.float32)
-    C, pi, pv, pl, ks, ns = _distill_lists(idx, val, teacher_lse, n, R)
+        _vector(t, name, R, torch.float32, dev)
+    C, pi, pv, pl, ks, ns = _distill_lists(idx, val, teacher_lse, n, R, dev)
     code = _dtype(z)
     keep, ws, nbytes = _workspace(workspace, z, stream, "distill_workspace_size", code, R, V)
     rc = lib.distill_loss(C, pi, pv, pl, ks, ns, z.data_ptr(), code, R, V, ldz, tau, _at(row_weight),
-                          loss.data_ptr(), lse.data_ptr(), _at(dz), lddz, _at(_err_flag(err_flag)), ws, nbytes,
-                          _raw_stream(stream, z))
+                          loss.data_ptr(), lse.data_ptr(), _at(dz), lddz, _err_flag(err_flag, dev), ws, nbytes,
+                          _raw_stream(stream, dev))
     if rc:
         _check(rc)
     return loss, lse, dz
@@ -1025,17 +1051,18 @@ def distill_backward(z, lse, idx, val, n, tau=1.0, teacher_lse=None, row_weight=
     if z.dim() != 2:
         raise ValueError("z must be a matrix [R, V]")
     R, V = z.shape
-    ldz = _matrix(z, "z", R, V, z.dtype)
+    dev = _device(z, "z", stream)
+    ldz = _matrix(z, "z", R, V, z.dtype, dev)
     dz = _new((R, V), z.dtype, z.device, stream) if dz is None else dz
-    lddz = _matrix(dz, "dz", R, V, z.dtype)
+    lddz = _matrix(dz, "dz", R, V, z.dtype, dev)
     for t, name in ((row_weight, "row_weight"), (lse, "lse")):
-        _vector(t, name, R, torch.float32)
-    C, pi, pv, pl, ks, ns = _distill_lists(idx, val, teacher_lse, n, R)
+        _vector(t, name, R, torch.float32, dev)
+    C, pi, pv, pl, ks, ns = _distill_lists(idx, val, teacher_lse, n, R, dev)
     code = _dtype(z)
     keep, ws, nbytes = _workspace(workspace, z, stream, "distill_workspace_size", code, R, V)
     rc = lib.distill_backward(C, pi, pv, pl, ks, ns, z.data_ptr(), code, R, V, ldz, tau, _at(row_weight),
-                              lse.data_ptr(), dz.data_ptr(), lddz, _at(_err_flag(err_flag)), ws, nbytes,
-                              _raw_stream(stream, z))
+                              lse.data_ptr(), dz.data_ptr(), lddz, _err_flag(err_flag, dev), ws, nbytes,
+                              _raw_stream(stream, dev))
     if rc:
         _check(rc)
     return dz

@@ -15,6 +15,7 @@ SOURCES = [os.path.join(HERE, "csrc", "fedavg_kernels.hip"),
            os.path.join(HERE, "csrc", "fedavg_api.hip")]
 HEADERS = [os.path.join(HERE, "csrc", "fedavg_internal.h"),
            os.path.join(HERE, "csrc", "learn_internal.h"),
+           os.path.join(HERE, "csrc", "device_once.h"),
            os.path.join(ROOT, "include", "fedavg.h")]
 
 # IEEE fp32 arithmetic: no fast-math, no FMA contraction beyond the explicit

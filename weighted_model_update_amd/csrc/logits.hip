@@ -4,6 +4,7 @@
 // All of it is bound by reading the logits (and writing the gradient): rows
 // are read in 16-byte vectors, whatever their alignment, with the softmax's
 // running maximum and sum kept per thread in the same pass.
+#include "device_once.h"
 #include "learn_internal.h"
 
 #include <algorithm>
@@ -1192,11 +1193,16 @@ hipError_t run_distill(const DistillArgs &a, int pieces, int64_t len, int stat_p
     static_assert((4 * FA_MAX_CLIENTS + (2 + 4) * FA_MAX_LIST_ENTRIES + Lists::MAX_HEADS) * 4 + 3 * FA_MAX_LIST_ENTRIES * 2 <= LISTS_LDS,
                   "the largest lists fit in LDS, with two slots an entry");
     if (lds > 64 << 10) { // more than a kernel gets without asking
-        static const hipError_t allowed =
-            hipFuncSetAttribute(reinterpret_cast<const void *>(&distill_kernel<T, THREADS, LOSS, FROM, KEEP>),
-                                hipFuncAttributeMaxDynamicSharedMemorySize, LISTS_LDS);
-        if (allowed != hipSuccess)
-            return allowed;
+        static DeviceOnce limit;
+        int device = 0;
+        hipError_t e = hipGetDevice(&device);
+        if (e == hipSuccess)
+            e = (hipError_t)limit.run(device, [] {
+                return (int)hipFuncSetAttribute(reinterpret_cast<const void *>(&distill_kernel<T, THREADS, LOSS, FROM, KEEP>),
+                                                hipFuncAttributeMaxDynamicSharedMemorySize, LISTS_LDS);
+            });
+        if (e != hipSuccess)
+            return e;
     }
     distill_kernel<T, THREADS, LOSS, FROM, KEEP><<<grid, THREADS, lds, s>>>(a, pieces, len, stat_pieces);
     return hipGetLastError();

@@ -34,14 +34,38 @@ template <> struct traits<float> { static constexpr int EPC = 4; };
 // GELU is the exact one, z Phi(z).  With x = |z| / sqrt(2),
 //     Phi(-|z|) = exp(-x^2) P(t) / 2,  t = 1 / (1 + 0.33 x),
 // P a polynomial without constant term fitted to exp(x^2) erfc(x) on
-// [0, 10] for the least relative error (9.4e-8 there, about 3e-7 as evaluated
-// in fp32, also deep in the tail).  It costs a third of the library's erff, and
-// the slope's exp(-z^2 / 2) comes with it.  The sigmoid likewise uses the
-// hardware's exp2 and reciprocal (one unit in the last place each).
-__device__ __forceinline__ float phi_below(float z, float &e) // Phi(-|z|); e = exp(-z^2 / 2)
+// [0, 10] for the least relative error (9.4e-8 there, 5e-7 as evaluated in
+// fp32).  It costs a third of the library's erff, and the slope's
+// exp(-z^2 / 2) comes with it.  The sigmoid likewise uses the hardware's exp2
+// and reciprocal (one unit in the last place each, results below 2^-126
+// flushed).  An exponent y is rounded when it is formed, which is a relative
+// error of up to 2^-24 |y| of its exp2: 8e-6 of GELU's tail at z = -13, 4e-6 of
+// the sigmoid's at z = -87.  For fp32 (EXACT) what that left off is multiplied
+// in; for bf16, whose results are rounded to 2^-9, it is not worth the
+// instructions.
+
+// exp(y c) for the two parts c = hi + lo of a constant and y^n = p + rest
+// (rest: what p lost, 0 for y itself)
+template <bool EXACT> __device__ __forceinline__ float exp_of(float p, float rest, float hi, float lo)
+{
+    const float y = p * hi;
+    float e = __builtin_amdgcn_exp2f(y);
+    if (EXACT) {
+        const float off = __builtin_fmaf(p, lo, __builtin_fmaf(rest, hi, __builtin_fmaf(p, hi, -y)));
+        // beyond, e is 0 or infinite and `off` may be NaN
+        e *= fabsf(y) < 256.f ? __builtin_fmaf(off, 0.69314718055994531f, 1.f) : 1.f;
+    }
+    return e;
+}
+
+constexpr double LOG2E = 1.44269504088896340736;
+constexpr float LOG2E_HI = (float)LOG2E, LOG2E_LO = (float)(LOG2E - (double)LOG2E_HI);
+
+template <bool EXACT> __device__ __forceinline__ float phi_below(float z, float &e) // Phi(-|z|); e = exp(-z^2 / 2)
 {
     const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(z), 0.33f * 0.70710678118654752f, 1.f));
-    e = __builtin_amdgcn_exp2f(z * z * (-0.5f * 1.44269504088896341f));
+    const float h = z * z;
+    e = exp_of<EXACT>(h, EXACT ? __builtin_fmaf(z, z, -h) : 0.f, -0.5f * LOG2E_HI, -0.5f * LOG2E_LO);
     float q = -0.1353444159f;
     q = __builtin_fmaf(q, t, 0.4602320194f);
     q = __builtin_fmaf(q, t, -0.3511412442f);
@@ -53,13 +77,13 @@ __device__ __forceinline__ float phi_below(float z, float &e) // Phi(-|z|); e = 
     return 0.5f * (q * t) * e;
 }
 
-__device__ __forceinline__ float sigmoid(float z)
+template <bool EXACT> __device__ __forceinline__ float sigmoid(float z)
 {
-    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+    return __builtin_amdgcn_rcpf(1.f + exp_of<EXACT>(z, 0.f, -LOG2E_HI, -LOG2E_LO));
 }
 
 // z[i] = act(z[i]); NaN stays NaN
-template <int W> __device__ __forceinline__ void apply_act(float *z, int act)
+template <bool EXACT, int W> __device__ __forceinline__ void apply_act(float *z, int act)
 {
     if (act == FA_ACT_RELU) {
 #pragma unroll
@@ -69,18 +93,18 @@ template <int W> __device__ __forceinline__ void apply_act(float *z, int act)
 #pragma unroll
         for (int i = 0; i < W; i++) {
             float e;
-            const float q = phi_below(z[i], e);
+            const float q = phi_below<EXACT>(z[i], e);
             z[i] *= z[i] > 0.f ? 1.f - q : q;
         }
     } else if (act == FA_ACT_SILU) {
 #pragma unroll
         for (int i = 0; i < W; i++)
-            z[i] *= sigmoid(z[i]);
+            z[i] *= sigmoid<EXACT>(z[i]);
     }
 }
 
 // d[i] *= act'(z[i])
-template <int W> __device__ __forceinline__ void apply_slope(float *d, const float *z, int act)
+template <bool EXACT, int W> __device__ __forceinline__ void apply_slope(float *d, const float *z, int act)
 {
     if (act == FA_ACT_RELU) {
 #pragma unroll
@@ -90,13 +114,13 @@ template <int W> __device__ __forceinline__ void apply_slope(float *d, const flo
 #pragma unroll
         for (int i = 0; i < W; i++) {
             float e;
-            const float q = phi_below(z[i], e);
+            const float q = phi_below<EXACT>(z[i], e);
             d[i] *= __builtin_fmaf(z[i] * e, 0.39894228040143268f, z[i] > 0.f ? 1.f - q : q);
         }
     } else if (act == FA_ACT_SILU) {
 #pragma unroll
         for (int i = 0; i < W; i++) {
-            const float s = sigmoid(z[i]);
+            const float s = sigmoid<EXACT>(z[i]);
             d[i] *= s * __builtin_fmaf(z[i], 1.f - s, 1.f);
         }
     }
@@ -194,7 +218,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs &p, int64_t m, int n, co
         z[i] = __builtin_fmaf(p.alpha, s[i], (float)bias.e[i]);
     if (p.pre)
         store_n<T, W>(static_cast<T *>(p.pre) + m * p.ldp + n, valid, z);
-    apply_act<W>(z, p.act);
+    apply_act<sizeof(T) == 4, W>(z, p.act);
     if (p.res) {
 #pragma unroll
         for (int i = 0; i < W; i++)
@@ -887,7 +911,7 @@ template <typename T> __global__ __launch_bounds__(AG_THREADS) void act_grad_ker
             const int64_t m = m0 + u * groups;
             if (m >= r1)
                 break;
-            apply_slope<AG_W>(d[u], z[u], p.act);
+            apply_slope<sizeof(T) == 4, AG_W>(d[u], z[u], p.act);
             if (p.dz)
                 store_n<T, AG_W>(static_cast<T *>(p.dz) + m * p.lddz + n, AG_W, d[u]);
 #pragma unroll

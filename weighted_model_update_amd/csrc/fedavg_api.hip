@@ -1986,11 +1986,9 @@ int distill_backward(int clients, const int32_t *const *idx, const float *const 
                           err_flag, workspace, workspace_bytes);
     if (rc != FA_OK)
         return rc;
-    if (R == 0 || V == 0)
-        return ok();
-    if (!dz)
+    if (R > 0 && V > 0 && !dz)
         return fail(FA_ERR_ARG, "dz is required");
-    const View ve{lse, 1, R, R, 4}, vd{dz, R, V, lddz, dsize(dtype)};
+    const View ve{lse, V > 0 ? 1 : 0, R, R, 4}, vd{dz, R, V, lddz, dsize(dtype)};
     if ((rc = check_view("lse", ve, false)) != FA_OK)
         return rc;
     const View vs{workspace, workspace ? 1 : 0, (int64_t)workspace_bytes, 0, 1}, vf{err_flag, err_flag ? 1 : 0, 1, 1, 4};

@@ -1082,7 +1082,7 @@ __global__ __launch_bounds__(THREADS, KEEP ? 4 : 1) void distill_kernel(DistillA
             } else if (FROM == LSE_PIECES) {
                 t = join_pieces(static_cast<const TopPiece *>(p.ws) + r * stat_pieces, stat_pieces, c2);
             } else {
-                lse = p.lse[r];
+                lse = p.lse ? p.lse[r] : NEG_INF; // none where V is 0
                 stored = !lse_too_coarse(lse);
                 if (!stored && stat_pieces > 0)
                     t = join_pieces(static_cast<const TopPiece *>(p.ws) + r * stat_pieces, stat_pieces, c2);

@@ -595,10 +595,12 @@ int linear_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void 
  * counts as largest, -0 as equal to +0.  The result is unique, hence
  * deterministic.  lse_out (device float[R], nullable) receives
  * log sum_i exp(x_i / tau), the normaliser of the row's softmax at temperature
- * tau: -inf for a row of -inf, NaN for one that holds NaN or +inf.
- * 1e-30 <= tau <= 1e30; 0 <= k <= min(V, FA_MAX_TOP); 0 <= V <= 2^30, 0 <= R <= 2^36 / max(V, 1)
- * (FA_ERR_RANGE).  The outputs and the workspace must not overlap x or one
- * another (FA_ERR_ARG).  Asynchronous on `stream`.
+ * tau: -inf for a row of -inf, NaN for one that holds NaN or +inf, infinite
+ * where max / tau passes fp32.
+ * 0 <= k <= min(V, FA_MAX_TOP), V <= 2^30 and R <= 2^36 / max(V, 1)
+ * (FA_ERR_RANGE); R, V >= 0 and 1e-30 <= tau <= 1e30 (FA_ERR_ARG).  The outputs
+ * and the workspace must not overlap x or one another (FA_ERR_ARG).
+ * Asynchronous on `stream`.
  */
 int logits_topk_workspace_size(fa_dtype dtype, int64_t R, int64_t V, int64_t k, size_t *bytes);
 int logits_topk(const void *x, fa_dtype dtype, int64_t R, int64_t V, int64_t ldx, int64_t k,
@@ -630,7 +632,7 @@ int logits_topk(const void *x, fa_dtype dtype, int64_t R, int64_t V, int64_t ldx
  *              client whose entries are all -inf has not sent the row either.
  *              A row that no client sent has loss 0 and gradient 0.
  * z            [R][V] of dtype, row pitch ldz.
- * tau          1e-30 to 1e30.
+ * tau          1e-30 to 1e30 (FA_ERR_ARG).
  * row_weight   device float[R], nullable (all 1).  A row of weight 0 (padding)
  *              is not read: its loss, lse and gradient are 0.  A row of z that
  *              is all -inf has lse -inf, loss 0 and gradient 0.

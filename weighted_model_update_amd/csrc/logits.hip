@@ -312,7 +312,10 @@ template <int THREADS_, int QUEUE_, int CAP_, int U_> struct TopLds {
 // digit is how many of them reach k.  (Two bits a step took twice the
 // barriers: 27.5 and 24.4 us for a row of 151936 fp32 in two kernels.)
 // It stops where at most `spare` more than k reach it; the lower bits are 0
-// then, which selects the same keys.
+// then, which selects the same keys.  With n <= k + spare keys that is at once,
+// and the result 0 bounds nothing: EXACT_KEY goes through all bits.
+constexpr int EXACT_KEY = -1;
+
 template <int BITS, typename L>
 __device__ __forceinline__ uint32_t kth_key(L &l, const uint32_t *keys, int n, int k, int spare)
 {
@@ -661,7 +664,11 @@ __device__ __forceinline__ void row_top(const T *x, int i0, int i1, int k, float
         top = max2(top, t);
     }
     l.best[threadIdx.x] = at >= i1 ? 0u : nan ? Key<T>::NAN_KEY : Key<T>::of(top); // 0: no entries
-    uint32_t bound = kth_key<Key<T>::BITS>(l, l.best, L::THREADS, k, k / 4);
+    // A quarter more than k may reach it, or, where there are no more threads
+    // than that, just k: 4096 rows of 8192 bf16, 256 threads, k = 204, 205, 256
+    // 91, 89, 262 us (a quarter more for all: 90, 129, 571, the last two with a
+    // bound of 0 and so with all entries for candidates).
+    uint32_t bound = kth_key<Key<T>::BITS>(l, l.best, L::THREADS, k, L::THREADS > k + k / 4 ? k / 4 : EXACT_KEY);
     __syncthreads();
     int q = stream_above<T, L>(x, i0, i1, bound, c, l, sm);
     int n = q > L::QUEUE ? L::CAP + 1 : take_queued<T, L>(q, i1, bound, l);
@@ -670,7 +677,7 @@ __device__ __forceinline__ void row_top(const T *x, int i0, int i1, int k, float
         __syncthreads();
         if (again == 0) {
             l.best[threadIdx.x] = Key<T>::of(sm.m); // of the numbers: FA_MAX_TOP threads or more have some
-            bound = max(bound, kth_key<Key<T>::BITS>(l, l.best, L::THREADS, k, 0));
+            bound = max(bound, kth_key<Key<T>::BITS>(l, l.best, L::THREADS, k, EXACT_KEY));
         } else {
             bound = kth_of_row<T, L>(x, i0, i1, k, l);
         }

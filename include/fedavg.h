@@ -618,7 +618,8 @@ int logits_topk(const void *x, fa_dtype dtype, int64_t R, int64_t V, int64_t ldx
  *     m = sum_c w_c sum_j q_cj,   g_r = row_weight[r]
  * L_c is the log-sum-exp of the list (the kept entries sum to one), or, when
  * teacher_lse is given, teacher_lse[c][r], the normaliser of the client's whole
- * row (logits_topk's lse_out; the entries not sent then carry no mass).
+ * row (logits_topk's lse_out; the entries not sent then carry no mass).  A given
+ * normaliser's own rounding, relative to its size, is a factor of q.
  *
  * clients      1 .. FA_MAX_CLIENTS; n as for fedavg_aggregate (n_c == 0: the
  *              client's lists are never read and may be NULL).

@@ -1,9 +1,10 @@
 // A client's top logits of each row (token), and the loss and gradient of a
 // student distilled from several clients' top logits.
 //
-// All of it is bound by reading the logits (and writing the gradient): rows
-// are read in 16-byte vectors, whatever their alignment, with the softmax's
-// running maximum and sum kept per thread in the same pass.
+// Rows are read in 16-byte vectors, whatever their alignment, with the softmax's
+// running maximum and sum kept per thread in the same pass.  The passes are
+// bound by reading the logits (and writing the gradient) and, where a logit
+// takes a dozen instructions, by the vector units.
 #include "device_once.h"
 #include "learn_internal.h"
 
@@ -130,9 +131,9 @@ constexpr float FUSED_UP_TO = 128.f;
 // A softmax's running maximum (of x, before the temperature) and sum of
 // exp((x - max) / tau), c = log2(e) / tau.  A maximum of -inf is taken off as
 // 0, so that -inf entries add 0; NaN and +inf turn the sum into NaN.  Each
-// thread's sum refers to its own running maximum.  v_exp_f32 flushes results below 2^-126, far under the sum's
-// rounding.  What bounds the pass after the memory is the vector unit: about
-// five instructions an entry, the exponential at a quarter of the rate.
+// thread's sum refers to its own running maximum.  v_exp_f32 flushes results
+// below 2^-126, far under the sum's rounding.  What bounds the pass beside the
+// memory is the vector unit: about five instructions an entry.
 struct Softmax {
     float m = NEG_INF, s = 0.f;
 
@@ -701,9 +702,11 @@ __device__ __forceinline__ float *piece_vals(const TopRowsArgs &p, int pieces)
 }
 
 // A workgroup per row (pieces = 1) or per piece of a row; a piece's results go
-// to the workspace, unused places with index -1.  Bound by memory: 4096 x
-// 128256 bf16, k = 64, in 247 us (1.05 GB, 4.3 TB/s), with 13 vector
-// instructions a logit.
+// to the workspace, unused places with index -1.  Bound by the vector units,
+// which issue in 76% of the cycles: 4096 x 128256 bf16, k = 64, in 247 us (1.05
+// GB, 4.3 TB/s, whatever of it the caches hold), with 12 vector instructions a
+// logit: the pass's five, a quarter of the row sampled before it, the selection,
+// and 8 spilled registers (69 MB of writes).
 template <typename T, typename L>
 __global__ __launch_bounds__(L::THREADS, 8) void top_rows_kernel(TopRowsArgs p, int pieces, int64_t len)
 {
@@ -747,8 +750,8 @@ __global__ __launch_bounds__(L::THREADS, 8) void top_rows_kernel(TopRowsArgs p, 
 }
 
 // Joins a row's pieces: their entries are the candidates, their softmax sums
-// are added in piece order.  Bound by latency: 12 us after the 20 of the pieces
-// (one row of 151936 fp32, 32 pieces, k = 32).
+// are added in piece order.  Bound by latency: about three eighths of the 23.4
+// us of a call (one row of 151936 fp32, 32 pieces, k = 32).
 using TopJoin = TopLds<512, 1, 4096, 1>;
 
 template <typename T> __global__ __launch_bounds__(TopJoin::THREADS) void top_join_kernel(TopRowsArgs p, int pieces)
@@ -886,8 +889,8 @@ struct Lists {
 };
 
 // The row's lists: q_cj = exp(v/tau - L_c) and what is summed over them; with
-// LOSS the listed logits, with `grad` also each index in [i0, i1) once, with sum_c w_c q_c added up in client
-// order.  One wavefront a client.  A list is used up to its first negative
+// LOSS the listed logits, with `grad` also each index in [i0, i1) once, with
+// sum_c w_c q_c added up in client order.  One wavefront a client.  A list is used up to its first negative
 // index; one that is not strictly increasing or passes V is left out whole and
 // raises the flag.
 template <typename T, int THREADS, bool LOSS>
@@ -1045,12 +1048,15 @@ enum { LSE_COMPUTE = 0, LSE_PIECES = 1, LSE_GIVEN = 2 };
 
 // A workgroup per row, or per piece of a row's gradient.  LOSS: writes loss
 // and lse (piece 0 does).  KEEP: chunks of the row that each thread keeps in
-// registers from the softmax's pass for the gradient's.  Bound by memory: loss
-// of 1024 x 151936 bf16, an eighth of them of weight 0, one list a row, 59 us
-// (272 MB, 4.6 TB/s); loss and gradient of 2048 x 128256, an eighth of weight 0,
-// with 8 lists 240 us (0.99 GB, 4.1 TB/s); gradient of
-// 1000 x 32003 fp32 with 16 lists of 100 in 85 us, of which its 16 lists,
-// read before the row, cost about 30.
+// registers from the softmax's pass for the gradient's.  Loss of 1024 x 151936
+// bf16, an eighth of them of weight 0, one list a row, 60 us (272 MB, 4.5 TB/s;
+// 53 of inputs that the last-level cache holds in part): all rows are resident
+// at once, and CUs with four live rows end after those with three.  Loss and
+// gradient of 2048 x 128256, an eighth of weight 0, with 8 lists 243 us (0.99
+// GB, 4.1 TB/s; vector units 53% busy): half of each row is read twice.
+// Gradient of 1000 x 32003 fp32 with 16 lists of 100 in 84 us (66 of inputs in
+// the last-level cache): its lists, read before the row, cost about 30, which
+// the two workgroups that 62 KB of lists leave a CU do not hide.
 template <typename T, int THREADS, bool LOSS, int FROM, int KEEP>
 __global__ __launch_bounds__(THREADS, KEEP ? 4 : 1) void distill_kernel(DistillArgs p, int grad_pieces, int64_t len, int stat_pieces)
 {

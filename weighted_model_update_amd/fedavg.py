@@ -759,6 +759,10 @@ def topk_count(N, frac):
 
 
 # ------------------------------------------------------------------ linear layer
+#
+# The calls below are operators and their gradients as calls of their own: they
+# record no autograd graph, so what they return carries no gradient function
+# even where an input requires a gradient.
 
 _ACTS = {"none": FA_ACT_NONE, None: FA_ACT_NONE, "relu": FA_ACT_RELU, "gelu": FA_ACT_GELU, "silu": FA_ACT_SILU}
 
@@ -875,8 +879,8 @@ def linear_forward(x, w, bias=None, act="none", residual=None, alpha=1.0, out=No
     residual [M, N]: float32 or bfloat16 GPU tensors of one dtype with unit
     stride along their rows.  out [M, N] (may be the residual) is made when
     None; preact [M, N], when given, receives the value before the activation,
-    which linear_backward takes.  Returns out.  See linear_forward in
-    include/fedavg.h."""
+    which linear_backward takes.  Returns out, outside autograd.  See
+    linear_forward in include/fedavg.h."""
     lib = load()
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w must be matrices")
@@ -1017,8 +1021,8 @@ def distill_loss(z, idx, val, n, tau=1.0, teacher_lse=None, row_weight=None, los
     float32 [R] normalisers, or None to renormalise each list.  row_weight:
     float32 [R], 0 for rows to leave out.  loss and lse (float32 [R]) are made
     when None; dz: a tensor [R, V] to fill (z itself is allowed), True to make
-    one, None for the loss alone.  Returns (loss, lse, dz).  See distill_loss
-    in include/fedavg.h."""
+    one, None for the loss alone.  Returns (loss, lse, dz), outside autograd.
+    See distill_loss in include/fedavg.h."""
     lib = load()
     if z.dim() != 2:
         raise ValueError("z must be a matrix [R, V]")

@@ -29,7 +29,7 @@ def seconds(x, k):
 def test_time_of_the_largest_k(dt, V):
     g = torch.Generator(device="cuda").manual_seed(V)
     x = torch.randn(4096, V, generator=g, device="cuda").to(dt)
-    assert seconds(x, fa.FA_MAX_TOP) < 5 * seconds(x, 128)
+    assert seconds(x, fa.FA_MAX_TOP) < 5.5 * seconds(x, 128)
 
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32], ids=str)

@@ -155,3 +155,23 @@ def test_loss_at_temperatures_whose_square_is_below_fp32(tau):
     z = rnd((R, V), 5, 2.5)
     idx, val = lists_of(R, V, (1,), 9)
     check_loss(z, idx, val, [1], tau)
+
+
+@pytest.mark.parametrize("tau", [0.5, 1e-3])
+def test_loss_of_listed_logits_under_the_lowest_value_at_small_temperatures(tau):
+    # log p is about 1e38 / tau, the loss tau^2 times that
+    z = rnd((2, 400), 5, 2.5)
+    z[:, 200:] = torch.finfo(torch.float32).min
+    idx, val = lists_of(2, 400, (30,), 9)
+    val = [v * tau for v in val]
+    check_loss(z, idx, val, [1], tau)
+
+
+def test_loss_of_listed_logits_all_under_the_lowest_value():
+    # each client's mass times 3.4e38, of which tau and the shares leave less
+    z = rnd((64, 40), 5, 2.5)
+    z[:, 8:] = torch.finfo(torch.float32).min
+    idx, val = lists_of(64, 40, (9, 6, 12), 3)
+    idx = [torch.stack([8 + torch.randperm(32, generator=torch.Generator().manual_seed(r))[:i.shape[1]].sort().values
+                        for r in range(64)]).int() for i in idx]
+    check_loss(z, idx, val, [3, 4, 5], 0.5)

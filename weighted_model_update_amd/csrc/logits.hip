@@ -819,7 +819,7 @@ constexpr int64_t DI_SMALL_BYTES = 16384; // rows up to this take the small work
 struct Lists {
     int *len;     // [clients] entries in use; 0: the client did not send the row
     float *mass;  // [clients] sum_j q_cj
-    float *kl;    // [clients] sum_j q_cj log q_cj, then less sum_j q_cj (z_j - max z) / tau
+    float *kl;    // [clients] sum_j q_cj log q_cj; from finish_kl on tau / 4 sum_j q_cj (log q_cj - log p_j)
     float *share; // [clients] n_c over the sum of n of the clients that sent the row
     float *q;     // [entries]
     float *z;     // [entries] the listed logits, for the loss
@@ -1003,19 +1003,23 @@ __device__ __forceinline__ void load_lists(const DistillArgs &p, int64_t r, cons
     __syncthreads();
 }
 
-// l.kl, less sum_j q_cj (z_j - top) / tau with the row's maximum `top`: taken off
-// first, so that a sum of log q - log p holds whatever the row's offset is.  Each
-// lane has the entries that it stored.
-template <int THREADS> __device__ __forceinline__ void finish_kl(const DistillArgs &p, float top, Lists &l)
+// l.kl = tau / 4 sum_j q_cj (log q_cj - log p_j) with the row's maximum and sum t:
+//     tau log p_j = (z_j - max) - tau log s,
+// where the maximum is taken off first, so that the difference holds whatever
+// the row's offset is, and not divided by tau, which might pass fp32 where its
+// product with tau does not; as neither does a quarter of the type's lowest
+// value.  Each lane has the entries that it stored.
+template <int THREADS> __device__ __forceinline__ void finish_kl(const DistillArgs &p, const Softmax &t, Lists &l)
 {
     const int lane = threadIdx.x % WAVE;
+    const float log_s = logf(t.s);
     for (int c = threadIdx.x / WAVE; c < p.clients; c += THREADS / WAVE) {
         float s = 0.f;
         for (int j = p.first[c] + lane; j < p.first[c] + l.len[c]; j += WAVE)
-            s += l.q[j] != 0.f ? l.q[j] * ((l.z[j] - top) * p.inv_tau) : 0.f;
+            s += l.q[j] != 0.f ? l.q[j] * (0.25f * l.z[j] - 0.25f * t.m) : 0.f;
         s = wave_sum(s);
         if (lane == 0)
-            l.kl[c] -= s;
+            l.kl[c] = __builtin_fmaf(0.25f * p.tau, __builtin_fmaf(log_s, l.mass[c], l.kl[c]), -s);
     }
     __syncthreads();
 }
@@ -1105,20 +1109,19 @@ __global__ __launch_bounds__(THREADS, KEEP ? 4 : 1) void distill_kernel(DistillA
             if (FROM != LSE_GIVEN)
                 lse = lse_of(t.m, t.s, p.inv_tau);
             if (LOSS)
-                finish_kl<THREADS>(p, t.m, l);
-            const float log_s = LOSS ? logf(t.s) : 0.f;
+                finish_kl<THREADS>(p, t, l);
             if (stored || t.m != NEG_INF || t.s != 0.f) // anything but -inf in the row
                 for (int c = 0; c < p.clients; c++)
                     if (l.len[c]) {
                         M = __builtin_fmaf(l.share[c], l.mass[c], M);
                         if (LOSS)
-                            kl = __builtin_fmaf(l.share[c], __builtin_fmaf(log_s, l.mass[c], l.kl[c]), kl);
+                            kl = __builtin_fmaf(l.share[c], l.kl[c], kl);
                         sent = true;
                     }
         }
         if (LOSS && first && threadIdx.x == 0) {
-            // not tau^2, which fp32 does not hold where tau * kl is a number
-            p.loss[r] = sent ? g * p.tau * (p.tau * kl) : 0.f;
+            // kl is tau / 4 times it: tau^2 may pass fp32 where tau kl does not
+            p.loss[r] = sent ? g * p.tau * kl * 4.f : 0.f;
             if (p.lse)
                 p.lse[r] = lse;
         }

@@ -1056,7 +1056,7 @@ enum { LSE_COMPUTE = 0, LSE_PIECES = 1, LSE_GIVEN = 2 };
 // bf16, an eighth of them of weight 0, one list a row, 60 us (272 MB, 4.5 TB/s;
 // 53 of inputs that the last-level cache holds in part): all rows are resident
 // at once, and CUs with four live rows end after those with three.  Loss and
-// gradient of 2048 x 128256, an eighth of weight 0, with 8 lists 243 us (0.99
+// gradient of 2048 x 128256, an eighth of weight 0, with 8 lists 244 us (0.99
 // GB, 4.1 TB/s; vector units 53% busy): half of each row is read twice.
 // Gradient of 1000 x 32003 fp32 with 16 lists of 100 in 84 us (66 of inputs in
 // the last-level cache): its lists, read before the row, cost about 30, which

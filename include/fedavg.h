@@ -578,6 +578,67 @@ int linear_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void 
                     void *db, void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Frozen layers on 8-bit weights, beside the adapters: the server sends the
+ * backbone's matrices as 8-bit integers with a scale for each row (output
+ * channel), and clients run them on tokens in 8 bits with a scale each.
+ *
+ * quantize_rows -- a matrix x [R][C] of dtype as q (int8 [R][C]) and
+ * scale (float[R]):
+ *     scale[r] = max_c |x[r][c]| / 127        (fp32 division)
+ *     q[r][c]  = x[r][c] / scale[r], rounded to fp32, then to the nearest whole
+ *                number (ties to even), kept within -127 .. 127
+ * so x[r][c] ~ q[r][c] scale[r].  A row of zeros, or one so small that its
+ * scale is 0 in fp32, has scale 0 and q 0.  A row that holds NaN or an infinity
+ * has scale NaN and q 0: what is formed from it is NaN.  C == 0 gives scale 0.
+ * R, C and R*C at most 2^36 (FA_ERR_RANGE).  x, q and scale must not overlap
+ * (FA_ERR_ARG).  Pointers need only the element's alignment.
+ */
+int quantize_rows(const void *x, fa_dtype dtype, int64_t R, int64_t C, int64_t ldx, int8_t *q,
+                  int64_t ldq, float *scale, void *stream);
+
+/* Device workspace bytes linear_int8_forward (backward == 0; quantized: x comes
+   in 8 bits) or linear_int8_backward (backward != 0) needs for these sizes on
+   the current device; may be 0. */
+int linear_int8_workspace_size(fa_dtype dtype, int64_t M, int64_t N, int64_t K, int quantized,
+                               int backward, size_t *bytes);
+
+/*
+ * linear_int8_forward -- linear_forward on 8-bit operands:
+ *     z = alpha * x_scale[m] * w_scale[n] * sum_k x[m][k] w[n][k] + bias[n]
+ *     out = act(z) + residual
+ * w          int8 [N][K] (any value), w_scale float[N]: quantize_rows of the weights.
+ * x          with x_scale (float[M]) int8 [M][K]; without (NULL) a matrix of
+ *            dtype, which the call brings to 8 bits as quantize_rows does.
+ * bias, residual, out, preact   of dtype, as for linear_forward.
+ * The sum over k is exact (32-bit whole numbers); it is rounded to fp32 and
+ * multiplied by x_scale, then w_scale, then alpha with the bias, in fp32.  A NaN
+ * scale makes its row or column NaN.
+ * K <= 2^17 - 1, so that the sums fit; otherwise linear_forward's limits.
+ * Aliasing as for linear_forward: out may be the residual.
+ */
+int linear_int8_forward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void *x, int64_t ldx,
+                        const float *x_scale, const int8_t *w, int64_t ldw, const float *w_scale,
+                        const void *bias, fa_act act, float alpha, const void *residual, int64_t ldr,
+                        void *out, int64_t ldo, void *preact, int64_t ldp, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/*
+ * linear_int8_backward -- the frozen layer's input gradient from dy, the
+ * gradient of out, and its bias's:
+ *     dz = dy * act'(preact),  dx = alpha * (dz * w_scale) w,  db = column sums of dz.
+ * The rounding of x to 8 bits counts as the identity; the weights have no
+ * gradient.  dx [M][K] and db (N values) are each nullable; w and w_scale are
+ * needed for dx, preact for an activation.  dz * w_scale is held in dtype for
+ * the product; db sums dz unrounded.  M == 0 gives zero db, N == 0 zero dx.
+ * Outputs must not overlap the inputs or each other, nor the workspace anything
+ * else (FA_ERR_ARG).
+ */
+int linear_int8_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void *dy, int64_t lddy,
+                         const int8_t *w, int64_t ldw, const float *w_scale, fa_act act, float alpha,
+                         const void *preact, int64_t ldp, void *dx, int64_t lddx, void *db,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
  * Exchange of distilled knowledge: clients send the top logits of each public
  * token instead of weights (FLARE page, section on what a federation may
  * exchange: model weights, adapters or distilled knowledge), and the server

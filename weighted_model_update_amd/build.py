@@ -11,10 +11,12 @@ LIB_PATH = os.path.join(HERE, "libfedavg.so")
 SOURCES = [os.path.join(HERE, "csrc", "fedavg_kernels.hip"),
            os.path.join(HERE, "csrc", "topk.hip"),
            os.path.join(HERE, "csrc", "linear.hip"),
+           os.path.join(HERE, "csrc", "int8.hip"),
            os.path.join(HERE, "csrc", "logits.hip"),
            os.path.join(HERE, "csrc", "fedavg_api.hip")]
 HEADERS = [os.path.join(HERE, "csrc", "fedavg_internal.h"),
            os.path.join(HERE, "csrc", "learn_internal.h"),
+           os.path.join(HERE, "csrc", "tiles.h"),
            os.path.join(HERE, "csrc", "device_once.h"),
            os.path.join(ROOT, "include", "fedavg.h")]
 

@@ -1774,6 +1774,245 @@ int linear_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void 
     return e == hipSuccess ? ok() : hip_fail(e, "join of the gradients launch");
 }
 
+// ============================================================ layers on 8-bit weights
+
+namespace {
+
+constexpr int64_t INT8_MAX_K = (1ll << 17) - 1; // 2^17 - 1 products of up to 2^14 stay below 2^31
+constexpr int64_t QUANTIZE_MAX_ROWS = 1ll << 36;
+
+int check_linear_int8(int dtype, int64_t M, int64_t N, int64_t K, int act)
+{
+    const int rc = check_linear(dtype, M, N, K, act);
+    if (rc == FA_OK && K > INT8_MAX_K)
+        return fail(FA_ERR_RANGE, "K must be at most 2^17 - 1");
+    return rc;
+}
+
+View vector_view(const void *p, int64_t n, size_t es) { return {p, p ? 1 : 0, n, n, es}; }
+
+// A vector that has to be there.
+int check_vector(const char *name, const View &v)
+{
+    return v.cols > 0 && !v.p ? fail(FA_ERR_ARG, "%s is required", name) : check_view(name, v, false);
+}
+
+// linear_int8_forward's workspace: x in 8 bits with its scales, where the call
+// makes them, and the product's partial sums.
+struct Int8Forward {
+    size_t q, scale, part;
+    size_t total() const { return q + scale + part; }
+};
+
+int64_t q_pitch(int64_t K) { return (K + 15) & ~15ll; }
+
+Int8Forward int8_forward_plan(int64_t M, int64_t N, int64_t K, bool quantized)
+{
+    return {quantized ? 0 : round256((size_t)M * q_pitch(K)), quantized ? 0 : round256((size_t)M * sizeof(float)),
+            fa::gemm8_workspace_bytes(M, N, K, cu_count())};
+}
+
+// linear_int8_backward's workspace: dz times the channels' scales, the column
+// sums' partials, the weights as values, and the product's partial sums.
+struct Int8Backward {
+    size_t dz, part, w, dx;
+    size_t total() const { return dz + part + w + dx; }
+};
+
+Int8Backward int8_backward_plan(int dtype, int64_t M, int64_t N, int64_t K)
+{
+    const int cus = cu_count();
+    return {round256((size_t)M * dz_pitch(N) * dsize(dtype)),
+            round256((size_t)fa::act_grad_partials(M, N, cus) * N * sizeof(float)),
+            round256((size_t)N * dz_pitch(K) * dsize(dtype)),
+            fa::gemm_workspace_bytes(dtype, M, K, N, fa::GEMM_B_OUTER, cus)};
+}
+
+} // namespace
+
+int quantize_rows(const void *x, fa_dtype dtype, int64_t R, int64_t C, int64_t ldx, int8_t *q, int64_t ldq,
+                  float *scale, void *stream)
+{
+    if (!dtype_ok(dtype))
+        return fail(FA_ERR_DTYPE, "dtype must be FA_F32 or FA_BF16");
+    if (R < 0 || C < 0)
+        return fail(FA_ERR_ARG, "R and C must be >= 0");
+    if (R > QUANTIZE_MAX_ROWS || C > QUANTIZE_MAX_ROWS || (C > 0 && R > QUANTIZE_MAX_ROWS / C))
+        return fail(FA_ERR_RANGE, "R, C and R * C must be at most 2^36");
+    if (R == 0)
+        return ok();
+    const View vx{x, R, C, ldx, dsize(dtype)}, vq{q, R, C, ldq, 1}, vs = vector_view(scale, R, sizeof(float));
+    int rc;
+    if ((rc = check_view("x", vx, false)) != FA_OK || (rc = check_view("q", vq, true)) != FA_OK ||
+        (rc = check_vector("scale", vs)) != FA_OK)
+        return rc;
+    if (views_overlap(vx, vq) || views_overlap(vx, vs) || views_overlap(vq, vs))
+        return fail(FA_ERR_ARG, "x, q and scale must not overlap");
+    const fa::QuantizeArgs a{x, R, C, ldx, q, ldq, C, scale};
+    const hipError_t e = fa::launch_quantize(a, dtype, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, "quantize launch");
+}
+
+int linear_int8_workspace_size(fa_dtype dtype, int64_t M, int64_t N, int64_t K, int quantized, int backward,
+                               size_t *bytes)
+{
+    if (!bytes)
+        return fail(FA_ERR_ARG, "need a result pointer");
+    const int rc = check_linear_int8(dtype, M, N, K, FA_ACT_NONE);
+    if (rc != FA_OK)
+        return rc;
+    *bytes = backward ? int8_backward_plan(dtype, M, N, K).total() : int8_forward_plan(M, N, K, quantized != 0).total();
+    return ok();
+}
+
+int linear_int8_forward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void *x, int64_t ldx,
+                        const float *x_scale, const int8_t *w, int64_t ldw, const float *w_scale, const void *bias,
+                        fa_act act, float alpha, const void *residual, int64_t ldr, void *out, int64_t ldo,
+                        void *preact, int64_t ldp, void *workspace, size_t workspace_bytes, void *stream)
+{
+    int rc = check_linear_int8(dtype, M, N, K, act);
+    if (rc != FA_OK)
+        return rc;
+    if (M == 0 || N == 0)
+        return ok();
+    const size_t es = dsize(dtype);
+    const bool quantized = x_scale != nullptr;
+    const View vx{x, M, K, ldx, quantized ? 1 : es}, vxs = vector_view(x_scale, M, sizeof(float)), vw{w, N, K, ldw, 1},
+        vws = vector_view(w_scale, N, sizeof(float)), vb = vector_view(bias, N, es), vr{residual, residual ? M : 0, N, ldr, es},
+        vo{out, M, N, ldo, es}, vp{preact, preact ? M : 0, N, ldp, es};
+    const View vs{workspace, workspace ? 1 : 0, (int64_t)workspace_bytes, 0, 1};
+    if ((rc = check_view("x", vx, false)) != FA_OK || (rc = check_view("x_scale", vxs, false)) != FA_OK ||
+        (rc = check_view("w", vw, false)) != FA_OK || (rc = check_vector("w_scale", vws)) != FA_OK ||
+        (rc = check_view("bias", vb, false)) != FA_OK || (rc = check_view("residual", vr, false)) != FA_OK ||
+        (rc = check_view("out", vo, true)) != FA_OK || (rc = check_view("preact", vp, true)) != FA_OK)
+        return rc;
+    for (const View &o : {vo, vp})
+        for (const View &i : {vx, vxs, vw, vws, vb, vs})
+            if (views_overlap(o, i))
+                return fail(FA_ERR_ARG, "out and preact must not overlap the inputs or the workspace");
+    for (const View &i : {vx, vxs, vw, vws, vb, vr})
+        if (views_overlap(vs, i))
+            return fail(FA_ERR_ARG, "the workspace must not overlap the inputs");
+    if (views_overlap(vo, vp) || views_overlap(vp, vr) || (views_overlap(vo, vr) && !same_view(vo, vr)))
+        return fail(FA_ERR_ARG, "out and preact must not overlap each other or, but for out being the "
+                                "residual itself, the residual");
+    const Int8Forward plan = int8_forward_plan(M, N, K, quantized);
+    if ((rc = check_workspace(workspace, workspace_bytes, plan.total())) != FA_OK)
+        return rc;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    fa::GemmArgs a{};
+    a.a = x;
+    a.lda = ldx;
+    a.row_scale = x_scale;
+    if (!quantized) {
+        float *scale = reinterpret_cast<float *>(ws + plan.q);
+        const fa::QuantizeArgs g{x, M, K, ldx, reinterpret_cast<int8_t *>(ws), q_pitch(K), q_pitch(K), scale};
+        const hipError_t e = fa::launch_quantize(g, dtype, s);
+        if (e != hipSuccess)
+            return hip_fail(e, "quantize launch");
+        a.a = ws;
+        a.lda = q_pitch(K);
+        a.a_padded = true;
+        a.row_scale = scale;
+    }
+    a.b = w;
+    a.ldb = ldw;
+    a.col_scale = w_scale;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.alpha = alpha;
+    a.bias = bias;
+    a.res = residual;
+    a.ldr = ldr;
+    a.out = out;
+    a.ldo = ldo;
+    a.pre = preact;
+    a.ldp = ldp;
+    a.act = act;
+    const hipError_t e = fa::launch_gemm8(a, dtype, ws + plan.q + plan.scale, cu_count(), s);
+    return e == hipSuccess ? ok() : hip_fail(e, "8-bit product launch");
+}
+
+int linear_int8_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const void *dy, int64_t lddy,
+                         const int8_t *w, int64_t ldw, const float *w_scale, fa_act act, float alpha,
+                         const void *preact, int64_t ldp, void *dx, int64_t lddx, void *db, void *workspace,
+                         size_t workspace_bytes, void *stream)
+{
+    int rc = check_linear_int8(dtype, M, N, K, act);
+    if (rc != FA_OK)
+        return rc;
+    if (!dx && !db)
+        return ok();
+    const size_t es = dsize(dtype);
+    const bool has_act = act != FA_ACT_NONE;
+    const View vy{dy, M, N, lddy, es}, vw{w, dx ? N : 0, K, ldw, 1},
+        vws{w_scale, dx ? 1 : 0, N, N, sizeof(float)}, vp{preact, has_act ? M : 0, N, ldp, es},
+        vdx{dx, dx ? M : 0, K, lddx, es}, vdb = vector_view(db, N, es);
+    const View vs{workspace, workspace ? 1 : 0, (int64_t)workspace_bytes, 0, 1};
+    if ((rc = check_view("dy", vy, false)) != FA_OK || (rc = check_view("w", vw, false)) != FA_OK ||
+        (rc = check_view("w_scale", vws, false)) != FA_OK || (rc = check_view("preact", vp, false)) != FA_OK ||
+        (rc = check_view("dx", vdx, true)) != FA_OK || (rc = check_view("db", vdb, true)) != FA_OK)
+        return rc;
+    for (const View &o : {vdx, vdb})
+        for (const View &i : {vy, vw, vws, vp, vs})
+            if (views_overlap(o, i))
+                return fail(FA_ERR_ARG, "dx and db must not overlap the inputs or the workspace");
+    for (const View &i : {vy, vw, vws, vp})
+        if (views_overlap(vs, i))
+            return fail(FA_ERR_ARG, "the workspace must not overlap the inputs");
+    if (views_overlap(vdx, vdb))
+        return fail(FA_ERR_ARG, "dx and db must not overlap each other");
+    const Int8Backward plan = int8_backward_plan(dtype, M, N, K);
+    if ((rc = check_workspace(workspace, workspace_bytes, plan.total())) != FA_OK)
+        return rc;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    const int cus = cu_count();
+    fa::Finish f{};
+    fa::ActGradArgs g{};
+    g.dy = dy;
+    g.lddy = lddy;
+    g.pre = preact;
+    g.ldp = ldp;
+    g.dz = dx ? ws : nullptr;
+    g.lddz = dz_pitch(N);
+    g.db = db;
+    g.part = reinterpret_cast<float *>(ws + plan.dz);
+    g.M = M;
+    g.N = N;
+    g.act = act;
+    g.col_scale = dx ? w_scale : nullptr;
+    hipError_t e = fa::launch_act_grad(g, dtype, cus, f, s);
+    if (e != hipSuccess)
+        return hip_fail(e, "activation gradient launch");
+    if (dx) {
+        char *values = ws + plan.dz + plan.part;
+        e = fa::launch_widen(w, ldw, N, K, dtype, values, dz_pitch(K), s);
+        if (e != hipSuccess)
+            return hip_fail(e, "weights as values launch");
+        fa::GemmArgs a{};
+        a.a = ws;
+        a.lda = dz_pitch(N);
+        a.a_padded = true;
+        a.b = values;
+        a.ldb = dz_pitch(K);
+        a.b_padded = true;
+        a.M = (int)M;
+        a.N = (int)K;
+        a.K = (int)N;
+        a.alpha = alpha;
+        a.out = dx;
+        a.ldo = lddx;
+        e = fa::launch_gemm(a, dtype, fa::GEMM_B_OUTER, values + plan.w, cus, f, s);
+        if (e != hipSuccess)
+            return hip_fail(e, "input gradient launch");
+    }
+    e = fa::launch_finish(f, dtype, s);
+    return e == hipSuccess ? ok() : hip_fail(e, "join of the gradients launch");
+}
+
 // ============================================================ top logits of rows, distillation
 
 namespace {

@@ -1,0 +1,392 @@
+// Layers on 8-bit weights: rows of a matrix as 8-bit integers with a scale each,
+// the products of such rows, and the weights as values for the input gradient.
+//
+// A row r is held as q(r,c) = rint(x(r,c) / s(r)), s(r) = max |x(r,.)| / 127, so
+//     x w^T (m,n)  ~  sx(m) sw(n) sum_k xq(m,k) wq(n,k),
+// a sum of whole numbers that the matrix cores form exactly (16x16x64); the
+// scales come once per result, in the epilogue.
+#include "tiles.h"
+
+#include <algorithm>
+
+namespace fa {
+namespace {
+
+// ------------------------------------------------------------ rows to 8 bits
+// Bound by memory.  A group of threads holds its row in registers between the
+// maximum and the quotients, QR_W values a thread at a time; what does not fit
+// is read again.
+constexpr int QR_THREADS = 256, QR_W = 16, QR_HELD = 4;
+
+__device__ __forceinline__ float quotient(float x, float scale)
+{
+    const float q = __builtin_rintf(x / scale); // to even, as the division is IEEE's
+    return fminf(fmaxf(q, -127.f), 127.f);
+}
+
+// ACROSS threads take a row.  `fill`: columns up to which zeros follow the row.
+template <typename T, int ACROSS>
+__global__ __launch_bounds__(QR_THREADS) void quantize_kernel(const T *x, int64_t ldx, int64_t R, int64_t C, int8_t *q,
+                                                              int64_t ldq, int64_t fill, float *scale)
+{
+    constexpr int ROWS = QR_THREADS / ACROSS;
+    __shared__ float tops[2][QR_THREADS / WAVE];
+    const int t = threadIdx.x % ACROSS;
+    int turn = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < R; r0 += (int64_t)gridDim.x * ROWS, turn ^= 1) {
+        const int64_t r = r0 + threadIdx.x / ACROSS;
+        const int64_t cols = r < R ? C : 0;
+        const T *row = x + (r < R ? r : 0) * ldx;
+        Raw<T, QR_W> held[QR_HELD];
+        float top = 0.f;
+        bool odd = false; // NaN or an infinity in the row
+        const auto look = [&](const Raw<T, QR_W> &v) {
+#pragma unroll
+            for (int i = 0; i < QR_W; i++) {
+                const float a = fabsf((float)v.e[i]);
+                odd |= !(a < INFINITY);
+                top = fmaxf(top, a);
+            }
+        };
+#pragma unroll
+        for (int h = 0; h < QR_HELD; h++) {
+            const int64_t c = ((int64_t)h * ACROSS + t) * QR_W, left = cols - c;
+            held[h].fetch(row + c, (int)(left < 0 ? 0 : left < QR_W ? left : QR_W));
+        }
+#pragma unroll
+        for (int h = 0; h < QR_HELD; h++)
+            look(held[h]);
+        for (int64_t c = ((int64_t)QR_HELD * ACROSS + t) * QR_W; c < cols; c += ACROSS * QR_W) {
+            Raw<T, QR_W> v;
+            v.fetch(row + c, (int)(cols - c < QR_W ? cols - c : QR_W));
+            look(v);
+        }
+        top = odd ? INFINITY : top;
+#pragma unroll
+        for (int d = 1; d < (ACROSS < WAVE ? ACROSS : WAVE); d *= 2)
+            top = fmaxf(top, __shfl_xor(top, d));
+        if constexpr (ACROSS > WAVE) {
+            if (threadIdx.x % WAVE == 0)
+                tops[turn][threadIdx.x / WAVE] = top;
+            __syncthreads();
+            top = tops[turn][0];
+#pragma unroll
+            for (int w = 1; w < ACROSS / WAVE; w++)
+                top = fmaxf(top, tops[turn][w]);
+        }
+        const bool flawed = !(top < INFINITY);
+        const float s = flawed ? __builtin_nanf("") : top / 127.f;
+        if (t == 0 && r < R)
+            scale[r] = s;
+        const bool live = s > 0.f;
+        const auto put = [&](int64_t c, const Raw<T, QR_W> &v) {
+            const int64_t end = r < R ? fill : 0;
+            if (c >= end)
+                return;
+            int8_t b[QR_W];
+#pragma unroll
+            for (int i = 0; i < QR_W; i++)
+                b[i] = live ? (int8_t)(int)quotient((float)v.e[i], s) : (int8_t)0;
+            if (end - c >= QR_W) {
+                __builtin_memcpy(q + r * ldq + c, b, QR_W);
+            } else {
+#pragma unroll
+                for (int i = 0; i < QR_W; i++)
+                    if (i < end - c)
+                        q[r * ldq + c + i] = b[i];
+            }
+        };
+#pragma unroll
+        for (int h = 0; h < QR_HELD; h++)
+            put(((int64_t)h * ACROSS + t) * QR_W, held[h]);
+        for (int64_t c = ((int64_t)QR_HELD * ACROSS + t) * QR_W; c < fill; c += ACROSS * QR_W) {
+            Raw<T, QR_W> v;
+            const int64_t left = cols - c;
+            v.fetch(row + c, (int)(left < 0 ? 0 : left < QR_W ? left : QR_W));
+            put(c, v);
+        }
+    }
+}
+
+// ------------------------------------------------------------ products
+// Workgroup (tile, split), as for the other products; partial sums are whole
+// numbers too, so a split changes no result.
+template <typename O, int BM, int BN, int WM, int WN, bool DIRECT>
+__global__ __launch_bounds__(WM *WN *WAVE) void gemm8_kernel(GemmArgs p, int tiles_m, int tiles_n, int kper, float *part)
+{
+    typedef int8_t T;
+    constexpr int THREADS = WM * WN * WAVE, BK = STEP_BYTES;
+    constexpr int AB = BM * STEP_BYTES, BB = BN * STEP_BYTES;
+    __shared__ __attribute__((aligned(1024))) char l0[AB + BB];
+    __shared__ __attribute__((aligned(1024))) char l1[AB + BB];
+
+    unsigned tm, tn;
+    tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    const int m0 = (int)tm * BM, n0 = (int)tn * BN;
+    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
+    const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
+    const T *a = static_cast<const T *>(p.a), *b = static_cast<const T *>(p.b);
+    const int k0 = blockIdx.y * kper, kend = p.K - k0 < kper ? p.K : k0 + kper;
+    const int steps = (kend - k0 + BK - 1) / BK;
+    Tile<T, BM, BN, WM, WN, false, false> t;
+    t.clear();
+    if constexpr (DIRECT) {
+        Direct<T, false, BM, THREADS, STEP_BYTES> da;
+        Direct<T, false, BN, THREADS, STEP_BYTES> db;
+        da.init(a, p.lda, m0, p.M, k0);
+        db.init(b, p.ldb, n0, p.N, k0);
+        t.run(l0, l1, steps, wm, wn, lane, [&](char *l, int s) {
+            da.start(l, kend - k0 - s * BK);
+            db.start(l + AB, kend - k0 - s * BK);
+        });
+    } else {
+        Stage<T, false, BM, THREADS> sa;
+        Stage<T, false, BN, THREADS> sb;
+        if (steps > 0) {
+            sa.load(a, p.lda, m0, p.M, k0, kend);
+            sb.load(b, p.ldb, n0, p.N, k0, kend);
+            sa.store(l0);
+            sb.store(l0 + AB);
+        }
+        __syncthreads();
+        for (int s = 0; s < steps; s++) {
+            char *cur = s & 1 ? l1 : l0, *next = s & 1 ? l0 : l1;
+            if (s + 1 < steps) {
+                sa.load(a, p.lda, m0, p.M, k0 + (s + 1) * BK, kend);
+                sb.load(b, p.ldb, n0, p.N, k0 + (s + 1) * BK, kend);
+            }
+            t.step(cur, cur + AB, wm, wn, lane);
+            if (s + 1 < steps) {
+                sa.store(next);
+                sb.store(next + AB);
+            }
+            __syncthreads();
+        }
+    }
+    write_tile<O, BM, BN, WM, WN, AB + BB>(p, m0, n0, t.acc, l0, l1, part);
+}
+
+template <typename O, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM *WN *WAVE) void pipe8_kernel(GemmArgs p, int tiles_m, int tiles_n)
+{
+    typedef int8_t T;
+    constexpr int THREADS = WM * WN * WAVE, BK = PIPE_STEP;
+    constexpr int AB = BM * PIPE_STEP, BB = BN * PIPE_STEP;
+    __shared__ __attribute__((aligned(1024))) char l0[AB + BB];
+    __shared__ __attribute__((aligned(1024))) char l1[AB + BB];
+    __shared__ __attribute__((aligned(1024))) char l2[AB + BB];
+    __shared__ __attribute__((aligned(1024))) char l3[AB + BB];
+
+    unsigned tm, tn;
+    tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    const int m0 = (int)tm * BM, n0 = (int)tn * BN;
+    Pipe<T, BM, BN, WM, WN, false, false> t;
+    Direct<T, false, BM, THREADS, PIPE_STEP> da;
+    Direct<T, false, BN, THREADS, PIPE_STEP> db;
+    da.init(static_cast<const T *>(p.a), p.lda, m0, p.M, 0);
+    db.init(static_cast<const T *>(p.b), p.ldb, n0, p.N, 0);
+    int left = p.K; // of the next step to copy; steps past the end copy zeros
+    t.run(l0, l1, l2, l3, (p.K + BK - 1) / BK, [&](char *l) {
+        da.start(l, left);
+        db.start(l + AB, left);
+        left -= BK;
+    });
+    write_tile<O, BM, BN, WM, WN, AB + BB>(p, m0, n0, t.acc, l0, l1, nullptr);
+}
+
+// Joins the splits' sums, four neighbours a thread, and finishes them.
+constexpr int J8_THREADS = 256, J8_W = 4;
+
+template <typename O> __global__ __launch_bounds__(J8_THREADS) void join8_kernel(GemmArgs p, const int32_t *part, int splits)
+{
+    const int64_t groups = (p.N + J8_W - 1) / J8_W;
+    const int64_t at = (int64_t)blockIdx.x * J8_THREADS + threadIdx.x;
+    if (at >= p.M * groups)
+        return;
+    const int64_t m = at / groups;
+    const int n = (int)(at % groups) * J8_W, valid = p.N - n;
+    int32_t sum[J8_W] = {};
+#pragma unroll 4
+    for (int z = 0; z < splits; z++) {
+        Raw<int32_t, J8_W> v;
+        v.fetch(part + ((int64_t)z * p.M + m) * p.N + n, valid);
+#pragma unroll
+        for (int i = 0; i < J8_W; i++)
+            sum[i] += v.e[i];
+    }
+    Raw<float, J8_W> cs;
+    cs.fetch(p.col_scale + n, valid);
+    Raw<O, J8_W> bias, res;
+    fetch_bias(p, n, bias);
+    fetch_residual(p, m, n, res);
+    float v[J8_W];
+    scaled_sums<J8_W>(sum, p.row_scale[m], cs.e, v);
+    epilogue<O, J8_W>(p, m, n, v, bias, res);
+}
+
+// ------------------------------------------------------------ weights as values
+// The whole numbers of wq in T (exact), rows of `ldo` elements with zeros behind
+// the row; bound by memory.
+constexpr int WV_THREADS = 256, WV_W = 16;
+
+template <typename T>
+__global__ __launch_bounds__(WV_THREADS) void widen_kernel(const int8_t *w, int64_t ldw, int64_t rows, int64_t cols, T *out,
+                                                           int64_t ldo)
+{
+    const int64_t per = (ldo + WV_W - 1) / WV_W, step = (int64_t)gridDim.x * WV_THREADS;
+    for (int64_t at = (int64_t)blockIdx.x * WV_THREADS + threadIdx.x; at < rows * per; at += step) {
+        const int64_t r = at / per, c = at % per * WV_W, left = cols - c;
+        Raw<int8_t, WV_W> v;
+        v.fetch(w + r * ldw + c, (int)(left < 0 ? 0 : left < WV_W ? left : WV_W));
+        int32_t e[WV_W];
+#pragma unroll
+        for (int i = 0; i < WV_W; i++)
+            e[i] = v.e[i];
+        store_n<T, WV_W>(out + r * ldo + c, (int)(ldo - c < WV_W ? ldo - c : WV_W), e);
+    }
+}
+
+// ------------------------------------------------------------ launches
+
+int64_t tiles8(int64_t M, int64_t N, int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); }
+
+bool pitch_ok(int64_t bytes) { return bytes * 257 < (int64_t)OUT_OF_RANGE; }
+
+// Whether rows start on 16 bytes and end on a whole chunk, or in zeros up to one.
+bool direct_ok(const void *p, int64_t ld, int64_t row, bool padded)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 16 == 0 && (padded || row % 16 == 0) && pitch_ok(ld);
+}
+
+enum { P8_256_256, P8_256_128, P8_128_256, P8_128_128, T8_64, T8_THIN_N, T8_THIN_M };
+
+struct Plan8 {
+    int tile, splits;
+};
+
+int pipe8_for(int64_t M, int64_t N, int cus)
+{
+    static const int us[5] = {222, 140, 138, 155, 90};
+    const auto rounds = [&](int64_t t) { return (t + cus - 1) / cus; };
+    const int64_t t128 = tiles8(M, N, 128, 128), whole = t128 / (2 * cus), rest = t128 % (2 * cus);
+    const int64_t costs[4] = {us[0] * rounds(tiles8(M, N, 256, 256)), us[1] * rounds(tiles8(M, N, 256, 128)),
+                              us[2] * rounds(tiles8(M, N, 128, 256)),
+                              us[3] * whole + (rest > cus ? us[3] : rest > 0 ? us[4] : 0)};
+    return (int)(std::min_element(costs, costs + 4) - costs);
+}
+
+Plan8 plan8(int64_t M, int64_t N, int64_t K, int cus)
+{
+    const int64_t steps = K / STEP_BYTES;
+    const auto split = [&](int64_t count, int64_t want) {
+        return (int)std::max<int64_t>(1, std::min<int64_t>(std::min((want + count - 1) / count, steps / 4), 16));
+    };
+    if (N <= 16)
+        return {T8_THIN_N, split(std::max<int64_t>(1, tiles8(M, N, 128, 16)), 3 * cus / 2)};
+    if (M <= 16)
+        return {T8_THIN_M, split(std::max<int64_t>(1, tiles8(M, N, 16, 128)), 3 * cus / 2)};
+    if (tiles8(M, N, 128, 128) >= cus)
+        return {pipe8_for(M, N, cus), 1};
+    return {T8_64, split(std::max<int64_t>(1, tiles8(M, N, 64, 64)), cus)};
+}
+
+template <typename O, int BM, int BN, int WM, int WN>
+hipError_t run_tile8(const GemmArgs &a, bool direct, int splits, void *ws, hipStream_t s)
+{
+    const int64_t tm = ((int64_t)a.M + BM - 1) / BM, tn = ((int64_t)a.N + BN - 1) / BN;
+    const int steps = std::max(1, (a.K + STEP_BYTES - 1) / STEP_BYTES), per = (steps + splits - 1) / splits;
+    const int used = (steps + per - 1) / per;
+    float *part = used > 1 ? static_cast<float *>(ws) : nullptr;
+    const dim3 grid((unsigned)(tm * tn), (unsigned)used), block(WM * WN * WAVE);
+    if (direct)
+        gemm8_kernel<O, BM, BN, WM, WN, true><<<grid, block, 0, s>>>(a, (int)tm, (int)tn, per * STEP_BYTES, part);
+    else
+        gemm8_kernel<O, BM, BN, WM, WN, false><<<grid, block, 0, s>>>(a, (int)tm, (int)tn, per * STEP_BYTES, part);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && used > 1) {
+        const int64_t threads = (int64_t)a.M * ((a.N + J8_W - 1) / J8_W);
+        join8_kernel<O><<<(unsigned)((threads + J8_THREADS - 1) / J8_THREADS), J8_THREADS, 0, s>>>(
+            a, reinterpret_cast<const int32_t *>(part), used);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+template <typename O, int BM, int BN, int WM, int WN> hipError_t run_pipe8(const GemmArgs &a, hipStream_t s)
+{
+    const int64_t tm = ((int64_t)a.M + BM - 1) / BM, tn = ((int64_t)a.N + BN - 1) / BN;
+    pipe8_kernel<O, BM, BN, WM, WN><<<(unsigned)(tm * tn), WM * WN * WAVE, 0, s>>>(a, (int)tm, (int)tn);
+    return hipGetLastError();
+}
+
+template <typename O> hipError_t gemm8_of(const GemmArgs &a, void *ws, int cus, hipStream_t s)
+{
+    const Plan8 p = plan8(a.M, a.N, a.K, cus);
+    const bool direct = direct_ok(a.a, a.lda, a.K, a.a_padded) && direct_ok(a.b, a.ldb, a.K, false);
+    if (p.tile <= P8_128_128) {
+        if (!direct)
+            return run_tile8<O, 128, 128, 2, 2>(a, false, 1, ws, s);
+        if (p.tile == P8_256_256)
+            return run_pipe8<O, 256, 256, 2, 4>(a, s);
+        if (p.tile == P8_256_128)
+            return run_pipe8<O, 256, 128, 4, 2>(a, s);
+        if (p.tile == P8_128_256)
+            return run_pipe8<O, 128, 256, 2, 4>(a, s);
+        return run_pipe8<O, 128, 128, 2, 4>(a, s);
+    }
+    if (p.tile == T8_64)
+        return run_tile8<O, 64, 64, 2, 2>(a, direct, p.splits, ws, s);
+    if (p.tile == T8_THIN_N)
+        return run_tile8<O, 128, 16, 4, 1>(a, direct, p.splits, ws, s);
+    return run_tile8<O, 16, 128, 1, 4>(a, direct, p.splits, ws, s);
+}
+
+template <typename T> hipError_t quantize(const QuantizeArgs &a, hipStream_t s)
+{
+    const T *x = static_cast<const T *>(a.x);
+    const auto grid = [&](int64_t rows) { return (unsigned)std::min<int64_t>((a.R + rows - 1) / rows, 1 << 20); };
+    if (a.C <= 16 * QR_W * QR_HELD)
+        quantize_kernel<T, 16><<<grid(QR_THREADS / 16), QR_THREADS, 0, s>>>(x, a.ldx, a.R, a.C, a.q, a.ldq, a.fill, a.scale);
+    else if (a.C <= WAVE * QR_W * QR_HELD)
+        quantize_kernel<T, WAVE><<<grid(QR_THREADS / WAVE), QR_THREADS, 0, s>>>(x, a.ldx, a.R, a.C, a.q, a.ldq, a.fill, a.scale);
+    else
+        quantize_kernel<T, QR_THREADS><<<grid(1), QR_THREADS, 0, s>>>(x, a.ldx, a.R, a.C, a.q, a.ldq, a.fill, a.scale);
+    return hipGetLastError();
+}
+
+} // namespace
+
+hipError_t launch_quantize(const QuantizeArgs &a, int dt, hipStream_t s)
+{
+    if (a.R == 0)
+        return hipSuccess;
+    return dt == FA_BF16 ? quantize<__bf16>(a, s) : quantize<float>(a, s);
+}
+
+size_t gemm8_workspace_bytes(int64_t M, int64_t N, int64_t K, int cus)
+{
+    const Plan8 p = plan8(M, N, K, cus);
+    return p.splits > 1 ? ((size_t)p.splits * M * N * sizeof(int32_t) + 255) / 256 * 256 : 0;
+}
+
+hipError_t launch_gemm8(const GemmArgs &a, int dt, void *ws, int cus, hipStream_t s)
+{
+    if (a.M == 0 || a.N == 0)
+        return hipSuccess;
+    return dt == FA_BF16 ? gemm8_of<__bf16>(a, ws, cus, s) : gemm8_of<float>(a, ws, cus, s);
+}
+
+hipError_t launch_widen(const int8_t *w, int64_t ldw, int64_t rows, int64_t cols, int dt, void *out, int64_t ldo, hipStream_t s)
+{
+    if (rows == 0 || cols == 0)
+        return hipSuccess;
+    const int64_t chunks = rows * ((ldo + WV_W - 1) / WV_W);
+    const unsigned grid = (unsigned)std::min<int64_t>((chunks + WV_THREADS - 1) / WV_THREADS, 1 << 20);
+    if (dt == FA_BF16)
+        widen_kernel<__bf16><<<grid, WV_THREADS, 0, s>>>(w, ldw, rows, cols, static_cast<__bf16 *>(out), ldo);
+    else
+        widen_kernel<float><<<grid, WV_THREADS, 0, s>>>(w, ldw, rows, cols, static_cast<float *>(out), ldo);
+    return hipGetLastError();
+}
+
+} // namespace fa

@@ -1,6 +1,6 @@
 // Internal interface between the host library and the kernels of the linear
-// layer (linear.hip), the per-row top logits and the distillation loss
-// (logits.hip).  Not part of the public ABI.
+// layer (linear.hip), the layers on 8-bit weights (int8.hip), the per-row top
+// logits and the distillation loss (logits.hip).  Not part of the public ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -26,7 +26,9 @@ struct GemmArgs {
     void *pre; // [M][N], pitch ldp, nullable: the value before the activation
     int64_t ldp;
     int act;
-    bool a_padded; // A's rows are followed by zeros up to whole chunks
+    bool a_padded, b_padded; // rows are followed by zeros up to whole chunks
+    // 8-bit operands: M and N factors of the sums; null for the others
+    const float *row_scale, *col_scale;
 };
 
 enum { GEMM_A_OUTER = 1, GEMM_B_OUTER = 2 };
@@ -42,6 +44,7 @@ struct ActGradArgs {
     float *part;
     int64_t M, N;
     int act;
+    const float *col_scale; // N factors of the stored dz, nullable; not of db
 };
 int64_t act_grad_partials(int64_t M, int64_t N, int cus);
 
@@ -62,6 +65,25 @@ size_t gemm_workspace_bytes(int dt, int64_t M, int64_t N, int64_t K, int layout,
 hipError_t launch_gemm(const GemmArgs &a, int dt, int layout, void *ws, int cus, Finish &f, hipStream_t s);
 hipError_t launch_act_grad(const ActGradArgs &a, int dt, int cus, Finish &f, hipStream_t s);
 hipError_t launch_finish(const Finish &f, int dt, hipStream_t s);
+
+// ---------------------------------------------------------------- 8-bit layers
+struct QuantizeArgs {
+    const void *x;
+    int64_t R, C, ldx;
+    int8_t *q;
+    int64_t ldq, fill; // zeros follow the row up to column `fill` >= C
+    float *scale;
+};
+hipError_t launch_quantize(const QuantizeArgs &a, int dt, hipStream_t s);
+
+// As launch_gemm, for rows of 8-bit integers on both sides; dt is the type of
+// bias, residual and results.
+size_t gemm8_workspace_bytes(int64_t M, int64_t N, int64_t K, int cus);
+hipError_t launch_gemm8(const GemmArgs &a, int dt, void *ws, int cus, hipStream_t s);
+
+// out [rows][ldo] = w as values of dt, zeros from column `cols` on.
+hipError_t launch_widen(const int8_t *w, int64_t ldw, int64_t rows, int64_t cols, int dt, void *out, int64_t ldo,
+                        hipStream_t s);
 
 // ---------------------------------------------------------------- logits
 struct TopRowsArgs {

@@ -43,6 +43,7 @@ EXPORTS = [
     "fedavg_sum_workspace_size", "fedavg_checksum_sum", "sparse_masked_accumulate_noalloc",
     "fedavg_arena_layout",
     "linear_workspace_size", "linear_forward", "linear_backward",
+    "quantize_rows", "linear_int8_workspace_size", "linear_int8_forward", "linear_int8_backward",
     "logits_topk_workspace_size", "logits_topk",
     "distill_workspace_size", "distill_loss", "distill_backward",
 ]
@@ -104,6 +105,12 @@ def load(build_if_missing=True):
                             P, sz, P], i32),
         "linear_backward": ([i32, i64, i64, i64, P, i64, P, i64, P, i64, i32, ctypes.c_float, P, i64, P, i64,
                              P, i64, P, P, sz, P], i32),
+        "quantize_rows": ([P, i32, i64, i64, i64, P, i64, P, P], i32),
+        "linear_int8_workspace_size": ([i32, i64, i64, i64, i32, i32, P], i32),
+        "linear_int8_forward": ([i32, i64, i64, i64, P, i64, P, P, i64, P, P, i32, ctypes.c_float, P, i64, P, i64, P,
+                                 i64, P, sz, P], i32),
+        "linear_int8_backward": ([i32, i64, i64, i64, P, i64, P, i64, P, i32, ctypes.c_float, P, i64, P, i64, P, P, sz,
+                                  P], i32),
         "logits_topk_workspace_size": ([i32, i64, i64, i64, P], i32),
         "logits_topk": ([P, i32, i64, i64, i64, i64, ctypes.c_float, P, P, P, P, sz, P], i32),
         "distill_workspace_size": ([i32, i64, i64, P], i32),
@@ -929,6 +936,105 @@ def linear_backward(dy, x, w, act="none", preact=None, alpha=1.0, dx=True, dw=Tr
     if rc:
         _check(rc)
     return dx, dw, db
+
+
+# ------------------------------------------------------------------ layers on 8-bit weights
+
+def quantize_rows(x, q=None, scale=None, stream=None):
+    """(q, scale): the matrix x [R, C], float32 or bfloat16, as 8-bit integers
+    [R, C] with a float32 scale for each row.  q and scale are made when None.
+    See quantize_rows in include/fedavg.h."""
+    lib = load()
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    dt, code = x.dtype, _dtype(x)
+    (R, C), dev = x.shape, _device(x, "x", stream)
+    if q is None:
+        q = _new((R, C), torch.int8, x.device, stream)
+    if scale is None:
+        scale = _new((R,), torch.float32, x.device, stream)
+    ldx, ldq = _matrix(x, "x", R, C, dt, dev), _matrix(q, "q", R, C, torch.int8, dev)
+    _vector(scale, "scale", R, torch.float32, dev)
+    rc = lib.quantize_rows(x.data_ptr(), code, R, C, ldx, q.data_ptr(), ldq, scale.data_ptr(), _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
+    return q, scale
+
+
+def linear_int8_workspace_size(M, N, K, dtype=torch.bfloat16, quantized=False, backward=False):
+    """Device workspace bytes linear_int8_forward (quantized: x comes in 8
+    bits) or linear_int8_backward needs."""
+    b = ctypes.c_size_t(0)
+    _check(load().linear_int8_workspace_size(_dtype_code(dtype), int(M), int(N), int(K), int(bool(quantized)),
+                                             int(bool(backward)), ctypes.byref(b)))
+    return b.value
+
+
+def linear_int8_forward(x, w, w_scale, bias=None, act="none", residual=None, alpha=1.0, x_scale=None, dtype=None,
+                        out=None, preact=None, workspace=None, stream=None):
+    """linear_forward on 8-bit weights w [N, K] with w_scale [N], as
+    quantize_rows gives them.  x [M, K] is float32 or bfloat16 and brought to
+    8 bits in the call, or int8 with x_scale [M]; then the results' type is
+    out's, else `dtype`, else bfloat16.  See linear_int8_forward in
+    include/fedavg.h."""
+    lib = load()
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w must be matrices")
+    quantized = x_scale is not None
+    if quantized:
+        dt = out.dtype if out is not None else torch.bfloat16 if dtype is None else dtype
+    else:
+        dt = x.dtype
+    if dtype is not None and dtype is not dt:
+        raise TypeError(f"the results are {dt}, not {dtype}")
+    code = _dtype_code(dt)
+    (M, K), N, act, dev = x.shape, w.shape[0], _act(act), _device(x, "x", stream)
+    ldx, ldw = _matrix(x, "x", M, K, torch.int8 if quantized else dt, dev), _matrix(w, "w", N, K, torch.int8, dev)
+    _vector(x_scale, "x_scale", M, torch.float32, dev)
+    _vector(w_scale, "w_scale", N, torch.float32, dev)
+    _vector(bias, "bias", N, dt, dev)
+    if out is None:
+        out = _new((M, N), dt, x.device, stream)
+    ldr, ldo = _matrix(residual, "residual", M, N, dt, dev), _matrix(out, "out", M, N, dt, dev)
+    ldp = _matrix(preact, "preact", M, N, dt, dev)
+    keep, ws, nbytes = _workspace(workspace, x, stream, "linear_int8_workspace_size", code, M, N, K, int(quantized), 0)
+    rc = lib.linear_int8_forward(code, M, N, K, x.data_ptr(), ldx, _at(x_scale), w.data_ptr(), ldw, _at(w_scale),
+                                 _at(bias), act, alpha, _at(residual), ldr, out.data_ptr(), ldo, _at(preact), ldp, ws,
+                                 nbytes, _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
+    return out
+
+
+def linear_int8_backward(dy, w, w_scale, act="none", preact=None, alpha=1.0, dx=True, db=False, workspace=None,
+                         stream=None):
+    """Gradients (dx, db) of linear_int8_forward from dy [M, N], the gradient
+    of its output, for frozen weights.  dx and db are each a tensor to fill,
+    True to make one, or None/False to leave that gradient out (returned as
+    None).  preact: what linear_int8_forward wrote there, for an activation.
+    See linear_int8_backward in include/fedavg.h."""
+    lib = load()
+    if dy.dim() != 2 or w.dim() != 2:
+        raise ValueError("dy and w must be matrices")
+    dt, code = dy.dtype, _dtype(dy)
+    (M, N), K, act, dev = dy.shape, w.shape[1], _act(act), _device(dy, "dy", stream)
+
+    def want(t, shape):
+        if t is None or t is False:
+            return None
+        return _new(shape, dt, dy.device, stream) if t is True else t
+
+    dx, db = want(dx, (M, K)), want(db, (N,))
+    lddy, ldw = _matrix(dy, "dy", M, N, dt, dev), _matrix(w, "w", N, K, torch.int8, dev)
+    _vector(w_scale, "w_scale", N, torch.float32, dev)
+    ldp, lddx = _matrix(preact, "preact", M, N, dt, dev), _matrix(dx, "dx", M, K, dt, dev)
+    _vector(db, "db", N, dt, dev)
+    keep, ws, nbytes = _workspace(workspace, dy, stream, "linear_int8_workspace_size", code, M, N, K, 0, 1)
+    rc = lib.linear_int8_backward(code, M, N, K, dy.data_ptr(), lddy, w.data_ptr(), ldw, _at(w_scale), act, alpha,
+                                  _at(preact), ldp, _at(dx), lddx, _at(db), ws, nbytes, _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
+    return dx, db
 
 
 # ------------------------------------------------------------------ top logits, distillation

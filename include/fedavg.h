@@ -639,6 +639,54 @@ int linear_int8_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const 
                          void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
+ * The server's step with the orthogonalised average: a matrix's averaged update
+ * has its singular values brought near one before it is added to the weights,
+ * so that directions that few clients push count as much as those that all do.
+ *
+ * t is a matrix of m rows and n columns, s = min(m, n).  X = t / |t| (Frobenius
+ * norm), then for each of `steps` steps with its coefficients (a, b, c)
+ *     X <- a X + (b G + c G G) X,   G = X X^T      (m <= n; else from the right,
+ *                                                   G = X^T X)
+ * which leaves X's singular vectors as they are and takes each singular value
+ * v to a v + b v^3 + c v^5.  O is the last X.  A matrix of zeros gives zeros,
+ * one that holds NaN or an infinity NaN throughout.
+ *
+ * Calls take B such matrices: rows ld* elements apart, matrices stride_*
+ * elements apart, an input's possibly 0.  A result's rows and matrices must not
+ * overlap one another (FA_ERR_ARG); they may lie one after another or interleave
+ * by rows.  Pointers need only the element's alignment.
+ * coef       host array of 3 * steps values, 1 <= steps <= FA_MAX_ORTHO_STEPS.
+ *            Coefficients under which singular values within 0 and 1 grow past
+ *            1e9 are refused (FA_ERR_RANGE).
+ * Limits: B and the longer side at most 2^20, s at most 2^15, B*m*n at most 2^33
+ * (FA_ERR_RANGE).  Precision: fp64 for s <= 64; beyond, that of fp32 products, on
+ * pairs of fp16.  Each result is rounded once to its type.  Sums have an order
+ * fixed by the sizes: results are deterministic.
+ *
+ * orthogonalize -- out = scale * O of x.  out may be x itself (same pointer,
+ * pitch and stride); otherwise they must not overlap (FA_ERR_ARG).
+ *
+ * orthogonal_step -- with `momentum` (float [B][m][n], updated; nullable):
+ *     momentum = beta * momentum + update
+ *     t = momentum, or update + beta * momentum (nesterov)
+ * without it t = update.  Then weights = keep * weights + rate * O.
+ * update of update_dtype, weights of dtype (both FA_F32 or FA_BF16);
+ * 0 <= beta <= 1 (FA_ERR_ARG).  update, momentum, weights and the workspace must
+ * not overlap (FA_ERR_ARG).
+ */
+#define FA_MAX_ORTHO_STEPS 32
+
+int orthogonalize_workspace_size(int64_t B, int64_t m, int64_t n, size_t *bytes);
+int orthogonalize(fa_dtype dtype, int64_t B, int64_t m, int64_t n, const void *x, int64_t ldx,
+                  int64_t stride_x, const double *coef, int steps, float scale, void *out, int64_t ldo,
+                  int64_t stride_o, void *workspace, size_t workspace_bytes, void *stream);
+int orthogonal_step(fa_dtype update_dtype, fa_dtype dtype, int64_t B, int64_t m, int64_t n,
+                    const void *update, int64_t ldu, int64_t stride_u, float *momentum, int64_t ldm,
+                    int64_t stride_m, float beta, int nesterov, const double *coef, int steps, float rate,
+                    float keep, void *weights, int64_t ldw, int64_t stride_w, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
  * Exchange of distilled knowledge: clients send the top logits of each public
  * token instead of weights (FLARE page, section on what a federation may
  * exchange: model weights, adapters or distilled knowledge), and the server

@@ -20,5 +20,6 @@ from .fedavg import (  # noqa: F401
     topk_workspace_size, topk_select, topk_count, SampleController, stream_windows,
     linear_workspace_size, linear_forward, linear_backward,
     quantize_rows, linear_int8_workspace_size, linear_int8_forward, linear_int8_backward,
+    orthogonalize_workspace_size, orthogonalize, orthogonal_step, ORTHO_COEF, FA_MAX_ORTHO_STEPS,
     logits_topk_workspace_size, logits_topk, distill_workspace_size, distill_loss, distill_backward,
 )

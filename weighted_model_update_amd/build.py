@@ -12,6 +12,7 @@ SOURCES = [os.path.join(HERE, "csrc", "fedavg_kernels.hip"),
            os.path.join(HERE, "csrc", "topk.hip"),
            os.path.join(HERE, "csrc", "linear.hip"),
            os.path.join(HERE, "csrc", "int8.hip"),
+           os.path.join(HERE, "csrc", "orthogonal.hip"),
            os.path.join(HERE, "csrc", "logits.hip"),
            os.path.join(HERE, "csrc", "fedavg_api.hip")]
 HEADERS = [os.path.join(HERE, "csrc", "fedavg_internal.h"),

@@ -2013,6 +2013,160 @@ int linear_int8_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const 
     return e == hipSuccess ? ok() : hip_fail(e, "join of the gradients launch");
 }
 
+// ============================================================ orthogonalised update
+
+namespace {
+
+constexpr int64_t ORTHO_MAX_BATCH = 1ll << 20, ORTHO_MAX_LONG = 1ll << 20, ORTHO_MAX_SHORT = 1ll << 15,
+                  ORTHO_MAX_ELEMS = 1ll << 33;
+
+// B matrices of m rows of n: rows `ld` apart, matrices `stride` apart.
+struct BatchView {
+    const void *p;
+    int64_t B, m, n, ld, stride;
+    size_t es;
+    int64_t matrix() const { return (m - 1) * ld + n; }   // elements from a matrix's first to its last
+    int64_t across() const { return (B - 1) * stride + n; } // ... from a row's first to the last matrix's same row
+    bool whole() const { return B == 1 || stride >= matrix(); } // one matrix after another
+    bool rowwise() const { return m == 1 || ld >= across(); }   // one row of all matrices after another
+    View view() const
+    {
+        if (whole())
+            return {p, p ? B : 0, matrix(), stride, es};
+        if (rowwise())
+            return {p, p ? m : 0, across(), ld, es};
+        return {p, p ? 1 : 0, (B - 1) * stride + matrix(), 0, es};
+    }
+};
+
+int check_batch(const char *name, const BatchView &v, bool out)
+{
+    if (!v.p)
+        return fail(FA_ERR_ARG, "%s is required", name);
+    if ((reinterpret_cast<uintptr_t>(v.p) & (v.es - 1)) != 0)
+        return fail(FA_ERR_ARG, "%s must be aligned to its element", name);
+    if (v.ld < 0 || v.stride < 0)
+        return fail(FA_ERR_ARG, "%s has a negative pitch or stride", name);
+    if (v.ld > (1ll << 40) || v.stride > (1ll << 40))
+        return fail(FA_ERR_RANGE, "%s spans too many elements", name);
+    const bool rows = v.m == 1 || v.ld >= v.n, matrices = v.B == 1 || v.stride >= v.n;
+    if (out && !(rows && matrices && (v.whole() || v.rowwise())))
+        return fail(FA_ERR_ARG, "%s has rows or matrices that overlap one another", name);
+    return FA_OK;
+}
+
+bool same_batch(const BatchView &a, const BatchView &b)
+{
+    return a.p == b.p && a.es == b.es && (a.ld == b.ld || a.m == 1) && (a.stride == b.stride || a.B == 1);
+}
+
+int check_ortho(int64_t B, int64_t m, int64_t n)
+{
+    if (B < 0 || m < 0 || n < 0)
+        return fail(FA_ERR_ARG, "B, m and n must be >= 0");
+    const int64_t s = std::min(m, n), l = std::max(m, n);
+    if (B > ORTHO_MAX_BATCH || l > ORTHO_MAX_LONG || s > ORTHO_MAX_SHORT || B * s > ORTHO_MAX_ELEMS / std::max<int64_t>(l, 1))
+        return fail(FA_ERR_RANGE, "B and the longer side must be at most 2^20, the shorter side 2^15, B * m * n 2^33");
+    return FA_OK;
+}
+
+int run_ortho(fa::OrthoArgs &a, int update_dtype, int dtype, const double *coef, int steps, const BatchView &x,
+              const BatchView &momentum, const BatchView &out, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!coef || steps < 1 || steps > FA_MAX_ORTHO_STEPS)
+        return fail(FA_ERR_ARG, "need the coefficients of 1 to %d steps", FA_MAX_ORTHO_STEPS);
+    for (int k = 0; k < steps; k++)
+        for (int i = 0; i < 3; i++)
+            a.coef[k][i] = coef[3 * k + i];
+    if (!fa::ortho_reach_ok(a.coef, steps))
+        return fail(FA_ERR_RANGE, "the coefficients let singular values of up to 1 grow past 1e9");
+    const int64_t B = x.B, m = x.m, n = x.n;
+    if (B == 0 || m == 0 || n == 0)
+        return ok();
+    int rc;
+    if ((rc = check_batch("the update", x, false)) != FA_OK || (rc = check_batch("the result", out, true)) != FA_OK ||
+        (momentum.p && (rc = check_batch("momentum", momentum, true)) != FA_OK))
+        return rc;
+    const View vs{workspace, workspace ? 1 : 0, (int64_t)workspace_bytes, 0, 1};
+    const bool in_place = !a.add && update_dtype == dtype && same_batch(x, out);
+    if ((!in_place && views_overlap(x.view(), out.view())) || views_overlap(x.view(), momentum.view()) ||
+        views_overlap(out.view(), momentum.view()))
+        return fail(FA_ERR_ARG, "the update, the momentum and the result must not overlap");
+    for (const BatchView *v : {&x, &momentum, &out})
+        if (views_overlap(v->view(), vs))
+            return fail(FA_ERR_ARG, "the workspace must not overlap anything else");
+    if ((rc = check_workspace(workspace, workspace_bytes, fa::ortho_workspace_bytes(B, m, n, cu_count()))) != FA_OK)
+        return rc;
+    a.x = x.p;
+    a.ldx = x.ld;
+    a.stride_x = x.stride;
+    a.momentum = const_cast<float *>(static_cast<const float *>(momentum.p));
+    a.ldm = momentum.ld;
+    a.stride_m = momentum.stride;
+    a.B = B;
+    a.m = m;
+    a.n = n;
+    a.steps = steps;
+    a.out = const_cast<void *>(out.p);
+    a.ldo = out.ld;
+    a.stride_o = out.stride;
+    a.ws = workspace;
+    const hipError_t e = fa::launch_ortho(a, update_dtype, dtype, cu_count(), static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, "orthogonalisation launch");
+}
+
+} // namespace
+
+int orthogonalize_workspace_size(int64_t B, int64_t m, int64_t n, size_t *bytes)
+{
+    if (!bytes)
+        return fail(FA_ERR_ARG, "need a result pointer");
+    const int rc = check_ortho(B, m, n);
+    if (rc != FA_OK)
+        return rc;
+    *bytes = fa::ortho_workspace_bytes(B, m, n, cu_count());
+    return ok();
+}
+
+int orthogonalize(fa_dtype dtype, int64_t B, int64_t m, int64_t n, const void *x, int64_t ldx, int64_t stride_x,
+                  const double *coef, int steps, float scale, void *out, int64_t ldo, int64_t stride_o,
+                  void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!dtype_ok(dtype))
+        return fail(FA_ERR_DTYPE, "dtype must be FA_F32 or FA_BF16");
+    const int rc = check_ortho(B, m, n);
+    if (rc != FA_OK)
+        return rc;
+    fa::OrthoArgs a{};
+    a.rate = scale;
+    const size_t es = dsize(dtype);
+    return run_ortho(a, dtype, dtype, coef, steps, {x, B, m, n, ldx, stride_x, es}, {nullptr, B, m, n, n, 0, 4},
+                     {out, B, m, n, ldo, stride_o, es}, workspace, workspace_bytes, stream);
+}
+
+int orthogonal_step(fa_dtype update_dtype, fa_dtype dtype, int64_t B, int64_t m, int64_t n, const void *update,
+                    int64_t ldu, int64_t stride_u, float *momentum, int64_t ldm, int64_t stride_m, float beta,
+                    int nesterov, const double *coef, int steps, float rate, float keep, void *weights, int64_t ldw,
+                    int64_t stride_w, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!dtype_ok(dtype) || !dtype_ok(update_dtype))
+        return fail(FA_ERR_DTYPE, "the types must be FA_F32 or FA_BF16");
+    const int rc = check_ortho(B, m, n);
+    if (rc != FA_OK)
+        return rc;
+    if (momentum && !(beta >= 0.f && beta <= 1.f))
+        return fail(FA_ERR_ARG, "beta must be within 0 and 1");
+    fa::OrthoArgs a{};
+    a.beta = beta;
+    a.nesterov = nesterov != 0;
+    a.add = 1;
+    a.rate = rate;
+    a.keep = keep;
+    return run_ortho(a, update_dtype, dtype, coef, steps, {update, B, m, n, ldu, stride_u, dsize(update_dtype)},
+                     {momentum, B, m, n, ldm, stride_m, 4}, {weights, B, m, n, ldw, stride_w, dsize(dtype)}, workspace,
+                     workspace_bytes, stream);
+}
+
 // ============================================================ top logits of rows, distillation
 
 namespace {

@@ -1,6 +1,7 @@
 // Internal interface between the host library and the kernels of the linear
 // layer (linear.hip), the layers on 8-bit weights (int8.hip), the per-row top
-// logits and the distillation loss (logits.hip).  Not part of the public ABI.
+// logits and the distillation loss (logits.hip), and the orthogonalised update
+// (orthogonal.hip).  Not part of the public ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -84,6 +85,30 @@ hipError_t launch_gemm8(const GemmArgs &a, int dt, void *ws, int cus, hipStream_
 // out [rows][ldo] = w as values of dt, zeros from column `cols` on.
 hipError_t launch_widen(const int8_t *w, int64_t ldw, int64_t rows, int64_t cols, int dt, void *out, int64_t ldo,
                         hipStream_t s);
+
+// ---------------------------------------------------------------- orthogonalised update
+// out = rate O, or keep out + rate O (add), O the orthogonalised t [B][m][n].
+struct OrthoArgs {
+    const void *x; // the update, pitch ldx, stride_x from matrix to matrix
+    int64_t ldx, stride_x;
+    float *momentum; // nullable
+    int64_t ldm, stride_m;
+    float beta;
+    int nesterov;
+    int64_t B, m, n;
+    int steps;
+    double coef[FA_MAX_ORTHO_STEPS][3];
+    void *out;
+    int64_t ldo, stride_o;
+    int add;
+    float keep, rate;
+    void *ws;
+};
+// Whether the coefficients keep the singular values within what the scaled
+// halves hold.
+bool ortho_reach_ok(const double (*coef)[3], int steps);
+size_t ortho_workspace_bytes(int64_t B, int64_t m, int64_t n, int cus);
+hipError_t launch_ortho(const OrthoArgs &o, int update_dt, int dt, int cus, hipStream_t s);
 
 // ---------------------------------------------------------------- logits
 struct TopRowsArgs {

@@ -1,0 +1,875 @@
+// The orthogonalised update: X = t / |t| (Frobenius), then for each step
+//     G = X X^T,   H = b G + c G^2,   X <- a X + H X
+// over the shorter side s of the matrix (a tall one has G = X^T X and X <- a X +
+// X H).  The singular values of X go through the odd polynomials a v + b v^3 +
+// c v^5 in turn while its singular vectors stay; with suitable coefficients
+// all of them end near one.
+//
+// Two forms.  For s <= 64 the whole sequence is one polynomial P of the first
+// Gram matrix, times X: the Gram matrix and P are formed in fp64 (the powers
+// of G square its condition), and X is read twice.  Longer sides take matrix
+// products of 16-bit floats: a value is held as hi + lo, two fp16 scaled by a
+// power of two (22 bits or more), and a product is hi hi + hi lo + lo hi with fp32
+// sums, as exact as one in fp32 at a third of the 16-bit rate (835 against 157
+// TFLOP/s at the peak).  a X is added to the finished sum: taken into H's
+// diagonal it would pass through every rounding of the sum (relative error 8e-6
+// instead of 2.8e-6 after 5 steps of a 512 x 512 matrix of rank 64 and noise,
+// where fp32 products give 2.5e-6).
+#include "tiles.h"
+
+#include <algorithm>
+#include <cmath>
+
+namespace fa {
+namespace {
+
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+
+// ------------------------------------------------------------ the argument t
+// v = beta v + u; t = u + beta v (nesterov) or v; without a momentum t = u.
+template <typename T, int W>
+__device__ __forceinline__ void argument(const OrthoArgs &p, const T *u, float *v, bool update, int valid, float *t)
+{
+    load_n<T, W>(u, valid, t);
+    if (!p.momentum)
+        return;
+    float m[W];
+    load_n<float, W>(v, valid, m);
+    if (update) {
+#pragma unroll
+        for (int i = 0; i < W; i++)
+            m[i] = __builtin_fmaf(p.beta, m[i], t[i]);
+        store_n<float, W>(v, valid, m);
+    }
+#pragma unroll
+    for (int i = 0; i < W; i++)
+        t[i] = p.nesterov ? __builtin_fmaf(p.beta, m[i], t[i]) : m[i];
+}
+
+template <typename T> __device__ __forceinline__ const T *update_at(const OrthoArgs &p, int64_t b, int64_t r, int64_t c)
+{
+    return static_cast<const T *>(p.x) + b * p.stride_x + r * p.ldx + c;
+}
+
+__device__ __forceinline__ float *momentum_at(const OrthoArgs &p, int64_t b, int64_t r, int64_t c)
+{
+    return p.momentum ? p.momentum + b * p.stride_m + r * p.ldm + c : nullptr;
+}
+
+// The result: o = rate v, or keep o + rate v where the call steps weights.
+template <typename O, int W>
+__device__ __forceinline__ void put_result(const OrthoArgs &p, int64_t b, int64_t r, int64_t c, int valid, const float *v)
+{
+    O *o = static_cast<O *>(p.out) + b * p.stride_o + r * p.ldo + c;
+    float old[W], z[W];
+    load_n<O, W>(o, p.add ? valid : 0, old);
+#pragma unroll
+    for (int i = 0; i < W; i++)
+        z[i] = p.add ? __builtin_fmaf(p.rate, v[i], p.keep * old[i]) : p.rate * v[i];
+    store_n<O, W>(o, valid, z);
+}
+
+// Matrix and part of a workgroup.
+__device__ __forceinline__ void matrix_of(int64_t id, int parts, int64_t &b, int &part)
+{
+    b = id / parts;
+    part = (int)(id % parts);
+}
+
+// ------------------------------------------------------------ long sides: norm and first X
+// Four columns a thread, `across` (a power of two) threads to a row; bound by
+// memory.  The squares are summed in fp64, in an order fixed by the sizes.
+constexpr int NORM_THREADS = 256, NORM_W = 4, NORM_MAX_PARTS = 256;
+
+template <typename T>
+__global__ __launch_bounds__(NORM_THREADS) void norm_kernel(OrthoArgs p, int parts, int64_t rows_per, int across, double *sums)
+{
+    __shared__ double waves[NORM_THREADS / WAVE];
+    int64_t b;
+    int part;
+    matrix_of(blockIdx.x, parts, b, part);
+    const int64_t r0 = part * rows_per, r1 = r0 + rows_per < p.m ? r0 + rows_per : p.m;
+    const int64_t c0 = (int64_t)(threadIdx.x % across) * NORM_W;
+    double sum = 0;
+    for (int64_t r = r0 + threadIdx.x / across; r < r1; r += NORM_THREADS / across)
+        for (int64_t c = c0; c < p.n; c += across * NORM_W) {
+            float t[NORM_W];
+            argument<T, NORM_W>(p, update_at<T>(p, b, r, c), momentum_at(p, b, r, c), true,
+                                (int)(p.n - c < NORM_W ? p.n - c : NORM_W), t);
+#pragma unroll
+            for (int i = 0; i < NORM_W; i++)
+                sum += c + i < p.n ? (double)t[i] * t[i] : 0.0;
+        }
+#pragma unroll
+    for (int d = 1; d < WAVE; d *= 2)
+        sum += __shfl_xor(sum, d);
+    if (threadIdx.x % WAVE == 0)
+        waves[threadIdx.x / WAVE] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        sums[b * parts + part] = waves[0] + waves[1] + waves[2] + waves[3];
+}
+
+// 1 / |t|; 0 for a matrix of zeros, NaN where the sum is NaN or infinite.
+__device__ __forceinline__ double inverse_norm(double square)
+{
+    return square == 0 ? 0.0 : square < INFINITY ? 1.0 / sqrt(square) : __builtin_nan("");
+}
+
+__device__ __forceinline__ void split_value(float v, _Float16 &hi, _Float16 &lo)
+{
+    hi = (_Float16)v;
+    lo = (_Float16)(v - (float)hi);
+}
+
+// X = t / |t| times `scale` as hi and lo planes [m][pitch], zeros behind the rows.
+template <typename T>
+__global__ __launch_bounds__(NORM_THREADS) void split_kernel(OrthoArgs p, int parts, int64_t rows_per, int across,
+                                                             const double *sums, float scale, _Float16 *x, int64_t pitch,
+                                                             int64_t lo, int64_t stride)
+{
+    __shared__ double factor;
+    int64_t b;
+    int part;
+    matrix_of(blockIdx.x, parts, b, part);
+    if (threadIdx.x < WAVE) {
+        double sum = 0;
+        for (int i = threadIdx.x; i < parts; i += WAVE)
+            sum += sums[b * parts + i];
+#pragma unroll
+        for (int d = 1; d < WAVE; d *= 2)
+            sum += __shfl_xor(sum, d);
+        if (threadIdx.x == 0)
+            factor = inverse_norm(sum) * scale;
+    }
+    __syncthreads();
+    const double f = factor;
+    const int64_t r0 = part * rows_per, r1 = r0 + rows_per < p.m ? r0 + rows_per : p.m;
+    const int64_t c0 = (int64_t)(threadIdx.x % across) * NORM_W;
+    for (int64_t r = r0 + threadIdx.x / across; r < r1; r += NORM_THREADS / across)
+        for (int64_t c = c0; c < pitch; c += across * NORM_W) {
+            float t[NORM_W];
+            argument<T, NORM_W>(p, update_at<T>(p, b, r, c), momentum_at(p, b, r, c), false,
+                                (int)(c >= p.n ? 0 : p.n - c < NORM_W ? p.n - c : NORM_W), t);
+            f16x4 h, l;
+#pragma unroll
+            for (int i = 0; i < NORM_W; i++) {
+                _Float16 hi, lw;
+                split_value(c + i < p.n ? (float)(t[i] * f) : 0.f, hi, lw);
+                h[i] = hi;
+                l[i] = lw;
+            }
+            _Float16 *to = x + b * stride + r * pitch + c;
+            *reinterpret_cast<f16x4 *>(to) = h;
+            *reinterpret_cast<f16x4 *>(to + lo) = l;
+        }
+}
+
+// ------------------------------------------------------------ long sides: products
+// A matrix of a batch as two planes: `lo` elements from hi to lo, `stride` from
+// one matrix to the next; rows start on 16 bytes and are followed by zeros.
+struct Planes {
+    _Float16 *p;
+    int64_t ld, lo, stride;
+};
+
+struct PairArgs {
+    Planes a, b;
+    int M, N, K;
+    int tiles_m, tiles_n, tiles; // tiles of one matrix; symmetric: of the lower triangle
+    // v = p T + q (sum); T absent: p is 0
+    float p, q;
+    Planes t;
+    Planes out; // out.p null: the result goes to o.out
+    OrthoArgs o;
+};
+
+// Tile of the lower triangle, rows one after another.
+__device__ __forceinline__ void triangle_tile(unsigned id, unsigned &tm, unsigned &tn)
+{
+    tm = (unsigned)((sqrtf(8.f * (float)id + 1.f) - 1.f) * 0.5f);
+    while (tm * (tm + 1) / 2 > id)
+        tm--;
+    while ((tm + 1) * (tm + 2) / 2 <= id)
+        tm++;
+    tn = id - tm * (tm + 1) / 2;
+}
+
+// Four neighbours (m, n .. n + 3) of a finished sum, n a multiple of 4.
+template <typename O>
+__device__ __forceinline__ void finish_pair(const PairArgs &p, int64_t b, int m, int n, f32x4 s, bool mirror)
+{
+    if (m >= p.M || n >= (p.out.p ? p.out.ld : (int64_t)p.N)) {
+        if (!mirror)
+            return;
+    }
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        v[i] = p.q * s[i];
+    if (p.t.p && m < p.M && n < p.t.ld) {
+        const _Float16 *at = p.t.p + b * p.t.stride + (int64_t)m * p.t.ld + n;
+        const f16x4 h = *reinterpret_cast<const f16x4 *>(at), l = *reinterpret_cast<const f16x4 *>(at + p.t.lo);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            v[i] = __builtin_fmaf(p.p, (float)h[i] + (float)l[i], v[i]);
+    }
+    if (!p.out.p) {
+        const int valid = p.N - n < 4 ? p.N - n : 4;
+        put_result<O, 4>(p.o, b, m, n, valid, v);
+        return;
+    }
+    f16x4 h, l;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        _Float16 hi, lw;
+        split_value(v[i], hi, lw);
+        h[i] = hi;
+        l[i] = lw;
+    }
+    _Float16 *base = p.out.p + b * p.out.stride;
+    if (m < p.M && n < p.out.ld) {
+        _Float16 *to = base + (int64_t)m * p.out.ld + n;
+        *reinterpret_cast<f16x4 *>(to) = h;
+        *reinterpret_cast<f16x4 *>(to + p.out.lo) = l;
+    }
+    if (mirror && m < p.out.ld) {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (n + i < p.N) {
+                _Float16 *to = base + (int64_t)(n + i) * p.out.ld + m;
+                to[0] = h[i];
+                to[p.out.lo] = l[i];
+            }
+    }
+}
+
+// The three products of the halves run as one sum over 3 K: (hi, hi), (hi, lo),
+// (lo, hi).
+// Workgroup (tile of a matrix, split).  With more than one split the sums go to
+// `part` [matrix][split][M][N].
+template <typename O, int BM, int BN, int WM, int WN, bool AO, bool BO, bool SYM>
+__global__ __launch_bounds__(WM *WN *WAVE) void pair_kernel(PairArgs p, int per, float *part)
+{
+    typedef _Float16 T;
+    constexpr int THREADS = WM * WN * WAVE, BK = STEP_BYTES / 2;
+    constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
+    constexpr int AB = BM * STEP_BYTES, BB = BN * STEP_BYTES;
+    __shared__ __attribute__((aligned(1024))) char l0[AB + BB];
+    __shared__ __attribute__((aligned(1024))) char l1[AB + BB];
+
+    const int64_t bt = blockIdx.x / (unsigned)p.tiles;
+    unsigned tm, tn;
+    if constexpr (SYM)
+        triangle_tile(blockIdx.x % (unsigned)p.tiles, tm, tn);
+    else
+        tile_of(blockIdx.x % (unsigned)p.tiles, p.tiles_m, p.tiles_n, tm, tn);
+    const int m0 = (int)tm * BM, n0 = (int)tn * BN;
+    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
+    const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
+    const int spk = (p.K + BK - 1) / BK; // steps of one of the three products
+    const int first = blockIdx.y * per, steps = 3 * spk - first < per ? 3 * spk - first : per;
+    Tile<T, BM, BN, WM, WN, AO, BO> t;
+    t.clear();
+    Direct<T, AO, BM, THREADS, STEP_BYTES> da;
+    Direct<T, BO, BN, THREADS, STEP_BYTES> db;
+    da.init(p.a.p + bt * p.a.stride, p.a.ld, m0, p.M, 0);
+    db.init(p.b.p + bt * p.b.stride, p.b.ld, n0, p.N, 0);
+    const char *a0 = da.base, *b0 = db.base;
+    t.run(l0, l1, steps, wm, wn, lane, [&](char *l, int s) {
+        const int seg = (first + s) / spk, k = (first + s) % spk;
+        da.base = a0 + (seg == 2 ? p.a.lo * 2 : 0) + k * da.advance;
+        db.base = b0 + (seg == 1 ? p.b.lo * 2 : 0) + k * db.advance;
+        da.start(l, p.K - k * BK);
+        db.start(l + AB, p.K - k * BK);
+    });
+#pragma unroll
+    for (int i = 0; i < FM; i++)
+#pragma unroll
+        for (int j = 0; j < FN; j++) {
+            const int m = m0 + wm + i * 16 + (lane & 15), n = n0 + wn + j * 16 + (lane >> 4) * 4;
+            if (part) {
+                if (m < p.M && n < p.N) {
+                    float v[4] = {t.acc[i][j][0], t.acc[i][j][1], t.acc[i][j][2], t.acc[i][j][3]};
+                    store_n<float, 4>(part + ((bt * gridDim.y + blockIdx.y) * p.M + m) * p.N + n, p.N - n, v);
+                }
+            } else {
+                finish_pair<O>(p, bt, m, n, t.acc[i][j], SYM && tm != tn);
+            }
+        }
+}
+
+// As above for large products: steps of 64 bytes through four buffers.
+template <typename O, int BM, int BN, int WM, int WN, bool AO, bool BO, bool SYM>
+__global__ __launch_bounds__(WM *WN *WAVE) void pair_pipe_kernel(PairArgs p)
+{
+    typedef _Float16 T;
+    constexpr int THREADS = WM * WN * WAVE, BK = PIPE_STEP / 2;
+    constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
+    constexpr int AB = BM * PIPE_STEP, BB = BN * PIPE_STEP;
+    __shared__ __attribute__((aligned(1024))) char l0[AB + BB];
+    __shared__ __attribute__((aligned(1024))) char l1[AB + BB];
+    __shared__ __attribute__((aligned(1024))) char l2[AB + BB];
+    __shared__ __attribute__((aligned(1024))) char l3[AB + BB];
+
+    const int64_t bt = blockIdx.x / (unsigned)p.tiles;
+    unsigned tm, tn;
+    if constexpr (SYM)
+        triangle_tile(blockIdx.x % (unsigned)p.tiles, tm, tn);
+    else
+        tile_of(blockIdx.x % (unsigned)p.tiles, p.tiles_m, p.tiles_n, tm, tn);
+    const int m0 = (int)tm * BM, n0 = (int)tn * BN;
+    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
+    const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
+    const int spk = (p.K + BK - 1) / BK;
+    Pipe<T, BM, BN, WM, WN, AO, BO> t;
+    Direct<T, AO, BM, THREADS, PIPE_STEP> da;
+    Direct<T, BO, BN, THREADS, PIPE_STEP> db;
+    da.init(p.a.p + bt * p.a.stride, p.a.ld, m0, p.M, 0);
+    db.init(p.b.p + bt * p.b.stride, p.b.ld, n0, p.N, 0);
+    const char *a0 = da.base, *b0 = db.base;
+    int left = p.K, seg = 0; // of the next step to copy; steps past the end copy zeros
+    t.run(l0, l1, l2, l3, 3 * spk, [&](char *l) {
+        da.start(l, left);
+        db.start(l + AB, left);
+        left -= BK;
+        if (left <= 0 && seg < 2) {
+            seg++;
+            left = p.K;
+            da.base = a0 + (seg == 2 ? p.a.lo * 2 : 0);
+            db.base = b0 + (seg == 1 ? p.b.lo * 2 : 0);
+        }
+    });
+#pragma unroll
+    for (int i = 0; i < FM; i++)
+#pragma unroll
+        for (int j = 0; j < FN; j++)
+            finish_pair<O>(p, bt, m0 + wm + i * 16 + (lane & 15), n0 + wn + j * 16 + (lane >> 4) * 4, t.acc[i][j],
+                           SYM && tm != tn);
+}
+
+// Joins the splits' sums in their order and finishes them, four neighbours a
+// thread; of a symmetric product an element above the diagonal is read below it.
+constexpr int PJ_THREADS = 256;
+
+template <typename O>
+__global__ __launch_bounds__(PJ_THREADS) void pair_join_kernel(PairArgs p, const float *part, int splits, int64_t batch, bool sym)
+{
+    const int64_t cols = p.out.p ? p.out.ld : p.N, groups = (cols + 3) / 4;
+    const int64_t at = (int64_t)blockIdx.x * PJ_THREADS + threadIdx.x;
+    if (at >= batch * p.M * groups)
+        return;
+    const int64_t b = at / (p.M * groups);
+    const int m = (int)(at / groups % p.M), n = (int)(at % groups) * 4;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int z = 0; z < splits; z++) {
+        const float *from = part + (b * splits + z) * p.M * p.N;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (n + i < p.N)
+                s[i] += sym && n + i > m ? from[(int64_t)(n + i) * p.N + m] : from[(int64_t)m * p.N + n + i];
+    }
+    finish_pair<O>(p, b, m, n, s, false);
+}
+
+// ------------------------------------------------------------ short sides, in fp64
+// Fragments of the matrix cores' 16x16x4 product in fp64: lane l holds row
+// l % 16 of the one operand and column l % 16 of the other, both at k = l / 16,
+// and of the result column l % 16, rows l / 16 + 4 r.
+__device__ __forceinline__ f64x4 mma64(double a, double b, f64x4 c)
+{
+    return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
+}
+
+constexpr int SHORT_MAX = 64, SHORT_THREADS = 256, SHORT_WAVES = SHORT_THREADS / WAVE;
+
+constexpr int blocks_of(int t) { return t * (t + 1) / 2; }
+
+// Four values of a short row i at k .. k + 3 of the long side.
+template <typename T, bool WIDE>
+__device__ __forceinline__ void short_values(const OrthoArgs &p, int64_t b, int i, int64_t k, int64_t s, int64_t l,
+                                             bool update, float *t)
+{
+    const int valid = (int)(i >= s || k >= l ? 0 : l - k < 4 ? l - k : 4);
+    if constexpr (WIDE) {
+        argument<T, 4>(p, update_at<T>(p, b, i, k), momentum_at(p, b, i, k), update, valid, t);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            argument<T, 1>(p, update_at<T>(p, b, k + j, i), momentum_at(p, b, k + j, i), update, j < valid, t + j);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        t[j] = j < valid ? t[j] : 0.f;
+}
+
+// Workgroup (matrix, part of the long side): the blocks (rb, cb <= rb) of 16 x 16
+// of this part's share of the Gram matrix, to part [matrix][part][block][256].
+template <typename T, int SB, bool WIDE>
+__global__ __launch_bounds__(SHORT_THREADS) void short_gram_kernel(OrthoArgs p, int parts, int64_t per, double *part)
+{
+    constexpr int NB = blocks_of(SB);
+    __shared__ double joined[SHORT_WAVES][256];
+    int64_t b;
+    int q;
+    matrix_of(blockIdx.x, parts, b, q);
+    const int64_t s = WIDE ? p.m : p.n, l = WIDE ? p.n : p.m;
+    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE, i = lane & 15, g = lane >> 4;
+    const int64_t k0 = q * per, k1 = k0 + per < l ? k0 + per : l;
+    f64x4 acc[NB];
+#pragma unroll
+    for (int e = 0; e < NB; e++)
+        acc[e] = f64x4{0, 0, 0, 0};
+    for (int64_t k = k0 + wave * 16; k < k1; k += SHORT_WAVES * 16) {
+        float t[SB][4];
+#pragma unroll
+        for (int r = 0; r < SB; r++)
+            short_values<T, WIDE>(p, b, r * 16 + i, k + g * 4, s, l, true, t[r]);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+#pragma unroll
+            for (int r = 0; r < SB; r++)
+#pragma unroll
+                for (int c = 0; c <= r; c++)
+                    acc[r * (r + 1) / 2 + c] = mma64(t[r][j], t[c][j], acc[r * (r + 1) / 2 + c]);
+        }
+    }
+    double *to = part + (b * parts + q) * (NB * 256);
+#pragma unroll
+    for (int e = 0; e < NB; e++) {
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 4; r++)
+            joined[wave][(g + 4 * r) * 16 + i] = acc[e][r];
+        __syncthreads();
+        double sum = joined[0][threadIdx.x];
+#pragma unroll
+        for (int w = 1; w < SHORT_WAVES; w++)
+            sum += joined[w][threadIdx.x];
+        to[e * 256 + threadIdx.x] = sum;
+    }
+}
+
+// C = A B for symmetric A and B that commute, so C is symmetric too: blocks of
+// the lower triangle, written on both sides.  alpha A B + beta D + gamma I.
+template <int SB>
+__device__ __forceinline__ void short_product(double (*c)[SB * 16 + 2], const double (*a)[SB * 16 + 2],
+                                              const double (*b)[SB * 16 + 2], double alpha, double beta,
+                                              const double (*d)[SB * 16 + 2], double gamma)
+{
+    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE, i = lane & 15, g = lane >> 4;
+    __syncthreads();
+    for (int e = wave; e < blocks_of(SB); e += SHORT_WAVES) {
+        int r = 0;
+        while ((r + 1) * (r + 2) / 2 <= e)
+            r++;
+        const int cb = e - r * (r + 1) / 2;
+        f64x4 acc = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < SB * 4; k++)
+            acc = mma64(a[r * 16 + i][4 * k + g], b[cb * 16 + i][4 * k + g], acc);
+#pragma unroll
+        for (int z = 0; z < 4; z++) {
+            const int row = r * 16 + g + 4 * z, col = cb * 16 + i;
+            double v = alpha * acc[z] + (row == col ? gamma : 0.0);
+            if (d)
+                v += beta * d[row][col];
+            c[row][col] = v;
+            if (r != cb)
+                c[col][row] = v;
+        }
+    }
+}
+
+// Workgroup: one matrix.  P of its Gram matrix, to poly [matrix][16 SB][16 SB];
+// the norm is the Gram matrix's trace.
+template <int SB>
+__global__ __launch_bounds__(SHORT_THREADS) void short_poly_kernel(OrthoArgs p, int parts, const double *part, double *poly)
+{
+    constexpr int S = SB * 16, NB = blocks_of(SB);
+    typedef double Matrix[S][S + 2];
+    __shared__ Matrix m0, m1, m2, m3;
+    __shared__ double norm;
+    const int64_t b = blockIdx.x;
+    const int s = (int)(p.m < p.n ? p.m : p.n);
+    double(*G)[S + 2] = m0, (*P)[S + 2] = m1, (*Q)[S + 2] = m2, (*T)[S + 2] = m3;
+    const double *from = part + b * parts * (NB * 256);
+    for (int e = 0; e < NB; e++) {
+        double sum = 0;
+        for (int q = 0; q < parts; q++)
+            sum += from[(int64_t)q * (NB * 256) + e * 256 + threadIdx.x];
+        int r = 0;
+        while ((r + 1) * (r + 2) / 2 <= e)
+            r++;
+        const int row = r * 16 + threadIdx.x / 16, col = (e - r * (r + 1) / 2) * 16 + threadIdx.x % 16;
+        G[row][col] = sum;
+        G[col][row] = sum;
+    }
+    __syncthreads();
+    if (threadIdx.x < WAVE) {
+        double t = threadIdx.x < s ? G[threadIdx.x % S][threadIdx.x % S] : 0.0;
+#pragma unroll
+        for (int d = 1; d < WAVE; d *= 2)
+            t += __shfl_xor(t, d);
+        if (threadIdx.x == 0)
+            norm = inverse_norm(t);
+    }
+    __syncthreads();
+    const double f = norm;
+    for (int e = threadIdx.x; e < S * S; e += SHORT_THREADS) {
+        G[e / S][e % S] *= f * f;
+        P[e / S][e % S] = e / S == e % S ? f : 0.0;
+    }
+    for (int k = 0; k < p.steps; k++) {
+        const double ca = p.coef[k][0], cb = p.coef[k][1], cc = p.coef[k][2];
+        short_product<SB>(Q, G, G, cc, cb, G, ca); // Q = a + b G + c G^2
+        short_product<SB>(T, Q, P, 1.0, 0.0, nullptr, 0.0);
+        double(*swap)[S + 2] = P;
+        P = T;
+        T = swap;
+        if (k + 1 < p.steps) {
+            short_product<SB>(T, Q, G, 1.0, 0.0, nullptr, 0.0); // G <- Q G Q
+            short_product<SB>(G, T, Q, 1.0, 0.0, nullptr, 0.0);
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < S * S; e += SHORT_THREADS)
+        poly[b * S * S + e] = P[e / S][e % S];
+}
+
+// Workgroup (matrix, part of the long side): P X (wide) or X P (tall), 16
+// columns (rows) a wavefront at a time.
+template <typename T, typename O, int SB, bool WIDE>
+__global__ __launch_bounds__(SHORT_THREADS) void short_apply_kernel(OrthoArgs p, int parts, int64_t per, const double *poly)
+{
+    constexpr int S = SB * 16;
+    __shared__ double P[S][S + 2];
+    int64_t b;
+    int q;
+    matrix_of(blockIdx.x, parts, b, q);
+    const int64_t s = WIDE ? p.m : p.n, l = WIDE ? p.n : p.m;
+    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE, i = lane & 15, g = lane >> 4;
+    const int64_t k0 = q * per, k1 = k0 + per < l ? k0 + per : l;
+    for (int e = threadIdx.x; e < S * S; e += SHORT_THREADS)
+        P[e / S][e % S] = poly[b * S * S + e];
+    __syncthreads();
+    for (int64_t k = k0 + wave * 16; k < k1; k += SHORT_WAVES * 16) {
+        // element j of t[r] is short index 16 r + 4 g + j at long index k + i
+        float t[SB][4];
+#pragma unroll
+        for (int r = 0; r < SB; r++) {
+            const int64_t at = k + i;
+            const int first = r * 16 + g * 4, valid = (int)(at >= l || first >= s ? 0 : s - first < 4 ? s - first : 4);
+            if constexpr (WIDE) {
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    argument<T, 1>(p, update_at<T>(p, b, first + j, at), momentum_at(p, b, first + j, at), false, j < valid, t[r] + j);
+            } else {
+                argument<T, 4>(p, update_at<T>(p, b, at, first), momentum_at(p, b, at, first), false, valid, t[r]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                t[r][j] = j < valid ? t[r][j] : 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < SB; c++) {
+            f64x4 acc = {0, 0, 0, 0};
+#pragma unroll
+            for (int r = 0; r < SB; r++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const double w = P[c * 16 + i][r * 16 + g * 4 + j];
+                    acc = WIDE ? mma64(w, t[r][j], acc) : mma64(t[r][j], w, acc);
+                }
+#pragma unroll
+            for (int z = 0; z < 4; z++) {
+                const float v = (float)acc[z];
+                const int64_t row = WIDE ? c * 16 + g + 4 * z : k + g + 4 * z, col = WIDE ? k + i : c * 16 + i;
+                put_result<O, 1>(p, b, row, col, row < p.m && col < p.n, &v);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------ launches
+
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Largest |a v + b v^3 + c v^5| and |b v^2 + c v^4| over v in [0, top], with a
+// margin for the grid and for rounding.
+void reach(const double *c, double top, double &next, double &inner)
+{
+    next = inner = 0;
+    for (int i = 0; i <= 2048; i++) {
+        const double v = top * i / 2048, v2 = v * v;
+        inner = std::max(inner, std::fabs((c[1] + c[2] * v2) * v2));
+        next = std::max(next, std::fabs((c[0] + (c[1] + c[2] * v2) * v2) * v));
+    }
+    next *= 1.05;
+    inner *= 1.05;
+}
+
+// Exponent of the power of two that brings values of up to `top` near 2^15,
+// below fp16's largest.
+int exponent_for(double top)
+{
+    int e;
+    std::frexp(std::max(top, 1e-30), &e); // top < 2^e
+    return 15 - e;
+}
+
+float power(int e) { return std::ldexp(1.f, e); }
+
+int norm_across(int64_t n)
+{
+    int a = 1;
+    while (a < 64 && (int64_t)a * NORM_W < n)
+        a *= 2;
+    return a;
+}
+
+struct LongPlan {
+    int64_t pitch_x, pitch_s, plane_x, plane_s; // elements of a row, of one plane of one matrix
+    int parts;
+    size_t sums, x, g, part;
+    size_t total() const { return sums + 2 * x + 2 * g + part; }
+};
+
+enum { PAIR_64, PAIR_128, PAIR_PIPE_128, PAIR_PIPE_256 };
+
+struct PairPlan {
+    int tile, splits;
+};
+
+int64_t pair_tiles(int64_t M, int64_t N, int64_t t, bool sym)
+{
+    const int64_t tm = ceil_div(M, t), tn = ceil_div(N, t);
+    return sym ? tm * (tm + 1) / 2 : tm * tn;
+}
+
+PairPlan pair_plan(int64_t B, int64_t M, int64_t N, int64_t K, bool sym, int cus)
+{
+    if (B * pair_tiles(M, N, 256, sym) >= cus / 2)
+        return {PAIR_PIPE_256, 1};
+    if (B * pair_tiles(M, N, 128, sym) >= cus / 2)
+        return {PAIR_PIPE_128, 1};
+    const int64_t count = B * pair_tiles(M, N, 64, sym), steps = 3 * ceil_div(K, STEP_BYTES / 2);
+    return {PAIR_64, (int)std::max<int64_t>(1, std::min<int64_t>({2 * cus / count, steps / 8, 16}))};
+}
+
+LongPlan long_plan(int64_t B, int64_t m, int64_t n, int cus)
+{
+    const int64_t s = std::min(m, n), l = std::max(m, n);
+    LongPlan p;
+    p.pitch_x = round_up(n, 8);
+    p.pitch_s = round_up(s, 8);
+    p.plane_x = m * p.pitch_x;
+    p.plane_s = s * p.pitch_s;
+    p.parts = (int)std::max<int64_t>(1, std::min<int64_t>({NORM_MAX_PARTS, ceil_div(4 * cus, B), ceil_div(m * n, 4096), m}));
+    const auto bytes = [](int64_t b) { return (size_t)round_up(b, 256); };
+    p.sums = bytes(B * p.parts * 8);
+    p.x = bytes(2 * B * p.plane_x * 2);
+    p.g = bytes(2 * B * p.plane_s * 2);
+    const PairPlan gram = pair_plan(B, s, s, l, true, cus), square = pair_plan(B, s, s, s, true, cus),
+                   apply = pair_plan(B, m, n, s, false, cus);
+    const auto part = [&](const PairPlan &q, int64_t M, int64_t N) { return q.splits > 1 ? q.splits * B * M * N * 4 : 0; };
+    p.part = bytes(std::max({part(gram, s, s), part(square, s, s), part(apply, m, n)}));
+    return p;
+}
+
+template <typename O, int BM, int WM, int WN, bool AO, bool BO, bool SYM>
+hipError_t run_pair(PairArgs a, int64_t B, int splits, float *part, hipStream_t st)
+{
+    const int steps = 3 * (int)ceil_div(a.K, STEP_BYTES / 2), per = (int)ceil_div(steps, splits), used = (int)ceil_div(steps, per);
+    pair_kernel<O, BM, BM, WM, WN, AO, BO, SYM><<<dim3((unsigned)(B * a.tiles), (unsigned)used), WM * WN * WAVE, 0, st>>>(
+        a, per, used > 1 ? part : nullptr);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && used > 1) {
+        const int64_t cols = a.out.p ? a.out.ld : a.N, threads = B * a.M * ceil_div(cols, 4);
+        pair_join_kernel<O><<<(unsigned)ceil_div(threads, PJ_THREADS), PJ_THREADS, 0, st>>>(a, part, used, B, SYM);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+template <typename O, bool AO, bool BO, bool SYM>
+hipError_t pair_product(PairArgs a, int64_t B, float *part, int cus, hipStream_t st)
+{
+    const PairPlan p = pair_plan(B, a.M, a.N, a.K, SYM, cus);
+    const int t = p.tile == PAIR_64 ? 64 : p.tile == PAIR_PIPE_256 ? 256 : 128;
+    a.tiles_m = (int)ceil_div(a.M, t);
+    a.tiles_n = (int)ceil_div(a.N, t);
+    a.tiles = (int)pair_tiles(a.M, a.N, t, SYM);
+    if (p.tile == PAIR_64)
+        return run_pair<O, 64, 2, 2, AO, BO, SYM>(a, B, p.splits, part, st);
+    const unsigned grid = (unsigned)(B * a.tiles);
+    if (p.tile == PAIR_PIPE_128)
+        pair_pipe_kernel<O, 128, 128, 2, 4, AO, BO, SYM><<<grid, 512, 0, st>>>(a);
+    else
+        pair_pipe_kernel<O, 256, 256, 2, 4, AO, BO, SYM><<<grid, 512, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T, typename O> hipError_t run_long(const OrthoArgs &o, int cus, hipStream_t st)
+{
+    const int64_t m = o.m, n = o.n, s = std::min(m, n), l = std::max(m, n), B = o.B;
+    const bool wide = m <= n;
+    const LongPlan p = long_plan(B, m, n, cus);
+    char *ws = static_cast<char *>(o.ws);
+    double *sums = reinterpret_cast<double *>(ws);
+    const auto planes = [&](size_t at, int64_t ld, int64_t plane) {
+        return Planes{reinterpret_cast<_Float16 *>(ws + at), ld, plane, 2 * plane};
+    };
+    Planes x = planes(p.sums, p.pitch_x, p.plane_x), y = planes(p.sums + p.x, p.pitch_x, p.plane_x);
+    const Planes g = planes(p.sums + 2 * p.x, p.pitch_s, p.plane_s), h = planes(p.sums + 2 * p.x + p.g, p.pitch_s, p.plane_s);
+    float *part = reinterpret_cast<float *>(ws + p.sums + 2 * p.x + 2 * p.g);
+    const int64_t rows_per = ceil_div(m, p.parts);
+    const int across = norm_across(n);
+    const unsigned grid = (unsigned)(B * p.parts);
+    double top = 1.01; // singular values of X
+    int ex = exponent_for(top);
+    norm_kernel<T><<<grid, NORM_THREADS, 0, st>>>(o, p.parts, rows_per, across, sums);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    split_kernel<T><<<grid, NORM_THREADS, 0, st>>>(o, p.parts, rows_per, across, sums, power(ex), x.p, x.ld, x.lo, x.stride);
+    e = hipGetLastError();
+    for (int k = 0; k < o.steps && e == hipSuccess; k++) {
+        double next, inner;
+        reach(o.coef[k], top, next, inner);
+        const int eg = exponent_for(top * top), eh = exponent_for(inner), en = exponent_for(next);
+        PairArgs a{};
+        a.o = o;
+        // G
+        a.a = a.b = x;
+        a.M = a.N = (int)s;
+        a.K = (int)l;
+        a.q = power(eg - 2 * ex);
+        a.out = g;
+        e = wide ? pair_product<O, false, false, true>(a, B, part, cus, st) : pair_product<O, true, true, true>(a, B, part, cus, st);
+        if (e != hipSuccess)
+            return e;
+        // H = b G + c G^2
+        a.a = a.b = a.t = g;
+        a.K = (int)s;
+        a.p = (float)(o.coef[k][1] * power(eh - eg));
+        a.q = (float)(o.coef[k][2] * power(eh - 2 * eg));
+        a.out = h;
+        e = pair_product<O, false, false, true>(a, B, part, cus, st);
+        if (e != hipSuccess)
+            return e;
+        // a X + H X, or a X + X H
+        const bool last = k + 1 == o.steps;
+        a.a = wide ? h : x;
+        a.b = wide ? x : h;
+        a.t = x;
+        a.M = (int)m;
+        a.N = (int)n;
+        a.p = (float)(o.coef[k][0] * power(last ? -ex : en - ex));
+        a.q = power(last ? -eh - ex : en - eh - ex);
+        a.out = last ? Planes{} : y;
+        e = wide ? pair_product<O, false, true, false>(a, B, part, cus, st) : pair_product<O, false, false, false>(a, B, part, cus, st);
+        std::swap(x, y);
+        ex = en;
+        top = next;
+    }
+    return e;
+}
+
+struct ShortPlan {
+    int sb, parts;
+    int64_t per;
+    size_t part, poly;
+};
+
+ShortPlan short_plan(int64_t B, int64_t m, int64_t n, int cus)
+{
+    const int64_t s = std::min(m, n), l = std::max(m, n);
+    ShortPlan p;
+    p.sb = (int)ceil_div(s, 16);
+    const int64_t want = std::max<int64_t>(1, std::min(ceil_div(2 * cus, B), ceil_div(l, 16 * SHORT_WAVES)));
+    p.per = round_up(ceil_div(l, want), 16 * SHORT_WAVES);
+    p.parts = (int)ceil_div(l, p.per);
+    p.part = (size_t)B * p.parts * blocks_of(p.sb) * 256 * 8;
+    p.poly = (size_t)B * p.sb * p.sb * 256 * 8;
+    return p;
+}
+
+template <typename T, typename O, int SB, bool WIDE> hipError_t run_short_form(const OrthoArgs &o, const ShortPlan &p, hipStream_t st)
+{
+    double *part = static_cast<double *>(o.ws), *poly = part + p.part / 8;
+    const unsigned grid = (unsigned)(o.B * p.parts);
+    short_gram_kernel<T, SB, WIDE><<<grid, SHORT_THREADS, 0, st>>>(o, p.parts, p.per, part);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    short_poly_kernel<SB><<<(unsigned)o.B, SHORT_THREADS, 0, st>>>(o, p.parts, part, poly);
+    e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    short_apply_kernel<T, O, SB, WIDE><<<grid, SHORT_THREADS, 0, st>>>(o, p.parts, p.per, poly);
+    return hipGetLastError();
+}
+
+template <typename T, typename O, int SB> hipError_t run_short_sb(const OrthoArgs &o, const ShortPlan &p, hipStream_t st)
+{
+    return o.m <= o.n ? run_short_form<T, O, SB, true>(o, p, st) : run_short_form<T, O, SB, false>(o, p, st);
+}
+
+template <typename T, typename O> hipError_t run_short(const OrthoArgs &o, int cus, hipStream_t st)
+{
+    const ShortPlan p = short_plan(o.B, o.m, o.n, cus);
+    switch (p.sb) {
+    case 1:
+        return run_short_sb<T, O, 1>(o, p, st);
+    case 2:
+        return run_short_sb<T, O, 2>(o, p, st);
+    case 3:
+        return run_short_sb<T, O, 3>(o, p, st);
+    default:
+        return run_short_sb<T, O, 4>(o, p, st);
+    }
+}
+
+template <typename T, typename O> hipError_t run(const OrthoArgs &o, int cus, hipStream_t st)
+{
+    return std::min(o.m, o.n) <= SHORT_MAX ? run_short<T, O>(o, cus, st) : run_long<T, O>(o, cus, st);
+}
+
+} // namespace
+
+bool ortho_reach_ok(const double (*coef)[3], int steps)
+{
+    double top = 1.01;
+    for (int k = 0; k < steps; k++) {
+        double next, inner;
+        reach(coef[k], top, next, inner);
+        if (!std::isfinite(coef[k][0] + coef[k][1] + coef[k][2]) || !(next < 1e9) || !(inner < 1e9))
+            return false;
+        top = next;
+    }
+    return true;
+}
+
+size_t ortho_workspace_bytes(int64_t B, int64_t m, int64_t n, int cus)
+{
+    if (B == 0 || m == 0 || n == 0)
+        return 0;
+    if (std::min(m, n) <= SHORT_MAX) {
+        const ShortPlan p = short_plan(B, m, n, cus);
+        return p.part + p.poly;
+    }
+    return long_plan(B, m, n, cus).total();
+}
+
+hipError_t launch_ortho(const OrthoArgs &o, int update_dt, int dt, int cus, hipStream_t s)
+{
+    if (update_dt == FA_BF16)
+        return dt == FA_BF16 ? run<__bf16, __bf16>(o, cus, s) : run<__bf16, float>(o, cus, s);
+    return dt == FA_BF16 ? run<float, __bf16>(o, cus, s) : run<float, float>(o, cus, s);
+}
+
+} // namespace fa

@@ -25,6 +25,7 @@ FA_OPT_INDEX_TILES = 7
 FA_ACT_NONE, FA_ACT_RELU, FA_ACT_GELU, FA_ACT_SILU = 0, 1, 2, 3
 FA_MAX_CLIENTS = 64
 FA_MAX_TOP, FA_MAX_LIST_ENTRIES = 256, 4096
+FA_MAX_ORTHO_STEPS = 32
 FA_MAX_N = 1 << 40
 
 STATUS_NAMES = {
@@ -44,6 +45,7 @@ EXPORTS = [
     "fedavg_arena_layout",
     "linear_workspace_size", "linear_forward", "linear_backward",
     "quantize_rows", "linear_int8_workspace_size", "linear_int8_forward", "linear_int8_backward",
+    "orthogonalize_workspace_size", "orthogonalize", "orthogonal_step",
     "logits_topk_workspace_size", "logits_topk",
     "distill_workspace_size", "distill_loss", "distill_backward",
 ]
@@ -111,6 +113,10 @@ def load(build_if_missing=True):
                                  i64, P, sz, P], i32),
         "linear_int8_backward": ([i32, i64, i64, i64, P, i64, P, i64, P, i32, ctypes.c_float, P, i64, P, i64, P, P, sz,
                                   P], i32),
+        "orthogonalize_workspace_size": ([i64, i64, i64, P], i32),
+        "orthogonalize": ([i32, i64, i64, i64, P, i64, i64, P, i32, ctypes.c_float, P, i64, i64, P, sz, P], i32),
+        "orthogonal_step": ([i32, i32, i64, i64, i64, P, i64, i64, P, i64, i64, ctypes.c_float, i32, P, i32,
+                             ctypes.c_float, ctypes.c_float, P, i64, i64, P, sz, P], i32),
         "logits_topk_workspace_size": ([i32, i64, i64, i64, P], i32),
         "logits_topk": ([P, i32, i64, i64, i64, i64, ctypes.c_float, P, P, P, P, sz, P], i32),
         "distill_workspace_size": ([i32, i64, i64, P], i32),
@@ -1035,6 +1041,101 @@ def linear_int8_backward(dy, w, w_scale, act="none", preact=None, alpha=1.0, dx=
     if rc:
         _check(rc)
     return dx, db
+
+
+# ------------------------------------------------------------------ orthogonalised update
+
+# Five such steps take singular values from 0.003 of the norm on to between 0.68
+# and 1.21.
+ORTHO_COEF = (3.4445, -4.7750, 2.0315)
+
+
+def _batch(t, name, shape, dtype, dev):
+    """(row pitch, matrix stride) of [m, n] or [B, m, n] on GPU `dev`."""
+    if t is None:
+        return 0, 0
+    _on_device(t, name, dev)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    *lead, ld, inner = t.stride()
+    if inner != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must have unit stride along its rows")
+    return ld, lead[0] if lead else 0
+
+
+@functools.lru_cache(maxsize=64)
+def _coefficients(coef, steps):
+    rows = list(coef) if isinstance(coef[0], tuple) else [coef] * steps
+    if len(rows) != steps or any(len(r) != 3 for r in rows):
+        raise ValueError("coef must be three numbers, or three for each step")
+    flat = [float(v) for r in rows for v in r]
+    return (ctypes.c_double * len(flat))(*flat)
+
+
+def _coef_of(coef, steps):
+    steps = int(steps)
+    if not 1 <= steps <= FA_MAX_ORTHO_STEPS:
+        raise ValueError(f"steps must be 1 to {FA_MAX_ORTHO_STEPS}, got {steps}")
+    return _coefficients(tuple(tuple(c) if isinstance(c, (list, tuple)) else c for c in coef), steps)
+
+
+def _matrices(t, name):
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be a matrix or a batch of matrices")
+    return (t.shape[0] if t.dim() == 3 else 1), t.shape[-2], t.shape[-1]
+
+
+def orthogonalize_workspace_size(B, m, n):
+    """Device workspace bytes orthogonalize or orthogonal_step needs."""
+    b = ctypes.c_size_t(0)
+    _check(load().orthogonalize_workspace_size(int(B), int(m), int(n), ctypes.byref(b)))
+    return b.value
+
+
+def orthogonalize(x, steps=5, coef=ORTHO_COEF, scale=1.0, out=None, workspace=None, stream=None):
+    """scale times x [m, n] or [B, m, n] (float32 or bfloat16, unit stride along
+    the rows) with each matrix's singular values brought near one: `steps`
+    steps of a v + b v^3 + c v^5 after division by the Frobenius norm; coef is
+    (a, b, c), or one such triple for each step.  out is made when None and may
+    be x itself.  See orthogonalize in include/fedavg.h."""
+    lib = load()
+    (B, m, n), dt, code, dev = _matrices(x, "x"), x.dtype, _dtype(x), _device(x, "x", stream)
+    coef = _coef_of(coef, steps)
+    if out is None:
+        out = _new(tuple(x.shape), dt, x.device, stream)
+    (ldx, sx), (ldo, so) = _batch(x, "x", x.shape, dt, dev), _batch(out, "out", x.shape, dt, dev)
+    keep, ws, nbytes = _workspace(workspace, x, stream, "orthogonalize_workspace_size", B, m, n)
+    rc = lib.orthogonalize(code, B, m, n, x.data_ptr(), ldx, sx, coef, int(steps), scale, out.data_ptr(), ldo, so, ws,
+                           nbytes, _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
+    return out
+
+
+def orthogonal_step(weights, update, rate, keep=1.0, momentum=None, beta=0.95, nesterov=True, steps=5,
+                    coef=ORTHO_COEF, workspace=None, stream=None):
+    """weights = keep * weights + rate * O in place, O the orthogonalised
+    `update` (an averaged delta of the weights' shape, [m, n] or [B, m, n]), or,
+    with a float32 momentum, which is updated, of momentum = beta * momentum +
+    update (nesterov: of update + beta * momentum).  steps and coef as for
+    orthogonalize.  Returns weights.  See orthogonal_step in include/fedavg.h."""
+    lib = load()
+    (B, m, n), dev = _matrices(weights, "weights"), _device(weights, "weights", stream)
+    code, ucode = _dtype(weights), _dtype(update)
+    coef = _coef_of(coef, steps)
+    shape = weights.shape
+    ldw, sw = _batch(weights, "weights", shape, weights.dtype, dev)
+    ldu, su = _batch(update, "update", shape, update.dtype, dev)
+    ldm, sm = _batch(momentum, "momentum", shape, torch.float32, dev)
+    held, ws, nbytes = _workspace(workspace, weights, stream, "orthogonalize_workspace_size", B, m, n)
+    rc = lib.orthogonal_step(ucode, code, B, m, n, update.data_ptr(), ldu, su, _at(momentum), ldm, sm, beta,
+                             int(bool(nesterov)), coef, int(steps), rate, keep, weights.data_ptr(), ldw, sw, ws, nbytes,
+                             _raw_stream(stream, dev))
+    if rc:
+        _check(rc)
+    return weights
 
 
 # ------------------------------------------------------------------ top logits, distillation

@@ -123,11 +123,21 @@ __device__ __forceinline__ void split_value(float v, _Float16 &hi, _Float16 &lo)
     lo = (_Float16)(v - (float)hi);
 }
 
-// X = t / |t| times `scale` as hi and lo planes [m][pitch], zeros behind the rows.
+// A matrix of a batch as two planes: `lo` elements from hi to lo, `stride` from
+// one matrix to the next.  Rows and columns are followed by zeros up to a
+// multiple of PAD, the longest step of k.
+constexpr int PAD = STEP_BYTES / 2;
+
+struct Planes {
+    _Float16 *p;
+    int64_t ld, lo, stride;
+};
+
+// X = t / |t| times `scale` as planes, with their zeros; also the zeros behind the
+// rows of the second X, whose own rows each step writes whole.
 template <typename T>
 __global__ __launch_bounds__(NORM_THREADS) void split_kernel(OrthoArgs p, int parts, int64_t rows_per, int across,
-                                                             const double *sums, float scale, _Float16 *x, int64_t pitch,
-                                                             int64_t lo, int64_t stride)
+                                                             const double *sums, float scale, Planes x, Planes y, int64_t rows)
 {
     __shared__ double factor;
     int64_t b;
@@ -145,35 +155,33 @@ __global__ __launch_bounds__(NORM_THREADS) void split_kernel(OrthoArgs p, int pa
     }
     __syncthreads();
     const double f = factor;
-    const int64_t r0 = part * rows_per, r1 = r0 + rows_per < p.m ? r0 + rows_per : p.m;
+    // the last part also takes the rows behind the matrix
+    const int64_t r0 = part * rows_per, r1 = part + 1 == parts ? rows : r0 + rows_per;
     const int64_t c0 = (int64_t)(threadIdx.x % across) * NORM_W;
     for (int64_t r = r0 + threadIdx.x / across; r < r1; r += NORM_THREADS / across)
-        for (int64_t c = c0; c < pitch; c += across * NORM_W) {
+        for (int64_t c = c0; c < x.ld; c += across * NORM_W) {
             float t[NORM_W];
-            argument<T, NORM_W>(p, update_at<T>(p, b, r, c), momentum_at(p, b, r, c), false,
-                                (int)(c >= p.n ? 0 : p.n - c < NORM_W ? p.n - c : NORM_W), t);
+            const int valid = (int)(r >= p.m || c >= p.n ? 0 : p.n - c < NORM_W ? p.n - c : NORM_W);
+            argument<T, NORM_W>(p, update_at<T>(p, b, r, c), momentum_at(p, b, r, c), false, valid, t);
             f16x4 h, l;
 #pragma unroll
             for (int i = 0; i < NORM_W; i++) {
                 _Float16 hi, lw;
-                split_value(c + i < p.n ? (float)(t[i] * f) : 0.f, hi, lw);
+                split_value(i < valid ? (float)(t[i] * f) : 0.f, hi, lw);
                 h[i] = hi;
                 l[i] = lw;
             }
-            _Float16 *to = x + b * stride + r * pitch + c;
-            *reinterpret_cast<f16x4 *>(to) = h;
-            *reinterpret_cast<f16x4 *>(to + lo) = l;
+            const int64_t at = b * x.stride + r * x.ld + c;
+            *reinterpret_cast<f16x4 *>(x.p + at) = h;
+            *reinterpret_cast<f16x4 *>(x.p + at + x.lo) = l;
+            if (r >= p.m) {
+                *reinterpret_cast<f16x4 *>(y.p + at) = h;
+                *reinterpret_cast<f16x4 *>(y.p + at + y.lo) = l;
+            }
         }
 }
 
 // ------------------------------------------------------------ long sides: products
-// A matrix of a batch as two planes: `lo` elements from hi to lo, `stride` from
-// one matrix to the next; rows start on 16 bytes and are followed by zeros.
-struct Planes {
-    _Float16 *p;
-    int64_t ld, lo, stride;
-};
-
 struct PairArgs {
     Planes a, b;
     int M, N, K;
@@ -185,193 +193,360 @@ struct PairArgs {
     OrthoArgs o;
 };
 
-// Tile of the lower triangle, rows one after another.
-__device__ __forceinline__ void triangle_tile(unsigned id, unsigned &tm, unsigned &tn)
+// Consecutive workgroups go to the 8 XCDs in turn: each gets a contiguous run of
+// the tiles, so that the rows which neighbours share stay in its own L2.
+__device__ __forceinline__ unsigned xcd_order(unsigned id, unsigned total)
 {
-    tm = (unsigned)((sqrtf(8.f * (float)id + 1.f) - 1.f) * 0.5f);
-    while (tm * (tm + 1) / 2 > id)
-        tm--;
-    while ((tm + 1) * (tm + 2) / 2 <= id)
-        tm++;
-    tn = id - tm * (tm + 1) / 2;
+    const unsigned per = total / XCDS, rest = total % XCDS, x = id % XCDS;
+    return x * per + (x < rest ? x : rest) + id / XCDS;
 }
 
-// Four neighbours (m, n .. n + 3) of a finished sum, n a multiple of 4.
-template <typename O>
-__device__ __forceinline__ void finish_pair(const PairArgs &p, int64_t b, int m, int n, f32x4 s, bool mirror)
+// Tile `id` of a matrix: bands of GROUP tile rows, or, of a symmetric product,
+// the lower triangle row by row.
+template <bool SYM>
+__device__ __forceinline__ void pair_tile(unsigned id, unsigned tiles_m, unsigned tiles_n, unsigned &tm, unsigned &tn)
 {
-    if (m >= p.M || n >= (p.out.p ? p.out.ld : (int64_t)p.N)) {
-        if (!mirror)
-            return;
+    if constexpr (SYM) {
+        tm = (unsigned)((sqrtf(8.f * (float)id + 1.f) - 1.f) * 0.5f);
+        while (tm * (tm + 1) / 2 > id)
+            tm--;
+        while ((tm + 1) * (tm + 2) / 2 <= id)
+            tm++;
+        tn = id - tm * (tm + 1) / 2;
+    } else {
+        const unsigned band = GROUP * tiles_n, first = id / band * GROUP;
+        const unsigned high = tiles_m - first < GROUP ? tiles_m - first : GROUP;
+        tm = first + id % band % high;
+        tn = id % band / high;
     }
-    float v[4];
+}
+
+// Finishes EMIT neighbours of row m from their sums; n is a multiple of EMIT.
+constexpr int EMIT = 8;
+
+template <typename O>
+__device__ __forceinline__ void emit(const PairArgs &p, int64_t b, int m, int n, const float *s)
+{
+    float v[EMIT];
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < EMIT; i++)
         v[i] = p.q * s[i];
-    if (p.t.p && m < p.M && n < p.t.ld) {
+    if (p.t.p) {
         const _Float16 *at = p.t.p + b * p.t.stride + (int64_t)m * p.t.ld + n;
-        const f16x4 h = *reinterpret_cast<const f16x4 *>(at), l = *reinterpret_cast<const f16x4 *>(at + p.t.lo);
+        const f16x8 h = *reinterpret_cast<const f16x8 *>(at), l = *reinterpret_cast<const f16x8 *>(at + p.t.lo);
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < EMIT; i++)
             v[i] = __builtin_fmaf(p.p, (float)h[i] + (float)l[i], v[i]);
     }
     if (!p.out.p) {
-        const int valid = p.N - n < 4 ? p.N - n : 4;
-        put_result<O, 4>(p.o, b, m, n, valid, v);
+        put_result<O, EMIT>(p.o, b, m, n, p.N - n < EMIT ? p.N - n : EMIT, v);
         return;
     }
-    f16x4 h, l;
+    f16x8 h, l;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < EMIT; i++) {
         _Float16 hi, lw;
         split_value(v[i], hi, lw);
         h[i] = hi;
         l[i] = lw;
     }
-    _Float16 *base = p.out.p + b * p.out.stride;
-    if (m < p.M && n < p.out.ld) {
-        _Float16 *to = base + (int64_t)m * p.out.ld + n;
-        *reinterpret_cast<f16x4 *>(to) = h;
-        *reinterpret_cast<f16x4 *>(to + p.out.lo) = l;
-    }
-    if (mirror && m < p.out.ld) {
+    _Float16 *to = p.out.p + b * p.out.stride + (int64_t)m * p.out.ld + n;
+    *reinterpret_cast<f16x8 *>(to) = h;
+    *reinterpret_cast<f16x8 *>(to + p.out.lo) = l;
+}
+
+// Columns of a row that are written: planes also get the zeros behind the row.
+__device__ __forceinline__ int64_t emit_columns(const PairArgs &p) { return p.out.p ? p.out.ld : p.N; }
+
+// The finished tile goes through LDS, 16 rows of each row of wavefronts at a
+// time in two buffers that take turns, so that whole rows are read and written;
+// a symmetric product's other side is read along the columns.
+template <typename O, int BM, int BN, int WM, int WN>
+__device__ __forceinline__ void emit_tile(const PairArgs &p, int64_t b, int m0, int n0,
+                                          const f32x4 (&acc)[BM / WM / 16][BN / WN / 16], char *b0, char *b1, bool mirror)
+{
+    constexpr int THREADS = WM * WN * WAVE, FM = BM / WM / 16, FN = BN / WN / 16;
+    constexpr int ROWS = WM * 16, CHUNKS = ROWS * BN / EMIT;
+    static_assert(CHUNKS % THREADS == 0, "every thread writes as much");
+    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE, wn = (wave % WN) * (BN / WN);
+    const int64_t cols = emit_columns(p);
+    const auto row = [&](int i, int r) { return m0 + r / 16 * (BM / WM) + i * 16 + r % 16; };
+    __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            if (n + i < p.N) {
-                _Float16 *to = base + (int64_t)(n + i) * p.out.ld + m;
-                to[0] = h[i];
-                to[p.out.lo] = l[i];
+    for (int i = 0; i < FM; i++) {
+        float *o = reinterpret_cast<float *>(i & 1 ? b1 : b0);
+#pragma unroll
+        for (int j = 0; j < FN; j++)
+            *reinterpret_cast<f32x4 *>(
+                o + write_tile_at<BN>((wave / WN) * 16 + (lane & 15), wn + j * 16 + (lane >> 4) * 4)) = acc[i][j];
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < CHUNKS / THREADS; e++) {
+            const int at = threadIdx.x + e * THREADS, r = at / (BN / EMIT), c = at % (BN / EMIT) * EMIT;
+            const int m = row(i, r), n = n0 + c;
+            if (m < p.M && n < cols) {
+                float v[EMIT];
+#pragma unroll
+                for (int g = 0; g < EMIT; g += 4)
+                    __builtin_memcpy(v + g, o + write_tile_at<BN>(r, c + g), 16);
+                emit<O>(p, b, m, n, v);
             }
+        }
+        if (mirror) {
+#pragma unroll
+            for (int e = 0; e < CHUNKS / THREADS; e++) {
+                const int at = threadIdx.x + e * THREADS, c = at / (ROWS / EMIT), r = at % (ROWS / EMIT) * EMIT;
+                const int n = n0 + c, m = row(i, r);
+                if (n < p.N && m < cols) {
+                    float v[EMIT];
+#pragma unroll
+                    for (int g = 0; g < EMIT; g++)
+                        v[g] = o[write_tile_at<BN>(r + g, c & ~3) + (c & 3)];
+                    emit<O>(p, b, n, m, v);
+                }
+            }
+        }
     }
 }
 
-// The three products of the halves run as one sum over 3 K: (hi, hi), (hi, lo),
-// (lo, hi).
-// Workgroup (tile of a matrix, split).  With more than one split the sums go to
-// `part` [matrix][split][M][N].
-template <typename O, int BM, int BN, int WM, int WN, bool AO, bool BO, bool SYM>
-__global__ __launch_bounds__(WM *WN *WAVE) void pair_kernel(PairArgs p, int per, float *part)
+// A step's tiles of one operand: the hi plane's, then the lo plane's.  Planes are
+// padded with zeros, rows and columns, to whole steps, so only the tile's own
+// edge is checked, once.
+template <bool OUTER, int ROWS, int THREADS, int STEP> struct PairCopy {
+    Direct<_Float16, OUTER, ROWS, THREADS, STEP> d;
+    int64_t lo;
+
+    __device__ __forceinline__ void init(const Planes &x, int64_t b, int r0, int rows)
+    {
+        d.init(x.p + b * x.stride, x.ld, r0, rows, 0);
+        lo = x.lo * 2;
+    }
+
+    __device__ __forceinline__ void skip(int64_t steps) { d.base += steps * d.advance; }
+
+    __device__ __forceinline__ void start(char *tile)
+    {
+        d.start_whole(tile, 0);
+        d.start_whole(tile + ROWS * STEP, lo);
+        d.base += d.advance;
+    }
+};
+
+// acc += the three products of one pair of fragments.
+__device__ __forceinline__ f32x4 mma_pair(const Frag &bh, const Frag &bl, const Frag &ah, const Frag &al, f32x4 acc)
+{
+    acc = mma<_Float16>(bl, ah, acc);
+    acc = mma<_Float16>(bh, al, acc);
+    return mma<_Float16>(bh, ah, acc);
+}
+
+// Small products: workgroup (tile of a matrix, split), steps of 128 bytes in two
+// buffers.  With more than one split the sums go to `part` [matrix][split][M][N].
+template <typename O, bool AO, bool BO, bool SYM>
+__global__ __launch_bounds__(256) void pair_kernel(PairArgs p, int per, float *part)
 {
     typedef _Float16 T;
-    constexpr int THREADS = WM * WN * WAVE, BK = STEP_BYTES / 2;
-    constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
-    constexpr int AB = BM * STEP_BYTES, BB = BN * STEP_BYTES;
-    __shared__ __attribute__((aligned(1024))) char l0[AB + BB];
-    __shared__ __attribute__((aligned(1024))) char l1[AB + BB];
-
-    const int64_t bt = blockIdx.x / (unsigned)p.tiles;
+    constexpr int BM = 64, WM = 2, WN = 2, THREADS = 256, BK = STEP_BYTES / 2, F = 2;
+    constexpr int AB = BM * STEP_BYTES; // one plane of one operand
+    __shared__ __attribute__((aligned(1024))) char l0[4 * AB];
+    __shared__ __attribute__((aligned(1024))) char l1[4 * AB];
+    const unsigned id = xcd_order(blockIdx.x, gridDim.x);
+    const int64_t bt = id / (unsigned)p.tiles;
     unsigned tm, tn;
-    if constexpr (SYM)
-        triangle_tile(blockIdx.x % (unsigned)p.tiles, tm, tn);
-    else
-        tile_of(blockIdx.x % (unsigned)p.tiles, p.tiles_m, p.tiles_n, tm, tn);
-    const int m0 = (int)tm * BM, n0 = (int)tn * BN;
+    pair_tile<SYM>(id % (unsigned)p.tiles, p.tiles_m, p.tiles_n, tm, tn);
+    const int m0 = (int)tm * BM, n0 = (int)tn * BM;
     const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
-    const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
-    const int spk = (p.K + BK - 1) / BK; // steps of one of the three products
-    const int first = blockIdx.y * per, steps = 3 * spk - first < per ? 3 * spk - first : per;
-    Tile<T, BM, BN, WM, WN, AO, BO> t;
-    t.clear();
-    Direct<T, AO, BM, THREADS, STEP_BYTES> da;
-    Direct<T, BO, BN, THREADS, STEP_BYTES> db;
-    da.init(p.a.p + bt * p.a.stride, p.a.ld, m0, p.M, 0);
-    db.init(p.b.p + bt * p.b.stride, p.b.ld, n0, p.N, 0);
-    const char *a0 = da.base, *b0 = db.base;
-    t.run(l0, l1, steps, wm, wn, lane, [&](char *l, int s) {
-        const int seg = (first + s) / spk, k = (first + s) % spk;
-        da.base = a0 + (seg == 2 ? p.a.lo * 2 : 0) + k * da.advance;
-        db.base = b0 + (seg == 1 ? p.b.lo * 2 : 0) + k * db.advance;
-        da.start(l, p.K - k * BK);
-        db.start(l + AB, p.K - k * BK);
-    });
+    const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BM / WN);
+    const int all = (p.K + BK - 1) / BK, first = blockIdx.y * per, steps = all - first < per ? all - first : per;
+    f32x4 acc[F][F];
 #pragma unroll
-    for (int i = 0; i < FM; i++)
+    for (int i = 0; i < F; i++)
 #pragma unroll
-        for (int j = 0; j < FN; j++) {
+        for (int j = 0; j < F; j++)
+            acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    PairCopy<AO, BM, THREADS, STEP_BYTES> a;
+    PairCopy<BO, BM, THREADS, STEP_BYTES> b;
+    a.init(p.a, bt, m0, p.M);
+    b.init(p.b, bt, n0, p.N);
+    a.skip(first);
+    b.skip(first);
+    const auto copy = [&](char *l) {
+        a.start(l);
+        b.start(l + 2 * AB);
+    };
+    const auto step = [&](const char *l) {
+#pragma unroll
+        for (int kk = 0; kk < 2; kk++) {
+            Frag ah[F], al[F], bh[F], bl[F];
+#pragma unroll
+            for (int i = 0; i < F; i++) {
+                ah[i] = read_frag<T, AO, BM, STEP_BYTES>(l, wm + i * 16, kk, lane);
+                al[i] = read_frag<T, AO, BM, STEP_BYTES>(l + AB, wm + i * 16, kk, lane);
+                bh[i] = read_frag<T, BO, BM, STEP_BYTES>(l + 2 * AB, wn + i * 16, kk, lane);
+                bl[i] = read_frag<T, BO, BM, STEP_BYTES>(l + 3 * AB, wn + i * 16, kk, lane);
+            }
+#pragma unroll
+            for (int i = 0; i < F; i++)
+#pragma unroll
+                for (int j = 0; j < F; j++)
+                    acc[i][j] = mma_pair(bh[j], bl[j], ah[i], al[i], acc[i][j]);
+        }
+    };
+    copy(l0);
+    int s = 0;
+    for (; s + 1 < steps; s += 2) {
+        copies_done<0, true>();
+        copy(l1);
+        step(l0);
+        copies_done<0, true>();
+        if (s + 2 < steps)
+            copy(l0);
+        step(l1);
+    }
+    copies_done<0, true>();
+    if (s < steps)
+        step(l0);
+    if (!part) {
+        emit_tile<O, BM, BM, WM, WN>(p, bt, m0, n0, acc, l0, l1, SYM && tm != tn);
+        return;
+    }
+    float *to = part + (bt * gridDim.y + blockIdx.y) * p.M * p.N;
+#pragma unroll
+    for (int i = 0; i < F; i++)
+#pragma unroll
+        for (int j = 0; j < F; j++) {
             const int m = m0 + wm + i * 16 + (lane & 15), n = n0 + wn + j * 16 + (lane >> 4) * 4;
-            if (part) {
-                if (m < p.M && n < p.N) {
-                    float v[4] = {t.acc[i][j][0], t.acc[i][j][1], t.acc[i][j][2], t.acc[i][j][3]};
-                    store_n<float, 4>(part + ((bt * gridDim.y + blockIdx.y) * p.M + m) * p.N + n, p.N - n, v);
-                }
-            } else {
-                finish_pair<O>(p, bt, m, n, t.acc[i][j], SYM && tm != tn);
+            if (m < p.M && n < p.N) {
+                const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                store_n<float, 4>(to + (int64_t)m * p.N + n, p.N - n, v);
             }
         }
 }
 
-// As above for large products: steps of 64 bytes through four buffers.
+// Large products, bound by the matrix cores: steps of 64 bytes of k in two buffers.
+// A step is walked by rows of fragments of A.  Row i + 3's are read from LDS
+// while row i's products run; two rows before the step's end all its reads are
+// done, so after a barrier the copies of the step after the next take its
+// buffer, and the next step's first fragments are read behind those two rows.
+constexpr int PAIR_SLOTS = 4;
+
 template <typename O, int BM, int BN, int WM, int WN, bool AO, bool BO, bool SYM>
 __global__ __launch_bounds__(WM *WN *WAVE) void pair_pipe_kernel(PairArgs p)
 {
     typedef _Float16 T;
-    constexpr int THREADS = WM * WN * WAVE, BK = PIPE_STEP / 2;
+    constexpr int THREADS = WM * WN * WAVE, BK = PIPE_STEP / 2, STEP = PIPE_STEP;
     constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
-    constexpr int AB = BM * PIPE_STEP, BB = BN * PIPE_STEP;
-    __shared__ __attribute__((aligned(1024))) char l0[AB + BB];
-    __shared__ __attribute__((aligned(1024))) char l1[AB + BB];
-    __shared__ __attribute__((aligned(1024))) char l2[AB + BB];
-    __shared__ __attribute__((aligned(1024))) char l3[AB + BB];
-
-    const int64_t bt = blockIdx.x / (unsigned)p.tiles;
+    constexpr int AB = BM * STEP, BB = BN * STEP; // one plane of each operand
+    static_assert(FM % PAIR_SLOTS == 0, "a row keeps its registers from step to step");
+    __shared__ __attribute__((aligned(1024))) char l0[2 * (AB + BB)];
+    __shared__ __attribute__((aligned(1024))) char l1[2 * (AB + BB)];
+    const unsigned id = xcd_order(blockIdx.x, gridDim.x);
+    const int64_t bt = id / (unsigned)p.tiles;
     unsigned tm, tn;
-    if constexpr (SYM)
-        triangle_tile(blockIdx.x % (unsigned)p.tiles, tm, tn);
-    else
-        tile_of(blockIdx.x % (unsigned)p.tiles, p.tiles_m, p.tiles_n, tm, tn);
+    pair_tile<SYM>(id % (unsigned)p.tiles, p.tiles_m, p.tiles_n, tm, tn);
     const int m0 = (int)tm * BM, n0 = (int)tn * BN;
     const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
     const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
-    const int spk = (p.K + BK - 1) / BK;
-    Pipe<T, BM, BN, WM, WN, AO, BO> t;
-    Direct<T, AO, BM, THREADS, PIPE_STEP> da;
-    Direct<T, BO, BN, THREADS, PIPE_STEP> db;
-    da.init(p.a.p + bt * p.a.stride, p.a.ld, m0, p.M, 0);
-    db.init(p.b.p + bt * p.b.stride, p.b.ld, n0, p.N, 0);
-    const char *a0 = da.base, *b0 = db.base;
-    int left = p.K, seg = 0; // of the next step to copy; steps past the end copy zeros
-    t.run(l0, l1, l2, l3, 3 * spk, [&](char *l) {
-        da.start(l, left);
-        db.start(l + AB, left);
-        left -= BK;
-        if (left <= 0 && seg < 2) {
-            seg++;
-            left = p.K;
-            da.base = a0 + (seg == 2 ? p.a.lo * 2 : 0);
-            db.base = b0 + (seg == 1 ? p.b.lo * 2 : 0);
-        }
-    });
+    const int steps = (p.K + BK - 1) / BK;
+    PairCopy<AO, BM, THREADS, STEP> a;
+    PairCopy<BO, BN, THREADS, STEP> b;
+    a.init(p.a, bt, m0, p.M);
+    b.init(p.b, bt, n0, p.N);
+    f32x4 acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; i++)
 #pragma unroll
         for (int j = 0; j < FN; j++)
-            finish_pair<O>(p, bt, m0 + wm + i * 16 + (lane & 15), n0 + wn + j * 16 + (lane >> 4) * 4, t.acc[i][j],
-                           SYM && tm != tn);
+            acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    Frag ah[PAIR_SLOTS], al[PAIR_SLOTS], bh[2][FN], bl[2][FN];
+    const auto copy = [&](char *l) {
+        a.start(l);
+        b.start(l + 2 * AB);
+    };
+    const auto read_a = [&](const char *l, int i) {
+        ah[i % PAIR_SLOTS] = read_frag<T, AO, BM, STEP>(l, wm + i * 16, 0, lane);
+        al[i % PAIR_SLOTS] = read_frag<T, AO, BM, STEP>(l + AB, wm + i * 16, 0, lane);
+    };
+    const auto read_b = [&](const char *l, int s) {
+#pragma unroll
+        for (int j = 0; j < FN; j++) {
+            bh[s][j] = read_frag<T, BO, BN, STEP>(l + 2 * AB, wn + j * 16, 0, lane);
+            bl[s][j] = read_frag<T, BO, BN, STEP>(l + 2 * AB + BB, wn + j * 16, 0, lane);
+        }
+    };
+    // `more`: steps after this one, of which those from the second on are copied
+    const auto step = [&](char *cur, const char *next, int s, int more) {
+#pragma unroll
+        for (int i = 0; i < FM; i++) {
+            if (i == FM - 2) {
+                copies_done<0, true>();
+                __builtin_amdgcn_sched_barrier(0);
+                if (more > 1)
+                    copy(cur);
+                if (more > 0)
+                    read_b(next, s ^ 1);
+            }
+            if (i < FM - 3)
+                read_a(cur, i + 3);
+            else if (i >= FM - 2 && more > 0) {
+                if (i == FM - 2)
+                    read_a(next, 0);
+                else {
+                    read_a(next, 1);
+                    read_a(next, 2);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < FN; j++)
+                acc[i][j] = mma_pair(bh[s][j], bl[s][j], ah[i % PAIR_SLOTS], al[i % PAIR_SLOTS], acc[i][j]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    copy(l0);
+    copies_done<0, true>();
+    if (steps > 1)
+        copy(l1);
+    read_b(l0, 0);
+    read_a(l0, 0);
+    read_a(l0, 1);
+    read_a(l0, 2);
+    int t = 0;
+    for (; t + 3 < steps; t += 2) {
+        step(l0, l1, 0, 2);
+        step(l1, l0, 1, 2);
+    }
+    // the last one to three steps
+    step(l0, l1, 0, steps - 1 - t);
+    if (t + 1 < steps)
+        step(l1, l0, 1, steps - 2 - t);
+    if (t + 2 < steps)
+        step(l0, l1, 0, 0);
+    emit_tile<O, BM, BN, WM, WN>(p, bt, m0, n0, acc, l0, l1, SYM && tm != tn);
 }
 
-// Joins the splits' sums in their order and finishes them, four neighbours a
+// Joins the splits' sums in their order and finishes them, EMIT neighbours a
 // thread; of a symmetric product an element above the diagonal is read below it.
 constexpr int PJ_THREADS = 256;
 
 template <typename O>
 __global__ __launch_bounds__(PJ_THREADS) void pair_join_kernel(PairArgs p, const float *part, int splits, int64_t batch, bool sym)
 {
-    const int64_t cols = p.out.p ? p.out.ld : p.N, groups = (cols + 3) / 4;
+    const int64_t groups = (emit_columns(p) + EMIT - 1) / EMIT;
     const int64_t at = (int64_t)blockIdx.x * PJ_THREADS + threadIdx.x;
     if (at >= batch * p.M * groups)
         return;
     const int64_t b = at / (p.M * groups);
-    const int m = (int)(at / groups % p.M), n = (int)(at % groups) * 4;
-    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    const int m = (int)(at / groups % p.M), n = (int)(at % groups) * EMIT;
+    float s[EMIT] = {};
 #pragma unroll 4
     for (int z = 0; z < splits; z++) {
         const float *from = part + (b * splits + z) * p.M * p.N;
 #pragma unroll
-        for (int i = 0; i < 4; i++)
+        for (int i = 0; i < EMIT; i++)
             if (n + i < p.N)
                 s[i] += sym && n + i > m ? from[(int64_t)(n + i) * p.N + m] : from[(int64_t)m * p.N + n + i];
     }
-    finish_pair<O>(p, b, m, n, s, false);
+    emit<O>(p, b, m, n, s);
 }
 
 // ------------------------------------------------------------ short sides, in fp64
@@ -633,12 +808,13 @@ int norm_across(int64_t n)
 
 struct LongPlan {
     int64_t pitch_x, pitch_s, plane_x, plane_s; // elements of a row, of one plane of one matrix
+    int64_t rows_per; // rows of a part in the passes over t, none empty
     int parts;
     size_t sums, x, g, part;
     size_t total() const { return sums + 2 * x + 2 * g + part; }
 };
 
-enum { PAIR_64, PAIR_128, PAIR_PIPE_128, PAIR_PIPE_256 };
+enum { PAIR_64, PAIR_PIPE_128, PAIR_PIPE_256 };
 
 struct PairPlan {
     int tile, splits;
@@ -656,19 +832,21 @@ PairPlan pair_plan(int64_t B, int64_t M, int64_t N, int64_t K, bool sym, int cus
         return {PAIR_PIPE_256, 1};
     if (B * pair_tiles(M, N, 128, sym) >= cus / 2)
         return {PAIR_PIPE_128, 1};
-    const int64_t count = B * pair_tiles(M, N, 64, sym), steps = 3 * ceil_div(K, STEP_BYTES / 2);
-    return {PAIR_64, (int)std::max<int64_t>(1, std::min<int64_t>({2 * cus / count, steps / 8, 16}))};
+    const int64_t count = B * pair_tiles(M, N, 64, sym), steps = ceil_div(K, STEP_BYTES / 2);
+    return {PAIR_64, (int)std::max<int64_t>(1, std::min<int64_t>({2 * cus / count, steps / 3, 16}))};
 }
 
 LongPlan long_plan(int64_t B, int64_t m, int64_t n, int cus)
 {
     const int64_t s = std::min(m, n), l = std::max(m, n);
     LongPlan p;
-    p.pitch_x = round_up(n, 8);
-    p.pitch_s = round_up(s, 8);
-    p.plane_x = m * p.pitch_x;
+    p.pitch_x = round_up(n, PAD);
+    p.pitch_s = round_up(s, PAD);
+    p.plane_x = round_up(m, PAD) * p.pitch_x;
     p.plane_s = s * p.pitch_s;
-    p.parts = (int)std::max<int64_t>(1, std::min<int64_t>({NORM_MAX_PARTS, ceil_div(4 * cus, B), ceil_div(m * n, 4096), m}));
+    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>({NORM_MAX_PARTS, ceil_div(4 * cus, B), ceil_div(m * n, 4096), m}));
+    p.rows_per = ceil_div(m, parts);
+    p.parts = (int)ceil_div(m, p.rows_per);
     const auto bytes = [](int64_t b) { return (size_t)round_up(b, 256); };
     p.sums = bytes(B * p.parts * 8);
     p.x = bytes(2 * B * p.plane_x * 2);
@@ -680,15 +858,14 @@ LongPlan long_plan(int64_t B, int64_t m, int64_t n, int cus)
     return p;
 }
 
-template <typename O, int BM, int WM, int WN, bool AO, bool BO, bool SYM>
+template <typename O, bool AO, bool BO, bool SYM>
 hipError_t run_pair(PairArgs a, int64_t B, int splits, float *part, hipStream_t st)
 {
-    const int steps = 3 * (int)ceil_div(a.K, STEP_BYTES / 2), per = (int)ceil_div(steps, splits), used = (int)ceil_div(steps, per);
-    pair_kernel<O, BM, BM, WM, WN, AO, BO, SYM><<<dim3((unsigned)(B * a.tiles), (unsigned)used), WM * WN * WAVE, 0, st>>>(
-        a, per, used > 1 ? part : nullptr);
+    const int steps = (int)ceil_div(a.K, STEP_BYTES / 2), per = (int)ceil_div(steps, splits), used = (int)ceil_div(steps, per);
+    pair_kernel<O, AO, BO, SYM><<<dim3((unsigned)(B * a.tiles), (unsigned)used), 256, 0, st>>>(a, per, used > 1 ? part : nullptr);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && used > 1) {
-        const int64_t cols = a.out.p ? a.out.ld : a.N, threads = B * a.M * ceil_div(cols, 4);
+        const int64_t threads = B * a.M * ceil_div(a.out.p ? a.out.ld : a.N, EMIT);
         pair_join_kernel<O><<<(unsigned)ceil_div(threads, PJ_THREADS), PJ_THREADS, 0, st>>>(a, part, used, B, SYM);
         e = hipGetLastError();
     }
@@ -704,7 +881,7 @@ hipError_t pair_product(PairArgs a, int64_t B, float *part, int cus, hipStream_t
     a.tiles_n = (int)ceil_div(a.N, t);
     a.tiles = (int)pair_tiles(a.M, a.N, t, SYM);
     if (p.tile == PAIR_64)
-        return run_pair<O, 64, 2, 2, AO, BO, SYM>(a, B, p.splits, part, st);
+        return run_pair<O, AO, BO, SYM>(a, B, p.splits, part, st);
     const unsigned grid = (unsigned)(B * a.tiles);
     if (p.tile == PAIR_PIPE_128)
         pair_pipe_kernel<O, 128, 128, 2, 4, AO, BO, SYM><<<grid, 512, 0, st>>>(a);
@@ -726,16 +903,15 @@ template <typename T, typename O> hipError_t run_long(const OrthoArgs &o, int cu
     Planes x = planes(p.sums, p.pitch_x, p.plane_x), y = planes(p.sums + p.x, p.pitch_x, p.plane_x);
     const Planes g = planes(p.sums + 2 * p.x, p.pitch_s, p.plane_s), h = planes(p.sums + 2 * p.x + p.g, p.pitch_s, p.plane_s);
     float *part = reinterpret_cast<float *>(ws + p.sums + 2 * p.x + 2 * p.g);
-    const int64_t rows_per = ceil_div(m, p.parts);
     const int across = norm_across(n);
     const unsigned grid = (unsigned)(B * p.parts);
     double top = 1.01; // singular values of X
     int ex = exponent_for(top);
-    norm_kernel<T><<<grid, NORM_THREADS, 0, st>>>(o, p.parts, rows_per, across, sums);
+    norm_kernel<T><<<grid, NORM_THREADS, 0, st>>>(o, p.parts, p.rows_per, across, sums);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    split_kernel<T><<<grid, NORM_THREADS, 0, st>>>(o, p.parts, rows_per, across, sums, power(ex), x.p, x.ld, x.lo, x.stride);
+    split_kernel<T><<<grid, NORM_THREADS, 0, st>>>(o, p.parts, p.rows_per, across, sums, power(ex), x, y, round_up(m, PAD));
     e = hipGetLastError();
     for (int k = 0; k < o.steps && e == hipSuccess; k++) {
         double next, inner;

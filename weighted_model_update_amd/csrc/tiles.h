@@ -441,6 +441,22 @@ template <typename T, bool OUTER, int ROWS, int THREADS, int STEP> struct Direct
         }
         base += advance;
     }
+
+    // The same of an operand padded with zeros to whole steps, `shift` bytes
+    // from its base, which stays.
+    __device__ __forceinline__ void start_whole(char *tile, int64_t shift) const
+    {
+        const __amdgpu_buffer_rsrc_t rsrc =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(base + shift), 0, (int)OUT_OF_RANGE, 0x00020000);
+#pragma unroll
+        for (int c = 0; c < CH; c++) {
+            const int first = (threadIdx.x / WAVE) * WAVE + c * THREADS;
+            if (CHUNKS % THREADS != 0 && first >= CHUNKS)
+                break;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rsrc, (__attribute__((address_space(3))) void *)(tile + first * 16), 16, off[c], 0, 0, 0);
+        }
+    }
 };
 
 // s_waitcnt with at most n copies outstanding, and the LDS accesses done or as

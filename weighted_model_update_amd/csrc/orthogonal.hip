@@ -186,6 +186,11 @@ struct PairArgs {
     Planes a, b;
     int M, N, K;
     int tiles_m, tiles_n, tiles; // tiles of one matrix; symmetric: of the lower triangle
+    // The first `whole` tiles of the batch are a workgroup's each, the `rest` are
+    // split along k into `splits` of `per` steps, whose sums go to `part`.
+    unsigned whole, rest, splits;
+    int per;
+    float *part;
     // v = p T + q (sum); T absent: p is 0
     float p, q;
     Planes t;
@@ -258,55 +263,137 @@ __device__ __forceinline__ void emit(const PairArgs &p, int64_t b, int m, int n,
 // Columns of a row that are written: planes also get the zeros behind the row.
 __device__ __forceinline__ int64_t emit_columns(const PairArgs &p) { return p.out.p ? p.out.ld : p.N; }
 
-// The finished tile goes through LDS, 16 rows of each row of wavefronts at a
-// time in two buffers that take turns, so that whole rows are read and written;
-// a symmetric product's other side is read along the columns.
+// A workgroup's share: a tile of a matrix, whole or a split of it.
+struct Share {
+    int64_t b;
+    unsigned tm, tn;
+    int first, steps; // of k
+    float *part;      // where a split's sums go
+    bool mirror;      // the other side of a symmetric product is written too
+};
+
+template <bool SYM, int BM, int BN> __device__ __forceinline__ Share share_of(const PairArgs &p, int all)
+{
+    Share s{0, 0, 0, 0, all, nullptr, false};
+    unsigned id;
+    if (blockIdx.x < p.whole) {
+        id = xcd_order(blockIdx.x, p.whole);
+    } else {
+        // splits of one range of k run together: they share what they read
+        const unsigned at = xcd_order(blockIdx.x - p.whole, p.rest * p.splits), split = at / p.rest;
+        id = p.whole + at % p.rest;
+        if (p.splits > 1) {
+            s.first = (int)split * p.per;
+            s.steps = all - s.first < p.per ? all - s.first : p.per;
+            s.part = p.part + ((int64_t)(id - p.whole) * p.splits + split) * (BM * BN);
+        }
+    }
+    s.b = id / (unsigned)p.tiles;
+    pair_tile<SYM>(id % (unsigned)p.tiles, p.tiles_m, p.tiles_n, s.tm, s.tn);
+    s.mirror = SYM && s.tm != s.tn;
+    return s;
+}
+
+// Rows i of the wavefronts' fragments, which lie in LDS at `o`, 16 of each row
+// of wavefronts: whole rows are read and written; a symmetric product's other
+// side is read along the columns.
 template <typename O, int BM, int BN, int WM, int WN>
-__device__ __forceinline__ void emit_tile(const PairArgs &p, int64_t b, int m0, int n0,
-                                          const f32x4 (&acc)[BM / WM / 16][BN / WN / 16], char *b0, char *b1, bool mirror)
+__device__ __forceinline__ void emit_rows(const PairArgs &p, const Share &s, int i, const float *o)
+{
+    constexpr int THREADS = WM * WN * WAVE, ROWS = WM * 16, CHUNKS = ROWS * BN / EMIT;
+    static_assert(CHUNKS % THREADS == 0, "every thread writes as much");
+    const int64_t cols = emit_columns(p);
+    const int m0 = (int)s.tm * BM, n0 = (int)s.tn * BN;
+    const auto row = [&](int r) { return m0 + r / 16 * (BM / WM) + i * 16 + r % 16; };
+#pragma unroll
+    for (int e = 0; e < CHUNKS / THREADS; e++) {
+        const int at = threadIdx.x + e * THREADS, r = at / (BN / EMIT), c = at % (BN / EMIT) * EMIT;
+        const int m = row(r), n = n0 + c;
+        if (m < p.M && n < cols) {
+            float v[EMIT];
+#pragma unroll
+            for (int g = 0; g < EMIT; g += 4)
+                __builtin_memcpy(v + g, o + write_tile_at<BN>(r, c + g), 16);
+            emit<O>(p, s.b, m, n, v);
+        }
+    }
+    if (s.mirror) {
+#pragma unroll
+        for (int e = 0; e < CHUNKS / THREADS; e++) {
+            const int at = threadIdx.x + e * THREADS, c = at / (ROWS / EMIT), r = at % (ROWS / EMIT) * EMIT;
+            const int n = n0 + c, m = row(r);
+            if (n < p.N && m < cols) {
+                float v[EMIT];
+#pragma unroll
+                for (int g = 0; g < EMIT; g++)
+                    v[g] = o[write_tile_at<BN>(r + g, c & ~3) + (c & 3)];
+                emit<O>(p, s.b, n, m, v);
+            }
+        }
+    }
+}
+
+template <int BN, int WN> __device__ __forceinline__ int fragment_at(int j)
+{
+    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
+    return write_tile_at<BN>((wave / WN) * 16 + (lane & 15), (wave % WN) * (BN / WN) + j * 16 + (lane >> 4) * 4);
+}
+
+// The finished tile, through LDS in two buffers that take turns; a split's sums
+// go to memory as the threads hold them.
+template <typename O, int BM, int BN, int WM, int WN>
+__device__ __forceinline__ void emit_tile(const PairArgs &p, const Share &s, const f32x4 (&acc)[BM / WM / 16][BN / WN / 16],
+                                          char *b0, char *b1)
 {
     constexpr int THREADS = WM * WN * WAVE, FM = BM / WM / 16, FN = BN / WN / 16;
-    constexpr int ROWS = WM * 16, CHUNKS = ROWS * BN / EMIT;
-    static_assert(CHUNKS % THREADS == 0, "every thread writes as much");
-    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE, wn = (wave % WN) * (BN / WN);
-    const int64_t cols = emit_columns(p);
-    const auto row = [&](int i, int r) { return m0 + r / 16 * (BM / WM) + i * 16 + r % 16; };
+    if (s.part) {
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+#pragma unroll
+            for (int j = 0; j < FN; j++)
+                reinterpret_cast<f32x4 *>(s.part)[(i * FN + j) * THREADS + threadIdx.x] = acc[i][j];
+        return;
+    }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < FM; i++) {
         float *o = reinterpret_cast<float *>(i & 1 ? b1 : b0);
 #pragma unroll
         for (int j = 0; j < FN; j++)
-            *reinterpret_cast<f32x4 *>(
-                o + write_tile_at<BN>((wave / WN) * 16 + (lane & 15), wn + j * 16 + (lane >> 4) * 4)) = acc[i][j];
+            *reinterpret_cast<f32x4 *>(o + fragment_at<BN, WN>(j)) = acc[i][j];
         __syncthreads();
-#pragma unroll
-        for (int e = 0; e < CHUNKS / THREADS; e++) {
-            const int at = threadIdx.x + e * THREADS, r = at / (BN / EMIT), c = at % (BN / EMIT) * EMIT;
-            const int m = row(i, r), n = n0 + c;
-            if (m < p.M && n < cols) {
-                float v[EMIT];
-#pragma unroll
-                for (int g = 0; g < EMIT; g += 4)
-                    __builtin_memcpy(v + g, o + write_tile_at<BN>(r, c + g), 16);
-                emit<O>(p, b, m, n, v);
-            }
-        }
-        if (mirror) {
-#pragma unroll
-            for (int e = 0; e < CHUNKS / THREADS; e++) {
-                const int at = threadIdx.x + e * THREADS, c = at / (ROWS / EMIT), r = at % (ROWS / EMIT) * EMIT;
-                const int n = n0 + c, m = row(i, r);
-                if (n < p.N && m < cols) {
-                    float v[EMIT];
-#pragma unroll
-                    for (int g = 0; g < EMIT; g++)
-                        v[g] = o[write_tile_at<BN>(r + g, c & ~3) + (c & 3)];
-                    emit<O>(p, b, n, m, v);
-                }
-            }
-        }
+        emit_rows<O, BM, BN, WM, WN>(p, s, i, o);
     }
+}
+
+// Joins the splits' sums in their order: workgroup (split tile, rows i of its
+// fragments).
+template <typename O, int BM, int BN, int WM, int WN, bool SYM>
+__global__ __launch_bounds__(WM *WN *WAVE) void pair_join_kernel(PairArgs p)
+{
+    constexpr int THREADS = WM * WN * WAVE, FM = BM / WM / 16, FN = BN / WN / 16;
+    __shared__ __attribute__((aligned(16))) float o[WM * 16 * BN];
+    const unsigned tile = blockIdx.x / FM;
+    const int i = blockIdx.x % FM;
+    Share s{0, 0, 0, 0, 0, nullptr, false};
+    s.b = (p.whole + tile) / (unsigned)p.tiles;
+    pair_tile<SYM>((p.whole + tile) % (unsigned)p.tiles, p.tiles_m, p.tiles_n, s.tm, s.tn);
+    s.mirror = SYM && s.tm != s.tn;
+    const f32x4 *from = reinterpret_cast<const f32x4 *>(p.part + (int64_t)tile * p.splits * (BM * BN)) + i * FN * THREADS + threadIdx.x;
+    f32x4 sum[FN];
+#pragma unroll
+    for (int j = 0; j < FN; j++)
+        sum[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (unsigned z = 0; z < p.splits; z++)
+#pragma unroll
+        for (int j = 0; j < FN; j++)
+            sum[j] += from[z * (BM * BN / 4) + j * THREADS];
+#pragma unroll
+    for (int j = 0; j < FN; j++)
+        *reinterpret_cast<f32x4 *>(o + fragment_at<BN, WN>(j)) = sum[j];
+    __syncthreads();
+    emit_rows<O, BM, BN, WM, WN>(p, s, i, o);
 }
 
 // A step's tiles of one operand: the hi plane's, then the lo plane's.  Planes are
@@ -316,13 +403,13 @@ template <bool OUTER, int ROWS, int THREADS, int STEP> struct PairCopy {
     Direct<_Float16, OUTER, ROWS, THREADS, STEP> d;
     int64_t lo;
 
-    __device__ __forceinline__ void init(const Planes &x, int64_t b, int r0, int rows)
+    // r0: the tile's first row, of `rows`; first: its first step
+    __device__ __forceinline__ void init(const Planes &x, int64_t b, int r0, int rows, int first)
     {
         d.init(x.p + b * x.stride, x.ld, r0, rows, 0);
+        d.base += first * d.advance;
         lo = x.lo * 2;
     }
-
-    __device__ __forceinline__ void skip(int64_t steps) { d.base += steps * d.advance; }
 
     __device__ __forceinline__ void start(char *tile)
     {
@@ -340,24 +427,19 @@ __device__ __forceinline__ f32x4 mma_pair(const Frag &bh, const Frag &bl, const 
     return mma<_Float16>(bh, ah, acc);
 }
 
-// Small products: workgroup (tile of a matrix, split), steps of 128 bytes in two
-// buffers.  With more than one split the sums go to `part` [matrix][split][M][N].
+// Small products: 64 x 64 tiles, steps of 128 bytes of k in two buffers.
 template <typename O, bool AO, bool BO, bool SYM>
-__global__ __launch_bounds__(256) void pair_kernel(PairArgs p, int per, float *part)
+__global__ __launch_bounds__(256) void pair_kernel(PairArgs p)
 {
     typedef _Float16 T;
     constexpr int BM = 64, WM = 2, WN = 2, THREADS = 256, BK = STEP_BYTES / 2, F = 2;
     constexpr int AB = BM * STEP_BYTES; // one plane of one operand
     __shared__ __attribute__((aligned(1024))) char l0[4 * AB];
     __shared__ __attribute__((aligned(1024))) char l1[4 * AB];
-    const unsigned id = xcd_order(blockIdx.x, gridDim.x);
-    const int64_t bt = id / (unsigned)p.tiles;
-    unsigned tm, tn;
-    pair_tile<SYM>(id % (unsigned)p.tiles, p.tiles_m, p.tiles_n, tm, tn);
-    const int m0 = (int)tm * BM, n0 = (int)tn * BM;
+    const Share sh = share_of<SYM, BM, BM>(p, (p.K + BK - 1) / BK);
+    const int m0 = (int)sh.tm * BM, n0 = (int)sh.tn * BM, steps = sh.steps;
     const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
     const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BM / WN);
-    const int all = (p.K + BK - 1) / BK, first = blockIdx.y * per, steps = all - first < per ? all - first : per;
     f32x4 acc[F][F];
 #pragma unroll
     for (int i = 0; i < F; i++)
@@ -366,10 +448,8 @@ __global__ __launch_bounds__(256) void pair_kernel(PairArgs p, int per, float *p
             acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     PairCopy<AO, BM, THREADS, STEP_BYTES> a;
     PairCopy<BO, BM, THREADS, STEP_BYTES> b;
-    a.init(p.a, bt, m0, p.M);
-    b.init(p.b, bt, n0, p.N);
-    a.skip(first);
-    b.skip(first);
+    a.init(p.a, sh.b, m0, p.M, sh.first);
+    b.init(p.b, sh.b, n0, p.N, sh.first);
     const auto copy = [&](char *l) {
         a.start(l);
         b.start(l + 2 * AB);
@@ -406,21 +486,7 @@ __global__ __launch_bounds__(256) void pair_kernel(PairArgs p, int per, float *p
     copies_done<0, true>();
     if (s < steps)
         step(l0);
-    if (!part) {
-        emit_tile<O, BM, BM, WM, WN>(p, bt, m0, n0, acc, l0, l1, SYM && tm != tn);
-        return;
-    }
-    float *to = part + (bt * gridDim.y + blockIdx.y) * p.M * p.N;
-#pragma unroll
-    for (int i = 0; i < F; i++)
-#pragma unroll
-        for (int j = 0; j < F; j++) {
-            const int m = m0 + wm + i * 16 + (lane & 15), n = n0 + wn + j * 16 + (lane >> 4) * 4;
-            if (m < p.M && n < p.N) {
-                const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                store_n<float, 4>(to + (int64_t)m * p.N + n, p.N - n, v);
-            }
-        }
+    emit_tile<O, BM, BM, WM, WN>(p, sh, acc, l0, l1);
 }
 
 // Large products, bound by the matrix cores: steps of 64 bytes of k in two buffers.
@@ -440,18 +506,14 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pair_pipe_kernel(PairArgs p)
     static_assert(FM % PAIR_SLOTS == 0, "a row keeps its registers from step to step");
     __shared__ __attribute__((aligned(1024))) char l0[2 * (AB + BB)];
     __shared__ __attribute__((aligned(1024))) char l1[2 * (AB + BB)];
-    const unsigned id = xcd_order(blockIdx.x, gridDim.x);
-    const int64_t bt = id / (unsigned)p.tiles;
-    unsigned tm, tn;
-    pair_tile<SYM>(id % (unsigned)p.tiles, p.tiles_m, p.tiles_n, tm, tn);
-    const int m0 = (int)tm * BM, n0 = (int)tn * BN;
+    const Share sh = share_of<SYM, BM, BN>(p, (p.K + BK - 1) / BK);
+    const int m0 = (int)sh.tm * BM, n0 = (int)sh.tn * BN, steps = sh.steps;
     const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
     const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
-    const int steps = (p.K + BK - 1) / BK;
     PairCopy<AO, BM, THREADS, STEP> a;
     PairCopy<BO, BN, THREADS, STEP> b;
-    a.init(p.a, bt, m0, p.M);
-    b.init(p.b, bt, n0, p.N);
+    a.init(p.a, sh.b, m0, p.M, sh.first);
+    b.init(p.b, sh.b, n0, p.N, sh.first);
     f32x4 acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; i++)
@@ -521,32 +583,7 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pair_pipe_kernel(PairArgs p)
         step(l1, l0, 1, steps - 2 - t);
     if (t + 2 < steps)
         step(l0, l1, 0, 0);
-    emit_tile<O, BM, BN, WM, WN>(p, bt, m0, n0, acc, l0, l1, SYM && tm != tn);
-}
-
-// Joins the splits' sums in their order and finishes them, EMIT neighbours a
-// thread; of a symmetric product an element above the diagonal is read below it.
-constexpr int PJ_THREADS = 256;
-
-template <typename O>
-__global__ __launch_bounds__(PJ_THREADS) void pair_join_kernel(PairArgs p, const float *part, int splits, int64_t batch, bool sym)
-{
-    const int64_t groups = (emit_columns(p) + EMIT - 1) / EMIT;
-    const int64_t at = (int64_t)blockIdx.x * PJ_THREADS + threadIdx.x;
-    if (at >= batch * p.M * groups)
-        return;
-    const int64_t b = at / (p.M * groups);
-    const int m = (int)(at / groups % p.M), n = (int)(at % groups) * EMIT;
-    float s[EMIT] = {};
-#pragma unroll 4
-    for (int z = 0; z < splits; z++) {
-        const float *from = part + (b * splits + z) * p.M * p.N;
-#pragma unroll
-        for (int i = 0; i < EMIT; i++)
-            if (n + i < p.N)
-                s[i] += sym && n + i > m ? from[(int64_t)(n + i) * p.N + m] : from[(int64_t)m * p.N + n + i];
-    }
-    emit<O>(p, b, m, n, s);
+    emit_tile<O, BM, BN, WM, WN>(p, sh, acc, l0, l1);
 }
 
 // ------------------------------------------------------------ short sides, in fp64
@@ -814,26 +851,45 @@ struct LongPlan {
     size_t total() const { return sums + 2 * x + 2 * g + part; }
 };
 
-enum { PAIR_64, PAIR_PIPE_128, PAIR_PIPE_256 };
-
-struct PairPlan {
-    int tile, splits;
-};
-
 int64_t pair_tiles(int64_t M, int64_t N, int64_t t, bool sym)
 {
     const int64_t tm = ceil_div(M, t), tn = ceil_div(N, t);
     return sym ? tm * (tm + 1) / 2 : tm * tn;
 }
 
+// The tiles that do not fill a round of workgroups are split along k.
+struct PairPlan {
+    int tile;
+    int64_t whole, rest;
+    int splits, per;
+    size_t part_bytes() const { return splits > 1 ? (size_t)rest * splits * tile * tile * 4 : 0; }
+};
+
 PairPlan pair_plan(int64_t B, int64_t M, int64_t N, int64_t K, bool sym, int cus)
 {
-    if (B * pair_tiles(M, N, 256, sym) >= cus / 2)
-        return {PAIR_PIPE_256, 1};
-    if (B * pair_tiles(M, N, 128, sym) >= cus / 2)
-        return {PAIR_PIPE_128, 1};
-    const int64_t count = B * pair_tiles(M, N, 64, sym), steps = ceil_div(K, STEP_BYTES / 2);
-    return {PAIR_64, (int)std::max<int64_t>(1, std::min<int64_t>({2 * cus / count, steps / 3, 16}))};
+    // tile, bytes of k of a step, tiles at once on a CU, us of a step
+    static const struct {
+        int tile, step, at_once;
+        double full, alone;
+    } kinds[] = {{256, PIPE_STEP, 1, 2.4, 2.4}, {128, PIPE_STEP, 2, 1.35, 0.8}, {64, STEP_BYTES, 2, 1.0, 0.6}};
+    PairPlan best{};
+    double least = 0;
+    for (const auto &k : kinds) {
+        const int64_t count = B * pair_tiles(M, N, k.tile, sym), steps = ceil_div(2 * K, k.step), slots = (int64_t)cus * k.at_once;
+        const int64_t whole = count / slots * slots, rest = count - whole;
+        for (int s = 1; s <= 16 && (s == 1 || (rest > 0 && steps >= 4 * s)); s++) {
+            const int64_t per = ceil_div(steps, s), used = ceil_div(steps, per), groups = rest * used;
+            const double step = groups > 0 && groups <= cus ? k.alone : k.full;
+            double t = (double)(whole / slots * steps) * k.full + (double)(ceil_div(groups, slots) * per) * step;
+            if (used > 1)
+                t += 4 + (double)(groups * k.tile * k.tile) * 8 / 3.5e6;
+            if (!best.tile || t < least) {
+                best = {k.tile, whole, rest, (int)used, (int)per};
+                least = t;
+            }
+        }
+    }
+    return best;
 }
 
 LongPlan long_plan(int64_t B, int64_t m, int64_t n, int cus)
@@ -853,41 +909,42 @@ LongPlan long_plan(int64_t B, int64_t m, int64_t n, int cus)
     p.g = bytes(2 * B * p.plane_s * 2);
     const PairPlan gram = pair_plan(B, s, s, l, true, cus), square = pair_plan(B, s, s, s, true, cus),
                    apply = pair_plan(B, m, n, s, false, cus);
-    const auto part = [&](const PairPlan &q, int64_t M, int64_t N) { return q.splits > 1 ? q.splits * B * M * N * 4 : 0; };
-    p.part = bytes(std::max({part(gram, s, s), part(square, s, s), part(apply, m, n)}));
+    p.part = bytes((int64_t)std::max({gram.part_bytes(), square.part_bytes(), apply.part_bytes()}));
     return p;
 }
 
-template <typename O, bool AO, bool BO, bool SYM>
-hipError_t run_pair(PairArgs a, int64_t B, int splits, float *part, hipStream_t st)
+template <typename O, int BM, int WM, int WN, bool SYM> hipError_t join_pair(const PairArgs &a, hipStream_t st)
 {
-    const int steps = (int)ceil_div(a.K, STEP_BYTES / 2), per = (int)ceil_div(steps, splits), used = (int)ceil_div(steps, per);
-    pair_kernel<O, AO, BO, SYM><<<dim3((unsigned)(B * a.tiles), (unsigned)used), 256, 0, st>>>(a, per, used > 1 ? part : nullptr);
-    hipError_t e = hipGetLastError();
-    if (e == hipSuccess && used > 1) {
-        const int64_t threads = B * a.M * ceil_div(a.out.p ? a.out.ld : a.N, EMIT);
-        pair_join_kernel<O><<<(unsigned)ceil_div(threads, PJ_THREADS), PJ_THREADS, 0, st>>>(a, part, used, B, SYM);
-        e = hipGetLastError();
-    }
-    return e;
+    if (a.splits > 1)
+        pair_join_kernel<O, BM, BM, WM, WN, SYM><<<a.rest * (BM / WM / 16), WM * WN * WAVE, 0, st>>>(a);
+    return hipGetLastError();
 }
 
 template <typename O, bool AO, bool BO, bool SYM>
 hipError_t pair_product(PairArgs a, int64_t B, float *part, int cus, hipStream_t st)
 {
     const PairPlan p = pair_plan(B, a.M, a.N, a.K, SYM, cus);
-    const int t = p.tile == PAIR_64 ? 64 : p.tile == PAIR_PIPE_256 ? 256 : 128;
-    a.tiles_m = (int)ceil_div(a.M, t);
-    a.tiles_n = (int)ceil_div(a.N, t);
-    a.tiles = (int)pair_tiles(a.M, a.N, t, SYM);
-    if (p.tile == PAIR_64)
-        return run_pair<O, AO, BO, SYM>(a, B, p.splits, part, st);
-    const unsigned grid = (unsigned)(B * a.tiles);
-    if (p.tile == PAIR_PIPE_128)
+    a.tiles_m = (int)ceil_div(a.M, p.tile);
+    a.tiles_n = (int)ceil_div(a.N, p.tile);
+    a.tiles = (int)pair_tiles(a.M, a.N, p.tile, SYM);
+    a.whole = (unsigned)p.whole;
+    a.rest = (unsigned)p.rest;
+    a.splits = (unsigned)p.splits;
+    a.per = p.per;
+    a.part = part;
+    const unsigned grid = a.whole + a.rest * a.splits;
+    if (p.tile == 64)
+        pair_kernel<O, AO, BO, SYM><<<grid, 256, 0, st>>>(a);
+    else if (p.tile == 128)
         pair_pipe_kernel<O, 128, 128, 2, 4, AO, BO, SYM><<<grid, 512, 0, st>>>(a);
     else
         pair_pipe_kernel<O, 256, 256, 2, 4, AO, BO, SYM><<<grid, 512, 0, st>>>(a);
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    return p.tile == 64    ? join_pair<O, 64, 2, 2, SYM>(a, st)
+           : p.tile == 128 ? join_pair<O, 128, 2, 4, SYM>(a, st)
+                           : join_pair<O, 256, 2, 4, SYM>(a, st);
 }
 
 template <typename T, typename O> hipError_t run_long(const OrthoArgs &o, int cus, hipStream_t st)

@@ -109,6 +109,27 @@ def test_coefficients_and_steps(shape, coef, steps):
     check(x, fa.orthogonalize(x, steps=steps, coef=coef), coef=coef, steps=steps)
 
 
+@pytest.mark.parametrize("shape", [(70, 300), (300, 70), (2, 200, 900), (520, 2100)], ids=str)
+@pytest.mark.parametrize("coef,steps", [(QUINTIC, 5), (QUINTIC, 2), (CUBIC, 20), (((5.0, -9.0, 5.0),) + (CUBIC,) * 4, 5),
+                                        ((100.0, 0.0, 0.0), 3)], ids=["quintic", "two", "cubic", "steep", "linear"])
+def test_groups_of_steps(shape, coef, steps):
+    """bf16 results of long matrices run several steps on one Gram matrix.  Its
+    rounding, half a step of fp32, grows by at most 3e4 in a group, and H takes
+    it times |b| of at most 23: in the worst direction 3e4 23 2^-24 = 0.04 of an
+    entry, but spread over the s directions of which one in s is that one: its
+    share of the norm, 0.04 / sqrt(s), is below 0.005; groups end before that."""
+    x = update(shape, torch.bfloat16, 6)
+    want = formula(x, coef, steps, torch.float64)
+    got = fa.orthogonalize(x, steps=steps, coef=coef)
+    assert off(got, want) <= ref.half_step(torch.bfloat16) + 0.04 / math.sqrt(min(shape[-2:]))
+    # the same call with fp32 results, rounded afterwards: a step at a time
+    alone = fa.orthogonalize(x.float(), steps=steps, coef=coef)
+    assert off(got, alone.double()) <= ref.half_step(torch.bfloat16) + 0.04 / math.sqrt(min(shape[-2:]))
+    w = torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
+    fa.orthogonal_step(w, x.float(), rate=1.0, steps=steps, coef=coef)
+    assert torch.equal(w, got)
+
+
 @pytest.mark.parametrize("shape", [(40, 60), (60, 40), (100, 80), (80, 300)], ids=str)
 def test_the_largest_number_of_steps(shape):
     x = rnd(shape, torch.float32, 8)

@@ -43,6 +43,7 @@ NAN, INF = float("nan"), float("inf")
     (orthogonalize, dict(m=(1 << 15) + 1, n=(1 << 15) + 1), RANGE), (orthogonalize, dict(B=1 << 10, m=1 << 12, n=1 << 12), RANGE),
     (orthogonalize, dict(steps=0), ARG), (orthogonalize, dict(steps=33), ARG), (orthogonalize, dict(coef=None), ARG),
     (orthogonalize, dict(coef=(1e10, 0, 0)), RANGE), (orthogonalize, dict(coef=(100.0, 0, 0)), RANGE),
+    (orthogonalize, dict(coef=(8.0, -23.0, 17.0), steps=6), RANGE),
     (orthogonalize, dict(coef=(1, NAN, 0)), RANGE), (orthogonalize, dict(coef=(1, 0, INF)), RANGE),
     (orthogonalize, dict(x=None), ARG), (orthogonalize, dict(out=None), ARG), (orthogonalize, dict(x=at(1, 1)), ARG),
     (orthogonalize, dict(out=at(2, 1)), ARG), (orthogonalize, dict(ldx=-1), ARG), (orthogonalize, dict(sx=-1), ARG),

@@ -15,6 +15,16 @@
 // diagonal it would pass through every rounding of the sum (relative error 8e-6
 // instead of 2.8e-6 after 5 steps of a 512 x 512 matrix of rank 64 and noise,
 // where fp32 products give 2.5e-6).
+//
+// Steps may run on the Gram matrix alone, as for short sides: with Q = a + H
+//     G <- Q G Q,   P <- Q P,   and X <- P X at the end of the group,
+// all symmetric, so half the products.  Five steps of 14336 x 4096 take 19 products of
+// s x s and two with X instead of 15 with X: 2.1 times fewer operations.
+// Errors of G grow by up to a^2 a step instead of being left behind with the old
+// G: over five steps to 7e-6 .. 3e-5 of the result, against 2e-6 with a new Gram
+// matrix each step.  So results in bf16, which round to 2^-9, take groups (until
+// the growth passes GROWTH_MAX) where the matrix is long enough to gain; fp32
+// results take a Gram matrix each step.
 #include "tiles.h"
 
 #include <algorithm>
@@ -191,9 +201,9 @@ struct PairArgs {
     unsigned whole, rest, splits;
     int per;
     float *part;
-    // v = p T + q (sum); T absent: p is 0
-    float p, q;
-    Planes t;
+    // v = q (sum) + p T + r U, T and U nullable
+    float p, q, r;
+    Planes t, u;
     Planes out; // out.p null: the result goes to o.out
     OrthoArgs o;
 };
@@ -236,13 +246,17 @@ __device__ __forceinline__ void emit(const PairArgs &p, int64_t b, int m, int n,
 #pragma unroll
     for (int i = 0; i < EMIT; i++)
         v[i] = p.q * s[i];
-    if (p.t.p) {
-        const _Float16 *at = p.t.p + b * p.t.stride + (int64_t)m * p.t.ld + n;
-        const f16x8 h = *reinterpret_cast<const f16x8 *>(at), l = *reinterpret_cast<const f16x8 *>(at + p.t.lo);
+    const auto add = [&](const Planes &x, float f) {
+        const _Float16 *at = x.p + b * x.stride + (int64_t)m * x.ld + n;
+        const f16x8 h = *reinterpret_cast<const f16x8 *>(at), l = *reinterpret_cast<const f16x8 *>(at + x.lo);
 #pragma unroll
         for (int i = 0; i < EMIT; i++)
-            v[i] = __builtin_fmaf(p.p, (float)h[i] + (float)l[i], v[i]);
-    }
+            v[i] = __builtin_fmaf(f, (float)h[i] + (float)l[i], v[i]);
+    };
+    if (p.u.p)
+        add(p.u, p.r);
+    if (p.t.p)
+        add(p.t, p.p);
     if (!p.out.p) {
         put_result<O, EMIT>(p.o, b, m, n, p.N - n < EMIT ? p.N - n : EMIT, v);
         return;
@@ -810,19 +824,54 @@ __global__ __launch_bounds__(SHORT_THREADS) void short_apply_kernel(OrthoArgs p,
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Largest |a v + b v^3 + c v^5| and |b v^2 + c v^4| over v in [0, top], with a
-// margin for the grid and for rounding.
-void reach(const double *c, double top, double &next, double &inner)
-{
-    next = inner = 0;
-    for (int i = 0; i <= 2048; i++) {
-        const double v = top * i / 2048, v2 = v * v;
-        inner = std::max(inner, std::fabs((c[1] + c[2] * v2) * v2));
-        next = std::max(next, std::fabs((c[0] + (c[1] + c[2] * v2) * v2) * v));
+// Singular values v of X over [0, top] as they go through the steps, and with
+// them bounds of the matrices that the steps form, with a margin for the grid and
+// for rounding.
+struct Spectrum {
+    static constexpr int N = 1025;
+    double v[N], p[N]; // p: of the group's product P
+    double alpha;      // p at v = 0
+
+    void start(double top)
+    {
+        for (int i = 0; i < N; i++) {
+            v[i] = top * i / (N - 1);
+            p[i] = 1;
+        }
+        alpha = 1;
     }
-    next *= 1.05;
-    inner *= 1.05;
-}
+
+    template <typename F> double largest(F f) const
+    {
+        double most = 0;
+        for (int i = 0; i < N; i++)
+            most = std::max(most, std::fabs(f(i)));
+        return 1.05 * most;
+    }
+
+    static double inner(const double *c, double v) { return (c[1] + c[2] * v * v) * v * v; }
+    double top() const { return largest([&](int i) { return v[i]; }); }
+    double h(const double *c) const { return largest([&](int i) { return inner(c, v[i]); }); }
+    double t(const double *c) const { return largest([&](int i) { return (c[0] + inner(c, v[i])) * v[i] * v[i]; }); }
+    double k() const { return largest([&](int i) { return p[i] - alpha; }); }
+    double growth(const double *c) const
+    {
+        const double q = largest([&](int i) { return c[0] + inner(c, v[i]); });
+        return std::max(1.0, q * q);
+    }
+
+    void step(const double *c)
+    {
+        for (int i = 0; i < N; i++) {
+            const double q = c[0] + inner(c, v[i]);
+            v[i] = std::fabs(q * v[i]);
+            p[i] *= q;
+        }
+        alpha *= c[0];
+    }
+};
+
+constexpr double START_TOP = 1.01, GROWTH_MAX = 3e4;
 
 // Exponent of the power of two that brings values of up to `top` near 2^15,
 // below fp16's largest.
@@ -833,7 +882,7 @@ int exponent_for(double top)
     return 15 - e;
 }
 
-float power(int e) { return std::ldexp(1.f, e); }
+double power(int e) { return std::ldexp(1.0, e); }
 
 int norm_across(int64_t n)
 {
@@ -847,8 +896,10 @@ struct LongPlan {
     int64_t pitch_x, pitch_s, plane_x, plane_s; // elements of a row, of one plane of one matrix
     int64_t rows_per; // rows of a part in the passes over t, none empty
     int parts;
+    bool groups; // whether groups of steps on the Gram matrix pay
     size_t sums, x, g, part;
-    size_t total() const { return sums + 2 * x + 2 * g + part; }
+    int squares() const { return groups ? 5 : 2; } // s x s matrices: G, H; T, K and the next K
+    size_t total() const { return sums + 2 * x + squares() * g + part; }
 };
 
 int64_t pair_tiles(int64_t M, int64_t N, int64_t t, bool sym)
@@ -905,6 +956,7 @@ LongPlan long_plan(int64_t B, int64_t m, int64_t n, int cus)
     p.parts = (int)ceil_div(m, p.rows_per);
     const auto bytes = [](int64_t b) { return (size_t)round_up(b, 256); };
     p.sums = bytes(B * p.parts * 8);
+    p.groups = 4 * l >= 5 * s;
     p.x = bytes(2 * B * p.plane_x * 2);
     p.g = bytes(2 * B * p.plane_s * 2);
     const PairPlan gram = pair_plan(B, s, s, l, true, cus), square = pair_plan(B, s, s, s, true, cus),
@@ -951,63 +1003,108 @@ template <typename T, typename O> hipError_t run_long(const OrthoArgs &o, int cu
 {
     const int64_t m = o.m, n = o.n, s = std::min(m, n), l = std::max(m, n), B = o.B;
     const bool wide = m <= n;
-    const LongPlan p = long_plan(B, m, n, cus);
+    const LongPlan plan = long_plan(B, m, n, cus);
     char *ws = static_cast<char *>(o.ws);
     double *sums = reinterpret_cast<double *>(ws);
-    const auto planes = [&](size_t at, int64_t ld, int64_t plane) {
-        return Planes{reinterpret_cast<_Float16 *>(ws + at), ld, plane, 2 * plane};
+    ws += plan.sums;
+    const auto planes = [&](size_t bytes, int64_t ld, int64_t plane) {
+        const Planes p{reinterpret_cast<_Float16 *>(ws), ld, plane, 2 * plane};
+        ws += bytes;
+        return p;
     };
-    Planes x = planes(p.sums, p.pitch_x, p.plane_x), y = planes(p.sums + p.x, p.pitch_x, p.plane_x);
-    const Planes g = planes(p.sums + 2 * p.x, p.pitch_s, p.plane_s), h = planes(p.sums + 2 * p.x + p.g, p.pitch_s, p.plane_s);
-    float *part = reinterpret_cast<float *>(ws + p.sums + 2 * p.x + 2 * p.g);
+    Planes x = planes(plan.x, plan.pitch_x, plan.plane_x), y = planes(plan.x, plan.pitch_x, plan.plane_x), sq[5]{};
+    for (int i = 0; i < plan.squares(); i++)
+        sq[i] = planes(plan.g, plan.pitch_s, plan.plane_s);
+    Planes &g = sq[0], &h = sq[1], &t = sq[2], &kp = sq[3], &next = sq[4];
+    float *part = reinterpret_cast<float *>(ws);
     const int across = norm_across(n);
-    const unsigned grid = (unsigned)(B * p.parts);
-    double top = 1.01; // singular values of X
-    int ex = exponent_for(top);
-    norm_kernel<T><<<grid, NORM_THREADS, 0, st>>>(o, p.parts, p.rows_per, across, sums);
+    const unsigned grid = (unsigned)(B * plan.parts);
+    int ex = exponent_for(START_TOP);
+    norm_kernel<T><<<grid, NORM_THREADS, 0, st>>>(o, plan.parts, plan.rows_per, across, sums);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    split_kernel<T><<<grid, NORM_THREADS, 0, st>>>(o, p.parts, p.rows_per, across, sums, power(ex), x, y, round_up(m, PAD));
+    split_kernel<T><<<grid, NORM_THREADS, 0, st>>>(o, plan.parts, plan.rows_per, across, sums, (float)power(ex), x, y, round_up(m, PAD));
     e = hipGetLastError();
-    for (int k = 0; k < o.steps && e == hipSuccess; k++) {
-        double next, inner;
-        reach(o.coef[k], top, next, inner);
-        const int eg = exponent_for(top * top), eh = exponent_for(inner), en = exponent_for(next);
-        PairArgs a{};
-        a.o = o;
-        // G
-        a.a = a.b = x;
-        a.M = a.N = (int)s;
-        a.K = (int)l;
-        a.q = power(eg - 2 * ex);
-        a.out = g;
-        e = wide ? pair_product<O, false, false, true>(a, B, part, cus, st) : pair_product<O, true, true, true>(a, B, part, cus, st);
+
+    // out = q A B + p T + r U of symmetric s x s matrices
+    const auto square = [&](const Planes &a, const Planes &b, double q, const Planes &t, double p, const Planes &u, double r,
+                            const Planes &out) {
+        PairArgs v{};
+        v.a = a;
+        v.b = b;
+        v.M = v.N = v.K = (int)s;
+        v.q = (float)q;
+        v.t = t;
+        v.p = (float)p;
+        v.u = u;
+        v.r = (float)r;
+        v.out = out;
+        return pair_product<float, false, false, true>(v, B, part, cus, st);
+    };
+    const bool grouped = plan.groups && sizeof(O) == 2;
+    Spectrum z;
+    double top = START_TOP;
+    for (int k = 0; k < o.steps && e == hipSuccess;) {
+        z.start(top);
+        if (!h.p) // without groups, the last step's K has H's place
+            std::swap(kp, h);
+        PairArgs v{};
+        v.a = v.b = x;
+        v.M = v.N = (int)s;
+        v.K = (int)l;
+        int eg = exponent_for(top * top), ek = 0;
+        v.q = (float)power(eg - 2 * ex);
+        v.out = g;
+        e = wide ? pair_product<float, false, false, true>(v, B, part, cus, st) : pair_product<float, true, true, true>(v, B, part, cus, st);
+        double growth = 1;
+        for (bool first = true, more = true; more && e == hipSuccess; first = false, k++) {
+            const double *c = o.coef[k];
+            growth *= z.growth(c);
+            more = grouped && k + 1 < o.steps && growth <= GROWTH_MAX;
+            const int eh = exponent_for(z.h(c)), et = exponent_for(z.t(c));
+            const double alpha = z.alpha;
+            z.step(c);
+            // H = b G + c G^2
+            e = square(g, g, c[2] * power(eh - 2 * eg), g, c[1] * power(eh - eg), {}, 0, h);
+            if (more && e == hipSuccess) {
+                // T = Q G = a G + H G, then G = T Q = a T + T H
+                const int en = exponent_for(z.top() * z.top());
+                e = square(h, g, power(et - eh - eg), g, c[0] * power(et - eg), {}, 0, t);
+                if (e == hipSuccess)
+                    e = square(t, h, power(en - et - eh), t, c[0] * power(en - et), {}, 0, g);
+                eg = en;
+            }
+            // P = alpha + K: Q P = a alpha + (alpha H + a K + H K)
+            if (first) {
+                std::swap(kp, h);
+                ek = eh;
+            } else if (e == hipSuccess) {
+                const int en = exponent_for(z.k());
+                e = square(h, kp, power(en - eh - ek), kp, c[0] * power(en - ek), h, alpha * power(en - eh), next);
+                std::swap(kp, next);
+                ek = en;
+            }
+        }
         if (e != hipSuccess)
             return e;
-        // H = b G + c G^2
-        a.a = a.b = a.t = g;
-        a.K = (int)s;
-        a.p = (float)(o.coef[k][1] * power(eh - eg));
-        a.q = (float)(o.coef[k][2] * power(eh - 2 * eg));
-        a.out = h;
-        e = pair_product<O, false, false, true>(a, B, part, cus, st);
-        if (e != hipSuccess)
-            return e;
-        // a X + H X, or a X + X H
-        const bool last = k + 1 == o.steps;
-        a.a = wide ? h : x;
-        a.b = wide ? x : h;
-        a.t = x;
-        a.M = (int)m;
-        a.N = (int)n;
-        a.p = (float)(o.coef[k][0] * power(last ? -ex : en - ex));
-        a.q = power(last ? -eh - ex : en - eh - ex);
-        a.out = last ? Planes{} : y;
-        e = wide ? pair_product<O, false, true, false>(a, B, part, cus, st) : pair_product<O, false, false, false>(a, B, part, cus, st);
+        // X = alpha X + K X, or alpha X + X K
+        const bool last = k == o.steps;
+        top = z.top();
+        const int en = exponent_for(top);
+        v.o = o;
+        v.a = wide ? kp : x;
+        v.b = wide ? x : kp;
+        v.t = x;
+        v.M = (int)m;
+        v.N = (int)n;
+        v.K = (int)s;
+        v.p = (float)(z.alpha * power(last ? -ex : en - ex));
+        v.q = (float)power(last ? -ek - ex : en - ek - ex);
+        v.out = last ? Planes{} : y;
+        e = wide ? pair_product<O, false, true, false>(v, B, part, cus, st) : pair_product<O, false, false, false>(v, B, part, cus, st);
         std::swap(x, y);
         ex = en;
-        top = next;
     }
     return e;
 }
@@ -1076,13 +1173,14 @@ template <typename T, typename O> hipError_t run(const OrthoArgs &o, int cus, hi
 
 bool ortho_reach_ok(const double (*coef)[3], int steps)
 {
-    double top = 1.01;
+    Spectrum z;
+    z.start(START_TOP);
     for (int k = 0; k < steps; k++) {
-        double next, inner;
-        reach(coef[k], top, next, inner);
-        if (!std::isfinite(coef[k][0] + coef[k][1] + coef[k][2]) || !(next < 1e9) || !(inner < 1e9))
+        if (!std::isfinite(coef[k][0] + coef[k][1] + coef[k][2]) || !(z.h(coef[k]) < 1e9))
             return false;
-        top = next;
+        z.step(coef[k]);
+        if (!(z.top() < 1e9))
+            return false;
     }
     return true;
 }

@@ -88,10 +88,59 @@ __device__ __forceinline__ void matrix_of(int64_t id, int parts, int64_t &b, int
 }
 
 // ------------------------------------------------------------ long sides: norm and first X
-// Four columns a thread, `across` (a power of two) threads to a row; bound by
-// memory.  The squares are summed in fp64, in an order fixed by the sizes.
-constexpr int NORM_THREADS = 256, NORM_W = 4, NORM_MAX_PARTS = 256;
+// Bound by memory.  A part is some rows of a matrix; `across` (a power of two)
+// threads stand side by side on NORM_W columns each, and every thread has NORM_U
+// such pieces on their way at a time.  14336 x 4096 bf16: the squares' sum in
+// NORM_US1 us, the split into halves in NORM_US2 (352 MB moved).
+constexpr int NORM_THREADS = 256, NORM_W = 8, NORM_U = 4, NORM_MAX_PARTS = 1024;
 
+// Walks the pieces of rows [r0, r1), columns [0, cols): take(r, c, t) gets the
+// argument's values at c .. c + NORM_W - 1, 0 where t has none.
+template <typename T, typename F>
+__device__ __forceinline__ void walk(const OrthoArgs &p, int64_t b, int64_t r0, int64_t r1, int64_t cols, int across, bool update,
+                                     F take)
+{
+    const unsigned groups = NORM_THREADS / across, wide = (unsigned)((cols + across * NORM_W - 1) / (across * NORM_W));
+    const unsigned all = (unsigned)(r1 - r0) * wide; // a part has at most 2^23 pieces
+    const int64_t c0 = (int64_t)(threadIdx.x % across) * NORM_W;
+    for (unsigned q0 = threadIdx.x / across; q0 < all; q0 += groups * NORM_U) {
+        Raw<T, NORM_W> u[NORM_U];
+        Raw<float, NORM_W> m[NORM_U];
+        int64_t r[NORM_U], c[NORM_U];
+        int valid[NORM_U];
+#pragma unroll
+        for (int e = 0; e < NORM_U; e++) {
+            const unsigned q = q0 + e * groups;
+            r[e] = q < all ? r0 + q / wide : r1;
+            c[e] = (int64_t)(q % wide) * (across * NORM_W) + c0;
+            valid[e] = (int)(r[e] >= r1 || r[e] >= p.m || c[e] >= p.n ? 0 : p.n - c[e] < NORM_W ? p.n - c[e] : NORM_W);
+            u[e].fetch(update_at<T>(p, b, r[e], c[e]), valid[e]);
+            if (p.momentum)
+                m[e].fetch(momentum_at(p, b, r[e], c[e]), valid[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < NORM_U; e++) {
+            if (r[e] >= r1)
+                break;
+            float t[NORM_W];
+#pragma unroll
+            for (int i = 0; i < NORM_W; i++) {
+                t[i] = (float)u[e].e[i];
+                if (p.momentum) {
+                    if (update)
+                        m[e].e[i] = __builtin_fmaf(p.beta, m[e].e[i], t[i]);
+                    t[i] = p.nesterov ? __builtin_fmaf(p.beta, m[e].e[i], t[i]) : m[e].e[i];
+                }
+                t[i] = i < valid[e] ? t[i] : 0.f;
+            }
+            if (update && p.momentum)
+                store_n<float, NORM_W>(momentum_at(p, b, r[e], c[e]), valid[e], m[e].e);
+            take(r[e], c[e], t);
+        }
+    }
+}
+
+// The squares are summed in fp64, in an order fixed by the sizes.
 template <typename T>
 __global__ __launch_bounds__(NORM_THREADS) void norm_kernel(OrthoArgs p, int parts, int64_t rows_per, int across, double *sums)
 {
@@ -100,17 +149,12 @@ __global__ __launch_bounds__(NORM_THREADS) void norm_kernel(OrthoArgs p, int par
     int part;
     matrix_of(blockIdx.x, parts, b, part);
     const int64_t r0 = part * rows_per, r1 = r0 + rows_per < p.m ? r0 + rows_per : p.m;
-    const int64_t c0 = (int64_t)(threadIdx.x % across) * NORM_W;
     double sum = 0;
-    for (int64_t r = r0 + threadIdx.x / across; r < r1; r += NORM_THREADS / across)
-        for (int64_t c = c0; c < p.n; c += across * NORM_W) {
-            float t[NORM_W];
-            argument<T, NORM_W>(p, update_at<T>(p, b, r, c), momentum_at(p, b, r, c), true,
-                                (int)(p.n - c < NORM_W ? p.n - c : NORM_W), t);
+    walk<T>(p, b, r0, r1, p.n, across, true, [&](int64_t, int64_t, const float *t) {
 #pragma unroll
-            for (int i = 0; i < NORM_W; i++)
-                sum += c + i < p.n ? (double)t[i] * t[i] : 0.0;
-        }
+        for (int i = 0; i < NORM_W; i++)
+            sum += (double)t[i] * t[i];
+    });
 #pragma unroll
     for (int d = 1; d < WAVE; d *= 2)
         sum += __shfl_xor(sum, d);
@@ -155,6 +199,7 @@ __global__ __launch_bounds__(NORM_THREADS) void split_kernel(OrthoArgs p, int pa
     matrix_of(blockIdx.x, parts, b, part);
     if (threadIdx.x < WAVE) {
         double sum = 0;
+#pragma unroll 4
         for (int i = threadIdx.x; i < parts; i += WAVE)
             sum += sums[b * parts + i];
 #pragma unroll
@@ -165,29 +210,29 @@ __global__ __launch_bounds__(NORM_THREADS) void split_kernel(OrthoArgs p, int pa
     }
     __syncthreads();
     const double f = factor;
-    // the last part also takes the rows behind the matrix
-    const int64_t r0 = part * rows_per, r1 = part + 1 == parts ? rows : r0 + rows_per;
-    const int64_t c0 = (int64_t)(threadIdx.x % across) * NORM_W;
-    for (int64_t r = r0 + threadIdx.x / across; r < r1; r += NORM_THREADS / across)
-        for (int64_t c = c0; c < x.ld; c += across * NORM_W) {
-            float t[NORM_W];
-            const int valid = (int)(r >= p.m || c >= p.n ? 0 : p.n - c < NORM_W ? p.n - c : NORM_W);
-            argument<T, NORM_W>(p, update_at<T>(p, b, r, c), momentum_at(p, b, r, c), false, valid, t);
-            f16x4 h, l;
+    const int64_t r0 = part * rows_per, r1 = r0 + rows_per < p.m ? r0 + rows_per : p.m;
+    walk<T>(p, b, r0, r1, x.ld, across, false, [&](int64_t r, int64_t c, const float *t) {
+        if (c >= x.ld)
+            return;
+        f16x8 h, l;
 #pragma unroll
-            for (int i = 0; i < NORM_W; i++) {
-                _Float16 hi, lw;
-                split_value(i < valid ? (float)(t[i] * f) : 0.f, hi, lw);
-                h[i] = hi;
-                l[i] = lw;
-            }
+        for (int i = 0; i < NORM_W; i++) {
+            _Float16 hi, lw;
+            split_value((float)(t[i] * f), hi, lw);
+            // zeros stay zeros behind a row of a matrix whose norm is NaN
+            h[i] = c + i < p.n ? hi : (_Float16)0;
+            l[i] = c + i < p.n ? lw : (_Float16)0;
+        }
+        const int64_t at = b * x.stride + r * x.ld + c;
+        *reinterpret_cast<f16x8 *>(x.p + at) = h;
+        *reinterpret_cast<f16x8 *>(x.p + at + x.lo) = l;
+    });
+    // the rows behind the matrix, of both X
+    for (int64_t r = p.m + part; r < rows; r += parts)
+        for (int64_t c = threadIdx.x * NORM_W; c < x.ld; c += NORM_THREADS * NORM_W) {
             const int64_t at = b * x.stride + r * x.ld + c;
-            *reinterpret_cast<f16x4 *>(x.p + at) = h;
-            *reinterpret_cast<f16x4 *>(x.p + at + x.lo) = l;
-            if (r >= p.m) {
-                *reinterpret_cast<f16x4 *>(y.p + at) = h;
-                *reinterpret_cast<f16x4 *>(y.p + at + y.lo) = l;
-            }
+            for (_Float16 *to : {x.p + at, x.p + at + x.lo, y.p + at, y.p + at + y.lo})
+                *reinterpret_cast<f16x8 *>(to) = f16x8{};
         }
 }
 
@@ -312,7 +357,7 @@ template <bool SYM, int BM, int BN> __device__ __forceinline__ Share share_of(co
 // of wavefronts: whole rows are read and written; a symmetric product's other
 // side is read along the columns.
 template <typename O, int BM, int BN, int WM, int WN>
-__device__ __forceinline__ void emit_rows(const PairArgs &p, const Share &s, int i, const float *o)
+__device__ __forceinline__ void emit_rows(const PairArgs &p, const Share &s, int i, const float *o, int thread)
 {
     constexpr int THREADS = WM * WN * WAVE, ROWS = WM * 16, CHUNKS = ROWS * BN / EMIT;
     static_assert(CHUNKS % THREADS == 0, "every thread writes as much");
@@ -321,7 +366,7 @@ __device__ __forceinline__ void emit_rows(const PairArgs &p, const Share &s, int
     const auto row = [&](int r) { return m0 + r / 16 * (BM / WM) + i * 16 + r % 16; };
 #pragma unroll
     for (int e = 0; e < CHUNKS / THREADS; e++) {
-        const int at = threadIdx.x + e * THREADS, r = at / (BN / EMIT), c = at % (BN / EMIT) * EMIT;
+        const int at = thread + e * THREADS, r = at / (BN / EMIT), c = at % (BN / EMIT) * EMIT;
         const int m = row(r), n = n0 + c;
         if (m < p.M && n < cols) {
             float v[EMIT];
@@ -334,7 +379,7 @@ __device__ __forceinline__ void emit_rows(const PairArgs &p, const Share &s, int
     if (s.mirror) {
 #pragma unroll
         for (int e = 0; e < CHUNKS / THREADS; e++) {
-            const int at = threadIdx.x + e * THREADS, c = at / (ROWS / EMIT), r = at % (ROWS / EMIT) * EMIT;
+            const int at = thread + e * THREADS, c = at / (ROWS / EMIT), r = at % (ROWS / EMIT) * EMIT;
             const int n = n0 + c, m = row(r);
             if (n < p.N && m < cols) {
                 float v[EMIT];
@@ -347,9 +392,9 @@ __device__ __forceinline__ void emit_rows(const PairArgs &p, const Share &s, int
     }
 }
 
-template <int BN, int WN> __device__ __forceinline__ int fragment_at(int j)
+template <int BN, int WN> __device__ __forceinline__ int fragment_at(int j, int thread)
 {
-    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
+    const int wave = thread / WAVE, lane = thread % WAVE;
     return write_tile_at<BN>((wave / WN) * 16 + (lane & 15), (wave % WN) * (BN / WN) + j * 16 + (lane >> 4) * 4);
 }
 
@@ -374,9 +419,9 @@ __device__ __forceinline__ void emit_tile(const PairArgs &p, const Share &s, con
         float *o = reinterpret_cast<float *>(i & 1 ? b1 : b0);
 #pragma unroll
         for (int j = 0; j < FN; j++)
-            *reinterpret_cast<f32x4 *>(o + fragment_at<BN, WN>(j)) = acc[i][j];
+            *reinterpret_cast<f32x4 *>(o + fragment_at<BN, WN>(j, threadIdx.x)) = acc[i][j];
         __syncthreads();
-        emit_rows<O, BM, BN, WM, WN>(p, s, i, o);
+        emit_rows<O, BM, BN, WM, WN>(p, s, i, o, threadIdx.x);
     }
 }
 
@@ -405,9 +450,9 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pair_join_kernel(PairArgs p)
             sum[j] += from[z * (BM * BN / 4) + j * THREADS];
 #pragma unroll
     for (int j = 0; j < FN; j++)
-        *reinterpret_cast<f32x4 *>(o + fragment_at<BN, WN>(j)) = sum[j];
+        *reinterpret_cast<f32x4 *>(o + fragment_at<BN, WN>(j, threadIdx.x)) = sum[j];
     __syncthreads();
-    emit_rows<O, BM, BN, WM, WN>(p, s, i, o);
+    emit_rows<O, BM, BN, WM, WN>(p, s, i, o, threadIdx.x);
 }
 
 // A step's tiles of one operand: the hi plane's, then the lo plane's.  Planes are
@@ -441,18 +486,28 @@ __device__ __forceinline__ f32x4 mma_pair(const Frag &bh, const Frag &bl, const 
     return mma<_Float16>(bh, ah, acc);
 }
 
-// Small products: 64 x 64 tiles, steps of 128 bytes of k in two buffers.
-template <typename O, bool AO, bool BO, bool SYM>
-__global__ __launch_bounds__(256) void pair_kernel(PairArgs p)
+// Small products: 64 x 64 tiles, steps of 128 bytes of k.  Two groups of four
+// wavefronts take half a step's k each, since one wavefront a SIMD leaves the
+// matrix cores idle while it reads LDS; their sums are joined at the end.  With
+// a tile a CU or fewer a step waits for memory, and four buffers (DEEP) let three
+// steps be on their way; with more tiles two workgroups a CU, with two buffers
+// each, hide it.  PAIR64_NOTE
+template <typename O, bool AO, bool BO, bool SYM, bool DEEP>
+__global__ __launch_bounds__(512) void pair_kernel(PairArgs p)
 {
     typedef _Float16 T;
-    constexpr int BM = 64, WM = 2, WN = 2, THREADS = 256, BK = STEP_BYTES / 2, F = 2;
+    constexpr int BM = 64, WM = 2, WN = 2, GROUP_THREADS = WM * WN * WAVE, THREADS = 2 * GROUP_THREADS;
+    constexpr int BK = STEP_BYTES / 2, F = 2;
     constexpr int AB = BM * STEP_BYTES; // one plane of one operand
+    constexpr int COPIES = 4 * AB / 16 / THREADS; // per thread and step
     __shared__ __attribute__((aligned(1024))) char l0[4 * AB];
     __shared__ __attribute__((aligned(1024))) char l1[4 * AB];
+    __shared__ __attribute__((aligned(1024))) char l2[DEEP ? 4 * AB : 16];
+    __shared__ __attribute__((aligned(1024))) char l3[DEEP ? 4 * AB : 16];
     const Share sh = share_of<SYM, BM, BM>(p, (p.K + BK - 1) / BK);
     const int m0 = (int)sh.tm * BM, n0 = (int)sh.tn * BM, steps = sh.steps;
-    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
+    const int group = threadIdx.x / GROUP_THREADS, thread = threadIdx.x % GROUP_THREADS;
+    const int wave = thread / WAVE, lane = thread % WAVE;
     const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BM / WN);
     f32x4 acc[F][F];
 #pragma unroll
@@ -469,38 +524,88 @@ __global__ __launch_bounds__(256) void pair_kernel(PairArgs p)
         b.start(l + 2 * AB);
     };
     const auto step = [&](const char *l) {
+        Frag ah[F], al[F], bh[F], bl[F];
 #pragma unroll
-        for (int kk = 0; kk < 2; kk++) {
-            Frag ah[F], al[F], bh[F], bl[F];
-#pragma unroll
-            for (int i = 0; i < F; i++) {
-                ah[i] = read_frag<T, AO, BM, STEP_BYTES>(l, wm + i * 16, kk, lane);
-                al[i] = read_frag<T, AO, BM, STEP_BYTES>(l + AB, wm + i * 16, kk, lane);
-                bh[i] = read_frag<T, BO, BM, STEP_BYTES>(l + 2 * AB, wn + i * 16, kk, lane);
-                bl[i] = read_frag<T, BO, BM, STEP_BYTES>(l + 3 * AB, wn + i * 16, kk, lane);
-            }
-#pragma unroll
-            for (int i = 0; i < F; i++)
-#pragma unroll
-                for (int j = 0; j < F; j++)
-                    acc[i][j] = mma_pair(bh[j], bl[j], ah[i], al[i], acc[i][j]);
+        for (int i = 0; i < F; i++) {
+            ah[i] = read_frag<T, AO, BM, STEP_BYTES>(l, wm + i * 16, group, lane);
+            al[i] = read_frag<T, AO, BM, STEP_BYTES>(l + AB, wm + i * 16, group, lane);
+            bh[i] = read_frag<T, BO, BM, STEP_BYTES>(l + 2 * AB, wn + i * 16, group, lane);
+            bl[i] = read_frag<T, BO, BM, STEP_BYTES>(l + 3 * AB, wn + i * 16, group, lane);
         }
+#pragma unroll
+        for (int i = 0; i < F; i++)
+#pragma unroll
+            for (int j = 0; j < F; j++)
+                acc[i][j] = mma_pair(bh[j], bl[j], ah[i], al[i], acc[i][j]);
     };
-    copy(l0);
-    int s = 0;
-    for (; s + 1 < steps; s += 2) {
+    if constexpr (DEEP) {
+        // step t from `cur`; `free` held step t - 1 and takes step t + 3
+        const auto turn = [&](const char *cur, char *free, int t) {
+            if (t + 2 < steps)
+                copies_done<2 * COPIES, true>();
+            else if (t + 1 < steps)
+                copies_done<COPIES, true>();
+            else
+                copies_done<0, true>();
+            if (t + 3 < steps)
+                copy(free);
+            step(cur);
+        };
+        copy(l0);
+        if (steps > 1)
+            copy(l1);
+        if (steps > 2)
+            copy(l2);
+        for (int t = 0; t < steps; t += 4) {
+            turn(l0, l3, t);
+            if (t + 1 < steps)
+                turn(l1, l0, t + 1);
+            if (t + 2 < steps)
+                turn(l2, l1, t + 2);
+            if (t + 3 < steps)
+                turn(l3, l2, t + 3);
+        }
+    } else {
+        copy(l0);
+        int s = 0;
+        for (; s + 1 < steps; s += 2) {
+            copies_done<0, true>();
+            copy(l1);
+            step(l0);
+            copies_done<0, true>();
+            if (s + 2 < steps)
+                copy(l0);
+            step(l1);
+        }
         copies_done<0, true>();
-        copy(l1);
-        step(l0);
-        copies_done<0, true>();
-        if (s + 2 < steps)
-            copy(l0);
-        step(l1);
+        if (s < steps)
+            step(l0);
     }
-    copies_done<0, true>();
-    if (s < steps)
-        step(l0);
-    emit_tile<O, BM, BM, WM, WN>(p, sh, acc, l0, l1);
+    // the second group's sums of fragments i = 0 go to the first, the first's of
+    // i = 1 to the second, and each finishes its own
+    __syncthreads();
+    f32x4 *give = reinterpret_cast<f32x4 *>(l0), mine[F];
+#pragma unroll
+    for (int j = 0; j < F; j++)
+        give[(group * F + j) * GROUP_THREADS + thread] = group == 0 ? acc[1][j] : acc[0][j];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < F; j++) {
+        const f32x4 other = give[((group ^ 1) * F + j) * GROUP_THREADS + thread];
+        mine[j] = (group == 0 ? acc[0][j] : acc[1][j]) + other;
+    }
+    if (sh.part) {
+#pragma unroll
+        for (int j = 0; j < F; j++)
+            reinterpret_cast<f32x4 *>(sh.part)[(group * F + j) * GROUP_THREADS + thread] = mine[j];
+        return;
+    }
+    float *o = reinterpret_cast<float *>(l1 + group * 2 * AB);
+#pragma unroll
+    for (int j = 0; j < F; j++)
+        *reinterpret_cast<f32x4 *>(o + fragment_at<BM, WN>(j, thread)) = mine[j];
+    __syncthreads();
+    emit_rows<O, BM, BM, WM, WN>(p, sh, group, o, thread);
 }
 
 // Large products, bound by the matrix cores: steps of 64 bytes of k in two buffers.
@@ -985,8 +1090,10 @@ hipError_t pair_product(PairArgs a, int64_t B, float *part, int cus, hipStream_t
     a.per = p.per;
     a.part = part;
     const unsigned grid = a.whole + a.rest * a.splits;
-    if (p.tile == 64)
-        pair_kernel<O, AO, BO, SYM><<<grid, 256, 0, st>>>(a);
+    if (p.tile == 64 && grid <= (unsigned)cus)
+        pair_kernel<O, AO, BO, SYM, true><<<grid, 512, 0, st>>>(a);
+    else if (p.tile == 64)
+        pair_kernel<O, AO, BO, SYM, false><<<grid, 512, 0, st>>>(a);
     else if (p.tile == 128)
         pair_pipe_kernel<O, 128, 128, 2, 4, AO, BO, SYM><<<grid, 512, 0, st>>>(a);
     else

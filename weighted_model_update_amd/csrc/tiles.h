@@ -193,10 +193,18 @@ template <typename T, int W> struct Raw {
     {
         if (valid >= W) {
             __builtin_memcpy(e, p, sizeof e);
+        } else if (valid > 0) {
+            // no load is under a condition of its own, so none waits for another
+#pragma unroll
+            for (int i = 0; i < W; i++)
+                e[i] = p[i < valid ? i : valid - 1];
+#pragma unroll
+            for (int i = 0; i < W; i++)
+                e[i] = i < valid ? e[i] : (T)0;
         } else {
 #pragma unroll
             for (int i = 0; i < W; i++)
-                e[i] = i < valid ? p[i] : (T)0;
+                e[i] = (T)0;
         }
     }
 };
@@ -461,14 +469,14 @@ template <typename T, bool OUTER, int ROWS, int THREADS, int STEP> struct Direct
 
 // s_waitcnt with at most n copies outstanding, and the LDS accesses done or as
 // they are.
-constexpr int wait_copies(int n, bool lds) { return 0x0070 | n | (lds ? 0 : 0x0f00); }
+constexpr int wait_copies(int n, bool lds) { return 0x0070 | (n & 15) | (n >> 4) << 14 | (lds ? 0 : 0x0f00); }
 
 // Waits for all but the last COPIES of this wavefront's copies into LDS, with
 // LDS also for its reads, then for the other wavefronts; no access to memory
 // moves across.
 template <int COPIES, bool LDS> __device__ __forceinline__ void copies_done()
 {
-    static_assert(COPIES < 16, "the counter's low bits");
+    static_assert(COPIES < 64, "the counter's bits");
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(wait_copies(COPIES, LDS));
     __builtin_amdgcn_s_barrier();

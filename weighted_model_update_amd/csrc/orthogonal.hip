@@ -608,14 +608,16 @@ __global__ __launch_bounds__(512) void pair_kernel(PairArgs p)
     emit_rows<O, BM, BM, WM, WN>(p, sh, group, o, thread);
 }
 
-// Large products, bound by the matrix cores: steps of 64 bytes of k in two buffers.
-// A step is walked by rows of fragments of A.  Row i + 3's are read from LDS
-// while row i's products run; two rows before the step's end all its reads are
-// done, so after a barrier the copies of the step after the next take its
-// buffer, and the next step's first fragments are read behind those two rows.
+// Larger products, bound by the matrix cores: steps of 64 bytes of k in BUFS
+// buffers.  A step is walked by rows of fragments of A.  Row i + 3's are read
+// from LDS while row i's products run; two rows before the step's end all its
+// reads are done, so after a barrier the copies of step t + BUFS take its buffer,
+// and the next step's first fragments are read behind those two rows.  Two
+// 128 x 128 tiles share a CU with two buffers each; one alone takes four, since
+// its step is shorter than the way from memory.  PAIRPIPE_NOTE
 constexpr int PAIR_SLOTS = 4;
 
-template <typename O, int BM, int BN, int WM, int WN, bool AO, bool BO, bool SYM>
+template <typename O, int BM, int BN, int WM, int WN, bool AO, bool BO, bool SYM, int BUFS>
 __global__ __launch_bounds__(WM *WN *WAVE) void pair_pipe_kernel(PairArgs p)
 {
     typedef _Float16 T;
@@ -625,6 +627,10 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pair_pipe_kernel(PairArgs p)
     static_assert(FM % PAIR_SLOTS == 0, "a row keeps its registers from step to step");
     __shared__ __attribute__((aligned(1024))) char l0[2 * (AB + BB)];
     __shared__ __attribute__((aligned(1024))) char l1[2 * (AB + BB)];
+    __shared__ __attribute__((aligned(1024))) char l2[BUFS == 4 ? 2 * (AB + BB) : 16];
+    __shared__ __attribute__((aligned(1024))) char l3[BUFS == 4 ? 2 * (AB + BB) : 16];
+    constexpr int COPIES = 2 * (AB + BB) / 16 / THREADS; // per thread and step
+    static_assert(BUFS == 2 || BUFS == 4, "the buffers above");
     const Share sh = share_of<SYM, BM, BN>(p, (p.K + BK - 1) / BK);
     const int m0 = (int)sh.tm * BM, n0 = (int)sh.tn * BN, steps = sh.steps;
     const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
@@ -655,24 +661,27 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pair_pipe_kernel(PairArgs p)
             bl[s][j] = read_frag<T, BO, BN, STEP>(l + 2 * AB + BB, wn + j * 16, 0, lane);
         }
     };
-    // `more`: steps after this one, of which those from the second on are copied
-    const auto step = [&](char *cur, const char *next, int s, int more) {
+    // step t; inner: steps t + 1 .. t + BUFS are there
+    const auto step = [&](char *cur, const char *next, int s, int t, bool inner) {
 #pragma unroll
         for (int i = 0; i < FM; i++) {
             if (i == FM - 2) {
-                copies_done<0, true>();
+                if (inner || t + BUFS - 1 < steps)
+                    copies_done<(BUFS - 2) * COPIES, true>();
+                else
+                    copies_done<0, true>();
                 __builtin_amdgcn_sched_barrier(0);
-                if (more > 1)
+                if (inner || t + BUFS < steps)
                     copy(cur);
-                if (more > 0)
+                if (inner || t + 1 < steps)
                     read_b(next, s ^ 1);
             }
-            if (i < FM - 3)
+            if (i < FM - 3) {
                 read_a(cur, i + 3);
-            else if (i >= FM - 2 && more > 0) {
-                if (i == FM - 2)
+            } else if (i >= FM - 2 && (inner || t + 1 < steps)) {
+                if (i == FM - 2) {
                     read_a(next, 0);
-                else {
+                } else {
                     read_a(next, 1);
                     read_a(next, 2);
                 }
@@ -684,24 +693,50 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pair_pipe_kernel(PairArgs p)
         }
     };
     copy(l0);
-    copies_done<0, true>();
     if (steps > 1)
         copy(l1);
+    if constexpr (BUFS == 4) {
+        if (steps > 2)
+            copy(l2);
+        if (steps > 3)
+            copy(l3);
+    }
+    if (steps >= BUFS)
+        copies_done<(BUFS - 1) * COPIES, true>();
+    else
+        copies_done<0, true>();
     read_b(l0, 0);
     read_a(l0, 0);
     read_a(l0, 1);
     read_a(l0, 2);
     int t = 0;
-    for (; t + 3 < steps; t += 2) {
-        step(l0, l1, 0, 2);
-        step(l1, l0, 1, 2);
+    if constexpr (BUFS == 4) {
+        for (; t + 2 * BUFS - 1 < steps; t += BUFS) {
+            step(l0, l1, 0, t, true);
+            step(l1, l2, 1, t + 1, true);
+            step(l2, l3, 0, t + 2, true);
+            step(l3, l0, 1, t + 3, true);
+        }
+        for (; t < steps; t += BUFS) {
+            step(l0, l1, 0, t, false);
+            if (t + 1 < steps)
+                step(l1, l2, 1, t + 1, false);
+            if (t + 2 < steps)
+                step(l2, l3, 0, t + 2, false);
+            if (t + 3 < steps)
+                step(l3, l0, 1, t + 3, false);
+        }
+    } else {
+        for (; t + 2 * BUFS - 1 < steps; t += BUFS) {
+            step(l0, l1, 0, t, true);
+            step(l1, l0, 1, t + 1, true);
+        }
+        for (; t < steps; t += BUFS) {
+            step(l0, l1, 0, t, false);
+            if (t + 1 < steps)
+                step(l1, l0, 1, t + 1, false);
+        }
     }
-    // the last one to three steps
-    step(l0, l1, 0, steps - 1 - t);
-    if (t + 1 < steps)
-        step(l1, l0, 1, steps - 2 - t);
-    if (t + 2 < steps)
-        step(l0, l1, 0, 0);
     emit_tile<O, BM, BN, WM, WN>(p, sh, acc, l0, l1);
 }
 
@@ -1090,14 +1125,17 @@ hipError_t pair_product(PairArgs a, int64_t B, float *part, int cus, hipStream_t
     a.per = p.per;
     a.part = part;
     const unsigned grid = a.whole + a.rest * a.splits;
-    if (p.tile == 64 && grid <= (unsigned)cus)
+    const bool alone = grid <= (unsigned)cus; // a workgroup a CU
+    if (p.tile == 64 && alone)
         pair_kernel<O, AO, BO, SYM, true><<<grid, 512, 0, st>>>(a);
     else if (p.tile == 64)
         pair_kernel<O, AO, BO, SYM, false><<<grid, 512, 0, st>>>(a);
+    else if (p.tile == 128 && alone)
+        pair_pipe_kernel<O, 128, 128, 2, 4, AO, BO, SYM, 4><<<grid, 512, 0, st>>>(a);
     else if (p.tile == 128)
-        pair_pipe_kernel<O, 128, 128, 2, 4, AO, BO, SYM><<<grid, 512, 0, st>>>(a);
+        pair_pipe_kernel<O, 128, 128, 2, 4, AO, BO, SYM, 2><<<grid, 512, 0, st>>>(a);
     else
-        pair_pipe_kernel<O, 256, 256, 2, 4, AO, BO, SYM><<<grid, 512, 0, st>>>(a);
+        pair_pipe_kernel<O, 256, 256, 2, 4, AO, BO, SYM, 2><<<grid, 512, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;

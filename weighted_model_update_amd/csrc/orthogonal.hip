@@ -1058,11 +1058,17 @@ struct PairPlan {
 
 PairPlan pair_plan(int64_t B, int64_t M, int64_t N, int64_t K, bool sym, int cus)
 {
-    // tile, bytes of k of a step, tiles at once on a CU, us of a step
+    // tile, bytes of k of a step, tiles at once on a CU, us of a step of a round
+    // of them and of one workgroup a CU.  Measured, us of a product (which is
+    // between 4 and 6 longer than its steps): 4096 x 4096 by 4096 in 256, 128: 308,
+    // 357; symmetric 2048, K = 2048 in 256, 128, 64: 130, 44, 54; symmetric 1000,
+    // K = 1000: 75, 24, 12.  Splits cost their sums' way to memory and back:
+    // symmetric 4096 in 256, 3 splits, 202 + 36 against 271 whole; symmetric 2048 in
+    // 128, 2 splits, 38 + 8 against 44.
     static const struct {
         int tile, step, at_once;
         double full, alone;
-    } kinds[] = {{256, PIPE_STEP, 1, 2.4, 2.4}, {128, PIPE_STEP, 2, 1.35, 0.8}, {64, STEP_BYTES, 2, 1.0, 0.6}};
+    } kinds[] = {{256, PIPE_STEP, 1, 2.36, 2.05}, {128, PIPE_STEP, 2, 1.35, 0.62}, {64, STEP_BYTES, 2, 0.94, 0.5}};
     PairPlan best{};
     double least = 0;
     for (const auto &k : kinds) {
@@ -1073,7 +1079,7 @@ PairPlan pair_plan(int64_t B, int64_t M, int64_t N, int64_t K, bool sym, int cus
             const double step = groups > 0 && groups <= cus ? k.alone : k.full;
             double t = (double)(whole / slots * steps) * k.full + (double)(ceil_div(groups, slots) * per) * step;
             if (used > 1)
-                t += 4 + (double)(groups * k.tile * k.tile) * 8 / 3.5e6;
+                t += 4 + (double)(groups * k.tile * k.tile) * 8 / 7e6;
             if (!best.tile || t < least) {
                 best = {k.tile, whole, rest, (int)used, (int)per};
                 least = t;

@@ -202,12 +202,16 @@ def test_views_and_untouched_gaps(shape, dt, rowwise):
     check(rows, fa.orthogonalize(rows, steps=2), steps=2)
 
 
-@pytest.mark.parametrize("shape", [(10, 300), (300, 10), (3, 64, 64), (130, 70), (2, 70, 130)], ids=str)
-def test_in_place(shape):
-    x = rnd(shape, torch.bfloat16, 2)
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("shape", [(10, 300), (300, 10), (3, 64, 64), (130, 70), (2, 70, 130), (2, 64, 450), (20, 700), (3, 48, 450), (33, 64),
+                                   (2, 40, 9000), (450, 64), (600, 33, 70)], ids=str)
+def test_in_place(shape, dt):
+    x = rnd(shape, DTYPES[dt], 2)
     want = fa.orthogonalize(x)
-    assert fa.orthogonalize(x, out=x) is x
-    assert torch.equal(x, want)
+    for _ in range(3):
+        y = x.clone()
+        assert fa.orthogonalize(y, out=y) is y
+        assert torch.equal(y, want)
 
 
 def test_one_update_of_a_flat_model():

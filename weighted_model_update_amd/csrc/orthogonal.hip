@@ -741,6 +741,15 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pair_pipe_kernel(PairArgs p)
 }
 
 // ------------------------------------------------------------ short sides, in fp64
+// Three stages: the Gram matrix G, its polynomial P, the product with X.  A
+// workgroup has a part of the long side; a call whose matrices have one part
+// each runs all three in one launch, else G's parts go through memory, and P is
+// formed by every workgroup of the last stage where that is cheap (s <= 32).
+// SHORT_NOTE
+constexpr int SHORT_MAX = 64, SHORT_THREADS = 512, SHORT_WAVES = SHORT_THREADS / WAVE, SHORT_STEP = 64;
+constexpr int64_t SHORT_ALONE = 256;
+enum { STAGE_GRAM = 1, STAGE_POLY = 2, STAGE_APPLY = 4 };
+
 // Fragments of the matrix cores' 16x16x4 product in fp64: lane l holds row
 // l % 16 of the one operand and column l % 16 of the other, both at k = l / 16,
 // and of the result column l % 16, rows l / 16 + 4 r.
@@ -749,214 +758,383 @@ __device__ __forceinline__ f64x4 mma64(double a, double b, f64x4 c)
     return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
 }
 
-constexpr int SHORT_MAX = 64, SHORT_THREADS = 256, SHORT_WAVES = SHORT_THREADS / WAVE;
-
+// A symmetric matrix as its blocks of 16 x 16 on and below the diagonal, row by
+// row; rows are spread over the banks.
 constexpr int blocks_of(int t) { return t * (t + 1) / 2; }
+typedef double Block[16][18];
 
-// Four values of a short row i at k .. k + 3 of the long side.
+__device__ __forceinline__ void block_at(int e, int &r, int &c)
+{
+    r = (e >= 1) + (e >= 3) + (e >= 6);
+    c = e - r * (r + 1) / 2;
+}
+
+// Element (16 r + i, 16 c + k).
+__device__ __forceinline__ double symmetric_at(const Block *m, int r, int i, int c, int k)
+{
+    return c <= r ? m[r * (r + 1) / 2 + c][i][k] : m[c * (c + 1) / 2 + r][k][i];
+}
+
+// Four values of short row i at k .. k + 3 of the long side, 0 where there are none.
 template <typename T, bool WIDE>
-__device__ __forceinline__ void short_values(const OrthoArgs &p, int64_t b, int i, int64_t k, int64_t s, int64_t l,
-                                             bool update, float *t)
+__device__ __forceinline__ void short_values(const OrthoArgs &p, int64_t b, int i, int64_t k, int64_t s, int64_t l, float *t)
 {
     const int valid = (int)(i >= s || k >= l ? 0 : l - k < 4 ? l - k : 4);
     if constexpr (WIDE) {
-        argument<T, 4>(p, update_at<T>(p, b, i, k), momentum_at(p, b, i, k), update, valid, t);
+        argument<T, 4>(p, update_at<T>(p, b, i, k), momentum_at(p, b, i, k), true, valid, t);
     } else {
 #pragma unroll
         for (int j = 0; j < 4; j++)
-            argument<T, 1>(p, update_at<T>(p, b, k + j, i), momentum_at(p, b, k + j, i), update, j < valid, t + j);
+            argument<T, 1>(p, update_at<T>(p, b, k + j, i), momentum_at(p, b, k + j, i), true, j < valid, t + j);
     }
 #pragma unroll
     for (int j = 0; j < 4; j++)
         t[j] = j < valid ? t[j] : 0.f;
 }
 
-// Workgroup (matrix, part of the long side): the blocks (rb, cb <= rb) of 16 x 16
-// of this part's share of the Gram matrix, to part [matrix][part][block][256].
-template <typename T, int SB, bool WIDE>
-__global__ __launch_bounds__(SHORT_THREADS) void short_gram_kernel(OrthoArgs p, int parts, int64_t per, double *part)
+// G of the columns (rows) [k0, k1) of the long side into `to`, with `scratch` of
+// SHORT_WAVES * 256 doubles.
+template <typename T, int SB, bool WIDE, typename PUT>
+__device__ __forceinline__ void short_gram(const OrthoArgs &p, int64_t b, int64_t k0, int64_t k1, double *scratch, PUT put)
 {
-    constexpr int NB = blocks_of(SB);
-    __shared__ double joined[SHORT_WAVES][256];
-    int64_t b;
-    int q;
-    matrix_of(blockIdx.x, parts, b, q);
-    const int64_t s = WIDE ? p.m : p.n, l = WIDE ? p.n : p.m;
+    constexpr int NB = blocks_of(SB), U = SB <= 2 ? 4 : 2;
+    const int64_t s = WIDE ? p.m : p.n;
     const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE, i = lane & 15, g = lane >> 4;
-    const int64_t k0 = q * per, k1 = k0 + per < l ? k0 + per : l;
     f64x4 acc[NB];
 #pragma unroll
     for (int e = 0; e < NB; e++)
         acc[e] = f64x4{0, 0, 0, 0};
-    for (int64_t k = k0 + wave * 16; k < k1; k += SHORT_WAVES * 16) {
-        float t[SB][4];
+    // 16 of the long side a wavefront, U such pieces on their way
+    for (int64_t k = k0 + wave * 16; k < k1; k += SHORT_WAVES * 16 * U) {
+        float t[U][SB][4];
 #pragma unroll
-        for (int r = 0; r < SB; r++)
-            short_values<T, WIDE>(p, b, r * 16 + i, k + g * 4, s, l, true, t[r]);
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
+        for (int u = 0; u < U; u++)
 #pragma unroll
             for (int r = 0; r < SB; r++)
+                short_values<T, WIDE>(p, b, r * 16 + i, k + u * SHORT_WAVES * 16 + g * 4, s, k1, t[u][r]);
 #pragma unroll
-                for (int c = 0; c <= r; c++)
-                    acc[r * (r + 1) / 2 + c] = mma64(t[r][j], t[c][j], acc[r * (r + 1) / 2 + c]);
+        for (int u = 0; u < U; u++) {
+            if (u > 0 && k + u * SHORT_WAVES * 16 >= k1)
+                break;
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+#pragma unroll
+                for (int r = 0; r < SB; r++)
+#pragma unroll
+                    for (int c = 0; c <= r; c++)
+                        acc[r * (r + 1) / 2 + c] = mma64(t[u][r][j], t[u][c][j], acc[r * (r + 1) / 2 + c]);
         }
     }
-    double *to = part + (b * parts + q) * (NB * 256);
 #pragma unroll
     for (int e = 0; e < NB; e++) {
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < 4; r++)
-            joined[wave][(g + 4 * r) * 16 + i] = acc[e][r];
+        for (int z = 0; z < 4; z++)
+            scratch[wave * 256 + (g + 4 * z) * 16 + i] = acc[e][z];
         __syncthreads();
-        double sum = joined[0][threadIdx.x];
+        if (threadIdx.x < 256) {
+            double sum = scratch[threadIdx.x];
 #pragma unroll
-        for (int w = 1; w < SHORT_WAVES; w++)
-            sum += joined[w][threadIdx.x];
-        to[e * 256 + threadIdx.x] = sum;
-    }
-}
-
-// C = A B for symmetric A and B that commute, so C is symmetric too: blocks of
-// the lower triangle, written on both sides.  alpha A B + beta D + gamma I.
-template <int SB>
-__device__ __forceinline__ void short_product(double (*c)[SB * 16 + 2], const double (*a)[SB * 16 + 2],
-                                              const double (*b)[SB * 16 + 2], double alpha, double beta,
-                                              const double (*d)[SB * 16 + 2], double gamma)
-{
-    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE, i = lane & 15, g = lane >> 4;
-    __syncthreads();
-    for (int e = wave; e < blocks_of(SB); e += SHORT_WAVES) {
-        int r = 0;
-        while ((r + 1) * (r + 2) / 2 <= e)
-            r++;
-        const int cb = e - r * (r + 1) / 2;
-        f64x4 acc = {0, 0, 0, 0};
-#pragma unroll
-        for (int k = 0; k < SB * 4; k++)
-            acc = mma64(a[r * 16 + i][4 * k + g], b[cb * 16 + i][4 * k + g], acc);
-#pragma unroll
-        for (int z = 0; z < 4; z++) {
-            const int row = r * 16 + g + 4 * z, col = cb * 16 + i;
-            double v = alpha * acc[z] + (row == col ? gamma : 0.0);
-            if (d)
-                v += beta * d[row][col];
-            c[row][col] = v;
-            if (r != cb)
-                c[col][row] = v;
+            for (int w = 1; w < SHORT_WAVES; w++)
+                sum += scratch[w * 256 + threadIdx.x];
+            put(e, (int)threadIdx.x, sum);
         }
     }
 }
 
-// Workgroup: one matrix.  P of its Gram matrix, to poly [matrix][16 SB][16 SB];
-// the norm is the Gram matrix's trace.
-template <int SB>
-__global__ __launch_bounds__(SHORT_THREADS) void short_poly_kernel(OrthoArgs p, int parts, const double *part, double *poly)
+// Block e of A B for symmetric A and B that commute: its four values of a lane.
+template <int SB> __device__ __forceinline__ f64x4 block_product(const Block *a, const Block *b, int e, int s)
 {
-    constexpr int S = SB * 16, NB = blocks_of(SB);
-    typedef double Matrix[S][S + 2];
-    __shared__ Matrix m0, m1, m2, m3;
-    __shared__ double norm;
-    const int64_t b = blockIdx.x;
+    const int lane = threadIdx.x % WAVE, i = lane & 15, g = lane >> 4;
+    int r, c;
+    block_at(e, r, c);
+    // all fragments first: the products then wait for LDS once.  Blocks above the
+    // diagonal are read across; e is the same for a wavefront.
+    double av[SB * 4], bv[SB * 4];
+    const auto fetch = [&](const Block *m, int row, double *v) {
+#pragma unroll
+        for (int kb = 0; kb < SB; kb++) {
+            if (kb <= row) {
+                const double *at = &m[row * (row + 1) / 2 + kb][i][g];
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    v[kb * 4 + q] = at[q * 4];
+            } else {
+                const double *at = &m[kb * (kb + 1) / 2 + row][g][i];
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    v[kb * 4 + q] = at[q * 4 * 18];
+            }
+        }
+    };
+    fetch(a, r, av);
+    fetch(b, c, bv);
+    f64x4 acc = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < SB * 4; k++)
+        if (k * 4 < s)
+            acc = mma64(av[k], bv[k], acc);
+    return acc;
+}
+
+// P from G, both in m: m[0] holds G at the start, the result is the index of P.
+// Q = a + b G + c G^2; P <- Q P; G <- (Q G) Q.  Per step three rounds of block
+// products, independent within a round.
+template <int SB, int THREADS>
+__device__ __forceinline__ int short_poly(const OrthoArgs &p, Block (*m)[blocks_of(SB)], double *norm)
+{
+    constexpr int NB = blocks_of(SB), WAVES = THREADS / WAVE;
     const int s = (int)(p.m < p.n ? p.m : p.n);
-    double(*G)[S + 2] = m0, (*P)[S + 2] = m1, (*Q)[S + 2] = m2, (*T)[S + 2] = m3;
-    const double *from = part + b * parts * (NB * 256);
-    for (int e = 0; e < NB; e++) {
-        double sum = 0;
-        for (int q = 0; q < parts; q++)
-            sum += from[(int64_t)q * (NB * 256) + e * 256 + threadIdx.x];
-        int r = 0;
-        while ((r + 1) * (r + 2) / 2 <= e)
-            r++;
-        const int row = r * 16 + threadIdx.x / 16, col = (e - r * (r + 1) / 2) * 16 + threadIdx.x % 16;
-        G[row][col] = sum;
-        G[col][row] = sum;
-    }
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE), lane = threadIdx.x % WAVE, i = lane & 15, g = lane >> 4;
     __syncthreads();
     if (threadIdx.x < WAVE) {
-        double t = threadIdx.x < s ? G[threadIdx.x % S][threadIdx.x % S] : 0.0;
+        double t = (int)threadIdx.x < s ? m[0][blocks_of((threadIdx.x >> 4) % SB + 1) - 1][threadIdx.x & 15][threadIdx.x & 15] : 0.0;
 #pragma unroll
         for (int d = 1; d < WAVE; d *= 2)
             t += __shfl_xor(t, d);
         if (threadIdx.x == 0)
-            norm = inverse_norm(t);
+            *norm = inverse_norm(t);
     }
     __syncthreads();
-    const double f = norm;
-    for (int e = threadIdx.x; e < S * S; e += SHORT_THREADS) {
-        G[e / S][e % S] *= f * f;
-        P[e / S][e % S] = e / S == e % S ? f : 0.0;
-    }
+    const double f = *norm;
+    for (int e = threadIdx.x; e < NB * 256; e += THREADS)
+        m[0][e / 256][e / 16 % 16][e % 16] *= f * f;
+    constexpr int G = 0, Q = 1, T = 2;
+    int P = 3, N = 4;
+    const auto put = [&](Block *to, int e, auto value) {
+#pragma unroll
+        for (int z = 0; z < 4; z++)
+            to[e][g + 4 * z][i] = value(z);
+    };
     for (int k = 0; k < p.steps; k++) {
         const double ca = p.coef[k][0], cb = p.coef[k][1], cc = p.coef[k][2];
-        short_product<SB>(Q, G, G, cc, cb, G, ca); // Q = a + b G + c G^2
-        short_product<SB>(T, Q, P, 1.0, 0.0, nullptr, 0.0);
-        double(*swap)[S + 2] = P;
-        P = T;
-        T = swap;
-        if (k + 1 < p.steps) {
-            short_product<SB>(T, Q, G, 1.0, 0.0, nullptr, 0.0); // G <- Q G Q
-            short_product<SB>(G, T, Q, 1.0, 0.0, nullptr, 0.0);
+        const bool last = k + 1 == p.steps;
+        __syncthreads();
+        for (int e = wave; e < NB; e += WAVES) {
+            const f64x4 v = block_product<SB>(m[G], m[G], e, s);
+            int r, c;
+            block_at(e, r, c);
+            const auto q = [&](int z) { return cc * v[z] + cb * m[G][e][g + 4 * z][i] + (r == c && g + 4 * z == i ? ca : 0.0); };
+            put(m[Q], e, q);
+            if (k == 0) // P was the norm's inverse
+                put(m[P], e, [&](int z) { return f * q(z); });
+        }
+        __syncthreads();
+        for (int e = wave + (k == 0 ? NB : 0); e < (last ? NB : 2 * NB); e += WAVES) {
+            const bool first = e < NB;
+            const f64x4 v = block_product<SB>(m[Q], first ? m[P] : m[G], first ? e : e - NB, s);
+            put(first ? m[N] : m[T], first ? e : e - NB, [&](int z) { return v[z]; });
+        }
+        if (k > 0) {
+            const int swap = P;
+            P = N;
+            N = swap;
+        }
+        if (last)
+            break;
+        __syncthreads();
+        for (int e = wave; e < NB; e += WAVES) {
+            const f64x4 v = block_product<SB>(m[T], m[Q], e, s);
+            put(m[G], e, [&](int z) { return v[z]; });
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < S * S; e += SHORT_THREADS)
-        poly[b * S * S + e] = P[e / S][e % S];
+    return P;
 }
 
-// Workgroup (matrix, part of the long side): P X (wide) or X P (tall), 16
-// columns (rows) a wavefront at a time.
+// P X (wide) or X P (tall) for the columns (rows) [k0, k1) of the long side, a piece
+// of SHORT_STEP columns or 16 rows a wavefront.
 template <typename T, typename O, int SB, bool WIDE>
-__global__ __launch_bounds__(SHORT_THREADS) void short_apply_kernel(OrthoArgs p, int parts, int64_t per, const double *poly)
+__device__ __forceinline__ void short_apply(const OrthoArgs &p, int64_t b, int64_t k0, int64_t k1, const Block *P)
 {
-    constexpr int S = SB * 16;
-    __shared__ double P[S][S + 2];
-    int64_t b;
-    int q;
-    matrix_of(blockIdx.x, parts, b, q);
-    const int64_t s = WIDE ? p.m : p.n, l = WIDE ? p.n : p.m;
+    const int64_t s = WIDE ? p.m : p.n;
     const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE, i = lane & 15, g = lane >> 4;
-    const int64_t k0 = q * per, k1 = k0 + per < l ? k0 + per : l;
-    for (int e = threadIdx.x; e < S * S; e += SHORT_THREADS)
-        P[e / S][e % S] = poly[b * S * S + e];
-    __syncthreads();
-    for (int64_t k = k0 + wave * 16; k < k1; k += SHORT_WAVES * 16) {
-        // element j of t[r] is short index 16 r + 4 g + j at long index k + i
-        float t[SB][4];
-#pragma unroll
-        for (int r = 0; r < SB; r++) {
-            const int64_t at = k + i;
-            const int first = r * 16 + g * 4, valid = (int)(at >= l || first >= s ? 0 : s - first < 4 ? s - first : 4);
-            if constexpr (WIDE) {
-#pragma unroll
-                for (int j = 0; j < 4; j++)
-                    argument<T, 1>(p, update_at<T>(p, b, first + j, at), momentum_at(p, b, first + j, at), false, j < valid, t[r] + j);
-            } else {
-                argument<T, 4>(p, update_at<T>(p, b, at, first), momentum_at(p, b, at, first), false, valid, t[r]);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                t[r][j] = j < valid ? t[r][j] : 0.f;
-        }
-#pragma unroll
-        for (int c = 0; c < SB; c++) {
-            f64x4 acc = {0, 0, 0, 0};
+    if constexpr (WIDE) {
+        // Where there are fewer pieces than wavefronts, SB of these share a piece,
+        // 16 rows of the result each; X is then read before any of it is written,
+        // as the result may lie in its place.
+        const int64_t pieces = (k1 - k0 + SHORT_STEP - 1) / SHORT_STEP;
+        const bool shared = SB > 1 && pieces < SHORT_WAVES;
+        constexpr int SHARES = SHORT_WAVES / SB;
+        const int first = shared ? wave / SB : wave, stride = shared ? SHARES : SHORT_WAVES;
+        for (int64_t q0 = 0; q0 < pieces; q0 += stride) {
+            const int64_t piece = q0 + first;
+            const bool mine = first < stride && piece < pieces;
+            // t[r][j][q]: short index 16 r + 4 g + j at long index at + q
+            const int64_t at = k0 + piece * SHORT_STEP + 4 * i;
+            const int valid = (int)(!mine || at >= k1 ? 0 : k1 - at < 4 ? k1 - at : 4);
+            float t[SB][4][4];
 #pragma unroll
             for (int r = 0; r < SB; r++)
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    const double w = P[c * 16 + i][r * 16 + g * 4 + j];
-                    acc = WIDE ? mma64(w, t[r][j], acc) : mma64(t[r][j], w, acc);
-                }
+                    const int row = r * 16 + g * 4 + j, n = row < s ? valid : 0;
+                    argument<T, 4>(p, update_at<T>(p, b, row, at), momentum_at(p, b, row, at), false, n, t[r][j]);
 #pragma unroll
-            for (int z = 0; z < 4; z++) {
-                const float v = (float)acc[z];
-                const int64_t row = WIDE ? c * 16 + g + 4 * z : k + g + 4 * z, col = WIDE ? k + i : c * 16 + i;
-                put_result<O, 1>(p, b, row, col, row < p.m && col < p.n, &v);
+                    for (int q = 0; q < 4; q++)
+                        t[r][j][q] = q < n ? t[r][j][q] : 0.f;
+                }
+            if (shared)
+                __syncthreads();
+            const int c0 = shared ? wave % SB : 0, c1 = !mine ? 0 : shared ? c0 + 1 : SB;
+#pragma unroll 1 // unrolled, the fragments of P of all c are held at once
+            for (int c = c0; c < c1; c++) {
+                f64x4 acc[4];
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    acc[q] = f64x4{0, 0, 0, 0};
+#pragma unroll
+                for (int r = 0; r < SB; r++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const double w = symmetric_at(P, c, i, r, g * 4 + j);
+#pragma unroll
+                        for (int q = 0; q < 4; q++)
+                            acc[q] = mma64(w, t[r][j][q], acc[q]);
+                    }
+#pragma unroll
+                for (int z = 0; z < 4; z++) {
+                    const float v[4] = {(float)acc[0][z], (float)acc[1][z], (float)acc[2][z], (float)acc[3][z]};
+                    const int row = c * 16 + g + 4 * z;
+                    if (row < s)
+                        put_result<O, 4>(p, b, row, at, valid, v);
+                }
+            }
+        }
+    } else {
+        for (int64_t k = k0 + wave * 16; k < k1; k += SHORT_WAVES * 16 * 4) {
+            // t[u][r][j]: long index k + 128 (u0 + u) + i at short index 16 r + 4 g + j
+            constexpr int U = SB <= 2 ? 4 : 2;
+#pragma unroll 1
+            for (int u0 = 0; u0 < 4; u0 += U) {
+                if (k + u0 * SHORT_WAVES * 16 >= k1)
+                    break;
+                float t[U][SB][4];
+#pragma unroll
+                for (int u = 0; u < U; u++)
+#pragma unroll
+                    for (int r = 0; r < SB; r++) {
+                        const int64_t at = k + (u0 + u) * SHORT_WAVES * 16 + i, first = r * 16 + g * 4;
+                        const int n = (int)(at >= k1 || first >= s ? 0 : s - first < 4 ? s - first : 4);
+                        argument<T, 4>(p, update_at<T>(p, b, at, first), momentum_at(p, b, at, first), false, n, t[u][r]);
+#pragma unroll
+                        for (int j = 0; j < 4; j++)
+                            t[u][r][j] = j < n ? t[u][r][j] : 0.f;
+                    }
+                // lane i gives short indices SB i .. SB i + SB - 1
+                const int col = SB * i, valid = (int)(col >= s ? 0 : s - col < SB ? s - col : SB);
+                f64x4 acc[U][SB];
+#pragma unroll
+                for (int u = 0; u < U; u++)
+#pragma unroll
+                    for (int c = 0; c < SB; c++)
+                        acc[u][c] = f64x4{0, 0, 0, 0};
+#pragma unroll
+                for (int r = 0; r < SB; r++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+#pragma unroll
+                        for (int c = 0; c < SB; c++) {
+                            const double w = symmetric_at(P, (col + c) >> 4, (col + c) & 15, r, g * 4 + j);
+#pragma unroll
+                            for (int u = 0; u < U; u++)
+                                acc[u][c] = mma64(t[u][r][j], w, acc[u][c]);
+                        }
+#pragma unroll
+                for (int u = 0; u < U; u++)
+#pragma unroll
+                    for (int z = 0; z < 4; z++) {
+                        float v[SB];
+#pragma unroll
+                        for (int c = 0; c < SB; c++)
+                            v[c] = (float)acc[u][c][z];
+                        const int64_t row = k + (u0 + u) * SHORT_WAVES * 16 + g + 4 * z;
+                        if (row < k1 && valid > 0)
+                            put_result<O, SB>(p, b, row, col, valid, v);
+                    }
             }
         }
     }
+}
+
+// P alone runs on more wavefronts: four a SIMD hide each other's reads of LDS.
+template <int STAGES> constexpr int short_threads() { return STAGES == STAGE_POLY ? 1024 : SHORT_THREADS; }
+
+// Workgroup (matrix, part of the long side).  `part` [matrix][parts][block][256]
+// holds G's parts, `poly` [matrix][block] P between the stages' launches.
+template <typename T, typename O, int SB, bool WIDE, int STAGES>
+__global__ __launch_bounds__(short_threads<STAGES>()) void short_kernel(OrthoArgs p, int parts, int64_t per, int sums, double *part,
+                                                                        Block *poly)
+{
+    constexpr int NB = blocks_of(SB), MATRICES = STAGES & STAGE_POLY ? 5 : 1, THREADS = short_threads<STAGES>();
+    constexpr bool GRAM = STAGES & STAGE_GRAM, POLY = STAGES & STAGE_POLY, APPLY = STAGES & STAGE_APPLY;
+    constexpr int GROUPS = THREADS / 256;
+    __shared__ __attribute__((aligned(16))) Block m[MATRICES][NB];
+    __shared__ double scratch[GRAM ? SHORT_WAVES * 256 : POLY ? THREADS : 1];
+    __shared__ double norm;
+    int64_t b = blockIdx.x;
+    int q = 0;
+    if (GRAM || APPLY)
+        matrix_of(blockIdx.x, parts, b, q);
+    const int64_t l = WIDE ? p.n : p.m, k0 = q * per, k1 = k0 + per < l ? k0 + per : l;
+    if constexpr (GRAM) {
+        double *to = part + (b * parts + q) * (NB * 256);
+        short_gram<T, SB, WIDE>(p, b, k0, k1, scratch, [&](int e, int at, double v) {
+            if constexpr (POLY)
+                m[0][e][at / 16][at % 16] = v;
+            else
+                to[e * 256 + at] = v;
+        });
+    } else if constexpr (POLY) {
+        // groups of 256 threads take the parts in turn
+        const double *from = part + b * sums * (NB * 256);
+        const int at = threadIdx.x % 256, group = threadIdx.x / 256;
+        for (int e = 0; e < NB; e++) {
+            double sum = 0;
+#pragma unroll 8
+            for (int z = group; z < sums; z += GROUPS)
+                sum += from[(int64_t)z * (NB * 256) + e * 256 + at];
+            __syncthreads();
+            scratch[threadIdx.x] = sum;
+            __syncthreads();
+            if (group == 0) {
+#pragma unroll
+                for (int z = 1; z < GROUPS; z++)
+                    sum += scratch[z * 256 + at];
+                m[0][e][at / 16][at % 16] = sum;
+            }
+        }
+    }
+    int P = 0;
+    if constexpr (POLY)
+        P = short_poly<SB, THREADS>(p, m, &norm);
+    double *flat = reinterpret_cast<double *>(poly + b * NB);
+    constexpr int SIZE = sizeof(Block) / sizeof(double) * NB;
+    if constexpr (POLY && !APPLY)
+        for (int e = threadIdx.x; e < SIZE; e += THREADS)
+            flat[e] = reinterpret_cast<const double *>(m[P])[e];
+    if constexpr (APPLY && !POLY) {
+        for (int e = threadIdx.x; e < SIZE; e += THREADS)
+            reinterpret_cast<double *>(m[0])[e] = flat[e];
+        __syncthreads();
+    }
+    if constexpr (APPLY)
+        short_apply<T, O, SB, WIDE>(p, b, k0, k1, m[P]);
+}
+
+// Sums of up to JOIN_PARTS of G's parts, for calls with many.
+constexpr int JOIN_PARTS = 32;
+
+__global__ __launch_bounds__(256) void short_join_kernel(const double *part, int parts, int sums, int blocks, double *out)
+{
+    const int e = blockIdx.x % blocks;
+    const int64_t q = blockIdx.x / blocks % sums, b = blockIdx.x / blocks / sums;
+    const int first = (int)q * JOIN_PARTS, end = first + JOIN_PARTS < parts ? first + JOIN_PARTS : parts;
+    double sum = 0;
+#pragma unroll 8
+    for (int z = first; z < end; z++)
+        sum += part[((b * parts + z) * blocks + e) * 256 + threadIdx.x];
+    out[((b * sums + q) * blocks + e) * 256 + threadIdx.x] = sum;
 }
 
 // ------------------------------------------------------------ launches
@@ -1261,38 +1439,66 @@ template <typename T, typename O> hipError_t run_long(const OrthoArgs &o, int cu
 }
 
 struct ShortPlan {
-    int sb, parts;
+    int sb, parts, sums; // sums: parts of G that P is formed from
     int64_t per;
-    size_t part, poly;
+    size_t part, joined, poly;
+    size_t total() const { return part + joined + poly; }
 };
 
 ShortPlan short_plan(int64_t B, int64_t m, int64_t n, int cus)
 {
     const int64_t s = std::min(m, n), l = std::max(m, n);
-    ShortPlan p;
+    ShortPlan p{};
     p.sb = (int)ceil_div(s, 16);
-    const int64_t want = std::max<int64_t>(1, std::min(ceil_div(2 * cus, B), ceil_div(l, 16 * SHORT_WAVES)));
-    p.per = round_up(ceil_div(l, want), 16 * SHORT_WAVES);
+    // with s <= 32 and up to SHORT_ALONE of the long side a workgroup takes a
+    // matrix to the end
+    const int64_t want = p.sb <= 2 && l <= SHORT_ALONE ? 1 : std::max<int64_t>(1, ceil_div(2 * cus, B));
+    p.per = std::max<int64_t>(SHORT_STEP, round_up(ceil_div(l, want), SHORT_STEP));
     p.parts = (int)ceil_div(l, p.per);
-    p.part = (size_t)B * p.parts * blocks_of(p.sb) * 256 * 8;
-    p.poly = (size_t)B * p.sb * p.sb * 256 * 8;
+    p.sums = p.parts;
+    const int64_t matrix = blocks_of(p.sb) * 256 * 8;
+    if (p.parts > 1 || p.sb > 2) {
+        p.part = (size_t)(B * p.parts * matrix);
+        if (p.parts > JOIN_PARTS) {
+            p.sums = (int)ceil_div(p.parts, JOIN_PARTS);
+            p.joined = (size_t)(B * p.sums * matrix);
+        }
+        if (p.sb > 2)
+            p.poly = (size_t)(B * blocks_of(p.sb)) * sizeof(Block);
+    }
     return p;
 }
 
 template <typename T, typename O, int SB, bool WIDE> hipError_t run_short_form(const OrthoArgs &o, const ShortPlan &p, hipStream_t st)
 {
-    double *part = static_cast<double *>(o.ws), *poly = part + p.part / 8;
+    char *ws = static_cast<char *>(o.ws);
+    double *part = reinterpret_cast<double *>(ws), *joined = reinterpret_cast<double *>(ws + p.part);
+    Block *poly = reinterpret_cast<Block *>(ws + p.part + p.joined);
     const unsigned grid = (unsigned)(o.B * p.parts);
-    short_gram_kernel<T, SB, WIDE><<<grid, SHORT_THREADS, 0, st>>>(o, p.parts, p.per, part);
+    if constexpr (SB <= 2)
+        if (p.parts == 1) {
+            short_kernel<T, O, SB, WIDE, STAGE_GRAM | STAGE_POLY | STAGE_APPLY><<<grid, SHORT_THREADS, 0, st>>>(o, 1, p.per, 1, part, poly);
+            return hipGetLastError();
+        }
+    short_kernel<T, float, SB, WIDE, STAGE_GRAM><<<grid, SHORT_THREADS, 0, st>>>(o, p.parts, p.per, p.sums, part, poly);
     hipError_t e = hipGetLastError();
+    if (e == hipSuccess && p.sums < p.parts) {
+        short_join_kernel<<<(unsigned)(o.B * p.sums * blocks_of(SB)), 256, 0, st>>>(part, p.parts, p.sums, blocks_of(SB), joined);
+        e = hipGetLastError();
+        part = joined;
+    }
     if (e != hipSuccess)
         return e;
-    short_poly_kernel<SB><<<(unsigned)o.B, SHORT_THREADS, 0, st>>>(o, p.parts, part, poly);
-    e = hipGetLastError();
-    if (e != hipSuccess)
-        return e;
-    short_apply_kernel<T, O, SB, WIDE><<<grid, SHORT_THREADS, 0, st>>>(o, p.parts, p.per, poly);
-    return hipGetLastError();
+    if constexpr (SB <= 2) {
+        short_kernel<T, O, SB, WIDE, STAGE_POLY | STAGE_APPLY><<<grid, SHORT_THREADS, 0, st>>>(o, p.parts, p.per, p.sums, part, poly);
+    } else {
+        short_kernel<float, float, SB, true, STAGE_POLY>
+            <<<(unsigned)o.B, short_threads<STAGE_POLY>(), 0, st>>>(o, p.parts, p.per, p.sums, part, poly);
+        e = hipGetLastError();
+        if (e == hipSuccess)
+            short_kernel<T, O, SB, WIDE, STAGE_APPLY><<<grid, SHORT_THREADS, 0, st>>>(o, p.parts, p.per, p.sums, part, poly);
+    }
+    return e == hipSuccess ? hipGetLastError() : e;
 }
 
 template <typename T, typename O, int SB> hipError_t run_short_sb(const OrthoArgs &o, const ShortPlan &p, hipStream_t st)
@@ -1340,10 +1546,8 @@ size_t ortho_workspace_bytes(int64_t B, int64_t m, int64_t n, int cus)
 {
     if (B == 0 || m == 0 || n == 0)
         return 0;
-    if (std::min(m, n) <= SHORT_MAX) {
-        const ShortPlan p = short_plan(B, m, n, cus);
-        return p.part + p.poly;
-    }
+    if (std::min(m, n) <= SHORT_MAX)
+        return short_plan(B, m, n, cus).total();
     return long_plan(B, m, n, cus).total();
 }
 

@@ -13,15 +13,78 @@ namespace fa {
 namespace {
 
 // ------------------------------------------------------------ rows to 8 bits
-// Bound by memory.  A group of threads holds its row in registers between the
-// maximum and the quotients, QR_W values a thread at a time; what does not fit
-// is read again.
+// A group of threads holds its row in registers between the maximum and the
+// quotients, QR_W values a thread at a time; what does not fit is read again.
+// Bound by memory once the quotients are products: 14336 x 4096 bf16 (176 MB) in
+// QR_US us, with a division for each value 48.
 constexpr int QR_THREADS = 256, QR_W = 16, QR_HELD = 4;
 
-__device__ __forceinline__ float quotient(float x, float scale)
+// Largest magnitude among W values, as the bits of an fp32 (NaN and infinities
+// are the largest).
+template <int W> __device__ __forceinline__ uint32_t top_bits(const Raw<float, W> &v, uint32_t top)
+{
+#pragma unroll
+    for (int i = 0; i < W; i++) {
+        const uint32_t b = __builtin_bit_cast(uint32_t, v.e[i]) & 0x7fffffffu;
+        top = b > top ? b : top;
+    }
+    return top;
+}
+
+template <int W> __device__ __forceinline__ uint32_t top_bits(const Raw<__bf16, W> &v, uint32_t top)
+{
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 most = {(uint16_t)(top >> 16), 0};
+#pragma unroll
+    for (int i = 0; i < W; i += 2) {
+        u16x2 b;
+        __builtin_memcpy(&b, v.e + i, 4);
+        most = __builtin_elementwise_max(most, b & (uint16_t)0x7fff);
+    }
+    return (uint32_t)(most.x > most.y ? most.x : most.y) << 16;
+}
+
+__device__ __forceinline__ int quotient(float x, float scale)
 {
     const float q = __builtin_rintf(x / scale); // to even, as the division is IEEE's
-    return fminf(fmaxf(q, -127.f), 127.f);
+    return (int)fminf(fmaxf(q, -127.f), 127.f);
+}
+
+// q = the whole number nearest to fp32(x / scale).  t = fma(x, 1 / scale, 3 2^22)
+// has it in its low bits; x times the rounded inverse is off by at most 127 2^-24
+// and so is the rounded quotient, so only within 2.3e-5 of a tie can the two
+// differ, and values that near are divided.  Scales below 2^-100, whose inverse
+// leaves fp32 or loses bits, divide throughout.
+constexpr float QR_MAGIC = 12582912.f, QR_TIE = 0.4999f, QR_LEAST = 0x1p-100f;
+
+template <typename T> __device__ __forceinline__ u32x4 quotients(const Raw<T, QR_W> &v, float scale, float inverse)
+{
+    u32x4 out;
+    float far = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; w++) {
+        uint32_t b[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float x = (float)v.e[w * 4 + i], t = __builtin_fmaf(x, inverse, QR_MAGIC);
+            far = fmaxf(far, fabsf(__builtin_fmaf(x, inverse, QR_MAGIC - t)));
+            b[i] = __builtin_bit_cast(uint32_t, t);
+        }
+        // the low bytes of four words
+        out[w] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400), __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400),
+                                       0x05040100);
+    }
+    if (!(far < QR_TIE) || scale < QR_LEAST) {
+#pragma unroll
+        for (int w = 0; w < 4; w++) {
+            uint32_t word = 0;
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                word |= (uint32_t)(quotient((float)v.e[w * 4 + i], scale) & 255) << (8 * i);
+            out[w] = word;
+        }
+    }
+    return out;
 }
 
 // ACROSS threads take a row.  `fill`: columns up to which zeros follow the row.
@@ -30,7 +93,7 @@ __global__ __launch_bounds__(QR_THREADS) void quantize_kernel(const T *x, int64_
                                                               int64_t ldq, int64_t fill, float *scale)
 {
     constexpr int ROWS = QR_THREADS / ACROSS;
-    __shared__ float tops[2][QR_THREADS / WAVE];
+    __shared__ uint32_t tops[2][QR_THREADS / WAVE];
     const int t = threadIdx.x % ACROSS;
     int turn = 0;
     for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < R; r0 += (int64_t)gridDim.x * ROWS, turn ^= 1) {
@@ -38,16 +101,7 @@ __global__ __launch_bounds__(QR_THREADS) void quantize_kernel(const T *x, int64_
         const int64_t cols = r < R ? C : 0;
         const T *row = x + (r < R ? r : 0) * ldx;
         Raw<T, QR_W> held[QR_HELD];
-        float top = 0.f;
-        bool odd = false; // NaN or an infinity in the row
-        const auto look = [&](const Raw<T, QR_W> &v) {
-#pragma unroll
-            for (int i = 0; i < QR_W; i++) {
-                const float a = fabsf((float)v.e[i]);
-                odd |= !(a < INFINITY);
-                top = fmaxf(top, a);
-            }
-        };
+        uint32_t top = 0;
 #pragma unroll
         for (int h = 0; h < QR_HELD; h++) {
             const int64_t c = ((int64_t)h * ACROSS + t) * QR_W, left = cols - c;
@@ -55,16 +109,17 @@ __global__ __launch_bounds__(QR_THREADS) void quantize_kernel(const T *x, int64_
         }
 #pragma unroll
         for (int h = 0; h < QR_HELD; h++)
-            look(held[h]);
+            top = top_bits(held[h], top);
         for (int64_t c = ((int64_t)QR_HELD * ACROSS + t) * QR_W; c < cols; c += ACROSS * QR_W) {
             Raw<T, QR_W> v;
             v.fetch(row + c, (int)(cols - c < QR_W ? cols - c : QR_W));
-            look(v);
+            top = top_bits(v, top);
         }
-        top = odd ? INFINITY : top;
 #pragma unroll
-        for (int d = 1; d < (ACROSS < WAVE ? ACROSS : WAVE); d *= 2)
-            top = fmaxf(top, __shfl_xor(top, d));
+        for (int d = 1; d < (ACROSS < WAVE ? ACROSS : WAVE); d *= 2) {
+            const uint32_t other = __shfl_xor(top, d);
+            top = other > top ? other : top;
+        }
         if constexpr (ACROSS > WAVE) {
             if (threadIdx.x % WAVE == 0)
                 tops[turn][threadIdx.x / WAVE] = top;
@@ -72,28 +127,26 @@ __global__ __launch_bounds__(QR_THREADS) void quantize_kernel(const T *x, int64_
             top = tops[turn][0];
 #pragma unroll
             for (int w = 1; w < ACROSS / WAVE; w++)
-                top = fmaxf(top, tops[turn][w]);
+                top = tops[turn][w] > top ? tops[turn][w] : top;
         }
-        const bool flawed = !(top < INFINITY);
-        const float s = flawed ? __builtin_nanf("") : top / 127.f;
+        const float s = top >= 0x7f800000u ? __builtin_nanf("") : __builtin_bit_cast(float, top) / 127.f;
         if (t == 0 && r < R)
             scale[r] = s;
         const bool live = s > 0.f;
+        const float inverse = 1.f / s;
         const auto put = [&](int64_t c, const Raw<T, QR_W> &v) {
             const int64_t end = r < R ? fill : 0;
             if (c >= end)
                 return;
-            int8_t b[QR_W];
-#pragma unroll
-            for (int i = 0; i < QR_W; i++)
-                b[i] = live ? (int8_t)(int)quotient((float)v.e[i], s) : (int8_t)0;
+            const u32x4 b = live ? quotients(v, s, inverse) : u32x4{0, 0, 0, 0};
+            int8_t *to = q + r * ldq + c;
             if (end - c >= QR_W) {
-                __builtin_memcpy(q + r * ldq + c, b, QR_W);
+                __builtin_memcpy(to, &b, QR_W);
             } else {
 #pragma unroll
                 for (int i = 0; i < QR_W; i++)
                     if (i < end - c)
-                        q[r * ldq + c + i] = b[i];
+                        to[i] = (int8_t)(b[i / 4] >> (i % 4 * 8));
             }
         };
 #pragma unroll

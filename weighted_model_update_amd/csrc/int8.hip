@@ -165,7 +165,8 @@ __global__ __launch_bounds__(QR_THREADS) void quantize_kernel(const T *x, int64_
 
 // ------------------------------------------------------------ products
 // Workgroup (tile, split), as for the other products; partial sums are whole
-// numbers too, so a split changes no result.
+// numbers too, so a split changes no result.  Steps are short, so aligned operands
+// go through four buffers.  GEMM8_NOTE
 template <typename O, int BM, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(WM *WN *WAVE) void gemm8_kernel(GemmArgs p, int tiles_m, int tiles_n, int kper, float *part)
 {
@@ -174,6 +175,8 @@ __global__ __launch_bounds__(WM *WN *WAVE) void gemm8_kernel(GemmArgs p, int til
     constexpr int AB = BM * STEP_BYTES, BB = BN * STEP_BYTES;
     __shared__ __attribute__((aligned(1024))) char l0[AB + BB];
     __shared__ __attribute__((aligned(1024))) char l1[AB + BB];
+    __shared__ __attribute__((aligned(1024))) char l2[DIRECT ? AB + BB : 16];
+    __shared__ __attribute__((aligned(1024))) char l3[DIRECT ? AB + BB : 16];
 
     unsigned tm, tn;
     tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
@@ -190,7 +193,7 @@ __global__ __launch_bounds__(WM *WN *WAVE) void gemm8_kernel(GemmArgs p, int til
         Direct<T, false, BN, THREADS, STEP_BYTES> db;
         da.init(a, p.lda, m0, p.M, k0);
         db.init(b, p.ldb, n0, p.N, k0);
-        t.run(l0, l1, steps, wm, wn, lane, [&](char *l, int s) {
+        t.template run<AB / 16 / THREADS + BB / 16 / THREADS>(l0, l1, l2, l3, steps, wm, wn, lane, [&](char *l, int s) {
             da.start(l, kend - k0 - s * BK);
             db.start(l + AB, kend - k0 - s * BK);
         });
@@ -277,6 +280,152 @@ template <typename O> __global__ __launch_bounds__(J8_THREADS) void join8_kernel
     float v[J8_W];
     scaled_sums<J8_W>(sum, p.row_scale[m], cs.e, v);
     epilogue<O, J8_W>(p, m, n, v, bias, res);
+}
+
+// ------------------------------------------------------------ few tokens
+// Up to FEW_M rows of x against all weights, in one launch: bound by the weights'
+// bytes and by latency.  A workgroup has 16 columns and each of its wavefronts a
+// range of k (the next 16 after them, where there are more than FEW_PER_CU
+// workgroups a CU); the first 2 FEW_AHEAD fragments of the weights are on their way
+// before the workgroup looks at x, which it brings to 8 bits itself (X: its type;
+// int8_t: as it is), FEW_PIECES pieces of 4096 in all.  One token through 14336 x 4096 weights (59 MB) in FEW_US us;
+// as 16 x 128 tiles after a launch for x, with the join of two splits, 18.6.
+constexpr int FEW_M = 4, FEW_WAVES = 4, FEW_THREADS = FEW_WAVES * WAVE, FEW_AHEAD = 4, FEW_PER_CU = 4, FEW_PIECES = 4;
+
+__device__ __forceinline__ int64_t few_pitch(int64_t K) { return (K + WAVE - 1) / WAVE * WAVE; }
+
+template <typename O, typename X>
+__global__ __launch_bounds__(FEW_THREADS) void few_kernel(GemmArgs p, int range)
+{
+    extern __shared__ __attribute__((aligned(16))) int8_t xq[]; // [M][pitch], zeros behind the rows
+    __shared__ int32_t sums[FEW_WAVES][FEW_M][16];
+    __shared__ uint32_t tops[FEW_PIECES][FEW_WAVES];
+    __shared__ float scales[FEW_M];
+    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE, i = lane & 15, g = lane >> 4;
+    const int pitch = (int)few_pitch(p.K);
+    const int k0 = wave * range, k1 = p.K - k0 < range ? p.K : k0 + range; // may be empty
+    const int steps = k1 > k0 ? (k1 - k0 + WAVE - 1) / WAVE : 0;
+    // fragments of row n0 + i, 16 bytes each; past the row's end or the last row zeros
+    Frag fw[2][FEW_AHEAD];
+    const auto fetch = [&](Frag (&f)[FEW_AHEAD], int64_t n0, int first) {
+        const int8_t *w = static_cast<const int8_t *>(p.b) + (n0 + i) * p.ldb + k0 + g * 16;
+        const int left = n0 + i < p.N ? k1 - k0 - g * 16 : 0;
+#pragma unroll
+        for (int e = 0; e < FEW_AHEAD; e++) {
+            const int k = (first + e) * WAVE;
+            f[e].v = u32x4{0, 0, 0, 0};
+            if (k < left)
+                f[e].v = *reinterpret_cast<const u32x4 *>(w + k);
+        }
+    };
+
+    // x in pieces of a row, one a thread, FEW_PIECES in all: they are on their way
+    // before the weights, which they would have to wait for otherwise
+    constexpr bool WHOLE = __is_same(X, int8_t);
+    const int per_row = (pitch + FEW_THREADS * 16 - 1) / (FEW_THREADS * 16);
+    const auto piece = [&](int e, int &m, int &c) {
+        m = e / per_row;
+        c = (e % per_row * FEW_THREADS + threadIdx.x) * 16;
+    };
+    Raw<X, 16> x[FEW_PIECES];
+#pragma unroll
+    for (int e = 0; e < FEW_PIECES; e++) {
+        int m, c;
+        piece(e, m, c);
+        const int n = m < p.M ? p.K - c : 0;
+        x[e].fetch(static_cast<const X *>(p.a) + m * p.lda + c, n < 0 ? 0 : n < 16 ? n : 16);
+    }
+    int64_t n0 = (int64_t)blockIdx.x * 16;
+    fetch(fw[0], n0, 0);
+    fetch(fw[1], n0, FEW_AHEAD);
+    uint32_t top[FEW_PIECES] = {};
+    if constexpr (!WHOLE) {
+#pragma unroll
+        for (int e = 0; e < FEW_PIECES; e++) {
+            top[e] = top_bits(x[e], 0);
+#pragma unroll
+            for (int d = 1; d < WAVE; d *= 2) {
+                const uint32_t other = __shfl_xor(top[e], d);
+                top[e] = other > top[e] ? other : top[e];
+            }
+            if (lane == 0)
+                tops[e][wave] = top[e];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < FEW_PIECES; e++)
+#pragma unroll
+            for (int f = 0; f < FEW_PIECES; f++)
+                if (e / per_row == f / per_row)
+#pragma unroll
+                    for (int v = 0; v < FEW_WAVES; v++)
+                        top[e] = tops[f][v] > top[e] ? tops[f][v] : top[e];
+    }
+#pragma unroll
+    for (int e = 0; e < FEW_PIECES; e++) {
+        int m, c;
+        piece(e, m, c);
+        u32x4 q;
+        if constexpr (WHOLE) {
+            __builtin_memcpy(&q, x[e].e, 16);
+        } else {
+            const float s = top[e] >= 0x7f800000u ? __builtin_nanf("") : __builtin_bit_cast(float, top[e]) / 127.f;
+            q = s > 0.f ? quotients(x[e], s, 1.f / s) : u32x4{0, 0, 0, 0};
+            if (threadIdx.x == 0 && m < p.M)
+                scales[m] = s;
+        }
+        if (m < p.M && c < pitch)
+            *reinterpret_cast<u32x4 *>(xq + m * pitch + c) = q;
+    }
+    __syncthreads();
+
+    // rows of x past M repeat the last: their results are not looked at
+    const int8_t *xr = xq + (i < p.M ? i : p.M - 1) * pitch + k0 + g * 16;
+    for (;;) {
+        i32x4 acc = {0, 0, 0, 0};
+        const auto use = [&](const Frag (&f)[FEW_AHEAD], int first) {
+#pragma unroll
+            for (int e = 0; e < FEW_AHEAD; e++)
+                if (first + e < steps) {
+                    Frag fx;
+                    fx.v = *reinterpret_cast<const u32x4 *>(xr + (first + e) * WAVE);
+                    acc = mma<int8_t>(f[e], fx, acc);
+                }
+        };
+        const int64_t next = n0 + (int64_t)gridDim.x * 16;
+        for (int s = 0; s < steps; s += 2 * FEW_AHEAD) {
+            // behind the last steps the next columns' first fragments
+            const bool more = s + 2 * FEW_AHEAD < steps;
+            use(fw[0], s);
+            fetch(fw[0], more ? n0 : next, more ? s + 2 * FEW_AHEAD : 0);
+            use(fw[1], s + FEW_AHEAD);
+            fetch(fw[1], more ? n0 : next, more ? s + 3 * FEW_AHEAD : FEW_AHEAD);
+        }
+        // lane l holds row l % 16, columns 4 (l / 16) ..
+        if (i < p.M)
+            *reinterpret_cast<i32x4 *>(&sums[wave][i][g * 4]) = acc;
+        __syncthreads();
+        const int m = threadIdx.x / 16;
+        const int64_t n = n0 + threadIdx.x % 16;
+        if (m < p.M && n < p.N) {
+            int32_t sum[1] = {0};
+#pragma unroll
+            for (int e = 0; e < FEW_WAVES; e++)
+                sum[0] += sums[e][m][threadIdx.x % 16];
+            const float row = WHOLE ? p.row_scale[m] : scales[m];
+            const float col[1] = {p.col_scale[n]};
+            float v[1];
+            Raw<O, 1> bias, res;
+            fetch_bias(p, (int)n, bias);
+            fetch_residual(p, m, (int)n, res);
+            scaled_sums<1>(sum, row, col, v);
+            epilogue<O, 1>(p, m, (int)n, v, bias, res);
+        }
+        n0 = next;
+        if (n0 >= p.N)
+            break;
+        __syncthreads();
+    }
 }
 
 // ------------------------------------------------------------ weights as values
@@ -374,10 +523,21 @@ template <typename O, int BM, int BN, int WM, int WN> hipError_t run_pipe8(const
     return hipGetLastError();
 }
 
+template <typename O, typename X> hipError_t run_few(const GemmArgs &a, int cus, hipStream_t s)
+{
+    const int per = (a.K + FEW_WAVES - 1) / FEW_WAVES, range = (per + WAVE - 1) / WAVE * WAVE;
+    const size_t lds = (size_t)a.M * ((a.K + WAVE - 1) / WAVE * WAVE);
+    const unsigned grid = (unsigned)std::min<int64_t>(((int64_t)a.N + 15) / 16, (int64_t)FEW_PER_CU * cus);
+    few_kernel<O, X><<<grid, FEW_THREADS, lds, s>>>(a, range);
+    return hipGetLastError();
+}
+
 template <typename O> hipError_t gemm8_of(const GemmArgs &a, void *ws, int cus, hipStream_t s)
 {
     const Plan8 p = plan8(a.M, a.N, a.K, cus);
     const bool direct = direct_ok(a.a, a.lda, a.K, a.a_padded) && direct_ok(a.b, a.ldb, a.K, false);
+    if (few8_ok(a.M, a.K, a.b, a.ldb))
+        return run_few<O, int8_t>(a, cus, s);
     if (p.tile <= P8_128_128) {
         if (!direct)
             return run_tile8<O, 128, 128, 2, 2>(a, false, 1, ws, s);
@@ -422,6 +582,17 @@ size_t gemm8_workspace_bytes(int64_t M, int64_t N, int64_t K, int cus)
 {
     const Plan8 p = plan8(M, N, K, cus);
     return p.splits > 1 ? ((size_t)p.splits * M * N * sizeof(int32_t) + 255) / 256 * 256 : 0;
+}
+
+bool few8_ok(int64_t M, int64_t K, const void *w, int64_t ldw)
+{
+    return M >= 1 && K >= 1 && M * ((K + FEW_THREADS * 16 - 1) / (FEW_THREADS * 16)) <= FEW_PIECES &&
+           (reinterpret_cast<uintptr_t>(w) & 15) == 0 && ldw % 16 == 0 && K % 16 == 0;
+}
+
+hipError_t launch_few8(const GemmArgs &a, int dt, int cus, hipStream_t s)
+{
+    return dt == FA_BF16 ? run_few<__bf16, __bf16>(a, cus, s) : run_few<float, float>(a, cus, s);
 }
 
 hipError_t launch_gemm8(const GemmArgs &a, int dt, void *ws, int cus, hipStream_t s)

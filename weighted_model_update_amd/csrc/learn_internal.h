@@ -82,6 +82,12 @@ hipError_t launch_quantize(const QuantizeArgs &a, int dt, hipStream_t s);
 size_t gemm8_workspace_bytes(int64_t M, int64_t N, int64_t K, int cus);
 hipError_t launch_gemm8(const GemmArgs &a, int dt, void *ws, int cus, hipStream_t s);
 
+// Whether a product takes one launch that also brings x to 8 bits: few rows, which
+// a workgroup holds, and weights whose rows are whole chunks.
+bool few8_ok(int64_t M, int64_t K, const void *w, int64_t ldw);
+// That launch, from rows a.a of dt (a.row_scale is not used).
+hipError_t launch_few8(const GemmArgs &a, int dt, int cus, hipStream_t s);
+
 // out [rows][ldo] = w as values of dt, zeros from column `cols` on.
 hipError_t launch_widen(const int8_t *w, int64_t ldw, int64_t rows, int64_t cols, int dt, void *out, int64_t ldo,
                         hipStream_t s);

@@ -541,6 +541,42 @@ template <typename T, int BM, int BN, int WM, int WN, bool AO, bool BO> struct T
             step(l0, l0 + AB, wm, wn, lane);
         __syncthreads();
     }
+
+    // The same through four buffers, three steps on their way.  COPIES: the least
+    // that a wavefront copies in a step.
+    template <int COPIES, typename COPY>
+    __device__ __forceinline__ void run(char *l0, char *l1, char *l2, char *l3, int steps, int wm, int wn, int lane, COPY copy)
+    {
+        constexpr int AB = BM * STEP_BYTES;
+        // step t from `cur`; `free` held step t - 1 and takes step t + 3
+        const auto turn = [&](const char *cur, char *free, int t) {
+            if (t + 2 < steps)
+                copies_done<2 * COPIES, true>();
+            else if (t + 1 < steps)
+                copies_done<COPIES, true>();
+            else
+                copies_done<0, true>();
+            if (t + 3 < steps)
+                copy(free, t + 3);
+            step(cur, cur + AB, wm, wn, lane);
+        };
+        if (steps > 0)
+            copy(l0, 0);
+        if (steps > 1)
+            copy(l1, 1);
+        if (steps > 2)
+            copy(l2, 2);
+        for (int t = 0; t < steps; t += 4) {
+            turn(l0, l3, t);
+            if (t + 1 < steps)
+                turn(l1, l0, t + 1);
+            if (t + 2 < steps)
+                turn(l2, l1, t + 2);
+            if (t + 3 < steps)
+                turn(l3, l2, t + 3);
+        }
+        __syncthreads();
+    }
 };
 
 // Steps of 64 bytes of k through four buffers: while the matrix cores work on

@@ -276,7 +276,8 @@ def check_backward(dy, w, ws, act, pre, alpha, dx, db):
 
 @pytest.mark.parametrize("dt", list(DTYPES))
 @pytest.mark.parametrize("shape", [(1, 1, 1), (3, 5, 7), (1, 1000, 640), (17, 33, 65), (33, 96, 144), (300, 16, 264), (1000, 9, 133),
-                                   (64, 1000, 16), (129, 257, 130), (513, 384, 1030), (2050, 130, 2060), (40, 5000, 48)], ids=str)
+                                   (64, 1000, 16), (129, 257, 130), (513, 384, 1030), (2050, 130, 2060), (40, 5000, 48), (3, 4096, 1008),
+                                   (513, 385, 1040), (130, 9000, 64), (1100, 71, 4112), (2050, 130, 2064)], ids=str)
 def test_backward(shape, dt):
     M, N, K = shape
     t, act = DTYPES[dt], ACTS[(M + N + K) % 4]
@@ -312,6 +313,31 @@ def test_backward_pitched_views_and_untouched_gaps(dt, odd):
     same = rnd((1, N), t, 5).expand(M, N)
     dx, db = fa.linear_int8_backward(same, w, ws, db=True)
     check_backward(same, w, ws, "none", None, 1.0, dx, db)
+
+
+@pytest.mark.parametrize("dt", list(DTYPES))
+@pytest.mark.parametrize("shape", [(5, 300, 64), (700, 200, 1040)], ids=str)
+def test_backward_the_whole_range_of_values(shape, dt):
+    """Gradients over many orders of magnitude, up to the largest fp32 and down to
+    subnormals; NaN and infinities stay in their rows."""
+    M, N, K = shape
+    t = DTYPES[dt]
+    w, ws = ints((N, K), 1, -128), torch.ones(N, device="cuda")
+    dy = rnd((M, N), t, 2) * torch.exp2(torch.randint(-100, 90, (M, N), generator=torch.Generator().manual_seed(3)).cuda().float()).to(t)
+    dy[1] = 0
+    dy[1, 3] = 2e38
+    dy[2] = rnd((1, N), t, 4) * 2.0 ** -125
+    w[3] = w[3].clamp(-1, 1)
+    dx, _ = fa.linear_int8_backward(dy, w, ws)
+    check_backward(dy, w, ws, "none", None, 1.0, dx, None)
+    want = dx.clone()
+    dy[0, 5], dy[4, 7] = float("inf"), float("nan")
+    w[5], w[7] = 1, 2
+    dx, _ = fa.linear_int8_backward(dy, w, ws)
+    assert bool((dx[0] == float("inf")).all()) and bool(dx[4].isnan().all())
+    w[5], w[7] = ints((N, K), 1, -128)[5], ints((N, K), 1, -128)[7]
+    dx, _ = fa.linear_int8_backward(dy, w, ws)
+    assert torch.equal(dx[1:4], want[1:4])
 
 
 def test_backward_no_tokens_or_channels():

@@ -1780,6 +1780,7 @@ namespace {
 
 constexpr int64_t INT8_MAX_K = (1ll << 17) - 1; // 2^17 - 1 products of up to 2^14 stay below 2^31
 constexpr int64_t QUANTIZE_MAX_ROWS = 1ll << 36;
+constexpr int64_t INT8_GRAD_ROWS = 2048;
 
 int check_linear_int8(int dtype, int64_t M, int64_t N, int64_t K, int act)
 {
@@ -1812,8 +1813,9 @@ Int8Forward int8_forward_plan(int64_t M, int64_t N, int64_t K, bool quantized)
             fa::gemm8_workspace_bytes(M, N, K, cu_count())};
 }
 
-// linear_int8_backward's workspace: dz times the channels' scales, the column
-// sums' partials, the weights as values, and the product's partial sums.
+// linear_int8_backward's workspace: dz times the channels' scales (for fp32 as
+// three bf16), the column sums' partials, and the product's partial sums; where
+// the weights cannot be read as they are, also the weights as values.
 struct Int8Backward {
     size_t dz, part, w, dx;
     size_t total() const { return dz + part + w + dx; }
@@ -1822,10 +1824,10 @@ struct Int8Backward {
 Int8Backward int8_backward_plan(int dtype, int64_t M, int64_t N, int64_t K)
 {
     const int cus = cu_count();
-    return {round256((size_t)M * dz_pitch(N) * dsize(dtype)),
+    return {round256((size_t)M * dz_pitch(N) * (dtype == FA_BF16 ? 2 : 6)),
             round256((size_t)fa::act_grad_partials(M, N, cus) * N * sizeof(float)),
             round256((size_t)N * dz_pitch(K) * dsize(dtype)),
-            fa::gemm_workspace_bytes(dtype, M, K, N, fa::GEMM_B_OUTER, cus)};
+            std::max(fa::gemm_workspace_bytes(dtype, M, K, N, fa::GEMM_B_OUTER, cus), fa::grad8_workspace_bytes(M, N, K, cus))};
 }
 
 } // namespace
@@ -1986,28 +1988,39 @@ int linear_int8_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const 
     g.N = N;
     g.act = act;
     g.col_scale = dx ? w_scale : nullptr;
+    // With more rows a bf16 product repays the weights' way through memory as
+    // values, which the faster kernel for large products reads: 2048, 4096 x 8192 x
+    // 2048 in 104, 179 us directly, 108, 167 as values; 64 x 14336 x 4096 30 and
+    // 82.  fp32 has the faster kernel here: 4096 x 8192 x 2048 467 and 1035.
+    const bool direct = dx && fa::grad8_ok(N, K, w, ldw) && (dtype == FA_F32 || M <= INT8_GRAD_ROWS);
+    g.plane = direct && dtype == FA_F32 ? M * dz_pitch(N) : 0;
     hipError_t e = fa::launch_act_grad(g, dtype, cus, f, s);
     if (e != hipSuccess)
         return hip_fail(e, "activation gradient launch");
     if (dx) {
         char *values = ws + plan.dz + plan.part;
-        e = fa::launch_widen(w, ldw, N, K, dtype, values, dz_pitch(K), s);
-        if (e != hipSuccess)
-            return hip_fail(e, "weights as values launch");
         fa::GemmArgs a{};
         a.a = ws;
         a.lda = dz_pitch(N);
         a.a_padded = true;
-        a.b = values;
-        a.ldb = dz_pitch(K);
-        a.b_padded = true;
+        a.b = w;
+        a.ldb = ldw;
+        if (!direct) {
+            e = fa::launch_widen(w, ldw, N, K, dtype, values, dz_pitch(K), s);
+            if (e != hipSuccess)
+                return hip_fail(e, "weights as values launch");
+            a.b = values;
+            a.ldb = dz_pitch(K);
+            a.b_padded = true;
+        }
         a.M = (int)M;
         a.N = (int)K;
         a.K = (int)N;
         a.alpha = alpha;
         a.out = dx;
         a.ldo = lddx;
-        e = fa::launch_gemm(a, dtype, fa::GEMM_B_OUTER, values + plan.w, cus, f, s);
+        e = direct ? fa::launch_grad8(a, dtype, g.plane, values + plan.w, cus, f, s)
+                   : fa::launch_gemm(a, dtype, fa::GEMM_B_OUTER, values + plan.w, cus, f, s);
         if (e != hipSuccess)
             return hip_fail(e, "input gradient launch");
     }

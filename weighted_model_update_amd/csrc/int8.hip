@@ -428,6 +428,190 @@ __global__ __launch_bounds__(FEW_THREADS) void few_kernel(GemmArgs p, int range)
     }
 }
 
+// ------------------------------------------------------------ the input gradient
+// dx(m,k) = sum_n u(m,n) w(n,k) with u = dz sw in PLANES of bf16: one for bf16
+// results, three for fp32 (u = a + 2^-8 b + 2^-16 c, 8 bits each, exactly).  The
+// 8-bit weights are exact in bf16 as well, so three products on the 16-bit matrix
+// cores, whose sums are joined at the end, give fp32's precision at five times its
+// rate.  w stays in 8 bits up to the
+// registers: a transposing read gives a lane its column's eight bytes.
+// GRAD8_NOTE
+constexpr int GRAD_STEP = 64; // n a step
+
+// Rows of 8-bit weights, GRAD_STEP of them by COLS; the 16-byte chunks of row k
+// are exchanged so that the rows that a read touches spread over the banks.
+template <int COLS, int THREADS> struct ByteRows {
+    static constexpr int CPR = COLS / 16, CHUNKS = GRAD_STEP * CPR, CH = CHUNKS / THREADS;
+    static_assert(CHUNKS % THREADS == 0, "every thread copies as much");
+    uint32_t off[CH];
+    const char *base;
+    int64_t advance;
+
+    static __device__ __forceinline__ int swizzle(int k) { return COLS == 64 ? (k >> 2) & 3 : (k >> 1) & 7; }
+
+    __device__ __forceinline__ void init(const int8_t *w, int64_t ld, int c0, int cols, int k0)
+    {
+        base = reinterpret_cast<const char *>(w + (int64_t)k0 * ld + c0);
+        advance = GRAD_STEP * ld;
+#pragma unroll
+        for (int c = 0; c < CH; c++) {
+            const int q = threadIdx.x + c * THREADS, k = q / CPR, ch = (q % CPR) ^ swizzle(k);
+            off[c] = c0 + ch * 16 < cols ? (uint32_t)(k * ld) + ch * 16 : OUT_OF_RANGE;
+        }
+    }
+
+    __device__ __forceinline__ void start(char *tile, int64_t shift, int left) const
+    {
+        const __amdgpu_buffer_rsrc_t rsrc =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(base + shift), 0, (int)OUT_OF_RANGE, 0x00020000);
+#pragma unroll
+        for (int c = 0; c < CH; c++) {
+            const int first = (threadIdx.x / WAVE) * WAVE + c * THREADS;
+            uint32_t o = off[c];
+            if (left < GRAD_STEP)
+                o = (threadIdx.x + c * THREADS) / CPR < left ? o : OUT_OF_RANGE;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rsrc, (__attribute__((address_space(3))) void *)(tile + first * 16), 16, o, 0, 0, 0);
+        }
+    }
+
+    // Columns c0 .. c0 + 15 at the rows 32 kk .. 32 kk + 31 as a fragment in bf16.
+    static __device__ __forceinline__ Frag read(const char *tile, int c0, int kk, int lane)
+    {
+        typedef int v2i __attribute__((ext_vector_type(2)));
+        const int i = lane & 15, g = lane >> 4, k = kk * 32 + 8 * g + (i >> 1);
+        const char *at = tile + (k * COLS + (((c0 >> 4) ^ swizzle(k)) << 4) + 8 * (i & 1));
+        const v2i b = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) v2i *)const_cast<char *>(at));
+        Frag f;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                v[e] = __builtin_bit_cast(uint32_t, (float)(int8_t)(b[h] >> (8 * e)));
+            f.v[2 * h] = __builtin_amdgcn_perm(v[1], v[0], 0x07060302); // the upper halves: exact
+            f.v[2 * h + 1] = __builtin_amdgcn_perm(v[3], v[2], 0x07060302);
+        }
+        return f;
+    }
+};
+
+template <typename O, int PLANES, int BM, int BN, int WM, int WN, int BUFS>
+__global__ __launch_bounds__(WM *WN *WAVE) void grad8_kernel(GemmArgs p, int64_t plane, int tiles_m, int tiles_n, int kper, float *part)
+{
+    typedef __bf16 T;
+    constexpr int THREADS = WM * WN * WAVE, FM = BM / WM / 16, FN = BN / WN / 16;
+    constexpr int AB = BM * STEP_BYTES, BYTES = PLANES * AB + GRAD_STEP * BN; // of a buffer
+    constexpr int COPIES = BYTES / 16 / THREADS;
+    static_assert(AB % (16 * THREADS) == 0 && (BUFS == 2 || BUFS == 4), "every thread copies as much");
+    __shared__ __attribute__((aligned(1024))) char l0[BYTES];
+    __shared__ __attribute__((aligned(1024))) char l1[BYTES];
+    __shared__ __attribute__((aligned(1024))) char l2[BUFS == 4 ? BYTES : 16];
+    __shared__ __attribute__((aligned(1024))) char l3[BUFS == 4 ? BYTES : 16];
+
+    unsigned tm, tn;
+    tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    const int m0 = (int)tm * BM, n0 = (int)tn * BN;
+    const int wave = threadIdx.x / WAVE, lane = threadIdx.x % WAVE;
+    const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
+    const int k0 = blockIdx.y * kper, kend = p.K - k0 < kper ? p.K : k0 + kper;
+    const int steps = (kend - k0 + GRAD_STEP - 1) / GRAD_STEP;
+    Direct<T, false, BM, THREADS, STEP_BYTES> a;
+    ByteRows<BN, THREADS> b;
+    a.init(static_cast<const T *>(p.a), p.lda, m0, p.M, k0);
+    b.init(static_cast<const int8_t *>(p.b), p.ldb, n0, p.N, k0);
+    f32x4 acc[PLANES][FM][FN];
+#pragma unroll
+    for (int q = 0; q < PLANES; q++)
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+#pragma unroll
+            for (int j = 0; j < FN; j++)
+                acc[q][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const auto copy = [&](char *l, int s) {
+        const int left = kend - k0 - s * GRAD_STEP;
+#pragma unroll
+        for (int q = 0; q < PLANES; q++)
+            a.start_at(l + q * AB, s * a.advance + q * plane * 2, left);
+        b.start(l + PLANES * AB, s * b.advance, left);
+    };
+    const auto step = [&](const char *l) {
+#pragma unroll
+        for (int kk = 0; kk < 2; kk++) {
+            Frag fa[PLANES][FM], fb[FN];
+#pragma unroll
+            for (int j = 0; j < FN; j++)
+                fb[j] = ByteRows<BN, THREADS>::read(l + PLANES * AB, wn + j * 16, kk, lane);
+#pragma unroll
+            for (int q = 0; q < PLANES; q++)
+#pragma unroll
+                for (int i = 0; i < FM; i++)
+                    fa[q][i] = read_frag<T, false, BM, STEP_BYTES>(l + q * AB, wm + i * 16, kk, lane);
+#pragma unroll
+            for (int q = 0; q < PLANES; q++)
+#pragma unroll
+                for (int i = 0; i < FM; i++)
+#pragma unroll
+                    for (int j = 0; j < FN; j++)
+                        acc[q][i][j] = mma<T>(fb[j], fa[q][i], acc[q][i][j]);
+        }
+    };
+    if constexpr (BUFS == 4) {
+        const auto turn = [&](const char *cur, char *free, int t) {
+            if (t + 2 < steps)
+                copies_done<2 * COPIES, true>();
+            else if (t + 1 < steps)
+                copies_done<COPIES, true>();
+            else
+                copies_done<0, true>();
+            if (t + 3 < steps)
+                copy(free, t + 3);
+            step(cur);
+        };
+        if (steps > 0)
+            copy(l0, 0);
+        if (steps > 1)
+            copy(l1, 1);
+        if (steps > 2)
+            copy(l2, 2);
+        for (int t = 0; t < steps; t += 4) {
+            turn(l0, l3, t);
+            if (t + 1 < steps)
+                turn(l1, l0, t + 1);
+            if (t + 2 < steps)
+                turn(l2, l1, t + 2);
+            if (t + 3 < steps)
+                turn(l3, l2, t + 3);
+        }
+    } else {
+        if (steps > 0)
+            copy(l0, 0);
+        for (int s = 0; s < steps; s += 2) {
+            copies_done<0, true>();
+            if (s + 1 < steps)
+                copy(l1, s + 1);
+            step(l0);
+            if (s + 1 < steps) {
+                copies_done<0, true>();
+                if (s + 2 < steps)
+                    copy(l0, s + 2);
+                step(l1);
+            }
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = PLANES - 1; q > 0; q--)
+#pragma unroll
+        for (int i = 0; i < FM; i++)
+#pragma unroll
+            for (int j = 0; j < FN; j++)
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    acc[q - 1][i][j][e] = __builtin_fmaf(0x1p-8f, acc[q][i][j][e], acc[q - 1][i][j][e]);
+    write_tile<O, BM, BN, WM, WN, BYTES>(p, m0, n0, acc[0], l0, l1, part);
+}
+
 // ------------------------------------------------------------ weights as values
 // The whole numbers of wq in T (exact), rows of `ldo` elements with zeros behind
 // the row; bound by memory.
@@ -523,6 +707,41 @@ template <typename O, int BM, int BN, int WM, int WN> hipError_t run_pipe8(const
     return hipGetLastError();
 }
 
+// Tiles of the input gradient and how often n is split.
+struct GradPlan {
+    int tile, splits, kper;
+};
+
+GradPlan grad_plan(int64_t M, int64_t N, int64_t K, int cus)
+{
+    const bool large = tiles8(M, N, 128, 128) >= cus;
+    const int64_t count = large ? tiles8(M, N, 128, 128) : std::max<int64_t>(1, tiles8(M, N, 64, 64));
+    const int64_t steps = std::max<int64_t>(1, (K + GRAD_STEP - 1) / GRAD_STEP);
+    const int64_t want = large ? 1 : std::max<int64_t>(1, std::min<int64_t>({2 * cus / count, steps / 4, 16}));
+    const int64_t per = (steps + want - 1) / want;
+    return {large ? 128 : 64, (int)((steps + per - 1) / per), (int)(per * GRAD_STEP)};
+}
+
+template <typename O, int PLANES> hipError_t run_grad(const GemmArgs &a, int64_t plane, float *ws, int cus, Finish &f, hipStream_t s)
+{
+    const GradPlan p = grad_plan(a.M, a.N, a.K, cus);
+    const int tm = (a.M + p.tile - 1) / p.tile, tn = (a.N + p.tile - 1) / p.tile;
+    float *part = p.splits > 1 ? ws : nullptr;
+    const dim3 grid((unsigned)((int64_t)tm * tn), (unsigned)p.splits);
+    if (p.tile == 128)
+        grad8_kernel<O, PLANES, 128, 128, 2, 4, 2><<<grid, 512, 0, s>>>(a, plane, tm, tn, p.kper, part);
+    else
+        grad8_kernel<O, PLANES, 64, 64, 2, 2, 4><<<grid, 256, 0, s>>>(a, plane, tm, tn, p.kper, part);
+    if (p.splits > 1) {
+        const int j = f.blocks[0] > 0;
+        f.p[j] = a;
+        f.part[j] = part;
+        f.splits[j] = p.splits;
+        f.blocks[j] = finish_blocks(a.M, a.N);
+    }
+    return hipGetLastError();
+}
+
 template <typename O, typename X> hipError_t run_few(const GemmArgs &a, int cus, hipStream_t s)
 {
     const int per = (a.K + FEW_WAVES - 1) / FEW_WAVES, range = (per + WAVE - 1) / WAVE * WAVE;
@@ -600,6 +819,26 @@ hipError_t launch_gemm8(const GemmArgs &a, int dt, void *ws, int cus, hipStream_
     if (a.M == 0 || a.N == 0)
         return hipSuccess;
     return dt == FA_BF16 ? gemm8_of<__bf16>(a, ws, cus, s) : gemm8_of<float>(a, ws, cus, s);
+}
+
+bool grad8_ok(int64_t N, int64_t K, const void *w, int64_t ldw)
+{
+    // as direct_ok, for the rows of w along K
+    return N >= 1 && direct_ok(w, ldw, K, false);
+}
+
+size_t grad8_workspace_bytes(int64_t M, int64_t N, int64_t K, int cus)
+{
+    const GradPlan p = grad_plan(M, K, N, cus);
+    return p.splits > 1 ? ((size_t)p.splits * M * K * sizeof(float) + 255) / 256 * 256 : 0;
+}
+
+hipError_t launch_grad8(const GemmArgs &a, int dt, int64_t plane, void *ws, int cus, Finish &f, hipStream_t s)
+{
+    if (a.M == 0 || a.N == 0)
+        return hipSuccess;
+    float *part = static_cast<float *>(ws);
+    return dt == FA_BF16 ? run_grad<__bf16, 1>(a, plane, part, cus, f, s) : run_grad<float, 3>(a, plane, part, cus, f, s);
 }
 
 hipError_t launch_widen(const int8_t *w, int64_t ldw, int64_t rows, int64_t cols, int dt, void *out, int64_t ldo, hipStream_t s)

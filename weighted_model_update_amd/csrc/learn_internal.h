@@ -46,6 +46,9 @@ struct ActGradArgs {
     int64_t M, N;
     int act;
     const float *col_scale; // N factors of the stored dz, nullable; not of db
+    // fp32 alone, 0: dz in fp32.  Else dz = a + 2^-8 b + 2^-16 c as three bf16
+    // matrices, `plane` elements apart.
+    int64_t plane;
 };
 int64_t act_grad_partials(int64_t M, int64_t N, int cus);
 
@@ -66,6 +69,7 @@ size_t gemm_workspace_bytes(int dt, int64_t M, int64_t N, int64_t K, int layout,
 hipError_t launch_gemm(const GemmArgs &a, int dt, int layout, void *ws, int cus, Finish &f, hipStream_t s);
 hipError_t launch_act_grad(const ActGradArgs &a, int dt, int cus, Finish &f, hipStream_t s);
 hipError_t launch_finish(const Finish &f, int dt, hipStream_t s);
+int64_t finish_blocks(int64_t M, int64_t N); // Finish.blocks of a split product
 
 // ---------------------------------------------------------------- 8-bit layers
 struct QuantizeArgs {
@@ -87,6 +91,12 @@ hipError_t launch_gemm8(const GemmArgs &a, int dt, void *ws, int cus, hipStream_
 bool few8_ok(int64_t M, int64_t K, const void *w, int64_t ldw);
 // That launch, from rows a.a of dt (a.row_scale is not used).
 hipError_t launch_few8(const GemmArgs &a, int dt, int cus, hipStream_t s);
+
+// dx = alpha u w for u [M][N] (a.a, pitch a.lda, zeros behind the row) in bf16, one
+// matrix (dt FA_BF16) or three of them, `plane` elements apart (FA_F32), and 8-bit w [N][K] (a.b).  As a product: a.M = M, a.N = K, a.K = N.
+bool grad8_ok(int64_t N, int64_t K, const void *w, int64_t ldw);
+size_t grad8_workspace_bytes(int64_t M, int64_t N, int64_t K, int cus);
+hipError_t launch_grad8(const GemmArgs &a, int dt, int64_t plane, void *ws, int cus, Finish &f, hipStream_t s);
 
 // out [rows][ldo] = w as values of dt, zeros from column `cols` on.
 hipError_t launch_widen(const int8_t *w, int64_t ldw, int64_t rows, int64_t cols, int dt, void *out, int64_t ldo,

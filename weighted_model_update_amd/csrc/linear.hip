@@ -224,7 +224,7 @@ hipError_t run_tile(const GemmArgs &a, int layout, int splits, float *ws, Finish
         f.p[j] = a;
         f.part[j] = part;
         f.splits[j] = k.splits;
-        f.blocks[j] = ((int64_t)a.M * ((a.N + JOIN_W - 1) / JOIN_W) + FINISH_THREADS - 1) / FINISH_THREADS;
+        f.blocks[j] = finish_blocks(a.M, a.N);
     }
     return hipGetLastError();
 }
@@ -254,6 +254,26 @@ template <typename T, int BM, int BN, int WM, int WN> hipError_t run_pipe(const 
 // rows are spread over idle threads: GELU of 1126 x 112 16.2 -> 5.4 us, of
 // 1594 x 2440 21.9 -> 12.2 (against 16 rows a thread, 2048 columns a workgroup).
 constexpr int AG_THREADS = 256, AG_W = 8, AG_U = 4;
+
+// An fp32 as a + 2^-8 b + 2^-16 c of bf16: 8 bits each, cut off rather than
+// rounded, so that the first stays finite; the others are scaled so that small
+// values keep their bits.  NaN and infinities have the first alone.
+__device__ __forceinline__ void store_planes(__bf16 *to, int64_t plane, const float *v)
+{
+    __bf16 e[3][AG_W];
+#pragma unroll
+    for (int i = 0; i < AG_W; i++) {
+        const auto cut = [](float x) { return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & 0xffff0000u); };
+        const bool finite = fabsf(v[i]) < INFINITY;
+        const float hi = finite ? cut(v[i]) : v[i], rest = finite ? (v[i] - hi) * 256.f : 0.f, mid = cut(rest);
+        e[0][i] = (__bf16)hi;
+        e[1][i] = (__bf16)mid;
+        e[2][i] = (__bf16)((rest - mid) * 256.f);
+    }
+#pragma unroll
+    for (int q = 0; q < 3; q++)
+        __builtin_memcpy(to + q * plane, e[q], sizeof e[q]);
+}
 
 template <typename T> __global__ __launch_bounds__(AG_THREADS) void act_grad_kernel(ActGradArgs p, int64_t rows_per, int across)
 {
@@ -288,8 +308,12 @@ template <typename T> __global__ __launch_bounds__(AG_THREADS) void act_grad_ker
                 for (int i = 0; i < AG_W; i++)
                     d[u][i] *= scale[i];
             }
-            if (p.dz)
+            if (p.dz && p.plane) {
+                if constexpr (sizeof(T) == 4)
+                    store_planes(static_cast<__bf16 *>(p.dz) + m * p.lddz + n, p.plane, d[u]);
+            } else if (p.dz) {
                 store_n<T, AG_W>(static_cast<T *>(p.dz) + m * p.lddz + n, AG_W, d[u]);
+            }
         }
     }
     if (!p.db)
@@ -485,6 +509,11 @@ template <typename T> hipError_t gemm_of(GemmArgs a, int layout, float *ws, int 
 }
 
 } // namespace
+
+int64_t finish_blocks(int64_t M, int64_t N)
+{
+    return (M * ((N + JOIN_W - 1) / JOIN_W) + FINISH_THREADS - 1) / FINISH_THREADS;
+}
 
 size_t gemm_workspace_bytes(int dt, int64_t M, int64_t N, int64_t K, int layout, int cus)
 {

@@ -472,8 +472,8 @@ template <bool OUTER, int ROWS, int THREADS, int STEP> struct PairCopy {
 
     __device__ __forceinline__ void start(char *tile)
     {
-        d.start_whole(tile, 0);
-        d.start_whole(tile + ROWS * STEP, lo);
+        d.start_at(tile, 0, d.BK);
+        d.start_at(tile + ROWS * STEP, lo, d.BK);
         d.base += d.advance;
     }
 };

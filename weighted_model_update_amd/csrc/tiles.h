@@ -450,9 +450,8 @@ template <typename T, bool OUTER, int ROWS, int THREADS, int STEP> struct Direct
         base += advance;
     }
 
-    // The same of an operand padded with zeros to whole steps, `shift` bytes
-    // from its base, which stays.
-    __device__ __forceinline__ void start_whole(char *tile, int64_t shift) const
+    // The same `shift` bytes from the base, which stays.
+    __device__ __forceinline__ void start_at(char *tile, int64_t shift, int left) const
     {
         const __amdgpu_buffer_rsrc_t rsrc =
             __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(base + shift), 0, (int)OUT_OF_RANGE, 0x00020000);
@@ -461,8 +460,14 @@ template <typename T, bool OUTER, int ROWS, int THREADS, int STEP> struct Direct
             const int first = (threadIdx.x / WAVE) * WAVE + c * THREADS;
             if (CHUNKS % THREADS != 0 && first >= CHUNKS)
                 break;
+            uint32_t o = off[c];
+            if (left < BK) {
+                const int q = threadIdx.x + c * THREADS;
+                const int k = OUTER ? q / CPR : ((q % CPR) ^ inner_swizzle<STEP>(q / CPR)) * EPC;
+                o = k < left ? o : OUT_OF_RANGE;
+            }
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rsrc, (__attribute__((address_space(3))) void *)(tile + first * 16), 16, off[c], 0, 0, 0);
+                rsrc, (__attribute__((address_space(3))) void *)(tile + first * 16), 16, o, 0, 0, 0);
         }
     }
 };

@@ -630,6 +630,7 @@ int linear_int8_forward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const v
  * gradient.  dx [M][K] and db (N values) are each nullable; w and w_scale are
  * needed for dx, preact for an activation.  dz * w_scale is held in dtype for
  * the product; db sums dz unrounded.  M == 0 gives zero db, N == 0 zero dx.
+ * N <= 2^22 (FA_ERR_RANGE).
  * Outputs must not overlap the inputs or each other, nor the workspace anything
  * else (FA_ERR_ARG).
  */

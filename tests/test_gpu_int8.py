@@ -129,7 +129,7 @@ def check_forward(xq, xs, w, ws, bias, act, residual, alpha, out, pre):
 # 256) and the steps of 64 and 128 values; sums split over workgroups; odd widths
 SHAPES = [(1, 1, 1), (1, 40, 16), (3, 5, 7), (16, 16, 64), (17, 33, 65), (1, 1000, 4096), (2, 130, 9000), (16, 300, 1024),
           (33, 96, 144), (64, 64, 128), (65, 129, 1040), (300, 16, 1024), (1000, 9, 133), (129, 257, 130), (257, 264, 2000),
-          (520, 1032, 128), (1100, 1030, 321), (2050, 2100, 208), (4100, 2050, 96), (2050, 4100, 96)]
+          (520, 1032, 128), (1100, 1030, 321), (2050, 2100, 208), (4100, 2050, 96), (2050, 4100, 96), (1500, 1400, 1001)]
 
 
 @pytest.mark.parametrize("dt", list(DTYPES))

@@ -56,7 +56,7 @@ BIG = 1 << 17
     (forward, dict(work=at(11)), ARG), (forward, dict(work=at(3)), ARG), (forward, dict(work=at(4)), ARG),
     (forward, dict(M=20, N=8192, K=16384, ldx=16384, ldw=16384, ldr=8192, ldo=8192, ldp=8192, work=None), WORKSPACE),
     (backward, dict(dtype=2), DTYPE), (backward, dict(act=-1), ARG), (backward, dict(N=-1), ARG),
-    (backward, dict(K=BIG, ldw=BIG, lddx=BIG), RANGE),
+    (backward, dict(K=BIG, ldw=BIG, lddx=BIG), RANGE), (backward, dict(N=(1 << 22) + 1, lddy=1 << 23, ldp=1 << 23), RANGE),
     (backward, dict(dy=None), ARG), (backward, dict(w=None), ARG), (backward, dict(ws=None), ARG), (backward, dict(pre=None), ARG),
     (backward, dict(dy=at(1, 1)), ARG), (backward, dict(lddx=15), ARG), (backward, dict(lddy=-8), ARG),
     (backward, dict(dx=at(1)), ARG), (backward, dict(dx=at(2)), ARG), (backward, dict(dx=at(11, 4)), ARG),

@@ -1780,7 +1780,7 @@ namespace {
 
 constexpr int64_t INT8_MAX_K = (1ll << 17) - 1; // 2^17 - 1 products of up to 2^14 stay below 2^31
 constexpr int64_t QUANTIZE_MAX_ROWS = 1ll << 36;
-constexpr int64_t INT8_GRAD_ROWS = 2048;
+constexpr int64_t INT8_GRAD_ROWS = 2048, INT8_GRAD_MAX_N = 1ll << 22;
 
 int check_linear_int8(int dtype, int64_t M, int64_t N, int64_t K, int act)
 {
@@ -1814,8 +1814,8 @@ Int8Forward int8_forward_plan(int64_t M, int64_t N, int64_t K, bool quantized)
 }
 
 // linear_int8_backward's workspace: dz times the channels' scales (for fp32 as
-// three bf16), the column sums' partials, and the product's partial sums; where
-// the weights cannot be read as they are, also the weights as values.
+// three bf16), the column sums' partials, the weights as values (large bf16
+// products) or with whole rows, and the product's partial sums.
 struct Int8Backward {
     size_t dz, part, w, dx;
     size_t total() const { return dz + part + w + dx; }
@@ -1826,8 +1826,8 @@ Int8Backward int8_backward_plan(int dtype, int64_t M, int64_t N, int64_t K)
     const int cus = cu_count();
     return {round256((size_t)M * dz_pitch(N) * (dtype == FA_BF16 ? 2 : 6)),
             round256((size_t)fa::act_grad_partials(M, N, cus) * N * sizeof(float)),
-            round256((size_t)N * dz_pitch(K) * dsize(dtype)),
-            std::max(fa::gemm_workspace_bytes(dtype, M, K, N, fa::GEMM_B_OUTER, cus), fa::grad8_workspace_bytes(M, N, K, cus))};
+            round256(M > INT8_GRAD_ROWS && dtype == FA_BF16 ? (size_t)N * dz_pitch(K) * 2 : (size_t)N * q_pitch(K)),
+            std::max(fa::gemm_workspace_bytes(dtype, M, K, N, fa::GEMM_B_OUTER, cus), fa::grad8_workspace_bytes(dtype, M, N, K, cus))};
 }
 
 } // namespace
@@ -1863,6 +1863,8 @@ int linear_int8_workspace_size(fa_dtype dtype, int64_t M, int64_t N, int64_t K, 
     const int rc = check_linear_int8(dtype, M, N, K, FA_ACT_NONE);
     if (rc != FA_OK)
         return rc;
+    if (backward && N > INT8_GRAD_MAX_N)
+        return fail(FA_ERR_RANGE, "N must be at most 2^22");
     *bytes = backward ? int8_backward_plan(dtype, M, N, K).total() : int8_forward_plan(M, N, K, quantized != 0).total();
     return ok();
 }
@@ -1949,6 +1951,8 @@ int linear_int8_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const 
         return rc;
     if (!dx && !db)
         return ok();
+    if (N > INT8_GRAD_MAX_N)
+        return fail(FA_ERR_RANGE, "N must be at most 2^22");
     const size_t es = dsize(dtype);
     const bool has_act = act != FA_ACT_NONE;
     const View vy{dy, M, N, lddy, es}, vw{w, dx ? N : 0, K, ldw, 1},
@@ -1992,35 +1996,39 @@ int linear_int8_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const 
     // values, which the faster kernel for large products reads: 2048, 4096 x 8192 x
     // 2048 in 104, 179 us directly, 108, 167 as values; 64 x 14336 x 4096 30 and
     // 82.  fp32 has the faster kernel here: 4096 x 8192 x 2048 467 and 1035.
-    const bool direct = dx && fa::grad8_ok(N, K, w, ldw) && (dtype == FA_F32 || M <= INT8_GRAD_ROWS);
-    g.plane = direct && dtype == FA_F32 ? M * dz_pitch(N) : 0;
+    const bool values = dtype == FA_BF16 && M > INT8_GRAD_ROWS;
+    g.plane = dx && dtype == FA_F32 ? M * dz_pitch(N) : 0;
     hipError_t e = fa::launch_act_grad(g, dtype, cus, f, s);
     if (e != hipSuccess)
         return hip_fail(e, "activation gradient launch");
     if (dx) {
-        char *values = ws + plan.dz + plan.part;
+        char *own = ws + plan.dz + plan.part; // weights
         fa::GemmArgs a{};
         a.a = ws;
         a.lda = dz_pitch(N);
         a.a_padded = true;
         a.b = w;
         a.ldb = ldw;
-        if (!direct) {
-            e = fa::launch_widen(w, ldw, N, K, dtype, values, dz_pitch(K), s);
-            if (e != hipSuccess)
-                return hip_fail(e, "weights as values launch");
-            a.b = values;
+        if (values) {
+            e = fa::launch_widen(w, ldw, N, K, own, dz_pitch(K), s);
+            a.b = own;
             a.ldb = dz_pitch(K);
             a.b_padded = true;
+        } else if (!fa::grad8_ok(N, K, w, ldw)) {
+            e = fa::launch_copy8(w, ldw, N, K, reinterpret_cast<int8_t *>(own), q_pitch(K), s);
+            a.b = own;
+            a.ldb = q_pitch(K);
         }
+        if (e != hipSuccess)
+            return hip_fail(e, "weights' copy launch");
         a.M = (int)M;
         a.N = (int)K;
         a.K = (int)N;
         a.alpha = alpha;
         a.out = dx;
         a.ldo = lddx;
-        e = direct ? fa::launch_grad8(a, dtype, g.plane, values + plan.w, cus, f, s)
-                   : fa::launch_gemm(a, dtype, fa::GEMM_B_OUTER, values + plan.w, cus, f, s);
+        e = values ? fa::launch_gemm(a, dtype, fa::GEMM_B_OUTER, own + plan.w, cus, f, s)
+                   : fa::launch_grad8(a, dtype, g.plane, own + plan.w, cus, f, s);
         if (e != hipSuccess)
             return hip_fail(e, "input gradient launch");
     }

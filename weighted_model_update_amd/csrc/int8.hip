@@ -166,7 +166,9 @@ __global__ __launch_bounds__(QR_THREADS) void quantize_kernel(const T *x, int64_
 // ------------------------------------------------------------ products
 // Workgroup (tile, split), as for the other products; partial sums are whole
 // numbers too, so a split changes no result.  Steps are short, so aligned operands
-// go through four buffers.  GEMM8_NOTE
+// go through four buffers: 777 x 2048 x 8192 in 64 x 64 tiles 33 us, with two 37.
+// Fragments and bytes are those of the 16-bit products, at twice the operations:
+// 8192 x 14336 x 4096 in 525 us (1.83 POP/s; the vendor library's product alone 505).
 template <typename O, int BM, int BN, int WM, int WN, bool DIRECT>
 __global__ __launch_bounds__(WM *WN *WAVE) void gemm8_kernel(GemmArgs p, int tiles_m, int tiles_n, int kper, float *part)
 {
@@ -435,7 +437,11 @@ __global__ __launch_bounds__(FEW_THREADS) void few_kernel(GemmArgs p, int range)
 // cores, whose sums are joined at the end, give fp32's precision at five times its
 // rate.  w stays in 8 bits up to the
 // registers: a transposing read gives a lane its column's eight bytes.
-// GRAD8_NOTE
+// 4096 x 8192 x 2048 fp32 in 451 us with the pass over dz (0.91 PFLOP/s of
+// 16-bit products), as products in fp32 1035; 64 x 14336 x 4096 bf16 in 29, with the
+// weights written out as values first 82.  Small tiles take four buffers where
+// they are short (bf16), two and a second workgroup on the CU where not: 512 x 8192
+// x 2048 fp32 82 us, with four 102.
 constexpr int GRAD_STEP = 64; // n a step
 
 // Rows of 8-bit weights, GRAD_STEP of them by COLS; the 16-byte chunks of row k
@@ -614,7 +620,7 @@ __global__ __launch_bounds__(WM *WN *WAVE) void grad8_kernel(GemmArgs p, int64_t
 
 // ------------------------------------------------------------ weights as values
 // The whole numbers of wq in T (exact), rows of `ldo` elements with zeros behind
-// the row; bound by memory.
+// the row; with T = int8_t a copy whose rows are whole chunks.  Bound by memory.
 constexpr int WV_THREADS = 256, WV_W = 16;
 
 template <typename T>
@@ -712,26 +718,28 @@ struct GradPlan {
     int tile, splits, kper;
 };
 
-GradPlan grad_plan(int64_t M, int64_t N, int64_t K, int cus)
+GradPlan grad_plan(int64_t M, int64_t N, int64_t K, int planes, int cus)
 {
+    // Small tiles fill a CU three times over (bf16) or twice (fp32): with one, two,
+    // three a CU 512 x 8192 x 2048 bf16 72, 51, 46 us, fp32 98, 82, 105.
     const bool large = tiles8(M, N, 128, 128) >= cus;
     const int64_t count = large ? tiles8(M, N, 128, 128) : std::max<int64_t>(1, tiles8(M, N, 64, 64));
     const int64_t steps = std::max<int64_t>(1, (K + GRAD_STEP - 1) / GRAD_STEP);
-    const int64_t want = large ? 1 : std::max<int64_t>(1, std::min<int64_t>({2 * cus / count, steps / 4, 16}));
+    const int64_t want = large ? 1 : std::max<int64_t>(1, std::min<int64_t>({(planes == 1 ? 3 : 2) * cus / count, steps / 4, 16}));
     const int64_t per = (steps + want - 1) / want;
     return {large ? 128 : 64, (int)((steps + per - 1) / per), (int)(per * GRAD_STEP)};
 }
 
 template <typename O, int PLANES> hipError_t run_grad(const GemmArgs &a, int64_t plane, float *ws, int cus, Finish &f, hipStream_t s)
 {
-    const GradPlan p = grad_plan(a.M, a.N, a.K, cus);
+    const GradPlan p = grad_plan(a.M, a.N, a.K, PLANES, cus);
     const int tm = (a.M + p.tile - 1) / p.tile, tn = (a.N + p.tile - 1) / p.tile;
     float *part = p.splits > 1 ? ws : nullptr;
     const dim3 grid((unsigned)((int64_t)tm * tn), (unsigned)p.splits);
     if (p.tile == 128)
         grad8_kernel<O, PLANES, 128, 128, 2, 4, 2><<<grid, 512, 0, s>>>(a, plane, tm, tn, p.kper, part);
     else
-        grad8_kernel<O, PLANES, 64, 64, 2, 2, 4><<<grid, 256, 0, s>>>(a, plane, tm, tn, p.kper, part);
+        grad8_kernel<O, PLANES, 64, 64, 2, 2, PLANES == 1 ? 4 : 2><<<grid, 256, 0, s>>>(a, plane, tm, tn, p.kper, part);
     if (p.splits > 1) {
         const int j = f.blocks[0] > 0;
         f.p[j] = a;
@@ -751,10 +759,56 @@ template <typename O, typename X> hipError_t run_few(const GemmArgs &a, int cus,
     return hipGetLastError();
 }
 
-template <typename O> hipError_t gemm8_of(const GemmArgs &a, void *ws, int cus, hipStream_t s)
+template <typename T> hipError_t widen(const int8_t *w, int64_t ldw, int64_t rows, int64_t cols, T *out, int64_t ldo, hipStream_t s)
+{
+    const int64_t chunks = rows * ((ldo + WV_W - 1) / WV_W);
+    const unsigned grid = (unsigned)std::min<int64_t>((chunks + WV_THREADS - 1) / WV_THREADS, 1 << 20);
+    widen_kernel<T><<<grid, WV_THREADS, 0, s>>>(w, ldw, rows, cols, out, ldo);
+    return hipGetLastError();
+}
+
+int64_t row16(int64_t K) { return (K + 15) / 16 * 16; }
+
+// Large products repay copies of odd rows with whole ones, us staged through
+// registers and copied: 8191 x 4096 x 4095 269, 189; 4096 x 8191 x 100 60, 50;
+// 2047 x 2047 x 513 26, 22; 300 x 4096 x 1001 20, 23; 8 x 14336 x 4097 23, 45.
+constexpr double PACK8_LEAST = 2e9;
+constexpr int64_t PACK8_ROWS = 512;
+
+bool pack8_wanted(int64_t M, int64_t N, int64_t K)
+{
+    return K % 16 != 0 && M >= PACK8_ROWS && (double)M * (double)N * (double)K >= PACK8_LEAST && pitch_ok(row16(K));
+}
+
+size_t part8_bytes(int64_t M, int64_t N, int64_t K, int cus)
+{
+    const Plan8 p = plan8(M, N, K, cus);
+    return p.splits > 1 ? ((size_t)p.splits * M * N * sizeof(int32_t) + 255) / 256 * 256 : 0;
+}
+
+template <typename O> hipError_t gemm8_of(GemmArgs a, void *ws, int cus, hipStream_t s)
 {
     const Plan8 p = plan8(a.M, a.N, a.K, cus);
-    const bool direct = direct_ok(a.a, a.lda, a.K, a.a_padded) && direct_ok(a.b, a.ldb, a.K, false);
+    bool ok_a = direct_ok(a.a, a.lda, a.K, a.a_padded), ok_b = direct_ok(a.b, a.ldb, a.K, false);
+    if (!(ok_a && ok_b) && pack8_wanted(a.M, a.N, a.K)) {
+        int8_t *to = static_cast<int8_t *>(ws) + part8_bytes(a.M, a.N, a.K, cus);
+        const int64_t row = row16(a.K);
+        hipError_t e = ok_b ? hipSuccess : widen<int8_t>(static_cast<const int8_t *>(a.b), a.ldb, a.N, a.K, to, row, s);
+        if (!ok_b) {
+            a.b = to;
+            a.ldb = row;
+            to += a.N * row;
+        }
+        if (e == hipSuccess && !ok_a) {
+            e = widen<int8_t>(static_cast<const int8_t *>(a.a), a.lda, a.M, a.K, to, row, s);
+            a.a = to;
+            a.lda = row;
+        }
+        if (e != hipSuccess)
+            return e;
+        ok_a = ok_b = true;
+    }
+    const bool direct = ok_a && ok_b;
     if (few8_ok(a.M, a.K, a.b, a.ldb))
         return run_few<O, int8_t>(a, cus, s);
     if (p.tile <= P8_128_128) {
@@ -799,8 +853,7 @@ hipError_t launch_quantize(const QuantizeArgs &a, int dt, hipStream_t s)
 
 size_t gemm8_workspace_bytes(int64_t M, int64_t N, int64_t K, int cus)
 {
-    const Plan8 p = plan8(M, N, K, cus);
-    return p.splits > 1 ? ((size_t)p.splits * M * N * sizeof(int32_t) + 255) / 256 * 256 : 0;
+    return part8_bytes(M, N, K, cus) + (pack8_wanted(M, N, K) ? ((size_t)((M + N) * row16(K)) + 255) / 256 * 256 : 0);
 }
 
 bool few8_ok(int64_t M, int64_t K, const void *w, int64_t ldw)
@@ -827,9 +880,9 @@ bool grad8_ok(int64_t N, int64_t K, const void *w, int64_t ldw)
     return N >= 1 && direct_ok(w, ldw, K, false);
 }
 
-size_t grad8_workspace_bytes(int64_t M, int64_t N, int64_t K, int cus)
+size_t grad8_workspace_bytes(int dt, int64_t M, int64_t N, int64_t K, int cus)
 {
-    const GradPlan p = grad_plan(M, K, N, cus);
+    const GradPlan p = grad_plan(M, K, N, dt == FA_BF16 ? 1 : 3, cus);
     return p.splits > 1 ? ((size_t)p.splits * M * K * sizeof(float) + 255) / 256 * 256 : 0;
 }
 
@@ -841,17 +894,14 @@ hipError_t launch_grad8(const GemmArgs &a, int dt, int64_t plane, void *ws, int 
     return dt == FA_BF16 ? run_grad<__bf16, 1>(a, plane, part, cus, f, s) : run_grad<float, 3>(a, plane, part, cus, f, s);
 }
 
-hipError_t launch_widen(const int8_t *w, int64_t ldw, int64_t rows, int64_t cols, int dt, void *out, int64_t ldo, hipStream_t s)
+hipError_t launch_widen(const int8_t *w, int64_t ldw, int64_t rows, int64_t cols, void *out, int64_t ldo, hipStream_t s)
 {
-    if (rows == 0 || cols == 0)
-        return hipSuccess;
-    const int64_t chunks = rows * ((ldo + WV_W - 1) / WV_W);
-    const unsigned grid = (unsigned)std::min<int64_t>((chunks + WV_THREADS - 1) / WV_THREADS, 1 << 20);
-    if (dt == FA_BF16)
-        widen_kernel<__bf16><<<grid, WV_THREADS, 0, s>>>(w, ldw, rows, cols, static_cast<__bf16 *>(out), ldo);
-    else
-        widen_kernel<float><<<grid, WV_THREADS, 0, s>>>(w, ldw, rows, cols, static_cast<float *>(out), ldo);
-    return hipGetLastError();
+    return rows == 0 || cols == 0 ? hipSuccess : widen<__bf16>(w, ldw, rows, cols, static_cast<__bf16 *>(out), ldo, s);
+}
+
+hipError_t launch_copy8(const int8_t *w, int64_t ldw, int64_t rows, int64_t cols, int8_t *out, int64_t ldo, hipStream_t s)
+{
+    return rows == 0 || cols == 0 ? hipSuccess : widen<int8_t>(w, ldw, rows, cols, out, ldo, s);
 }
 
 } // namespace fa

@@ -95,12 +95,12 @@ hipError_t launch_few8(const GemmArgs &a, int dt, int cus, hipStream_t s);
 // dx = alpha u w for u [M][N] (a.a, pitch a.lda, zeros behind the row) in bf16, one
 // matrix (dt FA_BF16) or three of them, `plane` elements apart (FA_F32), and 8-bit w [N][K] (a.b).  As a product: a.M = M, a.N = K, a.K = N.
 bool grad8_ok(int64_t N, int64_t K, const void *w, int64_t ldw);
-size_t grad8_workspace_bytes(int64_t M, int64_t N, int64_t K, int cus);
+size_t grad8_workspace_bytes(int dt, int64_t M, int64_t N, int64_t K, int cus);
 hipError_t launch_grad8(const GemmArgs &a, int dt, int64_t plane, void *ws, int cus, Finish &f, hipStream_t s);
 
-// out [rows][ldo] = w as values of dt, zeros from column `cols` on.
-hipError_t launch_widen(const int8_t *w, int64_t ldw, int64_t rows, int64_t cols, int dt, void *out, int64_t ldo,
-                        hipStream_t s);
+// out [rows][ldo] = w in bf16, or as it is, zeros from column `cols` on.
+hipError_t launch_widen(const int8_t *w, int64_t ldw, int64_t rows, int64_t cols, void *out, int64_t ldo, hipStream_t s);
+hipError_t launch_copy8(const int8_t *w, int64_t ldw, int64_t rows, int64_t cols, int8_t *out, int64_t ldo, hipStream_t s);
 
 // ---------------------------------------------------------------- orthogonalised update
 // out = rate O, or keep out + rate O (add), O the orthogonalised t [B][m][n].

@@ -1553,8 +1553,10 @@ size_t ortho_workspace_bytes(int64_t B, int64_t m, int64_t n, int cus)
 {
     if (B == 0 || m == 0 || n == 0)
         return 0;
+    // A call that takes one launch needs none; it asks for some all the same, so that a
+    // missing workspace shows at every size.
     if (std::min(m, n) <= SHORT_MAX)
-        return short_plan(B, m, n, cus).total();
+        return std::max<size_t>(256, short_plan(B, m, n, cus).total());
     return long_plan(B, m, n, cus).total();
 }
 

@@ -66,6 +66,11 @@ def test_refusals(call, kw, code):
     assert lib().fedavg_last_error()
 
 
+def test_an_input_whose_span_leaves_64_bits_is_refused():
+    # rows and matrices both 2^40 elements apart, neither within the other: 2^61 elements
+    assert orthogonalize(B=1 << 20, m=1 << 10, n=8, ldx=1 << 40, sx=1 << 40, ldo=8, so=1 << 13) == RANGE
+
+
 @pytest.mark.parametrize("empty", [dict(B=0), dict(m=0), dict(n=0)], ids=str)
 def test_nothing_to_do(empty):
     assert orthogonalize(**empty, x=None, out=None, ws=None) == 0

@@ -2070,7 +2070,7 @@ int check_batch(const char *name, const BatchView &v, bool out)
         return fail(FA_ERR_ARG, "%s must be aligned to its element", name);
     if (v.ld < 0 || v.stride < 0)
         return fail(FA_ERR_ARG, "%s has a negative pitch or stride", name);
-    if (v.ld > (1ll << 40) || v.stride > (1ll << 40))
+    if (v.ld > (1ll << 40) || v.stride > (1ll << 40) || (v.B - 1) * v.stride + v.matrix() > (1ll << 58))
         return fail(FA_ERR_RANGE, "%s spans too many elements", name);
     const bool rows = v.m == 1 || v.ld >= v.n, matrices = v.B == 1 || v.stride >= v.n;
     if (out && !(rows && matrices && (v.whole() || v.rowwise())))

@@ -491,9 +491,9 @@ __device__ __forceinline__ f32x4 mma_pair(const Frag &bh, const Frag &bl, const 
 // matrix cores idle while it reads LDS; their sums are joined at the end.  With
 // a tile a CU or fewer a step waits for memory, and four buffers (DEEP) let three
 // steps be on their way; with more tiles two workgroups a CU, with two buffers
-// each, hide it.  All of a 1000 x 1000 call's
-// 15 products: 252 us with one group and two buffers, 226 with four, 202 with two
-// groups and four; XX^T of 1000 x 1000 alone 12 us.
+// each, hide it.  All of a 1000 x 1000 call's 15 products: 252 us with one group
+// and two buffers, 226 with four, 202 with two groups and four; XX^T of 1000 x 1000
+// alone 12 us.
 template <typename O, bool AO, bool BO, bool SYM, bool DEEP>
 __global__ __launch_bounds__(512) void pair_kernel(PairArgs p)
 {
@@ -747,12 +747,13 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pair_pipe_kernel(PairArgs p)
 
 // ------------------------------------------------------------ short sides, in fp64
 // Three stages: the Gram matrix G, its polynomial P, the product with X.  A
-// workgroup has a part of the long side; a call whose matrices have one part
-// each runs all three in one launch, else G's parts go through memory, and P is
-// formed by every workgroup of the last stage where that is cheap (s <= 32).
-// 128 matrices of 16 x 4096 bf16 in one launch 36 us, 67 MB.  One of 64 x 1000: 111 us
-// in one launch, 68 in three; P of 64 x 64 by itself, 15 products one after another on
-// one CU, takes 51 us with 8 wavefronts and 40 with 16.
+// workgroup has a part of the long side; with s <= 32 a call whose matrices have one
+// part each runs all three in one launch.  Else G's parts go through memory, and
+// for s <= 32, where that is cheap, every workgroup of the last stage forms P.
+// 128 matrices of 16 x 4096 fp32 (67 MB): 12 us for the Gram matrices, 24 for P and
+// the product.  One of 64 x 1000: 111 us in one launch, 68 in three; P of 64 x 64 by
+// itself, 15 products one after another on one CU, takes 51 us with 8 wavefronts and
+// 40 with 16.
 constexpr int SHORT_MAX = 64, SHORT_THREADS = 512, SHORT_WAVES = SHORT_THREADS / WAVE, SHORT_STEP = 64;
 constexpr int64_t SHORT_ALONE = 256;
 enum { STAGE_GRAM = 1, STAGE_POLY = 2, STAGE_APPLY = 4 };

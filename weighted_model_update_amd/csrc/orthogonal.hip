@@ -246,7 +246,7 @@ struct PairArgs {
     unsigned whole, rest, splits;
     int per;
     float *part;
-    // v = q (sum) + p T + r U, T and U nullable
+    // v = q (sum) + p T + r U; T nullable, U too, and null without T
     float p, q, r;
     Planes t, u;
     Planes out; // out.p null: the result goes to o.out
@@ -281,27 +281,47 @@ __device__ __forceinline__ void pair_tile(unsigned id, unsigned tiles_m, unsigne
     }
 }
 
-// Finishes EMIT neighbours of row m from their sums; n is a multiple of EMIT.
+// EMIT neighbours of T and U, on their way while the sums are finished.
 constexpr int EMIT = 8;
 
-template <typename O>
-__device__ __forceinline__ void emit(const PairArgs &p, int64_t b, int m, int n, const float *s)
-{
-    float v[EMIT];
-#pragma unroll
-    for (int i = 0; i < EMIT; i++)
-        v[i] = p.q * s[i];
-    const auto add = [&](const Planes &x, float f) {
-        const _Float16 *at = x.p + b * x.stride + (int64_t)m * x.ld + n;
-        const f16x8 h = *reinterpret_cast<const f16x8 *>(at), l = *reinterpret_cast<const f16x8 *>(at + x.lo);
+struct Addends {
+    f16x8 th, tl, uh, ul;
+
+    __device__ __forceinline__ void fetch(const PairArgs &p, int64_t b, int m, int n, bool any)
+    {
+        th = tl = uh = ul = f16x8{};
+        const auto load = [&](const Planes &x, f16x8 &h, f16x8 &l) {
+            const _Float16 *at = x.p + b * x.stride + (int64_t)m * x.ld + n;
+            h = *reinterpret_cast<const f16x8 *>(at);
+            l = *reinterpret_cast<const f16x8 *>(at + x.lo);
+        };
+        if (any && p.t.p)
+            load(p.t, th, tl);
+        if (any && p.u.p)
+            load(p.u, uh, ul);
+    }
+
+    // v = q s + r U + p T
+    __device__ __forceinline__ void finish(const PairArgs &p, float *v) const
+    {
 #pragma unroll
         for (int i = 0; i < EMIT; i++)
-            v[i] = __builtin_fmaf(f, (float)h[i] + (float)l[i], v[i]);
-    };
-    if (p.u.p)
-        add(p.u, p.r);
-    if (p.t.p)
-        add(p.t, p.p);
+            v[i] = p.q * v[i];
+        if (p.u.p)
+#pragma unroll
+            for (int i = 0; i < EMIT; i++)
+                v[i] = __builtin_fmaf(p.r, (float)uh[i] + (float)ul[i], v[i]);
+        if (p.t.p)
+#pragma unroll
+            for (int i = 0; i < EMIT; i++)
+                v[i] = __builtin_fmaf(p.p, (float)th[i] + (float)tl[i], v[i]);
+    }
+};
+
+// Stores EMIT neighbours of row m; n is a multiple of EMIT.
+template <typename O>
+__device__ __forceinline__ void emit(const PairArgs &p, int64_t b, int m, int n, const float *v)
+{
     if (!p.out.p) {
         put_result<O, EMIT>(p.o, b, m, n, p.N - n < EMIT ? p.N - n : EMIT, v);
         return;
@@ -354,43 +374,69 @@ template <bool SYM, int BM, int BN> __device__ __forceinline__ Share share_of(co
 }
 
 // Rows i of the wavefronts' fragments, which lie in LDS at `o`, 16 of each row
-// of wavefronts: whole rows are read and written; a symmetric product's other
-// side is read along the columns.
-template <typename O, int BM, int BN, int WM, int WN>
-__device__ __forceinline__ void emit_rows(const PairArgs &p, const Share &s, int i, const float *o, int thread)
-{
-    constexpr int THREADS = WM * WN * WAVE, ROWS = WM * 16, CHUNKS = ROWS * BN / EMIT;
+// of wavefronts: whole rows are read and written.  A symmetric product's other
+// side is the finished values, read along the columns.
+template <int BM, int BN, int WM, int WN> struct Rows {
+    static constexpr int THREADS = WM * WN * WAVE, ROWS = WM * 16, CHUNKS = ROWS * BN / EMIT, PER = CHUNKS / THREADS;
     static_assert(CHUNKS % THREADS == 0, "every thread writes as much");
-    const int64_t cols = emit_columns(p);
-    const int m0 = (int)s.tm * BM, n0 = (int)s.tn * BN;
-    const auto row = [&](int r) { return m0 + r / 16 * (BM / WM) + i * 16 + r % 16; };
+    Addends add[PER];
+
+    static __device__ __forceinline__ int row(const Share &s, int i, int r)
+    {
+        return (int)s.tm * BM + r / 16 * (BM / WM) + i * 16 + r % 16;
+    }
+
+    __device__ __forceinline__ void fetch(const PairArgs &p, const Share &s, int i, int thread)
+    {
+        const int64_t cols = emit_columns(p);
 #pragma unroll
-    for (int e = 0; e < CHUNKS / THREADS; e++) {
-        const int at = thread + e * THREADS, r = at / (BN / EMIT), c = at % (BN / EMIT) * EMIT;
-        const int m = row(r), n = n0 + c;
-        if (m < p.M && n < cols) {
+        for (int e = 0; e < PER; e++) {
+            const int at = thread + e * THREADS, m = row(s, i, at / (BN / EMIT)), n = (int)s.tn * BN + at % (BN / EMIT) * EMIT;
+            add[e].fetch(p, s.b, m, n, m < p.M && n < cols);
+        }
+    }
+
+    template <typename O>
+    __device__ __forceinline__ void emit_all(const PairArgs &p, const Share &s, int i, float *o, int thread) const
+    {
+        const int64_t cols = emit_columns(p);
+        const int n0 = (int)s.tn * BN;
+#pragma unroll
+        for (int e = 0; e < PER; e++) {
+            const int at = thread + e * THREADS, r = at / (BN / EMIT), c = at % (BN / EMIT) * EMIT;
+            const int m = row(s, i, r), n = n0 + c;
             float v[EMIT];
 #pragma unroll
             for (int g = 0; g < EMIT; g += 4)
                 __builtin_memcpy(v + g, o + write_tile_at<BN>(r, c + g), 16);
-            emit<O>(p, s.b, m, n, v);
+            add[e].finish(p, v);
+            if (m < p.M && n < cols)
+                emit<O>(p, s.b, m, n, v);
+            if (s.mirror && p.t.p)
+#pragma unroll
+                for (int g = 0; g < EMIT; g += 4)
+                    __builtin_memcpy(o + write_tile_at<BN>(r, c + g), v + g, 16);
         }
-    }
-    if (s.mirror) {
+        if (s.mirror) {
+            const float q = p.t.p ? 1.f : p.q; // without T and U the sums are still there
+            if (p.t.p)
+                __syncthreads();
 #pragma unroll
-        for (int e = 0; e < CHUNKS / THREADS; e++) {
-            const int at = thread + e * THREADS, c = at / (ROWS / EMIT), r = at % (ROWS / EMIT) * EMIT;
-            const int n = n0 + c, m = row(r);
-            if (n < p.N && m < cols) {
-                float v[EMIT];
+            for (int e = 0; e < PER; e++) {
+                const int at = thread + e * THREADS, c = at / (ROWS / EMIT), r = at % (ROWS / EMIT) * EMIT;
+                const int n = n0 + c, m = row(s, i, r);
+                if (n < p.N && m < cols) {
+                    float v[EMIT];
 #pragma unroll
-                for (int g = 0; g < EMIT; g++)
-                    v[g] = o[write_tile_at<BN>(r + g, c & ~3) + (c & 3)];
-                emit<O>(p, s.b, n, m, v);
+                    for (int g = 0; g < EMIT; g++)
+                        v[g] = q * o[write_tile_at<BN>(r + g, c & ~3) + (c & 3)];
+                    emit<O>(p, s.b, n, m, v);
+                }
             }
         }
     }
-}
+};
+
 
 template <int BN, int WN> __device__ __forceinline__ int fragment_at(int j, int thread)
 {
@@ -413,15 +459,19 @@ __device__ __forceinline__ void emit_tile(const PairArgs &p, const Share &s, con
                 reinterpret_cast<f32x4 *>(s.part)[(i * FN + j) * THREADS + threadIdx.x] = acc[i][j];
         return;
     }
+    Rows<BM, BN, WM, WN> rows[2];
+    rows[0].fetch(p, s, 0, threadIdx.x);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < FM; i++) {
         float *o = reinterpret_cast<float *>(i & 1 ? b1 : b0);
+        if (i + 1 < FM)
+            rows[(i + 1) & 1].fetch(p, s, i + 1, threadIdx.x);
 #pragma unroll
         for (int j = 0; j < FN; j++)
             *reinterpret_cast<f32x4 *>(o + fragment_at<BN, WN>(j, threadIdx.x)) = acc[i][j];
         __syncthreads();
-        emit_rows<O, BM, BN, WM, WN>(p, s, i, o, threadIdx.x);
+        rows[i & 1].template emit_all<O>(p, s, i, o, threadIdx.x);
     }
 }
 
@@ -439,6 +489,8 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pair_join_kernel(PairArgs p)
     pair_tile<SYM>((p.whole + tile) % (unsigned)p.tiles, p.tiles_m, p.tiles_n, s.tm, s.tn);
     s.mirror = SYM && s.tm != s.tn;
     const f32x4 *from = reinterpret_cast<const f32x4 *>(p.part + (int64_t)tile * p.splits * (BM * BN)) + i * FN * THREADS + threadIdx.x;
+    Rows<BM, BN, WM, WN> rows;
+    rows.fetch(p, s, i, threadIdx.x);
     f32x4 sum[FN];
 #pragma unroll
     for (int j = 0; j < FN; j++)
@@ -452,7 +504,7 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pair_join_kernel(PairArgs p)
     for (int j = 0; j < FN; j++)
         *reinterpret_cast<f32x4 *>(o + fragment_at<BN, WN>(j, threadIdx.x)) = sum[j];
     __syncthreads();
-    emit_rows<O, BM, BN, WM, WN>(p, s, i, o, threadIdx.x);
+    rows.template emit_all<O>(p, s, i, o, threadIdx.x);
 }
 
 // A step's tiles of one operand: the hi plane's, then the lo plane's.  Planes are
@@ -583,6 +635,9 @@ __global__ __launch_bounds__(512) void pair_kernel(PairArgs p)
         if (s < steps)
             step(l0);
     }
+    Rows<BM, BM, WM, WN> rows;
+    if (!sh.part)
+        rows.fetch(p, sh, group, thread);
     // the second group's sums of fragments i = 0 go to the first, the first's of
     // i = 1 to the second, and each finishes its own
     __syncthreads();
@@ -607,7 +662,7 @@ __global__ __launch_bounds__(512) void pair_kernel(PairArgs p)
     for (int j = 0; j < F; j++)
         *reinterpret_cast<f32x4 *>(o + fragment_at<BM, WN>(j, thread)) = mine[j];
     __syncthreads();
-    emit_rows<O, BM, BM, WM, WN>(p, sh, group, o, thread);
+    rows.template emit_all<O>(p, sh, group, o, thread);
 }
 
 // Larger products, bound by the matrix cores: steps of 64 bytes of k in BUFS

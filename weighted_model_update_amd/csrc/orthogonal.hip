@@ -177,14 +177,23 @@ __device__ __forceinline__ void split_value(float v, _Float16 &hi, _Float16 &lo)
     lo = (_Float16)(v - (float)hi);
 }
 
-// A matrix of a batch as two planes: `lo` elements from hi to lo, `stride` from
-// one matrix to the next.  Rows and columns are followed by zeros up to a
-// multiple of PAD, the longest step of k.
-constexpr int PAD = STEP_BYTES / 2;
+// A matrix of a batch as pairs: 32 columns' hi values are followed by their lo
+// values, so that a step of one row is a whole cache line: the square of
+// 4096 x 4096 in 176 us, 14336 x 4096 by 4096 x 4096 in 1.06 ms; as two matrices
+// apart, whose steps are half lines, 213 us and 1.16 ms.
+// `ld` columns a row, `stride` elements from one matrix to the next.  Rows and
+// columns are followed by zeros up to a multiple of PAD, the longest step of k.
+constexpr int PAD = STEP_BYTES / 2, PAIR = 32;
 
 struct Planes {
     _Float16 *p;
-    int64_t ld, lo, stride;
+    int64_t ld, stride;
+
+    // hi of row r, column c and up, of 8; lo lies PAIR behind
+    __device__ __forceinline__ _Float16 *at(int64_t b, int64_t r, int64_t c) const
+    {
+        return p + b * stride + r * 2 * ld + c + c / PAIR * PAIR;
+    }
 };
 
 // X = t / |t| times `scale` as planes, with their zeros; also the zeros behind the
@@ -223,17 +232,15 @@ __global__ __launch_bounds__(NORM_THREADS) void split_kernel(OrthoArgs p, int pa
             h[i] = c + i < p.n ? hi : (_Float16)0;
             l[i] = c + i < p.n ? lw : (_Float16)0;
         }
-        const int64_t at = b * x.stride + r * x.ld + c;
-        *reinterpret_cast<f16x8 *>(x.p + at) = h;
-        *reinterpret_cast<f16x8 *>(x.p + at + x.lo) = l;
+        _Float16 *to = x.at(b, r, c);
+        *reinterpret_cast<f16x8 *>(to) = h;
+        *reinterpret_cast<f16x8 *>(to + PAIR) = l;
     });
     // the rows behind the matrix, of both X
     for (int64_t r = p.m + part; r < rows; r += parts)
-        for (int64_t c = threadIdx.x * NORM_W; c < x.ld; c += NORM_THREADS * NORM_W) {
-            const int64_t at = b * x.stride + r * x.ld + c;
-            for (_Float16 *to : {x.p + at, x.p + at + x.lo, y.p + at, y.p + at + y.lo})
+        for (int64_t c = threadIdx.x * NORM_W; c < x.ld; c += NORM_THREADS * NORM_W)
+            for (_Float16 *to : {x.at(b, r, c), x.at(b, r, c) + PAIR, y.at(b, r, c), y.at(b, r, c) + PAIR})
                 *reinterpret_cast<f16x8 *>(to) = f16x8{};
-        }
 }
 
 // ------------------------------------------------------------ long sides: products
@@ -291,9 +298,9 @@ struct Addends {
     {
         th = tl = uh = ul = f16x8{};
         const auto load = [&](const Planes &x, f16x8 &h, f16x8 &l) {
-            const _Float16 *at = x.p + b * x.stride + (int64_t)m * x.ld + n;
+            const _Float16 *at = x.at(b, m, n);
             h = *reinterpret_cast<const f16x8 *>(at);
-            l = *reinterpret_cast<const f16x8 *>(at + x.lo);
+            l = *reinterpret_cast<const f16x8 *>(at + PAIR);
         };
         if (any && p.t.p)
             load(p.t, th, tl);
@@ -334,9 +341,9 @@ __device__ __forceinline__ void emit(const PairArgs &p, int64_t b, int m, int n,
         h[i] = hi;
         l[i] = lw;
     }
-    _Float16 *to = p.out.p + b * p.out.stride + (int64_t)m * p.out.ld + n;
+    _Float16 *to = p.out.at(b, m, n);
     *reinterpret_cast<f16x8 *>(to) = h;
-    *reinterpret_cast<f16x8 *>(to + p.out.lo) = l;
+    *reinterpret_cast<f16x8 *>(to + PAIR) = l;
 }
 
 // Columns of a row that are written: planes also get the zeros behind the row.
@@ -507,26 +514,50 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pair_join_kernel(PairArgs p)
     rows.template emit_all<O>(p, s, i, o, threadIdx.x);
 }
 
-// A step's tiles of one operand: the hi plane's, then the lo plane's.  Planes are
-// padded with zeros, rows and columns, to whole steps, so only the tile's own
-// edge is checked, once.
+// A step's tile of one operand, hi and lo: STEP bytes of k of each.  An inner
+// operand's rows of 128 bytes are PAIR values of k (a step of more has several
+// such tiles), an outer one's rows are the 2 ROWS values of one k, as they lie in
+// memory or (halves) hi before lo: a fragment's two addresses are then a constant
+// apart, without which two outer operands need more registers than two workgroups
+// a CU have (X^T X of 14336 x 4096: 601 us, with one workgroup 757).
+// Matrices are padded with zeros, rows and columns, to whole steps, so only the
+// tile's own edge is checked, once.
 template <bool OUTER, int ROWS, int THREADS, int STEP> struct PairCopy {
-    Direct<_Float16, OUTER, ROWS, THREADS, STEP> d;
-    int64_t lo;
+    static constexpr int PARTS = OUTER ? 1 : STEP / 2 / PAIR, BYTES = 2 * ROWS * STEP / PARTS;
+    typedef Direct<_Float16, OUTER, OUTER ? 2 * ROWS : ROWS, THREADS, OUTER ? STEP : 4 * PAIR> Copies;
+    Copies d;
 
     // r0: the tile's first row, of `rows`; first: its first step
-    __device__ __forceinline__ void init(const Planes &x, int64_t b, int r0, int rows, int first)
+    __device__ __forceinline__ void init(const Planes &x, int64_t b, int r0, int rows, int first, bool halves)
     {
-        d.init(x.p + b * x.stride, x.ld, r0, rows, 0);
-        d.base += first * d.advance;
-        lo = x.lo * 2;
+        d.init(x.p + b * x.stride, 2 * x.ld, OUTER ? 2 * r0 : r0, OUTER ? (int)(2 * x.ld) : rows, 0);
+        d.base += first * (PARTS * d.advance);
+        if (OUTER && halves)
+            d.halves(2 * x.ld, r0, PAIR);
     }
 
     __device__ __forceinline__ void start(char *tile)
     {
-        d.start_at(tile, 0, d.BK);
-        d.start_at(tile + ROWS * STEP, lo, d.BK);
-        d.base += d.advance;
+        if constexpr (OUTER) {
+            // rows that far apart have their chunks in the same order; past the last
+            // column the sum stays out of range
+            static_assert(2 * THREADS / Copies::CPR % 16 == 0 || Copies::CH <= 2, "two offsets are enough");
+            d.start_apart(tile, (uint32_t)(d.advance / Copies::BK) * (2 * THREADS / Copies::CPR));
+        } else {
+#pragma unroll
+            for (int q = 0; q < PARTS; q++)
+                d.start_at(tile + q * BYTES, q * d.advance, Copies::BK);
+        }
+        d.base += PARTS * d.advance;
+    }
+
+    // Fragment of the rows from r0 at the 32 values kk of the step's k; lo: 0 or 1
+    static __device__ __forceinline__ Frag read(const char *tile, int r0, int kk, int lo, int lane, bool halves)
+    {
+        if constexpr (OUTER)
+            return read_frag<_Float16, true, 2 * ROWS, STEP>(tile, halves ? lo * ROWS + r0 : r0 + r0 / PAIR * PAIR + lo * PAIR, kk, lane);
+        else
+            return read_frag<_Float16, false, ROWS, 4 * PAIR>(tile + kk * BYTES, r0, lo, lane);
     }
 };
 
@@ -549,7 +580,6 @@ __device__ __forceinline__ f32x4 mma_pair(const Frag &bh, const Frag &bl, const 
 template <typename O, bool AO, bool BO, bool SYM, bool DEEP>
 __global__ __launch_bounds__(512) void pair_kernel(PairArgs p)
 {
-    typedef _Float16 T;
     constexpr int BM = 64, WM = 2, WN = 2, GROUP_THREADS = WM * WN * WAVE, THREADS = 2 * GROUP_THREADS;
     constexpr int BK = STEP_BYTES / 2, F = 2;
     constexpr int AB = BM * STEP_BYTES; // one plane of one operand
@@ -571,8 +601,8 @@ __global__ __launch_bounds__(512) void pair_kernel(PairArgs p)
             acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     PairCopy<AO, BM, THREADS, STEP_BYTES> a;
     PairCopy<BO, BM, THREADS, STEP_BYTES> b;
-    a.init(p.a, sh.b, m0, p.M, sh.first);
-    b.init(p.b, sh.b, n0, p.N, sh.first);
+    a.init(p.a, sh.b, m0, p.M, sh.first, AO && BO);
+    b.init(p.b, sh.b, n0, p.N, sh.first, AO && BO);
     const auto copy = [&](char *l) {
         a.start(l);
         b.start(l + 2 * AB);
@@ -581,10 +611,10 @@ __global__ __launch_bounds__(512) void pair_kernel(PairArgs p)
         Frag ah[F], al[F], bh[F], bl[F];
 #pragma unroll
         for (int i = 0; i < F; i++) {
-            ah[i] = read_frag<T, AO, BM, STEP_BYTES>(l, wm + i * 16, group, lane);
-            al[i] = read_frag<T, AO, BM, STEP_BYTES>(l + AB, wm + i * 16, group, lane);
-            bh[i] = read_frag<T, BO, BM, STEP_BYTES>(l + 2 * AB, wn + i * 16, group, lane);
-            bl[i] = read_frag<T, BO, BM, STEP_BYTES>(l + 3 * AB, wn + i * 16, group, lane);
+            ah[i] = a.read(l, wm + i * 16, group, 0, lane, AO && BO);
+            al[i] = a.read(l, wm + i * 16, group, 1, lane, AO && BO);
+            bh[i] = b.read(l + 2 * AB, wn + i * 16, group, 0, lane, AO && BO);
+            bl[i] = b.read(l + 2 * AB, wn + i * 16, group, 1, lane, AO && BO);
         }
 #pragma unroll
         for (int i = 0; i < F; i++)
@@ -674,13 +704,12 @@ __global__ __launch_bounds__(512) void pair_kernel(PairArgs p)
 // its step is shorter than the way from memory: XX^T of 2048 x 2048, half of its
 // tiles, 44 us with four buffers and 51 with two, 52 with four wavefronts of
 // 64 x 64 instead of eight.  14336 x 4096 by 4096 x 4096 in 256 x 256 tiles takes
-// 1.2 ms, 1.2 PFLOP/s over the three products.
+// 1.06 ms, 1.36 PFLOP/s over the three products.
 constexpr int PAIR_SLOTS = 4;
 
 template <typename O, int BM, int BN, int WM, int WN, bool AO, bool BO, bool SYM, int BUFS>
-__global__ __launch_bounds__(WM *WN *WAVE) void pair_pipe_kernel(PairArgs p)
+__global__ __launch_bounds__(WM *WN *WAVE, BM * BN * BUFS <= 2 * 128 * 128 ? 4 : 2) void pair_pipe_kernel(PairArgs p)
 {
-    typedef _Float16 T;
     constexpr int THREADS = WM * WN * WAVE, BK = PIPE_STEP / 2, STEP = PIPE_STEP;
     constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
     constexpr int AB = BM * STEP, BB = BN * STEP; // one plane of each operand
@@ -697,8 +726,8 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pair_pipe_kernel(PairArgs p)
     const int wm = (wave / WN) * (BM / WM), wn = (wave % WN) * (BN / WN);
     PairCopy<AO, BM, THREADS, STEP> a;
     PairCopy<BO, BN, THREADS, STEP> b;
-    a.init(p.a, sh.b, m0, p.M, sh.first);
-    b.init(p.b, sh.b, n0, p.N, sh.first);
+    a.init(p.a, sh.b, m0, p.M, sh.first, AO && BO);
+    b.init(p.b, sh.b, n0, p.N, sh.first, AO && BO);
     f32x4 acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; i++)
@@ -711,14 +740,14 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pair_pipe_kernel(PairArgs p)
         b.start(l + 2 * AB);
     };
     const auto read_a = [&](const char *l, int i) {
-        ah[i % PAIR_SLOTS] = read_frag<T, AO, BM, STEP>(l, wm + i * 16, 0, lane);
-        al[i % PAIR_SLOTS] = read_frag<T, AO, BM, STEP>(l + AB, wm + i * 16, 0, lane);
+        ah[i % PAIR_SLOTS] = a.read(l, wm + i * 16, 0, 0, lane, AO && BO);
+        al[i % PAIR_SLOTS] = a.read(l, wm + i * 16, 0, 1, lane, AO && BO);
     };
     const auto read_b = [&](const char *l, int s) {
 #pragma unroll
         for (int j = 0; j < FN; j++) {
-            bh[s][j] = read_frag<T, BO, BN, STEP>(l + 2 * AB, wn + j * 16, 0, lane);
-            bl[s][j] = read_frag<T, BO, BN, STEP>(l + 2 * AB + BB, wn + j * 16, 0, lane);
+            bh[s][j] = b.read(l + 2 * AB, wn + j * 16, 0, 0, lane, AO && BO);
+            bl[s][j] = b.read(l + 2 * AB, wn + j * 16, 0, 1, lane, AO && BO);
         }
     };
     // step t; inner: steps t + 1 .. t + BUFS are there
@@ -1297,7 +1326,7 @@ struct PairPlan {
     size_t part_bytes() const { return splits > 1 ? (size_t)rest * splits * tile * tile * 4 : 0; }
 };
 
-PairPlan pair_plan(int64_t B, int64_t M, int64_t N, int64_t K, bool sym, int cus)
+PairPlan pair_plan(int64_t B, int64_t M, int64_t N, int64_t K, bool sym, bool outer, int cus)
 {
     // tile, bytes of k of a step, tiles at once on a CU, us of a step of a round
     // of them and of one workgroup a CU.  Measured, us of a product (which is
@@ -1313,6 +1342,9 @@ PairPlan pair_plan(int64_t B, int64_t M, int64_t N, int64_t K, bool sym, int cus
     PairPlan best{};
     double least = 0;
     for (const auto &k : kinds) {
+        // two outer operands' addresses do not fit into the registers beside 256 x 256 sums
+        if (outer && k.tile == 256)
+            continue;
         const int64_t count = B * pair_tiles(M, N, k.tile, sym), steps = ceil_div(2 * K, k.step), slots = (int64_t)cus * k.at_once;
         const int64_t whole = count / slots * slots, rest = count - whole;
         for (int s = 1; s <= 16 && (s == 1 || (rest > 0 && steps >= 4 * s)); s++) {
@@ -1346,8 +1378,8 @@ LongPlan long_plan(int64_t B, int64_t m, int64_t n, int cus)
     p.groups = 4 * l >= 5 * s;
     p.x = bytes(2 * B * p.plane_x * 2);
     p.g = bytes(2 * B * p.plane_s * 2);
-    const PairPlan gram = pair_plan(B, s, s, l, true, cus), square = pair_plan(B, s, s, s, true, cus),
-                   apply = pair_plan(B, m, n, s, false, cus);
+    const PairPlan gram = pair_plan(B, s, s, l, true, m > n, cus), square = pair_plan(B, s, s, s, true, false, cus),
+                   apply = pair_plan(B, m, n, s, false, false, cus);
     p.part = bytes((int64_t)std::max({gram.part_bytes(), square.part_bytes(), apply.part_bytes()}));
     return p;
 }
@@ -1362,7 +1394,7 @@ template <typename O, int BM, int WM, int WN, bool SYM> hipError_t join_pair(con
 template <typename O, bool AO, bool BO, bool SYM>
 hipError_t pair_product(PairArgs a, int64_t B, float *part, int cus, hipStream_t st)
 {
-    const PairPlan p = pair_plan(B, a.M, a.N, a.K, SYM, cus);
+    const PairPlan p = pair_plan(B, a.M, a.N, a.K, SYM, AO && BO, cus);
     a.tiles_m = (int)ceil_div(a.M, p.tile);
     a.tiles_n = (int)ceil_div(a.N, p.tile);
     a.tiles = (int)pair_tiles(a.M, a.N, p.tile, SYM);
@@ -1381,7 +1413,7 @@ hipError_t pair_product(PairArgs a, int64_t B, float *part, int cus, hipStream_t
         pair_pipe_kernel<O, 128, 128, 2, 4, AO, BO, SYM, 4><<<grid, 512, 0, st>>>(a);
     else if (p.tile == 128)
         pair_pipe_kernel<O, 128, 128, 2, 4, AO, BO, SYM, 2><<<grid, 512, 0, st>>>(a);
-    else
+    else if constexpr (!(AO && BO))
         pair_pipe_kernel<O, 256, 256, 2, 4, AO, BO, SYM, 2><<<grid, 512, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
@@ -1400,7 +1432,7 @@ template <typename T, typename O> hipError_t run_long(const OrthoArgs &o, int cu
     double *sums = reinterpret_cast<double *>(ws);
     ws += plan.sums;
     const auto planes = [&](size_t bytes, int64_t ld, int64_t plane) {
-        const Planes p{reinterpret_cast<_Float16 *>(ws), ld, plane, 2 * plane};
+        const Planes p{reinterpret_cast<_Float16 *>(ws), ld, 2 * plane};
         ws += bytes;
         return p;
     };

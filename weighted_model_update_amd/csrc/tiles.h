@@ -428,6 +428,19 @@ template <typename T, bool OUTER, int ROWS, int THREADS, int STEP> struct Direct
         }
     }
 
+    // For an outer operand whose rows hold two matrices' columns in turns of `turn`:
+    // the tile's rows get the first matrix's, then the second's.  r0: the first column.
+    __device__ __forceinline__ void halves(int64_t ld, int r0, int turn)
+    {
+#pragma unroll
+        for (int c = 0; c < CH; c++) {
+            const int q = threadIdx.x + c * THREADS, k = q / CPR;
+            const int at = ((q % CPR) ^ outer_swizzle<T, ROWS>(k)) * EPC, col = at % (ROWS / 2);
+            off[c] = 2 * (r0 + col) < ld ? (uint32_t)((k * ld + col + col / turn * turn + at / (ROWS / 2) * turn) * (int64_t)sizeof(T))
+                                         : OUT_OF_RANGE;
+        }
+    }
+
     // Starts the copies of one step; `left`: values of k from its first on.
     __device__ __forceinline__ void start(char *tile, int left)
     {
@@ -469,6 +482,20 @@ template <typename T, bool OUTER, int ROWS, int THREADS, int STEP> struct Direct
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 rsrc, (__attribute__((address_space(3))) void *)(tile + first * 16), 16, o, 0, 0, 0);
         }
+    }
+
+    // The same of a step that is all there, where chunks c and c + 2 of a thread lie
+    // `apart` bytes from each other; two offsets stay in registers.
+    __device__ __forceinline__ void start_apart(char *tile, uint32_t apart) const
+    {
+        static_assert(CHUNKS % THREADS == 0, "every thread copies as much");
+        const __amdgpu_buffer_rsrc_t rsrc =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(base), 0, (int)OUT_OF_RANGE, 0x00020000);
+#pragma unroll
+        for (int c = 0; c < CH; c++)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rsrc, (__attribute__((address_space(3))) void *)(tile + ((threadIdx.x / WAVE) * WAVE + c * THREADS) * 16), 16,
+                off[c & 1] + (c >> 1) * apart, 0, 0, 0);
     }
 };
 

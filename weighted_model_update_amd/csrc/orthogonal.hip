@@ -707,6 +707,7 @@ __global__ __launch_bounds__(512) void pair_kernel(PairArgs p)
 // 1.06 ms, 1.36 PFLOP/s over the three products.
 constexpr int PAIR_SLOTS = 4;
 
+// Tiles that share a CU have half of its registers each.
 template <typename O, int BM, int BN, int WM, int WN, bool AO, bool BO, bool SYM, int BUFS>
 __global__ __launch_bounds__(WM *WN *WAVE, BM * BN * BUFS <= 2 * 128 * 128 ? 4 : 2) void pair_pipe_kernel(PairArgs p)
 {

@@ -1065,20 +1065,22 @@ def _batch(t, name, shape, dtype, dev):
     return ld, lead[0] if lead else 0
 
 
-@functools.lru_cache(maxsize=64)
-def _coefficients(coef, steps):
-    rows = list(coef) if isinstance(coef[0], tuple) else [coef] * steps
-    if len(rows) != steps or any(len(r) != 3 for r in rows):
-        raise ValueError("coef must be three numbers, or three for each step")
-    flat = [float(v) for r in rows for v in r]
-    return (ctypes.c_double * len(flat))(*flat)
-
-
 def _coef_of(coef, steps):
+    """The coefficients' values as the call takes them.  They are read at every
+    call: coef may hold arrays or tensors, which change."""
     steps = int(steps)
     if not 1 <= steps <= FA_MAX_ORTHO_STEPS:
         raise ValueError(f"steps must be 1 to {FA_MAX_ORTHO_STEPS}, got {steps}")
-    return _coefficients(tuple(tuple(c) if isinstance(c, (list, tuple)) else c for c in coef), steps)
+    try:
+        rows = [[float(v) for v in coef]] * steps
+    except (TypeError, ValueError, RuntimeError):  # rows, or no numbers
+        try:
+            rows = [[float(v) for v in row] for row in coef]
+        except (TypeError, ValueError, RuntimeError):
+            rows = []
+    if len(rows) != steps or any(len(r) != 3 for r in rows):
+        raise ValueError("coef must be three numbers, or three for each step")
+    return (ctypes.c_double * (3 * steps))(*sum(rows, []))
 
 
 def _matrices(t, name):

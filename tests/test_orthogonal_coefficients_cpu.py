@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+from test_learn_cpu import RANGE
 from weighted_model_update_amd import fedavg
 
 
@@ -49,3 +50,37 @@ def test_forms(make):
 def test_shapes_that_are_refused(coef, steps):
     with pytest.raises(ValueError, match="three numbers"):
         fedavg._coef_of(coef, steps)
+
+
+# ------------------------------------------------------------------ what they let X grow to
+
+def accepted(coef, steps):
+    """The call's answer for no matrices: coefficients are checked all the same."""
+    return fedavg.load().orthogonalize(0, 0, 8, 16, None, 16, 128, fedavg._coef_of(coef, steps), steps, 1.0, None, 16, 128, None, 0,
+                                       None)
+
+
+OK, QUINTIC, CUBIC = 0, fedavg.ORTHO_COEF, (1.5, -0.5, 0.0)
+
+
+@pytest.mark.parametrize("coef", [QUINTIC, CUBIC, (1.0, 0.0, 0.0), (0.0, 0.0, 0.0), (0.5, 0.0, 0.0)], ids=str)
+def test_steps_that_stay_bounded_are_taken_in_any_number(coef):
+    """[0, 1.01] goes to [0, 1.2024] under the default and stays there."""
+    for steps in range(1, 33):
+        assert accepted(coef, steps) == OK
+
+
+# (3, -4, 2) takes [0, 0.5626] to 1.0882, from where the default returns; (4, -6, 3) to
+# 1.3530, from where it goes to 2.0446, 38.8 and the cubic to 2.9e4, 1.2e13
+STEEP = ((8.0, -23.0, 17.0), (0.25, 0.0, 0.0))
+
+
+@pytest.mark.parametrize("rows,code", [
+    (STEEP + ((3.0, -4.0, 2.0), QUINTIC, QUINTIC, CUBIC, CUBIC, CUBIC, CUBIC), OK),
+    (STEEP + ((4.0, -6.0, 3.0), QUINTIC, QUINTIC, CUBIC), OK),
+    (STEEP + ((4.0, -6.0, 3.0), QUINTIC, QUINTIC, CUBIC, CUBIC), RANGE),
+    # 1.01e9 and 0.909e9
+    (((1.0, 0.0, 0.0), (1e9, 0.0, 0.0)), RANGE), (((0.9, 0.0, 0.0), (1e9, 0.0, 0.0)), OK),
+], ids=["back", "before it grows", "grows", "at the end", "below"])
+def test_bounds_of_steps_in_turn(rows, code):
+    assert accepted(rows, len(rows)) == code

@@ -1235,61 +1235,84 @@ __global__ __launch_bounds__(256) void short_join_kernel(const double *part, int
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Singular values v of X over [0, top] as they go through the steps, and with
-// them bounds of the matrices that the steps form, with a margin for the grid and
-// for rounding.
+// What the steps can make of X, whose singular values v begin within 0 and 1 (and
+// a margin): v = 0 stays and the steps are continuous, so after each they fill
+// [0, top] with the largest |a v + b v^3 + c v^5| over the last such range, which is
+// found exactly.  No margin is added to it here: a step would enlarge that too,
+// and the next one what came of it (1.05 a step, with the default coefficients:
+// 1.2, 1.3, 1.8, 16, 2e6).
 struct Spectrum {
-    static constexpr int N = 1025;
-    double v[N], p[N]; // p: of the group's product P
-    double alpha;      // p at v = 0
+    double top;
+    double least, most, alpha; // the group's product P: its range, and at v = 0
 
-    void start(double top)
+    void start(double t)
     {
-        for (int i = 0; i < N; i++) {
-            v[i] = top * i / (N - 1);
-            p[i] = 1;
-        }
-        alpha = 1;
+        top = t;
+        group();
     }
+    void group() { least = most = alpha = 1; }
 
-    template <typename F> double largest(F f) const
+    // Takes f(w) at the ends of w = v^2 and where k0 + k1 w + k2 w^2 = 0, f's turns.
+    template <typename F, typename TAKE> void visit(double k0, double k1, double k2, F f, TAKE take) const
+    {
+        const double end = top * top, size = std::max({std::fabs(k0), std::fabs(k1), std::fabs(k2)});
+        take(f(0.0));
+        take(f(end));
+        if (!(size > 0))
+            return;
+        k0 /= size;
+        k1 /= size;
+        k2 /= size;
+        const double square = k1 * k1 - 4 * k0 * k2, sum = -0.5 * (k1 + std::copysign(std::sqrt(std::max(square, 0.0)), k1));
+        for (const double w : {sum / k2, k0 / sum})
+            if (square >= 0 && w > 0 && w < end)
+                take(f(w));
+    }
+    template <typename F> double largest(double k0, double k1, double k2, F f) const
     {
         double most = 0;
-        for (int i = 0; i < N; i++)
-            most = std::max(most, std::fabs(f(i)));
-        return 1.05 * most;
+        visit(k0, k1, k2, f, [&](double v) { most = std::max(most, std::fabs(v)); });
+        return most;
     }
 
-    static double inner(const double *c, double v) { return (c[1] + c[2] * v * v) * v * v; }
-    double top() const { return largest([&](int i) { return v[i]; }); }
-    double h(const double *c) const { return largest([&](int i) { return inner(c, v[i]); }); }
-    double t(const double *c) const { return largest([&](int i) { return (c[0] + inner(c, v[i])) * v[i] * v[i]; }); }
-    double k() const { return largest([&](int i) { return p[i] - alpha; }); }
+    double h(const double *c) const
+    {
+        return largest(c[1], 2 * c[2], 0, [&](double w) { return (c[1] + c[2] * w) * w; });
+    }
+    double t(const double *c) const
+    {
+        return largest(c[0], 2 * c[1], 3 * c[2], [&](double w) { return (c[0] + (c[1] + c[2] * w) * w) * w; });
+    }
+    double k() const { return std::max(std::fabs(most - alpha), std::fabs(least - alpha)); }
     double growth(const double *c) const
     {
-        const double q = largest([&](int i) { return c[0] + inner(c, v[i]); });
+        const double q = 1.05 * largest(c[1], 2 * c[2], 0, [&](double w) { return c[0] + (c[1] + c[2] * w) * w; });
         return std::max(1.0, q * q);
     }
 
     void step(const double *c)
     {
-        for (int i = 0; i < N; i++) {
-            const double q = c[0] + inner(c, v[i]);
-            v[i] = std::fabs(q * v[i]);
-            p[i] *= q;
-        }
+        double q0 = c[0], q1 = c[0];
+        visit(c[1], 2 * c[2], 0, [&](double w) { return c[0] + (c[1] + c[2] * w) * w; }, [&](double q) {
+            q0 = std::min(q0, q);
+            q1 = std::max(q1, q);
+        });
+        const auto ends = {least * q0, least * q1, most * q0, most * q1};
+        least = std::min(ends);
+        most = std::max(ends);
         alpha *= c[0];
+        top = largest(c[0], 3 * c[1], 5 * c[2], [&](double w) { return (c[0] + (c[1] + c[2] * w) * w) * std::sqrt(w); });
     }
 };
 
 constexpr double START_TOP = 1.01, GROWTH_MAX = 3e4;
 
-// Exponent of the power of two that brings values of up to `top` near 2^15,
-// below fp16's largest.
+// Exponent of the power of two that brings values of up to `top`, and 5% more for
+// rounding, near 2^15, below fp16's largest.
 int exponent_for(double top)
 {
     int e;
-    std::frexp(std::max(top, 1e-30), &e); // top < 2^e
+    std::frexp(std::max(1.05 * top, 1e-30), &e); // below 2^e
     return 15 - e;
 }
 
@@ -1469,16 +1492,16 @@ template <typename T, typename O> hipError_t run_long(const OrthoArgs &o, int cu
     };
     const bool grouped = plan.groups && sizeof(O) == 2;
     Spectrum z;
-    double top = START_TOP;
+    z.start(START_TOP);
     for (int k = 0; k < o.steps && e == hipSuccess;) {
-        z.start(top);
+        z.group();
         if (!h.p) // without groups, the last step's K has H's place
             std::swap(kp, h);
         PairArgs v{};
         v.a = v.b = x;
         v.M = v.N = (int)s;
         v.K = (int)l;
-        int eg = exponent_for(top * top), ek = 0;
+        int eg = exponent_for(z.top * z.top), ek = 0;
         v.q = (float)power(eg - 2 * ex);
         v.out = g;
         e = wide ? pair_product<float, false, false, true>(v, B, part, cus, st) : pair_product<float, true, true, true>(v, B, part, cus, st);
@@ -1494,7 +1517,7 @@ template <typename T, typename O> hipError_t run_long(const OrthoArgs &o, int cu
             e = square(g, g, c[2] * power(eh - 2 * eg), g, c[1] * power(eh - eg), {}, 0, h);
             if (more && e == hipSuccess) {
                 // T = Q G = a G + H G, then G = T Q = a T + T H
-                const int en = exponent_for(z.top() * z.top());
+                const int en = exponent_for(z.top * z.top);
                 e = square(h, g, power(et - eh - eg), g, c[0] * power(et - eg), {}, 0, t);
                 if (e == hipSuccess)
                     e = square(t, h, power(en - et - eh), t, c[0] * power(en - et), {}, 0, g);
@@ -1515,8 +1538,7 @@ template <typename T, typename O> hipError_t run_long(const OrthoArgs &o, int cu
             return e;
         // X = alpha X + K X, or alpha X + X K
         const bool last = k == o.steps;
-        top = z.top();
-        const int en = exponent_for(top);
+        const int en = exponent_for(z.top);
         v.o = o;
         v.a = wide ? kp : x;
         v.b = wide ? x : kp;
@@ -1632,7 +1654,7 @@ bool ortho_reach_ok(const double (*coef)[3], int steps)
         if (!std::isfinite(coef[k][0] + coef[k][1] + coef[k][2]) || !(z.h(coef[k]) < 1e9))
             return false;
         z.step(coef[k]);
-        if (!(z.top() < 1e9))
+        if (!(z.top < 1e9))
             return false;
     }
     return true;

@@ -658,7 +658,8 @@ int linear_int8_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const 
  * by rows.  Pointers need only the element's alignment.
  * coef       host array of 3 * steps values, 1 <= steps <= FA_MAX_ORTHO_STEPS.
  *            Coefficients under which singular values within 0 and 1 grow past
- *            1e9 are refused (FA_ERR_RANGE).
+ *            1e9 are refused (FA_ERR_RANGE); for s > 64 also those that, times the
+ *            scales that such values need, leave fp32.
  * Limits: B and the longer side at most 2^20, s at most 2^15, B*m*n at most 2^33
  * (FA_ERR_RANGE).  Precision: fp64 for s <= 64; beyond, that of fp32 products, on
  * pairs of fp16.  Each result is rounded once to its type.  Sums have an order

@@ -84,3 +84,26 @@ STEEP = ((8.0, -23.0, 17.0), (0.25, 0.0, 0.0))
 ], ids=["back", "before it grows", "grows", "at the end", "below"])
 def test_bounds_of_steps_in_turn(rows, code):
     assert accepted(rows, len(rows)) == code
+
+
+def coefficients_only(coef, steps, m, n, dtype):
+    return fedavg.load().orthogonalize(dtype, 0, m, n, None, n, m * n, fedavg._coef_of(coef, steps), steps, 1.0, None, n, m * n, None,
+                                       0, None)
+
+
+# X as small as 1e-26 and a coefficient that would bring its fifth power back: as
+# scales in fp32, 1e75 times 2^(111 - 2 * 114)
+FAR = ((1e-26, 0.0, 0.0), (1.0, 0.0, 1e75))
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("m,n", [(100, 110), (110, 100), (100, 900)])
+def test_scales_that_leave_fp32_are_refused_on_long_sides(m, n, dtype):
+    assert coefficients_only(FAR, 2, m, n, dtype) == RANGE
+    assert coefficients_only(((0.0, 0.0, 0.0), (1e300, 0.0, 0.0)), 2, m, n, dtype) == RANGE
+    assert coefficients_only(((1e-26, 0.0, 0.0), (1.0, 0.0, 1e70)), 2, m, n, dtype) == OK
+    # in fp64 they do not
+    assert coefficients_only(FAR, 2, 60, n, dtype) == OK
+    for steps in range(1, 33):
+        for coef in (QUINTIC, CUBIC, (1.0, 0.0, 0.0)):
+            assert coefficients_only(coef, steps, m, n, dtype) == OK

@@ -2101,9 +2101,12 @@ int run_ortho(fa::OrthoArgs &a, int update_dtype, int dtype, const double *coef,
     for (int k = 0; k < steps; k++)
         for (int i = 0; i < 3; i++)
             a.coef[k][i] = coef[3 * k + i];
-    if (!fa::ortho_reach_ok(a.coef, steps))
-        return fail(FA_ERR_RANGE, "the coefficients let singular values of up to 1 grow past 1e9");
     const int64_t B = x.B, m = x.m, n = x.n;
+    a.m = m;
+    a.n = n;
+    a.steps = steps;
+    if (!fa::ortho_reach_ok(a, dtype))
+        return fail(FA_ERR_RANGE, "the coefficients let singular values of up to 1 grow past 1e9, or leave what fp32 scales hold");
     if (B == 0 || m == 0 || n == 0)
         return ok();
     int rc;
@@ -2127,9 +2130,6 @@ int run_ortho(fa::OrthoArgs &a, int update_dtype, int dtype, const double *coef,
     a.ldm = momentum.ld;
     a.stride_m = momentum.stride;
     a.B = B;
-    a.m = m;
-    a.n = n;
-    a.steps = steps;
     a.out = const_cast<void *>(out.p);
     a.ldo = out.ld;
     a.stride_o = out.stride;

@@ -120,9 +120,9 @@ struct OrthoArgs {
     float keep, rate;
     void *ws;
 };
-// Whether the coefficients keep the singular values within what the scaled
-// halves hold.
-bool ortho_reach_ok(const double (*coef)[3], int steps);
+// Whether the steps keep the singular values below 1e9 and, on long sides, their
+// scales within fp32, by o.m, o.n, o.steps, o.coef and the result's type.
+bool ortho_reach_ok(const OrthoArgs &o, int dt);
 size_t ortho_workspace_bytes(int64_t B, int64_t m, int64_t n, int cus);
 hipError_t launch_ortho(const OrthoArgs &o, int update_dt, int dt, int cus, hipStream_t s);
 

@@ -28,6 +28,7 @@
 #include "tiles.h"
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 namespace fa {
@@ -1326,6 +1327,80 @@ int norm_across(int64_t n)
     return a;
 }
 
+// A step on long sides with its scales: X, G, H, K are held times powers of two
+// that bring their bounds near fp16's largest.
+struct LongStep {
+    bool first, more;     // of its group; whether the group goes on
+    float gram;           // first: G = gram (X X^T)
+    float hh, h;          // H = hh G^2 + h G
+    float tt, t, gg, g;   // more: T = tt H G + t G = Q G, then G = gg T H + g T = T Q
+    float kk, k, kh;      // not first: K = kk H K + k K + kh H, where P = alpha + K
+    float xx, x;          // not more: X = xx K X + x X
+};
+
+// The steps of a call and the exponent of the first X.  False where a scale or
+// a coefficient times it leaves fp32.
+bool long_steps(const double (*coef)[3], int steps, bool grouped, LongStep *out, int &start)
+{
+    Spectrum z;
+    z.start(START_TOP);
+    int ex = start = exponent_for(z.top), eg = 0, ek = 0;
+    double growth = 1;
+    bool first = true, ok = true;
+    const auto fp32 = [&](double v) {
+        ok = ok && std::fabs(v) <= (double)FLT_MAX;
+        return (float)v;
+    };
+    for (int i = 0; i < steps; i++) {
+        const double *c = coef[i];
+        LongStep &s = out[i] = {};
+        const bool last = i + 1 == steps;
+        if (first) {
+            z.group();
+            growth = 1;
+            eg = exponent_for(z.top * z.top);
+            s.gram = fp32(power(eg - 2 * ex));
+        }
+        growth *= z.growth(c);
+        s.first = first;
+        s.more = grouped && !last && growth <= GROWTH_MAX;
+        const int eh = exponent_for(z.h(c)), et = exponent_for(z.t(c));
+        const double alpha = z.alpha;
+        z.step(c);
+        // H = b G + c G^2
+        s.hh = fp32(c[2] * power(eh - 2 * eg));
+        s.h = fp32(c[1] * power(eh - eg));
+        if (s.more) {
+            // T = Q G = a G + H G, then G = T Q = a T + T H
+            const int en = exponent_for(z.top * z.top);
+            s.tt = fp32(power(et - eh - eg));
+            s.t = fp32(c[0] * power(et - eg));
+            s.gg = fp32(power(en - et - eh));
+            s.g = fp32(c[0] * power(en - et));
+            eg = en;
+        }
+        // P = alpha + K: Q P = a alpha + (alpha H + a K + H K)
+        if (first) {
+            ek = eh;
+        } else {
+            const int en = exponent_for(z.k());
+            s.kk = fp32(power(en - eh - ek));
+            s.k = fp32(c[0] * power(en - ek));
+            s.kh = fp32(alpha * power(en - eh));
+            ek = en;
+        }
+        if (!s.more) {
+            // X = alpha X + K X, or alpha X + X K; the last X is the result's
+            const int en = last ? 0 : exponent_for(z.top);
+            s.x = fp32(z.alpha * power(en - ex));
+            s.xx = fp32(power(en - ek - ex));
+            ex = en;
+        }
+        first = !s.more;
+    }
+    return ok;
+}
+
 struct LongPlan {
     int64_t pitch_x, pitch_s, plane_x, plane_s; // elements of a row, of one plane of one matrix
     int64_t rows_per; // rows of a part in the passes over t, none empty
@@ -1335,6 +1410,8 @@ struct LongPlan {
     int squares() const { return groups ? 5 : 2; } // s x s matrices: G, H; T, K and the next K
     size_t total() const { return sums + 2 * x + squares() * g + part; }
 };
+
+bool groups_pay(int64_t s, int64_t l) { return 4 * l >= 5 * s; }
 
 int64_t pair_tiles(int64_t M, int64_t N, int64_t t, bool sym)
 {
@@ -1399,7 +1476,7 @@ LongPlan long_plan(int64_t B, int64_t m, int64_t n, int cus)
     p.parts = (int)ceil_div(m, p.rows_per);
     const auto bytes = [](int64_t b) { return (size_t)round_up(b, 256); };
     p.sums = bytes(B * p.parts * 8);
-    p.groups = 4 * l >= 5 * s;
+    p.groups = groups_pay(s, l);
     p.x = bytes(2 * B * p.plane_x * 2);
     p.g = bytes(2 * B * p.plane_s * 2);
     const PairPlan gram = pair_plan(B, s, s, l, true, m > n, cus), square = pair_plan(B, s, s, s, true, false, cus),
@@ -1449,7 +1526,7 @@ hipError_t pair_product(PairArgs a, int64_t B, float *part, int cus, hipStream_t
 
 template <typename T, typename O> hipError_t run_long(const OrthoArgs &o, int cus, hipStream_t st)
 {
-    const int64_t m = o.m, n = o.n, s = std::min(m, n), l = std::max(m, n), B = o.B;
+    const int64_t m = o.m, n = o.n, s = std::min(m, n), B = o.B;
     const bool wide = m <= n;
     const LongPlan plan = long_plan(B, m, n, cus);
     char *ws = static_cast<char *>(o.ws);
@@ -1465,80 +1542,63 @@ template <typename T, typename O> hipError_t run_long(const OrthoArgs &o, int cu
         sq[i] = planes(plan.g, plan.pitch_s, plan.plane_s);
     Planes &g = sq[0], &h = sq[1], &t = sq[2], &kp = sq[3], &next = sq[4];
     float *part = reinterpret_cast<float *>(ws);
+    LongStep list[FA_MAX_ORTHO_STEPS];
+    int start;
+    if (!long_steps(o.coef, o.steps, plan.groups && sizeof(O) == 2, list, start))
+        return hipErrorInvalidValue;
     const int across = norm_across(n);
     const unsigned grid = (unsigned)(B * plan.parts);
-    int ex = exponent_for(START_TOP);
     norm_kernel<T><<<grid, NORM_THREADS, 0, st>>>(o, plan.parts, plan.rows_per, across, sums);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    split_kernel<T><<<grid, NORM_THREADS, 0, st>>>(o, plan.parts, plan.rows_per, across, sums, (float)power(ex), x, y, round_up(m, PAD));
+    split_kernel<T><<<grid, NORM_THREADS, 0, st>>>(o, plan.parts, plan.rows_per, across, sums, (float)power(start), x, y, round_up(m, PAD));
     e = hipGetLastError();
 
     // out = q A B + p T + r U of symmetric s x s matrices
-    const auto square = [&](const Planes &a, const Planes &b, double q, const Planes &t, double p, const Planes &u, double r,
+    const auto square = [&](const Planes &a, const Planes &b, float q, const Planes &t, float p, const Planes &u, float r,
                             const Planes &out) {
         PairArgs v{};
         v.a = a;
         v.b = b;
         v.M = v.N = v.K = (int)s;
-        v.q = (float)q;
+        v.q = q;
         v.t = t;
-        v.p = (float)p;
+        v.p = p;
         v.u = u;
-        v.r = (float)r;
+        v.r = r;
         v.out = out;
         return pair_product<float, false, false, true>(v, B, part, cus, st);
     };
-    const bool grouped = plan.groups && sizeof(O) == 2;
-    Spectrum z;
-    z.start(START_TOP);
-    for (int k = 0; k < o.steps && e == hipSuccess;) {
-        z.group();
-        if (!h.p) // without groups, the last step's K has H's place
-            std::swap(kp, h);
-        PairArgs v{};
-        v.a = v.b = x;
-        v.M = v.N = (int)s;
-        v.K = (int)l;
-        int eg = exponent_for(z.top * z.top), ek = 0;
-        v.q = (float)power(eg - 2 * ex);
-        v.out = g;
-        e = wide ? pair_product<float, false, false, true>(v, B, part, cus, st) : pair_product<float, true, true, true>(v, B, part, cus, st);
-        double growth = 1;
-        for (bool first = true, more = true; more && e == hipSuccess; first = false, k++) {
-            const double *c = o.coef[k];
-            growth *= z.growth(c);
-            more = grouped && k + 1 < o.steps && growth <= GROWTH_MAX;
-            const int eh = exponent_for(z.h(c)), et = exponent_for(z.t(c));
-            const double alpha = z.alpha;
-            z.step(c);
-            // H = b G + c G^2
-            e = square(g, g, c[2] * power(eh - 2 * eg), g, c[1] * power(eh - eg), {}, 0, h);
-            if (more && e == hipSuccess) {
-                // T = Q G = a G + H G, then G = T Q = a T + T H
-                const int en = exponent_for(z.top * z.top);
-                e = square(h, g, power(et - eh - eg), g, c[0] * power(et - eg), {}, 0, t);
-                if (e == hipSuccess)
-                    e = square(t, h, power(en - et - eh), t, c[0] * power(en - et), {}, 0, g);
-                eg = en;
-            }
-            // P = alpha + K: Q P = a alpha + (alpha H + a K + H K)
-            if (first) {
+    for (int i = 0; i < o.steps && e == hipSuccess; i++) {
+        const LongStep &l = list[i];
+        if (l.first) {
+            if (!h.p) // without groups, the last step's K has H's place
                 std::swap(kp, h);
-                ek = eh;
-            } else if (e == hipSuccess) {
-                const int en = exponent_for(z.k());
-                e = square(h, kp, power(en - eh - ek), kp, c[0] * power(en - ek), h, alpha * power(en - eh), next);
-                std::swap(kp, next);
-                ek = en;
-            }
+            PairArgs v{};
+            v.a = v.b = x;
+            v.M = v.N = (int)s;
+            v.K = (int)std::max(m, n);
+            v.q = l.gram;
+            v.out = g;
+            e = wide ? pair_product<float, false, false, true>(v, B, part, cus, st) : pair_product<float, true, true, true>(v, B, part, cus, st);
         }
-        if (e != hipSuccess)
-            return e;
-        // X = alpha X + K X, or alpha X + X K
-        const bool last = k == o.steps;
-        const int en = exponent_for(z.top);
+        if (e == hipSuccess)
+            e = square(g, g, l.hh, g, l.h, {}, 0, h);
+        if (l.more && e == hipSuccess) {
+            e = square(h, g, l.tt, g, l.t, {}, 0, t);
+            if (e == hipSuccess)
+                e = square(t, h, l.gg, t, l.g, {}, 0, g);
+        }
+        if (l.first) {
+            std::swap(kp, h);
+        } else if (e == hipSuccess) {
+            e = square(h, kp, l.kk, kp, l.k, h, l.kh, next);
+            std::swap(kp, next);
+        }
+        if (l.more || e != hipSuccess)
+            continue;
+        PairArgs v{};
         v.o = o;
         v.a = wide ? kp : x;
         v.b = wide ? x : kp;
@@ -1546,12 +1606,11 @@ template <typename T, typename O> hipError_t run_long(const OrthoArgs &o, int cu
         v.M = (int)m;
         v.N = (int)n;
         v.K = (int)s;
-        v.p = (float)(z.alpha * power(last ? -ex : en - ex));
-        v.q = (float)power(last ? -ek - ex : en - ek - ex);
-        v.out = last ? Planes{} : y;
+        v.p = l.x;
+        v.q = l.xx;
+        v.out = i + 1 == o.steps ? Planes{} : y;
         e = wide ? pair_product<O, false, true, false>(v, B, part, cus, st) : pair_product<O, false, false, false>(v, B, part, cus, st);
         std::swap(x, y);
-        ex = en;
     }
     return e;
 }
@@ -1646,18 +1705,22 @@ template <typename T, typename O> hipError_t run(const OrthoArgs &o, int cus, hi
 
 } // namespace
 
-bool ortho_reach_ok(const double (*coef)[3], int steps)
+bool ortho_reach_ok(const OrthoArgs &o, int dt)
 {
     Spectrum z;
     z.start(START_TOP);
-    for (int k = 0; k < steps; k++) {
-        if (!std::isfinite(coef[k][0] + coef[k][1] + coef[k][2]) || !(z.h(coef[k]) < 1e9))
+    for (int k = 0; k < o.steps; k++) {
+        const double *c = o.coef[k];
+        if (!std::isfinite(c[0] + c[1] + c[2]) || !(z.h(c) < 1e9))
             return false;
-        z.step(coef[k]);
+        z.step(c);
         if (!(z.top < 1e9))
             return false;
     }
-    return true;
+    const int64_t s = std::min(o.m, o.n);
+    LongStep list[FA_MAX_ORTHO_STEPS];
+    int start;
+    return s <= SHORT_MAX || long_steps(o.coef, o.steps, groups_pay(s, std::max(o.m, o.n)) && dt == FA_BF16, list, start);
 }
 
 size_t ortho_workspace_bytes(int64_t B, int64_t m, int64_t n, int cus)

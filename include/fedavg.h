@@ -678,6 +678,9 @@ int linear_int8_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const 
  */
 #define FA_MAX_ORTHO_STEPS 32
 
+/* Device workspace bytes for these sizes with any steps, on the current device.  (With
+   s <= 64 a call whose steps need one Gram matrix alone, up to 6 of the default
+   coefficients, takes less and looks for no more.) */
 int orthogonalize_workspace_size(int64_t B, int64_t m, int64_t n, size_t *bytes);
 int orthogonalize(fa_dtype dtype, int64_t B, int64_t m, int64_t n, const void *x, int64_t ldx,
                   int64_t stride_x, const double *coef, int steps, float scale, void *out, int64_t ldo,

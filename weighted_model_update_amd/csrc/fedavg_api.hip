@@ -2102,6 +2102,7 @@ int run_ortho(fa::OrthoArgs &a, int update_dtype, int dtype, const double *coef,
         for (int i = 0; i < 3; i++)
             a.coef[k][i] = coef[3 * k + i];
     const int64_t B = x.B, m = x.m, n = x.n;
+    a.B = B;
     a.m = m;
     a.n = n;
     a.steps = steps;
@@ -2121,7 +2122,7 @@ int run_ortho(fa::OrthoArgs &a, int update_dtype, int dtype, const double *coef,
     for (const BatchView *v : {&x, &momentum, &out})
         if (views_overlap(v->view(), vs))
             return fail(FA_ERR_ARG, "the workspace must not overlap anything else");
-    if ((rc = check_workspace(workspace, workspace_bytes, fa::ortho_workspace_bytes(B, m, n, cu_count()))) != FA_OK)
+    if ((rc = check_workspace(workspace, workspace_bytes, fa::ortho_workspace_needed(a, cu_count()))) != FA_OK)
         return rc;
     a.x = x.p;
     a.ldx = x.ld;
@@ -2129,7 +2130,6 @@ int run_ortho(fa::OrthoArgs &a, int update_dtype, int dtype, const double *coef,
     a.momentum = const_cast<float *>(static_cast<const float *>(momentum.p));
     a.ldm = momentum.ld;
     a.stride_m = momentum.stride;
-    a.B = B;
     a.out = const_cast<void *>(out.p);
     a.ldo = out.ld;
     a.stride_o = out.stride;

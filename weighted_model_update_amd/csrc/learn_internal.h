@@ -114,6 +114,7 @@ struct OrthoArgs {
     int64_t B, m, n;
     int steps;
     double coef[FA_MAX_ORTHO_STEPS][3];
+    bool unit; // x is divided by its norm already
     void *out;
     int64_t ldo, stride_o;
     int add;
@@ -123,7 +124,9 @@ struct OrthoArgs {
 // Whether the steps keep the singular values below 1e9 and, on long sides, their
 // scales within fp32, by o.m, o.n, o.steps, o.coef and the result's type.
 bool ortho_reach_ok(const OrthoArgs &o, int dt);
+// For any steps, and for those of a call.
 size_t ortho_workspace_bytes(int64_t B, int64_t m, int64_t n, int cus);
+size_t ortho_workspace_needed(const OrthoArgs &o, int cus);
 hipError_t launch_ortho(const OrthoArgs &o, int update_dt, int dt, int cus, hipStream_t s);
 
 // ---------------------------------------------------------------- logits

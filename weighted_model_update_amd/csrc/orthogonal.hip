@@ -7,7 +7,8 @@
 //
 // Two forms.  For s <= 64 the whole sequence is one polynomial P of the first
 // Gram matrix, times X: the Gram matrix and P are formed in fp64 (the powers
-// of G square its condition), and X is read twice.  Longer sides take matrix
+// of G square its condition), and X is read twice.  More steps than a Gram matrix
+// carries in fp64 go in groups, with X in fp64 between them.  Longer sides take matrix
 // products of 16-bit floats: a value is held as hi + lo, two fp16 scaled by a
 // power of two (22 bits or more), and a product is hi hi + hi lo + lo hi with fp32
 // sums, as exact as one in fp32 at a third of the 16-bit rate (835 against 157
@@ -79,6 +80,48 @@ __device__ __forceinline__ void put_result(const OrthoArgs &p, int64_t b, int64_
     for (int i = 0; i < W; i++)
         z[i] = p.add ? __builtin_fmaf(p.rate, v[i], p.keep * old[i]) : p.rate * v[i];
     store_n<O, W>(o, valid, z);
+}
+
+// What short sides compute on: fp32 values, or the X of fp64 between two groups of
+// steps, which is neither scaled nor added to anything.
+template <typename T> struct value {
+    typedef float type;
+};
+template <> struct value<double> {
+    typedef double type;
+};
+
+template <typename T, int W>
+__device__ __forceinline__ void values_at(const OrthoArgs &p, int64_t b, int64_t r, int64_t c, bool update, int valid,
+                                          typename value<T>::type *t)
+{
+    if constexpr (__is_same(T, double)) {
+        const double *x = update_at<double>(p, b, r, c);
+        if (valid >= W) {
+            __builtin_memcpy(t, x, W * sizeof(double));
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; i++)
+                t[i] = i < valid ? x[i] : 0.0;
+        }
+    } else {
+        argument<T, W>(p, update_at<T>(p, b, r, c), momentum_at(p, b, r, c), update, valid, t);
+    }
+}
+
+template <typename O, int W>
+__device__ __forceinline__ void put_values(const OrthoArgs &p, int64_t b, int64_t r, int64_t c, int valid,
+                                           const typename value<O>::type *v)
+{
+    if constexpr (__is_same(O, double)) {
+        double *o = static_cast<double *>(p.out) + b * p.stride_o + r * p.ldo + c;
+#pragma unroll
+        for (int i = 0; i < W; i++)
+            if (i < valid)
+                o[i] = v[i];
+    } else {
+        put_result<O, W>(p, b, r, c, valid, v);
+    }
 }
 
 // Matrix and part of a workgroup.
@@ -871,19 +914,20 @@ __device__ __forceinline__ double symmetric_at(const Block *m, int r, int i, int
 
 // Four values of short row i at k .. k + 3 of the long side, 0 where there are none.
 template <typename T, bool WIDE>
-__device__ __forceinline__ void short_values(const OrthoArgs &p, int64_t b, int i, int64_t k, int64_t s, int64_t l, float *t)
+__device__ __forceinline__ void short_values(const OrthoArgs &p, int64_t b, int i, int64_t k, int64_t s, int64_t l,
+                                             typename value<T>::type *t)
 {
     const int valid = (int)(i >= s || k >= l ? 0 : l - k < 4 ? l - k : 4);
     if constexpr (WIDE) {
-        argument<T, 4>(p, update_at<T>(p, b, i, k), momentum_at(p, b, i, k), true, valid, t);
+        values_at<T, 4>(p, b, i, k, true, valid, t);
     } else {
 #pragma unroll
         for (int j = 0; j < 4; j++)
-            argument<T, 1>(p, update_at<T>(p, b, k + j, i), momentum_at(p, b, k + j, i), true, j < valid, t + j);
+            values_at<T, 1>(p, b, k + j, i, true, j < valid, t + j);
     }
 #pragma unroll
     for (int j = 0; j < 4; j++)
-        t[j] = j < valid ? t[j] : 0.f;
+        t[j] = j < valid ? t[j] : 0;
 }
 
 // G of the columns (rows) [k0, k1) of the long side into `to`, with `scratch` of
@@ -900,7 +944,7 @@ __device__ __forceinline__ void short_gram(const OrthoArgs &p, int64_t b, int64_
         acc[e] = f64x4{0, 0, 0, 0};
     // 16 of the long side a wavefront, U such pieces on their way
     for (int64_t k = k0 + wave * 16; k < k1; k += SHORT_WAVES * 16 * U) {
-        float t[U][SB][4];
+        typename value<T>::type t[U][SB][4];
 #pragma unroll
         for (int u = 0; u < U; u++)
 #pragma unroll
@@ -987,7 +1031,7 @@ __device__ __forceinline__ int short_poly(const OrthoArgs &p, Block (*m)[blocks_
         for (int d = 1; d < WAVE; d *= 2)
             t += __shfl_xor(t, d);
         if (threadIdx.x == 0)
-            *norm = inverse_norm(t);
+            *norm = p.unit ? 1.0 : inverse_norm(t);
     }
     __syncthreads();
     const double f = *norm;
@@ -1057,16 +1101,16 @@ __device__ __forceinline__ void short_apply(const OrthoArgs &p, int64_t b, int64
             // t[r][j][q]: short index 16 r + 4 g + j at long index at + q
             const int64_t at = k0 + piece * SHORT_STEP + 4 * i;
             const int valid = (int)(!mine || at >= k1 ? 0 : k1 - at < 4 ? k1 - at : 4);
-            float t[SB][4][4];
+            typename value<T>::type t[SB][4][4];
 #pragma unroll
             for (int r = 0; r < SB; r++)
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     const int row = r * 16 + g * 4 + j, n = row < s ? valid : 0;
-                    argument<T, 4>(p, update_at<T>(p, b, row, at), momentum_at(p, b, row, at), false, n, t[r][j]);
+                    values_at<T, 4>(p, b, row, at, false, n, t[r][j]);
 #pragma unroll
                     for (int q = 0; q < 4; q++)
-                        t[r][j][q] = q < n ? t[r][j][q] : 0.f;
+                        t[r][j][q] = q < n ? t[r][j][q] : 0;
                 }
             if (shared)
                 __syncthreads();
@@ -1088,10 +1132,11 @@ __device__ __forceinline__ void short_apply(const OrthoArgs &p, int64_t b, int64
                     }
 #pragma unroll
                 for (int z = 0; z < 4; z++) {
-                    const float v[4] = {(float)acc[0][z], (float)acc[1][z], (float)acc[2][z], (float)acc[3][z]};
+                    typedef typename value<O>::type V;
+                    const V v[4] = {(V)acc[0][z], (V)acc[1][z], (V)acc[2][z], (V)acc[3][z]};
                     const int row = c * 16 + g + 4 * z;
                     if (row < s)
-                        put_result<O, 4>(p, b, row, at, valid, v);
+                        put_values<O, 4>(p, b, row, at, valid, v);
                 }
             }
         }
@@ -1103,17 +1148,17 @@ __device__ __forceinline__ void short_apply(const OrthoArgs &p, int64_t b, int64
             for (int u0 = 0; u0 < 4; u0 += U) {
                 if (k + u0 * SHORT_WAVES * 16 >= k1)
                     break;
-                float t[U][SB][4];
+                typename value<T>::type t[U][SB][4];
 #pragma unroll
                 for (int u = 0; u < U; u++)
 #pragma unroll
                     for (int r = 0; r < SB; r++) {
                         const int64_t at = k + (u0 + u) * SHORT_WAVES * 16 + i, first = r * 16 + g * 4;
                         const int n = (int)(at >= k1 || first >= s ? 0 : s - first < 4 ? s - first : 4);
-                        argument<T, 4>(p, update_at<T>(p, b, at, first), momentum_at(p, b, at, first), false, n, t[u][r]);
+                        values_at<T, 4>(p, b, at, first, false, n, t[u][r]);
 #pragma unroll
                         for (int j = 0; j < 4; j++)
-                            t[u][r][j] = j < n ? t[u][r][j] : 0.f;
+                            t[u][r][j] = j < n ? t[u][r][j] : 0;
                     }
                 // lane i gives short indices SB i .. SB i + SB - 1
                 const int col = SB * i, valid = (int)(col >= s ? 0 : s - col < SB ? s - col : SB);
@@ -1138,13 +1183,13 @@ __device__ __forceinline__ void short_apply(const OrthoArgs &p, int64_t b, int64
                 for (int u = 0; u < U; u++)
 #pragma unroll
                     for (int z = 0; z < 4; z++) {
-                        float v[SB];
+                        typename value<O>::type v[SB];
 #pragma unroll
                         for (int c = 0; c < SB; c++)
-                            v[c] = (float)acc[u][c][z];
+                            v[c] = (typename value<O>::type)acc[u][c][z];
                         const int64_t row = k + (u0 + u) * SHORT_WAVES * 16 + g + 4 * z;
                         if (row < k1 && valid > 0)
-                            put_result<O, SB>(p, b, row, col, valid, v);
+                            put_values<O, SB>(p, b, row, col, valid, v);
                     }
             }
         }
@@ -1214,6 +1259,20 @@ __global__ __launch_bounds__(short_threads<STAGES>()) void short_kernel(OrthoArg
     }
     if constexpr (APPLY)
         short_apply<T, O, SB, WIDE>(p, b, k0, k1, m[P]);
+}
+
+// t in fp64 into p.out, of calls whose steps go in groups; the momentum is stepped.
+template <typename T> __global__ __launch_bounds__(256) void short_lift_kernel(OrthoArgs p)
+{
+    const int64_t wide = (p.n + 3) / 4, all = p.B * p.m * wide;
+    for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < all; at += (int64_t)gridDim.x * 256) {
+        const int64_t b = at / wide / p.m, r = at / wide % p.m, c = at % wide * 4;
+        const int valid = (int)(p.n - c < 4 ? p.n - c : 4);
+        float t[4];
+        values_at<T, 4>(p, b, r, c, true, valid, t);
+        const double v[4] = {t[0], t[1], t[2], t[3]};
+        put_values<double, 4>(p, b, r, c, valid, v);
+    }
 }
 
 // Sums of up to JOIN_PARTS of G's parts, for calls with many.
@@ -1622,7 +1681,8 @@ struct ShortPlan {
     size_t total() const { return part + joined + poly; }
 };
 
-ShortPlan short_plan(int64_t B, int64_t m, int64_t n, int cus)
+// `apart`: each stage in a launch of its own.
+ShortPlan short_plan(int64_t B, int64_t m, int64_t n, int cus, bool apart = false)
 {
     const int64_t s = std::min(m, n), l = std::max(m, n);
     ShortPlan p{};
@@ -1634,16 +1694,138 @@ ShortPlan short_plan(int64_t B, int64_t m, int64_t n, int cus)
     p.parts = (int)ceil_div(l, p.per);
     p.sums = p.parts;
     const int64_t matrix = blocks_of(p.sb) * 256 * 8;
-    if (p.parts > 1 || p.sb > 2) {
+    if (p.parts > 1 || p.sb > 2 || apart) {
         p.part = (size_t)(B * p.parts * matrix);
         if (p.parts > JOIN_PARTS) {
             p.sums = (int)ceil_div(p.parts, JOIN_PARTS);
             p.joined = (size_t)(B * p.sums * matrix);
         }
-        if (p.sb > 2)
+        if (p.sb > 2 || apart)
             p.poly = (size_t)(B * blocks_of(p.sb)) * sizeof(Block);
     }
     return p;
+}
+
+// Rounding of G, s 2^-53, grows by a step's largest Q^2 until G is formed anew: in
+// directions that X does not have, too, where it ends as eigenvalues of either sign
+// on which the steps have no hold (rank 4 of 16 x 400, the default coefficients: an
+// error of 2e-13 after 5 steps, 5e-7 after 16, 2e7 after 18).  A group ends when that
+// growth has passed SHORT_GROWTH_MAX: 64 2^-53 4e5 = 3e-9.
+constexpr double SHORT_GROWTH_MAX = 4e5;
+
+// Steps of the group that begins with step k.
+int short_group(const OrthoArgs &o, int k)
+{
+    Spectrum z;
+    z.start(START_TOP);
+    for (int i = 0; i < k; i++)
+        z.step(o.coef[i]);
+    double growth = 1;
+    int end = k;
+    do {
+        growth *= z.growth(o.coef[end]);
+        z.step(o.coef[end++]);
+    } while (end < o.steps && growth <= SHORT_GROWTH_MAX);
+    return end - k;
+}
+
+// Calls of several groups hold the X of as many matrices as have SHORT_HELD elements
+// (at least one) in fp64, and take their batch in such passes.
+constexpr int64_t SHORT_HELD = 1ll << 22;
+
+struct ShortGroups {
+    int64_t matrices;
+    ShortPlan p;
+    size_t total() const { return p.total() + x; }
+    size_t x;
+};
+
+ShortGroups short_groups(int64_t B, int64_t m, int64_t n, int cus)
+{
+    ShortGroups g{};
+    g.matrices = std::min(B, std::max<int64_t>(1, SHORT_HELD / (m * n)));
+    g.p = short_plan(g.matrices, m, n, cus, true);
+    g.x = (size_t)(g.matrices * m * n) * sizeof(double);
+    return g;
+}
+
+template <typename O, int SB, bool WIDE> hipError_t run_short_groups(const OrthoArgs &o, int update_dt, int cus, hipStream_t st)
+{
+    const ShortGroups plan = short_groups(o.B, o.m, o.n, cus);
+    const ShortPlan &p = plan.p;
+    char *ws = static_cast<char *>(o.ws);
+    double *part = reinterpret_cast<double *>(ws), *joined = reinterpret_cast<double *>(ws + p.part);
+    Block *poly = reinterpret_cast<Block *>(ws + p.part + p.joined);
+    double *x = reinterpret_cast<double *>(ws + p.total());
+    const size_t es = update_dt == FA_BF16 ? 2 : 4;
+    hipError_t e = hipSuccess;
+    for (int64_t b = 0; b < o.B && e == hipSuccess; b += plan.matrices) {
+        OrthoArgs t = o;
+        t.B = std::min(plan.matrices, o.B - b);
+        t.x = static_cast<const char *>(o.x) + b * o.stride_x * es;
+        t.momentum = o.momentum ? o.momentum + b * o.stride_m : nullptr;
+        t.out = x;
+        t.ldo = o.n;
+        t.stride_o = o.m * o.n;
+        const int64_t pieces = t.B * t.m * ceil_div(t.n, 4);
+        const unsigned lift = (unsigned)std::min<int64_t>(ceil_div(pieces, 256), 1 << 16), grid = (unsigned)(t.B * p.parts);
+        if (update_dt == FA_BF16)
+            short_lift_kernel<__bf16><<<lift, 256, 0, st>>>(t);
+        else
+            short_lift_kernel<float><<<lift, 256, 0, st>>>(t);
+        e = hipGetLastError();
+        for (int k = 0, steps; k < o.steps && e == hipSuccess; k += steps) {
+            steps = short_group(o, k);
+            OrthoArgs g = t;
+            g.x = x;
+            g.ldx = o.n;
+            g.stride_x = o.m * o.n;
+            g.momentum = nullptr;
+            g.unit = k > 0;
+            g.steps = steps;
+            std::copy(o.coef[k], o.coef[k] + 3 * steps, g.coef[0]);
+            short_kernel<double, float, SB, WIDE, STAGE_GRAM><<<grid, SHORT_THREADS, 0, st>>>(g, p.parts, p.per, p.sums, part, poly);
+            e = hipGetLastError();
+            const double *sums = part;
+            if (e == hipSuccess && p.sums < p.parts) {
+                short_join_kernel<<<(unsigned)(t.B * p.sums * blocks_of(SB)), 256, 0, st>>>(part, p.parts, p.sums, blocks_of(SB), joined);
+                e = hipGetLastError();
+                sums = joined;
+            }
+            if (e == hipSuccess) {
+                short_kernel<float, float, SB, true, STAGE_POLY>
+                    <<<(unsigned)t.B, short_threads<STAGE_POLY>(), 0, st>>>(g, p.parts, p.per, p.sums, const_cast<double *>(sums), poly);
+                e = hipGetLastError();
+            }
+            if (e != hipSuccess)
+                break;
+            if (k + steps < o.steps) {
+                short_kernel<double, double, SB, WIDE, STAGE_APPLY><<<grid, SHORT_THREADS, 0, st>>>(g, p.parts, p.per, p.sums, part, poly);
+            } else {
+                g.out = static_cast<char *>(o.out) + b * o.stride_o * sizeof(O);
+                g.ldo = o.ldo;
+                g.stride_o = o.stride_o;
+                short_kernel<double, O, SB, WIDE, STAGE_APPLY><<<grid, SHORT_THREADS, 0, st>>>(g, p.parts, p.per, p.sums, part, poly);
+            }
+            e = hipGetLastError();
+        }
+    }
+    return e;
+}
+
+template <typename O> hipError_t run_short_passes(const OrthoArgs &o, int update_dt, int cus, hipStream_t st)
+{
+    const bool wide = o.m <= o.n;
+    switch (ceil_div(std::min(o.m, o.n), 16)) {
+    case 1:
+        return wide ? run_short_groups<O, 1, true>(o, update_dt, cus, st) : run_short_groups<O, 1, false>(o, update_dt, cus, st);
+    case 2:
+        return wide ? run_short_groups<O, 2, true>(o, update_dt, cus, st) : run_short_groups<O, 2, false>(o, update_dt, cus, st);
+    case 3:
+        return wide ? run_short_groups<O, 3, true>(o, update_dt, cus, st) : run_short_groups<O, 3, false>(o, update_dt, cus, st);
+    default:
+        return wide ? run_short_groups<O, 4, true>(o, update_dt, cus, st) : run_short_groups<O, 4, false>(o, update_dt, cus, st);
+    }
 }
 
 template <typename T, typename O, int SB, bool WIDE> hipError_t run_short_form(const OrthoArgs &o, const ShortPlan &p, hipStream_t st)
@@ -1730,12 +1912,21 @@ size_t ortho_workspace_bytes(int64_t B, int64_t m, int64_t n, int cus)
     // A call that takes one launch needs none; it asks for some all the same, so that a
     // missing workspace shows at every size.
     if (std::min(m, n) <= SHORT_MAX)
-        return std::max<size_t>(256, short_plan(B, m, n, cus).total());
+        return std::max({(size_t)256, short_plan(B, m, n, cus).total(), short_groups(B, m, n, cus).total()});
     return long_plan(B, m, n, cus).total();
+}
+
+size_t ortho_workspace_needed(const OrthoArgs &o, int cus)
+{
+    if (o.B > 0 && o.m > 0 && o.n > 0 && std::min(o.m, o.n) <= SHORT_MAX && short_group(o, 0) == o.steps)
+        return std::max<size_t>(256, short_plan(o.B, o.m, o.n, cus).total());
+    return ortho_workspace_bytes(o.B, o.m, o.n, cus);
 }
 
 hipError_t launch_ortho(const OrthoArgs &o, int update_dt, int dt, int cus, hipStream_t s)
 {
+    if (std::min(o.m, o.n) <= SHORT_MAX && short_group(o, 0) < o.steps)
+        return dt == FA_BF16 ? run_short_passes<__bf16>(o, update_dt, cus, s) : run_short_passes<float>(o, update_dt, cus, s);
     if (update_dt == FA_BF16)
         return dt == FA_BF16 ? run<__bf16, __bf16>(o, cus, s) : run<__bf16, float>(o, cus, s);
     return dt == FA_BF16 ? run<float, __bf16>(o, cus, s) : run<float, float>(o, cus, s);

@@ -2052,6 +2052,7 @@ struct BatchView {
     int64_t across() const { return (B - 1) * stride + n; } // ... from a row's first to the last matrix's same row
     bool whole() const { return B == 1 || stride >= matrix(); } // one matrix after another
     bool rowwise() const { return m == 1 || ld >= across(); }   // one row of all matrices after another
+    // Whole matrices, or rows of all of them.
     View view() const
     {
         if (whole())
@@ -2060,7 +2061,24 @@ struct BatchView {
             return {p, p ? m : 0, across(), ld, es};
         return {p, p ? 1 : 0, (B - 1) * stride + matrix(), 0, es};
     }
+    // Single rows of one pitch, where matrices start a whole number of rows apart, or
+    // rows a whole number of matrices; there may be others between them.
+    View rows() const
+    {
+        const int64_t any = p ? 1 : 0;
+        if (m > 1 && ld >= n && (B == 1 || stride % ld == 0))
+            return {p, any * ((B == 1 ? 0 : (B - 1) * (stride / ld)) + m), n, ld, es};
+        if (B > 1 && stride >= n && (m == 1 || ld % stride == 0))
+            return {p, any * ((m == 1 ? 0 : (m - 1) * (ld / stride)) + B), n, stride, es};
+        return view();
+    }
 };
+
+// Columns of one buffer's rows are apart as rows, rows of its matrices as matrices.
+bool batches_overlap(const BatchView &a, const BatchView &b)
+{
+    return views_overlap(a.rows(), b.rows()) && views_overlap(a.view(), b.view());
+}
 
 int check_batch(const char *name, const BatchView &v, bool out)
 {
@@ -2116,8 +2134,7 @@ int run_ortho(fa::OrthoArgs &a, int update_dtype, int dtype, const double *coef,
         return rc;
     const View vs{workspace, workspace ? 1 : 0, (int64_t)workspace_bytes, 0, 1};
     const bool in_place = !a.add && update_dtype == dtype && same_batch(x, out);
-    if ((!in_place && views_overlap(x.view(), out.view())) || views_overlap(x.view(), momentum.view()) ||
-        views_overlap(out.view(), momentum.view()))
+    if ((!in_place && batches_overlap(x, out)) || batches_overlap(x, momentum) || batches_overlap(out, momentum))
         return fail(FA_ERR_ARG, "the update, the momentum and the result must not overlap");
     for (const BatchView *v : {&x, &momentum, &out})
         if (views_overlap(v->view(), vs))

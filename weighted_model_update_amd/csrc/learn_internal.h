@@ -45,9 +45,9 @@ struct ActGradArgs {
     float *part;
     int64_t M, N;
     int act;
-    const float *col_scale; // N factors of the stored dz, nullable; not of db
-    // fp32 alone, 0: dz in fp32.  Else dz = a + 2^-8 b + 2^-16 c as three bf16
-    // matrices, `plane` elements apart.
+    // N factors of the stored dz, not of db; nullable.  With them there is a dz, and
+    // fp32's is dz = a + 2^-8 b + 2^-16 c as three bf16 matrices, `plane` elements apart.
+    const float *col_scale;
     int64_t plane;
 };
 int64_t act_grad_partials(int64_t M, int64_t N, int cus);

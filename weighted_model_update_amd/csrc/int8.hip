@@ -694,10 +694,9 @@ hipError_t run_tile8(const GemmArgs &a, bool direct, int splits, void *ws, hipSt
     const int used = (steps + per - 1) / per;
     float *part = used > 1 ? static_cast<float *>(ws) : nullptr;
     const dim3 grid((unsigned)(tm * tn), (unsigned)used), block(WM * WN * WAVE);
-    if (direct)
-        gemm8_kernel<O, BM, BN, WM, WN, true><<<grid, block, 0, s>>>(a, (int)tm, (int)tn, per * STEP_BYTES, part);
-    else
-        gemm8_kernel<O, BM, BN, WM, WN, false><<<grid, block, 0, s>>>(a, (int)tm, (int)tn, per * STEP_BYTES, part);
+    constexpr bool SMALL = BM * BN < 128 * 128; // larger tiles of aligned operands are pipe8_kernel's
+    const auto kernel = SMALL && direct ? gemm8_kernel<O, BM, BN, WM, WN, SMALL> : gemm8_kernel<O, BM, BN, WM, WN, false>;
+    kernel<<<grid, block, 0, s>>>(a, (int)tm, (int)tn, per * STEP_BYTES, part);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && used > 1) {
         const int64_t threads = (int64_t)a.M * ((a.N + J8_W - 1) / J8_W);

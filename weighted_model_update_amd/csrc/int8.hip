@@ -291,9 +291,9 @@ template <typename O> __global__ __launch_bounds__(J8_THREADS) void join8_kernel
 // workgroups a CU); the first 2 FEW_AHEAD fragments of the weights are on their way
 // before the workgroup looks at x, which it brings to 8 bits itself (X: its type;
 // int8_t: as it is), FEW_PIECES pieces of 4096 in all.  One token of bf16 through
-// 14336 x 4096 weights (59 MB): 15.4 us, as 16 x 128 tiles after a launch for x, with
-// the join of two splits, 18.6; with 8 fragments on their way, or loads past the
-// caches, 18.4.
+// 14336 x 4096 weights (59 MB): 12.7 us.  With x after the weights it was 15.4, and
+// then as 16 x 128 tiles after a launch for x, with the join of two splits, 18.6; with
+// 8 fragments on their way, or loads past the caches, 18.4.
 constexpr int FEW_M = 4, FEW_WAVES = 4, FEW_THREADS = FEW_WAVES * WAVE, FEW_AHEAD = 4, FEW_PER_CU = 4, FEW_PIECES = 4;
 
 __device__ __forceinline__ int64_t few_pitch(int64_t K) { return (K + WAVE - 1) / WAVE * WAVE; }
@@ -660,9 +660,16 @@ struct Plan8 {
     int tile, splits;
 };
 
+// Larger tiles are compared by the rounds that they need on all CUs, as for bf16: one
+// of 256x256, 256x128 or 128x256 fits a CU at a time, two of 128x128.  Measured on
+// 256 CUs, us of a round for K = 16384; the last is a round of 128x128 with one tile
+// a CU.  For example, in that order: 8192x14336x4096 436, 545, 543, 589;
+// 4096x2048x16384 172, 132, 133, 161; 2048x2048x16384 158, 103, 97, 77;
+// 6144x4096x16384, two rounds of 256x256 of which the second is half, 370, 387, 386,
+// 461.
 int pipe8_for(int64_t M, int64_t N, int cus)
 {
-    static const int us[5] = {222, 140, 138, 155, 90};
+    static const int us[5] = {215, 131, 132, 161, 77};
     const auto rounds = [&](int64_t t) { return (t + cus - 1) / cus; };
     const int64_t t128 = tiles8(M, N, 128, 128), whole = t128 / (2 * cus), rest = t128 % (2 * cus);
     const int64_t costs[4] = {us[0] * rounds(tiles8(M, N, 256, 256)), us[1] * rounds(tiles8(M, N, 256, 128)),
@@ -671,6 +678,17 @@ int pipe8_for(int64_t M, int64_t N, int cus)
     return (int)(std::min_element(costs, costs + 4) - costs);
 }
 
+// Products that 64x64 tiles would cover with more than two a CU take larger ones: us of
+// 128x128 and 64x64, operands in turn: 1024x2048x4096 (512 tiles) 32, 21; 1152x2048
+// 31.6, 33.7; 1920x2048 33, 38; 777x2048x8192 54, 36; 300x8192x4096 32, 37.  Staged
+// through registers, larger tiles pay later: 300x8192x1001 20, 14; 400x8192 21, 17;
+// 500x12288 27, 31; 400x14336x2047 35, 42.  Fewer 64x64 tiles than CUs are split
+// along k up to the CUs, in four steps or more: 256x1024x4096 in 1, 2, 4, 8 15, 12.5,
+// 11.2, 13.5; 100x128x4096 in 4, 8, 16 8.6, 7.7, 8.0; 64x4096x14336 in 2, 4, 8 33, 22,
+// 21; 333x555x2048 in 1, 4 9.5, 10.3.  Thin tiles, which stream one operand, up to
+// three workgroups for two CUs: 16x4096x4096 (32 tiles) in 4, 8, 12, 16 9.6, 9.9, 11.4,
+// 11.8; 16x8192x8192 in 2, 4, 6 21, 17, 19; 8x14336x4096 in 1, 2, 4 17.1, 15.2, 16.4;
+// staged 16x8192x4095 in 4, 6, 8 20, 16, 17.
 Plan8 plan8(int64_t M, int64_t N, int64_t K, int cus)
 {
     const int64_t steps = K / STEP_BYTES;
@@ -681,7 +699,7 @@ Plan8 plan8(int64_t M, int64_t N, int64_t K, int cus)
         return {T8_THIN_N, split(std::max<int64_t>(1, tiles8(M, N, 128, 16)), 3 * cus / 2)};
     if (M <= 16)
         return {T8_THIN_M, split(std::max<int64_t>(1, tiles8(M, N, 16, 128)), 3 * cus / 2)};
-    if (tiles8(M, N, 128, 128) >= cus)
+    if (tiles8(M, N, 64, 64) > 2 * cus)
         return {pipe8_for(M, N, cus), 1};
     return {T8_64, split(std::max<int64_t>(1, tiles8(M, N, 64, 64)), cus)};
 }
@@ -813,8 +831,10 @@ template <typename O> hipError_t gemm8_of(GemmArgs a, void *ws, int cus, hipStre
     if (few8_ok(a.M, a.K, a.b, a.ldb))
         return run_few<O, int8_t>(a, cus, s);
     if (p.tile <= P8_128_128) {
-        if (!direct)
+        if (!direct && tiles8(a.M, a.N, 128, 128) > cus)
             return run_tile8<O, 128, 128, 2, 2>(a, false, 1, ws, s);
+        if (!direct)
+            return run_tile8<O, 64, 64, 2, 2>(a, false, 1, ws, s);
         if (p.tile == P8_256_256)
             return run_pipe8<O, 256, 256, 2, 4>(a, s);
         if (p.tile == P8_256_128)

@@ -8,7 +8,7 @@ import torch
 
 import learn_ref as ref
 import weighted_model_update_amd as fa
-from test_gpu_orthogonal import CUBIC, QUINTIC, check, formula, off, rnd
+from test_gpu_orthogonal import CUBIC, QUINTIC, check, formula, off, rnd, update
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +95,45 @@ def test_steps_with_other_coefficients_on_long_sides():
     for shape in ((100, 110), (110, 100), (130, 1000)):
         x = rnd(shape, torch.float32, 24)
         check(x, fa.orthogonalize(x, steps=len(rows), coef=rows), coef=rows, steps=len(rows))
+
+
+# ------------------------------------------------------------------ groups of steps
+
+def carried_in_groups(x, rows):
+    """A bound of the error of steps on one Gram matrix, relative to the result's norm.
+    With l an eigenvalue of G and q = a + b l + c l^2, a step takes l to l q^2 and P to
+    q P, and errors e of l and p of P to |q^2 + 2 l q q'| e and |q| p + |P q'| e.
+    Every product adds 2^-22 of its largest value (two roundings to 24 bits and the
+    low halves' product, 2^-24 each): two for G, one each for H, P and the product with
+    X.  A group ends when the largest q^2, with a margin of 5%, have passed 3e4."""
+    unit = 2.0 ** -22
+    errors, values = 0.0, 0.0
+    for t in (x if x.dim() == 3 else x[None]).double().cpu():
+        v = torch.linalg.svdvals(t / t.norm())
+        dv, top, growth = torch.zeros_like(v), 1.01, 0.0
+        for i, (a, b, c) in enumerate(rows):
+            if growth == 0.0:
+                l, P, growth = v * v, torch.ones_like(v), 1.0
+                e, p = torch.full_like(v, unit * float(l.max())), torch.zeros_like(v)
+            grid = torch.linspace(0, top ** 2, 2001, dtype=torch.float64)
+            q, slope, most = a + (b + c * l) * l, b + 2 * c * l, a + (b + c * grid) * grid
+            growth *= max(1.0, float((1.05 * most).abs().max()) ** 2)
+            top = float((most * grid.sqrt()).abs().max())
+            p = q.abs() * p + P.abs() * (slope.abs() * e + unit * float(((b + c * grid) * grid).abs().max())) + unit * float((q * P).abs().max())
+            P, e, l = q * P, (q * q + 2 * l * q * slope).abs() * e + 2 * unit * top ** 2, l * q * q
+            if growth > 3e4 or i + 1 == len(rows):
+                v, dv, growth = (P * v).abs(), P.abs() * dv + p * v + unit * top, 0.0
+        errors, values = errors + float(dv.square().sum()), values + float(v.square().sum())
+    return math.sqrt(errors / values)
+
+
+@pytest.mark.parametrize("shape", [(70, 300), (300, 70), (2, 200, 900), (520, 2100)], ids=str)
+@pytest.mark.parametrize("rows", [(QUINTIC,) * 5, (QUINTIC,) * 2, (QUINTIC,) * 10, (CUBIC,) * 20, ((5.0, -9.0, 5.0),) + (CUBIC,) * 4,
+                                  ((100.0, 0.0, 0.0),) * 3], ids=["quintic", "two", "ten", "cubic", "steep", "linear"])
+def test_groups_of_steps_beside_the_rounding(shape, rows):
+    """bf16 rounds to the nearest, so a value d off is rounded to within |want rounded -
+    want| + d of itself: the result is off by that and 2 d."""
+    x = update(shape, torch.bfloat16, 6)
+    want = formula(x, rows, len(rows), torch.float64)
+    got = fa.orthogonalize(x, steps=len(rows), coef=rows)
+    assert off(got, want) <= off(want.bfloat16(), want) + 2 * carried_in_groups(x, rows)

@@ -91,11 +91,11 @@ def test_in_place_views_and_momentum(shape, steps):
 
 
 def test_batches_of_more_than_a_pass_holds():
-    x = rnd((23, 64, 4096), torch.float32, 38)
-    x[7], x[11, 3, 3] = 0, float("inf")
+    x = rnd((75, 64, 4096), torch.float32, 38)
+    x[7], x[40, 3, 3] = 0, float("inf")
     out = fa.orthogonalize(x, steps=12)
-    assert bool((out[7] == 0).all()) and bool(out[11].isnan().all())
-    for b in (0, 10, 12, 22):
+    assert bool((out[7] == 0).all()) and bool(out[40].isnan().all())
+    for b in (0, 31, 32, 64, 74):
         check(x[b], out[b], steps=12)
     y = x.clone()
     assert torch.equal(fa.orthogonalize(y, steps=12, out=y).view(torch.int32), out.view(torch.int32))

@@ -1731,7 +1731,7 @@ int short_group(const OrthoArgs &o, int k)
 
 // Calls of several groups hold the X of as many matrices as have SHORT_HELD elements
 // (at least one) in fp64, and take their batch in such passes.
-constexpr int64_t SHORT_HELD = 1ll << 22;
+constexpr int64_t SHORT_HELD = 1ll << 23;
 
 struct ShortGroups {
     int64_t matrices;

@@ -137,3 +137,26 @@ def test_groups_of_steps_beside_the_rounding(shape, rows):
     want = formula(x, rows, len(rows), torch.float64)
     got = fa.orthogonalize(x, steps=len(rows), coef=rows)
     assert off(got, want) <= off(want.bfloat16(), want) + 2 * carried_in_groups(x, rows)
+
+
+def left_over(x, steps):
+    """What a call with bf16 results is off by, relative to the norm, without the
+    rounding of the result: a step whose weights are the rounded result's negative
+    leaves the difference, to eight bits of it."""
+    want = formula(x, QUINTIC, steps, torch.float64)
+    near = want.bfloat16()
+    w = -near
+    fa.orthogonal_step(w, x, rate=1.0, steps=steps)
+    return float((w.double() + near.double() - want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("rank", [1, 2, 3, 5])
+@pytest.mark.parametrize("shape", [(100, 300), (300, 1000), (600, 1000), (1000, 300), (1000, 1300)], ids=str)
+def test_groups_of_steps_on_low_rank(shape, rank):
+    """Rounding in directions that the matrix does not have grows by 3.4 a step, as
+    that of fp32 products does, in a group and outside one: 2^-24 3.4^5 = 3e-5 for each
+    of the four roundings of a product (two factors, the low halves' product, the sum)
+    and of the up to four products a step, if all are alike; equal rows round alike."""
+    for seed in (1, 2, 3):
+        x = low_rank(shape, rank, seed).bfloat16()
+        assert left_over(x, 5) <= 16 * 2.0 ** -24 * QUINTIC[0] ** 5

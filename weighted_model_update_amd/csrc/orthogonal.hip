@@ -13,19 +13,19 @@
 // power of two (22 bits or more), and a product is hi hi + hi lo + lo hi with fp32
 // sums, as exact as one in fp32 at a third of the 16-bit rate (835 against 157
 // TFLOP/s at the peak).  a X is added to the finished sum: taken into H's
-// diagonal it would pass through every rounding of the sum (relative error 8e-6
-// instead of 2.8e-6 after 5 steps of a 512 x 512 matrix of rank 64 and noise,
-// where fp32 products give 2.5e-6).
+// diagonal it would pass through every rounding of the sum, for three times the
+// error.  After 5 steps of a 512 x 512 matrix of rank 64 and noise the relative error is
+// 1.0e-6, where fp32 products give 2.1e-6; of 2048 x 2048 1.7e-6 and 2.8e-6.
 //
 // Steps may run on the Gram matrix alone, as for short sides: with Q = a + H
 //     G <- Q G Q,   P <- Q P,   and X <- P X at the end of the group,
 // all symmetric, so half the products.  Five steps of 14336 x 4096 take 17 products of
 // s x s and two with X instead of 5 and 10: 2.1 times fewer operations.
 // Errors of G grow by up to a^2 a step instead of being left behind with the old
-// G: over five steps to 7e-6 .. 3e-5 of the result, against 2e-6 with a new Gram
-// matrix each step.  So results in bf16, which round to 2^-9, take groups (until
-// the growth passes GROWTH_MAX) where the matrix is long enough to gain; fp32
-// results take a Gram matrix each step.
+// G: over five steps to 6e-6 of the result (noise) .. 7e-4 (2048 x 8192 of rank 1),
+// against 1e-6 .. 1e-4 with a new Gram matrix each step.  So results in bf16, whose
+// rounding is 1.7e-3 of the norm, take groups (until the growth passes GROWTH_MAX)
+// where the matrix is long enough to gain; fp32 results take a Gram matrix each step.
 #include "tiles.h"
 
 #include <algorithm>
@@ -399,12 +399,16 @@ struct Share {
     unsigned tm, tn;
     int first, steps; // of k
     float *part;      // where a split's sums go
-    bool mirror;      // the other side of a symmetric product is written too
+    // Of a symmetric product the lower side is written to the upper one too, also
+    // within the tiles of the diagonal: what the rounding of H G differs by from
+    // that of G H would grow with G (600 x 1000 of rank 2 in whole numbers, 5 steps
+    // on one Gram matrix: an error of 4e-3 of the result, so 2e-4).
+    bool mirror, diagonal;
 };
 
 template <bool SYM, int BM, int BN> __device__ __forceinline__ Share share_of(const PairArgs &p, int all)
 {
-    Share s{0, 0, 0, 0, all, nullptr, false};
+    Share s{0, 0, 0, 0, all, nullptr, false, false};
     unsigned id;
     if (blockIdx.x < p.whole) {
         id = xcd_order(blockIdx.x, p.whole);
@@ -420,13 +424,14 @@ template <bool SYM, int BM, int BN> __device__ __forceinline__ Share share_of(co
     }
     s.b = id / (unsigned)p.tiles;
     pair_tile<SYM>(id % (unsigned)p.tiles, p.tiles_m, p.tiles_n, s.tm, s.tn);
-    s.mirror = SYM && s.tm != s.tn;
+    s.mirror = SYM;
+    s.diagonal = SYM && s.tm == s.tn;
     return s;
 }
 
 // Rows i of the wavefronts' fragments, which lie in LDS at `o`, 16 of each row
-// of wavefronts: whole rows are read and written.  A symmetric product's other
-// side is the finished values, read along the columns.
+// of wavefronts: whole rows are read and written.  A symmetric product's upper
+// side is the finished values of the lower, read along the columns.
 template <int BM, int BN, int WM, int WN> struct Rows {
     static constexpr int THREADS = WM * WN * WAVE, ROWS = WM * 16, CHUNKS = ROWS * BN / EMIT, PER = CHUNKS / THREADS;
     static_assert(CHUNKS % THREADS == 0, "every thread writes as much");
@@ -461,7 +466,7 @@ template <int BM, int BN, int WM, int WN> struct Rows {
             for (int g = 0; g < EMIT; g += 4)
                 __builtin_memcpy(v + g, o + write_tile_at<BN>(r, c + g), 16);
             add[e].finish(p, v);
-            if (m < p.M && n < cols)
+            if (m < p.M && n < cols && !(s.diagonal && n + EMIT > m))
                 emit<O>(p, s.b, m, n, v);
             if (s.mirror && p.t.p)
 #pragma unroll
@@ -476,11 +481,15 @@ template <int BM, int BN, int WM, int WN> struct Rows {
             for (int e = 0; e < PER; e++) {
                 const int at = thread + e * THREADS, c = at / (ROWS / EMIT), r = at % (ROWS / EMIT) * EMIT;
                 const int n = n0 + c, m = row(s, i, r);
-                if (n < p.N && m < cols) {
+                if (n < p.N && m < cols && !(s.diagonal && m + EMIT <= n)) {
+                    // on the diagonal the row's own values up to it, which lie among these rows
+                    const int own = s.diagonal ? n - m : 0;
                     float v[EMIT];
 #pragma unroll
-                    for (int g = 0; g < EMIT; g++)
-                        v[g] = q * o[write_tile_at<BN>(r + g, c & ~3) + (c & 3)];
+                    for (int g = 0; g < EMIT; g++) {
+                        const int k = g < own ? own : g, j = g < own ? c - own + g : c;
+                        v[g] = q * o[write_tile_at<BN>(r + k, j & ~3) + (j & 3)];
+                    }
                     emit<O>(p, s.b, n, m, v);
                 }
             }
@@ -535,10 +544,11 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pair_join_kernel(PairArgs p)
     __shared__ __attribute__((aligned(16))) float o[WM * 16 * BN];
     const unsigned tile = blockIdx.x / FM;
     const int i = blockIdx.x % FM;
-    Share s{0, 0, 0, 0, 0, nullptr, false};
+    Share s{0, 0, 0, 0, 0, nullptr, false, false};
     s.b = (p.whole + tile) / (unsigned)p.tiles;
     pair_tile<SYM>((p.whole + tile) % (unsigned)p.tiles, p.tiles_m, p.tiles_n, s.tm, s.tn);
-    s.mirror = SYM && s.tm != s.tn;
+    s.mirror = SYM;
+    s.diagonal = SYM && s.tm == s.tn;
     const f32x4 *from = reinterpret_cast<const f32x4 *>(p.part + (int64_t)tile * p.splits * (BM * BN)) + i * FN * THREADS + threadIdx.x;
     Rows<BM, BN, WM, WN> rows;
     rows.fetch(p, s, i, threadIdx.x);

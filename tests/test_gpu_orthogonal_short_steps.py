@@ -6,7 +6,7 @@ import torch
 
 import learn_ref as ref
 import weighted_model_update_amd as fa
-from test_gpu_orthogonal import DTYPES, QUINTIC, check, formula, rnd
+from test_gpu_orthogonal import DTYPES, QUINTIC, check, formula, off, rnd
 from test_gpu_orthogonal_steps import low_rank
 
 pytestmark = pytest.mark.gpu
@@ -131,3 +131,32 @@ def test_groups_end_alike_for_every_number_of_steps():
         x = rnd(shape, torch.float32, 50)
         for steps in range(1, 33):
             check(x, fa.orthogonalize(x, steps=steps), steps=steps)
+
+
+@pytest.mark.parametrize("steps", [5, 6, 7, 8])
+@pytest.mark.parametrize("shape", [(48, 200), (200, 48), (64, 1000), (33, 90), (16, 400)], ids=str)
+def test_one_gram_matrix_of_low_rank(shape, steps):
+    """Up to 8 steps on one Gram matrix: the result's rounding, and, as for
+    test_short_sides_of_low_rank, 10 s 2^-53 3.4^steps here and in the formula."""
+    for rank in (2, 3, 8):
+        x = low_rank(shape, rank, 51)
+        want = formula(x, QUINTIC, steps, torch.float64)
+        out = fa.orthogonalize(x, steps=steps)
+        assert off(out, want) <= 2.0 ** -24 + 2 * 10 * min(shape) * 2.0 ** -53 * QUINTIC[0] ** steps
+
+
+def test_singular_values_of_every_size():
+    """From 1 to 1e-9 of the largest.  At the end of a group G's rounding has grown to at
+    most 2^-53 1e8 times the steps' five products; X takes it with |b| of 4.8: 3e-7 in the
+    one direction of s that has grown as much by then, the result's rounding beside it."""
+    for shape in ((16, 400), (64, 1000), (300, 33)):
+        m, n = shape
+        g = torch.Generator().manual_seed(52)
+        k = min(shape)
+        u, _ = torch.linalg.qr(torch.randn(m, k, generator=g, dtype=torch.float64))
+        v, _ = torch.linalg.qr(torch.randn(n, k, generator=g, dtype=torch.float64))
+        x = ((u * torch.logspace(0, -9, k, dtype=torch.float64)) @ v.t()).float().cuda()
+        for steps in (5, 8, 9, 12):
+            want = formula(x, QUINTIC, steps, torch.float64)
+            out = fa.orthogonalize(x, steps=steps)
+            assert off(out, want) <= 2.0 ** -24 + 3e-7 / k ** 0.5

@@ -301,6 +301,7 @@ struct PairArgs {
     float p, q, r;
     Planes t, u;
     Planes out; // out.p null: the result goes to o.out
+    bool even;  // of a symmetric product: the diagonal's tiles are symmetric too
     OrthoArgs o;
 };
 
@@ -399,10 +400,11 @@ struct Share {
     unsigned tm, tn;
     int first, steps; // of k
     float *part;      // where a split's sums go
-    // Of a symmetric product the lower side is written to the upper one too, also
-    // within the tiles of the diagonal: what the rounding of H G differs by from
-    // that of G H would grow with G (600 x 1000 of rank 2 in whole numbers, 5 steps
-    // on one Gram matrix: an error of 4e-3 of the result, so 2e-4).
+    // Of a symmetric product the lower side is written to the upper one too, where G is
+    // carried through several steps also within the tiles of the diagonal: what it
+    // differed by from its transpose, as the rounding of T Q does from that of Q T, would
+    // grow with it (600 x 1000 of rank 2 in whole numbers, 5 steps: an error of 4e-3 of
+    // the result, so 2e-4; T, H and K need not).
     bool mirror, diagonal;
 };
 
@@ -424,8 +426,8 @@ template <bool SYM, int BM, int BN> __device__ __forceinline__ Share share_of(co
     }
     s.b = id / (unsigned)p.tiles;
     pair_tile<SYM>(id % (unsigned)p.tiles, p.tiles_m, p.tiles_n, s.tm, s.tn);
-    s.mirror = SYM;
-    s.diagonal = SYM && s.tm == s.tn;
+    s.diagonal = SYM && s.tm == s.tn && p.even;
+    s.mirror = SYM && (s.tm != s.tn || p.even);
     return s;
 }
 
@@ -482,14 +484,16 @@ template <int BM, int BN, int WM, int WN> struct Rows {
                 const int at = thread + e * THREADS, c = at / (ROWS / EMIT), r = at % (ROWS / EMIT) * EMIT;
                 const int n = n0 + c, m = row(s, i, r);
                 if (n < p.N && m < cols && !(s.diagonal && m + EMIT <= n)) {
-                    // on the diagonal the row's own values up to it, which lie among these rows
-                    const int own = s.diagonal ? n - m : 0;
                     float v[EMIT];
 #pragma unroll
-                    for (int g = 0; g < EMIT; g++) {
-                        const int k = g < own ? own : g, j = g < own ? c - own + g : c;
-                        v[g] = q * o[write_tile_at<BN>(r + k, j & ~3) + (j & 3)];
-                    }
+                    for (int g = 0; g < EMIT; g++)
+                        v[g] = q * o[write_tile_at<BN>(r + g, c & ~3) + (c & 3)];
+                    // on the diagonal the row's own values up to it, which lie among these rows
+                    if (s.diagonal && n > m)
+#pragma unroll
+                        for (int g = 0; g < EMIT; g++)
+                            if (g < n - m)
+                                v[g] = q * o[write_tile_at<BN>(r + n - m, (c - n + m + g) & ~3) + ((c - n + m + g) & 3)];
                     emit<O>(p, s.b, n, m, v);
                 }
             }
@@ -547,8 +551,8 @@ __global__ __launch_bounds__(WM *WN *WAVE) void pair_join_kernel(PairArgs p)
     Share s{0, 0, 0, 0, 0, nullptr, false, false};
     s.b = (p.whole + tile) / (unsigned)p.tiles;
     pair_tile<SYM>((p.whole + tile) % (unsigned)p.tiles, p.tiles_m, p.tiles_n, s.tm, s.tn);
-    s.mirror = SYM;
-    s.diagonal = SYM && s.tm == s.tn;
+    s.diagonal = SYM && s.tm == s.tn && p.even;
+    s.mirror = SYM && (s.tm != s.tn || p.even);
     const f32x4 *from = reinterpret_cast<const f32x4 *>(p.part + (int64_t)tile * p.splits * (BM * BN)) + i * FN * THREADS + threadIdx.x;
     Rows<BM, BN, WM, WN> rows;
     rows.fetch(p, s, i, threadIdx.x);
@@ -1083,7 +1087,18 @@ __device__ __forceinline__ int short_poly(const OrthoArgs &p, Block (*m)[blocks_
         __syncthreads();
         for (int e = wave; e < NB; e += WAVES) {
             const f64x4 v = block_product<SB>(m[T], m[Q], e, s);
-            put(m[G], e, [&](int z) { return v[z]; });
+            int r, c;
+            block_at(e, r, c);
+            // The diagonal's blocks get their lower side twice: what G differed by from its
+            // transpose would grow with it (64 x 1000 of rank 3, 8 steps: an error of 1e-6,
+            // so 2e-11; the others need not).  What is left out goes to the padding, without
+            // a branch of single lanes.
+#pragma unroll
+            for (int z = 0; z < 4; z++) {
+                const int row = g + 4 * z;
+                m[G][e][row][r == c && row < i ? 16 : i] = v[z];
+                m[G][e][r == c ? i : row][r == c && row > i ? row : 16] = v[z];
+            }
         }
     }
     __syncthreads();
@@ -1626,8 +1641,9 @@ template <typename T, typename O> hipError_t run_long(const OrthoArgs &o, int cu
 
     // out = q A B + p T + r U of symmetric s x s matrices
     const auto square = [&](const Planes &a, const Planes &b, float q, const Planes &t, float p, const Planes &u, float r,
-                            const Planes &out) {
+                            const Planes &out, bool even = false) {
         PairArgs v{};
+        v.even = even;
         v.a = a;
         v.b = b;
         v.M = v.N = v.K = (int)s;
@@ -1650,6 +1666,7 @@ template <typename T, typename O> hipError_t run_long(const OrthoArgs &o, int cu
             v.K = (int)std::max(m, n);
             v.q = l.gram;
             v.out = g;
+            v.even = l.more;
             e = wide ? pair_product<float, false, false, true>(v, B, part, cus, st) : pair_product<float, true, true, true>(v, B, part, cus, st);
         }
         if (e == hipSuccess)
@@ -1657,7 +1674,7 @@ template <typename T, typename O> hipError_t run_long(const OrthoArgs &o, int cu
         if (l.more && e == hipSuccess) {
             e = square(h, g, l.tt, g, l.t, {}, 0, t);
             if (e == hipSuccess)
-                e = square(t, h, l.gg, t, l.g, {}, 0, g);
+                e = square(t, h, l.gg, t, l.g, {}, 0, g, true);
         }
         if (l.first) {
             std::swap(kp, h);
@@ -1716,12 +1733,14 @@ ShortPlan short_plan(int64_t B, int64_t m, int64_t n, int cus, bool apart = fals
     return p;
 }
 
-// Rounding of G, s 2^-53, grows by a step's largest Q^2 until G is formed anew: in
-// directions that X does not have, too, where it ends as eigenvalues of either sign
-// on which the steps have no hold (rank 4 of 16 x 400, the default coefficients: an
-// error of 2e-13 after 5 steps, 5e-7 after 16, 2e7 after 18).  A group ends when that
-// growth has passed SHORT_GROWTH_MAX: 64 2^-53 4e5 = 3e-9.
-constexpr double SHORT_GROWTH_MAX = 4e5;
+// Rounding of G, 2^-53 of its largest eigenvalue, grows by a step's largest Q^2 until G
+// is formed anew.  A singular value that grew as much has it as an error, and
+// directions that X does not have end as eigenvalues of either sign on which the
+// steps have no hold: singular values spread from 1 to 1e-9 in 64 x 1000, the default
+// coefficients, are off by 7e-10 after 8 steps, 7e-9 after 9, 8e-6 after 12, and rank 2
+// is lost from 16 on.  A group ends when that growth has passed SHORT_GROWTH_MAX:
+// 2^-53 1e8 = 1e-8, below fp32's half step.
+constexpr double SHORT_GROWTH_MAX = 1e8;
 
 // Steps of the group that begins with step k.
 int short_group(const OrthoArgs &o, int k)

@@ -662,8 +662,11 @@ int linear_int8_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const 
  *            scales that such values need, leave fp32.
  * Limits: B and the longer side at most 2^20, s at most 2^15, B*m*n at most 2^33
  * (FA_ERR_RANGE).  Precision: fp64 for s <= 64; beyond, that of fp32 products, on
- * pairs of fp16.  Each result is rounded once to its type.  Sums have an order
- * fixed by the sizes: results are deterministic.
+ * pairs of fp16, but for bf16 results with 4 max(m, n) >= 5 s, where several steps
+ * share a Gram matrix, to an error that stays below the result's own rounding.
+ * Rounding in directions that t does not have grows by |a| a step, here as
+ * in the formula: 2^-53 (s <= 64) or 2^-24 times a^steps.  Each result is rounded once
+ * to its type.  Sums have an order fixed by the sizes: results are deterministic.
  *
  * orthogonalize -- out = scale * O of x.  out may be x itself (same pointer,
  * pitch and stride); otherwise they must not overlap (FA_ERR_ARG).
@@ -679,7 +682,7 @@ int linear_int8_backward(fa_dtype dtype, int64_t M, int64_t N, int64_t K, const 
 #define FA_MAX_ORTHO_STEPS 32
 
 /* Device workspace bytes for these sizes with any steps, on the current device.  (With
-   s <= 64 a call whose steps need one Gram matrix alone, up to 6 of the default
+   s <= 64 a call whose steps need one Gram matrix alone, up to 8 of the default
    coefficients, takes less and looks for no more.) */
 int orthogonalize_workspace_size(int64_t B, int64_t m, int64_t n, size_t *bytes);
 int orthogonalize(fa_dtype dtype, int64_t B, int64_t m, int64_t n, const void *x, int64_t ldx,

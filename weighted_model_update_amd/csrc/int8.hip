@@ -16,7 +16,9 @@ namespace {
 // A group of threads holds its row in registers between the maximum and the
 // quotients, QR_W values a thread at a time; what does not fit is read again.
 // Bound by memory once the quotients are products: 14336 x 4096 bf16 (176 MB) in
-// 39 us, with a division for each value 48.
+// 38 us, 4.6 TB/s, where a copy of x (235 MB) takes 56, 4.2 TB/s; with a division for
+// each value 48.  A row of 4096 on 256 threads takes 54 us, on a wavefront with one
+// piece held and the others read twice, in fewer registers, 49.
 constexpr int QR_THREADS = 256, QR_W = 16, QR_HELD = 4;
 
 // Largest magnitude among W values, as the bits of an fp32 (NaN and infinities
@@ -291,9 +293,9 @@ template <typename O> __global__ __launch_bounds__(J8_THREADS) void join8_kernel
 // workgroups a CU); the first 2 FEW_AHEAD fragments of the weights are on their way
 // before the workgroup looks at x, which it brings to 8 bits itself (X: its type;
 // int8_t: as it is), FEW_PIECES pieces of 4096 in all.  One token of bf16 through
-// 14336 x 4096 weights (59 MB): 12.7 us.  With x after the weights it was 15.4, and
-// then as 16 x 128 tiles after a launch for x, with the join of two splits, 18.6; with
-// 8 fragments on their way, or loads past the caches, 18.4.
+// 14336 x 4096 weights (59 MB): 12.7 to 13.7 us.  Other forms were timed beside an
+// earlier one of 15.4: as 16 x 128 tiles after a launch for x, with the join of two
+// splits, 18.6; with 8 fragments on their way, or loads past the caches, 18.4.
 constexpr int FEW_M = 4, FEW_WAVES = 4, FEW_THREADS = FEW_WAVES * WAVE, FEW_AHEAD = 4, FEW_PER_CU = 4, FEW_PIECES = 4;
 
 __device__ __forceinline__ int64_t few_pitch(int64_t K) { return (K + WAVE - 1) / WAVE * WAVE; }

@@ -31,6 +31,12 @@ def test_what_a_call_got_is_not_changed_by_the_next():
     assert list(first) == [1.0, 0.0, 0.0] and list(second) == [2.0, 0.0, 0.0]
 
 
+def test_coefficients_made_on_the_way():
+    assert values((v for v in (1.0, 2.0, 3.0)), 2) == [1.0, 2.0, 3.0] * 2
+    assert values(((k, 0.0, 1.0) for k in range(3)), 3) == [0.0, 0.0, 1.0, 1.0, 0.0, 1.0, 2.0, 0.0, 1.0]
+    assert values((iter((k, 0.0, 1.0)) for k in range(2)), 2) == [0.0, 0.0, 1.0, 1.0, 0.0, 1.0]
+
+
 ROW, ROWS = [1.5, -0.5, 0.25], [[1.5, -0.5, 0.25], [2.0, -1.0, 0.0]]
 
 

@@ -1071,6 +1071,7 @@ def _coef_of(coef, steps):
     steps = int(steps)
     if not 1 <= steps <= FA_MAX_ORTHO_STEPS:
         raise ValueError(f"steps must be 1 to {FA_MAX_ORTHO_STEPS}, got {steps}")
+    coef = list(coef)
     try:
         rows = [[float(v) for v in coef]] * steps
     except (TypeError, ValueError, RuntimeError):  # rows, or no numbers

@@ -160,3 +160,15 @@ def test_singular_values_of_every_size():
             want = formula(x, QUINTIC, steps, torch.float64)
             out = fa.orthogonalize(x, steps=steps)
             assert off(out, want) <= 2.0 ** -24 + 3e-7 / k ** 0.5
+
+
+@pytest.mark.parametrize("shape", [(20000, 5, 3), (17000, 3, 20), (3500, 40, 33)], ids=str)
+def test_large_batches_of_small_matrices(shape):
+    x = rnd(shape, torch.float32, 53)
+    x[5] = 0
+    out = fa.orthogonalize(x, steps=12)
+    assert bool((out[5] == 0).all())
+    for b in (0, 1, shape[0] // 2, shape[0] - 1):
+        check(x[b], out[b], steps=12)
+    # the last ones by themselves, in a pass of their own
+    assert torch.equal(out[-100:], fa.orthogonalize(x[-100:], steps=12))

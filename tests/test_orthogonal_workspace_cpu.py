@@ -31,3 +31,9 @@ def test_the_held_matrices_are_bounded():
     for B in (1 << 10, 1 << 16):
         assert bytes_of(B, 16, 4096) - bytes_of(B // 2, 16, 4096) < B * 16 * 4096
     assert bytes_of(1, 64, 1 << 20) < 3 * 8 * 64 << 20
+
+
+def test_large_batches_of_small_matrices():
+    for m, n in ((1, 1), (8, 8), (5, 16), (16, 100)):
+        assert bytes_of(1 << 20, m, n) <= (1 << 28)
+        assert bytes_of(1 << 20, m, n) == bytes_of(1 << 19, m, n)

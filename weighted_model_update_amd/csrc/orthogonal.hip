@@ -1759,8 +1759,9 @@ int short_group(const OrthoArgs &o, int k)
 }
 
 // Calls of several groups hold the X of as many matrices as have SHORT_HELD elements
-// (at least one) in fp64, and take their batch in such passes.
-constexpr int64_t SHORT_HELD = 1ll << 23;
+// (at least one) in fp64, with G and P of up to SHORT_BLOCKS blocks, and take their
+// batch in such passes: 128 MB, or one matrix.
+constexpr int64_t SHORT_HELD = 1ll << 23, SHORT_BLOCKS = 1ll << 14;
 
 struct ShortGroups {
     int64_t matrices;
@@ -1772,7 +1773,7 @@ struct ShortGroups {
 ShortGroups short_groups(int64_t B, int64_t m, int64_t n, int cus)
 {
     ShortGroups g{};
-    g.matrices = std::min(B, std::max<int64_t>(1, SHORT_HELD / (m * n)));
+    g.matrices = std::min({B, std::max<int64_t>(1, SHORT_HELD / (m * n)), SHORT_BLOCKS / blocks_of((int)ceil_div(std::min(m, n), 16))});
     g.p = short_plan(g.matrices, m, n, cus, true);
     g.x = (size_t)(g.matrices * m * n) * sizeof(double);
     return g;
